@@ -25,8 +25,9 @@ OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsyn.so")
 INCLUDE = os.path.join(ROOT, "include")
 
-SOURCES = ["api.cu", "quant.cu", "gemv.cu", "gemv_f16.cu", "gemm.cu", "noalloc.cu", "gguf.cpp"]
-HEADERS = ["common.cuh", "quant_dev.cuh", "kernels.h"]
+SOURCES = ["api.cu", "quant.cu", "gemv.cu", "gemv_f16.cu", "gemm.cu", "noalloc.cu", "kv_append.cu", "attn_decode.cu",
+           "api_attn.cu", "gguf.cpp"]
+HEADERS = ["common.cuh", "quant_dev.cuh", "kv_cache.cuh", "kernels.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -85,6 +85,12 @@ struct Workspace {
 std::mutex g_mu;
 std::map<int, DeviceState> g_dev;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
+// the attention's workspaces: counters (zero between calls), then partial results
+struct AttnWorkspace {
+    void* ptr = nullptr;
+    size_t zeroed = 0, rest = 0;
+};
+std::map<std::pair<int, cudaStream_t>, AttnWorkspace> g_attn_ws;
 
 int current_device(int* dev) {
     return cudaGetDevice(dev) == cudaSuccess ? SYN_OK : SYN_ERR_CUDA;
@@ -125,6 +131,15 @@ int sms_of(const DeviceState* st) {
 
 namespace syn {
 int sm_limit() { return g_sm_limit.load(); }
+bool deterministic() { return g_det.load() != 0; }
+int call_state(int* sms, int** words) {
+    DeviceState* st;
+    const int rc = device_state(&st);
+    if (rc) return rc;
+    *sms = sms_of(st);
+    *words = st->words;
+    return SYN_OK;
+}
 }  // namespace syn
 
 namespace {
@@ -182,6 +197,34 @@ int workspace_for(cudaStream_t s, size_t need, void** out) {
 
 namespace syn {
 void note_launches(int n) { g_launches += n; }
+
+int attn_workspace(cudaStream_t s, size_t zeroed, size_t rest, size_t* zeroed_at, void** out) {
+    int dev;
+    if (current_device(&dev) != SYN_OK) return SYN_ERR_CUDA;
+    std::lock_guard<std::mutex> lk(g_mu);
+    AttnWorkspace& w = g_attn_ws[{dev, s}];
+    if (w.zeroed < zeroed || w.rest < rest) {
+        const size_t z = std::max(w.zeroed, zeroed), r = std::max(w.rest, rest);
+        if (cudaDeviceSynchronize() != cudaSuccess) return SYN_ERR_CUDA;  // (refused while capturing)
+        if (w.ptr) cudaFree(w.ptr);
+        w = AttnWorkspace{};
+        if (cudaMalloc(&w.ptr, z + r) != cudaSuccess) {
+            (void)cudaGetLastError();  // not sticky: keep it out of the next launch check
+            w.ptr = nullptr;
+            return SYN_ERR_NOMEM;
+        }
+        if (cudaMemset(w.ptr, 0, z) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+            cudaFree(w.ptr);
+            w.ptr = nullptr;
+            return SYN_ERR_CUDA;
+        }
+        w.zeroed = z;
+        w.rest = r;
+    }
+    *zeroed_at = w.zeroed;
+    *out = w.ptr;
+    return SYN_OK;
+}
 }  // namespace syn
 
 extern "C" {
@@ -211,7 +254,7 @@ const char* syn_strerror(int status) {
     case SYN_ERR_FORMAT: return "malformed GGUF file";
     case SYN_ERR_IO: return "file could not be opened, mapped or written";
     case SYN_ERR_NOTFOUND: return "no such GGUF key or tensor";
-    case SYN_ERR_BOUNDS: return "a kernel index check failed (SYN_DEBUG build)";
+    case SYN_ERR_BOUNDS: return "a cache page or slot out of range, or (SYN_DEBUG build) a failed index check";
     default: return "unknown status";
     }
 }
@@ -333,6 +376,14 @@ int syn_release(void) {
         if (it->first.first == dev) {
             cudaFree(it->second.ptr);
             it = g_ws.erase(it);
+        } else {
+            ++it;
+        }
+    }
+    for (auto it = g_attn_ws.begin(); it != g_attn_ws.end();) {
+        if (it->first.first == dev) {
+            cudaFree(it->second.ptr);
+            it = g_attn_ws.erase(it);
         } else {
             ++it;
         }
@@ -606,12 +657,13 @@ int syn_device_status(int clear) {
     // the index-check words of the kernel files (a failed check outranks a timeout it caused)
     int wb = 0;
     for (int v : {syn::debug_bounds_quant(clear), syn::debug_bounds_gemv(clear), syn::debug_bounds_gemv_f16(clear),
-                  syn::debug_bounds_gemm(clear)}) {
+                  syn::debug_bounds_gemm(clear), syn::debug_bounds_kv_append(clear), syn::debug_bounds_attn_decode(clear)}) {
         if (v < 0) return SYN_ERR_CUDA;
         wb |= v;
     }
     if (wb) return SYN_ERR_BOUNDS;
 #endif
+    if (w == SYN_DEVERR_BOUNDS) return SYN_ERR_BOUNDS;  // a page or slot outside the cache
     return (w || ws) ? SYN_ERR_TIMEOUT : SYN_OK;
 }
 

@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace syn {
 
 cudaError_t launch_quantize(int type, const float* src, void* dst, int64_t n_blocks, int* range_err,
@@ -60,6 +62,74 @@ cudaError_t launch_x_to_half(const float* X, int64_t n, void* xh, int sms, cudaS
 cudaError_t launch_gemv_f16(const void* W, int64_t n_out, int64_t n_in, const float* X, int64_t n_tok, float* Y,
                             void* ws, int sms, cudaStream_t s);
 
+// ---- paged key-value cache and attention (kv_append.cu, attn_decode.cu, attn_prefill.cu) ----
+
+struct KvCache;  // kv_cache.cuh
+
+struct RopeDesc {
+    const uint64_t* turns;  // n_rot / 2 turns per position, as 64-bit fractions
+    const uint8_t* axis;    // n_rot / 2 position axes, or NULL (all 0)
+    int n_rot, n_axes, halves;
+    float magnitude;
+};
+struct AttnDesc {
+    const float* slopes;    // n_heads, or NULL
+    const int32_t* prefix;  // per sequence, or NULL
+    const int32_t* first;   // per query, or NULL
+    int64_t q_stride, out_stride;
+    int n_heads, window, out_f16;
+    float scale, cap;
+};
+
+cudaError_t launch_kv_append(const KvCache& c, const RopeDesc& r, int64_t n_tok, const float* q, int64_t q_stride,
+                             int n_heads, void* q_out, const float* k, int64_t k_stride, const float* v,
+                             int64_t v_stride, const int32_t* pos, const int64_t* slots, int* err, cudaStream_t s);
+cudaError_t launch_kv_read(const KvCache& c, int64_t n, const int64_t* slots, void* k, void* v, int* err, int sms,
+                           cudaStream_t s);
+
+// One token of each sequence.  part (decode_part_floats) and count (decode_count_words, zero
+// before the first call and left zero by every call) are the launch's scratch.  whole: no item
+// is split between CTAs.  *launches gets the number of kernels.
+constexpr int DECODE_CTAS_PER_SM = 4;
+cudaError_t launch_attn_decode(const KvCache& c, const AttnDesc& a, int64_t n_seq, const void* q, const int32_t* pages,
+                               int64_t max_pages, const int32_t* lens, void* out, float* part, int* count, bool whole,
+                               int* err, int sms, int* launches, cudaStream_t s);
+int64_t decode_count_words(int64_t n_seq, int n_heads, int n_kv, int dim);
+int64_t decode_part_floats(int n_heads, int n_kv, int dim, int sms);
+
+// What the C entry points of api_attn.cu share with api.cu: the SMs of this call and the
+// status words ([0]) of the current device; the attention's workspace of (device, stream), at
+// least `zeroed` bytes that were zero when it was allocated, then (from byte *zeroed_at on) at
+// least `rest` bytes; the deterministic mode.
+int call_state(int* sms, int** words);
+int attn_workspace(cudaStream_t s, size_t zeroed, size_t rest, size_t* zeroed_at, void** out);
+bool deterministic();
+
+// Shared-memory limit and resident CTAs per SM of a kernel, looked up once per device.
+class ResidentCtas {
+    std::atomic<int> n_[64] = {};
+
+  public:
+    cudaError_t get(const void* kern, int threads, int smem, int* out) {
+        int dev;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64 && n_[dev].load() > 0) {
+            *out = n_[dev].load();
+            return cudaSuccess;
+        }
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        int n = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        if (dev >= 0 && dev < 64) n_[dev].store(n);
+        *out = n;
+        return cudaSuccess;
+    }
+};
+
 // Adds n to the count syn_launch_count reports.
 void note_launches(int n);
 
@@ -77,6 +147,8 @@ int debug_bounds_quant(int clear);
 int debug_bounds_gemv(int clear);
 int debug_bounds_gemv_f16(int clear);
 int debug_bounds_gemm(int clear);
+int debug_bounds_kv_append(int clear);
+int debug_bounds_attn_decode(int clear);
 cudaError_t launch_bounds_selftest(cudaStream_t s);
 #endif
 

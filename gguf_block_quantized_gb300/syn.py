@@ -21,6 +21,8 @@ OK, ERR_TYPE, ERR_SHAPE, ERR_NULL, ERR_ALIGN, ERR_RANGE, ERR_CUDA, ERR_TIMEOUT, 
 ERR_TOO_LARGE = -10
 ERR_FORMAT, ERR_IO, ERR_NOTFOUND = -11, -12, -13
 ERR_BOUNDS = -14
+ROPE_ADJACENT, ROPE_HALVES = 0, 1
+OUT_F32, OUT_F16 = 0, 1
 # GGUF metadata value types and ggml tensor element types (include/syn.h)
 GGUF_UINT8, GGUF_INT8, GGUF_UINT16, GGUF_INT16, GGUF_UINT32, GGUF_INT32, GGUF_FLOAT32, GGUF_BOOL, \
     GGUF_STRING, GGUF_ARRAY, GGUF_UINT64, GGUF_INT64, GGUF_FLOAT64 = range(13)
@@ -103,6 +105,34 @@ EXPORTS += [
     ("syn_gguf_writer_add_tensor", _i32, [_vp, _cp, _u32, _i32, _P(_i64), _vp, _i64]),
     ("syn_gguf_writer_finish", _i32, [_vp]),
     ("syn_gguf_writer_abort", None, [_vp]),
+]
+
+class KVCacheDesc(ctypes.Structure):
+    """syn_kv_cache."""
+    _fields_ = [("type", _i32), ("n_kv_heads", _i32), ("head_dim", _i32), ("page_size", _i32), ("n_pages", _i64),
+                ("k", _vp), ("v", _vp), ("page_stride", _i64)]
+
+
+class RopeDesc(ctypes.Structure):
+    """syn_rope."""
+    _fields_ = [("n_rot", _i32), ("layout", _i32), ("n_axes", _i32), ("magnitude", ctypes.c_float), ("turns", _vp),
+                ("axis", _vp)]
+
+
+class AttnDesc(ctypes.Structure):
+    """syn_attn."""
+    _fields_ = [("n_heads", _i32), ("window", _i32), ("scale", ctypes.c_float), ("cap", ctypes.c_float),
+                ("slopes", _vp), ("prefix", _vp), ("first", _vp), ("q_stride", _i64), ("out_stride", _i64),
+                ("out_type", _i32)]
+
+
+EXPORTS += [
+    ("syn_kv_tile_bytes", _i64, [_i32, _i32, _i32]),
+    ("syn_rope_turns", _i32, [_i32, ctypes.c_double, ctypes.c_double, _vp, _vp]),
+    ("syn_kv_append", _i32, [_P(KVCacheDesc), _P(RopeDesc), _i64, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _vp, _vp,
+                             _vp]),
+    ("syn_kv_read", _i32, [_P(KVCacheDesc), _i64, _vp, _vp, _vp, _vp]),
+    ("syn_attn_decode", _i32, [_P(KVCacheDesc), _P(AttnDesc), _i64, _vp, _vp, _i64, _vp, _vp, _vp]),
 ]
 
 for _name, _res, _args in EXPORTS:
@@ -265,6 +295,178 @@ class PreparedBatch:
 
 def prepare_batch(items, n_tok: int, stream=None, staged=None) -> PreparedBatch:
     return PreparedBatch(items, n_tok, stream, staged)
+
+
+# ---- paged key-value cache and attention ---------------------------------------------------
+
+class KVCache:
+    """A paged cache over two torch pools (held by reference): ``k`` and ``v`` with the pages in
+    the first dimension, each page contiguous: float16 (n_pages, n_kv_heads, page_size, head_dim)
+    for F16, uint8 (n_pages, n_kv_heads, tile bytes) for Q8_0.  Pages may be a strided slice of a
+    larger allocation (the same stride for both pools)."""
+
+    def __init__(self, t: int, n_kv_heads: int, head_dim: int, page_size: int, k, v):
+        tile = int(syn_kv_tile_bytes(t, head_dim, page_size))
+        if tile < 0:
+            raise SynError(ERR_TYPE if t not in (F16, Q8_0) else ERR_SHAPE, "KVCache")
+        for pool in (k, v):
+            if pool.shape[0] != k.shape[0] or pool.stride(0) * pool.element_size() != k.stride(0) * k.element_size() \
+                    or pool[0].numel() * pool.element_size() != n_kv_heads * tile or not pool[0].is_contiguous():
+                raise ValueError("a pool is (n_pages, ...) with n_kv_heads contiguous tiles of "
+                                 f"{tile} bytes per page, both pools alike")
+        self.type, self.n_kv_heads, self.head_dim, self.page_size = t, n_kv_heads, head_dim, page_size
+        self.n_pages, self.k, self.v = k.shape[0], k, v
+        stride = k.stride(0) * k.element_size() if k.shape[0] > 1 else 0
+        self.desc = KVCacheDesc(t, n_kv_heads, head_dim, page_size, k.shape[0], _ptr(k), _ptr(v), stride)
+
+    @classmethod
+    def empty(cls, t: int, n_kv_heads: int, head_dim: int, page_size: int, n_pages: int, device="cuda"):
+        """A cache over new pools of its own (zeroed)."""
+        torch = _torch()
+        tile = int(syn_kv_tile_bytes(t, head_dim, page_size))
+        if tile < 0 or n_kv_heads < 1 or n_pages < 1:
+            raise SynError(ERR_TYPE if t not in (F16, Q8_0) else ERR_SHAPE, "KVCache")
+        shape = (n_pages, n_kv_heads, page_size, head_dim) if t == F16 else (n_pages, n_kv_heads, tile)
+        k, v = (torch.zeros(shape, dtype=torch.float16 if t == F16 else torch.uint8, device=device) for _ in range(2))
+        return cls(t, n_kv_heads, head_dim, page_size, k, v)
+
+
+class Rope:
+    """A rotation (syn_rope): ``n_rot`` values of each row, turns per position
+    scale * base^(-2i/n_rot) / (2 pi factors[i]); ``axis`` (n_rot/2 small integers) gives each pair
+    its position axis, None one axis for all."""
+
+    def __init__(self, n_rot: int, base: float = 10000.0, scale: float = 1.0, factors=None, layout: int = ROPE_HALVES,
+                 axis=None, magnitude: float = 1.0, device="cuda"):
+        import numpy as np
+        torch = _torch()
+        turns = np.zeros(max(n_rot // 2, 1), np.uint64)
+        f = None if factors is None else np.ascontiguousarray(factors, np.float32)
+        if f is not None and f.size != n_rot // 2:
+            raise ValueError("factors: one per pair")
+        check(syn_rope_turns(n_rot, base, scale, None if f is None else f.ctypes.data, turns.ctypes.data),
+              "syn_rope_turns")
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self.axis, self.n_axes = None, 1
+        if axis is not None:
+            a = np.ascontiguousarray(axis, np.uint8)
+            if a.size != n_rot // 2:
+                raise ValueError("axis: one per pair")
+            self.n_axes = int(a.max()) + 1 if a.size else 1
+            self.axis = torch.from_numpy(a.copy()).to(device)
+        self.n_rot, self.layout = n_rot, layout
+        self.desc = RopeDesc(n_rot, layout, self.n_axes, magnitude, _ptr(self.turns),
+                             None if self.axis is None else _ptr(self.axis))
+
+
+class Prepared:
+    """A call whose arguments stay the same (a program over fixed buffers): marshalled once, each
+    call is the one library call.  Holds what it points at; returns the call's outputs."""
+
+    def __init__(self, name: str, args, result, keep):
+        self._name, self._fn, self._args, self._result, self._keep = name, globals()[name], args, result, keep
+
+    def __call__(self):
+        rc = self._fn(*self._args)
+        if rc:
+            check(rc, self._name)
+        return self._result
+
+
+def _typed(x, dtype, what: str):
+    """An optional tensor that the library reads as it lies: its type, and contiguous."""
+    if x is None:
+        return None
+    if x.dtype != dtype or not x.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} tensor")
+    return _ptr(x)
+
+
+def _rows(x, dtype, head_dim: int, what: str):
+    """(pointer, stride between tokens) of a (tokens, heads, head_dim) tensor whose rows are contiguous."""
+    if x.dim() != 3 or x.dtype != dtype or x.shape[2] != head_dim or (x.shape[2] > 1 and x.stride(2) != 1) or \
+            (x.shape[1] > 1 and x.stride(1) != head_dim):
+        raise ValueError(f"{what}: a {dtype} tensor (tokens, heads, {head_dim}), each token's rows contiguous")
+    return _ptr(x), (x.stride(0) if x.shape[0] > 1 else 0)
+
+
+def prepare_kv_append(cache: KVCache, rope: Rope, k, v, pos, slots, q=None, q_out=None, stream=None) -> Prepared:
+    """syn_kv_append: k, v (and q) fp32 (n_tok, heads, head_dim), possibly slices of a fused buffer;
+    pos int32 (n_axes or more, n_tok) or (n_tok,); slots int64 (n_tok).  The call returns q rotated, float16
+    (None without q)."""
+    torch = _torch()
+    n_tok, dim = k.shape[0], cache.head_dim
+    kp, ks = _rows(k, torch.float32, dim, "k")
+    vp, vs = _rows(v, torch.float32, dim, "v")
+    if k.shape[1] != cache.n_kv_heads or v.shape[1] != cache.n_kv_heads or v.shape[0] != n_tok or \
+            slots.numel() != n_tok or (rope.n_rot and (pos.shape[-1] != n_tok or pos.numel() < rope.n_axes * n_tok)) or \
+            (q is not None and q.shape[0] != n_tok):
+        raise ValueError("k, v, q, pos and slots do not agree on tokens, heads or axes")
+    qp, qs, n_heads = None, 0, 0
+    if q is not None:
+        qp, qs = _rows(q, torch.float32, dim, "q")
+        n_heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((n_tok, n_heads, dim), dtype=torch.float16, device=q.device)
+        elif q_out.shape != (n_tok, n_heads, dim):
+            raise ValueError("q_out: the shape of q")
+    args = (ctypes.byref(cache.desc), ctypes.byref(rope.desc), n_tok, qp, qs, n_heads,
+            _typed(q_out if q is not None else None, torch.float16, "q_out"), kp, ks, vp, vs,
+            _typed(pos, torch.int32, "pos"), _typed(slots, torch.int64, "slots"), _stream(stream))
+    return Prepared("syn_kv_append", args, q_out if q is not None else None, (cache, rope, k, v, pos, slots, q, q_out))
+
+
+def kv_append(cache: KVCache, rope: Rope, k, v, pos, slots, q=None, q_out=None, stream=None):
+    return prepare_kv_append(cache, rope, k, v, pos, slots, q, q_out, stream)()
+
+
+def prepare_kv_read(cache: KVCache, slots, stream=None) -> Prepared:
+    """syn_kv_read: the call returns (k, v), float16 (n, n_kv_heads, head_dim) buffers of its own."""
+    torch = _torch()
+    shape = (slots.numel(), cache.n_kv_heads, cache.head_dim)
+    k, v = (torch.empty(shape, dtype=torch.float16, device=slots.device) for _ in range(2))
+    args = (ctypes.byref(cache.desc), slots.numel(), _typed(slots, torch.int64, "slots"), _ptr(k), _ptr(v),
+            _stream(stream))
+    return Prepared("syn_kv_read", args, (k, v), (cache, slots))
+
+
+def kv_read(cache: KVCache, slots, stream=None):
+    return prepare_kv_read(cache, slots, stream)()
+
+
+def _attn_desc(cache: KVCache, q, out, n_seq: int, pages, lens, scale, cap, window, slopes, prefix, first):
+    """(syn_attn, q pointer, out tensor, out pointer) after the checks both attention calls share."""
+    torch = _torch()
+    qp, qs = _rows(q, torch.float16, cache.head_dim, "q")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    if out.dtype not in (torch.float32, torch.float16) or out.shape != q.shape:
+        raise ValueError("out: float32 or float16, the shape of q")
+    op, os_ = _rows(out, out.dtype, cache.head_dim, "out")
+    if pages.dim() != 2 or pages.shape[0] != n_seq or lens.numel() != n_seq or \
+            (slopes is not None and slopes.numel() != q.shape[1]) or \
+            (prefix is not None and prefix.numel() != n_seq) or (first is not None and first.numel() != q.shape[0]):
+        raise ValueError("pages, lens, slopes, prefix and first do not agree with q on sequences, heads or tokens")
+    desc = AttnDesc(q.shape[1], window, cache.head_dim ** -0.5 if scale is None else scale, cap,
+                    _typed(slopes, torch.float32, "slopes"), _typed(prefix, torch.int32, "prefix"),
+                    _typed(first, torch.int32, "first"), qs, os_, OUT_F16 if out.dtype == torch.float16 else OUT_F32)
+    return desc, qp, out, op
+
+
+def prepare_attn_decode(cache: KVCache, q, pages, lens, out=None, scale=None, cap: float = 0.0, window: int = 0,
+                        slopes=None, prefix=None, first=None, stream=None) -> Prepared:
+    """syn_attn_decode: q float16 (n_seq, n_heads, head_dim), pages int32 (n_seq, max_pages), lens
+    int32 (n_seq); out float32 (the default) or float16, the shape of q; scale None: 1/sqrt(head_dim).
+    The call returns out."""
+    torch = _torch()
+    desc, qp, out, op = _attn_desc(cache, q, out, q.shape[0], pages, lens, scale, cap, window, slopes, prefix, first)
+    args = (ctypes.byref(cache.desc), ctypes.byref(desc), q.shape[0], qp, _typed(pages, torch.int32, "pages"),
+            pages.shape[1], _typed(lens, torch.int32, "lens"), op, _stream(stream))
+    return Prepared("syn_attn_decode", args, out, (cache, desc, q, pages, lens, out, slopes, prefix, first))
+
+
+def attn_decode(cache: KVCache, q, pages, lens, out=None, **options):
+    return prepare_attn_decode(cache, q, pages, lens, out, **options)()
 
 
 def block_sums(t: int, W, n_out: int, n_in: int, Xq, n_tok: int, stream=None):

@@ -89,8 +89,9 @@ enum {
     SYN_ERR_FORMAT = -11, /* a GGUF file is malformed or not a GGUF file               */
     SYN_ERR_IO = -12,     /* a file could not be opened, mapped or written             */
     SYN_ERR_NOTFOUND = -13, /* no GGUF key / tensor with that name or index              */
-    SYN_ERR_BOUNDS = -14, /* SYN_DEBUG build only: a kernel found an index or copy window
-                             outside its buffers and skipped that access; results invalid */
+    SYN_ERR_BOUNDS = -14, /* a cache page or slot index outside the pool was not followed, or
+                             (SYN_DEBUG build) a kernel found an index or copy window outside
+                             its buffers and skipped that access; results invalid */
 };
 
 /* Elements per block: 32 (Q8_0, Q4_0, Q5_0), 256 (Q4_K, Q6_K, Q8_K) or 1 (F16); -1 for an
@@ -288,8 +289,8 @@ SYN_API int syn_set_sm_limit(int n);
  * included) gave up a bounded wait since the last clear.  A kernel that gives up records
  * the timeout, stops its other threads, waits for the copies and tensor-core operations it
  * had already issued and returns: the device stays usable, the outputs of that call are
- * invalid.  In the SYN_DEBUG build (index checks in every kernel) it returns
- * SYN_ERR_BOUNDS if a check failed.  Synchronizes the device.  It allocates nothing: a
+ * invalid.  SYN_ERR_BOUNDS if a kernel met a cache page or slot index outside its pool, or, in
+ * the SYN_DEBUG build (index checks in every kernel), if a check failed.  Synchronizes the device.  It allocates nothing: a
  * device on which no product has run reads SYN_OK. */
 SYN_API int syn_device_status(int clear);
 
@@ -332,6 +333,127 @@ SYN_API int64_t syn_launch_count(void);
  * counted by syn_launch_count. */
 SYN_API int syn_mul_mat_prefill_static(int type, const void* W, int64_t n_out, int64_t n_in,
                                const float* X, int64_t n_tok, float* Y, syn_stream_t stream);
+
+/* ======================================================================================
+ * Paged key-value cache and attention: what stands between a layer's q/k/v products and its
+ * output product.  syn_kv_append rotates q and k by position and writes k and v into the
+ * cache; syn_attn_decode (one new token per sequence) and syn_attn_prefill (several) read it.
+ *
+ * A cache is two pools of n_pages pages, one of keys and one of values.  A page holds, for
+ * each kv head in turn, one tile of page_size rows of head_dim values:
+ *   F16    [page_size][head_dim] halves
+ *   Q8_0   [page_size][head_dim] int8 codes, then [page_size][head_dim / 32] fp16 scales: the
+ *          values of Q8_0 blocks (d = fp16(amax/127), value = d*code), codes and scales apart
+ *          so that both start on 16-byte boundaries
+ * head_dim is a multiple of 32 from 32 to 256, page_size a power of two from 8 to 65536.  The
+ * pools may lie in one allocation (page_stride then spans both pools' page).  A slot is the
+ * place of one token's rows: page * page_size + row within the page.  A sequence's row j lives
+ * in page pages[s * max_pages + j / page_size], row j % page_size.
+ *
+ * Lengths, tables, slots and positions are read on the device, so a captured graph can be
+ * replayed as they change.  A page or slot index outside the pool is not followed: that row is
+ * skipped (or reads as zeros) and syn_device_status returns SYN_ERR_BOUNDS; the outputs that
+ * depend on it are invalid.  A length that its page table cannot hold is cut to it.
+ * ====================================================================================== */
+typedef struct {
+    int type;            /* SYN_TYPE_F16 or SYN_TYPE_Q8_0 */
+    int n_kv_heads;
+    int head_dim;
+    int page_size;       /* rows of a page */
+    int64_t n_pages;
+    void* k;             /* pools, 16-byte aligned */
+    void* v;
+    int64_t page_stride; /* bytes between pages of a pool, a multiple of 16; 0: n_kv_heads tiles */
+} syn_kv_cache;
+
+/* Bytes of one tile: page_size * head_dim * 2 (F16) or * 17/16 (Q8_0); -1 for a type, head_dim
+ * or page_size that a cache cannot have.  Host function. */
+SYN_API int64_t syn_kv_tile_bytes(int type, int head_dim, int page_size);
+
+/* Which values of a row form pair i of the rotation. */
+enum {
+    SYN_ROPE_ADJACENT = 0, /* (2i, 2i + 1)       */
+    SYN_ROPE_HALVES = 1,   /* (i, i + n_rot / 2) */
+};
+
+/* A rotation: the first n_rot values of each row (a multiple of 8, 0: none) are turned pair by
+ * pair, (a, b) -> magnitude * (a cos t - b sin t, a sin t + b cos t), by t = 2 pi * turns[i] *
+ * (the token's position on axis[i]). */
+typedef struct {
+    int n_rot;
+    int layout;             /* SYN_ROPE_* */
+    int n_axes;             /* rows of pos, 1..8 (1: text; 3: time, height and width) */
+    float magnitude;
+    const uint64_t* turns;  /* DEVICE, n_rot / 2 (syn_rope_turns) */
+    const uint8_t* axis;    /* DEVICE, n_rot / 2 values below n_axes, or NULL: all 0 */
+} syn_rope;
+
+/* The turns per position of each pair, scale * base^(-2i/n_rot) / (2 pi * factors[i]), as 64-bit
+ * fractions of a turn (the position times it wraps at whole turns, exactly).  HOST function:
+ * factors (n_rot / 2, or NULL for ones: the per-pair divisors of scaled-context models) and out
+ * (n_rot / 2) are host pointers; copy out to the device for syn_rope.turns.  SYN_ERR_SHAPE for a
+ * bad n_rot, base or scale, SYN_ERR_RANGE for a zero or non-finite factor, SYN_ERR_NULL. */
+SYN_API int syn_rope_turns(int n_rot, double base, double scale, const float* factors, uint64_t* out);
+
+/* For each of n_tok tokens: q (n_heads rows of head_dim, fp32) rotated and rounded to fp16 into
+ * q_out (n_tok x n_heads x head_dim, contiguous); k (n_kv_heads rows) rotated, and v, written to
+ * slot slots[t] of the cache (F16: rounded to nearest even, infinite past 65504; Q8_0: the
+ * encoder of syn_quantize; a block with a non-finite value, or whose scale overflows fp16, reads
+ * back as NaN).  A token with a negative slot is not stored (its q is still rotated).  Two tokens
+ * of a call must not have the same slot.
+ * pos: n_axes x n_tok positions (any int32; may be NULL when n_rot is 0).  Strides are in fp32
+ * values between tokens, multiples of 4 (0: contiguous rows), so q, k and v may be slices of one
+ * fused buffer.  n_heads 0 with q NULL stores k and v alone.  fp32 pointers and q_out are 16-byte
+ * aligned.  The rotation's angle is exact to 2^-24 turns at every position.  Asynchronous. */
+SYN_API int syn_kv_append(const syn_kv_cache* cache, const syn_rope* rope, int64_t n_tok, const float* q,
+                          int64_t q_stride, int n_heads, void* q_out, const float* k, int64_t k_stride,
+                          const float* v, int64_t v_stride, const int32_t* pos, const int64_t* slots,
+                          syn_stream_t stream);
+
+/* The rows at n slots back as fp16 values (Q8_0: d*code, rounded once): k and v get n x
+ * n_kv_heads x head_dim halves each.  A negative slot reads as zeros.  Asynchronous. */
+SYN_API int syn_kv_read(const syn_kv_cache* cache, int64_t n, const int64_t* slots, void* k, void* v,
+                        syn_stream_t stream);
+
+/* Element type of the attention's output. */
+enum {
+    SYN_OUT_F32 = 0,
+    SYN_OUT_F16 = 1,
+};
+
+/* The attention's options.  For a query at position p of its sequence and a key j of it:
+ *   s_j = scale * q.k_j;  cap > 0: s_j = cap * tanh(s_j / cap);  slopes: s_j -= slopes[head] * |p - j|
+ *   visible(j) = first <= j < length and (j < prefix or (j <= p and (window == 0 or p - j < window)))
+ *   out = sum_j softmax(s)_j v_j over the visible keys; zeros where no key is visible
+ * so first[] (one per query) separates packed documents, and a prefix is seen by every query of
+ * its sequence, before and after it and past the window.  What a key or value that a query does
+ * not see holds (infinities and NaN included) does not reach that query's output. */
+typedef struct {
+    int n_heads;            /* query heads, a multiple of n_kv_heads: head i reads kv head
+                               i / (n_heads / n_kv_heads) */
+    int window;             /* 0: none */
+    float scale;            /* usually 1 / sqrt(head_dim) */
+    float cap;              /* 0: none */
+    const float* slopes;    /* DEVICE, n_heads, or NULL */
+    const int32_t* prefix;  /* DEVICE, n_seq, or NULL */
+    const int32_t* first;   /* DEVICE, one per query token, or NULL */
+    int64_t q_stride;       /* values between tokens of q and of out, multiples of 8; 0: */
+    int64_t out_stride;     /* n_heads * head_dim */
+    int out_type;           /* SYN_OUT_* */
+} syn_attn;
+
+/* Attention of one new token of each of n_seq sequences, the last of its lens[s] rows (its k and
+ * v are in the cache: append first).  q: n_seq x n_heads x head_dim fp16; out likewise, fp32 or
+ * fp16.  pages: n_seq x max_pages; a length of 0 gives zeros.  Sums, maxima and scores are fp32
+ * and the products carry 22 bits, so an fp32 output is exact to about 1e-6 of its row's norm.
+ * The work is split over the lengths (see syn_set_deterministic: in that mode no sequence is
+ * split, and a sequence's output does not depend on the others of the call).  Pointers 16-byte
+ * (q, out, pools) or 4-byte aligned.  The call may allocate its workspace, which belongs to
+ * (device, stream) and grows with n_seq * n_heads; make the first call of a size before capturing
+ * a graph (growth synchronizes the device).  Asynchronous. */
+SYN_API int syn_attn_decode(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_seq, const void* q,
+                            const int32_t* pages, int64_t max_pages, const int32_t* lens, void* out,
+                            syn_stream_t stream);
 
 /* ======================================================================================
  * GGUF container (host code; only syn_gguf_upload touches the GPU)

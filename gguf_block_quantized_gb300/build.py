@@ -26,8 +26,8 @@ LIB = os.path.join(HERE, "libsyn.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["api.cu", "quant.cu", "gemv.cu", "gemv_f16.cu", "gemm.cu", "noalloc.cu", "kv_append.cu", "attn_decode.cu",
-           "api_attn.cu", "gguf.cpp"]
-HEADERS = ["common.cuh", "quant_dev.cuh", "kv_cache.cuh", "kernels.h"]
+           "attn_prefill.cu", "api_attn.cu", "gguf.cpp"]
+HEADERS = ["common.cuh", "quant_dev.cuh", "kv_cache.cuh", "tcgen05.cuh", "kernels.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

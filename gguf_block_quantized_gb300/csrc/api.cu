@@ -657,7 +657,8 @@ int syn_device_status(int clear) {
     // the index-check words of the kernel files (a failed check outranks a timeout it caused)
     int wb = 0;
     for (int v : {syn::debug_bounds_quant(clear), syn::debug_bounds_gemv(clear), syn::debug_bounds_gemv_f16(clear),
-                  syn::debug_bounds_gemm(clear), syn::debug_bounds_kv_append(clear), syn::debug_bounds_attn_decode(clear)}) {
+                  syn::debug_bounds_gemm(clear), syn::debug_bounds_kv_append(clear), syn::debug_bounds_attn_decode(clear),
+                  syn::debug_bounds_attn_prefill(clear)}) {
         if (v < 0) return SYN_ERR_CUDA;
         wb |= v;
     }

@@ -1,5 +1,6 @@
 // api_attn.cu — the C entry points of the paged key-value cache and its attention (declared in
-// include/syn.h): argument checks, workspaces, dispatch to kv_append.cu and attn_decode.cu.
+// include/syn.h): argument checks, workspaces, dispatch to kv_append.cu, attn_decode.cu and
+// attn_prefill.cu.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -196,6 +197,35 @@ int syn_attn_decode(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_s
     int launches = 0;
     rc = check_cuda(syn::launch_attn_decode(c, a, n_seq, q, pages, max_pages, lens, out, part, count,
                                             syn::deterministic(), words, sms, &launches, s));
+    syn::note_launches(launches);
+    return rc;
+}
+
+int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_seq, int64_t n_tok, const void* q,
+                     const int32_t* starts, const int32_t* pages, int64_t max_pages, const int32_t* lens, void* out,
+                     syn_stream_t stream) {
+    syn::KvCache c;
+    int rc = cache_of(cache, &c);
+    if (rc) return rc;
+    if (n_seq < 0 || n_seq > INT32_MAX || n_tok < 0 || max_pages < 1 || max_pages > INT32_MAX) return SYN_ERR_SHAPE;
+    syn::AttnDesc a;
+    rc = attn_of(attn, c, n_tok ? n_tok : 1, q, out, &a);
+    if (rc) return rc;
+    if (n_tok > (INT32_MAX - 1024) / a.n_heads) return SYN_ERR_SHAPE;  // 32-bit row numbers
+    if (n_seq == 0 || n_tok == 0) return SYN_OK;
+    if (!starts || !pages || !lens) return SYN_ERR_NULL;
+    if (!aligned(starts, 4) || !aligned(pages, 4) || !aligned(lens, 4)) return SYN_ERR_ALIGN;
+    int sms, *words;
+    rc = syn::call_state(&sms, &words);
+    if (rc) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int* count;
+    float* part;
+    rc = scratch_for(s, sms, syn::prefill_part_floats(c.dim, sms), &count, &part);
+    if (rc) return rc;
+    int launches = 0;
+    rc = check_cuda(syn::launch_attn_prefill(c, a, n_seq, n_tok, q, starts, pages, max_pages, lens, out, part, count,
+                                             !syn::deterministic(), words, sms, &launches, s));
     syn::note_launches(launches);
     return rc;
 }

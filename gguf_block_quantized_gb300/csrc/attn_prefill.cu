@@ -1,0 +1,828 @@
+// attn_prefill.cu — attention of several new tokens of each sequence over the paged cache, on the
+// 5th-generation tensor cores (tcgen05, sm_103a).
+//
+//   x_j = log2(e) * (cap*tanh(scale*q.k_j/cap) - slope*|p - j|),  p_j = 2^(x_j - m),
+//   out = sum_j p_j v_j / sum_j p_j  over the keys the query sees, m a running maximum.
+//
+// One CTA per item: 128 or 256 rows of (new token, query head of one kv head), the heads of a
+// token next to each other, so that all the heads of a kv head share the cached rows; the item's
+// keys come in tiles of BN.  Warp roles:
+//   softmax  4 warps per 128 rows, a thread per row: S from tensor memory, the row's maximum, p in
+//            fp16 back into the columns of S, the sum in fp32; O is rescaled in tensor memory when
+//            a row's maximum has grown by more than 2^8 (p stays below 2^14 in fp16: rarely);
+//   MMA      one warp: S = Q K^T (Q and K from shared memory), O += P V (P from tensor memory, V as
+//            an MN-major operand: cached rows are used as they lie);
+//   loader   F16: one warp, tensor-map copies of page pieces into a ring of tiles (128-byte
+//            swizzle); Q8_0: four warps expand codes to fp16 into the same layout.
+// All hand-offs are mbarriers with bounded waits.
+//
+// Rows that a mask empties give zeros.  A masked score is replaced before the maximum; V rows past
+// the sequence's end are zeroed in shared memory.  A V row that only some rows of the item see may
+// still hold infinities or NaN, and 0 * inf is not 0: a row whose sums come out non-finite is
+// computed again, key by key, from the keys it sees.
+//
+// Few rows over a long cache: an item's tiles are split between CTAs (no CTA waits: the last to
+// finish, by a counter, joins the partials in order).
+#include <algorithm>
+#include <climits>
+
+#include "kernels.h"
+#include "kv_cache.cuh"
+#include "tcgen05.cuh"
+
+namespace syn {
+
+constexpr int PRE_MAX_SEQ = 1024;     // sequences of one launch
+constexpr float PRE_P_LOG2 = 6.0f;    // p is held as 2^6 p
+constexpr float PRE_GROW_LOG2 = 8.0f; // the maximum's lag
+
+struct PrefillParams {
+    KvCache c;
+    const __half* q;
+    int64_t q_stride, out_stride;
+    void* out;
+    const int32_t* starts;
+    const int32_t* pages;
+    int64_t max_pages;
+    const int32_t* lens;
+    const float* slopes;
+    const int32_t* prefix;
+    const int32_t* first;
+    float* part;
+    int* count;
+    int* err;
+    float scale, cap;
+    int n_seq, n_tok, g, window, out_f16, sms, split;
+    uint32_t idesc_s, idesc_o;
+};
+
+template <int D>
+struct PreShape {
+    static constexpr int QT = D <= 128 ? 2 : 1;     // 128-row tiles of an item
+    static constexpr int BN = D <= 128 ? 128 : 64;  // keys of a tile
+    static constexpr int NS = D <= 64 ? 6 : 4;      // tiles (K or V) in the ring
+    static constexpr int R = 128 * QT;
+    static constexpr int STAGE = BN * D * 2;
+    static constexpr int Q_TILE = 128 * D * 2;
+    static constexpr int Q = 0;
+    static constexpr int RING = QT * Q_TILE;
+    static constexpr int BARS = RING + NS * STAGE;
+    static constexpr int INFO = BARS + (8 * (2 * NS + 9) + 8 + 15) / 16 * 16;
+    static constexpr int BYTES = INFO + 64 + 4 * (PRE_MAX_SEQ + 1);
+    static constexpr int O_COL = QT == 2 ? 256 : 128;  // S slots below it
+    static constexpr int SLOT = QT == 2 ? 128 : 64;    // columns of an S slot
+};
+
+template <int D, bool Q8>
+constexpr int PRE_THREADS = 32 * (4 * PreShape<D>::QT + 1 + (Q8 ? 4 : 1));
+
+// the tiles that hold a key some row of the item sees: [a0, a1) of the prefix, [b0, b1)
+struct Tiles {
+    int a0, a1, b0, b1;
+    __device__ __forceinline__ int count() const { return a1 - a0 + b1 - b0; }
+    __device__ __forceinline__ int at(int i) const { return i < a1 - a0 ? a0 + i : b0 + (i - (a1 - a0)); }
+};
+
+// bits of the keys 32w .. 32w+31 of a tile that lie in [lo, hi)
+__device__ __forceinline__ uint32_t span_bits(int lo, int hi, int w) {
+    const int a = min(max(lo - 32 * w, 0), 32), b = min(max(hi - 32 * w, 0), 32);
+    const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1u, below_a = a == 32 ? 0xffffffffu : (1u << a) - 1u;
+    return below_b & ~below_a;
+}
+
+// tanh from one exponential: 1 - 2/(1 + 2^(2y log2 e)), within a few 2^-24 of 1
+__device__ __forceinline__ float tanh_ex2(float y) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2(2.8853900817779268f * y)));
+    return fmaf(-2.0f, r, 1.0f);
+}
+
+// One row computed key by key by a warp (lane l takes the values l, l + 32, ...): its maximum, sum
+// and weighted values over the keys of tiles [t0, t1) that it sees.
+template <int D, bool Q8>
+__device__ __noinline__ void row_by_hand(const PrefillParams& p, const int32_t* table, int len, int h, const __half* qrow,
+                                         const Visible& vis, int pos, float slope, const Tiles& tiles, int t0, int t1,
+                                         float& m, float& l, float (&o)[D / 32]) {
+    const int lane = threadIdx.x & 31, dim = p.c.dim;
+    m = -INFINITY;
+    l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; i++) o[i] = 0.0f;
+    for (int t = t0; t < t1; t++) {
+        const int j0 = tiles.at(t) * PreShape<D>::BN;
+        for (int j = j0; j < min(j0 + PreShape<D>::BN, len); j++) {
+            if (!vis(j)) continue;
+            const int id = table[j >> p.c.page_shift];
+            if (id < 0 || id >= p.c.n_pages) continue;
+            const int cell = j & ((1 << p.c.page_shift) - 1);
+            const int64_t base = (int64_t)id * p.c.page_stride + (int64_t)h * p.c.tile;
+            auto value = [&](const uint8_t* pool, int e) {
+                if (!Q8) return __half2float(reinterpret_cast<const __half*>(pool + base)[(int64_t)cell * dim + e]);
+                const float d = h2f_bits(*reinterpret_cast<const uint16_t*>(
+                    pool + base + ((int64_t)dim << p.c.page_shift) + 2 * ((int64_t)cell * (dim >> 5) + (e >> 5))));
+                return d * (float)reinterpret_cast<const int8_t*>(pool + base)[(int64_t)cell * dim + e];
+            };
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 32; i++)
+                if (lane + 32 * i < dim) s = fmaf(__half2float(qrow[lane + 32 * i]), value(p.c.k, lane + 32 * i), s);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+            s *= p.scale;
+            if (p.cap > 0.0f) s = p.cap * tanhf(s / p.cap);
+            s = fmaf(-slope, fabsf((float)(pos - j)), s) * 1.4426950408889634f;
+            const float nm = fmaxf(m, s), ms = nm == -INFINITY ? 0.0f : nm;
+            const float f = ex2(m - ms), w = ex2(s - ms + PRE_P_LOG2);
+            m = nm;
+            l = fmaf(l, f, w);
+#pragma unroll
+            for (int i = 0; i < D / 32; i++)
+                if (lane + 32 * i < dim) o[i] = fmaf(o[i], f, w * value(p.c.v, lane + 32 * i));
+        }
+    }
+}
+
+__device__ __forceinline__ void store_out(const PrefillParams& p, int64_t at, float y) {
+    if (p.out_f16) static_cast<__half*>(p.out)[at] = __float2half_rn(y);
+    else static_cast<float*>(p.out)[at] = y;
+}
+
+template <int D, bool Q8, bool MOD>
+__global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
+    k_attn_prefill(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PrefillParams p) {
+    using L = PreShape<D>;
+    constexpr int QT = L::QT, BN = L::BN, NS = L::NS, R = L::R;
+    constexpr int THREADS = PRE_THREADS<D, Q8>;
+    constexpr int MMA_WARP = 4 * QT, LOAD_WARP = MMA_WARP + 1;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BARS);
+    uint64_t* kv_full = bars;
+    uint64_t* kv_empty = kv_full + NS;
+    uint64_t* s_full = kv_empty + NS;  // [2] S in its slot
+    uint64_t* p_full = s_full + 2;     // [2] P in its slot
+    uint64_t* o_done = p_full + 2;     // [2] a P V product is complete
+    uint64_t* q_full = o_done + 2;     // [2]
+    uint64_t* mma_idle = q_full + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* info = reinterpret_cast<int*>(smem + L::INFO);  // [0] carry, [1] min first, [2] min low, [3] max end, [4..] sums
+    int* pre = info + 16;                                // [n_seq + 1] items (of one kv head) before each sequence
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int dim = p.c.dim, nh = (dim + 63) >> 6;  // 64-value column chunks of a row
+
+    // ---- this CTA's item -------------------------------------------------------------------
+    auto new_tokens = [&](int s) {  // (starts that run backwards or past the call's tokens count as none)
+        const int a = p.starts[s], b = p.starts[s + 1];
+        return a < 0 || b > p.n_tok ? 0 : max(b - a, 0);
+    };
+    if (tid == 0) info[0] = 0, pre[0] = 0;
+    __syncthreads();
+    for (int base = 0; base < p.n_seq; base += THREADS) {
+        const int s = base + tid;
+        int x = s < p.n_seq ? (int)(((int64_t)new_tokens(s) * p.g + R - 1) / R) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        int* sums = reinterpret_cast<int*>(smem);  // (nothing else uses it yet)
+        if (lane == 31) sums[warp] = x;
+        __syncthreads();
+        int before = info[0];
+        for (int w = 0; w < warp; w++) before += sums[w];
+        if (s < p.n_seq) pre[s + 1] = before + x;
+        __syncthreads();
+        if (tid == THREADS - 1) info[0] = before + x;
+        __syncthreads();
+    }
+    const int n_tiles_q = pre[p.n_seq];
+    const int64_t items = (int64_t)n_tiles_q * p.c.n_kv;
+    // splits of an item: as many as leave every SM one CTA
+    const int max_split = p.split && items > 0 && items < p.sms ? (int)(p.sms / items) : 1;
+    const int64_t b = (int64_t)blockIdx.x / max_split;
+    const int sp = (int)(blockIdx.x - b * max_split);
+    if (b >= items) return;
+    // the last tiles of a sequence see the most keys: they go first
+    const int qtile = n_tiles_q - 1 - (int)(b / p.c.n_kv), h = (int)(b % p.c.n_kv);
+    int s;
+    {
+        int lo = 0, hi = p.n_seq - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid + 1] > qtile) hi = mid;
+            else lo = mid + 1;
+        }
+        s = lo;
+    }
+    const int row0 = (qtile - pre[s]) * R;  // first row of the item among its sequence's
+    const int n_new = new_tokens(s), tok0 = p.starts[s];
+    const int rows = (int)min((int64_t)R, (int64_t)n_new * p.g - row0);
+    const int len = max(0, (int)min((int64_t)p.lens[s], min(p.max_pages << p.c.page_shift, (int64_t)INT_MAX - 1024)));
+    const int32_t* table = p.pages + (int64_t)s * p.max_pages;
+
+    // ---- what this thread's row sees, and the keys that some row sees -----------------------
+    Visible vis;
+    vis.first = vis.pre = vis.low = vis.end = 0;
+    int pos = 0, my_tok = 0, my_head = 0;
+    const bool row_ok = tid < rows;
+    if (tid == 0) {
+        info[1] = info[2] = INT_MAX;
+        info[3] = 0;
+    }
+    __syncthreads();
+    if (tid < R) {
+        int mf = INT_MAX, ml = INT_MAX, me = 0;
+        if (row_ok) {
+            const int t = (row0 + tid) / p.g;
+            my_head = h * p.g + (row0 + tid - t * p.g);
+            my_tok = tok0 + t;
+            pos = len - n_new + t;
+            vis = visible_of(len, pos, p.first ? p.first[my_tok] : 0, p.prefix ? p.prefix[s] : 0, p.window);
+            if (vis.pre > vis.first || vis.end > vis.low) {
+                mf = vis.pre > vis.first ? vis.first : vis.low;
+                ml = vis.end > vis.low ? vis.low : vis.pre;
+                me = max(vis.end, vis.pre);
+            }
+        }
+        mf = __reduce_min_sync(0xffffffffu, mf);
+        ml = __reduce_min_sync(0xffffffffu, ml);
+        me = __reduce_max_sync(0xffffffffu, me);
+        if (lane == 0) {
+            atomicMin(&info[1], mf);
+            atomicMin(&info[2], ml);
+            atomicMax(&info[3], me);
+        }
+    }
+    if (tid == 0) {
+        for (int i = 0; i < NS; i++) {
+            mbar_init(smem_u32(&kv_full[i]), Q8 ? 4 : 1);
+            mbar_init(smem_u32(&kv_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_u32(&s_full[i]), 1);
+            mbar_init(smem_u32(&p_full[i]), 4);
+            mbar_init(smem_u32(&o_done[i]), 1);
+            mbar_init(smem_u32(&q_full[i]), 4);
+        }
+        mbar_init(smem_u32(mma_idle), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    // [min first, prefix) then [min low, max end): every key that some row sees lies in one of them
+    const int pre_end = p.prefix ? min(max(p.prefix[s], 0), len) : 0;
+    Tiles tiles;
+    {
+        const int mf = info[1], ml = info[2], me = info[3];
+        tiles.a0 = tiles.a1 = tiles.b0 = tiles.b1 = 0;
+        if (me > 0) {
+            tiles.b0 = ml / BN;
+            tiles.b1 = me > ml ? (me + BN - 1) / BN : tiles.b0;
+            tiles.a0 = tiles.a1 = mf / BN;
+            const int ae = min(pre_end, ml);
+            if (ae > mf) tiles.a1 = (ae + BN - 1) / BN;
+            if (tiles.b1 > tiles.b0) tiles.a1 = max(tiles.a0, min(tiles.a1, tiles.b0));
+        }
+    }
+    const int all = tiles.count();
+    const int n_split = min(max_split, max(1, all / 2));  // at least two tiles each
+    if (sp >= n_split) return;
+    const int t0 = (int)((int64_t)all * sp / n_split), t1 = (int)((int64_t)all * (sp + 1) / n_split);
+    const int nt = t1 - t0;
+    if (nt == 0) {  // (then the item is not split) no row sees a key
+        const int64_t n = (int64_t)rows * dim;
+        for (int64_t i = tid; i < n; i += THREADS) {
+            const int r = (int)(i / dim), t = (row0 + r) / p.g;
+            store_out(p, (int64_t)(tok0 + t) * p.out_stride + (int64_t)(h * p.g + row0 + r - t * p.g) * dim + (i - (int64_t)r * dim), 0.0f);
+        }
+        return;
+    }
+    const int q_act = QT == 2 && rows <= 128 ? 1 : QT;  // 128-row tiles in use
+
+    if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    float* part = p.part + (int64_t)blockIdx.x * R * (D + 2);  // [D][R] values, [R] maxima, [R] sums
+
+    // The ring's order: K of the first tile, then (two row tiles) V and the next K, or (one) the
+    // next K and V.  Piece i of 2*nt: is it V, and of which tile.
+    auto piece_v = [&](int i) { return QT == 2 ? (i & 1) : i == 2 * nt - 1 || (i > 0 && (i & 1) == 0); };
+    auto piece_tile = [&](int i) { return QT == 2 ? i >> 1 : i == 2 * nt - 1 ? nt - 1 : i == 0 ? 0 : (i & 1) ? (i + 1) >> 1 : (i >> 1) - 1; };
+
+    if (warp < MMA_WARP) {
+        // ------------------------------------ softmax ------------------------------------------
+        const int qt = warp >> 2;
+        const int r = tid;  // row of the item
+        if (qt < q_act) {
+            // Q rows into shared memory: row r of the tile, 16-byte piece j of chunk c at j ^ (r % 8)
+            uint8_t* qs = smem + L::Q + qt * L::Q_TILE;
+            const int pieces = dim >> 3;
+            for (int i = tid & 127; i < 128 * pieces; i += 128) {
+                const int rr = i / pieces, j = i - rr * pieces;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (qt * 128 + rr < rows) {
+                    const int row = row0 + qt * 128 + rr, t = row / p.g;
+                    w = *reinterpret_cast<const uint4*>(p.q + (int64_t)(tok0 + t) * p.q_stride +
+                                                        (int64_t)(h * p.g + row - t * p.g) * dim + 8 * j);
+                }
+                *reinterpret_cast<uint4*>(qs + (j >> 3) * (128 * 128) + rr * 128 + (((j & 7) ^ (rr & 7)) << 4)) = w;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&q_full[qt]));
+
+            const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+            const uint32_t o_base = lane_base + L::O_COL + qt * D;
+            const float c_log2 = p.scale * 1.4426950408889634f;
+            const float slope = MOD && p.slopes && row_ok ? p.slopes[my_head] * 1.4426950408889634f : 0.0f;
+            const float cap_log2 = p.cap * 1.4426950408889634f, to_cap = p.cap > 0.0f ? p.scale / p.cap : 0.0f;
+            float m = -INFINITY, l = 0.0f;
+            bool ok = true;
+            for (int i = 0; i < nt; i++) {
+                const int slot = QT == 2 ? qt : i & 1;
+                const uint32_t phase = QT == 2 ? i & 1 : (i >> 1) & 1;
+                if (!mbar_wait(smem_u32(&s_full[slot]), phase, p.err, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t s_base = lane_base + slot * L::SLOT;
+                uint32_t v[BN];
+#pragma unroll
+                for (int c = 0; c < BN; c += 32) TMEM_LD32(s_base + c, (v + c));
+                tmem_ld_wait();
+                const int j0 = tiles.at(t0 + i) * BN;
+                if (MOD) {
+#pragma unroll
+                    for (int c = 0; c < BN; c++) {
+                        float x = __uint_as_float(v[c]);
+                        x = p.cap > 0.0f ? cap_log2 * tanh_ex2(x * to_cap) : x * c_log2;
+                        if (p.slopes) x = fmaf(-slope, fabsf((float)(pos - j0 - c)), x);
+                        v[c] = __float_as_uint(x);
+                    }
+                }
+                const bool full = !row_ok || (j0 >= vis.low && j0 + BN <= vis.end) || (j0 >= vis.first && j0 + BN <= vis.pre);
+                if (!__all_sync(0xffffffffu, full)) {
+#pragma unroll
+                    for (int w = 0; w < BN / 32; w++) {
+                        const uint32_t bits = row_ok ? span_bits(vis.low - j0, vis.end - j0, w) | span_bits(vis.first - j0, vis.pre - j0, w)
+                                                     : 0xffffffffu;
+#pragma unroll
+                        for (int c = 0; c < 32; c++)
+                            if (!((bits >> c) & 1)) v[32 * w + c] = 0xff800000u;  // -inf
+                    }
+                }
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < BN; c += 8)
+#pragma unroll
+                    for (int u = 0; u < 4; u++)
+                        mx4[u] = fmaxf(mx4[u], fmaxf(__uint_as_float(v[c + 2 * u]), __uint_as_float(v[c + 2 * u + 1])));
+                float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                if (!MOD) mx *= c_log2;
+                // the reference of the powers follows the maximum when that has grown by 2^8
+                const bool grow = mx > m + PRE_GROW_LOG2 || (m == -INFINITY && mx > -INFINITY);
+                const float f = grow ? ex2(m - mx) : 1.0f;
+                if (grow) {
+                    m = mx;
+                    l *= f;
+                }
+                if (i > 0 && __any_sync(0xffffffffu, grow)) {
+                    // O holds the tiles before: wait for the last product into it, then scale
+                    if (!mbar_wait(smem_u32(&o_done[qt]), (i - 1) & 1, p.err, abort_flag)) { ok = false; break; }
+                    tc_fence_after();
+                    for (int c = 0; c < dim; c += 16) {
+                        uint32_t o[16];
+                        TMEM_LD16(o_base + c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int u = 0; u < 16; u++) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+                        TMEM_ST16(o_base + c, o);
+                    }
+                }
+                const float ms = (m == -INFINITY ? 0.0f : m) - PRE_P_LOG2;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < BN; c += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int u = 0; u < 16; u++) {
+                        const float x = __uint_as_float(v[c + 2 * u]), y = __uint_as_float(v[c + 2 * u + 1]);
+                        const float a = ex2(MOD ? x - ms : fmaf(x, c_log2, -ms)), e = ex2(MOD ? y - ms : fmaf(y, c_log2, -ms));
+                        sum[(2 * u) & 3] += a;
+                        sum[(2 * u + 1) & 3] += e;
+                        const __half2 hh = __floats2half2_rn(a, e);
+                        w[u] = *reinterpret_cast<const uint32_t*>(&hh);
+                    }
+                    TMEM_ST16(s_base + (c >> 1), w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&p_full[slot]));
+            }
+            // (one row tile: S of a tile is issued before the product of the one before, so the last
+            // two products may both be outstanding, and a parity tells only neighbours apart)
+            if (QT == 1 && nt > 1) ok = ok && mbar_wait(smem_u32(&o_done[qt]), (nt - 2) & 1, p.err, abort_flag);
+            if (ok && mbar_wait(smem_u32(&o_done[qt]), (nt - 1) & 1, p.err, abort_flag)) {
+                tc_fence_after();
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                float odd = l - l;  // NaN where something is not finite
+                const int64_t out0 = (int64_t)my_tok * p.out_stride + (int64_t)my_head * dim;
+                for (int c = 0; c < dim; c += 32) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    TMEM_LD32(o_base + c, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int u = 0; u < 32; u++) {
+                        const float x = __uint_as_float(o[u]);
+                        odd += x - x;
+                    }
+                    if (!row_ok) continue;
+                    if (n_split > 1) {
+#pragma unroll
+                        for (int u = 0; u < 32; u++) __stcg(part + (int64_t)(c + u) * R + r, __uint_as_float(o[u]));
+                    } else if (p.out_f16) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(p.out) + out0 + c);
+#pragma unroll
+                        for (int u = 0; u < 4; u++) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int x = 0; x < 4; x++) {
+                                const __half2 hh = __floats2half2_rn(__uint_as_float(o[8 * u + 2 * x]) * inv, __uint_as_float(o[8 * u + 2 * x + 1]) * inv);
+                                w[x] = *reinterpret_cast<const uint32_t*>(&hh);
+                            }
+                            dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + out0 + c);
+#pragma unroll
+                        for (int u = 0; u < 8; u++)
+                            dst[u] = make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
+                                                 __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
+                    }
+                }
+                if (n_split > 1 && row_ok) {
+                    __stcg(part + (int64_t)D * R + r, m);
+                    __stcg(part + (int64_t)(D + 1) * R + r, l);
+                }
+                // rows with a non-finite sum, one after the other, by the whole warp
+                __syncwarp();
+                uint32_t redo = __ballot_sync(0xffffffffu, row_ok && odd != 0.0f);
+                while (redo) {
+                    const int src = __ffs(redo) - 1;
+                    redo &= redo - 1;
+                    Visible w;
+                    w.first = __shfl_sync(0xffffffffu, vis.first, src);
+                    w.pre = __shfl_sync(0xffffffffu, vis.pre, src);
+                    w.low = __shfl_sync(0xffffffffu, vis.low, src);
+                    w.end = __shfl_sync(0xffffffffu, vis.end, src);
+                    const int wpos = __shfl_sync(0xffffffffu, pos, src), wt = __shfl_sync(0xffffffffu, my_tok, src),
+                              wh = __shfl_sync(0xffffffffu, my_head, src);
+                    float wm, wl, wo[D / 32];
+                    row_by_hand<D, Q8>(p, table, len, h, p.q + (int64_t)wt * p.q_stride + (int64_t)wh * dim, w, wpos,
+                                       p.slopes ? p.slopes[wh] : 0.0f, tiles, t0, t1, wm, wl, wo);
+                    const int wr = (r & ~31) + src;
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < D / 32; e++) {
+                        if (lane + 32 * e >= dim) continue;
+                        if (n_split > 1) __stcg(part + (int64_t)(lane + 32 * e) * R + wr, wo[e]);
+                        else store_out(p, (int64_t)wt * p.out_stride + (int64_t)wh * dim + lane + 32 * e, wl == 0.0f ? 0.0f : wo[e] / wl);
+                    }
+                    if (n_split > 1 && lane == 0) {
+                        __stcg(part + (int64_t)D * R + wr, wm);
+                        __stcg(part + (int64_t)(D + 1) * R + wr, wl);
+                    }
+                }
+            }
+        }
+    } else if (warp == MMA_WARP) {
+        // ------------------------------------ MMA ----------------------------------------------
+        int rc = 0;  // ring pieces taken
+        bool ok = true;
+        auto take = [&](int i) {  // wait for piece i of the ring
+            return mbar_wait(smem_u32(&kv_full[i % NS]), (i / NS) & 1, p.err, abort_flag);
+        };
+        auto issue_s = [&](int qt, int slot, int i) {  // S = Q K^T from piece i
+            if (lane == 0) {
+                const uint32_t qa = smem_u32(smem + L::Q + qt * L::Q_TILE), ka = smem_u32(smem + L::RING + (i % NS) * L::STAGE);
+                for (int ks = 0; ks < dim / 16; ks++)
+                    mma_f16(tmem + slot * L::SLOT, sdesc_sw128(qa + (ks >> 2) * (128 * 128) + (ks & 3) * 32),
+                            sdesc_sw128(ka + (ks >> 2) * (BN * 128) + (ks & 3) * 32), p.idesc_s, ks > 0);
+                mma_commit(smem_u32(&s_full[slot]));
+            }
+            __syncwarp();
+        };
+        auto issue_o = [&](int qt, int slot, int i, bool first) {  // O += P V from piece i
+            if (lane == 0) {
+                const uint32_t va = smem_u32(smem + L::RING + (i % NS) * L::STAGE);
+#pragma unroll
+                for (int ks = 0; ks < BN / 16; ks++)
+                    mma_f16_ts(tmem + L::O_COL + qt * D, tmem + slot * L::SLOT + 8 * ks,
+                               sdesc_sw128_mn(va + ks * 2048, BN * 128), p.idesc_o, !first || ks > 0);
+                mma_commit(smem_u32(&o_done[qt]));
+            }
+            __syncwarp();
+        };
+        auto release = [&](int i) {
+            if (lane == 0) mma_commit(smem_u32(&kv_empty[i % NS]));
+            __syncwarp();
+        };
+        // V rows past the sequence's end hold whatever the page holds: zeros
+        auto clean = [&](int i, int tile) {
+            const int j0 = tiles.at(t0 + tile) * BN;
+            if (Q8 || j0 + BN <= len) return;
+            uint8_t* va = smem + L::RING + (i % NS) * L::STAGE;
+            const int from = max(len - j0, 0);
+            for (int u = lane; u < (BN - from) * nh * 8; u += 32) {
+                const int c = u / ((BN - from) * 8), x = u - c * (BN - from) * 8;
+                *reinterpret_cast<uint4*>(va + c * (BN * 128) + from * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        for (int qt = 0; qt < q_act && ok; qt++) ok = mbar_wait(smem_u32(&q_full[qt]), 0, p.err, abort_flag);
+        if (ok && (ok = take(0))) {
+            tc_fence_after();
+            for (int qt = 0; qt < q_act; qt++) issue_s(qt, QT == 2 ? qt : 0, 0);
+            release(0);
+            rc = 1;
+            for (int i = 0; i < nt && ok; i++) {
+                if (QT == 2) {
+                    const int pv = 2 * i + 1, pk = 2 * i + 2;
+                    if (!(ok = take(pv))) break;
+                    clean(pv, i);
+                    if (i + 1 < nt && !(ok = take(pk))) break;
+                    for (int qt = 0; qt < q_act && ok; qt++) {
+                        if (!(ok = mbar_wait(smem_u32(&p_full[qt]), i & 1, p.err, abort_flag))) break;
+                        tc_fence_after();
+                        issue_o(qt, qt, pv, i == 0);
+                        if (i + 1 < nt) issue_s(qt, qt, pk);
+                    }
+                    if (!ok) break;
+                    release(pv);
+                    if (i + 1 < nt) release(pk);
+                    rc = i + 1 < nt ? pk + 1 : pv + 1;
+                } else {
+                    if (i + 1 < nt) {
+                        if (!(ok = take(rc))) break;
+                        tc_fence_after();
+                        issue_s(0, (i + 1) & 1, rc);
+                        release(rc);
+                        rc++;
+                    }
+                    if (!(ok = take(rc))) break;
+                    clean(rc, i);
+                    if (!(ok = mbar_wait(smem_u32(&p_full[i & 1]), (i >> 1) & 1, p.err, abort_flag))) break;
+                    tc_fence_after();
+                    issue_o(0, i & 1, rc, i == 0);
+                    release(rc);
+                    rc++;
+                }
+            }
+        }
+        // every product issued is complete before the accumulators are freed (the softmax warps
+        // have seen the last one finish, except after an abort)
+        if (lane == 0) mma_commit(smem_u32(mma_idle));
+        __syncwarp();
+        mbar_drain(smem_u32(mma_idle), 0, p.err);
+    } else {
+        // ------------------------------------ loader -------------------------------------------
+        int i = 0;
+#ifdef SYN_TEST_STALL
+        const int n_pieces = 0;  // timeout-test build: no tile is ever loaded, so the waits run out
+#else
+        const int n_pieces = 2 * nt;
+#endif
+        const uint32_t bytes = (uint32_t)nh * BN * 128;
+        if (!Q8) {
+            const int box = min(BN, 1 << p.c.page_shift), n_box = BN / box;
+            for (; i < n_pieces; i++) {
+                const int st = i % NS;
+                const bool is_v = piece_v(i);
+                const int j = tiles.at(t0 + piece_tile(i)) * BN + lane * box;
+                // pages past the end, and ids outside the pool, become the page after the last,
+                // which the copy fills with zeros
+                int id = (int)p.c.n_pages;
+                if (lane < n_box && j < len) {
+                    const int x = table[j >> p.c.page_shift];
+                    if ((unsigned)x < (unsigned long long)p.c.n_pages) id = x;
+                    else record_error(p.err, SYN_DEVERR_BOUNDS);
+                }
+                if (!mbar_wait(smem_u32(&kv_empty[st]), ((i / NS) & 1) ^ 1, p.err, abort_flag)) break;
+                const uint32_t full = smem_u32(&kv_full[st]);
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                __syncwarp();
+                if (lane < n_box && SYN_IN_BOUNDS((lane + 1) * box * 128 + (nh - 1) * BN * 128 <= L::STAGE && id >= 0)) {
+                    const uint32_t dst = smem_u32(smem + L::RING + st * L::STAGE) + lane * box * 128;
+                    for (int c = 0; c < nh; c++)
+                        tma_load_4d(dst + c * (BN * 128), is_v ? &vmap : &kmap, 64 * c, j & ((1 << p.c.page_shift) - 1), h, id, full);
+                }
+                __syncwarp();
+            }
+            // the tiles still in flight (issued, not consumed: only after an abort) land first
+            for (int u = max(0, i - NS); u < i; u++) mbar_drain(smem_u32(&kv_full[u % NS]), (u / NS) & 1, p.err);
+        } else {
+            // 128 threads: 16 codes of a row at a time, the next piece's loads before this one's work
+            constexpr int MOST = BN * (D / 16) / 128;
+            const int lt = tid - 32 * LOAD_WARP;
+            const int per_row = dim >> 4, n = BN * per_row;
+            const int64_t plane = (int64_t)dim << p.c.page_shift;
+            uint4 code[MOST];
+            uint16_t scale[MOST];
+            auto load = [&](int piece) {
+                const uint8_t* pool = (piece_v(piece) ? p.c.v : p.c.k) + (int64_t)h * p.c.tile;
+                const int j0 = tiles.at(t0 + piece_tile(piece)) * BN;
+#pragma unroll
+                for (int u = 0; u < MOST; u++) {
+                    const int idx = u * 128 + lt;
+                    code[u] = make_uint4(0, 0, 0, 0);
+                    scale[u] = 0;
+                    if (idx >= n) continue;
+                    const int row = idx / per_row, x = idx - row * per_row, j = j0 + row;
+                    if (j >= len) continue;
+                    const int id = table[j >> p.c.page_shift];
+                    if ((unsigned)id >= (unsigned long long)p.c.n_pages) {
+                        record_error(p.err, SYN_DEVERR_BOUNDS);
+                        continue;
+                    }
+                    const int cell = j & ((1 << p.c.page_shift) - 1);
+                    const uint8_t* base = pool + (int64_t)id * p.c.page_stride;
+                    code[u] = *reinterpret_cast<const uint4*>(base + (int64_t)cell * dim + 16 * x);
+                    scale[u] = *reinterpret_cast<const uint16_t*>(base + plane + 2 * ((int64_t)cell * (dim >> 5) + (x >> 1)));
+                }
+            };
+            if (n_pieces > 0) load(0);
+            for (; i < n_pieces; i++) {
+                const int st = i % NS;
+                if (!mbar_wait(smem_u32(&kv_empty[st]), ((i / NS) & 1) ^ 1, p.err, abort_flag)) break;
+                uint8_t* dst = smem + L::RING + st * L::STAGE;
+#pragma unroll
+                for (int u = 0; u < MOST; u++) {
+                    const int idx = u * 128 + lt;
+                    if (idx >= n) continue;
+                    const int row = idx / per_row, x = idx - row * per_row;
+                    // a byte b becomes 1024 + b by a permute with 0x64; value = scale * code, the one
+                    // rounding of the expansion (relative 2^-11, like that of p)
+                    const __half2 d = __half2half2(__ushort_as_half(scale[u])), k1152 = __float2half2_rn(1152.0f);
+                    const uint32_t cw[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
+                    uint32_t w[8];
+#pragma unroll
+                    for (int y = 0; y < 4; y++) {
+                        const uint32_t z = cw[y] ^ 0x80808080u;
+                        uint32_t a = __byte_perm(z, 0x64646464u, 0x4140), e = __byte_perm(z, 0x64646464u, 0x4342);
+                        const __half2 ha = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&a), k1152), d);
+                        const __half2 he = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&e), k1152), d);
+                        w[2 * y] = *reinterpret_cast<const uint32_t*>(&ha);
+                        w[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&he);
+                    }
+                    uint8_t* to = dst + (x >> 2) * (BN * 128) + row * 128;
+                    const int c = (2 * x) & 7;
+                    *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+                if (i + 1 < n_pieces) load(i + 1);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&kv_full[st]));
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (n_split == 1) return;
+    // ---- the last of the item's CTAs joins the partials ------------------------------------
+    const int item = (int)b;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        const int before = atomicAdd(&p.count[item], 1);
+        info[0] = before == n_split - 1;
+        if (before == n_split - 1) p.count[item] = 0;  // ready for the next call
+    }
+    __syncthreads();
+    if (!info[0] || *abort_flag) return;
+    __threadfence();
+    const float* base = p.part + (int64_t)(blockIdx.x - sp) * R * (D + 2);
+    for (int u = tid; u < rows * dim; u += THREADS) {
+        const int e = u / rows, r = u - e * rows;
+        float mx = -INFINITY, sum = 0.0f, acc = 0.0f;
+        for (int x = 0; x < n_split; x++) {
+            const float* q = base + (int64_t)x * R * (D + 2);
+            const float pm = __ldcg(q + (int64_t)D * R + r), ps = __ldcg(q + (int64_t)(D + 1) * R + r), po = __ldcg(q + (int64_t)e * R + r);
+            const float nm = fmaxf(mx, pm), ms = nm == -INFINITY ? 0.0f : nm;
+            const float fa = ex2(mx - ms), fb = ex2(pm - ms);
+            acc = acc * fa + po * fb;
+            sum = sum * fa + ps * fb;
+            mx = nm;
+        }
+        const int t = (row0 + r) / p.g;
+        store_out(p, (int64_t)(tok0 + t) * p.out_stride + (int64_t)(h * p.g + row0 + r - t * p.g) * dim + e, sum == 0.0f ? 0.0f : acc / sum);
+    }
+}
+
+// ---- host side ---------------------------------------------------------------------------
+
+template <int D, bool Q8, bool MOD>
+static cudaError_t run_prefill(const CUtensorMap& km, const CUtensorMap& vm, const PrefillParams& p, int grid, cudaStream_t s) {
+    auto kern = k_attn_prefill<D, Q8, MOD>;
+    constexpr int smem = 1024 + PreShape<D>::BYTES;
+    static_assert(smem <= 232448, "shared memory per CTA exceeds 227 KB");
+    static ResidentCtas resident;
+    int n;
+    const cudaError_t e = resident.get(reinterpret_cast<const void*>(kern), PRE_THREADS<D, Q8>, smem, &n);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, PRE_THREADS<D, Q8>, smem, s>>>(km, vm, p);
+    return cudaGetLastError();
+}
+
+static int prefill_rows(int dim) { return dim <= 128 ? 256 : 128; }
+
+// at most one split item per SM has a counter, one CTA per SM a partial
+int64_t prefill_part_floats(int dim, int sms) {
+    return (int64_t)sms * prefill_rows(dim) * ((dim <= 64 ? 64 : dim <= 128 ? 128 : 256) + 2);
+}
+
+cudaError_t launch_attn_prefill(const KvCache& c, const AttnDesc& a, int64_t n_seq, int64_t n_tok, const void* q,
+                                const int32_t* starts, const int32_t* pages, int64_t max_pages, const int32_t* lens,
+                                void* out, float* part, int* count, bool split, int* err, int sms, int* launches,
+                                cudaStream_t s) {
+    CUtensorMap km, vm;
+    const int D = c.dim <= 64 ? 64 : c.dim <= 128 ? 128 : 256, BN = D <= 128 ? 128 : 64;
+    if (!c.q8) {
+        PFN_encodeTiled encode = get_encode();
+        if (!encode) return cudaErrorNotSupported;
+        const int64_t page = int64_t(1) << c.page_shift;
+        cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)page, (cuuint64_t)c.n_kv, (cuuint64_t)c.n_pages};
+        cuuint64_t strides[3] = {(cuuint64_t)c.dim * 2, (cuuint64_t)c.tile, (cuuint64_t)c.page_stride};
+        cuuint32_t box[4] = {64, (cuuint32_t)std::min<int64_t>(BN, page), 1, 1}, estr[4] = {1, 1, 1, 1};
+        for (int i = 0; i < 2; i++)
+            if (encode(i ? &vm : &km, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, i ? c.v : c.k, dims, strides, box, estr,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return cudaErrorInvalidValue;
+    } else {
+        km = vm = CUtensorMap{};  // unused
+    }
+    PrefillParams p;
+    p.c = c;
+    p.q = static_cast<const __half*>(q);
+    p.q_stride = a.q_stride;
+    p.out_stride = a.out_stride;
+    p.out = out;
+    p.max_pages = max_pages;
+    p.slopes = a.slopes;
+    p.first = a.first;
+    p.part = part;
+    p.count = count;
+    p.err = err;
+    p.scale = a.scale;
+    p.cap = a.cap;
+    p.n_tok = (int)n_tok;
+    p.g = a.n_heads / c.n_kv;
+    p.window = a.window;
+    p.out_f16 = a.out_f16;
+    p.sms = sms;
+    p.split = split;
+    // kind::f16: D fp32, A and B fp16, M = 128; S: B K-major, N = BN; O: B MN-major, N = dim
+    p.idesc_s = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | (8u << 24);
+    p.idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(c.dim >> 3) << 17) | (8u << 24);
+    const int R = prefill_rows(c.dim);
+    // (a scale that is not positive takes the general path: the fast one scales the maximum)
+    const bool mod = a.cap > 0.0f || a.slopes || !(a.scale > 0.0f);
+    for (int64_t s0 = 0; s0 < n_seq; s0 += PRE_MAX_SEQ) {
+        p.n_seq = (int)std::min<int64_t>(PRE_MAX_SEQ, n_seq - s0);
+        p.starts = starts + s0;
+        p.pages = pages + s0 * max_pages;
+        p.lens = lens + s0;
+        p.prefix = a.prefix ? a.prefix + s0 : nullptr;
+        // every item has a CTA, and the splits of few items at most one per SM
+        const int64_t items = ((n_tok * p.g + R - 1) / R + p.n_seq) * c.n_kv;
+        const int64_t grid = std::max<int64_t>(items, sms);
+        if (grid > INT_MAX) return cudaErrorInvalidValue;
+        cudaError_t e;
+#define SYN_PRE(D)                                                                                              \
+    (c.q8 ? (mod ? run_prefill<D, true, true>(km, vm, p, (int)grid, s) : run_prefill<D, true, false>(km, vm, p, (int)grid, s)) \
+          : (mod ? run_prefill<D, false, true>(km, vm, p, (int)grid, s) : run_prefill<D, false, false>(km, vm, p, (int)grid, s)))
+        e = D == 64 ? SYN_PRE(64) : D == 128 ? SYN_PRE(128) : SYN_PRE(256);
+#undef SYN_PRE
+        if (e != cudaSuccess) return e;
+        (*launches)++;
+    }
+    return cudaSuccess;
+}
+
+#ifdef SYN_DEBUG
+SYN_BOUNDS_READER(debug_bounds_attn_prefill)
+#endif
+
+}  // namespace syn

@@ -97,6 +97,15 @@ cudaError_t launch_attn_decode(const KvCache& c, const AttnDesc& a, int64_t n_se
 int64_t decode_count_words(int64_t n_seq, int n_heads, int n_kv, int dim);
 int64_t decode_part_floats(int n_heads, int n_kv, int dim, int sms);
 
+// Several new tokens of each sequence (packed, starts[s] .. starts[s+1]).  part:
+// prefill_part_floats; count: at least `sms` words, as above.  split: items may be split
+// between CTAs.
+cudaError_t launch_attn_prefill(const KvCache& c, const AttnDesc& a, int64_t n_seq, int64_t n_tok, const void* q,
+                                const int32_t* starts, const int32_t* pages, int64_t max_pages, const int32_t* lens,
+                                void* out, float* part, int* count, bool split, int* err, int sms, int* launches,
+                                cudaStream_t s);
+int64_t prefill_part_floats(int dim, int sms);
+
 // What the C entry points of api_attn.cu share with api.cu: the SMs of this call and the
 // status words ([0]) of the current device; the attention's workspace of (device, stream), at
 // least `zeroed` bytes that were zero when it was allocated, then (from byte *zeroed_at on) at
@@ -149,6 +158,7 @@ int debug_bounds_gemv_f16(int clear);
 int debug_bounds_gemm(int clear);
 int debug_bounds_kv_append(int clear);
 int debug_bounds_attn_decode(int clear);
+int debug_bounds_attn_prefill(int clear);
 cudaError_t launch_bounds_selftest(cudaStream_t s);
 #endif
 

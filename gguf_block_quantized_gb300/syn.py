@@ -133,6 +133,7 @@ EXPORTS += [
                              _vp]),
     ("syn_kv_read", _i32, [_P(KVCacheDesc), _i64, _vp, _vp, _vp, _vp]),
     ("syn_attn_decode", _i32, [_P(KVCacheDesc), _P(AttnDesc), _i64, _vp, _vp, _i64, _vp, _vp, _vp]),
+    ("syn_attn_prefill", _i32, [_P(KVCacheDesc), _P(AttnDesc), _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
 ]
 
 for _name, _res, _args in EXPORTS:
@@ -467,6 +468,24 @@ def prepare_attn_decode(cache: KVCache, q, pages, lens, out=None, scale=None, ca
 
 def attn_decode(cache: KVCache, q, pages, lens, out=None, **options):
     return prepare_attn_decode(cache, q, pages, lens, out, **options)()
+
+
+def prepare_attn_prefill(cache: KVCache, q, starts, pages, lens, out=None, scale=None, cap: float = 0.0,
+                         window: int = 0, slopes=None, prefix=None, first=None, stream=None) -> Prepared:
+    """syn_attn_prefill: q float16 (n_tok, n_heads, head_dim), starts int32 (n_seq + 1), the rest as for
+    prepare_attn_decode (first: one per token).  The call returns out."""
+    torch = _torch()
+    n_seq = lens.numel()
+    if starts.numel() != n_seq + 1:
+        raise ValueError("starts: one more than the sequences")
+    desc, qp, out, op = _attn_desc(cache, q, out, n_seq, pages, lens, scale, cap, window, slopes, prefix, first)
+    args = (ctypes.byref(cache.desc), ctypes.byref(desc), n_seq, q.shape[0], qp, _typed(starts, torch.int32, "starts"),
+            _typed(pages, torch.int32, "pages"), pages.shape[1], _typed(lens, torch.int32, "lens"), op, _stream(stream))
+    return Prepared("syn_attn_prefill", args, out, (cache, desc, q, starts, pages, lens, out, slopes, prefix, first))
+
+
+def attn_prefill(cache: KVCache, q, starts, pages, lens, out=None, **options):
+    return prepare_attn_prefill(cache, q, starts, pages, lens, out, **options)()
 
 
 def block_sums(t: int, W, n_out: int, n_in: int, Xq, n_tok: int, stream=None):

@@ -455,6 +455,23 @@ SYN_API int syn_attn_decode(const syn_kv_cache* cache, const syn_attn* attn, int
                             const int32_t* pages, int64_t max_pages, const int32_t* lens, void* out,
                             syn_stream_t stream);
 
+/* Attention of several new tokens of each sequence: sequence s has the tokens starts[s] ..
+ * starts[s+1] - 1 (starts: n_seq + 1, ascending from 0, starts[n_seq] = n_tok), the last of its
+ * lens[s] rows (all of them in the cache: append first), so token i of its n stands at position
+ * lens[s] - n + i.  q: n_tok x n_heads x head_dim fp16; out likewise, fp32 or fp16.  A sequence may
+ * have no new token; a token before position 0 (lens[s] < n) sees nothing.
+ * The products run on the tensor cores with fp16 operands: p and (Q8_0) the expanded key and value
+ * are rounded to fp16 once, scores, sums and maxima are fp32, so an output of either type is exact to
+ * about 2^-11 of its row's values, not to fp32's last place (syn_attn_decode is).  A row whose
+ * sums are not finite is computed again from the keys it sees alone, far slower.
+ * Few tokens over a long cache are split over its length (not in deterministic mode, in which a
+ * token's output does not depend on the other sequences of the call).  Workspace, alignment and
+ * errors as for syn_attn_decode; SYN_ERR_SHAPE also for n_tok * n_heads >= 2^31 - 1024.
+ * Asynchronous. */
+SYN_API int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_seq, int64_t n_tok,
+                             const void* q, const int32_t* starts, const int32_t* pages, int64_t max_pages,
+                             const int32_t* lens, void* out, syn_stream_t stream);
+
 /* ======================================================================================
  * GGUF container (host code; only syn_gguf_upload touches the GPU)
  *

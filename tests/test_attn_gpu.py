@@ -371,3 +371,174 @@ def test_append_bad_slot_is_not_followed(syn):
     rk, _ = syn.kv_read(c, slots)
     assert syn.device_status(clear=True) == syn.ERR_BOUNDS
     assert (rk[0] == 0).all() and torch.equal(rk[1], k[1].half())
+
+
+# ---- prefill -------------------------------------------------------------------------------
+
+# p is rounded to fp16 (relative 2^-11 at most), as are the expanded Q8_0 keys and values; a score
+# error e changes the output by at most 2 e max|v|.  F16: 2^-11 max|v| for p and 2^-20 (1 + A) max|v|
+# for fp32 scores; Q8_0: also 2^-11 A (keys, twice e) and 2^-11 (values).  An fp16 output adds half a
+# unit of its last place.
+def prefill_bound(t, size, vmax, out, f16):
+    b = vmax * 2.0 ** -11 + size * 2.0 ** -20
+    if t == Q8_0:
+        b = b + vmax * 2.0 ** -11 + 2 * size * 2.0 ** -11
+    return b + (np.abs(out) * 2.0 ** -11 + 2.0 ** -24 if f16 else 0)
+
+
+def run_prefill(syn, t, heads, kv, dim, page, lens, new, seed, scale=None, garbage=np.nan, dts=("float32", "float16"),
+                qscale=1.0, **opt):
+    import torch
+    rng = np.random.default_rng([t, heads, kv, dim, page, seed])
+    cache, pages, seqs = make_cache(syn, rng, t, kv, dim, page, lens, garbage=garbage)
+    n_tok = sum(new)
+    q = (qscale * rng.standard_normal((n_tok, heads, dim))).astype(np.float16)
+    kw, rows, first, pre, sl = options(rng, lens, new, heads, **opt)
+    sc = dim ** -0.5 if scale is None else scale
+    ref, size = reference(q, seqs, rows, first, pre, kw["window"], sc, kw["cap"], sl)
+    vmax = np.concatenate([np.full((n, 1, 1), np.abs(v).max() if v.size else 0.0) for n, (_, v) in zip(new, seqs)])
+    starts = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    ld = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for dt in dts:
+        out = torch.full((n_tok, heads, dim), float("nan"), dtype=getattr(torch, dt), device="cuda")
+        got = syn.attn_prefill(cache, torch.from_numpy(q).cuda(), starts, pages, ld, out, scale=scale, **kw)
+        got = got.double().cpu().numpy()
+        err, bound = np.abs(got - ref), prefill_bound(t, size, vmax, ref, dt == "float16")
+        assert (err <= bound).all(), (np.nanmax(err / np.maximum(bound, 1e-30)), np.argwhere(~(err <= bound))[:5])
+    assert syn.device_status() == syn.OK
+
+
+@pytest.mark.parametrize("t", [F16, Q8_0])
+@pytest.mark.parametrize("heads,kv,dim,page", [(8, 2, 64, 16), (4, 4, 32, 8), (12, 1, 96, 32), (8, 1, 128, 64),
+                                               (5, 1, 128, 8), (3, 1, 160, 16), (4, 2, 256, 128), (24, 1, 64, 256)])
+def test_prefill_shapes(syn, t, heads, kv, dim, page):
+    run_prefill(syn, t, heads, kv, dim, page, [1, 17, 128, 129, 300, 5, 64, 0], [1, 17, 40, 129, 33, 0, 2, 0], 1)
+
+
+@pytest.mark.parametrize("t", [F16, Q8_0])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("opt", [{"cap": 5.0}, {"window": 37}, {"window": 1}, {"slopes": True}, {"docs": True}, {"prefix": True},
+                                 {"window": 140, "prefix": True}, {"cap": 20.0, "window": 100, "prefix": True, "slopes": True,
+                                                                   "docs": True}])
+def test_prefill_options(syn, t, dim, opt):
+    run_prefill(syn, t, 4, 2, dim, 16, [150, 400, 31, 270], [150, 60, 31, 1], 2, scale=0.1, **opt)
+
+
+@pytest.mark.parametrize("t", [F16, Q8_0])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prefill_split_long(syn, t, dim):
+    """A few tokens over a long cache: the item's keys are split between CTAs and joined."""
+    run_prefill(syn, t, 4, 2, dim, 64, [9001, 2000], [5, 1], 3)
+
+
+def test_prefill_growing_maxima(syn):
+    """Scores that grow along the row by far more than the maximum's lag."""
+    import torch
+    rng = np.random.default_rng(12)
+    dim, page, n = 64, 16, 700
+    k = rng.standard_normal((n, 1, dim)) * (1 + np.arange(n)[:, None, None] / 20.0)
+    v = rng.standard_normal((n, 1, dim))
+    q = rng.standard_normal((30, 2, dim)).astype(np.float16)
+    cache = syn.KVCache.empty(F16, 1, dim, page, 44)
+    kp = np.zeros((44 * page, 1, dim), np.float16)
+    vp = np.zeros_like(kp)
+    kp[:n], vp[:n] = k, v
+    cache.k.copy_(torch.from_numpy(kp.reshape(44, page, 1, dim).transpose(0, 2, 1, 3).copy()))
+    cache.v.copy_(torch.from_numpy(vp.reshape(44, page, 1, dim).transpose(0, 2, 1, 3).copy()))
+    pages = torch.arange(44, dtype=torch.int32, device="cuda").view(1, -1)
+    pos = np.arange(n - 30, n)
+    ref, size = attn_ref.attention(q, kp[:n], vp[:n], pos, np.zeros(30), 0, 0, 1.0, 0.0, None)
+    got = syn.attn_prefill(cache, torch.from_numpy(q).cuda(), torch.tensor([0, 30], dtype=torch.int32, device="cuda"), pages,
+                           torch.tensor([n], dtype=torch.int32, device="cuda"), scale=1.0).double().cpu().numpy()
+    assert (np.abs(got - ref) <= prefill_bound(F16, size, np.abs(vp).max(), ref, False)).all()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2])
+def test_prefill_scales_that_are_not_positive(syn, scale):
+    run_prefill(syn, F16, 2, 1, 64, 16, [200], [70], 4, scale=scale)
+
+
+@pytest.mark.parametrize("t", [F16, Q8_0])
+@pytest.mark.parametrize("split", [False, True])
+def test_prefill_nonfinite_values_stay_where_they_are_seen(syn, t, split):
+    """A NaN or infinity in a cached row reaches the rows that see it and no other, although they
+    share tiles."""
+    import torch
+    rng = np.random.default_rng(14)
+    heads, kv, dim, page, n, new = 4, 2, 64, 16, 1500 if split else 300, 40
+    cache, pages, seqs = make_cache(syn, rng, t, kv, dim, page, [n])
+    q = rng.standard_normal((new, heads, dim)).astype(np.float16)
+    bad = n - 20  # seen by the last 20 tokens
+    pg, cell = int(pages[0, bad // page]), bad % page
+    if t == F16:
+        cache.v[pg, :, cell, 5] = float("inf")
+        cache.k[pg, 0, cell, 3] = float("nan")
+    else:
+        for pool, code in ((cache.v, 0x7C00), (cache.k, 0x7E00)):
+            at = page * dim + cell * dim // 16
+            pool[pg, 0, at:at + 2] = torch.tensor([code & 255, code >> 8], dtype=torch.uint8, device="cuda")
+    k, v = seqs[0]
+    pos = np.arange(n - new, n)
+    ref, size = attn_ref.attention(q, k, v, pos, np.zeros(new), 0, 0, dim ** -0.5, 0.0, None)
+    got = syn.attn_prefill(cache, torch.from_numpy(q).cuda(), torch.tensor([0, new], dtype=torch.int32, device="cuda"), pages,
+                           torch.tensor([n], dtype=torch.int32, device="cuda")).double().cpu().numpy()
+    before = pos < bad
+    assert (np.abs(got - ref) <= prefill_bound(t, size, np.abs(v).max(), ref, False))[before].all()
+    assert np.isnan(got[~before][:, :heads // kv]).all()  # a NaN key: every value of the heads that see it
+    if t == F16:
+        assert not np.isfinite(got[~before][:, heads // kv:, 5]).any() and np.isfinite(got[~before][:, heads // kv:, :5]).all()
+    assert syn.device_status() == syn.OK
+
+
+def test_prefill_matches_decode_and_batches(syn):
+    """One new token gives what the one-token call gives; in deterministic mode a sequence's rows have
+    the same bits alone and in a batch."""
+    import torch
+    rng = np.random.default_rng(15)
+    heads, kv, dim, page = 8, 2, 128, 32
+    lens, new = [700, 90, 2000], [200, 90, 1]
+    cache, pages, _ = make_cache(syn, rng, F16, kv, dim, page, lens)
+    q = torch.from_numpy(rng.standard_normal((sum(new), heads, dim)).astype(np.float16)).cuda()
+    st = np.concatenate([[0], np.cumsum(new)])
+    starts, ld = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (st, lens))
+    old = syn.set_deterministic(True)
+    try:
+        both = syn.attn_prefill(cache, q, starts, pages, ld)
+        for s in range(3):
+            one = syn.attn_prefill(cache, q[st[s]:st[s + 1]].contiguous(), torch.tensor([0, new[s]], dtype=torch.int32, device="cuda"),
+                                   pages[s:s + 1].contiguous(), ld[s:s + 1].contiguous())
+            assert torch.equal(one, both[st[s]:st[s + 1]])
+    finally:
+        syn.set_deterministic(old)
+    last = syn.attn_decode(cache, q[-1:].contiguous(), pages[2:].contiguous(), ld[2:].contiguous())
+    assert (last[0] - both[-1]).abs().max().item() < 2.0 ** -11 * 6
+
+
+def test_prefill_strides_streams_and_bad_pages(syn):
+    import torch
+    rng = np.random.default_rng(16)
+    heads, kv, dim, page = 4, 2, 64, 16
+    lens, new = [90, 200], [30, 77]
+    cache, pages, seqs = make_cache(syn, rng, F16, kv, dim, page, lens, garbage=np.inf)
+    both = torch.stack([cache.k, cache.v], 1)
+    mixed = syn.KVCache(F16, kv, dim, page, both[:, 0], both[:, 1])
+    wide = torch.randn((107, heads + 4, dim), device="cuda").half()
+    wide_out = torch.zeros((107, heads + 8, dim), device="cuda")
+    q = wide[:, 2:2 + heads]
+    starts = torch.tensor([0, 30, 107], dtype=torch.int32, device="cuda")
+    ld = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    rows = [np.arange(60, 90), np.arange(123, 200)]
+    ref, size = reference(q.cpu().numpy(), seqs, rows, [np.zeros(30), np.zeros(77)], [0, 0], 0, dim ** -0.5, 0.0, None)
+    vmax = max(np.abs(v).max() for _, v in seqs)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    syn.attn_prefill(mixed, q, starts, pages, ld, wide_out[:, 3:3 + heads], stream=side)
+    side.synchronize()
+    got = wide_out[:, 3:3 + heads].double().cpu().numpy()
+    assert (np.abs(got - ref) <= prefill_bound(F16, size, vmax, ref, False)).all()
+    assert (wide_out[:, :3] == 0).all() and (wide_out[:, 3 + heads:] == 0).all()
+    p = pages.clone()
+    p[0, 2] = 10 ** 6
+    got = syn.attn_prefill(mixed, q, starts, p, ld).double().cpu().numpy()
+    assert syn.device_status(clear=True) == syn.ERR_BOUNDS
+    assert (np.abs(got - ref) <= prefill_bound(F16, size, vmax, ref, False))[30:].all()

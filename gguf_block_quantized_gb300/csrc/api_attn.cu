@@ -152,7 +152,7 @@ int syn_kv_append(const syn_kv_cache* cache, const syn_rope* rope, int64_t n_tok
     r.halves = rope->layout == SYN_ROPE_HALVES;
     r.magnitude = rope->magnitude;
     rc = check_cuda(syn::launch_kv_append(c, r, n_tok, q, q_stride, n_heads, q_out, k, k_stride, v, v_stride, pos, slots,
-                                          words, reinterpret_cast<cudaStream_t>(stream)));
+                                          words, sms, reinterpret_cast<cudaStream_t>(stream)));
     if (rc == SYN_OK) syn::note_launches(1);
     return rc;
 }

@@ -83,7 +83,8 @@ struct AttnDesc {
 
 cudaError_t launch_kv_append(const KvCache& c, const RopeDesc& r, int64_t n_tok, const float* q, int64_t q_stride,
                              int n_heads, void* q_out, const float* k, int64_t k_stride, const float* v,
-                             int64_t v_stride, const int32_t* pos, const int64_t* slots, int* err, cudaStream_t s);
+                             int64_t v_stride, const int32_t* pos, const int64_t* slots, int* err, int sms,
+                             cudaStream_t s);
 cudaError_t launch_kv_read(const KvCache& c, int64_t n, const int64_t* slots, void* k, void* v, int* err, int sms,
                            cudaStream_t s);
 

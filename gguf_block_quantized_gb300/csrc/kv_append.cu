@@ -8,18 +8,24 @@
 // the reduced angle is as exact at position 10^6 as at 1 (an fp32 product p * f loses
 // p * 2^-24 radians).  32 bits of the fraction go to sincospif.
 //
-// Bound: HBM (4 B read and about 2 B written per value).  One CTA per token: the n_rot/2 sines
-// are computed once for all heads (a thread per pair), while the rows' loads are in flight.  A
-// thread takes 4 consecutive values (16-byte loads, 8-byte stores, both coalesced); where the
-// other half of a pair lies n_rot/2 values away it is loaded again, from L1.  A Q8_0 block is 8
+// Bound: HBM (4 B read and about 2 B written per value).  Persistent CTAs: one warp runs ahead,
+// computing each token's n_rot/2 sines once for all heads and copying its rows (cp.async.bulk, in
+// pieces of up to 16 KB) into a ring in shared memory; eight warps take 4 consecutive values a
+// thread from there, rotate, and store them as 8 bytes (a warp's stores are contiguous).  So about
+// 150 KB of loads are in flight on an SM whatever the threads wait for.  A Q8_0 block is 8
 // neighbouring lanes, its amax three shuffles.
+#include <algorithm>
+
 #include "kernels.h"
 #include "kv_cache.cuh"
 
 namespace syn {
 
-constexpr int APPEND_THREADS = 256;
-constexpr int APPEND_DEEP = 4;  // units whose loads a thread has in flight
+constexpr int APPEND_WARPS = 8;                          // that rotate and store
+constexpr int APPEND_THREADS = 32 * (APPEND_WARPS + 1);  // and the one that loads
+constexpr int APPEND_STAGE = 16384;                      // a piece: whole rows
+constexpr int APPEND_STAGES = 4;
+constexpr int APPEND_CTAS_PER_SM = 3;                    // what the rings leave room for
 
 struct AppendParams {
     KvCache c;
@@ -30,15 +36,24 @@ struct AppendParams {
     const int64_t* slots;
     const uint64_t* turns;
     const uint8_t* axis;
-    int64_t n_tok;
+    int64_t n_tok, n_items;  // an item: the pieces of one of `parts` parts of a token
     int* err;
     int n_heads, n_rot, n_axes, halves;
+    int piece_rows, q_pieces, kv_pieces, parts;
     float magnitude;
 };
 
 __device__ __forceinline__ uint2 pack_half4(const float4& x) {
     const __half2 a = __floats2half2_rn(x.x, x.y), b = __floats2half2_rn(x.z, x.w);
     return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// round half away from zero of x / d: from the rounded reciprocal, whose quotient is off by less
+// than 2^-21 of itself (< 2^-14 below 128), and by a division where that could cross a tie
+__device__ __forceinline__ float q8_code(float x, float d, float inv) {
+    float y = fabsf(x) * inv;
+    if (fabsf(y - floorf(y) - 0.5f) < 6.2e-5f) y = fabsf(x) / d;
+    return copysignf(fminf(floorf(y + 0.5f), 127.0f), x);  // (the stored scale can lie below amax/127)
 }
 
 // 4 values of a Q8_0 block held by 8 neighbouring lanes: codes (packed) and the block's scale.
@@ -51,112 +66,180 @@ __device__ __forceinline__ uint32_t q8_codes(const float4& x, unsigned short& sc
     for (int o = 1; o < 8; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     const __half d = __float2half_rn(a / 127.0f);
     const float df = __half2float(d);
-    scale = df < INFINITY ? __half_as_ushort(d) : (unsigned short)0x7FFF;
-    const float v[4] = {x.x, x.y, x.z, x.w};
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        // round half away from zero (roundf), as the format's encoder does; the stored scale
-        // can lie below amax/127, so the code is clamped
-        float r = df > 0.0f && df < INFINITY ? roundf(v[i] / df) : 0.0f;
-        r = fminf(fmaxf(r, -127.0f), 127.0f);
-        w |= (uint32_t)(uint8_t)(int8_t)(int)r << (8 * i);
-    }
-    return w;
+    const bool fine = df < INFINITY;
+    scale = fine ? __half_as_ushort(d) : (unsigned short)0x7FFF;
+    if (!fine || df == 0.0f) return 0u;
+    const float inv = 1.0f / df;
+    const int c0 = (int)q8_code(x.x, df, inv), c1 = (int)q8_code(x.y, df, inv), c2 = (int)q8_code(x.z, df, inv),
+              c3 = (int)q8_code(x.w, df, inv);
+    return (uint32_t)(c0 & 255) | (uint32_t)(c1 & 255) << 8 | (uint32_t)(c2 & 255) << 16 | (uint32_t)(c3 & 255) << 24;
 }
 
-__global__ void __launch_bounds__(APPEND_THREADS) k_kv_append(const AppendParams p) {
-    __shared__ float2 cs[128];  // (cos, sin) of each pair, times the magnitude; n_rot <= 256
-    const int64_t t = blockIdx.x;
-    const int tid = threadIdx.x;
-    const int dim = p.c.dim, per_row = dim >> 2;  // 4-value units per row
-    const int rows = p.n_heads + 2 * p.c.n_kv, total = rows * per_row;
-    const int half_rot = p.n_rot >> 1;
-    const int64_t slot = p.slots[t];
-    const int64_t page = slot >> p.c.page_shift;
-    const int cell = (int)(slot & (((int64_t)1 << p.c.page_shift) - 1));
-    bool store = slot >= 0;
-    if (store && page >= p.c.n_pages) {
-        if (tid == 0) record_error(p.err, SYN_DEVERR_BOUNDS);
-        store = false;
-    }
-    const float* qrow = p.n_heads ? p.q + t * p.q_stride : nullptr;
-    const float* krow = p.k + t * p.k_stride;
-    const float* vrow = p.v + t * p.v_stride;
+struct AppendSmem {
+    uint8_t ring[APPEND_STAGES][APPEND_STAGE];
+    float2 cs[2][128];  // (cos, sin) of each pair, times the magnitude, of two items; n_rot <= 256
+    uint64_t full[APPEND_STAGES], empty[APPEND_STAGES], cs_full[2], cs_empty[2];
+    int abort;
+};
 
-    // (lanes past the end repeat the last unit's loads and take part in the shuffles)
-    for (int base = 0; base < total; base += APPEND_THREADS * APPEND_DEEP) {
-        float4 x[APPEND_DEEP], y[APPEND_DEEP];
-        int row[APPEND_DEEP], e[APPEND_DEEP];
-#pragma unroll
-        for (int i = 0; i < APPEND_DEEP; i++) {
-            const int u = min(base + i * APPEND_THREADS + tid, total - 1);
-            row[i] = u / per_row;
-            e[i] = (u - row[i] * per_row) << 2;
-            const bool is_q = row[i] < p.n_heads, is_v = row[i] >= p.n_heads + p.c.n_kv;
-            const float* src = is_q ? qrow + (int64_t)row[i] * dim
-                             : is_v ? vrow + (int64_t)(row[i] - p.n_heads - p.c.n_kv) * dim
-                                    : krow + (int64_t)(row[i] - p.n_heads) * dim;
-            if (base + i * APPEND_THREADS >= total) continue;  // (the same for the whole CTA)
-            x[i] = *reinterpret_cast<const float4*>(src + e[i]);
-            y[i] = x[i];
-            if (p.halves && !is_v && e[i] < p.n_rot)
-                y[i] = *reinterpret_cast<const float4*>(src + (e[i] < half_rot ? e[i] + half_rot : e[i] - half_rot));
+// The pieces of a token, in order: q rows, k rows, v rows, piece_rows at a time.
+struct Piece {
+    int kind, row, rows;  // kind 0 q, 1 k, 2 v
+};
+__device__ __forceinline__ Piece piece_of(const AppendParams& p, int i) {
+    Piece x;
+    x.kind = i < p.q_pieces ? 0 : i < p.q_pieces + p.kv_pieces ? 1 : 2;
+    x.row = (i - (x.kind == 0 ? 0 : x.kind == 1 ? p.q_pieces : p.q_pieces + p.kv_pieces)) * p.piece_rows;
+    x.rows = min(p.piece_rows, (x.kind == 0 ? p.n_heads : p.c.n_kv) - x.row);
+    return x;
+}
+
+template <bool Q8>
+__global__ void __launch_bounds__(APPEND_THREADS, APPEND_CTAS_PER_SM) k_kv_append(const AppendParams p) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    AppendSmem& sm = *reinterpret_cast<AppendSmem*>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int dim = p.c.dim, per_row = dim >> 2;  // 4-value units per row
+    const int half_rot = p.n_rot >> 1, pieces = p.q_pieces + 2 * p.kv_pieces;
+    volatile int* abort_flag = &sm.abort;
+    if (tid == 0) {
+        for (int i = 0; i < APPEND_STAGES; i++) {
+            mbar_init(smem_u32(&sm.full[i]), 1);
+            mbar_init(smem_u32(&sm.empty[i]), APPEND_WARPS);
         }
-        if (base == 0) {
-            for (int i = tid; i < half_rot; i += APPEND_THREADS) {
-                const int ax = p.axis ? min((int)p.axis[i], p.n_axes - 1) : 0;
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_u32(&sm.cs_full[i]), 1);
+            mbar_init(smem_u32(&sm.cs_empty[i]), APPEND_WARPS);
+        }
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+
+    int n = 0, it = 0;  // pieces and items of this CTA so far
+    if (warp == APPEND_WARPS) {
+        // ---- loads and sines, ahead of the others ------------------------------------------
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < p.n_items && ok; w += gridDim.x, it++) {
+            const int64_t t = w / p.parts;
+            const int part = (int)(w - t * p.parts);
+            const int i0 = pieces * part / p.parts, i1 = pieces * (part + 1) / p.parts;
+            int i = i0;
+            auto copy = [&]() {  // piece i, whose stage is free
+                if (lane == 0) {
+                    const Piece x = piece_of(p, i);
+                    const float* src = x.kind == 0 ? p.q + t * p.q_stride : x.kind == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride;
+                    const uint32_t bytes = (uint32_t)(x.rows * dim * 4), full = smem_u32(&sm.full[n % APPEND_STAGES]);
+                    const bool in = SYN_IN_BOUNDS(bytes > 0 && bytes <= APPEND_STAGE && t < p.n_tok);
+                    mbar_arrive_expect_tx(full, in ? bytes : 0u);
+                    if (in) bulk_g2s(smem_u32(sm.ring[n % APPEND_STAGES]), src + (int64_t)x.row * dim, bytes, full);
+                }
+                __syncwarp();
+                n++;
+                i++;
+            };
+#ifndef SYN_TEST_STALL  // (timeout-test build: no piece is ever loaded, so the waits for one run out)
+            // the ring is empty at the start: its loads need not wait for the sines
+            while (n < APPEND_STAGES && i < i1) copy();
+#endif
+            const int b = it & 1;
+            if (!mbar_wait(smem_u32(&sm.cs_empty[b]), ((it >> 1) & 1) ^ 1, p.err, abort_flag)) break;
+            for (int j = lane; j < half_rot; j += 32) {
+                const int ax = p.axis ? min((int)p.axis[j], p.n_axes - 1) : 0;
                 const int64_t pos = p.pos[(int64_t)ax * p.n_tok + t];
-                const uint64_t phase = (uint64_t)pos * p.turns[i];
+                const uint64_t phase = (uint64_t)pos * p.turns[j];
                 float s, c;
                 sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f /* 2^-31: half turns */, &s, &c);
-                cs[i] = make_float2(c * p.magnitude, s * p.magnitude);
+                sm.cs[b][j] = make_float2(c * p.magnitude, s * p.magnitude);
             }
-            __syncthreads();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.cs_full[b]));
+#ifndef SYN_TEST_STALL
+            while (i < i1) {
+                if (!mbar_wait(smem_u32(&sm.empty[n % APPEND_STAGES]), ((n / APPEND_STAGES) & 1) ^ 1, p.err, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                copy();
+            }
+#endif
         }
-#pragma unroll
-        for (int i = 0; i < APPEND_DEEP; i++) {
-            if (base + i * APPEND_THREADS >= total) break;
-            const bool live = base + i * APPEND_THREADS + tid < total;
-            const bool is_q = row[i] < p.n_heads, is_v = row[i] >= p.n_heads + p.c.n_kv;
-            float4 r = x[i];
-            if (!is_v && e[i] < p.n_rot) {
-                if (p.halves) {
-                    const bool lower = e[i] < half_rot;
-                    const float2* c = cs + (lower ? e[i] : e[i] - half_rot);
-                    const float sg = lower ? -1.0f : 1.0f;
-                    r.x = fmaf(x[i].x, c[0].x, sg * y[i].x * c[0].y);
-                    r.y = fmaf(x[i].y, c[1].x, sg * y[i].y * c[1].y);
-                    r.z = fmaf(x[i].z, c[2].x, sg * y[i].z * c[2].y);
-                    r.w = fmaf(x[i].w, c[3].x, sg * y[i].w * c[3].y);
-                } else {
-                    const float2 c0 = cs[e[i] >> 1], c1 = cs[(e[i] >> 1) + 1];
-                    r.x = fmaf(x[i].x, c0.x, -x[i].y * c0.y);
-                    r.y = fmaf(x[i].x, c0.y, x[i].y * c0.x);
-                    r.z = fmaf(x[i].z, c1.x, -x[i].w * c1.y);
-                    r.w = fmaf(x[i].z, c1.y, x[i].w * c1.x);
+        // the pieces still in flight (issued, not consumed: only after an abort) land first
+        for (int i = max(0, n - APPEND_STAGES); i < n; i++)
+            mbar_drain(smem_u32(&sm.full[i % APPEND_STAGES]), (i / APPEND_STAGES) & 1, p.err);
+        return;
+    }
+    // ---- rotate and store --------------------------------------------------------------------
+    for (int64_t w = blockIdx.x; w < p.n_items; w += gridDim.x, it++) {
+        const int64_t t = w / p.parts;
+        const int part = (int)(w - t * p.parts);
+        const int i0 = pieces * part / p.parts, i1 = pieces * (part + 1) / p.parts;
+        const int64_t slot = p.slots[t], page = slot >> p.c.page_shift;
+        const int cell = (int)(slot & (((int64_t)1 << p.c.page_shift) - 1));
+        bool store = slot >= 0;
+        if (store && page >= p.c.n_pages) {
+            if (tid == 0) record_error(p.err, SYN_DEVERR_BOUNDS);
+            store = false;
+        }
+        const int b = it & 1;
+        if (!mbar_wait(smem_u32(&sm.cs_full[b]), (it >> 1) & 1, p.err, abort_flag)) return;
+        const float2* cs = sm.cs[b];
+        for (int i = i0; i < i1; i++, n++) {
+            const Piece x = piece_of(p, i);
+            const int st = n % APPEND_STAGES;
+            if (!mbar_wait(smem_u32(&sm.full[st]), (n / APPEND_STAGES) & 1, p.err, abort_flag)) return;
+            const float* src = reinterpret_cast<const float*>(sm.ring[st]);
+            uint8_t* pool = (x.kind == 2 ? p.c.v : p.c.k) + page * p.c.page_stride + (int64_t)x.row * p.c.tile;
+            __half* qo = p.q_out + (t * p.n_heads + x.row) * dim;
+            const int units = x.rows * per_row;
+            // (units is a multiple of 8: the 8 lanes of a block stay together)
+            for (int u0 = 32 * warp; u0 < units; u0 += 32 * APPEND_WARPS) {
+                const int u = min(u0 + lane, units - 1), row = u / per_row, e = (u - row * per_row) << 2;
+                const bool live = u0 + lane < units;
+                const float4 a = *reinterpret_cast<const float4*>(src + 4 * u);
+                float4 r = a;
+                if (x.kind < 2 && e < p.n_rot) {
+                    if (p.halves) {
+                        const bool lower = e < half_rot;
+                        const float4 y = *reinterpret_cast<const float4*>(src + 4 * u + (lower ? half_rot : -half_rot));
+                        const float4* c = reinterpret_cast<const float4*>(cs + (lower ? e : e - half_rot));
+                        const float4 c0 = c[0], c1 = c[1];
+                        const float sg = lower ? -1.0f : 1.0f;
+                        r.x = fmaf(a.x, c0.x, sg * y.x * c0.y);
+                        r.y = fmaf(a.y, c0.z, sg * y.y * c0.w);
+                        r.z = fmaf(a.z, c1.x, sg * y.z * c1.y);
+                        r.w = fmaf(a.w, c1.z, sg * y.w * c1.w);
+                    } else {
+                        const float4 c = *reinterpret_cast<const float4*>(cs + (e >> 1));
+                        r.x = fmaf(a.x, c.x, -a.y * c.y);
+                        r.y = fmaf(a.x, c.y, a.y * c.x);
+                        r.z = fmaf(a.z, c.z, -a.w * c.w);
+                        r.w = fmaf(a.z, c.w, a.w * c.z);
+                    }
+                }
+                if (x.kind == 0) {
+                    if (live) *reinterpret_cast<uint2*>(qo + 4 * u) = pack_half4(r);
+                    continue;
+                }
+                uint8_t* tile = pool + (int64_t)row * p.c.tile;
+                const bool in = live && store && SYN_IN_BOUNDS(x.row + row < p.c.n_kv && page < p.c.n_pages && e + 4 <= dim);
+                if (Q8) {
+                    unsigned short scale;
+                    const uint32_t codes = q8_codes(r, scale);
+                    if (in) {
+                        *reinterpret_cast<uint32_t*>(tile + (int64_t)cell * dim + e) = codes;
+                        if ((e & 31) == 0)
+                            *reinterpret_cast<unsigned short*>(tile + ((int64_t)dim << p.c.page_shift) +
+                                                               2 * ((int64_t)cell * (dim >> 5) + (e >> 5))) = scale;
+                    }
+                } else if (in) {
+                    *reinterpret_cast<uint2*>(tile + 2 * ((int64_t)cell * dim + e)) = pack_half4(r);
                 }
             }
-            uint32_t codes = 0;
-            unsigned short scale = 0;
-            if (p.c.q8) codes = q8_codes(r, scale);
-            if (!live) continue;
-            if (is_q) {
-                *reinterpret_cast<uint2*>(p.q_out + (t * p.n_heads + row[i]) * dim + e[i]) = pack_half4(r);
-            } else if (store) {
-                const int h = row[i] - p.n_heads - (is_v ? p.c.n_kv : 0);
-                uint8_t* tile = (is_v ? p.c.v : p.c.k) + page * p.c.page_stride + (int64_t)h * p.c.tile;
-                if (!SYN_IN_BOUNDS(h >= 0 && h < p.c.n_kv && page >= 0 && page < p.c.n_pages && e[i] + 4 <= dim)) continue;
-                if (p.c.q8) {
-                    *reinterpret_cast<uint32_t*>(tile + (int64_t)cell * dim + e[i]) = codes;
-                    if ((e[i] & 31) == 0)
-                        *reinterpret_cast<unsigned short*>(tile + ((int64_t)dim << p.c.page_shift) +
-                                                           2 * ((int64_t)cell * (dim >> 5) + (e[i] >> 5))) = scale;
-                } else {
-                    *reinterpret_cast<uint2*>(tile + 2 * ((int64_t)cell * dim + e[i])) = pack_half4(r);
-                }
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.empty[st]));
         }
+        if (lane == 0) mbar_arrive(smem_u32(&sm.cs_empty[b]));
     }
 }
 
@@ -202,7 +285,8 @@ __global__ void __launch_bounds__(256) k_kv_read(const ReadParams p) {
 
 cudaError_t launch_kv_append(const KvCache& c, const RopeDesc& r, int64_t n_tok, const float* q, int64_t q_stride,
                              int n_heads, void* q_out, const float* k, int64_t k_stride, const float* v,
-                             int64_t v_stride, const int32_t* pos, const int64_t* slots, int* err, cudaStream_t s) {
+                             int64_t v_stride, const int32_t* pos, const int64_t* slots, int* err, int sms,
+                             cudaStream_t s) {
     AppendParams p;
     p.c = c;
     p.q = q;
@@ -223,7 +307,20 @@ cudaError_t launch_kv_append(const KvCache& c, const RopeDesc& r, int64_t n_tok,
     p.n_axes = r.n_axes;
     p.halves = r.halves;
     p.magnitude = r.magnitude;
-    k_kv_append<<<(unsigned)n_tok, APPEND_THREADS, 0, s>>>(p);
+    p.piece_rows = APPEND_STAGE / (4 * c.dim);
+    p.q_pieces = (n_heads + p.piece_rows - 1) / p.piece_rows;
+    p.kv_pieces = (c.n_kv + p.piece_rows - 1) / p.piece_rows;
+    // few tokens: each token's pieces are dealt to several CTAs
+    const int64_t ctas = (int64_t)sms * APPEND_CTAS_PER_SM;
+    p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(p.q_pieces + 2 * p.kv_pieces, ctas / n_tok));
+    p.n_items = n_tok * p.parts;
+    const int grid = (int)std::min<int64_t>(p.n_items, ctas);
+    static ResidentCtas resident[2];
+    auto kern = c.q8 ? k_kv_append<true> : k_kv_append<false>;
+    int per_sm;
+    const cudaError_t e = resident[c.q8].get(reinterpret_cast<const void*>(kern), APPEND_THREADS, sizeof(AppendSmem), &per_sm);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, APPEND_THREADS, sizeof(AppendSmem), s>>>(p);
     return cudaGetLastError();
 }
 

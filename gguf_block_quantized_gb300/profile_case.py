@@ -15,6 +15,10 @@ Cases (synthetic weights ~N(0, 0.02), activations ~N(0, 1)):
                      inputs of the benchmark's sweep
   prefill_llama8b_layer  one Llama-8B layer at 2048 tokens as a model calls it: q/k/v grouped
                      on one input, o, gate/up grouped on one input, down (Q4_K, Q6_K v/down)
+  kv_append_f16, kv_append_q8  4096 tokens of 32 / 8 heads of 128 into a paged cache (150 MB moved)
+  attn_decode_f16, attn_decode_q8  one token of each of 48 sequences of 2000 cached tokens, 32 / 8
+                     heads of 128, pages of 64 (F16: 393 MB of rows)
+  attn_prefill_f16, attn_prefill_q8  a prompt of 4096 tokens, 32 / 8 heads of 128
 """
 from __future__ import annotations
 
@@ -30,16 +34,57 @@ CASES = {
 }
 
 
+ATTN = ["kv_append_f16", "kv_append_q8", "attn_decode_f16", "attn_decode_q8", "attn_prefill_f16", "attn_prefill_q8"]
+
+
+def attn_case(case: str, reps: int):
+    """The paged-cache operators on random rows (the cache's content does not change their time)."""
+    import torch
+
+    from gguf_block_quantized_gb300 import syn
+
+    heads, kv, dim, page = 32, 8, 128, 64
+    t = syn.Q8_0 if case.endswith("q8") else syn.F16
+    seqs, rows = (48, 2000) if "decode" in case else (1, 4096)
+    per = -(-rows // page)
+    cache = syn.KVCache.empty(t, kv, dim, page, seqs * per)
+    pages = torch.randperm(seqs * per, device="cuda").to(torch.int32).view(seqs, per)
+    row = torch.arange(rows, device="cuda")
+    fused = torch.randn((rows, heads + 2 * kv, dim), device="cuda")
+    parts = {"q": fused[:, :heads], "k": fused[:, heads:heads + kv], "v": fused[:, heads + kv:]}
+    rope = syn.Rope(dim, 500000.0, layout=syn.ROPE_ADJACENT)
+    pos = row.to(torch.int32)
+    for s in range(seqs):
+        slots = pages[s].long()[row // page] * page + row % page
+        append = syn.prepare_kv_append(cache, rope, parts["k"], parts["v"], pos, slots, parts["q"])
+        q = append()
+    lens = torch.full((seqs,), rows, dtype=torch.int32, device="cuda")
+    if case.startswith("kv_append"):
+        step = append
+    elif "decode" in case:
+        step = syn.prepare_attn_decode(cache, q[:seqs].contiguous(), pages, lens)
+    else:
+        step = syn.prepare_attn_prefill(cache, q, torch.tensor([0, rows], dtype=torch.int32, device="cuda"), pages, lens)
+    for _ in range(reps):
+        step()
+    torch.cuda.synchronize()
+    assert syn.device_status() == syn.OK
+    print(f"{case}: {reps} calls done")
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--case", required=True, choices=sorted(CASES) + ["gemv_llama1b_layer", "gemv_llama8b_layers",
-                                                                     "prefill_llama8b_layer"])
+                                                                     "prefill_llama8b_layer"] + ATTN)
     ap.add_argument("--reps", type=int, default=3)
     args = ap.parse_args()
     import torch
 
     from gguf_block_quantized_gb300 import syn, synth
 
+    if args.case in ATTN:
+        attn_case(args.case, args.reps)
+        return
     if args.case == "gemv_llama1b_layer":
         from gguf_block_quantized_gb300 import workloads
         mats = workloads.LLAMA1B_LAYER

@@ -15,7 +15,7 @@
 //     from zero and is added to the fp32 sums by fma, because the tensor pipe's own additions
 //     truncate.  Scores likewise come from two short chains.  So the result is as exact as fp32
 //     arithmetic allows, which fp32 outputs show.
-//   - Work is cut by length, not by sequence: the steps (4 chunks, one per warp) of all
+//   - Work is cut by length, not by sequence: blocks of steps (4 chunks, one per warp) of all
 //     (sequence, kv head) items are dealt to the CTAs in equal contiguous ranges, found on the
 //     device from the lengths (a captured graph keeps working as they grow).  A CTA whose range
 //     covers an item writes the output; else it leaves a partial in the workspace, and the CTA
@@ -31,9 +31,9 @@ namespace syn {
 constexpr int DEC_WARPS = 4;
 constexpr int DEC_STAGES = 3;
 constexpr int DEC_MAX_SEQ = 1024;  // sequences of one launch (their step counts are in shared memory)
-// least steps a CTA takes: as many as its ring holds, whose loads are in flight together, so
-// cutting a short item finer would not end sooner
-constexpr int DEC_MIN_STEPS = 3;
+// Work is dealt in blocks of this many steps: as many as a ring holds, whose loads are in flight
+// together, so cutting a short item finer would not end it sooner.
+constexpr int DEC_BLOCK = 3;
 constexpr float DEC_P_LOG2 = 14.0f;  // p is held as 2^14 p, in fp16: small p stay normal numbers
 
 struct DecodeParams {
@@ -50,7 +50,7 @@ struct DecodeParams {
     float* part;  // per CTA two partial slots
     int* count;   // per item, zero between calls
     int* err;
-    float scale, cap;
+    float scale, cap, inv_cap;
     int n_seq, g, n_hg, window, out_f16, whole;
 };
 
@@ -58,6 +58,9 @@ struct DecodeParams {
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp16_all(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -81,6 +84,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
 
@@ -90,6 +98,19 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
     const float2 f = __half22float2(h);
     hi = h2u(h);
     lo = h2u(__floats2half2_rn(x - f.x, y - f.y));
+}
+
+// tanh to about 2^-22 of itself without branches: (e - 1)/(e + 1) with e = 2^(2|y| log2 e), and below
+// 0.55, where e - 1 would cancel, the fifth convergent of Lambert's continued fraction
+__device__ __forceinline__ float tanh_rel(float y) {
+    const float a = fminf(fabsf(y), 10.0f), u = a * a;
+    const bool small = a < 0.55f;
+    const float e = ex2(2.8853900817779268f * a);
+    const float num = small ? a * fmaf(u, u + 105.0f, 945.0f) : e - 1.0f;
+    const float den = small ? fmaf(u, fmaf(u, 15.0f, 420.0f), 945.0f) : e + 1.0f;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(den));
+    return copysignf(y == y ? num * r : y, y);
 }
 
 // ---- what a sequence needs ---------------------------------------------------------------
@@ -138,8 +159,12 @@ struct DecLayout {
     static constexpr int RING = DEC_WARPS * WARP;
 };
 
+// CTAs per SM that the ring leaves room for (so many registers are a thread's)
+template <int D, bool Q8>
+constexpr int DEC_RESIDENT = D == 64 ? (Q8 ? 4 : 4) : D == 128 ? (Q8 ? 3 : 2) : (Q8 ? 1 : 1);
+
 template <int D, int NT, bool Q8>
-__global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodeParams p) {
+__global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> : 1) k_attn_decode(const DecodeParams p) {
     using L = DecLayout<D, Q8>;
     constexpr int KSTEPS = D / 16;
     constexpr int H = 8 * NT;  // query heads of an item
@@ -148,21 +173,21 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
     float* sm_m = reinterpret_cast<float*>(smem + L::RING);  // [DEC_WARPS][H]
     float* sm_l = sm_m + DEC_WARPS * H;
     int* flags = reinterpret_cast<int*>(sm_l + DEC_WARPS * H);  // [0] scan carry, [1..4] warp sums, [5] last
-    int* pre = flags + 8;                                        // [n_seq + 1] steps before each sequence, of one head
+    int* pre = flags + 8;                                        // [n_seq + 1] blocks before each sequence, of one item
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r8 = lane >> 2, c4 = lane & 3;
     const int dim = p.c.dim;
     const int n_item_h = p.c.n_kv * p.n_hg;  // items of a sequence
 
-    // steps of every sequence, as a running sum
+    // blocks of every sequence, as a running sum
     if (tid == 0) flags[0] = 0, pre[0] = 0;
     __syncthreads();
     for (int base = 0; base < p.n_seq; base += 32 * DEC_WARPS) {
         const int s = base + tid;
         int n = 0;
         if (s < p.n_seq) {
-            n = (seq_chunks(seq_visible(p, s, seq_len(p, s))).count() + DEC_WARPS - 1) / DEC_WARPS;
+            n = (seq_chunks(seq_visible(p, s, seq_len(p, s))).count() + DEC_WARPS * DEC_BLOCK - 1) / (DEC_WARPS * DEC_BLOCK);
             if (n == 0) {  // no key to see: zeros, written by the CTAs in turn
                 if (s % gridDim.x == blockIdx.x) {
                     const int64_t n_out = (int64_t)p.c.n_kv * p.g * dim;
@@ -190,43 +215,54 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
     }
     const int64_t total = (int64_t)pre[p.n_seq] * n_item_h;
     if (total == 0) return;
-    const int64_t ctas = min((int64_t)gridDim.x, (total + DEC_MIN_STEPS - 1) / DEC_MIN_STEPS);
+    const int64_t ctas = min((int64_t)gridDim.x, total);
     if (!p.whole && blockIdx.x >= ctas) return;
-    // this CTA's range of steps; in `whole` mode its items are blockIdx.x, + gridDim.x, ...
+    // this CTA's range of blocks; in `whole` mode its items are blockIdx.x, + gridDim.x, ...
     int64_t at = blockIdx.x * total / ctas, stop = (blockIdx.x + 1) * total / ctas;
     int item_w = blockIdx.x;
 
+    constexpr float LOG2E = 1.4426950408889634f;
+    const float scale_log2 = p.scale * LOG2E;
     uint8_t* ring = smem + warp * L::WARP;
     const uint32_t ring_s = smem_u32(ring);
     const int row_pieces = Q8 ? dim >> 4 : dim >> 3;  // 16-byte pieces of a row
-    constexpr int DPIECES = Q8 ? D / 16 : D / 8;      // the same of the widest row this kernel takes
+    // A chunk's 16 rows lie one after the other in a page, so lane l copies the 16-byte pieces
+    // l, l + 32, ...: their places in a stage
+    constexpr int N_COPY = Q8 ? D / 32 : D / 16;
+    uint32_t to_k[N_COPY], to_v[N_COPY];
+#pragma unroll
+    for (int i = 0; i < N_COPY; i++) {
+        const int idx = i * 32 + lane, r = idx / row_pieces, j = idx - r * row_pieces;
+        to_k[i] = L::K + r * L::PK + (Q8 ? 16 * j : ((j ^ (r & 7)) << 4));
+        to_v[i] = L::V + r * L::PV + (Q8 ? 16 * j : ((j ^ (r & 7)) << 4));
+    }
 
     while (true) {
-        // the next segment: steps [st0, st1) of item (s, kv head h, head group hg)
-        int s, hh, st0, st1, n_steps;
+        // the next segment: blocks [st0, st1) of item (s, kv head h, head group hg)
+        int s, hh, st0, st1, n_blocks;
         if (p.whole) {
             if (item_w >= p.n_seq * n_item_h) break;
             s = item_w / n_item_h;
             hh = item_w - s * n_item_h;
-            n_steps = pre[s + 1] - pre[s];
+            n_blocks = pre[s + 1] - pre[s];
             item_w += gridDim.x;
-            if (n_steps == 0) continue;
+            if (n_blocks == 0) continue;
             st0 = 0;
-            st1 = n_steps;
+            st1 = n_blocks;
         } else {
             if (at >= stop) break;
-            int lo = 0, hi = p.n_seq - 1;  // the sequence whose steps hold `at`
+            int lo = 0, hi = p.n_seq - 1;  // the sequence whose blocks hold `at`
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
                 if ((int64_t)pre[mid + 1] * n_item_h > at) hi = mid;
                 else lo = mid + 1;
             }
             s = lo;
-            n_steps = pre[s + 1] - pre[s];
+            n_blocks = pre[s + 1] - pre[s];
             const int64_t rel = at - (int64_t)pre[s] * n_item_h;
-            hh = (int)(rel / n_steps);
-            st0 = (int)(rel - (int64_t)hh * n_steps);
-            st1 = (int)min((int64_t)n_steps, st0 + (stop - at));
+            hh = (int)(rel / n_blocks);
+            st0 = (int)(rel - (int64_t)hh * n_blocks);
+            st1 = (int)min((int64_t)n_blocks, st0 + (stop - at));
             at += st1 - st0;
         }
         const int h = hh / p.n_hg, hg = hh - h * p.n_hg;
@@ -272,6 +308,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
             }
 
         float m[NT][2], l[NT][2];
+        int e_run = 0;  // Q8_0: o is held relative to 2^(e_run - 15)
         float o[KSTEPS][NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
@@ -281,9 +318,13 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
             for (int mt = 0; mt < KSTEPS; mt++) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.0f;
         }
 
-        // this warp's chunks of the segment: st0*W + warp, then every W-th, below `chunk_end`
-        const int chunk_end = min(n_chunks, st1 * DEC_WARPS);
-        int next_issue = st0 * DEC_WARPS + warp;
+        // this warp's chunks of the segment, every DEC_WARPS-th below `chunk_end`
+        const int chunk0 = st0 * (DEC_WARPS * DEC_BLOCK) + warp;
+        const int chunk_end = min(n_chunks, st1 * (DEC_WARPS * DEC_BLOCK));
+        int next_issue = chunk0;
+        auto all_seen = [&](int row) {  // the 16 rows from `row`
+            return (row >= vis.low && row + 16 <= vis.end) || (row >= vis.first && row + 16 <= vis.pre);
+        };
         // the page ids of the next chunk to issue, looked up one chunk ahead (rows 0-7 and 8-15)
         auto page_of = [&](int row) {
             if (row >= len) return -1;
@@ -303,44 +344,57 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
             }
         };
         look_up();
+        [[maybe_unused]] const int64_t pool_end = p.c.tile + (p.c.n_pages - 1) * p.c.page_stride;  // from a head's tile of page 0
+        const int64_t plane = (int64_t)dim << p.c.page_shift;                     // Q8_0: a tile's scales
+        const int n_sp = dim >> 4;  // Q8_0: 16-byte pieces of 16 rows' scales (at most 16)
         auto issue = [&](int stage) {
             if (next_issue < chunk_end) {
                 const int row0 = ch.at(next_issue) << 4;
                 const uint32_t dst = ring_s + stage * L::STAGE;
-                const int64_t off_lo = (int64_t)max(id_lo, 0) * p.c.page_stride, off_hi = (int64_t)max(id_hi, 0) * p.c.page_stride;
                 const int cell_lo = row0 & ((1 << p.c.page_shift) - 1);
-                const int cell_hi = p.c.page_shift >= 4 ? cell_lo + 8 : 0;
-                constexpr int N = 16 * DPIECES / 32;
+                if (p.c.page_shift >= 4 && id_lo >= 0 && all_seen(row0)) {
+                    const int64_t off = (int64_t)id_lo * p.c.page_stride + (int64_t)cell_lo * row_pieces * 16;
+                    if (SYN_IN_BOUNDS(off >= 0 && off + 256 * row_pieces <= pool_end)) {
+                        const uint8_t *ks = kbase + off + 16 * lane, *vs = vbase + off + 16 * lane;
 #pragma unroll
-                for (int i = 0; i < N; i++) {
-                    const int idx = i * 32 + lane, r = idx / DPIECES, j = idx % DPIECES;
-                    if (j >= row_pieces) continue;
-                    const bool upper = r >= 8;
-                    // rows that the query does not see are not read: zeros (a masked V row may
-                    // hold anything, and 0 * inf is not 0)
-                    const bool ok = (upper ? id_hi : id_lo) >= 0 && vis(row0 + r);
-                    const int64_t off = ok ? (upper ? off_hi + (int64_t)(cell_hi + r - 8) * row_pieces * 16
-                                                    : off_lo + (int64_t)(cell_lo + r) * row_pieces * 16) + 16 * j
-                                           : 0;
-                    if (!SYN_IN_BOUNDS(off >= 0 && off + 16 <= p.c.tile + (p.c.n_pages - 1) * p.c.page_stride)) continue;
-                    const uint32_t nb = ok ? 16u : 0u;
-                    const uint32_t dk = dst + L::K + r * L::PK + (Q8 ? 16 * j : ((j ^ (r & 7)) << 4));
-                    const uint32_t dv = dst + L::V + r * L::PV + (Q8 ? 16 * j : ((j ^ (r & 7)) << 4));
-                    cp16(dk, kbase + off, nb);
-                    cp16(dv, vbase + off, nb);
-                }
-                if (Q8) {
-                    // scales: 16 rows of dim/32 halves, in 16-byte pieces (rows 0-7, 8-15 apart)
-                    const int n_sp = dim >> 4;  // pieces of 16 rows; dim <= 256: at most 16
-                    if (lane < 2 * n_sp) {
+                        for (int i = 0; i < N_COPY; i++) {
+                            if (2 * i >= row_pieces) break;
+                            cp16_all(dst + to_k[i], ks + 512 * i);
+                            cp16_all(dst + to_v[i], vs + 512 * i);
+                        }
+                        if (Q8 && lane < 2 * n_sp) {
+                            const int i = lane < n_sp ? lane : lane - n_sp;
+                            cp16_all(dst + (lane < n_sp ? L::KS : L::VS) + 16 * i,
+                                     (lane < n_sp ? kbase : vbase) + (int64_t)id_lo * p.c.page_stride + plane + (int64_t)cell_lo * n_sp + 16 * i);
+                        }
+                    }
+                } else {
+                    // a chunk at an end of what is seen, or over two pages: rows that the query does
+                    // not see are not read but zero (a masked V row may hold anything, and 0 * inf is
+                    // not 0)
+                    const int64_t off_lo = (int64_t)max(id_lo, 0) * p.c.page_stride, off_hi = (int64_t)max(id_hi, 0) * p.c.page_stride;
+                    const int cell_hi = p.c.page_shift >= 4 ? cell_lo + 8 : 0;
+#pragma unroll
+                    for (int i = 0; i < N_COPY; i++) {
+                        if (2 * i >= row_pieces) break;
+                        const int r = (int)(to_k[i] - L::K) / L::PK, j = i * 32 + lane - r * row_pieces;
+                        const bool upper = r >= 8;
+                        const bool ok = (upper ? id_hi : id_lo) >= 0 && vis(row0 + r);
+                        const int64_t off = ok ? (upper ? off_hi + (int64_t)(cell_hi + r - 8) * row_pieces * 16
+                                                        : off_lo + (int64_t)(cell_lo + r) * row_pieces * 16) + 16 * j
+                                               : 0;
+                        if (!SYN_IN_BOUNDS(off >= 0 && off + 16 <= pool_end)) continue;
+                        cp16(dst + to_k[i], kbase + off, ok ? 16u : 0u);
+                        cp16(dst + to_v[i], vbase + off, ok ? 16u : 0u);
+                    }
+                    if (Q8 && lane < 2 * n_sp) {  // scales: rows 0-7 and 8-15 apart
                         const int i = lane < n_sp ? lane : lane - n_sp;
                         const bool upper = 2 * i >= n_sp;
                         const bool ok = (upper ? id_hi : id_lo) >= 0;
-                        const int64_t plane = (int64_t)dim << p.c.page_shift;
-                        const int64_t off = ok ? plane + (upper ? off_hi + (int64_t)cell_hi * (dim >> 4) + 16 * (i - n_sp / 2)
-                                                                : off_lo + (int64_t)cell_lo * (dim >> 4) + 16 * i)
+                        const int64_t off = ok ? plane + (upper ? off_hi + (int64_t)cell_hi * n_sp + 16 * (i - n_sp / 2)
+                                                                : off_lo + (int64_t)cell_lo * n_sp + 16 * i)
                                                : 0;
-                        if (SYN_IN_BOUNDS(off >= 0 && off + 16 <= p.c.tile + (p.c.n_pages - 1) * p.c.page_stride))
+                        if (SYN_IN_BOUNDS(off >= 0 && off + 16 <= pool_end))
                             cp16(dst + (lane < n_sp ? L::KS : L::VS) + 16 * i, (lane < n_sp ? kbase : vbase) + off, ok ? 16u : 0u);
                     }
                 }
@@ -353,26 +407,27 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
         for (int i = 0; i < DEC_STAGES - 1; i++) issue(i);
 
         int stage = 0;
-        for (int ci = st0 * DEC_WARPS + warp; ci < chunk_end; ci += DEC_WARPS) {
+        for (int ci = chunk0; ci < chunk_end; ci += DEC_WARPS) {
             cp_wait<DEC_STAGES - 2>();
             __syncwarp();
             issue(stage == 0 ? DEC_STAGES - 1 : stage - 1);
             const int row0 = ch.at(ci) << 4;
             const uint32_t st = ring_s + stage * L::STAGE;
             const uint8_t* stp = ring + stage * L::STAGE;
-            const bool seen_a = vis(row0 + r8), seen_b = vis(row0 + r8 + 8);
+            const bool full = all_seen(row0);
+            const bool seen_a = full || vis(row0 + r8), seen_b = full || vis(row0 + r8 + 8);
 
             // S^T = K Q^T
             float sc[NT][4];
             if (Q8) {
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
+                const __half2 k1152 = __float2half2_rn(1152.0f);
 #pragma unroll
                 for (int b = 0; b < D / 32; b++) {
                     if (b * 32 >= dim) break;
                     // codes of a 32-value block: 8 per lane and row, exact in fp16
                     uint32_t a0[4], a1[4];
-                    const __half2 k1152 = __float2half2_rn(1152.0f);
 #pragma unroll
                     for (int u = 0; u < 2; u++) {
                         const uint2 w = *reinterpret_cast<const uint2*>(stp + L::K + (r8 + 8 * u) * L::PK + 32 * b + 8 * c4);
@@ -386,8 +441,8 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
                     const float db = h2f_bits(*reinterpret_cast<const uint16_t*>(stp + L::KS + 2 * ((r8 + 8) * (dim >> 5) + b)));
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
-                        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma16816(c, a0, qf[2 * b][nt][0], qf[2 * b][nt][1]);
+                        float c[4];
+                        mma16816_zero(c, a0, qf[2 * b][nt][0], qf[2 * b][nt][1]);
                         mma16816(c, a1, qf[2 * b + 1][nt][0], qf[2 * b + 1][nt][1]);
                         sc[nt][0] = fmaf(c[0], da, sc[nt][0]);
                         sc[nt][1] = fmaf(c[1], da, sc[nt][1]);
@@ -419,17 +474,24 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
             }
 
             // softmax of the chunk, in powers of two
-            constexpr float LOG2E = 1.4426950408889634f;
             uint32_t ph[NT][2], pl[NT][2];  // F16: P^T as the B operand (heads and tails)
             float pr[NT][4], alpha[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
+                if (p.cap > 0.0f || p.slopes) {
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    float x = sc[nt][j] * p.scale;
-                    if (p.cap > 0.0f) x = p.cap * tanhf(x / p.cap);
-                    if (p.slopes) x = fmaf(-slope[nt][j & 1], (float)(len - 1 - row0 - r8 - (j >> 1) * 8), x);
-                    sc[nt][j] = ((j >> 1) ? seen_b : seen_a) ? x * LOG2E : -INFINITY;
+                    for (int j = 0; j < 4; j++) {
+                        float x = sc[nt][j] * p.scale;
+                        if (p.cap > 0.0f) x = p.cap * tanh_rel(x * p.inv_cap);
+                        sc[nt][j] = fmaf(-slope[nt][j & 1], (float)(len - 1 - row0 - r8 - (j >> 1) * 8), x) * LOG2E;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; j++) sc[nt][j] *= scale_log2;
+                }
+                if (!full) {
+                    if (!seen_a) sc[nt][0] = sc[nt][1] = -INFINITY;
+                    if (!seen_b) sc[nt][2] = sc[nt][3] = -INFINITY;
                 }
 #pragma unroll
                 for (int j = 0; j < 2; j++) {
@@ -457,19 +519,49 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
 
             // O^T = O^T * alpha + V^T P^T
             if (Q8) {
+                // A row's value scales go into p, in fp32 and before the split, relative to 2^e, the
+                // largest power of two among the scales so far: p * scale then fits fp16 whatever
+                // the scales (o is kept in units of 2^e, as it is relative to 2^m).
+                uint32_t dv[D / 32][2];  // scales of rows (2c, 2c+1), (2c+8, 2c+9) of each block
+                uint32_t top = 0;
 #pragma unroll
                 for (int b = 0; b < D / 32; b++) {
                     if (b * 32 >= dim) break;
-                    // the block's scales go into p, relative to the largest power of two among
-                    // the chunk's 16 (p * scale then fits fp16, whatever the scale)
-                    const uint16_t ba = *reinterpret_cast<const uint16_t*>(stp + L::VS + 2 * (r8 * (dim >> 5) + b));
-                    const uint16_t bb = *reinterpret_cast<const uint16_t*>(stp + L::VS + 2 * ((r8 + 8) * (dim >> 5) + b));
-                    const uint32_t sa = seen_a ? ba : 0, sb = seen_b ? bb : 0;
-                    const int e = (int)(__reduce_max_sync(0xffffffffu, max(sa & 0x7FFF, sb & 0x7FFF)) >> 10);
-                    const float down = __int_as_float((127 + 15 - e) << 23), up = __int_as_float((127 - 15 + e) << 23);
-                    const float da = h2f_bits((uint16_t)sa) * down, db = h2f_bits((uint16_t)sb) * down;
+                    const uint16_t* sv = reinterpret_cast<const uint16_t*>(stp + L::VS) + 2 * c4 * (dim >> 5) + b;
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        uint32_t x = sv[8 * u * (dim >> 5)], y = sv[(8 * u + 1) * (dim >> 5)];
+                        if (!full) {
+                            x = vis(row0 + 2 * c4 + 8 * u) ? x : 0u;
+                            y = vis(row0 + 2 * c4 + 8 * u + 1) ? y : 0u;
+                        }
+                        dv[b][u] = x | y << 16;
+                        top = max(top, max(x, y) & 0x7FFFu);
+                    }
+                }
+                const int e_new = max(e_run, (int)(__reduce_max_sync(0xffffffffu, top) >> 10));
+                const float down = __int_as_float((127 + 15 - e_new) << 23), step = __int_as_float((127 + e_run - e_new) << 23);
+                e_run = e_new;
+                // p in the B operand's layout: rows 2c, 2c+1, 2c+8, 2c+9 of head lane/4, as the upper and
+                // lower halves of the fp32 words
+                float pb[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    alpha[nt][0] *= step;
+                    alpha[nt][1] *= step;
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        const uint32_t x = __float_as_uint(pr[nt][2 * u]), y = __float_as_uint(pr[nt][2 * u + 1]);
+                        const uint32_t hi = transpose8(__byte_perm(x, y, 0x7632)), lo = transpose8(__byte_perm(x, y, 0x5410));
+                        pb[nt][2 * u] = __uint_as_float(__byte_perm(lo, hi, 0x5410)) * down;
+                        pb[nt][2 * u + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632)) * down;
+                    }
+                }
+                const __half2 k1152 = __float2half2_rn(1152.0f);
+#pragma unroll
+                for (int b = 0; b < D / 32; b++) {
+                    if (b * 32 >= dim) break;
                     uint32_t a0[4], a1[4];
-                    const __half2 k1152 = __float2half2_rn(1152.0f);
 #pragma unroll
                     for (int u = 0; u < 2; u++) {
                         const uint8_t* vr = stp + L::V + (2 * c4 + 8 * u) * L::PV + 32 * b + 4 * r8;
@@ -481,23 +573,19 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
                         a1[2 * u] = h2u(__hsub2(u2h(__byte_perm(x23, 0x64646464u, 0x4140)), k1152));
                         a1[2 * u + 1] = h2u(__hsub2(u2h(__byte_perm(x23, 0x64646464u, 0x4342)), k1152));
                     }
+                    const float2 d0 = __half22float2(u2h(dv[b][0])), d1 = __half22float2(u2h(dv[b][1]));
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
                         uint32_t hi0, lo0, hi1, lo1;
-                        split_pair(pr[nt][0] * da, pr[nt][1] * da, hi0, lo0);
-                        split_pair(pr[nt][2] * db, pr[nt][3] * db, hi1, lo1);
-                        hi0 = transpose8(hi0);
-                        hi1 = transpose8(hi1);
-                        lo0 = transpose8(lo0);
-                        lo1 = transpose8(lo1);
+                        split_pair(pb[nt][0] * d0.x, pb[nt][1] * d0.y, hi0, lo0);
+                        split_pair(pb[nt][2] * d1.x, pb[nt][3] * d1.y, hi1, lo1);
 #pragma unroll
                         for (int u = 0; u < 2; u++) {
-                            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma16816(c, u ? a1 : a0, lo0, lo1);
+                            float c[4];
+                            mma16816_zero(c, u ? a1 : a0, lo0, lo1);
                             mma16816(c, u ? a1 : a0, hi0, hi1);
 #pragma unroll
-                            for (int j = 0; j < 4; j++)
-                                o[2 * b + u][nt][j] = fmaf(o[2 * b + u][nt][j], alpha[nt][j & 1], c[j] * up);
+                            for (int j = 0; j < 4; j++) o[2 * b + u][nt][j] = fmaf(o[2 * b + u][nt][j], alpha[nt][j & 1], c[j]);
                         }
                     }
                 }
@@ -511,8 +599,8 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
                     ldsm4t(rowa + (((2 * mt + cc) ^ (rr & 7)) << 4), a);
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
-                        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma16816(c, a, pl[nt][0], pl[nt][1]);
+                        float c[4];
+                        mma16816_zero(c, a, pl[nt][0], pl[nt][1]);
                         mma16816(c, a, ph[nt][0], ph[nt][1]);
 #pragma unroll
                         for (int j = 0; j < 4; j++) o[mt][nt][j] = fmaf(o[mt][nt][j], alpha[nt][j & 1], c[j]);
@@ -545,7 +633,8 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
                 const int hd = nt * 8 + 2 * c4 + j;
                 float mx = sm_m[hd];
                 for (int w = 1; w < DEC_WARPS; w++) mx = fmaxf(mx, sm_m[w * H + hd]);
-                const float f = ex2(m[nt][j] - (mx == -INFINITY ? 0.0f : mx));
+                float f = ex2(m[nt][j] - (mx == -INFINITY ? 0.0f : mx));
+                if (Q8) f *= __int_as_float((127 - 15 + e_run) << 23);
                 if (hd < heads) {
 #pragma unroll
                     for (int mt = 0; mt < KSTEPS; mt++) {
@@ -559,7 +648,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
                 }
             }
         __syncthreads();
-        const bool direct = st1 - st0 == n_steps;
+        const bool direct = st1 - st0 == n_blocks;
         // a partial's slot: 2*CTA + 1 where the segment begins its item, else 2*CTA
         float* part = p.part + (2 * (int64_t)blockIdx.x + (st0 == 0)) * H * (D + 2);
         for (int i = tid; i < heads * dim; i += 32 * DEC_WARPS) {
@@ -586,9 +675,9 @@ __global__ void __launch_bounds__(32 * DEC_WARPS) k_attn_decode(const DecodePara
             }
         }
         if (!direct) {
-            // the CTAs that share the item: those whose ranges hold its first and last step
-            const int64_t t0 = (int64_t)pre[s] * n_item_h + (int64_t)hh * n_steps;
-            const int i0 = (int)(((t0 + 1) * ctas - 1) / total), i1 = (int)(((t0 + n_steps) * ctas - 1) / total);
+            // the CTAs that share the item: those whose ranges hold its first and last block
+            const int64_t t0 = (int64_t)pre[s] * n_item_h + (int64_t)hh * n_blocks;
+            const int i0 = (int)(((t0 + 1) * ctas - 1) / total), i1 = (int)(((t0 + n_blocks) * ctas - 1) / total);
             const int item = s * n_item_h + hh;
             __threadfence();
             __syncthreads();
@@ -671,6 +760,7 @@ cudaError_t launch_attn_decode(const KvCache& c, const AttnDesc& a, int64_t n_se
         p.err = err;
         p.scale = a.scale;
         p.cap = a.cap;
+        p.inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
         p.n_seq = (int)std::min<int64_t>(DEC_MAX_SEQ, n_seq - s0);
         p.g = a.n_heads / c.n_kv;
         const int nt = decode_nt(p.g, c.dim);

@@ -27,7 +27,8 @@ int cache_of(const syn_kv_cache* c, syn::KvCache* out) {
         return SYN_ERR_SHAPE;
     const int64_t packed = tile * c->n_kv_heads;
     const int64_t stride = c->page_stride ? c->page_stride : packed;
-    if (stride < packed || stride % 16 || stride > kMaxElems / c->n_pages) return SYN_ERR_SHAPE;
+    if (stride < packed || stride % 16 || stride > kMaxElems / c->n_pages || stride >= (int64_t(1) << 35))
+        return SYN_ERR_SHAPE;
     if (!c->k || !c->v) return SYN_ERR_NULL;
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return SYN_ERR_ALIGN;
     out->k = static_cast<uint8_t*>(c->k);

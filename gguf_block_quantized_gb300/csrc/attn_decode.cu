@@ -15,7 +15,7 @@
 //     from zero and is added to the fp32 sums by fma, because the tensor pipe's own additions
 //     truncate.  Scores likewise come from two short chains.  So the result is as exact as fp32
 //     arithmetic allows, which fp32 outputs show.
-//   - Work is cut by length, not by sequence: blocks of steps (4 chunks, one per warp) of all
+//   - Work is cut by length, not by sequence: the steps (4 chunks, one per warp) of all
 //     (sequence, kv head) items are dealt to the CTAs in equal contiguous ranges, found on the
 //     device from the lengths (a captured graph keeps working as they grow).  A CTA whose range
 //     covers an item writes the output; else it leaves a partial in the workspace, and the CTA
@@ -29,11 +29,8 @@
 namespace syn {
 
 constexpr int DEC_WARPS = 4;
-constexpr int DEC_STAGES = 3;
+constexpr int DEC_SLOTS = 3;    // of a warp's ring: the keys or the values of a chunk each
 constexpr int DEC_MAX_SEQ = 1024;  // sequences of one launch (their step counts are in shared memory)
-// Work is dealt in blocks of this many steps: as many as a ring holds, whose loads are in flight
-// together, so cutting a short item finer would not end it sooner.
-constexpr int DEC_BLOCK = 3;
 constexpr float DEC_P_LOG2 = 14.0f;  // p is held as 2^14 p, in fp16: small p stay normal numbers
 
 struct DecodeParams {
@@ -51,6 +48,7 @@ struct DecodeParams {
     int* count;   // per item, zero between calls
     int* err;
     float scale, cap, inv_cap;
+    uint32_t stride16;  // page_stride / 16
     int n_seq, g, n_hg, window, out_f16, whole;
 };
 
@@ -150,20 +148,35 @@ struct DecLayout {
     // rows of one piece); Q8_0: pitches that put the rows a half-warp reads on different banks
     static constexpr int PK = Q8 ? ((D / 32) % 2 ? D : D + 32) : 2 * D;
     static constexpr int PV = Q8 ? D + 16 : 2 * D;
-    static constexpr int K = 0;
-    static constexpr int V = 16 * PK;
-    static constexpr int KS = V + 16 * PV;  // scales [16][dim/32]
-    static constexpr int VS = KS + (Q8 ? D : 0);
-    static constexpr int STAGE = VS + (Q8 ? D : 0);
-    static constexpr int WARP = DEC_STAGES * STAGE;
+    static constexpr int KS = 16 * PK, VS = 16 * PV;  // Q8_0: scales [16][dim/32], behind the rows
+    static constexpr int SLOT = 16 * (PK > PV ? PK : PV) + (Q8 ? D : 0);
+    // (the merge of the warps' parts, up to 16 heads of D fp32 values each, reuses a warp's ring)
+    static constexpr int MERGE = (D <= 128 ? 16 : 8) * D * 4;
+    static constexpr int WARP = DEC_SLOTS * SLOT > MERGE ? DEC_SLOTS * SLOT : MERGE;
     static constexpr int RING = DEC_WARPS * WARP;
 };
 
+// Q8_0: the scales of one row of a chunk (all of a row's at once where the row is as wide as the
+// kernel's, so that they lie on an aligned boundary)
+template <int D, bool EXACT>
+__device__ __forceinline__ void row_scales(const uint8_t* base, int r, int dim, __half (&d)[D / 32]) {
+    if (EXACT) {
+        const uint8_t* q = base + r * (D / 16);
+        if (D == 64) *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint32_t*>(q);
+        else if (D == 128) *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(q);
+        else *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(q);
+    } else {
+#pragma unroll
+        for (int b = 0; b < D / 32; b++) d[b] = b * 32 < dim ? reinterpret_cast<const __half*>(base)[r * (dim >> 5) + b] : __ushort_as_half(0);
+    }
+}
+
 // CTAs per SM that the ring leaves room for (so many registers are a thread's)
 template <int D, bool Q8>
-constexpr int DEC_RESIDENT = D == 64 ? (Q8 ? 4 : 4) : D == 128 ? (Q8 ? 3 : 2) : (Q8 ? 1 : 1);
+constexpr int DEC_RESIDENT = D == 64 ? 5 : D == 128 ? 4 : 2;
 
-template <int D, int NT, bool Q8>
+// D: the row width of the kernel's layout; EXACT: rows are that wide (else narrower: dim < D)
+template <int D, int NT, bool Q8, bool EXACT>
 __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> : 1) k_attn_decode(const DecodeParams p) {
     using L = DecLayout<D, Q8>;
     constexpr int KSTEPS = D / 16;
@@ -175,30 +188,14 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
     int* flags = reinterpret_cast<int*>(sm_l + DEC_WARPS * H);  // [0] scan carry, [1..4] warp sums, [5] last
     int* pre = flags + 8;                                        // [n_seq + 1] blocks before each sequence, of one item
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the shuffle tells the compiler that the warp's index is the same for its lanes)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int r8 = lane >> 2, c4 = lane & 3;
-    const int dim = p.c.dim;
+    const int dim = EXACT ? D : p.c.dim;
     const int n_item_h = p.c.n_kv * p.n_hg;  // items of a sequence
 
-    // blocks of every sequence, as a running sum
-    if (tid == 0) flags[0] = 0, pre[0] = 0;
-    __syncthreads();
-    for (int base = 0; base < p.n_seq; base += 32 * DEC_WARPS) {
-        const int s = base + tid;
-        int n = 0;
-        if (s < p.n_seq) {
-            n = (seq_chunks(seq_visible(p, s, seq_len(p, s))).count() + DEC_WARPS * DEC_BLOCK - 1) / (DEC_WARPS * DEC_BLOCK);
-            if (n == 0) {  // no key to see: zeros, written by the CTAs in turn
-                if (s % gridDim.x == blockIdx.x) {
-                    const int64_t n_out = (int64_t)p.c.n_kv * p.g * dim;
-                    for (int64_t i = 0; i < n_out; i++) {
-                        if (p.out_f16) static_cast<__half*>(p.out)[s * p.out_stride + i] = __float2half_rn(0.0f);
-                        else static_cast<float*>(p.out)[s * p.out_stride + i] = 0.0f;
-                    }
-                }
-            }
-        }
-        int x = n;
+    // pre[s + 1] = the sum of x up to sequence s (128 sequences at a time, flags[0] carries)
+    auto scan = [&](int s, int x) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -212,6 +209,39 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
         __syncthreads();
         if (tid == 32 * DEC_WARPS - 1) flags[0] = before + x;
         __syncthreads();
+    };
+    // steps of every sequence, as a running sum
+    if (tid == 0) flags[0] = 0, pre[0] = 0;
+    __syncthreads();
+    for (int base = 0; base < p.n_seq; base += 32 * DEC_WARPS) {
+        const int s = base + tid;
+        int n = 0;
+        if (s < p.n_seq) {
+            n = (seq_chunks(seq_visible(p, s, seq_len(p, s))).count() + DEC_WARPS - 1) / DEC_WARPS;
+            if (n == 0) {  // no key to see: zeros, written by the CTAs in turn
+                if (s % gridDim.x == blockIdx.x) {
+                    const int64_t n_out = (int64_t)p.c.n_kv * p.g * dim;
+                    for (int64_t i = 0; i < n_out; i++) {
+                        if (p.out_f16) static_cast<__half*>(p.out)[s * p.out_stride + i] = __float2half_rn(0.0f);
+                        else static_cast<float*>(p.out)[s * p.out_stride + i] = 0.0f;
+                    }
+                }
+            }
+        }
+        scan(s, n);
+    }
+    // Little work is dealt in blocks of 3 steps, one a CTA: a step's loads are in flight together
+    // with the next ones', so cutting a short item finer would end it no sooner, and it would have
+    // to be joined.
+    const int block = !p.whole && (int64_t)pre[p.n_seq] * n_item_h <= 3 * (int64_t)gridDim.x ? 3 : 1;
+    if (block > 1) {
+        if (tid == 0) flags[0] = 0;
+        for (int base = 0; base < p.n_seq; base += 32 * DEC_WARPS) {
+            const int s = base + tid;
+            int x = 0;
+            if (s < p.n_seq) x = (seq_chunks(seq_visible(p, s, seq_len(p, s))).count() + DEC_WARPS * block - 1) / (DEC_WARPS * block);
+            scan(s, x);
+        }
     }
     const int64_t total = (int64_t)pre[p.n_seq] * n_item_h;
     if (total == 0) return;
@@ -226,16 +256,36 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
     uint8_t* ring = smem + warp * L::WARP;
     const uint32_t ring_s = smem_u32(ring);
     const int row_pieces = Q8 ? dim >> 4 : dim >> 3;  // 16-byte pieces of a row
-    // A chunk's 16 rows lie one after the other in a page, so lane l copies the 16-byte pieces
-    // l, l + 32, ...: their places in a stage
+    // 16 rows lie one after the other in a page (of 16 rows or more), so lane l copies their
+    // 16-byte pieces l, l + 32, ...: the places in a slot, place(i) of piece i of this lane.  Rows
+    // as wide as the kernel's: with the swizzle they repeat every 8 rows, without it they are linear.
     constexpr int N_COPY = Q8 ? D / 32 : D / 16;
-    uint32_t to_k[N_COPY], to_v[N_COPY];
+    constexpr int N_TO = !EXACT ? N_COPY : Q8 ? 1 : D / 32;
+    uint32_t to_k[N_TO], to_v[N_TO];
 #pragma unroll
-    for (int i = 0; i < N_COPY; i++) {
+    for (int i = 0; i < N_TO; i++) {
         const int idx = i * 32 + lane, r = idx / row_pieces, j = idx - r * row_pieces;
-        to_k[i] = L::K + r * L::PK + (Q8 ? 16 * j : ((j ^ (r & 7)) << 4));
-        to_v[i] = L::V + r * L::PV + (Q8 ? 16 * j : ((j ^ (r & 7)) << 4));
+        to_k[i] = r * L::PK + (Q8 ? 16 * j : ((j ^ (r & 7)) << 4));
+        to_v[i] = r * L::PV + (Q8 ? 16 * j : ((j ^ (r & 7)) << 4));
     }
+    auto place = [&](const uint32_t (&to)[N_TO], int pitch, int i) -> uint32_t {
+        if (!EXACT) return to[i % N_TO];
+        return Q8 ? to[0] + i * (512 / D) * pitch : to[i % N_TO] + (i / N_TO) * 16 * D;
+    };
+    // F16: where ldmatrix finds 16-byte piece 2i (+ 8 for the next four) of this lane's row
+    uint32_t at_k[4], at_v[4];
+    {
+        const int rk = (lane & 7) + ((lane >> 3) & 1) * 8, ck = lane >> 4;
+        const int rv = (lane & 7) + (lane >> 4) * 8, cv = (lane >> 3) & 1;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            at_k[i] = rk * L::PK + (((2 * i + ck) ^ (rk & 7)) << 4);
+            at_v[i] = rv * L::PV + (((2 * i + cv) ^ (rv & 7)) << 4);
+        }
+    }
+    [[maybe_unused]] const int64_t pool_end = p.c.tile + (p.c.n_pages - 1) * p.c.page_stride;  // from a head's tile of page 0
+    const int64_t plane = (int64_t)dim << p.c.page_shift;  // Q8_0: where a tile's scales begin
+    const int page_mask = (1 << p.c.page_shift) - 1;
 
     while (true) {
         // the next segment: blocks [st0, st1) of item (s, kv head h, head group hg)
@@ -319,110 +369,111 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
         }
 
         // this warp's chunks of the segment, every DEC_WARPS-th below `chunk_end`
-        const int chunk0 = st0 * (DEC_WARPS * DEC_BLOCK) + warp;
-        const int chunk_end = min(n_chunks, st1 * (DEC_WARPS * DEC_BLOCK));
-        int next_issue = chunk0;
-        auto all_seen = [&](int row) {  // the 16 rows from `row`
-            return (row >= vis.low && row + 16 <= vis.end) || (row >= vis.first && row + 16 <= vis.pre);
-        };
-        // the page ids of the next chunk to issue, looked up one chunk ahead (rows 0-7 and 8-15)
-        auto page_of = [&](int row) {
+        const int chunk0 = st0 * block * DEC_WARPS + warp, chunk_end = min(n_chunks, st1 * block * DEC_WARPS);
+        // chunks whose 16 rows are all seen, in the causal part, and in one page
+        const int full0 = (vis.low + 15) & ~15;
+        const unsigned full_n = p.c.page_shift >= 4 ? (unsigned)max(0, (vis.end & ~15) - full0) : 0u;
+        auto all_seen = [&](int row) { return (unsigned)(row - full0) < full_n; };
+        bool bad_page = false;
+        auto page_of = [&](int row) {  // -1: past the end, or outside the pool
             if (row >= len) return -1;
             const int id = table[row >> p.c.page_shift];
-            if ((unsigned)id >= (unsigned long long)p.c.n_pages) {
-                record_error(p.err, SYN_DEVERR_BOUNDS);
-                return -1;
-            }
-            return id;
+            const bool ok = (unsigned)id < (unsigned)p.c.n_pages;
+            bad_page |= !ok;
+            return ok ? id : -1;
         };
-        int id_lo = -1, id_hi = -1;
+        // The next chunk whose keys are copied, and the pages of its rows 0-7 and 8-15, looked up one
+        // chunk ahead; the chunk whose values are copied next (its keys are on their way).
+        int k_next = chunk0, id_lo = -1, id_hi = -1;
+        int v_row = -1, v_lo = -1, v_hi = -1;
+        bool v_whole = false;
+        int64_t v_off = 0;  // of the chunk's first row from a head's tile of page 0
         auto look_up = [&]() {
-            if (next_issue < chunk_end) {
-                const int row = ch.at(next_issue) << 4;
+            if (k_next < chunk_end) {
+                const int row = ch.at(k_next) << 4;
                 id_lo = page_of(row);
                 id_hi = p.c.page_shift >= 4 ? id_lo : page_of(row + 8);
             }
         };
         look_up();
-        [[maybe_unused]] const int64_t pool_end = p.c.tile + (p.c.n_pages - 1) * p.c.page_stride;  // from a head's tile of page 0
-        const int64_t plane = (int64_t)dim << p.c.page_shift;                     // Q8_0: a tile's scales
-        const int n_sp = dim >> 4;  // Q8_0: 16-byte pieces of 16 rows' scales (at most 16)
-        auto issue = [&](int stage) {
-            if (next_issue < chunk_end) {
-                const int row0 = ch.at(next_issue) << 4;
-                const uint32_t dst = ring_s + stage * L::STAGE;
-                const int cell_lo = row0 & ((1 << p.c.page_shift) - 1);
-                if (p.c.page_shift >= 4 && id_lo >= 0 && all_seen(row0)) {
-                    const int64_t off = (int64_t)id_lo * p.c.page_stride + (int64_t)cell_lo * row_pieces * 16;
-                    if (SYN_IN_BOUNDS(off >= 0 && off + 256 * row_pieces <= pool_end)) {
-                        const uint8_t *ks = kbase + off + 16 * lane, *vs = vbase + off + 16 * lane;
+        auto copy = [&](uint32_t dst, const uint8_t* base, const uint32_t (&to)[N_TO], int pitch, int scales) {
+            if (v_whole) {
+                const uint8_t* src = base + v_off + 16 * lane;
+                if (!SYN_IN_BOUNDS(v_off >= 0 && v_off + 256 * row_pieces <= pool_end)) return;
 #pragma unroll
-                        for (int i = 0; i < N_COPY; i++) {
-                            if (2 * i >= row_pieces) break;
-                            cp16_all(dst + to_k[i], ks + 512 * i);
-                            cp16_all(dst + to_v[i], vs + 512 * i);
-                        }
-                        if (Q8 && lane < 2 * n_sp) {
-                            const int i = lane < n_sp ? lane : lane - n_sp;
-                            cp16_all(dst + (lane < n_sp ? L::KS : L::VS) + 16 * i,
-                                     (lane < n_sp ? kbase : vbase) + (int64_t)id_lo * p.c.page_stride + plane + (int64_t)cell_lo * n_sp + 16 * i);
-                        }
-                    }
-                } else {
-                    // a chunk at an end of what is seen, or over two pages: rows that the query does
-                    // not see are not read but zero (a masked V row may hold anything, and 0 * inf is
-                    // not 0)
-                    const int64_t off_lo = (int64_t)max(id_lo, 0) * p.c.page_stride, off_hi = (int64_t)max(id_hi, 0) * p.c.page_stride;
-                    const int cell_hi = p.c.page_shift >= 4 ? cell_lo + 8 : 0;
-#pragma unroll
-                    for (int i = 0; i < N_COPY; i++) {
-                        if (2 * i >= row_pieces) break;
-                        const int r = (int)(to_k[i] - L::K) / L::PK, j = i * 32 + lane - r * row_pieces;
-                        const bool upper = r >= 8;
-                        const bool ok = (upper ? id_hi : id_lo) >= 0 && vis(row0 + r);
-                        const int64_t off = ok ? (upper ? off_hi + (int64_t)(cell_hi + r - 8) * row_pieces * 16
-                                                        : off_lo + (int64_t)(cell_lo + r) * row_pieces * 16) + 16 * j
-                                               : 0;
-                        if (!SYN_IN_BOUNDS(off >= 0 && off + 16 <= pool_end)) continue;
-                        cp16(dst + to_k[i], kbase + off, ok ? 16u : 0u);
-                        cp16(dst + to_v[i], vbase + off, ok ? 16u : 0u);
-                    }
-                    if (Q8 && lane < 2 * n_sp) {  // scales: rows 0-7 and 8-15 apart
-                        const int i = lane < n_sp ? lane : lane - n_sp;
-                        const bool upper = 2 * i >= n_sp;
-                        const bool ok = (upper ? id_hi : id_lo) >= 0;
-                        const int64_t off = ok ? plane + (upper ? off_hi + (int64_t)cell_hi * n_sp + 16 * (i - n_sp / 2)
-                                                                : off_lo + (int64_t)cell_lo * n_sp + 16 * i)
-                                               : 0;
-                        if (SYN_IN_BOUNDS(off >= 0 && off + 16 <= pool_end))
-                            cp16(dst + (lane < n_sp ? L::KS : L::VS) + 16 * i, (lane < n_sp ? kbase : vbase) + off, ok ? 16u : 0u);
-                    }
+                for (int i = 0; i < N_COPY; i++) {
+                    if (2 * i >= row_pieces) break;
+                    cp16_all(dst + place(to, pitch, i), src + 512 * i);
                 }
-                next_issue += DEC_WARPS;
+                // Q8_0: the rows' scales, dim/16 pieces (rows of 16 * row_pieces bytes, scales of row_pieces)
+                if (Q8 && lane < row_pieces)
+                    cp16_all(dst + scales + 16 * lane, src + plane - (v_row & page_mask) * (15 * row_pieces));
+                return;
+            }
+            // a chunk at an end of what is seen, or pages of 8 rows: rows that the query does not
+            // see are not read but zero (a masked V row may hold anything, and 0 * inf is not 0)
+            const int64_t page = (int64_t)max(v_lo, 0) * p.c.page_stride, page_hi = (int64_t)max(v_hi, 0) * p.c.page_stride;
+            const int cell = v_row & page_mask, cell_hi = (v_row + 8) & page_mask;
+#pragma unroll
+            for (int i = 0; i < N_COPY; i++) {
+                if (2 * i >= row_pieces) break;
+                const uint32_t at_dst = place(to, pitch, i);
+                const int r = (int)at_dst / pitch, j = i * 32 + lane - r * row_pieces;
+                const bool upper = r >= 8, ok = (upper ? v_hi : v_lo) >= 0 && vis(v_row + r);
+                const int64_t off = ok ? (upper ? page_hi + (int64_t)(cell_hi + r - 8) * (row_pieces * 16)
+                                                : page + (int64_t)(cell + r) * (row_pieces * 16)) + 16 * j
+                                       : 0;
+                if (!SYN_IN_BOUNDS(off >= 0 && off + 16 <= pool_end)) continue;
+                cp16(dst + at_dst, base + off, ok ? 16u : 0u);
+            }
+            if (Q8 && lane < row_pieces) {  // scales: rows 0-7 and 8-15 apart
+                const bool upper = 2 * lane >= row_pieces, ok = (upper ? v_hi : v_lo) >= 0;
+                const int64_t off = ok ? plane + (upper ? page_hi + (int64_t)cell_hi * row_pieces + 16 * (lane - row_pieces / 2)
+                                                        : page + (int64_t)cell * row_pieces + 16 * lane)
+                                       : 0;
+                if (SYN_IN_BOUNDS(off >= 0 && off + 16 <= pool_end)) cp16(dst + scales + 16 * lane, base + off, ok ? 16u : 0u);
+            }
+        };
+        auto issue_k = [&](int slot) {
+            v_row = -1;
+            if (k_next < chunk_end) {
+                v_row = ch.at(k_next) << 4;
+                v_lo = id_lo;
+                v_hi = id_hi;
+                v_whole = v_lo >= 0 && all_seen(v_row);
+                v_off = (int64_t)((uint64_t)(uint32_t)v_lo * p.stride16 + (uint32_t)((v_row & page_mask) * row_pieces)) << 4;
+                copy(ring_s + slot * L::SLOT, kbase, to_k, L::PK, L::KS);
+                k_next += DEC_WARPS;
                 look_up();
             }
             cp_commit();
         };
-#pragma unroll
-        for (int i = 0; i < DEC_STAGES - 1; i++) issue(i);
+        auto issue_v = [&](int slot) {
+            if (v_row >= 0) copy(ring_s + slot * L::SLOT, vbase, to_v, L::PV, L::VS);
+            cp_commit();
+        };
+        issue_k(0);
+        issue_v(1);
+        issue_k(2);
 
-        int stage = 0;
+        int sk = 0, sv = 1;  // slots of the chunk's keys and values
         for (int ci = chunk0; ci < chunk_end; ci += DEC_WARPS) {
-            cp_wait<DEC_STAGES - 2>();
-            __syncwarp();
-            issue(stage == 0 ? DEC_STAGES - 1 : stage - 1);
             const int row0 = ch.at(ci) << 4;
-            const uint32_t st = ring_s + stage * L::STAGE;
-            const uint8_t* stp = ring + stage * L::STAGE;
             const bool full = all_seen(row0);
-            const bool seen_a = full || vis(row0 + r8), seen_b = full || vis(row0 + r8 + 8);
+            const uint32_t kt = ring_s + sk * L::SLOT, vt = ring_s + sv * L::SLOT;
+            const uint8_t *ktp = ring + sk * L::SLOT, *vtp = ring + sv * L::SLOT;
+            cp_wait<2>();
+            __syncwarp();
 
-            // S^T = K Q^T
+            // S^T = K Q^T, rows lane/4 and lane/4 + 8
             float sc[NT][4];
             if (Q8) {
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
                 const __half2 k1152 = __float2half2_rn(1152.0f);
+                alignas(16) __half da[D / 32], db[D / 32];
+                row_scales<D, EXACT>(ktp + L::KS, r8, dim, da);
+                row_scales<D, EXACT>(ktp + L::KS, r8 + 8, dim, db);
 #pragma unroll
                 for (int b = 0; b < D / 32; b++) {
                     if (b * 32 >= dim) break;
@@ -430,48 +481,45 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     uint32_t a0[4], a1[4];
 #pragma unroll
                     for (int u = 0; u < 2; u++) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(stp + L::K + (r8 + 8 * u) * L::PK + 32 * b + 8 * c4);
+                        const uint2 w = *reinterpret_cast<const uint2*>(ktp + (r8 + 8 * u) * L::PK + 32 * b + 8 * c4);
                         const uint32_t x = w.x ^ 0x80808080u, y = w.y ^ 0x80808080u;
                         a0[u] = h2u(__hsub2(u2h(__byte_perm(x, 0x64646464u, 0x4140)), k1152));
                         a0[2 + u] = h2u(__hsub2(u2h(__byte_perm(x, 0x64646464u, 0x4342)), k1152));
                         a1[u] = h2u(__hsub2(u2h(__byte_perm(y, 0x64646464u, 0x4140)), k1152));
                         a1[2 + u] = h2u(__hsub2(u2h(__byte_perm(y, 0x64646464u, 0x4342)), k1152));
                     }
-                    const float da = h2f_bits(*reinterpret_cast<const uint16_t*>(stp + L::KS + 2 * (r8 * (dim >> 5) + b)));
-                    const float db = h2f_bits(*reinterpret_cast<const uint16_t*>(stp + L::KS + 2 * ((r8 + 8) * (dim >> 5) + b)));
+                    const float fa = __half2float(da[b]), fb = __half2float(db[b]);
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
                         float c[4];
                         mma16816_zero(c, a0, qf[2 * b][nt][0], qf[2 * b][nt][1]);
                         mma16816(c, a1, qf[2 * b + 1][nt][0], qf[2 * b + 1][nt][1]);
-                        sc[nt][0] = fmaf(c[0], da, sc[nt][0]);
-                        sc[nt][1] = fmaf(c[1], da, sc[nt][1]);
-                        sc[nt][2] = fmaf(c[2], db, sc[nt][2]);
-                        sc[nt][3] = fmaf(c[3], db, sc[nt][3]);
+                        sc[nt][0] = fmaf(c[0], fa, sc[nt][0]);
+                        sc[nt][1] = fmaf(c[1], fa, sc[nt][1]);
+                        sc[nt][2] = fmaf(c[2], fb, sc[nt][2]);
+                        sc[nt][3] = fmaf(c[3], fb, sc[nt][3]);
                     }
                 }
             } else {
                 float s1[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++) sc[nt][j] = s1[nt][j] = 0.0f;
-                const int rr = (lane & 7) + ((lane >> 3) & 1) * 8, cc = lane >> 4;
-                const uint32_t rowa = st + L::K + rr * L::PK;
-#pragma unroll
                 for (int ks = 0; ks < KSTEPS; ks++) {
                     if (ks * 16 >= dim) break;
                     uint32_t a[4];
-                    ldsm4(rowa + (((2 * ks + cc) ^ (rr & 7)) << 4), a);
+                    ldsm4(kt + at_k[ks & 3] + 128 * (ks >> 2), a);
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++)
-                        mma16816(ks & 1 ? s1[nt] : sc[nt], a, qf[ks][nt][0], qf[ks][nt][1]);
+                    for (int nt = 0; nt < NT; nt++) {
+                        if (ks < 2) mma16816_zero(ks & 1 ? s1[nt] : sc[nt], a, qf[ks][nt][0], qf[ks][nt][1]);
+                        else mma16816(ks & 1 ? s1[nt] : sc[nt], a, qf[ks][nt][0], qf[ks][nt][1]);
+                    }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                     for (int j = 0; j < 4; j++) sc[nt][j] += s1[nt][j];
             }
+            __syncwarp();  // every lane has read the keys before their slot is filled again
+            issue_v(sk);
 
             // softmax of the chunk, in powers of two
             uint32_t ph[NT][2], pl[NT][2];  // F16: P^T as the B operand (heads and tails)
@@ -490,8 +538,8 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     for (int j = 0; j < 4; j++) sc[nt][j] *= scale_log2;
                 }
                 if (!full) {
-                    if (!seen_a) sc[nt][0] = sc[nt][1] = -INFINITY;
-                    if (!seen_b) sc[nt][2] = sc[nt][3] = -INFINITY;
+                    if (!vis(row0 + r8)) sc[nt][0] = sc[nt][1] = -INFINITY;
+                    if (!vis(row0 + r8 + 8)) sc[nt][2] = sc[nt][3] = -INFINITY;
                 }
 #pragma unroll
                 for (int j = 0; j < 2; j++) {
@@ -502,48 +550,47 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     const float ms = mx == -INFINITY ? 0.0f : mx;  // nothing seen yet
                     alpha[nt][j] = ex2(m[nt][j] - ms);
                     m[nt][j] = mx;
-                    pr[nt][j] = ex2(sc[nt][j] - ms + DEC_P_LOG2);
-                    pr[nt][j + 2] = ex2(sc[nt][j + 2] - ms + DEC_P_LOG2);
+                    pr[nt][j] = ex2(sc[nt][j] - (ms - DEC_P_LOG2));
+                    pr[nt][j + 2] = ex2(sc[nt][j + 2] - (ms - DEC_P_LOG2));
                     l[nt][j] = fmaf(l[nt][j], alpha[nt][j], pr[nt][j] + pr[nt][j + 2]);
                 }
                 if (!Q8) {
-                    uint32_t hi, lo;
-                    split_pair(pr[nt][0], pr[nt][1], hi, lo);
-                    ph[nt][0] = transpose8(hi);
-                    pl[nt][0] = transpose8(lo);
-                    split_pair(pr[nt][2], pr[nt][3], hi, lo);
-                    ph[nt][1] = transpose8(hi);
-                    pl[nt][1] = transpose8(lo);
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        uint32_t hi, lo;
+                        split_pair(pr[nt][2 * i], pr[nt][2 * i + 1], hi, lo);
+                        ph[nt][i] = transpose8(hi);
+                        pl[nt][i] = transpose8(lo);
+                    }
                 }
             }
+            cp_wait<2>();
+            __syncwarp();
 
             // O^T = O^T * alpha + V^T P^T
             if (Q8) {
                 // A row's value scales go into p, in fp32 and before the split, relative to 2^e, the
                 // largest power of two among the scales so far: p * scale then fits fp16 whatever
                 // the scales (o is kept in units of 2^e, as it is relative to 2^m).
-                uint32_t dv[D / 32][2];  // scales of rows (2c, 2c+1), (2c+8, 2c+9) of each block
+                alignas(16) __half dv[4][D / 32];  // scales of rows 2c, 2c+1, 2c+8, 2c+9
                 uint32_t top = 0;
 #pragma unroll
-                for (int b = 0; b < D / 32; b++) {
-                    if (b * 32 >= dim) break;
-                    const uint16_t* sv = reinterpret_cast<const uint16_t*>(stp + L::VS) + 2 * c4 * (dim >> 5) + b;
+                for (int u = 0; u < 4; u++) {
+                    const int r = 2 * c4 + (u & 1) + 8 * (u >> 1);
+                    row_scales<D, EXACT>(vtp + L::VS, r, dim, dv[u]);
+                    if (!full && !vis(row0 + r)) {
 #pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        uint32_t x = sv[8 * u * (dim >> 5)], y = sv[(8 * u + 1) * (dim >> 5)];
-                        if (!full) {
-                            x = vis(row0 + 2 * c4 + 8 * u) ? x : 0u;
-                            y = vis(row0 + 2 * c4 + 8 * u + 1) ? y : 0u;
-                        }
-                        dv[b][u] = x | y << 16;
-                        top = max(top, max(x, y) & 0x7FFFu);
+                        for (int b = 0; b < D / 32; b++) dv[u][b] = __ushort_as_half(0);
                     }
+#pragma unroll
+                    for (int b = 0; b < D / 32; b++)
+                        if (b * 32 < dim) top = max(top, (uint32_t)__half_as_ushort(dv[u][b]) & 0x7FFFu);
                 }
                 const int e_new = max(e_run, (int)(__reduce_max_sync(0xffffffffu, top) >> 10));
                 const float down = __int_as_float((127 + 15 - e_new) << 23), step = __int_as_float((127 + e_run - e_new) << 23);
                 e_run = e_new;
-                // p in the B operand's layout: rows 2c, 2c+1, 2c+8, 2c+9 of head lane/4, as the upper and
-                // lower halves of the fp32 words
+                // p in the B operand's layout (rows 2c, 2c+1, 2c+8, 2c+9 of head lane/4): the upper and
+                // lower halves of the fp32 words transposed apart
                 float pb[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
@@ -564,7 +611,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     uint32_t a0[4], a1[4];
 #pragma unroll
                     for (int u = 0; u < 2; u++) {
-                        const uint8_t* vr = stp + L::V + (2 * c4 + 8 * u) * L::PV + 32 * b + 4 * r8;
+                        const uint8_t* vr = vtp + (2 * c4 + 8 * u) * L::PV + 32 * b + 4 * r8;
                         const uint32_t x = *reinterpret_cast<const uint32_t*>(vr) ^ 0x80808080u;
                         const uint32_t y = *reinterpret_cast<const uint32_t*>(vr + L::PV) ^ 0x80808080u;
                         const uint32_t x01 = __byte_perm(x, y, 0x5140), x23 = __byte_perm(x, y, 0x7362);
@@ -573,12 +620,11 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                         a1[2 * u] = h2u(__hsub2(u2h(__byte_perm(x23, 0x64646464u, 0x4140)), k1152));
                         a1[2 * u + 1] = h2u(__hsub2(u2h(__byte_perm(x23, 0x64646464u, 0x4342)), k1152));
                     }
-                    const float2 d0 = __half22float2(u2h(dv[b][0])), d1 = __half22float2(u2h(dv[b][1]));
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
                         uint32_t hi0, lo0, hi1, lo1;
-                        split_pair(pb[nt][0] * d0.x, pb[nt][1] * d0.y, hi0, lo0);
-                        split_pair(pb[nt][2] * d1.x, pb[nt][3] * d1.y, hi1, lo1);
+                        split_pair(pb[nt][0] * __half2float(dv[0][b]), pb[nt][1] * __half2float(dv[1][b]), hi0, lo0);
+                        split_pair(pb[nt][2] * __half2float(dv[2][b]), pb[nt][3] * __half2float(dv[3][b]), hi1, lo1);
 #pragma unroll
                         for (int u = 0; u < 2; u++) {
                             float c[4];
@@ -590,13 +636,11 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     }
                 }
             } else {
-                const int rr = (lane & 7) + (lane >> 4) * 8, cc = (lane >> 3) & 1;
-                const uint32_t rowa = st + L::V + rr * L::PV;
 #pragma unroll
                 for (int mt = 0; mt < KSTEPS; mt++) {
                     if (mt * 16 >= dim) break;
                     uint32_t a[4];
-                    ldsm4t(rowa + (((2 * mt + cc) ^ (rr & 7)) << 4), a);
+                    ldsm4t(vt + at_v[mt & 3] + 128 * (mt >> 2), a);
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
                         float c[4];
@@ -607,10 +651,13 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     }
                 }
             }
-            stage = stage == DEC_STAGES - 1 ? 0 : stage + 1;
-            __syncwarp();  // every lane has read the stage before it is filled again
+            __syncwarp();  // every lane has read the values
+            issue_k(sv);
+            sk = sk == 0 ? 2 : sk - 1;
+            sv = sv == 0 ? 2 : sv - 1;
         }
         cp_wait<0>();
+        if (bad_page) record_error(p.err, SYN_DEVERR_BOUNDS);
 
         // the warps' parts of the segment, joined in shared memory
 #pragma unroll
@@ -619,10 +666,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
             for (int j = 0; j < 2; j++) {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
-                if (r8 == 0) {
-                    sm_m[warp * H + nt * 8 + 2 * c4 + j] = m[nt][j];
-                    sm_l[warp * H + nt * 8 + 2 * c4 + j] = l[nt][j];
-                }
+                if (r8 == 0) sm_m[warp * H + nt * 8 + 2 * c4 + j] = m[nt][j];
             }
         __syncthreads();
         float* buf = reinterpret_cast<float*>(ring);  // [H][D], this warp's
@@ -634,6 +678,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                 float mx = sm_m[hd];
                 for (int w = 1; w < DEC_WARPS; w++) mx = fmaxf(mx, sm_m[w * H + hd]);
                 float f = ex2(m[nt][j] - (mx == -INFINITY ? 0.0f : mx));
+                if (r8 == 0) sm_l[warp * H + hd] = l[nt][j] * f;  // (read after the next barrier)
                 if (Q8) f *= __int_as_float((127 - 15 + e_run) << 23);
                 if (hd < heads) {
 #pragma unroll
@@ -653,22 +698,22 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
         float* part = p.part + (2 * (int64_t)blockIdx.x + (st0 == 0)) * H * (D + 2);
         for (int i = tid; i < heads * dim; i += 32 * DEC_WARPS) {
             const int hd = i / dim, e = i - hd * dim;
-            float mx = sm_m[hd], acc = 0.0f, sum = 0.0f;
-            for (int w = 1; w < DEC_WARPS; w++) mx = fmaxf(mx, sm_m[w * H + hd]);
-            const float ms = mx == -INFINITY ? 0.0f : mx;
+            float acc = 0.0f, sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < DEC_WARPS; w++) {
                 acc += reinterpret_cast<const float*>(smem + w * L::WARP)[hd * D + e];
-                sum = fmaf(sm_l[w * H + hd], ex2(sm_m[w * H + hd] - ms), sum);
+                sum += sm_l[w * H + hd];
             }
             if (direct) {
                 const int64_t at_out = s * p.out_stride + (int64_t)(h * p.g + head0 + hd) * dim + e;
-                const float y = sum == 0.0f ? 0.0f : acc / sum;
+                const float y = sum == 0.0f ? 0.0f : __fdividef(acc, sum);
                 if (p.out_f16) static_cast<__half*>(p.out)[at_out] = __float2half_rn(y);
                 else static_cast<float*>(p.out)[at_out] = y;
             } else {
                 __stcg(part + hd * (D + 2) + e, acc);
                 if (e == 0) {
+                    float mx = sm_m[hd];
+                    for (int w = 1; w < DEC_WARPS; w++) mx = fmaxf(mx, sm_m[w * H + hd]);
                     __stcg(part + hd * (D + 2) + D, mx);
                     __stcg(part + hd * (D + 2) + D + 1, sum);
                 }
@@ -689,20 +734,41 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
             __syncthreads();
             if (flags[5]) {
                 __threadfence();
+                // joint maximum and sum of each head (sm_m and sm_l of warp 0 are free), then the
+                // weighted values, whose loads are independent
+                const float* first = p.part + (2 * (int64_t)i0 + 1) * H * (D + 2);
+                const float* rest = p.part + 2 * (int64_t)i0 * H * (D + 2);
+                const int64_t pitch = 2 * H * (D + 2);
+                for (int hd = warp; hd < heads; hd += DEC_WARPS) {
+                    float mx = -INFINITY, sum = 0.0f;
+                    for (int c = lane; c <= i1 - i0; c += 32)
+                        mx = fmaxf(mx, __ldcg((c == 0 ? first : rest + c * pitch) + hd * (D + 2) + D));
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    const float ms = mx == -INFINITY ? 0.0f : mx;
+                    for (int c = lane; c <= i1 - i0; c += 32) {
+                        const float* q = (c == 0 ? first : rest + c * pitch) + hd * (D + 2);
+                        sum = fmaf(__ldcg(q + D + 1), ex2(__ldcg(q + D) - ms), sum);
+                    }
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                    if (lane == 0) {
+                        sm_m[hd] = ms;
+                        sm_l[hd] = sum;
+                    }
+                }
+                __syncthreads();
                 for (int i = tid; i < heads * dim; i += 32 * DEC_WARPS) {
                     const int hd = i / dim, e = i - hd * dim;
-                    float mx = -INFINITY, sum = 0.0f, acc = 0.0f;
-                    for (int c = i0; c <= i1; c++) {
-                        const float* q = p.part + ((2 * (int64_t)c + (c == i0)) * H + hd) * (D + 2);
-                        const float pm = __ldcg(q + D), pl2 = __ldcg(q + D + 1), po = __ldcg(q + e);
-                        const float nm = fmaxf(mx, pm), ms = nm == -INFINITY ? 0.0f : nm;
-                        const float fa = ex2(mx - ms), fb = ex2(pm - ms);
-                        acc = acc * fa + po * fb;
-                        sum = sum * fa + pl2 * fb;
-                        mx = nm;
+                    const float ms = sm_m[hd], sum = sm_l[hd];
+                    float acc = 0.0f;
+#pragma unroll 8
+                    for (int c = 0; c <= i1 - i0; c++) {
+                        const float* q = (c == 0 ? first : rest + c * pitch) + hd * (D + 2);
+                        acc = fmaf(__ldcg(q + e), ex2(__ldcg(q + D) - ms), acc);
                     }
                     const int64_t at_out = s * p.out_stride + (int64_t)(h * p.g + head0 + hd) * dim + e;
-                    const float y = sum == 0.0f ? 0.0f : acc / sum;
+                    const float y = sum == 0.0f ? 0.0f : __fdividef(acc, sum);
                     if (p.out_f16) static_cast<__half*>(p.out)[at_out] = __float2half_rn(y);
                     else static_cast<float*>(p.out)[at_out] = y;
                 }
@@ -714,9 +780,9 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
 
 // ---- host side ---------------------------------------------------------------------------
 
-template <int D, int NT, bool Q8>
-static cudaError_t run_decode(const DecodeParams& p, int sms, cudaStream_t s) {
-    auto kern = k_attn_decode<D, NT, Q8>;
+template <int D, int NT, bool Q8, bool EXACT>
+static cudaError_t run_decode_as(const DecodeParams& p, int sms, cudaStream_t s) {
+    auto kern = k_attn_decode<D, NT, Q8, EXACT>;
     constexpr int smem = DecLayout<D, Q8>::RING + 2 * DEC_WARPS * 8 * NT * 4 + 32 + 4 * (DEC_MAX_SEQ + 1);
     static ResidentCtas resident;  // per device, looked up once
     int per_sm = 0;
@@ -725,6 +791,11 @@ static cudaError_t run_decode(const DecodeParams& p, int sms, cudaStream_t s) {
     const int grid = sms * std::min(per_sm, DECODE_CTAS_PER_SM);
     kern<<<grid, 32 * DEC_WARPS, smem, s>>>(p);
     return cudaGetLastError();
+}
+
+template <int D, int NT, bool Q8>
+static cudaError_t run_decode(const DecodeParams& p, int sms, cudaStream_t s) {
+    return p.c.dim == D ? run_decode_as<D, NT, Q8, true>(p, sms, s) : run_decode_as<D, NT, Q8, false>(p, sms, s);
 }
 
 // heads of a group: two columns of 8 where there are more than 8 and the accumulators fit
@@ -765,6 +836,7 @@ cudaError_t launch_attn_decode(const KvCache& c, const AttnDesc& a, int64_t n_se
         p.g = a.n_heads / c.n_kv;
         const int nt = decode_nt(p.g, c.dim);
         p.n_hg = (p.g + 8 * nt - 1) / (8 * nt);
+        p.stride16 = (uint32_t)(c.page_stride >> 4);
         p.window = a.window;
         p.out_f16 = a.out_f16;
         p.whole = whole;

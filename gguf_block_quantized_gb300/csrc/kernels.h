@@ -91,7 +91,7 @@ cudaError_t launch_kv_read(const KvCache& c, int64_t n, const int64_t* slots, vo
 // One token of each sequence.  part (decode_part_floats) and count (decode_count_words, zero
 // before the first call and left zero by every call) are the launch's scratch.  whole: no item
 // is split between CTAs.  *launches gets the number of kernels.
-constexpr int DECODE_CTAS_PER_SM = 4;
+constexpr int DECODE_CTAS_PER_SM = 5;
 cudaError_t launch_attn_decode(const KvCache& c, const AttnDesc& a, int64_t n_seq, const void* q, const int32_t* pages,
                                int64_t max_pages, const int32_t* lens, void* out, float* part, int* count, bool whole,
                                int* err, int sms, int* launches, cudaStream_t s);

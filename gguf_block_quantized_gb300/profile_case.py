@@ -18,6 +18,7 @@ Cases (synthetic weights ~N(0, 0.02), activations ~N(0, 1)):
   kv_append_f16, kv_append_q8  4096 tokens of 32 / 8 heads of 128 into a paged cache (150 MB moved)
   attn_decode_f16, attn_decode_q8  one token of each of 48 sequences of 2000 cached tokens, 32 / 8
                      heads of 128, pages of 64 (F16: 393 MB of rows)
+  attn_decode_long_f16, attn_decode_long_q8  one token of one sequence of 96000 rows
   attn_prefill_f16, attn_prefill_q8  a prompt of 4096 tokens, 32 / 8 heads of 128
 """
 from __future__ import annotations
@@ -34,7 +35,8 @@ CASES = {
 }
 
 
-ATTN = ["kv_append_f16", "kv_append_q8", "attn_decode_f16", "attn_decode_q8", "attn_prefill_f16", "attn_prefill_q8"]
+ATTN = ["kv_append_f16", "kv_append_q8", "attn_decode_f16", "attn_decode_q8", "attn_decode_long_f16",
+        "attn_decode_long_q8", "attn_prefill_f16", "attn_prefill_q8"]
 
 
 def attn_case(case: str, reps: int):
@@ -45,17 +47,19 @@ def attn_case(case: str, reps: int):
 
     heads, kv, dim, page = 32, 8, 128, 64
     t = syn.Q8_0 if case.endswith("q8") else syn.F16
-    seqs, rows = (48, 2000) if "decode" in case else (1, 4096)
+    seqs, rows = (1, 96000) if "long" in case else (48, 2000) if "decode" in case else (1, 4096)
     per = -(-rows // page)
     cache = syn.KVCache.empty(t, kv, dim, page, seqs * per)
     pages = torch.randperm(seqs * per, device="cuda").to(torch.int32).view(seqs, per)
-    row = torch.arange(rows, device="cuda")
-    fused = torch.randn((rows, heads + 2 * kv, dim), device="cuda")
+    n = min(rows, 8192)  # rows appended at once
+    row = torch.arange(n, device="cuda")
+    fused = torch.randn((n, heads + 2 * kv, dim), device="cuda")
     parts = {"q": fused[:, :heads], "k": fused[:, heads:heads + kv], "v": fused[:, heads + kv:]}
     rope = syn.Rope(dim, 500000.0, layout=syn.ROPE_ADJACENT)
     pos = row.to(torch.int32)
-    for s in range(seqs):
-        slots = pages[s].long()[row // page] * page + row % page
+    for s, base in [(s, b) for s in range(seqs) for b in range(0, rows - n + 1, n)]:
+        at = base + row
+        slots = pages[s].long()[at // page] * page + at % page
         append = syn.prepare_kv_append(cache, rope, parts["k"], parts["v"], pos, slots, parts["q"])
         q = append()
     lens = torch.full((seqs,), rows, dtype=torch.int32, device="cuda")

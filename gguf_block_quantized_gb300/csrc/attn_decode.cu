@@ -156,6 +156,96 @@ struct DecLayout {
     static constexpr int RING = DEC_WARPS * WARP;
 };
 
+// One CTA joins the partials of CTAs i0 .. i1 of an item and writes its output (at `at`).  The
+// weights 2^(m_i - m) of up to JOIN_TILE parts are laid into shared memory, then every thread adds
+// up 4 neighbouring values, its loads independent of each other; where the item has few values the
+// threads share its parts out.
+constexpr int JOIN_TILE = 64;
+template <int D, int H>
+__device__ __noinline__ void join_parts(const DecodeParams& p, int i0, int i1, int heads, int dim, uint8_t* smem, float* sm_m,
+                                        float* sm_l, int64_t at) {
+    constexpr int T = 32 * DEC_WARPS;
+    float* w = reinterpret_cast<float*>(smem);                      // [JOIN_TILE][H]
+    float4* sums = reinterpret_cast<float4*>(w + JOIN_TILE * H);    // [T]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n = i1 - i0 + 1, pitch = H * (D + 2);
+    // the first part is in the slot of a segment that begins its item
+    auto part_of = [&](int c) { return p.part + (2 * (int64_t)(i0 + c) + (c == 0)) * pitch; };
+    for (int hd = warp; hd < heads; hd += DEC_WARPS) {
+        float mx = -INFINITY, sum = 0.0f;
+        for (int c = lane; c < n; c += 32) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of(c) + H * D) + hd);
+            const float nm = fmaxf(mx, ml.x), ms = nm == -INFINITY ? 0.0f : nm;
+            sum = sum * ex2(mx - ms) + ml.y * ex2(ml.x - ms);
+            mx = nm;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            const float om = __shfl_xor_sync(0xffffffffu, mx, off), os = __shfl_xor_sync(0xffffffffu, sum, off);
+            const float nm = fmaxf(mx, om), ms = nm == -INFINITY ? 0.0f : nm;
+            sum = sum * ex2(mx - ms) + os * ex2(om - ms);
+            mx = nm;
+        }
+        if (lane == 0) {
+            sm_m[hd] = mx == -INFINITY ? 0.0f : mx;
+            sm_l[hd] = sum;
+        }
+    }
+    __syncthreads();
+    const int nv = heads * dim >> 2, dv = dim >> 2;  // 4-value pieces of the item, of a head
+    const int shares = max(1, T / nv), share = nv < T ? tid / nv : 0;
+    for (int v0 = 0; v0 < nv; v0 += T) {
+        const int v = nv < T ? tid - share * nv : v0 + tid;
+        const bool mine = v < nv && share < shares;
+        const int hd = mine ? v / dv : 0, e = (v - hd * dv) << 2;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int c0 = 0; c0 < n; c0 += JOIN_TILE) {
+            const int m = min(JOIN_TILE, n - c0);
+            __syncthreads();
+            for (int i = tid; i < m * heads; i += T) {
+                const int c = i / heads, x = i - c * heads;
+                w[c * H + x] = ex2(__ldcg(part_of(c0 + c) + H * D + 2 * x) - sm_m[x]);
+            }
+            __syncthreads();
+            if (mine) {
+#pragma unroll 16
+                for (int c = share; c < m; c += shares) {
+                    const float4 o = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + c) + hd * D + e));
+                    const float f = w[c * H + hd];
+                    acc.x = fmaf(o.x, f, acc.x);
+                    acc.y = fmaf(o.y, f, acc.y);
+                    acc.z = fmaf(o.z, f, acc.z);
+                    acc.w = fmaf(o.w, f, acc.w);
+                }
+            }
+        }
+        if (shares > 1) {
+            __syncthreads();
+            sums[tid] = acc;
+            __syncthreads();
+            if (share == 0)
+                for (int x = 1; x < shares; x++) {
+                    const float4 o = sums[x * nv + v];
+                    acc.x += o.x;
+                    acc.y += o.y;
+                    acc.z += o.z;
+                    acc.w += o.w;
+                }
+        }
+        if (mine && share == 0) {
+            const float sum = sm_l[hd];
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int64_t a = at + (int64_t)hd * dim + e;
+            if (p.out_f16) {
+                const __half2 x = __floats2half2_rn(acc.x * inv, acc.y * inv), y = __floats2half2_rn(acc.z * inv, acc.w * inv);
+                *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + a) = make_uint2(h2u(x), h2u(y));
+            } else {
+                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + a) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            }
+        }
+    }
+}
+
 // Q8_0: the scales of one row of a chunk (all of a row's at once where the row is as wide as the
 // kernel's, so that they lie on an aligned boundary)
 template <int D, bool EXACT>
@@ -181,7 +271,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
     using L = DecLayout<D, Q8>;
     constexpr int KSTEPS = D / 16;
     constexpr int H = 8 * NT;  // query heads of an item
-    static_assert(L::WARP >= H * D * 4, "the merge buffer reuses the ring");
+    static_assert(L::WARP >= H * D * 4 && L::RING >= 4 * (JOIN_TILE * H + 4 * 32 * DEC_WARPS), "merge and join reuse the ring");
     extern __shared__ __align__(128) uint8_t smem[];
     float* sm_m = reinterpret_cast<float*>(smem + L::RING);  // [DEC_WARPS][H]
     float* sm_l = sm_m + DEC_WARPS * H;
@@ -696,26 +786,34 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
         const bool direct = st1 - st0 == n_blocks;
         // a partial's slot: 2*CTA + 1 where the segment begins its item, else 2*CTA
         float* part = p.part + (2 * (int64_t)blockIdx.x + (st0 == 0)) * H * (D + 2);
-        for (int i = tid; i < heads * dim; i += 32 * DEC_WARPS) {
-            const int hd = i / dim, e = i - hd * dim;
-            float acc = 0.0f, sum = 0.0f;
+        for (int i = tid; i < heads * dim >> 2; i += 32 * DEC_WARPS) {
+            const int hd = i / (dim >> 2), e = (i - hd * (dim >> 2)) << 2;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < DEC_WARPS; w++) {
-                acc += reinterpret_cast<const float*>(smem + w * L::WARP)[hd * D + e];
+                const float4 x = *reinterpret_cast<const float4*>(smem + w * L::WARP + 4 * (hd * D + e));
+                acc.x += x.x;
+                acc.y += x.y;
+                acc.z += x.z;
+                acc.w += x.w;
                 sum += sm_l[w * H + hd];
             }
             if (direct) {
                 const int64_t at_out = s * p.out_stride + (int64_t)(h * p.g + head0 + hd) * dim + e;
-                const float y = sum == 0.0f ? 0.0f : __fdividef(acc, sum);
-                if (p.out_f16) static_cast<__half*>(p.out)[at_out] = __float2half_rn(y);
-                else static_cast<float*>(p.out)[at_out] = y;
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                if (p.out_f16) {
+                    const __half2 x = __floats2half2_rn(acc.x * inv, acc.y * inv), y = __floats2half2_rn(acc.z * inv, acc.w * inv);
+                    *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + at_out) = make_uint2(h2u(x), h2u(y));
+                } else {
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at_out) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+                }
             } else {
-                __stcg(part + hd * (D + 2) + e, acc);
+                __stcg(reinterpret_cast<float4*>(part + hd * D + e), acc);
                 if (e == 0) {
                     float mx = sm_m[hd];
                     for (int w = 1; w < DEC_WARPS; w++) mx = fmaxf(mx, sm_m[w * H + hd]);
-                    __stcg(part + hd * (D + 2) + D, mx);
-                    __stcg(part + hd * (D + 2) + D + 1, sum);
+                    __stcg(reinterpret_cast<float2*>(part + H * D) + hd, make_float2(mx, sum));
                 }
             }
         }
@@ -734,44 +832,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
             __syncthreads();
             if (flags[5]) {
                 __threadfence();
-                // joint maximum and sum of each head (sm_m and sm_l of warp 0 are free), then the
-                // weighted values, whose loads are independent
-                const float* first = p.part + (2 * (int64_t)i0 + 1) * H * (D + 2);
-                const float* rest = p.part + 2 * (int64_t)i0 * H * (D + 2);
-                const int64_t pitch = 2 * H * (D + 2);
-                for (int hd = warp; hd < heads; hd += DEC_WARPS) {
-                    float mx = -INFINITY, sum = 0.0f;
-                    for (int c = lane; c <= i1 - i0; c += 32)
-                        mx = fmaxf(mx, __ldcg((c == 0 ? first : rest + c * pitch) + hd * (D + 2) + D));
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                    const float ms = mx == -INFINITY ? 0.0f : mx;
-                    for (int c = lane; c <= i1 - i0; c += 32) {
-                        const float* q = (c == 0 ? first : rest + c * pitch) + hd * (D + 2);
-                        sum = fmaf(__ldcg(q + D + 1), ex2(__ldcg(q + D) - ms), sum);
-                    }
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                    if (lane == 0) {
-                        sm_m[hd] = ms;
-                        sm_l[hd] = sum;
-                    }
-                }
-                __syncthreads();
-                for (int i = tid; i < heads * dim; i += 32 * DEC_WARPS) {
-                    const int hd = i / dim, e = i - hd * dim;
-                    const float ms = sm_m[hd], sum = sm_l[hd];
-                    float acc = 0.0f;
-#pragma unroll 8
-                    for (int c = 0; c <= i1 - i0; c++) {
-                        const float* q = (c == 0 ? first : rest + c * pitch) + hd * (D + 2);
-                        acc = fmaf(__ldcg(q + e), ex2(__ldcg(q + D) - ms), acc);
-                    }
-                    const int64_t at_out = s * p.out_stride + (int64_t)(h * p.g + head0 + hd) * dim + e;
-                    const float y = sum == 0.0f ? 0.0f : __fdividef(acc, sum);
-                    if (p.out_f16) static_cast<__half*>(p.out)[at_out] = __float2half_rn(y);
-                    else static_cast<float*>(p.out)[at_out] = y;
-                }
+                join_parts<D, H>(p, i0, i1, heads, dim, smem, sm_m, sm_l, s * p.out_stride + (int64_t)(h * p.g + head0) * dim);
             }
         }
         __syncthreads();  // the ring and the flags are free for the next segment

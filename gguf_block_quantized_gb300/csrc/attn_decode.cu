@@ -300,6 +300,8 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
         if (tid == 32 * DEC_WARPS - 1) flags[0] = before + x;
         __syncthreads();
     };
+    griddep_release();
+    griddep_wait();
     // steps of every sequence, as a running sum
     if (tid == 0) flags[0] = 0, pre[0] = 0;
     __syncthreads();
@@ -850,8 +852,7 @@ static cudaError_t run_decode_as(const DecodeParams& p, int sms, cudaStream_t s)
     const cudaError_t e = resident.get(reinterpret_cast<const void*>(kern), 32 * DEC_WARPS, smem, &per_sm);
     if (e != cudaSuccess) return e;
     const int grid = sms * std::min(per_sm, DECODE_CTAS_PER_SM);
-    kern<<<grid, 32 * DEC_WARPS, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(kern, grid, 32 * DEC_WARPS, smem, s, p);
 }
 
 template <int D, int NT, bool Q8>

@@ -178,6 +178,8 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
         return a < 0 || b > p.n_tok ? 0 : max(b - a, 0);
     };
     if (tid == 0) info[0] = 0, pre[0] = 0;
+    griddep_release();
+    griddep_wait();
     __syncthreads();
     for (int base = 0; base < p.n_seq; base += THREADS) {
         const int s = base + tid;
@@ -741,8 +743,7 @@ static cudaError_t run_prefill(const CUtensorMap& km, const CUtensorMap& vm, con
     int n;
     const cudaError_t e = resident.get(reinterpret_cast<const void*>(kern), PRE_THREADS<D, Q8>, smem, &n);
     if (e != cudaSuccess) return e;
-    kern<<<grid, PRE_THREADS<D, Q8>, smem, s>>>(km, vm, p);
-    return cudaGetLastError();
+    return launch_overlapped(kern, grid, PRE_THREADS<D, Q8>, smem, s, km, vm, p);
 }
 
 static int prefill_rows(int dim) { return dim <= 128 ? 256 : 128; }

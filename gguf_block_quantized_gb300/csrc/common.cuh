@@ -226,6 +226,11 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t
         : "memory");
 }
 
+// Programmatic dependent launch: let the next kernel of the stream be launched (its CTAs take the
+// SMs that this grid's leave, and wait); wait for the kernels before this one.
+__device__ __forceinline__ void griddep_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Signed 4-way byte dot product.  The 4- and 6-bit weight codes (0..63) are below 128,
 // so they read the same as signed bytes.
 __device__ __forceinline__ int dp4a(uint32_t a, uint32_t b, int c) {

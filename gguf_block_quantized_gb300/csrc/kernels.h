@@ -140,6 +140,24 @@ class ResidentCtas {
     }
 };
 
+// Launches a kernel that may start before the one ahead of it on the stream has finished
+// (programmatic stream serialization).  The kernel runs griddep_wait() (common.cuh) before it
+// touches global memory; only its launch and set-up overlap.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kern)(P...), int grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Adds n to the count syn_launch_count reports.
 void note_launches(int n);
 

@@ -115,6 +115,8 @@ __global__ void __launch_bounds__(APPEND_THREADS, APPEND_CTAS_PER_SM) k_kv_appen
         fence_mbar_init();
     }
     __syncthreads();
+    griddep_release();
+    griddep_wait();
 
     int n = 0, it = 0;  // pieces and items of this CTA so far
     if (warp == APPEND_WARPS) {
@@ -256,6 +258,8 @@ struct ReadParams {
 
 __global__ void __launch_bounds__(256) k_kv_read(const ReadParams p) {
     const int dim = p.c.dim, per_tok = (p.c.n_kv * dim) >> 2;  // 4-value units of one tensor
+    griddep_release();
+    griddep_wait();
     for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < p.n_units; u += (int64_t)gridDim.x * blockDim.x) {
         const int64_t tt = u / per_tok;  // token, keys and values in turn
         const int at = (int)(u - tt * per_tok) << 2;
@@ -320,8 +324,7 @@ cudaError_t launch_kv_append(const KvCache& c, const RopeDesc& r, int64_t n_tok,
     int per_sm;
     const cudaError_t e = resident[c.q8].get(reinterpret_cast<const void*>(kern), APPEND_THREADS, sizeof(AppendSmem), &per_sm);
     if (e != cudaSuccess) return e;
-    kern<<<grid, APPEND_THREADS, sizeof(AppendSmem), s>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(kern, grid, APPEND_THREADS, sizeof(AppendSmem), s, p);
 }
 
 cudaError_t launch_kv_read(const KvCache& c, int64_t n, const int64_t* slots, void* k, void* v, int* err, int sms,
@@ -334,8 +337,7 @@ cudaError_t launch_kv_read(const KvCache& c, int64_t n, const int64_t* slots, vo
     p.n_units = n * 2 * ((int64_t)c.n_kv * c.dim / 4);
     p.err = err;
     const int64_t blocks = (p.n_units + 255) / 256, most = (int64_t)sms * 8;
-    k_kv_read<<<(unsigned)(blocks < most ? blocks : most), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(k_kv_read, (int)(blocks < most ? blocks : most), 256, 0, s, p);
 }
 
 #ifdef SYN_DEBUG

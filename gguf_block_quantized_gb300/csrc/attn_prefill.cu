@@ -67,7 +67,7 @@ struct PreShape {
     static constexpr int Q = 0;
     static constexpr int RING = QT * Q_TILE;
     static constexpr int BARS = RING + NS * STAGE;
-    static constexpr int INFO = BARS + (8 * (2 * NS + 9) + 8 + 15) / 16 * 16;
+    static constexpr int INFO = BARS + (8 * (2 * NS + 11) + 8 + 15) / 16 * 16;
     static constexpr int BYTES = INFO + 64 + 4 * (PRE_MAX_SEQ + 1);
     static constexpr int O_COL = QT == 2 ? 256 : 128;  // S slots below it
     static constexpr int SLOT = QT == 2 ? 128 : 64;    // columns of an S slot
@@ -88,6 +88,28 @@ __device__ __forceinline__ uint32_t span_bits(int lo, int hi, int w) {
     const int a = min(max(lo - 32 * w, 0), 32), b = min(max(hi - 32 * w, 0), 32);
     const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1u, below_a = a == 32 ? 0xffffffffu : (1u << a) - 1u;
     return below_b & ~below_a;
+}
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // tanh from one exponential: 1 - 2/(1 + 2^(2y log2 e)), within a few 2^-24 of 1
@@ -161,7 +183,8 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
     uint64_t* kv_empty = kv_full + NS;
     uint64_t* s_full = kv_empty + NS;  // [2] S in its slot
     uint64_t* p_full = s_full + 2;     // [2] P in its slot
-    uint64_t* o_done = p_full + 2;     // [2] a P V product is complete
+    uint64_t* p_half = p_full + 2;     // [2] its first half
+    uint64_t* o_done = p_half + 2;     // [2] a P V product is complete
     uint64_t* q_full = o_done + 2;     // [2]
     uint64_t* mma_idle = q_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 1);
@@ -265,6 +288,7 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_u32(&s_full[i]), 1);
             mbar_init(smem_u32(&p_full[i]), 4);
+            mbar_init(smem_u32(&p_half[i]), 4);
             mbar_init(smem_u32(&o_done[i]), 1);
             mbar_init(smem_u32(&q_full[i]), 4);
         }
@@ -350,41 +374,54 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
                 if (!mbar_wait(smem_u32(&s_full[slot]), phase, p.err, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t s_base = lane_base + slot * L::SLOT;
-                uint32_t v[BN];
-#pragma unroll
-                for (int c = 0; c < BN; c += 32) TMEM_LD32(s_base + c, (v + c));
-                tmem_ld_wait();
                 const int j0 = tiles.at(t0 + i) * BN;
-                if (MOD) {
-#pragma unroll
-                    for (int c = 0; c < BN; c++) {
-                        float x = __uint_as_float(v[c]);
-                        x = p.cap > 0.0f ? cap_log2 * tanh_ex2(x * to_cap) : x * c_log2;
-                        if (p.slopes) x = fmaf(-slope, fabsf((float)(pos - j0 - c)), x);
-                        v[c] = __float_as_uint(x);
-                    }
-                }
                 const bool full = !row_ok || (j0 >= vis.low && j0 + BN <= vis.end) || (j0 >= vis.first && j0 + BN <= vis.pre);
-                if (!__all_sync(0xffffffffu, full)) {
+                const bool masked = !__all_sync(0xffffffffu, full);  // (the same for the warp)
+                constexpr int N = BN / 32;
+                // Two passes over the row's scores in tensor memory, 32 at a time, the next ones on
+                // their way: the maximum, then the powers.  (All of them at once in registers spill.)
+                uint32_t va[32], vb[32];
+                float mx = -INFINITY;
+                TMEM_LD32(s_base, va);
+                TMEM_LD_WAIT32(va);
 #pragma unroll
-                    for (int w = 0; w < BN / 32; w++) {
+                for (int w = 0; w < N; w++) {
+                    uint32_t(&v)[32] = (w & 1) ? vb : va;
+                    uint32_t(&next)[32] = (w & 1) ? va : vb;
+                    if (!MOD) TMEM_LD32(s_base + (w + 1 < N ? 32 * (w + 1) : 0), next);  // (last: the second pass's first)
+                    if (MOD) {
+#pragma unroll
+                        for (int c = 0; c < 32; c++) {
+                            float x = __uint_as_float(v[c]);
+                            x = p.cap > 0.0f ? cap_log2 * tanh_ex2(x * to_cap) : x * c_log2;
+                            if (p.slopes) x = fmaf(-slope, fabsf((float)(pos - j0 - 32 * w - c)), x);
+                            v[c] = __float_as_uint(x);
+                        }
+                    }
+                    if (masked) {
                         const uint32_t bits = row_ok ? span_bits(vis.low - j0, vis.end - j0, w) | span_bits(vis.first - j0, vis.pre - j0, w)
                                                      : 0xffffffffu;
 #pragma unroll
                         for (int c = 0; c < 32; c++)
-                            if (!((bits >> c) & 1)) v[32 * w + c] = 0xff800000u;  // -inf
+                            if (!((bits >> c) & 1)) v[c] = 0xff800000u;  // -inf
                     }
+                    float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8)
+#pragma unroll
+                        for (int u = 0; u < 4; u++)
+                            m4[u] = fmaxf(fmaxf(m4[u], __uint_as_float(v[c + 2 * u])), __uint_as_float(v[c + 2 * u + 1]));
+                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    if (MOD) {  // (the finished scores go back: the second pass does not compute them again)
+                        TMEM_ST32(s_base + 32 * w, v);
+                        if (w + 1 == N) tmem_st_wait();
+                        TMEM_LD32(s_base + (w + 1 < N ? 32 * (w + 1) : 0), next);
+                    }
+                    TMEM_LD_WAIT32(next);
                 }
-                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < BN; c += 8)
-#pragma unroll
-                    for (int u = 0; u < 4; u++)
-                        mx4[u] = fmaxf(mx4[u], fmaxf(__uint_as_float(v[c + 2 * u]), __uint_as_float(v[c + 2 * u + 1])));
-                float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                 if (!MOD) mx *= c_log2;
                 // the reference of the powers follows the maximum when that has grown by 2^8
-                const bool grow = mx > m + PRE_GROW_LOG2 || (m == -INFINITY && mx > -INFINITY);
+                const bool grow = mx > m + PRE_GROW_LOG2;  // (or is the first that is not -inf)
                 const float f = grow ? ex2(m - mx) : 1.0f;
                 if (grow) {
                     m = mx;
@@ -404,22 +441,41 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
                     }
                 }
                 const float ms = (m == -INFINITY ? 0.0f : m) - PRE_P_LOG2;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const uint64_t c2 = pack2(MOD ? 1.0f : c_log2, MOD ? 1.0f : c_log2), ms2 = pack2(-ms, -ms);
+                uint64_t sum2[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < BN; c += 32) {
-                    uint32_t w[16];
+                for (int w = 0; w < N; w++) {
+                    // (the first pass read N + 1 times, an odd number: its last load is in the other buffer)
+                    uint32_t(&v)[32] = ((w + N) & 1) ? vb : va;
+                    uint32_t(&next)[32] = ((w + N) & 1) ? va : vb;
+                    if (w + 1 < N) TMEM_LD32(s_base + 32 * (w + 1), next);
+                    if (masked && !MOD) {
+                        const uint32_t bits = row_ok ? span_bits(vis.low - j0, vis.end - j0, w) | span_bits(vis.first - j0, vis.pre - j0, w)
+                                                     : 0xffffffffu;
+#pragma unroll
+                        for (int c = 0; c < 32; c++)
+                            if (!((bits >> c) & 1)) v[c] = 0xff800000u;
+                    }
+                    uint32_t pw[16];
 #pragma unroll
                     for (int u = 0; u < 16; u++) {
-                        const float x = __uint_as_float(v[c + 2 * u]), y = __uint_as_float(v[c + 2 * u + 1]);
-                        const float a = ex2(MOD ? x - ms : fmaf(x, c_log2, -ms)), e = ex2(MOD ? y - ms : fmaf(y, c_log2, -ms));
-                        sum[(2 * u) & 3] += a;
-                        sum[(2 * u + 1) & 3] += e;
+                        const float2 x = unpack2(fma2(pack2(__uint_as_float(v[2 * u]), __uint_as_float(v[2 * u + 1])), c2, ms2));
+                        const float a = ex2(x.x), e = ex2(x.y);
+                        sum2[u & 1] = add2(sum2[u & 1], pack2(a, e));
                         const __half2 hh = __floats2half2_rn(a, e);
-                        w[u] = *reinterpret_cast<const uint32_t*>(&hh);
+                        pw[u] = *reinterpret_cast<const uint32_t*>(&hh);
                     }
-                    TMEM_ST16(s_base + (c >> 1), w);
+                    if (w + 1 < N) TMEM_LD_WAIT32(next);  // (before P overwrites scores)
+                    TMEM_ST16(s_base + 16 * w, pw);
+                    if (w == N / 2 - 1) {  // the product with the first half of the tile's keys can begin
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&p_half[slot]));
+                    }
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const float2 sa = unpack2(add2(sum2[0], sum2[1]));
+                l += sa.x + sa.y;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -519,16 +575,24 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
             }
             __syncwarp();
         };
-        auto issue_o = [&](int qt, int slot, int i, bool first) {  // O += P V from piece i
-            if (lane == 0) {
-                const uint32_t va = smem_u32(smem + L::RING + (i % NS) * L::STAGE);
+        auto issue_o = [&](int qt, int slot, int i, uint32_t phase, bool first) {  // O += P V from piece i
+            const uint32_t va = smem_u32(smem + L::RING + (i % NS) * L::STAGE);
 #pragma unroll
-                for (int ks = 0; ks < BN / 16; ks++)
-                    mma_f16_ts(tmem + L::O_COL + qt * D, tmem + slot * L::SLOT + 8 * ks,
-                               sdesc_sw128_mn(va + ks * 2048, BN * 128), p.idesc_o, !first || ks > 0);
-                mma_commit(smem_u32(&o_done[qt]));
+            for (int half = 0; half < 2; half++) {
+                if (!mbar_wait(smem_u32(half ? &p_full[slot] : &p_half[slot]), phase, p.err, abort_flag)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < BN / 32; k++) {
+                        const int ks = half * (BN / 32) + k;
+                        mma_f16_ts(tmem + L::O_COL + qt * D, tmem + slot * L::SLOT + 8 * ks,
+                                   sdesc_sw128_mn(va + ks * 2048, BN * 128), p.idesc_o, !first || ks > 0);
+                    }
+                    if (half) mma_commit(smem_u32(&o_done[qt]));
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            return true;
         };
         auto release = [&](int i) {
             if (lane == 0) mma_commit(smem_u32(&kv_empty[i % NS]));
@@ -560,9 +624,7 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
                     clean(pv, i);
                     if (i + 1 < nt && !(ok = take(pk))) break;
                     for (int qt = 0; qt < q_act && ok; qt++) {
-                        if (!(ok = mbar_wait(smem_u32(&p_full[qt]), i & 1, p.err, abort_flag))) break;
-                        tc_fence_after();
-                        issue_o(qt, qt, pv, i == 0);
+                        if (!(ok = issue_o(qt, qt, pv, i & 1, i == 0))) break;
                         if (i + 1 < nt) issue_s(qt, qt, pk);
                     }
                     if (!ok) break;
@@ -579,9 +641,7 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
                     }
                     if (!(ok = take(rc))) break;
                     clean(rc, i);
-                    if (!(ok = mbar_wait(smem_u32(&p_full[i & 1]), (i >> 1) & 1, p.err, abort_flag))) break;
-                    tc_fence_after();
-                    issue_o(0, i & 1, rc, i == 0);
+                    if (!(ok = issue_o(0, i & 1, rc, (i >> 1) & 1, i == 0))) break;
                     release(rc);
                     rc++;
                 }

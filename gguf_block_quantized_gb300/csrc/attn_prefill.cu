@@ -12,8 +12,10 @@
 //            a row's maximum has grown by more than 2^8 (p stays below 2^14 in fp16: rarely);
 //   MMA      one warp: S = Q K^T (Q and K from shared memory), O += P V (P from tensor memory, V as
 //            an MN-major operand: cached rows are used as they lie);
-//   loader   F16: one warp, tensor-map copies of page pieces into a ring of tiles (128-byte
-//            swizzle); Q8_0: four warps expand codes to fp16 into the same layout.
+//   loader   one warp: F16: tensor-map copies of page pieces into a ring of tiles (128-byte
+//            swizzle); Q8_0: bulk copies of codes and scales into a ring of raw tiles, which
+//   expand   (Q8_0) four warps turn into fp16 tiles of the same layout.
+// Registers go where they are used (setmaxnreg): a softmax thread holds its row's 128 scores.
 // All hand-offs are mbarriers with bounded waits.
 //
 // Rows that a mask empties give zeros.  A masked score is replaced before the maximum; V rows past
@@ -56,25 +58,38 @@ struct PrefillParams {
     uint32_t idesc_s, idesc_o;
 };
 
-template <int D>
+template <int D, bool Q8>
 struct PreShape {
     static constexpr int QT = D <= 128 ? 2 : 1;     // 128-row tiles of an item
     static constexpr int BN = D <= 128 ? 128 : 64;  // keys of a tile
-    static constexpr int NS = D <= 64 ? 6 : 4;      // tiles (K or V) in the ring
+    static constexpr int NS = D <= 64 ? 6 : Q8 ? 3 : 4;  // tiles (K or V) in the ring
+    static constexpr int NR = Q8 ? 2 : 0;           // raw tiles (codes, then scales) ahead of it
     static constexpr int R = 128 * QT;
     static constexpr int STAGE = BN * D * 2;
+    static constexpr int RAW = BN * D + BN * D / 16;
     static constexpr int Q_TILE = 128 * D * 2;
     static constexpr int Q = 0;
     static constexpr int RING = QT * Q_TILE;
-    static constexpr int BARS = RING + NS * STAGE;
-    static constexpr int INFO = BARS + (8 * (2 * NS + 11) + 8 + 15) / 16 * 16;
+    static constexpr int RAWS = RING + NS * STAGE;
+    static constexpr int BARS = RAWS + NR * RAW;
+    static constexpr int INFO = BARS + (8 * (2 * NS + 2 * NR + 11) + 8 + 15) / 16 * 16;
     static constexpr int BYTES = INFO + 64 + 4 * (PRE_MAX_SEQ + 1);
     static constexpr int O_COL = QT == 2 ? 256 : 128;  // S slots below it
     static constexpr int SLOT = QT == 2 ? 128 : 64;    // columns of an S slot
+    // warps: softmax, then MMA, loader and two that idle, then (Q8_0) four that expand
+    static constexpr int MMA_WARP = 4 * QT, LOAD_WARP = MMA_WARP + 1, EXPAND_WARP = MMA_WARP + 4;
+    static constexpr int WARPS = MMA_WARP + 4 + (Q8 ? 4 : 0), THREADS = 32 * WARPS;
+    // registers a thread of each kind after the hand-over (two row tiles; their sum over the warps is
+    // what the launch gives them: 168 each of 12 warps, 128 each of 16)
+    static constexpr int SOFTMAX_REGS = Q8 ? 192 : 208, MMA_REGS = Q8 ? 40 : 88, EXPAND_REGS = 88;
+    static_assert(QT == 1 || (Q8 ? 8 * SOFTMAX_REGS + 4 * MMA_REGS + 4 * EXPAND_REGS <= 16 * 128
+                                 : 8 * SOFTMAX_REGS + 4 * MMA_REGS <= 12 * 168), "more registers than the launch has");
 };
 
-template <int D, bool Q8>
-constexpr int PRE_THREADS = 32 * (4 * PreShape<D>::QT + 1 + (Q8 ? 4 : 1));
+template <int N>
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // the tiles that hold a key some row of the item sees: [a0, a1) of the prefix, [b0, b1)
 struct Tiles {
@@ -112,11 +127,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// tanh from one exponential: 1 - 2/(1 + 2^(2y log2 e)), within a few 2^-24 of 1
-__device__ __forceinline__ float tanh_ex2(float y) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2(2.8853900817779268f * y)));
-    return fmaf(-2.0f, r, 1.0f);
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // One row computed key by key by a warp (lane l takes the values l, l + 32, ...): its maximum, sum
@@ -131,8 +145,8 @@ __device__ __noinline__ void row_by_hand(const PrefillParams& p, const int32_t* 
 #pragma unroll
     for (int i = 0; i < D / 32; i++) o[i] = 0.0f;
     for (int t = t0; t < t1; t++) {
-        const int j0 = tiles.at(t) * PreShape<D>::BN;
-        for (int j = j0; j < min(j0 + PreShape<D>::BN, len); j++) {
+        const int j0 = tiles.at(t) * PreShape<D, Q8>::BN;
+        for (int j = j0; j < min(j0 + PreShape<D, Q8>::BN, len); j++) {
             if (!vis(j)) continue;
             const int id = table[j >> p.c.page_shift];
             if (id < 0 || id >= p.c.n_pages) continue;
@@ -170,12 +184,11 @@ __device__ __forceinline__ void store_out(const PrefillParams& p, int64_t at, fl
 }
 
 template <int D, bool Q8, bool MOD>
-__global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
+__global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
     k_attn_prefill(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PrefillParams p) {
-    using L = PreShape<D>;
-    constexpr int QT = L::QT, BN = L::BN, NS = L::NS, R = L::R;
-    constexpr int THREADS = PRE_THREADS<D, Q8>;
-    constexpr int MMA_WARP = 4 * QT, LOAD_WARP = MMA_WARP + 1;
+    using L = PreShape<D, Q8>;
+    constexpr int QT = L::QT, BN = L::BN, NS = L::NS, NR = L::NR, R = L::R, THREADS = L::THREADS;
+    constexpr int MMA_WARP = L::MMA_WARP, LOAD_WARP = L::LOAD_WARP, EXPAND_WARP = L::EXPAND_WARP;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BARS);
@@ -186,13 +199,17 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
     uint64_t* p_half = p_full + 2;     // [2] its first half
     uint64_t* o_done = p_half + 2;     // [2] a P V product is complete
     uint64_t* q_full = o_done + 2;     // [2]
-    uint64_t* mma_idle = q_full + 2;
+    uint64_t* raw_full = q_full + 2;       // [NR] Q8_0: codes and scales have arrived
+    uint64_t* raw_empty = raw_full + NR;   // [NR]
+    uint64_t* mma_idle = raw_empty + NR;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile uint32_t* raw_there = reinterpret_cast<volatile uint32_t*>(smem + L::INFO + 48);  // [NR] boxes that arrived
     int* info = reinterpret_cast<int*>(smem + L::INFO);  // [0] carry, [1] min first, [2] min low, [3] max end, [4..] sums
     int* pre = info + 16;                                // [n_seq + 1] items (of one kv head) before each sequence
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the shuffle tells the compiler that the warp's index is the same for its lanes)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int dim = p.c.dim, nh = (dim + 63) >> 6;  // 64-value column chunks of a row
 
     // ---- this CTA's item -------------------------------------------------------------------
@@ -292,6 +309,10 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
             mbar_init(smem_u32(&o_done[i]), 1);
             mbar_init(smem_u32(&q_full[i]), 4);
         }
+        for (int i = 0; i < NR; i++) {
+            mbar_init(smem_u32(&raw_full[i]), 1);
+            mbar_init(smem_u32(&raw_empty[i]), 4);
+        }
         mbar_init(smem_u32(mma_idle), 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -334,6 +355,8 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
     const uint32_t tmem = *tmem_slot;
     float* part = p.part + (int64_t)blockIdx.x * R * (D + 2);  // [D][R] values, [R] maxima, [R] sums
 
+    auto softmax_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(R) : "memory"); };  // the softmax warps alone
+
     // The ring's order: K of the first tile, then (two row tiles) V and the next K, or (one) the
     // next K and V.  Piece i of 2*nt: is it V, and of which tile.
     auto piece_v = [&](int i) { return QT == 2 ? (i & 1) : i == 2 * nt - 1 || (i > 0 && (i & 1) == 0); };
@@ -341,6 +364,7 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
 
     if (warp < MMA_WARP) {
         // ------------------------------------ softmax ------------------------------------------
+        if (QT == 2) take_registers<L::SOFTMAX_REGS>();
         const int qt = warp >> 2;
         const int r = tid;  // row of the item
         if (qt < q_act) {
@@ -365,60 +389,64 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
             const uint32_t o_base = lane_base + L::O_COL + qt * D;
             const float c_log2 = p.scale * 1.4426950408889634f;
             const float slope = MOD && p.slopes && row_ok ? p.slopes[my_head] * 1.4426950408889634f : 0.0f;
-            const float cap_log2 = p.cap * 1.4426950408889634f, to_cap = p.cap > 0.0f ? p.scale / p.cap : 0.0f;
+            const float cap_log2 = p.cap * 1.4426950408889634f;
+            const float to_cap2 = p.cap > 0.0f ? 2.0f * c_log2 / p.cap : 0.0f;
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
             for (int i = 0; i < nt; i++) {
                 const int slot = QT == 2 ? qt : i & 1;
                 const uint32_t phase = QT == 2 ? i & 1 : (i >> 1) & 1;
-                if (!mbar_wait(smem_u32(&s_full[slot]), phase, p.err, abort_flag)) { ok = false; break; }
+                if (!mbar_wait_poll(smem_u32(&s_full[slot]), phase, p.err, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t s_base = lane_base + slot * L::SLOT;
                 const int j0 = tiles.at(t0 + i) * BN;
                 const bool full = !row_ok || (j0 >= vis.low && j0 + BN <= vis.end) || (j0 >= vis.first && j0 + BN <= vis.pre);
                 const bool masked = !__all_sync(0xffffffffu, full);  // (the same for the warp)
-                constexpr int N = BN / 32;
-                // Two passes over the row's scores in tensor memory, 32 at a time, the next ones on
-                // their way: the maximum, then the powers.  (All of them at once in registers spill.)
-                uint32_t va[32], vb[32];
-                float mx = -INFINITY;
-                TMEM_LD32(s_base, va);
-                TMEM_LD_WAIT32(va);
+                uint32_t v[BN];  // the row's scores
 #pragma unroll
-                for (int w = 0; w < N; w++) {
-                    uint32_t(&v)[32] = (w & 1) ? vb : va;
-                    uint32_t(&next)[32] = (w & 1) ? va : vb;
-                    if (!MOD) TMEM_LD32(s_base + (w + 1 < N ? 32 * (w + 1) : 0), next);  // (last: the second pass's first)
-                    if (MOD) {
+                for (int c = 0; c < BN; c += 32) TMEM_LD32(s_base + c, (v + c));
 #pragma unroll
-                        for (int c = 0; c < 32; c++) {
-                            float x = __uint_as_float(v[c]);
-                            x = p.cap > 0.0f ? cap_log2 * tanh_ex2(x * to_cap) : x * c_log2;
-                            if (p.slopes) x = fmaf(-slope, fabsf((float)(pos - j0 - 32 * w - c)), x);
-                            v[c] = __float_as_uint(x);
+                for (int c = 0; c < BN; c += 32) TMEM_LD_WAIT32((v + c));
+                if (MOD) {
+                    if (p.cap > 0.0f) {
+                        // cap*tanh(x/cap) = cap - 2 cap/(1 + 2^(2 x log2(e)/cap)), all in powers of two
+                        const uint64_t k2 = pack2(to_cap2, to_cap2), one2 = pack2(1.0f, 1.0f), zero2 = 0;
+                        const uint64_t m2 = pack2(-2.0f * cap_log2, -2.0f * cap_log2), cap2 = pack2(cap_log2, cap_log2);
+#pragma unroll
+                        for (int c = 0; c < BN; c += 2) {
+                            const float2 y = unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2, zero2));
+                            const float2 z = unpack2(add2(pack2(ex2(y.x), ex2(y.y)), one2));
+                            const float2 x = unpack2(fma2(pack2(rcp(z.x), rcp(z.y)), m2, cap2));
+                            v[c] = __float_as_uint(x.x);
+                            v[c + 1] = __float_as_uint(x.y);
                         }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < BN; c++) v[c] = __float_as_uint(__uint_as_float(v[c]) * c_log2);
                     }
-                    if (masked) {
+                    if (p.slopes) {
+                        const float far = (float)(pos - j0);
+#pragma unroll
+                        for (int c = 0; c < BN; c++) v[c] = __float_as_uint(fmaf(-slope, fabsf(far - (float)c), __uint_as_float(v[c])));
+                    }
+                }
+                if (masked) {
+#pragma unroll
+                    for (int w = 0; w < BN / 32; w++) {
                         const uint32_t bits = row_ok ? span_bits(vis.low - j0, vis.end - j0, w) | span_bits(vis.first - j0, vis.pre - j0, w)
                                                      : 0xffffffffu;
 #pragma unroll
                         for (int c = 0; c < 32; c++)
-                            if (!((bits >> c) & 1)) v[c] = 0xff800000u;  // -inf
+                            if (!((bits >> c) & 1)) v[32 * w + c] = 0xff800000u;  // -inf
                     }
-                    float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < 32; c += 8)
-#pragma unroll
-                        for (int u = 0; u < 4; u++)
-                            m4[u] = fmaxf(fmaxf(m4[u], __uint_as_float(v[c + 2 * u])), __uint_as_float(v[c + 2 * u + 1]));
-                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    if (MOD) {  // (the finished scores go back: the second pass does not compute them again)
-                        TMEM_ST32(s_base + 32 * w, v);
-                        if (w + 1 == N) tmem_st_wait();
-                        TMEM_LD32(s_base + (w + 1 < N ? 32 * (w + 1) : 0), next);
-                    }
-                    TMEM_LD_WAIT32(next);
                 }
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < BN; c += 8)
+#pragma unroll
+                    for (int u = 0; u < 4; u++)
+                        m4[u] = fmaxf(fmaxf(m4[u], __uint_as_float(v[c + 2 * u])), __uint_as_float(v[c + 2 * u + 1]));
+                float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 if (!MOD) mx *= c_log2;
                 // the reference of the powers follows the maximum when that has grown by 2^8
                 const bool grow = mx > m + PRE_GROW_LOG2;  // (or is the first that is not -inf)
@@ -429,7 +457,7 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
                 }
                 if (i > 0 && __any_sync(0xffffffffu, grow)) {
                     // O holds the tiles before: wait for the last product into it, then scale
-                    if (!mbar_wait(smem_u32(&o_done[qt]), (i - 1) & 1, p.err, abort_flag)) { ok = false; break; }
+                    if (!mbar_wait_poll(smem_u32(&o_done[qt]), (i - 1) & 1, p.err, abort_flag)) { ok = false; break; }
                     tc_fence_after();
                     for (int c = 0; c < dim; c += 16) {
                         uint32_t o[16];
@@ -444,30 +472,19 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
                 const uint64_t c2 = pack2(MOD ? 1.0f : c_log2, MOD ? 1.0f : c_log2), ms2 = pack2(-ms, -ms);
                 uint64_t sum2[2] = {0, 0};
 #pragma unroll
-                for (int w = 0; w < N; w++) {
-                    // (the first pass read N + 1 times, an odd number: its last load is in the other buffer)
-                    uint32_t(&v)[32] = ((w + N) & 1) ? vb : va;
-                    uint32_t(&next)[32] = ((w + N) & 1) ? va : vb;
-                    if (w + 1 < N) TMEM_LD32(s_base + 32 * (w + 1), next);
-                    if (masked && !MOD) {
-                        const uint32_t bits = row_ok ? span_bits(vis.low - j0, vis.end - j0, w) | span_bits(vis.first - j0, vis.pre - j0, w)
-                                                     : 0xffffffffu;
-#pragma unroll
-                        for (int c = 0; c < 32; c++)
-                            if (!((bits >> c) & 1)) v[c] = 0xff800000u;
-                    }
+                for (int w = 0; w < BN / 32; w++) {
                     uint32_t pw[16];
 #pragma unroll
                     for (int u = 0; u < 16; u++) {
-                        const float2 x = unpack2(fma2(pack2(__uint_as_float(v[2 * u]), __uint_as_float(v[2 * u + 1])), c2, ms2));
+                        const int c = 32 * w + 2 * u;
+                        const float2 x = unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), c2, ms2));
                         const float a = ex2(x.x), e = ex2(x.y);
                         sum2[u & 1] = add2(sum2[u & 1], pack2(a, e));
                         const __half2 hh = __floats2half2_rn(a, e);
                         pw[u] = *reinterpret_cast<const uint32_t*>(&hh);
                     }
-                    if (w + 1 < N) TMEM_LD_WAIT32(next);  // (before P overwrites scores)
                     TMEM_ST16(s_base + 16 * w, pw);
-                    if (w == N / 2 - 1) {  // the product with the first half of the tile's keys can begin
+                    if (w == BN / 64 - 1) {  // the product with the first half of the tile's keys can begin
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
@@ -483,8 +500,8 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
             }
             // (one row tile: S of a tile is issued before the product of the one before, so the last
             // two products may both be outstanding, and a parity tells only neighbours apart)
-            if (QT == 1 && nt > 1) ok = ok && mbar_wait(smem_u32(&o_done[qt]), (nt - 2) & 1, p.err, abort_flag);
-            if (ok && mbar_wait(smem_u32(&o_done[qt]), (nt - 1) & 1, p.err, abort_flag)) {
+            if (QT == 1 && nt > 1) ok = ok && mbar_wait_poll(smem_u32(&o_done[qt]), (nt - 2) & 1, p.err, abort_flag);
+            if (ok && mbar_wait_poll(smem_u32(&o_done[qt]), (nt - 1) & 1, p.err, abort_flag)) {
                 tc_fence_after();
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 float odd = l - l;  // NaN where something is not finite
@@ -558,46 +575,44 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
                 }
             }
         }
-    } else if (warp == MMA_WARP) {
+    } else if (warp < EXPAND_WARP) {
+      if (QT == 2) give_registers<L::MMA_REGS>();
+      if (warp == MMA_WARP) {
         // ------------------------------------ MMA ----------------------------------------------
         int rc = 0;  // ring pieces taken
         bool ok = true;
         auto take = [&](int i) {  // wait for piece i of the ring
-            return mbar_wait(smem_u32(&kv_full[i % NS]), (i / NS) & 1, p.err, abort_flag);
+            return mbar_wait_poll(smem_u32(&kv_full[i % NS]), (i / NS) & 1, p.err, abort_flag);
         };
+        const uint32_t lead = elect_lane();
+        const uint32_t ring_s = smem_u32(smem + L::RING), q_s = smem_u32(smem + L::Q);
+        const uint64_t k_major = sdesc_sw128(0), n_major = sdesc_sw128_mn(0, BN * 128);
         auto issue_s = [&](int qt, int slot, int i) {  // S = Q K^T from piece i
-            if (lane == 0) {
-                const uint32_t qa = smem_u32(smem + L::Q + qt * L::Q_TILE), ka = smem_u32(smem + L::RING + (i % NS) * L::STAGE);
-                for (int ks = 0; ks < dim / 16; ks++)
-                    mma_f16(tmem + slot * L::SLOT, sdesc_sw128(qa + (ks >> 2) * (128 * 128) + (ks & 3) * 32),
-                            sdesc_sw128(ka + (ks >> 2) * (BN * 128) + (ks & 3) * 32), p.idesc_s, ks > 0);
-                mma_commit(smem_u32(&s_full[slot]));
-            }
-            __syncwarp();
+            const uint64_t qd = k_major + ((q_s + qt * L::Q_TILE) >> 4), kd = k_major + ((ring_s + (i % NS) * L::STAGE) >> 4);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ks++)
+                if (ks * 16 < dim)
+                    mma_f16_lead(lead, tmem + slot * L::SLOT, qd + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
+                                 kd + (((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4), p.idesc_s, ks > 0);
+            mma_commit_lead(lead, smem_u32(&s_full[slot]));
         };
         auto issue_o = [&](int qt, int slot, int i, uint32_t phase, bool first) {  // O += P V from piece i
-            const uint32_t va = smem_u32(smem + L::RING + (i % NS) * L::STAGE);
+            const uint64_t vd = n_major + ((ring_s + (i % NS) * L::STAGE) >> 4);
 #pragma unroll
             for (int half = 0; half < 2; half++) {
-                if (!mbar_wait(smem_u32(half ? &p_full[slot] : &p_half[slot]), phase, p.err, abort_flag)) return false;
+                if (!mbar_wait_poll(smem_u32(half ? &p_full[slot] : &p_half[slot]), phase, p.err, abort_flag)) return false;
                 tc_fence_after();
-                if (lane == 0) {
 #pragma unroll
-                    for (int k = 0; k < BN / 32; k++) {
-                        const int ks = half * (BN / 32) + k;
-                        mma_f16_ts(tmem + L::O_COL + qt * D, tmem + slot * L::SLOT + 8 * ks,
-                                   sdesc_sw128_mn(va + ks * 2048, BN * 128), p.idesc_o, !first || ks > 0);
-                    }
-                    if (half) mma_commit(smem_u32(&o_done[qt]));
+                for (int k = 0; k < BN / 32; k++) {
+                    const int ks = half * (BN / 32) + k;
+                    mma_f16_ts_lead(lead, tmem + L::O_COL + qt * D, tmem + slot * L::SLOT + 8 * ks, vd + (ks * 2048 >> 4), p.idesc_o,
+                                    !first || ks > 0);
                 }
-                __syncwarp();
             }
+            mma_commit_lead(lead, smem_u32(&o_done[qt]));
             return true;
         };
-        auto release = [&](int i) {
-            if (lane == 0) mma_commit(smem_u32(&kv_empty[i % NS]));
-            __syncwarp();
-        };
+        auto release = [&](int i) { mma_commit_lead(lead, smem_u32(&kv_empty[i % NS])); };
         // V rows past the sequence's end hold whatever the page holds: zeros
         auto clean = [&](int i, int tile) {
             const int j0 = tiles.at(t0 + tile) * BN;
@@ -611,7 +626,7 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
             fence_proxy_async_smem();
             __syncwarp();
         };
-        for (int qt = 0; qt < q_act && ok; qt++) ok = mbar_wait(smem_u32(&q_full[qt]), 0, p.err, abort_flag);
+        for (int qt = 0; qt < q_act && ok; qt++) ok = mbar_wait_poll(smem_u32(&q_full[qt]), 0, p.err, abort_flag);
         if (ok && (ok = take(0))) {
             tc_fence_after();
             for (int qt = 0; qt < q_act; qt++) issue_s(qt, QT == 2 ? qt : 0, 0);
@@ -649,10 +664,9 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
         }
         // every product issued is complete before the accumulators are freed (the softmax warps
         // have seen the last one finish, except after an abort)
-        if (lane == 0) mma_commit(smem_u32(mma_idle));
-        __syncwarp();
+        mma_commit_lead(lead, smem_u32(mma_idle));
         mbar_drain(smem_u32(mma_idle), 0, p.err);
-    } else {
+      } else if (warp == LOAD_WARP) {
         // ------------------------------------ loader -------------------------------------------
         int i = 0;
 #ifdef SYN_TEST_STALL
@@ -660,97 +674,108 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
 #else
         const int n_pieces = 2 * nt;
 #endif
-        const uint32_t bytes = (uint32_t)nh * BN * 128;
-        if (!Q8) {
-            const int box = min(BN, 1 << p.c.page_shift), n_box = BN / box;
-            for (; i < n_pieces; i++) {
-                const int st = i % NS;
-                const bool is_v = piece_v(i);
-                const int j = tiles.at(t0 + piece_tile(i)) * BN + lane * box;
-                // pages past the end, and ids outside the pool, become the page after the last,
-                // which the copy fills with zeros
-                int id = (int)p.c.n_pages;
-                if (lane < n_box && j < len) {
-                    const int x = table[j >> p.c.page_shift];
-                    if ((unsigned)x < (unsigned long long)p.c.n_pages) id = x;
-                    else record_error(p.err, SYN_DEVERR_BOUNDS);
-                }
-                if (!mbar_wait(smem_u32(&kv_empty[st]), ((i / NS) & 1) ^ 1, p.err, abort_flag)) break;
+        const int box = min(BN, 1 << p.c.page_shift), n_box = BN / box;  // rows of a copy; lane l does the l-th
+        for (; i < n_pieces; i++) {
+            const int st = Q8 ? i % max(NR, 1) : i % NS;
+            const uint32_t turn = (uint32_t)(Q8 ? i / max(NR, 1) : i / NS);
+            const bool is_v = piece_v(i);
+            const int j = tiles.at(t0 + piece_tile(i)) * BN + lane * box;
+            int id = -1;  // past the end, or an id outside the pool
+            if (lane < n_box && j < len) {
+                const int x = table[j >> p.c.page_shift];
+                if ((unsigned)x < (unsigned)p.c.n_pages) id = x;
+                else record_error(p.err, SYN_DEVERR_BOUNDS);
+            }
+            if (!mbar_wait_poll(smem_u32(Q8 ? &raw_empty[st] : &kv_empty[st]), (turn & 1) ^ 1, p.err, abort_flag)) break;
+            const int cell = j & ((1 << p.c.page_shift) - 1);
+            if (!Q8) {
+                // a page that is not there becomes the page after the last: the copy fills it with zeros
                 const uint32_t full = smem_u32(&kv_full[st]);
-                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)nh * BN * 128);
                 __syncwarp();
-                if (lane < n_box && SYN_IN_BOUNDS((lane + 1) * box * 128 + (nh - 1) * BN * 128 <= L::STAGE && id >= 0)) {
+                if (lane < n_box && SYN_IN_BOUNDS((lane + 1) * box * 128 + (nh - 1) * BN * 128 <= L::STAGE)) {
                     const uint32_t dst = smem_u32(smem + L::RING + st * L::STAGE) + lane * box * 128;
                     for (int c = 0; c < nh; c++)
-                        tma_load_4d(dst + c * (BN * 128), is_v ? &vmap : &kmap, 64 * c, j & ((1 << p.c.page_shift) - 1), h, id, full);
+                        tma_load_4d(dst + c * (BN * 128), is_v ? &vmap : &kmap, 64 * c, cell, h, id < 0 ? (int)p.c.n_pages : id, full);
+                }
+            } else {
+                // (rows of pages that are not there, or past the end, are zeroed by the expanding warps)
+                const uint32_t full = smem_u32(&raw_full[st]), there = __ballot_sync(0xffffffffu, id >= 0);
+                const uint32_t codes = (uint32_t)(box * dim), scales = codes / 16;
+                if (lane == 0) {
+                    raw_there[st] = there;  // (before the arrival that lets raw_full complete)
+                    mbar_arrive_expect_tx(full, (uint32_t)__popc(there) * (codes + scales));
                 }
                 __syncwarp();
-            }
-            // the tiles still in flight (issued, not consumed: only after an abort) land first
-            for (int u = max(0, i - NS); u < i; u++) mbar_drain(smem_u32(&kv_full[u % NS]), (u / NS) & 1, p.err);
-        } else {
-            // 128 threads: 16 codes of a row at a time, the next piece's loads before this one's work
-            constexpr int MOST = BN * (D / 16) / 128;
-            const int lt = tid - 32 * LOAD_WARP;
-            const int per_row = dim >> 4, n = BN * per_row;
-            const int64_t plane = (int64_t)dim << p.c.page_shift;
-            uint4 code[MOST];
-            uint16_t scale[MOST];
-            auto load = [&](int piece) {
-                const uint8_t* pool = (piece_v(piece) ? p.c.v : p.c.k) + (int64_t)h * p.c.tile;
-                const int j0 = tiles.at(t0 + piece_tile(piece)) * BN;
-#pragma unroll
-                for (int u = 0; u < MOST; u++) {
-                    const int idx = u * 128 + lt;
-                    code[u] = make_uint4(0, 0, 0, 0);
-                    scale[u] = 0;
-                    if (idx >= n) continue;
-                    const int row = idx / per_row, x = idx - row * per_row, j = j0 + row;
-                    if (j >= len) continue;
-                    const int id = table[j >> p.c.page_shift];
-                    if ((unsigned)id >= (unsigned long long)p.c.n_pages) {
-                        record_error(p.err, SYN_DEVERR_BOUNDS);
-                        continue;
-                    }
-                    const int cell = j & ((1 << p.c.page_shift) - 1);
-                    const uint8_t* base = pool + (int64_t)id * p.c.page_stride;
-                    code[u] = *reinterpret_cast<const uint4*>(base + (int64_t)cell * dim + 16 * x);
-                    scale[u] = *reinterpret_cast<const uint16_t*>(base + plane + 2 * ((int64_t)cell * (dim >> 5) + (x >> 1)));
+                if (id >= 0 && SYN_IN_BOUNDS((uint32_t)(lane + 1) * codes <= BN * D && id < p.c.n_pages)) {
+                    const uint32_t dst = smem_u32(smem + L::RAWS + st * L::RAW);
+                    const uint8_t* tile = (is_v ? p.c.v : p.c.k) + (int64_t)id * p.c.page_stride + (int64_t)h * p.c.tile;
+                    bulk_g2s(dst + lane * codes, tile + (int64_t)cell * dim, codes, full);
+                    bulk_g2s(dst + BN * D + lane * scales, tile + ((int64_t)dim << p.c.page_shift) + (int64_t)cell * (dim >> 4), scales, full);
                 }
-            };
-            if (n_pieces > 0) load(0);
-            for (; i < n_pieces; i++) {
-                const int st = i % NS;
-                if (!mbar_wait(smem_u32(&kv_empty[st]), ((i / NS) & 1) ^ 1, p.err, abort_flag)) break;
-                uint8_t* dst = smem + L::RING + st * L::STAGE;
-#pragma unroll
-                for (int u = 0; u < MOST; u++) {
-                    const int idx = u * 128 + lt;
-                    if (idx >= n) continue;
-                    const int row = idx / per_row, x = idx - row * per_row;
-                    // a byte b becomes 1024 + b by a permute with 0x64; value = scale * code, the one
-                    // rounding of the expansion (relative 2^-11, like that of p)
-                    const __half2 d = __half2half2(__ushort_as_half(scale[u])), k1152 = __float2half2_rn(1152.0f);
-                    const uint32_t cw[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
+            }
+            __syncwarp();
+        }
+        // the tiles still in flight (issued, not consumed: only after an abort) land first
+        if (Q8) {
+            for (int u = max(0, i - NR); u < i; u++) mbar_drain(smem_u32(&raw_full[u % max(NR, 1)]), (u / max(NR, 1)) & 1, p.err);
+        } else {
+            for (int u = max(0, i - NS); u < i; u++) mbar_drain(smem_u32(&kv_full[u % NS]), (u / NS) & 1, p.err);
+        }
+      }
+    } else if (Q8) {
+        // ------------------------------------ expand (Q8_0) -------------------------------------
+        if (QT == 2) give_registers<L::EXPAND_REGS>();
+        const int lt = tid - 32 * EXPAND_WARP;
+        const int per_row = dim >> 4, n = BN * per_row;  // 16 codes at a time
+#ifdef SYN_TEST_STALL
+        const int n_pieces = 0;
+#else
+        const int n_pieces = 2 * nt;
+#endif
+        const int box_shift = min(p.c.page_shift, BN == 128 ? 7 : 6);
+        for (int i = 0; i < n_pieces; i++) {
+            const int rs = i % max(NR, 1), st = i % NS;
+            if (!mbar_wait_poll(smem_u32(&raw_full[rs]), (i / max(NR, 1)) & 1, p.err, abort_flag)) break;
+            if (!mbar_wait_poll(smem_u32(&kv_empty[st]), ((i / NS) & 1) ^ 1, p.err, abort_flag)) break;
+            const int left = len - tiles.at(t0 + piece_tile(i)) * BN;  // rows of the tile that exist
+            const uint32_t there = raw_there[rs];
+            const uint8_t* raw = smem + L::RAWS + rs * L::RAW;
+            uint8_t* dst = smem + L::RING + st * L::STAGE;
+#pragma unroll 2
+            for (int idx = lt; idx < n; idx += 128) {
+                const int row = idx / per_row, x = idx - row * per_row;
+                uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                if (row < left && ((there >> (row >> box_shift)) & 1)) {
+                    // a byte c becomes 1024 + c by a permute with 0x64; value = scale * code, the one rounding
+                    // of the expansion (relative 2^-11, like that of p)
+                    const uint4 code = *reinterpret_cast<const uint4*>(raw + row * dim + 16 * x);
+                    const __half2 d = __half2half2(__ushort_as_half(*reinterpret_cast<const uint16_t*>(raw + BN * D + 2 * (row * (dim >> 5) + (x >> 1)))));
+                    const __half2 k1152 = __float2half2_rn(1152.0f);
+                    const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
                     uint32_t w[8];
 #pragma unroll
                     for (int y = 0; y < 4; y++) {
                         const uint32_t z = cw[y] ^ 0x80808080u;
-                        uint32_t a = __byte_perm(z, 0x64646464u, 0x4140), e = __byte_perm(z, 0x64646464u, 0x4342);
-                        const __half2 ha = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&a), k1152), d);
-                        const __half2 he = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&e), k1152), d);
-                        w[2 * y] = *reinterpret_cast<const uint32_t*>(&ha);
-                        w[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&he);
+                        uint32_t lo = __byte_perm(z, 0x64646464u, 0x4140), hi = __byte_perm(z, 0x64646464u, 0x4342);
+                        const __half2 hl = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&lo), k1152), d);
+                        const __half2 hh = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&hi), k1152), d);
+                        w[2 * y] = *reinterpret_cast<const uint32_t*>(&hl);
+                        w[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&hh);
                     }
-                    uint8_t* to = dst + (x >> 2) * (BN * 128) + row * 128;
-                    const int c = (2 * x) & 7;
-                    *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                    a = make_uint4(w[0], w[1], w[2], w[3]);
+                    b = make_uint4(w[4], w[5], w[6], w[7]);
                 }
-                if (i + 1 < n_pieces) load(i + 1);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&kv_full[st]));
+                uint8_t* to = dst + (x >> 2) * (BN * 128) + row * 128;
+                const int c = (2 * x) & 7;
+                *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) = a;
+                *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) << 4)) = b;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&kv_full[st]));
+                mbar_arrive(smem_u32(&raw_empty[rs]));
             }
         }
     }
@@ -761,21 +786,21 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (n_split == 1) return;
+    if (n_split == 1 || warp >= MMA_WARP) return;  // (the others have given their registers away)
     // ---- the last of the item's CTAs joins the partials ------------------------------------
     const int item = (int)b;
     __threadfence();
-    __syncthreads();
+    softmax_sync();
     if (tid == 0) {
         const int before = atomicAdd(&p.count[item], 1);
         info[0] = before == n_split - 1;
         if (before == n_split - 1) p.count[item] = 0;  // ready for the next call
     }
-    __syncthreads();
+    softmax_sync();
     if (!info[0] || *abort_flag) return;
     __threadfence();
     const float* base = p.part + (int64_t)(blockIdx.x - sp) * R * (D + 2);
-    for (int u = tid; u < rows * dim; u += THREADS) {
+    for (int u = tid; u < rows * dim; u += R) {
         const int e = u / rows, r = u - e * rows;
         float mx = -INFINITY, sum = 0.0f, acc = 0.0f;
         for (int x = 0; x < n_split; x++) {
@@ -797,13 +822,21 @@ __global__ void __launch_bounds__(PRE_THREADS<D, Q8>, 1)
 template <int D, bool Q8, bool MOD>
 static cudaError_t run_prefill(const CUtensorMap& km, const CUtensorMap& vm, const PrefillParams& p, int grid, cudaStream_t s) {
     auto kern = k_attn_prefill<D, Q8, MOD>;
-    constexpr int smem = 1024 + PreShape<D>::BYTES;
+    constexpr int smem = 1024 + PreShape<D, Q8>::BYTES;
     static_assert(smem <= 232448, "shared memory per CTA exceeds 227 KB");
     static ResidentCtas resident;
     int n;
-    const cudaError_t e = resident.get(reinterpret_cast<const void*>(kern), PRE_THREADS<D, Q8>, smem, &n);
+    cudaError_t e = resident.get(reinterpret_cast<const void*>(kern), PreShape<D, Q8>::THREADS, smem, &n);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(kern, grid, PRE_THREADS<D, Q8>, smem, s, km, vm, p);
+    if (PreShape<D, Q8>::QT == 2) {
+        // the hand-over of registers deals out what the launch has: a build with fewer must not start
+        static const int regs = [&] {
+            cudaFuncAttributes a;
+            return cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kern)) == cudaSuccess ? a.numRegs : 0;
+        }();
+        if (regs < (Q8 ? 128 : 168)) return cudaErrorInvalidConfiguration;
+    }
+    return launch_overlapped(kern, grid, PreShape<D, Q8>::THREADS, smem, s, km, vm, p);
 }
 
 static int prefill_rows(int dim) { return dim <= 128 ? 256 : 128; }

@@ -368,18 +368,16 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         const int qt = warp >> 2;
         const int r = tid;  // row of the item
         if (qt < q_act) {
-            // Q rows into shared memory: row r of the tile, 16-byte piece j of chunk c at j ^ (r % 8)
-            uint8_t* qs = smem + L::Q + qt * L::Q_TILE;
-            const int pieces = dim >> 3;
-            for (int i = tid & 127; i < 128 * pieces; i += 128) {
-                const int rr = i / pieces, j = i - rr * pieces;
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (qt * 128 + rr < rows) {
-                    const int row = row0 + qt * 128 + rr, t = row / p.g;
-                    w = *reinterpret_cast<const uint4*>(p.q + (int64_t)(tok0 + t) * p.q_stride +
-                                                        (int64_t)(h * p.g + row - t * p.g) * dim + 8 * j);
-                }
-                *reinterpret_cast<uint4*>(qs + (j >> 3) * (128 * 128) + rr * 128 + (((j & 7) ^ (rr & 7)) << 4)) = w;
+            // this thread's Q row into shared memory, 16-byte piece j of chunk c at j ^ (row % 8)
+            uint8_t* qs = smem + L::Q + qt * L::Q_TILE + (tid & 127) * 128;
+            const uint4* qrow = reinterpret_cast<const uint4*>(p.q + (int64_t)my_tok * p.q_stride + (int64_t)my_head * dim);
+#pragma unroll
+            for (int j0 = 0; j0 < D / 8; j0 += 8) {  // (8 loads on their way at a time)
+                uint4 w[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++) w[j] = row_ok && 8 * (j0 + j) < dim ? __ldg(qrow + j0 + j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 8; j++) *reinterpret_cast<uint4*>(qs + (j0 >> 3) * (128 * 128) + ((j ^ (tid & 7)) << 4)) = w[j];
             }
             fence_proxy_async_smem();
             __syncwarp();

@@ -55,6 +55,7 @@ struct PrefillParams {
     int* err;
     float scale, cap;
     int n_seq, n_tok, g, window, out_f16, sms, split;
+    int q_tma;  // Q by tensor-map copies (g divides 128: a tile's rows are whole tokens)
     uint32_t idesc_s, idesc_o;
 };
 
@@ -74,6 +75,7 @@ struct PreShape {
     static constexpr int BARS = RAWS + NR * RAW;
     static constexpr int INFO = BARS + (8 * (2 * NS + 2 * NR + 11) + 8 + 15) / 16 * 16;
     static constexpr int BYTES = INFO + 64 + 4 * (PRE_MAX_SEQ + 1);
+    static constexpr int MAX_SPLIT = NS * STAGE / (4 * R);  // parts of an item whose weights fit into the ring
     static constexpr int O_COL = QT == 2 ? 256 : 128;  // S slots below it
     static constexpr int SLOT = QT == 2 ? 128 : 64;    // columns of an S slot
     // warps: softmax, then MMA, loader and two that idle, then (Q8_0) four that expand
@@ -119,6 +121,11 @@ __device__ __forceinline__ float2 unpack2(uint64_t v) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -185,7 +192,8 @@ __device__ __forceinline__ void store_out(const PrefillParams& p, int64_t at, fl
 
 template <int D, bool Q8, bool MOD>
 __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
-    k_attn_prefill(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PrefillParams p) {
+    k_attn_prefill(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ CUtensorMap qmap, const PrefillParams p) {
     using L = PreShape<D, Q8>;
     constexpr int QT = L::QT, BN = L::BN, NS = L::NS, NR = L::NR, R = L::R, THREADS = L::THREADS;
     constexpr int MMA_WARP = L::MMA_WARP, LOAD_WARP = L::LOAD_WARP, EXPAND_WARP = L::EXPAND_WARP;
@@ -212,91 +220,8 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int dim = p.c.dim, nh = (dim + 63) >> 6;  // 64-value column chunks of a row
 
-    // ---- this CTA's item -------------------------------------------------------------------
-    auto new_tokens = [&](int s) {  // (starts that run backwards or past the call's tokens count as none)
-        const int a = p.starts[s], b = p.starts[s + 1];
-        return a < 0 || b > p.n_tok ? 0 : max(b - a, 0);
-    };
-    if (tid == 0) info[0] = 0, pre[0] = 0;
-    griddep_release();
-    griddep_wait();
-    __syncthreads();
-    for (int base = 0; base < p.n_seq; base += THREADS) {
-        const int s = base + tid;
-        int x = s < p.n_seq ? (int)(((int64_t)new_tokens(s) * p.g + R - 1) / R) : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        int* sums = reinterpret_cast<int*>(smem);  // (nothing else uses it yet)
-        if (lane == 31) sums[warp] = x;
-        __syncthreads();
-        int before = info[0];
-        for (int w = 0; w < warp; w++) before += sums[w];
-        if (s < p.n_seq) pre[s + 1] = before + x;
-        __syncthreads();
-        if (tid == THREADS - 1) info[0] = before + x;
-        __syncthreads();
-    }
-    const int n_tiles_q = pre[p.n_seq];
-    const int64_t items = (int64_t)n_tiles_q * p.c.n_kv;
-    // splits of an item: as many as leave every SM one CTA
-    const int max_split = p.split && items > 0 && items < p.sms ? (int)(p.sms / items) : 1;
-    const int64_t b = (int64_t)blockIdx.x / max_split;
-    const int sp = (int)(blockIdx.x - b * max_split);
-    if (b >= items) return;
-    // the last tiles of a sequence see the most keys: they go first
-    const int qtile = n_tiles_q - 1 - (int)(b / p.c.n_kv), h = (int)(b % p.c.n_kv);
-    int s;
-    {
-        int lo = 0, hi = p.n_seq - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (pre[mid + 1] > qtile) hi = mid;
-            else lo = mid + 1;
-        }
-        s = lo;
-    }
-    const int row0 = (qtile - pre[s]) * R;  // first row of the item among its sequence's
-    const int n_new = new_tokens(s), tok0 = p.starts[s];
-    const int rows = (int)min((int64_t)R, (int64_t)n_new * p.g - row0);
-    const int len = max(0, (int)min((int64_t)p.lens[s], min(p.max_pages << p.c.page_shift, (int64_t)INT_MAX - 1024)));
-    const int32_t* table = p.pages + (int64_t)s * p.max_pages;
-
-    // ---- what this thread's row sees, and the keys that some row sees -----------------------
-    Visible vis;
-    vis.first = vis.pre = vis.low = vis.end = 0;
-    int pos = 0, my_tok = 0, my_head = 0;
-    const bool row_ok = tid < rows;
-    if (tid == 0) {
-        info[1] = info[2] = INT_MAX;
-        info[3] = 0;
-    }
-    __syncthreads();
-    if (tid < R) {
-        int mf = INT_MAX, ml = INT_MAX, me = 0;
-        if (row_ok) {
-            const int t = (row0 + tid) / p.g;
-            my_head = h * p.g + (row0 + tid - t * p.g);
-            my_tok = tok0 + t;
-            pos = len - n_new + t;
-            vis = visible_of(len, pos, p.first ? p.first[my_tok] : 0, p.prefix ? p.prefix[s] : 0, p.window);
-            if (vis.pre > vis.first || vis.end > vis.low) {
-                mf = vis.pre > vis.first ? vis.first : vis.low;
-                ml = vis.end > vis.low ? vis.low : vis.pre;
-                me = max(vis.end, vis.pre);
-            }
-        }
-        mf = __reduce_min_sync(0xffffffffu, mf);
-        ml = __reduce_min_sync(0xffffffffu, ml);
-        me = __reduce_max_sync(0xffffffffu, me);
-        if (lane == 0) {
-            atomicMin(&info[1], mf);
-            atomicMin(&info[2], ml);
-            atomicMax(&info[3], me);
-        }
-    }
+    // ---- set-up that touches no global memory, ahead of the kernel before this one -----------
+    auto softmax_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(R) : "memory"); };  // the softmax warps alone
     if (tid == 0) {
         for (int i = 0; i < NS; i++) {
             mbar_init(smem_u32(&kv_full[i]), Q8 ? 4 : 1);
@@ -307,7 +232,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             mbar_init(smem_u32(&p_full[i]), 4);
             mbar_init(smem_u32(&p_half[i]), 4);
             mbar_init(smem_u32(&o_done[i]), 1);
-            mbar_init(smem_u32(&q_full[i]), 4);
+            mbar_init(smem_u32(&q_full[i]), p.q_tma ? 1 : 4);
         }
         for (int i = 0; i < NR; i++) {
             mbar_init(smem_u32(&raw_full[i]), 1);
@@ -315,23 +240,153 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         }
         mbar_init(smem_u32(mma_idle), 1);
         *abort_flag = 0;
+        info[0] = 0;
+        info[1] = info[2] = INT_MAX;
+        info[3] = 0;
+        pre[0] = 0;
         fence_mbar_init();
     }
-    __syncthreads();
-    // [min first, prefix) then [min low, max end): every key that some row sees lies in one of them
-    const int pre_end = p.prefix ? min(max(p.prefix[s], 0), len) : 0;
-    Tiles tiles;
-    {
-        const int mf = info[1], ml = info[2], me = info[3];
-        tiles.a0 = tiles.a1 = tiles.b0 = tiles.b1 = 0;
-        if (me > 0) {
-            tiles.b0 = ml / BN;
-            tiles.b1 = me > ml ? (me + BN - 1) / BN : tiles.b0;
-            tiles.a0 = tiles.a1 = mf / BN;
-            const int ae = min(pre_end, ml);
-            if (ae > mf) tiles.a1 = (ae + BN - 1) / BN;
-            if (tiles.b1 > tiles.b0) tiles.a1 = max(tiles.a0, min(tiles.a1, tiles.b0));
+    griddep_release();
+    griddep_wait();
+
+    // ---- this CTA's item -------------------------------------------------------------------
+    auto new_tokens = [&](int s) {  // (starts that run backwards or past the call's tokens count as none)
+        const int a = p.starts[s], b = p.starts[s + 1];
+        return a < 0 || b > p.n_tok ? 0 : max(b - a, 0);
+    };
+    const int most_len = (int)min(p.max_pages << p.c.page_shift, (int64_t)INT_MAX - 1024);
+    // Items of all sequences, and the sequence that the item of this CTA belongs to: up to 32
+    // sequences by the lanes of each warp, from one round of loads; more through shared memory.
+    // splits of an item: as many as leave every SM one CTA
+    auto splits_of = [&](int64_t items) { return p.split && items > 0 && items < p.sms ? min((int)(p.sms / items), L::MAX_SPLIT) : 1; };
+    int n_tiles_q, s, before_s, n_new, tok0, len, prefix;
+    if (p.n_seq <= 32) {
+        const int mine = min(lane, p.n_seq - 1);
+        const int my_new = lane < p.n_seq ? new_tokens(mine) : 0, my_start = p.starts[mine], my_len = p.lens[mine];
+        const int my_prefix = p.prefix ? p.prefix[mine] : 0;
+        const int x = (int)(((int64_t)my_new * p.g + R - 1) / R);
+        int sum = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
         }
+        n_tiles_q = __shfl_sync(0xffffffffu, sum, 31);
+        const int64_t items = (int64_t)n_tiles_q * p.c.n_kv, b = (int64_t)blockIdx.x / splits_of(items);
+        if (b >= items) return;
+        const int qt = n_tiles_q - 1 - (int)(b / p.c.n_kv);
+        s = __ffs(__ballot_sync(0xffffffffu, sum > qt)) - 1;
+        before_s = __shfl_sync(0xffffffffu, sum - x, s);
+        n_new = __shfl_sync(0xffffffffu, my_new, s);
+        tok0 = __shfl_sync(0xffffffffu, my_start, s);
+        len = __shfl_sync(0xffffffffu, my_len, s);
+        prefix = __shfl_sync(0xffffffffu, my_prefix, s);
+    } else {
+        __syncthreads();
+        for (int base = 0; base < p.n_seq; base += THREADS) {
+            const int sq = base + tid;
+            int x = sq < p.n_seq ? (int)(((int64_t)new_tokens(sq) * p.g + R - 1) / R) : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            int* sums = reinterpret_cast<int*>(smem);  // (nothing else uses it yet)
+            if (lane == 31) sums[warp] = x;
+            __syncthreads();
+            int before = info[0];
+            for (int w = 0; w < warp; w++) before += sums[w];
+            if (sq < p.n_seq) pre[sq + 1] = before + x;
+            __syncthreads();
+            if (tid == THREADS - 1) info[0] = before + x;
+            __syncthreads();
+        }
+        n_tiles_q = pre[p.n_seq];
+        const int64_t items = (int64_t)n_tiles_q * p.c.n_kv, b = (int64_t)blockIdx.x / splits_of(items);
+        if (b >= items) return;
+        const int qt = n_tiles_q - 1 - (int)(b / p.c.n_kv);
+        int lo = 0, hi = p.n_seq - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid + 1] > qt) hi = mid;
+            else lo = mid + 1;
+        }
+        s = lo;
+        before_s = pre[s];
+        n_new = new_tokens(s);
+        tok0 = p.starts[s];
+        len = p.lens[s];
+        prefix = p.prefix ? p.prefix[s] : 0;
+    }
+    len = min(max(len, 0), most_len);
+    const int max_split = splits_of((int64_t)n_tiles_q * p.c.n_kv);
+    const int64_t b = (int64_t)blockIdx.x / max_split;
+    const int sp = (int)(blockIdx.x - b * max_split);
+    // the last tiles of a sequence see the most keys: they go first
+    const int qtile = n_tiles_q - 1 - (int)(b / p.c.n_kv), h = (int)(b % p.c.n_kv);
+    const int row0 = (qtile - before_s) * R;  // first row of the item among its sequence's
+    const int rows = (int)min((int64_t)R, (int64_t)n_new * p.g - row0);
+    const int32_t* table = p.pages + (int64_t)s * p.max_pages;
+
+    // ---- what this thread's row sees, and the keys that some row sees -----------------------
+    Visible vis;
+    vis.first = vis.pre = vis.low = vis.end = 0;
+    int pos = 0, my_tok = 0, my_head = 0;
+    const bool row_ok = tid < rows;
+    if (tid < R && row_ok) {
+        const int t = (row0 + tid) / p.g;
+        my_head = h * p.g + (row0 + tid - t * p.g);
+        my_tok = tok0 + t;
+        pos = len - n_new + t;
+        vis = visible_of(len, pos, p.first ? p.first[my_tok] : 0, prefix, p.window);
+    }
+    const int pre_end = min(max(prefix, 0), len);
+    // [mf, prefix) then [ml, me): every key that some row sees lies in one of them
+    int mf, ml, me;
+    if (p.first) {
+        mf = ml = INT_MAX;
+        me = 0;
+        if (row_ok && tid < R && (vis.pre > vis.first || vis.end > vis.low)) {
+            mf = vis.pre > vis.first ? vis.first : vis.low;
+            ml = vis.end > vis.low ? vis.low : vis.pre;
+            me = max(vis.end, vis.pre);
+        }
+        if (p.n_seq <= 32) __syncthreads();  // (info is set)
+        if (tid < R) {
+            mf = __reduce_min_sync(0xffffffffu, mf);
+            ml = __reduce_min_sync(0xffffffffu, ml);
+            me = __reduce_max_sync(0xffffffffu, me);
+            if (lane == 0) {
+                atomicMin(&info[1], mf);
+                atomicMin(&info[2], ml);
+                atomicMax(&info[3], me);
+            }
+        }
+        __syncthreads();
+        mf = info[1];
+        ml = info[2];
+        me = info[3];
+    } else {  // positions ascend: the item's first and last token tell
+        const int p_lo = len - n_new + row0 / p.g, p_hi = len - n_new + (row0 + rows - 1) / p.g;
+        if (p_hi >= 0) {
+            ml = p.window > 0 ? max(0, max(p_lo, 0) - p.window + 1) : 0;
+            mf = pre_end > 0 ? 0 : ml;
+            me = max(min(p_hi + 1, len), pre_end);
+        } else {
+            ml = pre_end;
+            mf = 0;
+            me = pre_end;
+        }
+    }
+    Tiles tiles;
+    tiles.a0 = tiles.a1 = tiles.b0 = tiles.b1 = 0;
+    if (me > 0) {
+        tiles.b0 = ml / BN;
+        tiles.b1 = me > ml ? (me + BN - 1) / BN : tiles.b0;
+        tiles.a0 = tiles.a1 = mf / BN;
+        const int ae = min(pre_end, ml);
+        if (ae > mf) tiles.a1 = (ae + BN - 1) / BN;
+        if (tiles.b1 > tiles.b0) tiles.a1 = max(tiles.a0, min(tiles.a1, tiles.b0));
     }
     const int all = tiles.count();
     const int n_split = min(max_split, max(1, all / 2));  // at least two tiles each
@@ -355,8 +410,6 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
     const uint32_t tmem = *tmem_slot;
     float* part = p.part + (int64_t)blockIdx.x * R * (D + 2);  // [D][R] values, [R] maxima, [R] sums
 
-    auto softmax_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(R) : "memory"); };  // the softmax warps alone
-
     // The ring's order: K of the first tile, then (two row tiles) V and the next K, or (one) the
     // next K and V.  Piece i of 2*nt: is it V, and of which tile.
     auto piece_v = [&](int i) { return QT == 2 ? (i & 1) : i == 2 * nt - 1 || (i > 0 && (i & 1) == 0); };
@@ -368,27 +421,29 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         const int qt = warp >> 2;
         const int r = tid;  // row of the item
         if (qt < q_act) {
-            // this thread's Q row into shared memory, 16-byte piece j of chunk c at j ^ (row % 8)
-            uint8_t* qs = smem + L::Q + qt * L::Q_TILE + (tid & 127) * 128;
-            const uint4* qrow = reinterpret_cast<const uint4*>(p.q + (int64_t)my_tok * p.q_stride + (int64_t)my_head * dim);
+            if (!p.q_tma) {
+                // this thread's Q row into shared memory, 16-byte piece j of chunk c at j ^ (row % 8)
+                uint8_t* qs = smem + L::Q + qt * L::Q_TILE + (tid & 127) * 128;
+                const uint4* qrow = reinterpret_cast<const uint4*>(p.q + (int64_t)my_tok * p.q_stride + (int64_t)my_head * dim);
 #pragma unroll
-            for (int j0 = 0; j0 < D / 8; j0 += 8) {  // (8 loads on their way at a time)
-                uint4 w[8];
+                for (int j0 = 0; j0 < D / 8; j0 += 8) {  // (8 loads on their way at a time)
+                    uint4 w[8];
 #pragma unroll
-                for (int j = 0; j < 8; j++) w[j] = row_ok && 8 * (j0 + j) < dim ? __ldg(qrow + j0 + j) : make_uint4(0, 0, 0, 0);
+                    for (int j = 0; j < 8; j++) w[j] = row_ok && 8 * (j0 + j) < dim ? __ldg(qrow + j0 + j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int j = 0; j < 8; j++) *reinterpret_cast<uint4*>(qs + (j0 >> 3) * (128 * 128) + ((j ^ (tid & 7)) << 4)) = w[j];
+                    for (int j = 0; j < 8; j++) *reinterpret_cast<uint4*>(qs + (j0 >> 3) * (128 * 128) + ((j ^ (tid & 7)) << 4)) = w[j];
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&q_full[qt]));
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&q_full[qt]));
 
             const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
             const uint32_t o_base = lane_base + L::O_COL + qt * D;
             const float c_log2 = p.scale * 1.4426950408889634f;
             const float slope = MOD && p.slopes && row_ok ? p.slopes[my_head] * 1.4426950408889634f : 0.0f;
             const float cap_log2 = p.cap * 1.4426950408889634f;
-            const float to_cap2 = p.cap > 0.0f ? 2.0f * c_log2 / p.cap : 0.0f;
+            const float to_cap = p.cap > 0.0f ? p.scale / p.cap : 0.0f, to_cap2 = 2.0f * 1.4426950408889634f * to_cap;
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
             for (int i = 0; i < nt; i++) {
@@ -406,13 +461,38 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < BN; c += 32) TMEM_LD_WAIT32((v + c));
                 if (MOD) {
+                    float big = 0.0f;
                     if (p.cap > 0.0f) {
+#pragma unroll
+                        for (int c = 0; c < BN; c += 2)
+                            big = fmaxf(fmaxf(big, fabsf(__uint_as_float(v[c]))), fabsf(__uint_as_float(v[c + 1])));
+                    }
+                    if (p.cap > 0.0f && __all_sync(0xffffffffu, big * to_cap <= 1.0f)) {
+                        // Scores up to the cap in size: tanh(y) = y times a polynomial in y^2, fitted on [0, 1]
+                        // to 5e-7, five paired instructions a score and none of the two special-function ones
+                        // of the general form, which has to share that unit with the powers (1.5 times the
+                        // time a tile's products take; a tile of 128 x 128 3100 -> 1900 cycles).
+                        const uint64_t k2 = pack2(to_cap, to_cap), s2 = pack2(c_log2, c_log2);
+#pragma unroll
+                        for (int c = 0; c < BN; c += 2) {
+                            const uint64_t x = pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                            const uint64_t y = mul2(x, k2), z = mul2(y, y);
+                            uint64_t t = fma2(z, pack2(-0.00308041f, -0.00308041f), pack2(0.01677678f, 0.01677678f));
+                            t = fma2(z, t, pack2(-0.05163546f, -0.05163546f));
+                            t = fma2(z, t, pack2(0.13282514f, 0.13282514f));
+                            t = fma2(z, t, pack2(-0.3332918f, -0.3332918f));
+                            t = fma2(z, t, pack2(0.99999944f, 0.99999944f));
+                            const float2 r2 = unpack2(mul2(mul2(x, s2), t));
+                            v[c] = __float_as_uint(r2.x);
+                            v[c + 1] = __float_as_uint(r2.y);
+                        }
+                    } else if (p.cap > 0.0f) {
                         // cap*tanh(x/cap) = cap - 2 cap/(1 + 2^(2 x log2(e)/cap)), all in powers of two
-                        const uint64_t k2 = pack2(to_cap2, to_cap2), one2 = pack2(1.0f, 1.0f), zero2 = 0;
+                        const uint64_t k2 = pack2(to_cap2, to_cap2), one2 = pack2(1.0f, 1.0f);
                         const uint64_t m2 = pack2(-2.0f * cap_log2, -2.0f * cap_log2), cap2 = pack2(cap_log2, cap_log2);
 #pragma unroll
                         for (int c = 0; c < BN; c += 2) {
-                            const float2 y = unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2, zero2));
+                            const float2 y = unpack2(mul2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2));
                             const float2 z = unpack2(add2(pack2(ex2(y.x), ex2(y.y)), one2));
                             const float2 x = unpack2(fma2(pack2(rcp(z.x), rcp(z.y)), m2, cap2));
                             v[c] = __float_as_uint(x.x);
@@ -504,39 +584,59 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 float odd = l - l;  // NaN where something is not finite
                 const int64_t out0 = (int64_t)my_tok * p.out_stride + (int64_t)my_head * dim;
-                for (int c = 0; c < dim; c += 32) {
-                    uint32_t o[32];
-                    __syncwarp();
-                    TMEM_LD32(o_base + c, o);
-                    tmem_ld_wait();
+                // The rows go through shared memory (this warp's share of the Q tile, which no product
+                // reads any more), so that the stores are whole rows: 16-byte piece j at j ^ (lane % 8).
+                uint8_t* stage = smem + L::Q + qt * L::Q_TILE + (warp & 3) * (L::Q_TILE / 4);
+                const int per = p.out_f16 ? D : D / 2;  // values of a row that its 2 D bytes hold
+                const uint32_t live = __ballot_sync(0xffffffffu, row_ok);
+                for (int c0 = 0; c0 < dim; c0 += per) {
+                    const int n = min(per, dim - c0);
+                    for (int c = 0; c < n; c += 16) {
+                        uint32_t o[16];
+                        __syncwarp();
+                        TMEM_LD16(o_base + c0 + c, o);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int u = 0; u < 32; u++) {
-                        const float x = __uint_as_float(o[u]);
-                        odd += x - x;
-                    }
-                    if (!row_ok) continue;
-                    if (n_split > 1) {
-#pragma unroll
-                        for (int u = 0; u < 32; u++) __stcg(part + (int64_t)(c + u) * R + r, __uint_as_float(o[u]));
-                    } else if (p.out_f16) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(p.out) + out0 + c);
-#pragma unroll
-                        for (int u = 0; u < 4; u++) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int x = 0; x < 4; x++) {
-                                const __half2 hh = __floats2half2_rn(__uint_as_float(o[8 * u + 2 * x]) * inv, __uint_as_float(o[8 * u + 2 * x + 1]) * inv);
-                                w[x] = *reinterpret_cast<const uint32_t*>(&hh);
-                            }
-                            dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int u = 0; u < 16; u++) {
+                            const float x = __uint_as_float(o[u]);
+                            odd += x - x;
                         }
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + out0 + c);
+                        if (n_split > 1) {
+                            if (row_ok) {
 #pragma unroll
-                        for (int u = 0; u < 8; u++)
-                            dst[u] = make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
-                                                 __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
+                                for (int u = 0; u < 16; u++) __stcg(part + (int64_t)(c0 + c + u) * R + r, __uint_as_float(o[u]));
+                            }
+                        } else if (p.out_f16) {
+#pragma unroll
+                            for (int u = 0; u < 2; u++) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int x = 0; x < 4; x++) {
+                                    const __half2 hh = __floats2half2_rn(__uint_as_float(o[8 * u + 2 * x]) * inv, __uint_as_float(o[8 * u + 2 * x + 1]) * inv);
+                                    w[x] = *reinterpret_cast<const uint32_t*>(&hh);
+                                }
+                                *reinterpret_cast<uint4*>(stage + lane * (2 * D) + (((c / 8 + u) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 4; u++)
+                                *reinterpret_cast<float4*>(stage + lane * (2 * D) + (((c / 4 + u) ^ (lane & 7)) << 4)) =
+                                    make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
+                                                __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
+                        }
                     }
+                    if (n_split > 1) continue;
+                    __syncwarp();
+                    const int esize = p.out_f16 ? 2 : 4, pieces = n * esize / 16;  // of a row
+                    const int rows_at_once = 32 / pieces, sub = lane / pieces, j = lane - sub * pieces;
+                    for (int rr = 0; rr < 32; rr += rows_at_once) {
+                        const int row = rr + sub;
+                        const int64_t at = __shfl_sync(0xffffffffu, out0, row & 31);
+                        if (sub < rows_at_once && row < 32 && ((live >> row) & 1))
+                            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (at + c0) * esize + 16 * j) =
+                                *reinterpret_cast<const uint4*>(stage + row * (2 * D) + ((j ^ (row & 7)) << 4));
+                    }
+                    __syncwarp();
                 }
                 if (n_split > 1 && row_ok) {
                     __stcg(part + (int64_t)D * R + r, m);
@@ -667,6 +767,15 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
       } else if (warp == LOAD_WARP) {
         // ------------------------------------ loader -------------------------------------------
         int i = 0;
+        if (p.q_tma && lane < q_act) {
+            // 128 / g tokens of g heads: the row order of the item.  (Tokens past the call's are zeros;
+            // those of the next sequence are rows that nobody writes.)
+            const uint32_t full = smem_u32(&q_full[lane]), dst = smem_u32(smem + L::Q + lane * L::Q_TILE);
+            mbar_arrive_expect_tx(full, (uint32_t)nh * 128 * 128);
+            for (int c = 0; c < nh; c++)
+                tma_load_3d(dst + c * (128 * 128), &qmap, 64 * c, h * p.g, tok0 + (row0 + 128 * lane) / p.g, full);
+        }
+        __syncwarp();
 #ifdef SYN_TEST_STALL
         const int n_pieces = 0;  // timeout-test build: no tile is ever loaded, so the waits run out
 #else
@@ -715,6 +824,8 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             __syncwarp();
         }
         // the tiles still in flight (issued, not consumed: only after an abort) land first
+        if (p.q_tma)
+            for (int u = 0; u < q_act; u++) mbar_drain(smem_u32(&q_full[u]), 0, p.err);
         if (Q8) {
             for (int u = max(0, i - NR); u < i; u++) mbar_drain(smem_u32(&raw_full[u % max(NR, 1)]), (u / max(NR, 1)) & 1, p.err);
         } else {
@@ -725,7 +836,10 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         // ------------------------------------ expand (Q8_0) -------------------------------------
         if (QT == 2) give_registers<L::EXPAND_REGS>();
         const int lt = tid - 32 * EXPAND_WARP;
-        const int per_row = dim >> 4, n = BN * per_row;  // 16 codes at a time
+        // 16 codes at a time: thread lt takes piece x of rows row0_t, row0_t + per_pass, ...
+        const int per_row = dim >> 4, per_pass = 128 / per_row, row0_t = lt / per_row, x = lt - row0_t * per_row;
+        const int flip = (x >> 2) & 1;  // pieces of the two 64-value chunks store their halves in opposite order (banks)
+        const __half2 k1152 = __float2half2_rn(1152.0f);
 #ifdef SYN_TEST_STALL
         const int n_pieces = 0;
 #else
@@ -740,16 +854,18 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             const uint32_t there = raw_there[rs];
             const uint8_t* raw = smem + L::RAWS + rs * L::RAW;
             uint8_t* dst = smem + L::RING + st * L::STAGE;
-#pragma unroll 2
-            for (int idx = lt; idx < n; idx += 128) {
-                const int row = idx / per_row, x = idx - row * per_row;
-                uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                if (row < left && ((there >> (row >> box_shift)) & 1)) {
+            if (row0_t < per_pass) {
+#pragma unroll 4
+                for (int row = row0_t; row < BN; row += per_pass) {
                     // a byte c becomes 1024 + c by a permute with 0x64; value = scale * code, the one rounding
-                    // of the expansion (relative 2^-11, like that of p)
-                    const uint4 code = *reinterpret_cast<const uint4*>(raw + row * dim + 16 * x);
-                    const __half2 d = __half2half2(__ushort_as_half(*reinterpret_cast<const uint16_t*>(raw + BN * D + 2 * (row * (dim >> 5) + (x >> 1)))));
-                    const __half2 k1152 = __float2half2_rn(1152.0f);
+                    // of the expansion (relative 2^-11, like that of p); rows that are not there are zeros
+                    uint4 code = *reinterpret_cast<const uint4*>(raw + row * dim + 16 * x);
+                    uint16_t bits = *reinterpret_cast<const uint16_t*>(raw + BN * D + 2 * (row * (dim >> 5) + (x >> 1)));
+                    if (!(row < left && ((there >> (row >> box_shift)) & 1))) {
+                        code = make_uint4(0, 0, 0, 0);
+                        bits = 0;
+                    }
+                    const __half2 d = __half2half2(__ushort_as_half(bits));
                     const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
                     uint32_t w[8];
 #pragma unroll
@@ -761,13 +877,12 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                         w[2 * y] = *reinterpret_cast<const uint32_t*>(&hl);
                         w[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&hh);
                     }
-                    a = make_uint4(w[0], w[1], w[2], w[3]);
-                    b = make_uint4(w[4], w[5], w[6], w[7]);
+                    uint8_t* to = dst + (x >> 2) * (BN * 128) + row * 128;
+                    const int c = (2 * x) & 7;
+                    const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
+                    *reinterpret_cast<uint4*>(to + (((c + flip) ^ (row & 7)) << 4)) = flip ? b : a;
+                    *reinterpret_cast<uint4*>(to + (((c + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
                 }
-                uint8_t* to = dst + (x >> 2) * (BN * 128) + row * 128;
-                const int c = (2 * x) & 7;
-                *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) = a;
-                *reinterpret_cast<uint4*>(to + (((c + 1) ^ (row & 7)) << 4)) = b;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -798,27 +913,39 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
     if (!info[0] || *abort_flag) return;
     __threadfence();
     const float* base = p.part + (int64_t)(blockIdx.x - sp) * R * (D + 2);
+    constexpr int64_t pitch = (int64_t)R * (D + 2);
+    // each row's weights of the parts (the ring is free), then the values: independent loads
+    float* weight = reinterpret_cast<float*>(smem + L::RING);  // [n_split][R]
+    if (row_ok) {
+        float mx = -INFINITY, sum = 0.0f;
+#pragma unroll 4
+        for (int x = 0; x < n_split; x++) mx = fmaxf(mx, __ldcg(base + x * pitch + (int64_t)D * R + tid));
+        const float ms = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll 4
+        for (int x = 0; x < n_split; x++) {
+            const float w = ex2(__ldcg(base + x * pitch + (int64_t)D * R + tid) - ms);
+            sum = fmaf(__ldcg(base + x * pitch + (int64_t)(D + 1) * R + tid), w, sum);
+            weight[x * R + tid] = w;
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        for (int x = 0; x < n_split; x++) weight[x * R + tid] *= inv;
+    }
+    softmax_sync();
     for (int u = tid; u < rows * dim; u += R) {
         const int e = u / rows, r = u - e * rows;
-        float mx = -INFINITY, sum = 0.0f, acc = 0.0f;
-        for (int x = 0; x < n_split; x++) {
-            const float* q = base + (int64_t)x * R * (D + 2);
-            const float pm = __ldcg(q + (int64_t)D * R + r), ps = __ldcg(q + (int64_t)(D + 1) * R + r), po = __ldcg(q + (int64_t)e * R + r);
-            const float nm = fmaxf(mx, pm), ms = nm == -INFINITY ? 0.0f : nm;
-            const float fa = ex2(mx - ms), fb = ex2(pm - ms);
-            acc = acc * fa + po * fb;
-            sum = sum * fa + ps * fb;
-            mx = nm;
-        }
+        float acc = 0.0f;
+#pragma unroll 8
+        for (int x = 0; x < n_split; x++) acc = fmaf(__ldcg(base + x * pitch + (int64_t)e * R + r), weight[x * R + r], acc);
         const int t = (row0 + r) / p.g;
-        store_out(p, (int64_t)(tok0 + t) * p.out_stride + (int64_t)(h * p.g + row0 + r - t * p.g) * dim + e, sum == 0.0f ? 0.0f : acc / sum);
+        store_out(p, (int64_t)(tok0 + t) * p.out_stride + (int64_t)(h * p.g + row0 + r - t * p.g) * dim + e, acc);
     }
 }
 
 // ---- host side ---------------------------------------------------------------------------
 
 template <int D, bool Q8, bool MOD>
-static cudaError_t run_prefill(const CUtensorMap& km, const CUtensorMap& vm, const PrefillParams& p, int grid, cudaStream_t s) {
+static cudaError_t run_prefill(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm, const PrefillParams& p,
+                               int grid, cudaStream_t s) {
     auto kern = k_attn_prefill<D, Q8, MOD>;
     constexpr int smem = 1024 + PreShape<D, Q8>::BYTES;
     static_assert(smem <= 232448, "shared memory per CTA exceeds 227 KB");
@@ -834,7 +961,7 @@ static cudaError_t run_prefill(const CUtensorMap& km, const CUtensorMap& vm, con
         }();
         if (regs < (Q8 ? 128 : 168)) return cudaErrorInvalidConfiguration;
     }
-    return launch_overlapped(kern, grid, PreShape<D, Q8>::THREADS, smem, s, km, vm, p);
+    return launch_overlapped(kern, grid, PreShape<D, Q8>::THREADS, smem, s, km, vm, qm, p);
 }
 
 static int prefill_rows(int dim) { return dim <= 128 ? 256 : 128; }
@@ -848,11 +975,24 @@ cudaError_t launch_attn_prefill(const KvCache& c, const AttnDesc& a, int64_t n_s
                                 const int32_t* starts, const int32_t* pages, int64_t max_pages, const int32_t* lens,
                                 void* out, float* part, int* count, bool split, int* err, int sms, int* launches,
                                 cudaStream_t s) {
-    CUtensorMap km, vm;
+    CUtensorMap km, vm, qm;
     const int D = c.dim <= 64 ? 64 : c.dim <= 128 ? 128 : 256, BN = D <= 128 ? 128 : 64;
+    PFN_encodeTiled encode = get_encode();
+    if (!encode) return cudaErrorNotSupported;
+    const int g = a.n_heads / c.n_kv;
+    const bool q_tma = g <= 128 && 128 % g == 0;
+    if (q_tma) {
+        cuuint64_t dims[3] = {(cuuint64_t)c.dim, (cuuint64_t)a.n_heads, (cuuint64_t)n_tok};
+        cuuint64_t strides[2] = {(cuuint64_t)c.dim * 2, (cuuint64_t)a.q_stride * 2};
+        cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)(128 / g)}, estr[3] = {1, 1, 1};
+        if (encode(&qm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    } else {
+        qm = CUtensorMap{};  // unused
+    }
     if (!c.q8) {
-        PFN_encodeTiled encode = get_encode();
-        if (!encode) return cudaErrorNotSupported;
         const int64_t page = int64_t(1) << c.page_shift;
         cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)page, (cuuint64_t)c.n_kv, (cuuint64_t)c.n_pages};
         cuuint64_t strides[3] = {(cuuint64_t)c.dim * 2, (cuuint64_t)c.tile, (cuuint64_t)c.page_stride};
@@ -880,7 +1020,8 @@ cudaError_t launch_attn_prefill(const KvCache& c, const AttnDesc& a, int64_t n_s
     p.scale = a.scale;
     p.cap = a.cap;
     p.n_tok = (int)n_tok;
-    p.g = a.n_heads / c.n_kv;
+    p.g = g;
+    p.q_tma = q_tma;
     p.window = a.window;
     p.out_f16 = a.out_f16;
     p.sms = sms;
@@ -903,8 +1044,8 @@ cudaError_t launch_attn_prefill(const KvCache& c, const AttnDesc& a, int64_t n_s
         if (grid > INT_MAX) return cudaErrorInvalidValue;
         cudaError_t e;
 #define SYN_PRE(D)                                                                                              \
-    (c.q8 ? (mod ? run_prefill<D, true, true>(km, vm, p, (int)grid, s) : run_prefill<D, true, false>(km, vm, p, (int)grid, s)) \
-          : (mod ? run_prefill<D, false, true>(km, vm, p, (int)grid, s) : run_prefill<D, false, false>(km, vm, p, (int)grid, s)))
+    (c.q8 ? (mod ? run_prefill<D, true, true>(km, vm, qm, p, (int)grid, s) : run_prefill<D, true, false>(km, vm, qm, p, (int)grid, s)) \
+          : (mod ? run_prefill<D, false, true>(km, vm, qm, p, (int)grid, s) : run_prefill<D, false, false>(km, vm, qm, p, (int)grid, s)))
         e = D == 64 ? SYN_PRE(64) : D == 128 ? SYN_PRE(128) : SYN_PRE(256);
 #undef SYN_PRE
         if (e != cudaSuccess) return e;

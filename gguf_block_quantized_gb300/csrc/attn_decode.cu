@@ -208,14 +208,21 @@ __device__ __noinline__ void join_parts(const DecodeParams& p, int i0, int i1, i
             }
             __syncthreads();
             if (mine) {
-#pragma unroll 16
-                for (int c = share; c < m; c += shares) {
-                    const float4 o = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + c) + hd * D + e));
-                    const float f = w[c * H + hd];
-                    acc.x = fmaf(o.x, f, acc.x);
-                    acc.y = fmaf(o.y, f, acc.y);
-                    acc.z = fmaf(o.z, f, acc.z);
-                    acc.w = fmaf(o.w, f, acc.w);
+                for (int c = share; c < m; c += 8 * shares) {  // (the last batch repeats its last load)
+                    float4 o[8];
+#pragma unroll
+                    for (int x = 0; x < 8; x++) {
+                        const int cx = c + x * shares < m ? c + x * shares : c;
+                        o[x] = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + cx) + hd * D + e));
+                    }
+#pragma unroll
+                    for (int x = 0; x < 8; x++) {
+                        const float f = c + x * shares < m ? w[(c + x * shares) * H + hd] : 0.0f;
+                        acc.x = fmaf(o[x].x, f, acc.x);
+                        acc.y = fmaf(o[x].y, f, acc.y);
+                        acc.z = fmaf(o[x].z, f, acc.z);
+                        acc.w = fmaf(o[x].w, f, acc.w);
+                    }
                 }
             }
         }

@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             if (ok && mbar_wait_poll(smem_u32(&o_done[qt]), (nt - 1) & 1, p.err, abort_flag)) {
                 tc_fence_after();
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                float odd = l - l;  // NaN where something is not finite
+                uint64_t odd2 = 0;  // 0 times every sum: NaN where one is not finite
                 const int64_t out0 = (int64_t)my_tok * p.out_stride + (int64_t)my_head * dim;
                 // The rows go through shared memory (this warp's share of the Q tile, which no product
                 // reads any more), so that the stores are whole rows: 16-byte piece j at j ^ (lane % 8).
@@ -591,24 +591,21 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 const uint32_t live = __ballot_sync(0xffffffffu, row_ok);
                 for (int c0 = 0; c0 < dim; c0 += per) {
                     const int n = min(per, dim - c0);
-                    for (int c = 0; c < n; c += 16) {
-                        uint32_t o[16];
+                    for (int c = 0; c < n; c += 32) {
+                        uint32_t o[32];
                         __syncwarp();
-                        TMEM_LD16(o_base + c0 + c, o);
-                        tmem_ld_wait();
+                        TMEM_LD32(o_base + c0 + c, o);
+                        TMEM_LD_WAIT32(o);
 #pragma unroll
-                        for (int u = 0; u < 16; u++) {
-                            const float x = __uint_as_float(o[u]);
-                            odd += x - x;
-                        }
+                        for (int u = 0; u < 32; u += 2) odd2 = fma2(pack2(__uint_as_float(o[u]), __uint_as_float(o[u + 1])), 0, odd2);
                         if (n_split > 1) {
                             if (row_ok) {
 #pragma unroll
-                                for (int u = 0; u < 16; u++) __stcg(part + (int64_t)(c0 + c + u) * R + r, __uint_as_float(o[u]));
+                                for (int u = 0; u < 32; u++) __stcg(part + (int64_t)(c0 + c + u) * R + r, __uint_as_float(o[u]));
                             }
                         } else if (p.out_f16) {
 #pragma unroll
-                            for (int u = 0; u < 2; u++) {
+                            for (int u = 0; u < 4; u++) {
                                 uint32_t w[4];
 #pragma unroll
                                 for (int x = 0; x < 4; x++) {
@@ -619,7 +616,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                             }
                         } else {
 #pragma unroll
-                            for (int u = 0; u < 4; u++)
+                            for (int u = 0; u < 8; u++)
                                 *reinterpret_cast<float4*>(stage + lane * (2 * D) + (((c / 4 + u) ^ (lane & 7)) << 4)) =
                                     make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
                                                 __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
@@ -629,6 +626,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                     __syncwarp();
                     const int esize = p.out_f16 ? 2 : 4, pieces = n * esize / 16;  // of a row
                     const int rows_at_once = 32 / pieces, sub = lane / pieces, j = lane - sub * pieces;
+#pragma unroll 4
                     for (int rr = 0; rr < 32; rr += rows_at_once) {
                         const int row = rr + sub;
                         const int64_t at = __shfl_sync(0xffffffffu, out0, row & 31);
@@ -644,7 +642,8 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 }
                 // rows with a non-finite sum, one after the other, by the whole warp
                 __syncwarp();
-                uint32_t redo = __ballot_sync(0xffffffffu, row_ok && odd != 0.0f);
+                const float2 odd = unpack2(fma2(pack2(l, l), 0, odd2));
+                uint32_t redo = __ballot_sync(0xffffffffu, row_ok && !(odd.x + odd.y == 0.0f));
                 while (redo) {
                     const int src = __ffs(redo) - 1;
                     redo &= redo - 1;
@@ -918,26 +917,54 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
     float* weight = reinterpret_cast<float*>(smem + L::RING);  // [n_split][R]
     if (row_ok) {
         float mx = -INFINITY, sum = 0.0f;
-#pragma unroll 4
-        for (int x = 0; x < n_split; x++) mx = fmaxf(mx, __ldcg(base + x * pitch + (int64_t)D * R + tid));
-        const float ms = mx == -INFINITY ? 0.0f : mx;
-#pragma unroll 4
-        for (int x = 0; x < n_split; x++) {
-            const float w = ex2(__ldcg(base + x * pitch + (int64_t)D * R + tid) - ms);
-            sum = fmaf(__ldcg(base + x * pitch + (int64_t)(D + 1) * R + tid), w, sum);
-            weight[x * R + tid] = w;
+        for (int x0 = 0; x0 < n_split; x0 += 8) {  // (the last batch repeats the last part's loads)
+            float pm[8], pl[8];
+#pragma unroll
+            for (int x = 0; x < 8; x++) {
+                const float* q = base + min(x0 + x, n_split - 1) * pitch + (int64_t)D * R + tid;
+                pm[x] = __ldcg(q);
+                pl[x] = __ldcg(q + R);
+            }
+#pragma unroll
+            for (int x = 0; x < 8; x++) {
+                if (x0 + x >= n_split) continue;
+                const float nm = fmaxf(mx, pm[x]), ms = nm == -INFINITY ? 0.0f : nm;
+                sum = sum * ex2(mx - ms) + pl[x] * ex2(pm[x] - ms);
+                mx = nm;
+                weight[(x0 + x) * R + tid] = pm[x];
+            }
         }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        for (int x = 0; x < n_split; x++) weight[x * R + tid] *= inv;
+        const float ms = mx == -INFINITY ? 0.0f : mx, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        for (int x = 0; x < n_split; x++) weight[x * R + tid] = ex2(weight[x * R + tid] - ms) * inv;
     }
     softmax_sync();
-    for (int u = tid; u < rows * dim; u += R) {
-        const int e = u / rows, r = u - e * rows;
-        float acc = 0.0f;
-#pragma unroll 8
-        for (int x = 0; x < n_split; x++) acc = fmaf(__ldcg(base + x * pitch + (int64_t)e * R + r), weight[x * R + r], acc);
-        const int t = (row0 + r) / p.g;
-        store_out(p, (int64_t)(tok0 + t) * p.out_stride + (int64_t)(h * p.g + row0 + r - t * p.g) * dim + e, acc);
+    for (int u0 = tid; u0 < rows * dim; u0 += 4 * R) {
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        int e[4], r[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int u = min(u0 + i * R, rows * dim - 1);
+            e[i] = u / rows;
+            r[i] = u - e[i] * rows;
+        }
+        for (int x0 = 0; x0 < n_split; x0 += 4) {
+            float po[4][4];
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) po[x][i] = __ldcg(base + min(x0 + x, n_split - 1) * pitch + (int64_t)e[i] * R + r[i]);
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    if (x0 + x < n_split) acc[i] = fmaf(po[x][i], weight[(x0 + x) * R + r[i]], acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if (u0 + i * R >= rows * dim) continue;
+            const int t = (row0 + r[i]) / p.g;
+            store_out(p, (int64_t)(tok0 + t) * p.out_stride + (int64_t)(h * p.g + row0 + r[i] - t * p.g) * dim + e[i], acc[i]);
+        }
     }
 }
 

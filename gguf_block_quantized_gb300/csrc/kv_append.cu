@@ -94,12 +94,14 @@ __device__ __forceinline__ Piece piece_of(const AppendParams& p, int i) {
     return x;
 }
 
-template <bool Q8>
+// DIM: head_dim, or 0 for a width without a kernel of its own.  With a width of 64, 128 or 256 a
+// lane's place in a row is the same for every row, so its sines stay in registers.
+template <bool Q8, int DIM>
 __global__ void __launch_bounds__(APPEND_THREADS, APPEND_CTAS_PER_SM) k_kv_append(const AppendParams p) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     AppendSmem& sm = *reinterpret_cast<AppendSmem*>(smem_raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int dim = p.c.dim, per_row = dim >> 2;  // 4-value units per row
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int dim = DIM ? DIM : p.c.dim, per_row = dim >> 2;  // 4-value units per row
     const int half_rot = p.n_rot >> 1, pieces = p.q_pieces + 2 * p.kv_pieces;
     volatile int* abort_flag = &sm.abort;
     if (tid == 0) {
@@ -186,6 +188,65 @@ __global__ void __launch_bounds__(APPEND_THREADS, APPEND_CTAS_PER_SM) k_kv_appen
         const int b = it & 1;
         if (!mbar_wait(smem_u32(&sm.cs_full[b]), (it >> 1) & 1, p.err, abort_flag)) return;
         const float2* cs = sm.cs[b];
+        // a unit's rotation: values e .. e + 3 of a row, the other halves of their pairs at e + other
+        struct Turn {
+            float4 c0, c1;
+            int other;
+            bool on;
+        };
+        auto turn_of = [&](int e) {
+            Turn k;
+            k.on = e < p.n_rot;
+            k.other = 0;
+            k.c0 = k.c1 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (k.on) {
+                if (p.halves) {  // cosines in c0; sines, signed, in c1
+                    const bool lower = e < half_rot;
+                    const float4* c = reinterpret_cast<const float4*>(cs + (lower ? e : e - half_rot));
+                    const float4 x = c[0], y = c[1];
+                    const float sg = lower ? -1.0f : 1.0f;
+                    k.other = lower ? half_rot : -half_rot;
+                    k.c0 = make_float4(x.x, x.z, y.x, y.z);
+                    k.c1 = make_float4(sg * x.y, sg * x.w, sg * y.y, sg * y.w);
+                } else {
+                    k.c0 = *reinterpret_cast<const float4*>(cs + (e >> 1));  // (cos, sin) of two pairs
+                }
+            }
+            return k;
+        };
+        auto turned = [&](const Turn& k, const float* src) {
+            const float4 a = *reinterpret_cast<const float4*>(src);
+            if (!k.on) return a;
+            float4 r;
+            if (p.halves) {
+                const float4 y = *reinterpret_cast<const float4*>(src + k.other);
+                r.x = fmaf(a.x, k.c0.x, y.x * k.c1.x);
+                r.y = fmaf(a.y, k.c0.y, y.y * k.c1.y);
+                r.z = fmaf(a.z, k.c0.z, y.z * k.c1.z);
+                r.w = fmaf(a.w, k.c0.w, y.w * k.c1.w);
+            } else {
+                r.x = fmaf(a.x, k.c0.x, -a.y * k.c0.y);
+                r.y = fmaf(a.x, k.c0.y, a.y * k.c0.x);
+                r.z = fmaf(a.z, k.c0.z, -a.w * k.c0.w);
+                r.w = fmaf(a.z, k.c0.w, a.w * k.c0.z);
+            }
+            return r;
+        };
+        auto put = [&](uint8_t* tile, const float4& r, int e, bool in) {  // 4 values of a cached row
+            if (Q8) {
+                unsigned short scale;
+                const uint32_t codes = q8_codes(r, scale);
+                if (in) {
+                    *reinterpret_cast<uint32_t*>(tile + cell * dim + e) = codes;
+                    if ((e & 31) == 0)
+                        *reinterpret_cast<unsigned short*>(tile + ((int64_t)dim << p.c.page_shift) + 2 * (cell * (dim >> 5) + (e >> 5))) = scale;
+                }
+            } else if (in) {
+                *reinterpret_cast<uint2*>(tile + 2 * (cell * dim + e)) = pack_half4(r);
+            }
+        };
+        const int e_mine = DIM ? (32 * warp + lane) % (DIM ? DIM / 4 : 1) * 4 : 0;
+        const Turn mine = turn_of(e_mine);
         for (int i = i0; i < i1; i++, n++) {
             const Piece x = piece_of(p, i);
             const int st = n % APPEND_STAGES;
@@ -194,48 +255,36 @@ __global__ void __launch_bounds__(APPEND_THREADS, APPEND_CTAS_PER_SM) k_kv_appen
             uint8_t* pool = (x.kind == 2 ? p.c.v : p.c.k) + page * p.c.page_stride + (int64_t)x.row * p.c.tile;
             __half* qo = p.q_out + (t * p.n_heads + x.row) * dim;
             const int units = x.rows * per_row;
-            // (units is a multiple of 8: the 8 lanes of a block stay together)
-            for (int u0 = 32 * warp; u0 < units; u0 += 32 * APPEND_WARPS) {
-                const int u = min(u0 + lane, units - 1), row = u / per_row, e = (u - row * per_row) << 2;
-                const bool live = u0 + lane < units;
-                const float4 a = *reinterpret_cast<const float4*>(src + 4 * u);
-                float4 r = a;
-                if (x.kind < 2 && e < p.n_rot) {
-                    if (p.halves) {
-                        const bool lower = e < half_rot;
-                        const float4 y = *reinterpret_cast<const float4*>(src + 4 * u + (lower ? half_rot : -half_rot));
-                        const float4* c = reinterpret_cast<const float4*>(cs + (lower ? e : e - half_rot));
-                        const float4 c0 = c[0], c1 = c[1];
-                        const float sg = lower ? -1.0f : 1.0f;
-                        r.x = fmaf(a.x, c0.x, sg * y.x * c0.y);
-                        r.y = fmaf(a.y, c0.z, sg * y.y * c0.w);
-                        r.z = fmaf(a.z, c1.x, sg * y.z * c1.y);
-                        r.w = fmaf(a.w, c1.z, sg * y.w * c1.w);
-                    } else {
-                        const float4 c = *reinterpret_cast<const float4*>(cs + (e >> 1));
-                        r.x = fmaf(a.x, c.x, -a.y * c.y);
-                        r.y = fmaf(a.x, c.y, a.y * c.x);
-                        r.z = fmaf(a.z, c.z, -a.w * c.w);
-                        r.w = fmaf(a.z, c.w, a.w * c.z);
-                    }
-                }
+            // (units is a multiple of 8: the 8 lanes of a Q8_0 block stay together)
+            if (DIM) {
+                const int u = 32 * warp + lane;
+                constexpr int ROWS = DIM ? 1024 / DIM : 1;  // rows that the eight warps take at a time
+                const int row = u / (DIM ? DIM / 4 : 1);
+                const bool there = SYN_IN_BOUNDS(x.row + x.rows <= (x.kind == 0 ? p.n_heads : p.c.n_kv) && (x.kind == 0 || !store || page < p.c.n_pages));
                 if (x.kind == 0) {
-                    if (live) *reinterpret_cast<uint2*>(qo + 4 * u) = pack_half4(r);
-                    continue;
-                }
-                uint8_t* tile = pool + (int64_t)row * p.c.tile;
-                const bool in = live && store && SYN_IN_BOUNDS(x.row + row < p.c.n_kv && page < p.c.n_pages && e + 4 <= dim);
-                if (Q8) {
-                    unsigned short scale;
-                    const uint32_t codes = q8_codes(r, scale);
-                    if (in) {
-                        *reinterpret_cast<uint32_t*>(tile + (int64_t)cell * dim + e) = codes;
-                        if ((e & 31) == 0)
-                            *reinterpret_cast<unsigned short*>(tile + ((int64_t)dim << p.c.page_shift) +
-                                                               2 * ((int64_t)cell * (dim >> 5) + (e >> 5))) = scale;
+#pragma unroll 4
+                    for (int k = 0; k < x.rows; k += ROWS)
+                        if (row + k < x.rows && there) *reinterpret_cast<uint2*>(qo + 4 * u + k * DIM) = pack_half4(turned(mine, src + 4 * u + k * DIM));
+                } else {
+                    uint8_t* tile = pool + row * p.c.tile;
+#pragma unroll 2
+                    for (int k = 0; k < x.rows; k += ROWS) {
+                        const float* s4 = src + 4 * min(u + k * (DIM / 4), units - 1);
+                        const float4 r = x.kind == 1 ? turned(mine, s4) : *reinterpret_cast<const float4*>(s4);
+                        put(tile, r, e_mine, row + k < x.rows && store && there);
+                        tile += ROWS * p.c.tile;
                     }
-                } else if (in) {
-                    *reinterpret_cast<uint2*>(tile + 2 * ((int64_t)cell * dim + e)) = pack_half4(r);
+                }
+            } else {
+                for (int u0 = 32 * warp; u0 < units; u0 += 32 * APPEND_WARPS) {
+                    const int u = min(u0 + lane, units - 1), row = u / per_row, e = (u - row * per_row) << 2;
+                    const bool live = u0 + lane < units;
+                    const float4 r = x.kind < 2 ? turned(turn_of(e), src + 4 * u) : *reinterpret_cast<const float4*>(src + 4 * u);
+                    if (x.kind == 0) {
+                        if (live) *reinterpret_cast<uint2*>(qo + 4 * u) = pack_half4(r);
+                    } else {
+                        put(pool + row * p.c.tile, r, e, live && store && SYN_IN_BOUNDS(x.row + row < p.c.n_kv && page < p.c.n_pages && e + 4 <= dim));
+                    }
                 }
             }
             __syncwarp();
@@ -252,38 +301,41 @@ struct ReadParams {
     const int64_t* slots;
     __half* k;
     __half* v;
-    int64_t n_units;
+    int64_t n;
     int* err;
 };
 
 __global__ void __launch_bounds__(256) k_kv_read(const ReadParams p) {
-    const int dim = p.c.dim, per_tok = (p.c.n_kv * dim) >> 2;  // 4-value units of one tensor
+    const int dim = p.c.dim, per_row = dim >> 3, per_tok = p.c.n_kv * per_row;  // 8-value units
     griddep_release();
     griddep_wait();
-    for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < p.n_units; u += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t tt = u / per_tok;  // token, keys and values in turn
-        const int at = (int)(u - tt * per_tok) << 2;
-        const int64_t t = tt >> 1;
-        const bool is_v = tt & 1;
-        const int h = at / dim, e = at - h * dim;
+    for (int64_t t = blockIdx.x; t < p.n; t += gridDim.x) {
         const int64_t slot = p.slots[t], page = slot >> p.c.page_shift;
         const int cell = (int)(slot & (((int64_t)1 << p.c.page_shift) - 1));
-        uint2 w = make_uint2(0, 0);
-        if (slot >= 0 && page < p.c.n_pages) {
-            const uint8_t* tile = (is_v ? p.c.v : p.c.k) + page * p.c.page_stride + (int64_t)h * p.c.tile;
-            if (p.c.q8) {
-                const uint32_t q = *reinterpret_cast<const uint32_t*>(tile + (int64_t)cell * dim + e);
-                const float d = h2f_bits(*reinterpret_cast<const unsigned short*>(
-                    tile + ((int64_t)dim << p.c.page_shift) + 2 * ((int64_t)cell * (dim >> 5) + (e >> 5))));
-                w = pack_half4(make_float4(d * (float)(int8_t)q, d * (float)(int8_t)(q >> 8),
-                                           d * (float)(int8_t)(q >> 16), d * (float)(int8_t)(q >> 24)));
-            } else {
-                w = *reinterpret_cast<const uint2*>(tile + 2 * ((int64_t)cell * dim + e));
+        const bool there = slot >= 0 && page < p.c.n_pages;
+        if (slot >= 0 && !there && threadIdx.x == 0) record_error(p.err, SYN_DEVERR_BOUNDS);
+        for (int u = threadIdx.x; u < 2 * per_tok; u += 256) {  // keys, then values
+            const bool is_v = u >= per_tok;
+            const int at = is_v ? u - per_tok : u, h = at / per_row, e = (at - h * per_row) << 3;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (there) {
+                const uint8_t* tile = (is_v ? p.c.v : p.c.k) + page * p.c.page_stride + (int64_t)h * p.c.tile;
+                if (p.c.q8) {
+                    const uint2 q = *reinterpret_cast<const uint2*>(tile + (int64_t)cell * dim + e);
+                    const float d = h2f_bits(*reinterpret_cast<const unsigned short*>(
+                        tile + ((int64_t)dim << p.c.page_shift) + 2 * ((int64_t)cell * (dim >> 5) + (e >> 5))));
+                    auto four = [&](uint32_t x) {
+                        return pack_half4(make_float4(d * (float)(int8_t)x, d * (float)(int8_t)(x >> 8), d * (float)(int8_t)(x >> 16),
+                                                      d * (float)(int8_t)(x >> 24)));
+                    };
+                    const uint2 a = four(q.x), b = four(q.y);
+                    w = make_uint4(a.x, a.y, b.x, b.y);
+                } else {
+                    w = *reinterpret_cast<const uint4*>(tile + 2 * ((int64_t)cell * dim + e));
+                }
             }
-        } else if (slot >= 0) {
-            record_error(p.err, SYN_DEVERR_BOUNDS);
+            *reinterpret_cast<uint4*>((is_v ? p.v : p.k) + (t * per_tok + at) * 8) = w;
         }
-        *reinterpret_cast<uint2*>((is_v ? p.v : p.k) + t * ((int64_t)per_tok << 2) + at) = w;
     }
 }
 
@@ -319,12 +371,18 @@ cudaError_t launch_kv_append(const KvCache& c, const RopeDesc& r, int64_t n_tok,
     p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(p.q_pieces + 2 * p.kv_pieces, ctas / n_tok));
     p.n_items = n_tok * p.parts;
     const int grid = (int)std::min<int64_t>(p.n_items, ctas);
-    static ResidentCtas resident[2];
-    auto kern = c.q8 ? k_kv_append<true> : k_kv_append<false>;
-    int per_sm;
-    const cudaError_t e = resident[c.q8].get(reinterpret_cast<const void*>(kern), APPEND_THREADS, sizeof(AppendSmem), &per_sm);
-    if (e != cudaSuccess) return e;
-    return launch_overlapped(kern, grid, APPEND_THREADS, sizeof(AppendSmem), s, p);
+    auto run = [&](auto kern, ResidentCtas& resident) {
+        int per_sm;
+        const cudaError_t e = resident.get(reinterpret_cast<const void*>(kern), APPEND_THREADS, sizeof(AppendSmem), &per_sm);
+        return e != cudaSuccess ? e : launch_overlapped(kern, grid, APPEND_THREADS, sizeof(AppendSmem), s, p);
+    };
+    static ResidentCtas resident[2][4];
+    switch (c.dim) {
+    case 64: return c.q8 ? run(k_kv_append<true, 64>, resident[1][0]) : run(k_kv_append<false, 64>, resident[0][0]);
+    case 128: return c.q8 ? run(k_kv_append<true, 128>, resident[1][1]) : run(k_kv_append<false, 128>, resident[0][1]);
+    case 256: return c.q8 ? run(k_kv_append<true, 256>, resident[1][2]) : run(k_kv_append<false, 256>, resident[0][2]);
+    default: return c.q8 ? run(k_kv_append<true, 0>, resident[1][3]) : run(k_kv_append<false, 0>, resident[0][3]);
+    }
 }
 
 cudaError_t launch_kv_read(const KvCache& c, int64_t n, const int64_t* slots, void* k, void* v, int* err, int sms,
@@ -334,10 +392,9 @@ cudaError_t launch_kv_read(const KvCache& c, int64_t n, const int64_t* slots, vo
     p.slots = slots;
     p.k = static_cast<__half*>(k);
     p.v = static_cast<__half*>(v);
-    p.n_units = n * 2 * ((int64_t)c.n_kv * c.dim / 4);
+    p.n = n;
     p.err = err;
-    const int64_t blocks = (p.n_units + 255) / 256, most = (int64_t)sms * 8;
-    return launch_overlapped(k_kv_read, (int)(blocks < most ? blocks : most), 256, 0, s, p);
+    return launch_overlapped(k_kv_read, (int)std::min<int64_t>(n, (int64_t)sms * 8), 256, 0, s, p);
 }
 
 #ifdef SYN_DEBUG

@@ -48,14 +48,6 @@ __device__ __forceinline__ uint2 pack_half4(const float4& x) {
     return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// round half away from zero of x / d: from the rounded reciprocal, whose quotient is off by less
-// than 2^-21 of itself (< 2^-14 below 128), and by a division where that could cross a tie
-__device__ __forceinline__ float q8_code(float x, float d, float inv) {
-    float y = fabsf(x) * inv;
-    if (fabsf(y - floorf(y) - 0.5f) < 6.2e-5f) y = fabsf(x) / d;
-    return copysignf(fminf(floorf(y + 0.5f), 127.0f), x);  // (the stored scale can lie below amax/127)
-}
-
 // 4 values of a Q8_0 block held by 8 neighbouring lanes: codes (packed) and the block's scale.
 // A block with a non-finite value, or whose scale overflows fp16, gets a NaN scale: it reads
 // back as NaN, never as something finite.
@@ -69,10 +61,25 @@ __device__ __forceinline__ uint32_t q8_codes(const float4& x, unsigned short& sc
     const bool fine = df < INFINITY;
     scale = fine ? __half_as_ushort(d) : (unsigned short)0x7FFF;
     if (!fine || df == 0.0f) return 0u;
-    const float inv = 1.0f / df;
-    const int c0 = (int)q8_code(x.x, df, inv), c1 = (int)q8_code(x.y, df, inv), c2 = (int)q8_code(x.z, df, inv),
-              c3 = (int)q8_code(x.w, df, inv);
-    return (uint32_t)(c0 & 255) | (uint32_t)(c1 & 255) << 8 | (uint32_t)(c2 & 255) << 16 | (uint32_t)(c3 & 255) << 24;
+    // The code is x / d rounded half away from zero.  x times the reciprocal is off by less than 2^-21
+    // of itself (2^-14 below 128): nearest-even rounding of it, by adding 1.5 * 2^23, gives that
+    // code unless it lies that near a tie; then the four are divided.
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(df));
+    constexpr float BIAS = 12582912.0f;
+    float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
+    float far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; i++) far = fmaxf(far, fabsf(y[i] - ((y[i] + BIAS) - BIAS)));
+    if (far > 0.5f - 6.2e-5f) {
+        const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) y[i] = copysignf(floorf(fabsf(v[i]) / df + 0.5f), v[i]);
+    }
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) c[i] = __float_as_uint(fminf(fmaxf(y[i], -127.0f), 127.0f) + BIAS);  // (the stored scale can lie below amax/127)
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }
 
 struct AppendSmem {

@@ -222,7 +222,7 @@ int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int* count;
     float* part;
-    rc = scratch_for(s, sms, syn::prefill_part_floats(c.dim, sms), &count, &part);
+    rc = scratch_for(s, sms + 2, syn::prefill_part_floats(c.dim, sms), &count, &part);
     if (rc) return rc;
     int launches = 0;
     rc = check_cuda(syn::launch_attn_prefill(c, a, n_seq, n_tok, q, starts, pages, max_pages, lens, out, part, count,

@@ -4,9 +4,11 @@
 //   x_j = log2(e) * (cap*tanh(scale*q.k_j/cap) - slope*|p - j|),  p_j = 2^(x_j - m),
 //   out = sum_j p_j v_j / sum_j p_j  over the keys the query sees, m a running maximum.
 //
-// One CTA per item: 128 or 256 rows of (new token, query head of one kv head), the heads of a
-// token next to each other, so that all the heads of a kv head share the cached rows; the item's
-// keys come in tiles of BN.  Warp roles:
+// An item is 128 or 256 rows of (new token, query head of one kv head), the heads of a token next to
+// each other, so that all the heads of a kv head share the cached rows; its keys come in tiles of
+// BN.  One persistent CTA per SM takes items until none is left, the longest first.  Warp roles:
+//   schedule one warp: takes the next item (a counter), works out what it needs, an item ahead of the
+//            others, so that loads and products of an item begin while the one before is written;
 //   softmax  4 warps per 128 rows, a thread per row: S from tensor memory, the row's maximum, p in
 //            fp16 back into the columns of S, the sum in fp32; O is rescaled in tensor memory when
 //            a row's maximum has grown by more than 2^8 (p stays below 2^14 in fp16: rarely);
@@ -51,7 +53,8 @@ struct PrefillParams {
     const int32_t* prefix;
     const int32_t* first;
     float* part;
-    int* count;
+    int* count;  // per item, zero between calls
+    int* turns;  // [0] items taken past the CTAs' first ones, [1] CTAs done; zero between calls
     int* err;
     float scale, cap;
     int n_seq, n_tok, g, window, out_f16, sms, split;
@@ -73,17 +76,18 @@ struct PreShape {
     static constexpr int RING = QT * Q_TILE;
     static constexpr int RAWS = RING + NS * STAGE;
     static constexpr int BARS = RAWS + NR * RAW;
-    static constexpr int INFO = BARS + (8 * (2 * NS + 2 * NR + 11) + 8 + 15) / 16 * 16;
-    static constexpr int BYTES = INFO + 64 + 4 * (PRE_MAX_SEQ + 1);
+    static constexpr int INFO = BARS + (8 * (2 * NS + 2 * NR + 19) + 8 + 15) / 16 * 16;
+    static constexpr int BYTES = INFO + 64 + 2 * 96 + 4 * (PRE_MAX_SEQ + 1);
     static constexpr int MAX_SPLIT = NS * STAGE / (4 * R);  // parts of an item whose weights fit into the ring
     static constexpr int O_COL = QT == 2 ? 256 : 128;  // S slots below it
     static constexpr int SLOT = QT == 2 ? 128 : 64;    // columns of an S slot
-    // warps: softmax, then MMA, loader and two that idle, then (Q8_0) four that expand
-    static constexpr int MMA_WARP = 4 * QT, LOAD_WARP = MMA_WARP + 1, EXPAND_WARP = MMA_WARP + 4;
+    // warps: softmax, then MMA, loader, scheduler and one that idles, then (Q8_0) four that expand
+    static constexpr int MMA_WARP = 4 * QT, LOAD_WARP = MMA_WARP + 1, PLAN_WARP = MMA_WARP + 2, EXPAND_WARP = MMA_WARP + 4;
+    static constexpr int READERS = MMA_WARP + 2 + (Q8 ? 4 : 0);  // warps that follow the scheduler
     static constexpr int WARPS = MMA_WARP + 4 + (Q8 ? 4 : 0), THREADS = 32 * WARPS;
     // registers a thread of each kind after the hand-over (two row tiles; their sum over the warps is
     // what the launch gives them: 168 each of 12 warps, 128 each of 16)
-    static constexpr int SOFTMAX_REGS = Q8 ? 192 : 208, MMA_REGS = Q8 ? 40 : 88, EXPAND_REGS = 88;
+    static constexpr int SOFTMAX_REGS = Q8 ? 184 : 208, MMA_REGS = Q8 ? 64 : 88, EXPAND_REGS = 80;
     static_assert(QT == 1 || (Q8 ? 8 * SOFTMAX_REGS + 4 * MMA_REGS + 4 * EXPAND_REGS <= 16 * 128
                                  : 8 * SOFTMAX_REGS + 4 * MMA_REGS <= 12 * 168), "more registers than the launch has");
 };
@@ -99,6 +103,16 @@ struct Tiles {
     __device__ __forceinline__ int count() const { return a1 - a0 + b1 - b0; }
     __device__ __forceinline__ int at(int i) const { return i < a1 - a0 ? a0 + i : b0 + (i - (a1 - a0)); }
 };
+
+// What the scheduler tells the other warps of an item.
+struct Item {
+    int nt;      // tiles of this part (0: no row sees a key; -1: no item is left)
+    int t0;      // its first tile
+    int n_split, sp, index;  // parts of the item, this one, the item's number
+    int s, h, row0, rows, n_new, tok0, len, prefix;
+    Tiles tiles;
+};
+static_assert(sizeof(Item) <= 96, "two items' space in shared memory");
 
 // bits of the keys 32w .. 32w+31 of a tile that lie in [lo, hi)
 __device__ __forceinline__ uint32_t span_bits(int lo, int hi, int w) {
@@ -210,18 +224,23 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
     uint64_t* raw_full = q_full + 2;       // [NR] Q8_0: codes and scales have arrived
     uint64_t* raw_empty = raw_full + NR;   // [NR]
     uint64_t* mma_idle = raw_empty + NR;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 1);
+    uint64_t* q_empty = mma_idle + 1;      // [2] the item's last S is complete
+    uint64_t* item_full = q_empty + 2;     // [2]
+    uint64_t* item_empty = item_full + 2;  // [2]
+    uint64_t* join_bar = item_empty + 2;   // the softmax warps, around a join
+    uint64_t* item_want = join_bar + 1;    // the loader has nothing left to load
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_want + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile uint32_t* raw_there = reinterpret_cast<volatile uint32_t*>(smem + L::INFO + 48);  // [NR] boxes that arrived
-    int* info = reinterpret_cast<int*>(smem + L::INFO);  // [0] carry, [1] min first, [2] min low, [3] max end, [4..] sums
-    int* pre = info + 16;                                // [n_seq + 1] items (of one kv head) before each sequence
+    int* info = reinterpret_cast<int*>(smem + L::INFO);  // [0] carry of the scan, [1] the join's verdict
+    volatile uint32_t* raw_there = reinterpret_cast<volatile uint32_t*>(info + 12);  // [NR] pieces that arrived
+    volatile int* item_ints = info + 16;  // [2][24] items
+    int* pre = info + 64;                 // [n_seq + 1] items (of one kv head) before each sequence
 
     // (the shuffle tells the compiler that the warp's index is the same for its lanes)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int dim = p.c.dim, nh = (dim + 63) >> 6;  // 64-value column chunks of a row
 
     // ---- set-up that touches no global memory, ahead of the kernel before this one -----------
-    auto softmax_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(R) : "memory"); };  // the softmax warps alone
     if (tid == 0) {
         for (int i = 0; i < NS; i++) {
             mbar_init(smem_u32(&kv_full[i]), Q8 ? 4 : 1);
@@ -233,59 +252,36 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             mbar_init(smem_u32(&p_half[i]), 4);
             mbar_init(smem_u32(&o_done[i]), 1);
             mbar_init(smem_u32(&q_full[i]), p.q_tma ? 1 : 4);
+            mbar_init(smem_u32(&q_empty[i]), 1);
+            mbar_init(smem_u32(&item_full[i]), 1);
+            mbar_init(smem_u32(&item_empty[i]), L::READERS);
         }
         for (int i = 0; i < NR; i++) {
             mbar_init(smem_u32(&raw_full[i]), 1);
             mbar_init(smem_u32(&raw_empty[i]), 4);
         }
         mbar_init(smem_u32(mma_idle), 1);
+        mbar_init(smem_u32(join_bar), MMA_WARP);
+        mbar_init(smem_u32(item_want), 1);
         *abort_flag = 0;
         info[0] = 0;
-        info[1] = info[2] = INT_MAX;
-        info[3] = 0;
         pre[0] = 0;
         fence_mbar_init();
     }
+    if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_slot), 512);
     griddep_release();
     griddep_wait();
 
-    // ---- this CTA's item -------------------------------------------------------------------
     auto new_tokens = [&](int s) {  // (starts that run backwards or past the call's tokens count as none)
         const int a = p.starts[s], b = p.starts[s + 1];
         return a < 0 || b > p.n_tok ? 0 : max(b - a, 0);
     };
-    const int most_len = (int)min(p.max_pages << p.c.page_shift, (int64_t)INT_MAX - 1024);
-    // Items of all sequences, and the sequence that the item of this CTA belongs to: up to 32
-    // sequences by the lanes of each warp, from one round of loads; more through shared memory.
-    // splits of an item: as many as leave every SM one CTA
-    auto splits_of = [&](int64_t items) { return p.split && items > 0 && items < p.sms ? min((int)(p.sms / items), L::MAX_SPLIT) : 1; };
-    int n_tiles_q, s, before_s, n_new, tok0, len, prefix;
-    if (p.n_seq <= 32) {
-        const int mine = min(lane, p.n_seq - 1);
-        const int my_new = lane < p.n_seq ? new_tokens(mine) : 0, my_start = p.starts[mine], my_len = p.lens[mine];
-        const int my_prefix = p.prefix ? p.prefix[mine] : 0;
-        const int x = (int)(((int64_t)my_new * p.g + R - 1) / R);
-        int sum = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
-        }
-        n_tiles_q = __shfl_sync(0xffffffffu, sum, 31);
-        const int64_t items = (int64_t)n_tiles_q * p.c.n_kv, b = (int64_t)blockIdx.x / splits_of(items);
-        if (b >= items) return;
-        const int qt = n_tiles_q - 1 - (int)(b / p.c.n_kv);
-        s = __ffs(__ballot_sync(0xffffffffu, sum > qt)) - 1;
-        before_s = __shfl_sync(0xffffffffu, sum - x, s);
-        n_new = __shfl_sync(0xffffffffu, my_new, s);
-        tok0 = __shfl_sync(0xffffffffu, my_start, s);
-        len = __shfl_sync(0xffffffffu, my_len, s);
-        prefix = __shfl_sync(0xffffffffu, my_prefix, s);
-    } else {
+    auto items_of = [&](int n_new) { return (int)(((int64_t)n_new * p.g + R - 1) / R); };
+    if (p.n_seq > 32) {  // (up to 32 sequences are the scheduler's lanes)
         __syncthreads();
         for (int base = 0; base < p.n_seq; base += THREADS) {
             const int sq = base + tid;
-            int x = sq < p.n_seq ? (int)(((int64_t)new_tokens(sq) * p.g + R - 1) / R) : 0;
+            int x = sq < p.n_seq ? items_of(new_tokens(sq)) : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -301,128 +297,95 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             if (tid == THREADS - 1) info[0] = before + x;
             __syncthreads();
         }
-        n_tiles_q = pre[p.n_seq];
-        const int64_t items = (int64_t)n_tiles_q * p.c.n_kv, b = (int64_t)blockIdx.x / splits_of(items);
-        if (b >= items) return;
-        const int qt = n_tiles_q - 1 - (int)(b / p.c.n_kv);
-        int lo = 0, hi = p.n_seq - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (pre[mid + 1] > qt) hi = mid;
-            else lo = mid + 1;
-        }
-        s = lo;
-        before_s = pre[s];
-        n_new = new_tokens(s);
-        tok0 = p.starts[s];
-        len = p.lens[s];
-        prefix = p.prefix ? p.prefix[s] : 0;
     }
-    len = min(max(len, 0), most_len);
-    const int max_split = splits_of((int64_t)n_tiles_q * p.c.n_kv);
-    const int64_t b = (int64_t)blockIdx.x / max_split;
-    const int sp = (int)(blockIdx.x - b * max_split);
-    // the last tiles of a sequence see the most keys: they go first
-    const int qtile = n_tiles_q - 1 - (int)(b / p.c.n_kv), h = (int)(b % p.c.n_kv);
-    const int row0 = (qtile - before_s) * R;  // first row of the item among its sequence's
-    const int rows = (int)min((int64_t)R, (int64_t)n_new * p.g - row0);
-    const int32_t* table = p.pages + (int64_t)s * p.max_pages;
-
-    // ---- what this thread's row sees, and the keys that some row sees -----------------------
-    Visible vis;
-    vis.first = vis.pre = vis.low = vis.end = 0;
-    int pos = 0, my_tok = 0, my_head = 0;
-    const bool row_ok = tid < rows;
-    if (tid < R && row_ok) {
-        const int t = (row0 + tid) / p.g;
-        my_head = h * p.g + (row0 + tid - t * p.g);
-        my_tok = tok0 + t;
-        pos = len - n_new + t;
-        vis = visible_of(len, pos, p.first ? p.first[my_tok] : 0, prefix, p.window);
-    }
-    const int pre_end = min(max(prefix, 0), len);
-    // [mf, prefix) then [ml, me): every key that some row sees lies in one of them
-    int mf, ml, me;
-    if (p.first) {
-        mf = ml = INT_MAX;
-        me = 0;
-        if (row_ok && tid < R && (vis.pre > vis.first || vis.end > vis.low)) {
-            mf = vis.pre > vis.first ? vis.first : vis.low;
-            ml = vis.end > vis.low ? vis.low : vis.pre;
-            me = max(vis.end, vis.pre);
-        }
-        if (p.n_seq <= 32) __syncthreads();  // (info is set)
-        if (tid < R) {
-            mf = __reduce_min_sync(0xffffffffu, mf);
-            ml = __reduce_min_sync(0xffffffffu, ml);
-            me = __reduce_max_sync(0xffffffffu, me);
-            if (lane == 0) {
-                atomicMin(&info[1], mf);
-                atomicMin(&info[2], ml);
-                atomicMax(&info[3], me);
-            }
-        }
-        __syncthreads();
-        mf = info[1];
-        ml = info[2];
-        me = info[3];
-    } else {  // positions ascend: the item's first and last token tell
-        const int p_lo = len - n_new + row0 / p.g, p_hi = len - n_new + (row0 + rows - 1) / p.g;
-        if (p_hi >= 0) {
-            ml = p.window > 0 ? max(0, max(p_lo, 0) - p.window + 1) : 0;
-            mf = pre_end > 0 ? 0 : ml;
-            me = max(min(p_hi + 1, len), pre_end);
-        } else {
-            ml = pre_end;
-            mf = 0;
-            me = pre_end;
-        }
-    }
-    Tiles tiles;
-    tiles.a0 = tiles.a1 = tiles.b0 = tiles.b1 = 0;
-    if (me > 0) {
-        tiles.b0 = ml / BN;
-        tiles.b1 = me > ml ? (me + BN - 1) / BN : tiles.b0;
-        tiles.a0 = tiles.a1 = mf / BN;
-        const int ae = min(pre_end, ml);
-        if (ae > mf) tiles.a1 = (ae + BN - 1) / BN;
-        if (tiles.b1 > tiles.b0) tiles.a1 = max(tiles.a0, min(tiles.a1, tiles.b0));
-    }
-    const int all = tiles.count();
-    const int n_split = min(max_split, max(1, all / 2));  // at least two tiles each
-    if (sp >= n_split) return;
-    const int t0 = (int)((int64_t)all * sp / n_split), t1 = (int)((int64_t)all * (sp + 1) / n_split);
-    const int nt = t1 - t0;
-    if (nt == 0) {  // (then the item is not split) no row sees a key
-        const int64_t n = (int64_t)rows * dim;
-        for (int64_t i = tid; i < n; i += THREADS) {
-            const int r = (int)(i / dim), t = (row0 + r) / p.g;
-            store_out(p, (int64_t)(tok0 + t) * p.out_stride + (int64_t)(h * p.g + row0 + r - t * p.g) * dim + (i - (int64_t)r * dim), 0.0f);
-        }
-        return;
-    }
-    const int q_act = QT == 2 && rows <= 128 ? 1 : QT;  // 128-row tiles in use
-
-    if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    float* part = p.part + (int64_t)blockIdx.x * R * (D + 2);  // [D][R] values, [R] maxima, [R] sums
+
+    // the next item, for the warps that follow the scheduler; false: none is left, or a wait gave up
+    int n_items = 0;
+    auto next_item = [&](Item& it) {
+        const int slot = n_items & 1;
+        if (!mbar_wait_poll(smem_u32(&item_full[slot]), (n_items >> 1) & 1, p.err, abort_flag)) return false;
+        volatile int* w = item_ints + 24 * slot;
+        it.nt = w[0];
+        it.t0 = w[1];
+        it.n_split = w[2];
+        it.sp = w[3];
+        it.index = w[4];
+        it.s = w[5];
+        it.h = w[6];
+        it.row0 = w[7];
+        it.rows = w[8];
+        it.n_new = w[9];
+        it.tok0 = w[10];
+        it.len = w[11];
+        it.prefix = w[12];
+        it.tiles.a0 = w[13];
+        it.tiles.a1 = w[14];
+        it.tiles.b0 = w[15];
+        it.tiles.b1 = w[16];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&item_empty[slot]));
+        n_items++;
+        return it.nt >= 0;
+    };
+    auto tiles_in_use = [&](const Item& it) { return QT == 2 && it.rows <= 128 ? 1 : QT; };  // 128-row tiles
 
     // The ring's order: K of the first tile, then (two row tiles) V and the next K, or (one) the
-    // next K and V.  Piece i of 2*nt: is it V, and of which tile.
-    auto piece_v = [&](int i) { return QT == 2 ? (i & 1) : i == 2 * nt - 1 || (i > 0 && (i & 1) == 0); };
-    auto piece_tile = [&](int i) { return QT == 2 ? i >> 1 : i == 2 * nt - 1 ? nt - 1 : i == 0 ? 0 : (i & 1) ? (i + 1) >> 1 : (i >> 1) - 1; };
+    // next K and V.  Piece i of an item's 2*nt: is it V, and of which tile.
+    auto piece_v = [&](int i, int nt) { return QT == 2 ? (i & 1) : i == 2 * nt - 1 || (i > 0 && (i & 1) == 0); };
+    auto piece_tile = [&](int i, int nt) { return QT == 2 ? i >> 1 : i == 2 * nt - 1 ? nt - 1 : i == 0 ? 0 : (i & 1) ? (i + 1) >> 1 : (i >> 1) - 1; };
 
     if (warp < MMA_WARP) {
         // ------------------------------------ softmax ------------------------------------------
         if (QT == 2) take_registers<L::SOFTMAX_REGS>();
         const int qt = warp >> 2;
         const int r = tid;  // row of the item
-        if (qt < q_act) {
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t o_base = lane_base + L::O_COL + qt * D;
+        const float c_log2 = p.scale * 1.4426950408889634f;
+        const float cap_log2 = p.cap * 1.4426950408889634f;
+        const float to_cap = p.cap > 0.0f ? p.scale / p.cap : 0.0f, to_cap2 = 2.0f * 1.4426950408889634f * to_cap;
+        int done = 0, q_turn = 0, joins = 0;  // tiles and Q tiles of this row tile, syncs of the softmax warps so far
+        auto softmax_sync = [&]() {  // (bounded, as every wait: a warp may have given up)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(join_bar));
+            return mbar_wait_poll(smem_u32(join_bar), joins++ & 1, p.err, abort_flag);
+        };
+        int owed = -1;  // the split item whose counter this CTA has not added to yet
+        auto count_part = [&](const Item& it, int index) {  // true: this was its last part
+            const int before = atomicAdd(&p.count[index], 1);
+            if (before == it.n_split - 1) p.count[index] = 0;  // ready for the next call
+            return before == it.n_split - 1;
+        };
+        Item it{};
+        while (next_item(it)) {
+            const bool row_ok = tid < it.rows;
+            Visible vis;
+            vis.first = vis.pre = vis.low = vis.end = 0;
+            int pos = 0, my_tok = 0, my_head = 0;
+            if (row_ok) {
+                const int t = (it.row0 + tid) / p.g;
+                my_head = it.h * p.g + (it.row0 + tid - t * p.g);
+                my_tok = it.tok0 + t;
+                pos = it.len - it.n_new + t;
+                vis = visible_of(it.len, pos, p.first ? p.first[my_tok] : 0, it.prefix, p.window);
+            }
+            const int64_t out0 = (int64_t)my_tok * p.out_stride + (int64_t)my_head * dim;
+            if (it.nt == 0) {  // no row of the item sees a key
+                if (row_ok)
+                    for (int e = 0; e < dim; e++) store_out(p, out0 + e, 0.0f);
+                continue;
+            }
+            if (qt >= tiles_in_use(it) && it.n_split == 1) continue;
+            float* part = p.part + (int64_t)blockIdx.x * R * (D + 2);  // [D][R] values, [R] maxima, [R] sums
+            if (it.n_split > 1) owed = it.index;
+            if (qt < tiles_in_use(it)) {
             if (!p.q_tma) {
                 // this thread's Q row into shared memory, 16-byte piece j of chunk c at j ^ (row % 8)
+                if (!mbar_wait_poll(smem_u32(&q_empty[qt]), (q_turn & 1) ^ 1, p.err, abort_flag)) break;
                 uint8_t* qs = smem + L::Q + qt * L::Q_TILE + (tid & 127) * 128;
                 const uint4* qrow = reinterpret_cast<const uint4*>(p.q + (int64_t)my_tok * p.q_stride + (int64_t)my_head * dim);
 #pragma unroll
@@ -436,23 +399,18 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&q_full[qt]));
+                q_turn++;
             }
-
-            const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-            const uint32_t o_base = lane_base + L::O_COL + qt * D;
-            const float c_log2 = p.scale * 1.4426950408889634f;
             const float slope = MOD && p.slopes && row_ok ? p.slopes[my_head] * 1.4426950408889634f : 0.0f;
-            const float cap_log2 = p.cap * 1.4426950408889634f;
-            const float to_cap = p.cap > 0.0f ? p.scale / p.cap : 0.0f, to_cap2 = 2.0f * 1.4426950408889634f * to_cap;
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
-            for (int i = 0; i < nt; i++) {
-                const int slot = QT == 2 ? qt : i & 1;
-                const uint32_t phase = QT == 2 ? i & 1 : (i >> 1) & 1;
+            for (int i = 0; i < it.nt; i++, done++) {
+                const int slot = QT == 2 ? qt : done & 1;
+                const uint32_t phase = QT == 2 ? done & 1 : (done >> 1) & 1;
                 if (!mbar_wait_poll(smem_u32(&s_full[slot]), phase, p.err, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t s_base = lane_base + slot * L::SLOT;
-                const int j0 = tiles.at(t0 + i) * BN;
+                const int j0 = it.tiles.at(it.t0 + i) * BN;
                 const bool full = !row_ok || (j0 >= vis.low && j0 + BN <= vis.end) || (j0 >= vis.first && j0 + BN <= vis.pre);
                 const bool masked = !__all_sync(0xffffffffu, full);  // (the same for the warp)
                 uint32_t v[BN];  // the row's scores
@@ -500,12 +458,30 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                         }
                     } else {
 #pragma unroll
-                        for (int c = 0; c < BN; c++) v[c] = __float_as_uint(__uint_as_float(v[c]) * c_log2);
+                        for (int c = 0; c < BN; c += 2) {
+                            const float2 x = unpack2(mul2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), pack2(c_log2, c_log2)));
+                            v[c] = __float_as_uint(x.x);
+                            v[c + 1] = __float_as_uint(x.y);
+                        }
                     }
                     if (p.slopes) {
                         const float far = (float)(pos - j0);
+                        if (!p.prefix) {
+                            // no key after the query is seen: the distance is far - c, two scores at a time (c counts
+                            // in whole numbers, exactly)
+                            uint64_t c2 = pack2(0.0f, 1.0f);
+                            const uint64_t two2 = pack2(2.0f, 2.0f), s2 = pack2(slope, slope), f2 = pack2(-slope * far, -slope * far);
 #pragma unroll
-                        for (int c = 0; c < BN; c++) v[c] = __float_as_uint(fmaf(-slope, fabsf(far - (float)c), __uint_as_float(v[c])));
+                            for (int c = 0; c < BN; c += 2) {
+                                const float2 x = unpack2(add2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), fma2(c2, s2, f2)));
+                                v[c] = __float_as_uint(x.x);
+                                v[c + 1] = __float_as_uint(x.y);
+                                c2 = add2(c2, two2);
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < BN; c++) v[c] = __float_as_uint(fmaf(-slope, fabsf(far - (float)c), __uint_as_float(v[c])));
+                        }
                     }
                 }
                 if (masked) {
@@ -535,7 +511,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 }
                 if (i > 0 && __any_sync(0xffffffffu, grow)) {
                     // O holds the tiles before: wait for the last product into it, then scale
-                    if (!mbar_wait_poll(smem_u32(&o_done[qt]), (i - 1) & 1, p.err, abort_flag)) { ok = false; break; }
+                    if (!mbar_wait_poll(smem_u32(&o_done[qt]), (done - 1) & 1, p.err, abort_flag)) { ok = false; break; }
                     tc_fence_after();
                     for (int c = 0; c < dim; c += 16) {
                         uint32_t o[16];
@@ -578,65 +554,45 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             }
             // (one row tile: S of a tile is issued before the product of the one before, so the last
             // two products may both be outstanding, and a parity tells only neighbours apart)
-            if (QT == 1 && nt > 1) ok = ok && mbar_wait_poll(smem_u32(&o_done[qt]), (nt - 2) & 1, p.err, abort_flag);
-            if (ok && mbar_wait_poll(smem_u32(&o_done[qt]), (nt - 1) & 1, p.err, abort_flag)) {
-                tc_fence_after();
+            if (QT == 1 && it.nt > 1) ok = ok && mbar_wait_poll(smem_u32(&o_done[qt]), (done - 2) & 1, p.err, abort_flag);
+            if (!ok || !mbar_wait_poll(smem_u32(&o_done[qt]), (done - 1) & 1, p.err, abort_flag)) break;
+            tc_fence_after();
+            {
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 uint64_t odd2 = 0;  // 0 times every sum: NaN where one is not finite
-                const int64_t out0 = (int64_t)my_tok * p.out_stride + (int64_t)my_head * dim;
-                // The rows go through shared memory (this warp's share of the Q tile, which no product
-                // reads any more), so that the stores are whole rows: 16-byte piece j at j ^ (lane % 8).
-                uint8_t* stage = smem + L::Q + qt * L::Q_TILE + (warp & 3) * (L::Q_TILE / 4);
-                const int per = p.out_f16 ? D : D / 2;  // values of a row that its 2 D bytes hold
-                const uint32_t live = __ballot_sync(0xffffffffu, row_ok);
-                for (int c0 = 0; c0 < dim; c0 += per) {
-                    const int n = min(per, dim - c0);
-                    for (int c = 0; c < n; c += 32) {
-                        uint32_t o[32];
-                        __syncwarp();
-                        TMEM_LD32(o_base + c0 + c, o);
-                        TMEM_LD_WAIT32(o);
+                for (int c = 0; c < dim; c += 32) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    TMEM_LD32(o_base + c, o);
+                    TMEM_LD_WAIT32(o);
 #pragma unroll
-                        for (int u = 0; u < 32; u += 2) odd2 = fma2(pack2(__uint_as_float(o[u]), __uint_as_float(o[u + 1])), 0, odd2);
-                        if (n_split > 1) {
-                            if (row_ok) {
+                    for (int u = 0; u < 32; u += 2) odd2 = fma2(pack2(__uint_as_float(o[u]), __uint_as_float(o[u + 1])), 0, odd2);
+                    if (!row_ok) continue;
+                    if (it.n_split > 1) {
 #pragma unroll
-                                for (int u = 0; u < 32; u++) __stcg(part + (int64_t)(c0 + c + u) * R + r, __uint_as_float(o[u]));
+                        for (int u = 0; u < 32; u++) __stcg(part + (int64_t)(c + u) * R + r, __uint_as_float(o[u]));
+                    } else if (p.out_f16) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(p.out) + out0 + c);
+#pragma unroll
+                        for (int u = 0; u < 4; u++) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int x = 0; x < 4; x++) {
+                                const __half2 hh = __floats2half2_rn(__uint_as_float(o[8 * u + 2 * x]) * inv, __uint_as_float(o[8 * u + 2 * x + 1]) * inv);
+                                w[x] = *reinterpret_cast<const uint32_t*>(&hh);
                             }
-                        } else if (p.out_f16) {
-#pragma unroll
-                            for (int u = 0; u < 4; u++) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int x = 0; x < 4; x++) {
-                                    const __half2 hh = __floats2half2_rn(__uint_as_float(o[8 * u + 2 * x]) * inv, __uint_as_float(o[8 * u + 2 * x + 1]) * inv);
-                                    w[x] = *reinterpret_cast<const uint32_t*>(&hh);
-                                }
-                                *reinterpret_cast<uint4*>(stage + lane * (2 * D) + (((c / 8 + u) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int u = 0; u < 8; u++)
-                                *reinterpret_cast<float4*>(stage + lane * (2 * D) + (((c / 4 + u) ^ (lane & 7)) << 4)) =
-                                    make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
-                                                __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
+                            dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + out0 + c);
+#pragma unroll
+                        for (int u = 0; u < 8; u++)
+                            dst[u] = make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
+                                                 __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
                     }
-                    if (n_split > 1) continue;
-                    __syncwarp();
-                    const int esize = p.out_f16 ? 2 : 4, pieces = n * esize / 16;  // of a row
-                    const int rows_at_once = 32 / pieces, sub = lane / pieces, j = lane - sub * pieces;
-#pragma unroll 4
-                    for (int rr = 0; rr < 32; rr += rows_at_once) {
-                        const int row = rr + sub;
-                        const int64_t at = __shfl_sync(0xffffffffu, out0, row & 31);
-                        if (sub < rows_at_once && row < 32 && ((live >> row) & 1))
-                            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (at + c0) * esize + 16 * j) =
-                                *reinterpret_cast<const uint4*>(stage + row * (2 * D) + ((j ^ (row & 7)) << 4));
-                    }
-                    __syncwarp();
                 }
-                if (n_split > 1 && row_ok) {
+                __syncwarp();
+                if (it.n_split > 1 && row_ok) {
                     __stcg(part + (int64_t)D * R + r, m);
                     __stcg(part + (int64_t)(D + 1) * R + r, l);
                 }
@@ -655,31 +611,102 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                     const int wpos = __shfl_sync(0xffffffffu, pos, src), wt = __shfl_sync(0xffffffffu, my_tok, src),
                               wh = __shfl_sync(0xffffffffu, my_head, src);
                     float wm, wl, wo[D / 32];
-                    row_by_hand<D, Q8>(p, table, len, h, p.q + (int64_t)wt * p.q_stride + (int64_t)wh * dim, w, wpos,
-                                       p.slopes ? p.slopes[wh] : 0.0f, tiles, t0, t1, wm, wl, wo);
+                    row_by_hand<D, Q8>(p, p.pages + (int64_t)it.s * p.max_pages, it.len, it.h, p.q + (int64_t)wt * p.q_stride + (int64_t)wh * dim, w, wpos,
+                                       p.slopes ? p.slopes[wh] : 0.0f, it.tiles, it.t0, it.t0 + it.nt, wm, wl, wo);
                     const int wr = (r & ~31) + src;
                     __syncwarp();
 #pragma unroll
                     for (int e = 0; e < D / 32; e++) {
                         if (lane + 32 * e >= dim) continue;
-                        if (n_split > 1) __stcg(part + (int64_t)(lane + 32 * e) * R + wr, wo[e]);
+                        if (it.n_split > 1) __stcg(part + (int64_t)(lane + 32 * e) * R + wr, wo[e]);
                         else store_out(p, (int64_t)wt * p.out_stride + (int64_t)wh * dim + lane + 32 * e, wl == 0.0f ? 0.0f : wo[e] / wl);
                     }
-                    if (n_split > 1 && lane == 0) {
+                    if (it.n_split > 1 && lane == 0) {
                         __stcg(part + (int64_t)D * R + wr, wm);
                         __stcg(part + (int64_t)(D + 1) * R + wr, wl);
                     }
                 }
             }
+            }
+            if (it.n_split == 1) continue;
+            // ---- the last of the item's CTAs joins the partials ------------------------------------
+            __threadfence();
+            if (!softmax_sync()) break;
+            if (tid == 0) info[1] = count_part(it, it.index);
+            owed = -1;
+            if (!softmax_sync()) break;
+            if (!info[1]) continue;
+            __threadfence();
+            const float* base = p.part + (int64_t)(blockIdx.x - it.sp) * R * (D + 2);
+            constexpr int64_t pitch = (int64_t)R * (D + 2);
+            // each row's weights of the parts (the ring is free), then the values: independent loads
+            float* weight = reinterpret_cast<float*>(smem + L::RING);  // [it.n_split][R]
+            if (row_ok) {
+                float mx = -INFINITY, sum = 0.0f;
+                for (int x0 = 0; x0 < it.n_split; x0 += 8) {  // (the last batch repeats the last part's loads)
+                    float pm[8], pl[8];
+#pragma unroll
+                    for (int x = 0; x < 8; x++) {
+                        const float* q = base + min(x0 + x, it.n_split - 1) * pitch + (int64_t)D * R + tid;
+                        pm[x] = __ldcg(q);
+                        pl[x] = __ldcg(q + R);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 8; x++) {
+                        if (x0 + x >= it.n_split) continue;
+                        const float nm = fmaxf(mx, pm[x]), ms = nm == -INFINITY ? 0.0f : nm;
+                        sum = sum * ex2(mx - ms) + pl[x] * ex2(pm[x] - ms);
+                        mx = nm;
+                        weight[(x0 + x) * R + tid] = pm[x];
+                    }
+                }
+                const float ms = mx == -INFINITY ? 0.0f : mx, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                for (int x = 0; x < it.n_split; x++) weight[x * R + tid] = ex2(weight[x * R + tid] - ms) * inv;
+            }
+            if (!softmax_sync()) break;
+            for (int u0 = tid; u0 < it.rows * dim; u0 += 4 * R) {
+                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                int e[4], r[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int u = min(u0 + i * R, it.rows * dim - 1);
+                    e[i] = u / it.rows;
+                    r[i] = u - e[i] * it.rows;
+                }
+                for (int x0 = 0; x0 < it.n_split; x0 += 4) {
+                    float po[4][4];
+#pragma unroll
+                    for (int x = 0; x < 4; x++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) po[x][i] = __ldcg(base + min(x0 + x, it.n_split - 1) * pitch + (int64_t)e[i] * R + r[i]);
+#pragma unroll
+                    for (int x = 0; x < 4; x++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            if (x0 + x < it.n_split) acc[i] = fmaf(po[x][i], weight[(x0 + x) * R + r[i]], acc[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    if (u0 + i * R >= it.rows * dim) continue;
+                    const int t = (it.row0 + r[i]) / p.g;
+                    store_out(p, (int64_t)(it.tok0 + t) * p.out_stride + (int64_t)(it.h * p.g + it.row0 + r[i] - t * p.g) * dim + e[i], acc[i]);
+                }
+            }
         }
+        // (after a wait that gave up: the counters of the calls to come start from zero all the same)
+        if (tid == 0 && owed >= 0) count_part(it, owed);
     } else if (warp < EXPAND_WARP) {
       if (QT == 2) give_registers<L::MMA_REGS>();
       if (warp == MMA_WARP) {
         // ------------------------------------ MMA ----------------------------------------------
-        int rc = 0;  // ring pieces taken
+        int rc = 0;                           // ring pieces taken so far
+        int done[2] = {0, 0}, q_turn[2] = {0, 0};  // tiles and Q tiles of each row tile so far
         bool ok = true;
+        Item it{};
         auto take = [&](int i) {  // wait for piece i of the ring
-            return mbar_wait_poll(smem_u32(&kv_full[i % NS]), (i / NS) & 1, p.err, abort_flag);
+            if (!mbar_wait_poll(smem_u32(&kv_full[i % NS]), (i / NS) & 1, p.err, abort_flag)) return false;
+            tc_fence_after();
+            return true;
         };
         const uint32_t lead = elect_lane();
         const uint32_t ring_s = smem_u32(smem + L::RING), q_s = smem_u32(smem + L::Q);
@@ -712,10 +739,10 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         auto release = [&](int i) { mma_commit_lead(lead, smem_u32(&kv_empty[i % NS])); };
         // V rows past the sequence's end hold whatever the page holds: zeros
         auto clean = [&](int i, int tile) {
-            const int j0 = tiles.at(t0 + tile) * BN;
-            if (Q8 || j0 + BN <= len) return;
+            const int j0 = it.tiles.at(it.t0 + tile) * BN;
+            if (Q8 || j0 + BN <= it.len) return;
             uint8_t* va = smem + L::RING + (i % NS) * L::STAGE;
-            const int from = max(len - j0, 0);
+            const int from = max(it.len - j0, 0);
             for (int u = lane; u < (BN - from) * nh * 8; u += 32) {
                 const int c = u / ((BN - from) * 8), x = u - c * (BN - from) * 8;
                 *reinterpret_cast<uint4*>(va + c * (BN * 128) + from * 128 + x * 16) = make_uint4(0, 0, 0, 0);
@@ -723,21 +750,34 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             fence_proxy_async_smem();
             __syncwarp();
         };
-        for (int qt = 0; qt < q_act && ok; qt++) ok = mbar_wait_poll(smem_u32(&q_full[qt]), 0, p.err, abort_flag);
-        if (ok && (ok = take(0))) {
-            tc_fence_after();
-            for (int qt = 0; qt < q_act; qt++) issue_s(qt, QT == 2 ? qt : 0, 0);
-            release(0);
-            rc = 1;
+        while (ok && next_item(it)) {
+            const int nt = it.nt, q_act = tiles_in_use(it);
+            if (nt == 0) continue;
+#pragma unroll
+            for (int qt = 0; qt < QT; qt++)
+                if (qt < q_act) ok = ok && mbar_wait_poll(smem_u32(&q_full[qt]), q_turn[qt]++ & 1, p.err, abort_flag);
+            if (!ok || !(ok = take(rc))) break;
+            // (S of the first tile goes where P of the last item's last tile was: in order behind its product)
+#pragma unroll
+            for (int qt = 0; qt < QT; qt++) {
+                if (qt >= q_act) continue;
+                issue_s(qt, QT == 2 ? qt : done[0] & 1, rc);
+                if (nt == 1) mma_commit_lead(lead, smem_u32(&q_empty[qt]));
+            }
+            release(rc);
+            rc++;
             for (int i = 0; i < nt && ok; i++) {
                 if (QT == 2) {
-                    const int pv = 2 * i + 1, pk = 2 * i + 2;
+                    const int pv = rc, pk = rc + 1;
                     if (!(ok = take(pv))) break;
                     clean(pv, i);
                     if (i + 1 < nt && !(ok = take(pk))) break;
-                    for (int qt = 0; qt < q_act && ok; qt++) {
-                        if (!(ok = issue_o(qt, qt, pv, i & 1, i == 0))) break;
+#pragma unroll
+                    for (int qt = 0; qt < QT; qt++) {
+                        if (qt >= q_act || !ok) continue;
+                        if (!(ok = issue_o(qt, qt, pv, done[qt]++ & 1, i == 0))) continue;
                         if (i + 1 < nt) issue_s(qt, qt, pk);
+                        if (i + 2 == nt) mma_commit_lead(lead, smem_u32(&q_empty[qt]));
                     }
                     if (!ok) break;
                     release(pv);
@@ -746,14 +786,15 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 } else {
                     if (i + 1 < nt) {
                         if (!(ok = take(rc))) break;
-                        tc_fence_after();
-                        issue_s(0, (i + 1) & 1, rc);
+                        issue_s(0, (done[0] + 1) & 1, rc);
+                        if (i + 2 == nt) mma_commit_lead(lead, smem_u32(&q_empty[0]));
                         release(rc);
                         rc++;
                     }
                     if (!(ok = take(rc))) break;
                     clean(rc, i);
-                    if (!(ok = issue_o(0, i & 1, rc, (i >> 1) & 1, i == 0))) break;
+                    if (!(ok = issue_o(0, done[0] & 1, rc, (done[0] >> 1) & 1, i == 0))) break;
+                    done[0]++;
                     release(rc);
                     rc++;
                 }
@@ -765,129 +806,299 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         mbar_drain(smem_u32(mma_idle), 0, p.err);
       } else if (warp == LOAD_WARP) {
         // ------------------------------------ loader -------------------------------------------
-        int i = 0;
-        if (p.q_tma && lane < q_act) {
-            // 128 / g tokens of g heads: the row order of the item.  (Tokens past the call's are zeros;
-            // those of the next sequence are rows that nobody writes.)
-            const uint32_t full = smem_u32(&q_full[lane]), dst = smem_u32(smem + L::Q + lane * L::Q_TILE);
-            mbar_arrive_expect_tx(full, (uint32_t)nh * 128 * 128);
-            for (int c = 0; c < nh; c++)
-                tma_load_3d(dst + c * (128 * 128), &qmap, 64 * c, h * p.g, tok0 + (row0 + 128 * lane) / p.g, full);
-        }
-        __syncwarp();
-#ifdef SYN_TEST_STALL
-        const int n_pieces = 0;  // timeout-test build: no tile is ever loaded, so the waits run out
-#else
-        const int n_pieces = 2 * nt;
-#endif
         const int box = min(BN, 1 << p.c.page_shift), n_box = BN / box;  // rows of a copy; lane l does the l-th
-        for (; i < n_pieces; i++) {
-            const int st = Q8 ? i % max(NR, 1) : i % NS;
-            const uint32_t turn = (uint32_t)(Q8 ? i / max(NR, 1) : i / NS);
-            const bool is_v = piece_v(i);
-            const int j = tiles.at(t0 + piece_tile(i)) * BN + lane * box;
-            int id = -1;  // past the end, or an id outside the pool
-            if (lane < n_box && j < len) {
-                const int x = table[j >> p.c.page_shift];
-                if ((unsigned)x < (unsigned)p.c.n_pages) id = x;
-                else record_error(p.err, SYN_DEVERR_BOUNDS);
-            }
-            if (!mbar_wait_poll(smem_u32(Q8 ? &raw_empty[st] : &kv_empty[st]), (turn & 1) ^ 1, p.err, abort_flag)) break;
-            const int cell = j & ((1 << p.c.page_shift) - 1);
-            if (!Q8) {
-                // a page that is not there becomes the page after the last: the copy fills it with zeros
-                const uint32_t full = smem_u32(&kv_full[st]);
-                if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)nh * BN * 128);
-                __syncwarp();
-                if (lane < n_box && SYN_IN_BOUNDS((lane + 1) * box * 128 + (nh - 1) * BN * 128 <= L::STAGE)) {
-                    const uint32_t dst = smem_u32(smem + L::RING + st * L::STAGE) + lane * box * 128;
-                    for (int c = 0; c < nh; c++)
-                        tma_load_4d(dst + c * (BN * 128), is_v ? &vmap : &kmap, 64 * c, cell, h, id < 0 ? (int)p.c.n_pages : id, full);
-                }
-            } else {
-                // (rows of pages that are not there, or past the end, are zeroed by the expanding warps)
-                const uint32_t full = smem_u32(&raw_full[st]), there = __ballot_sync(0xffffffffu, id >= 0);
-                const uint32_t codes = (uint32_t)(box * dim), scales = codes / 16;
-                if (lane == 0) {
-                    raw_there[st] = there;  // (before the arrival that lets raw_full complete)
-                    mbar_arrive_expect_tx(full, (uint32_t)__popc(there) * (codes + scales));
-                }
-                __syncwarp();
-                if (id >= 0 && SYN_IN_BOUNDS((uint32_t)(lane + 1) * codes <= BN * D && id < p.c.n_pages)) {
-                    const uint32_t dst = smem_u32(smem + L::RAWS + st * L::RAW);
-                    const uint8_t* tile = (is_v ? p.c.v : p.c.k) + (int64_t)id * p.c.page_stride + (int64_t)h * p.c.tile;
-                    bulk_g2s(dst + lane * codes, tile + (int64_t)cell * dim, codes, full);
-                    bulk_g2s(dst + BN * D + lane * scales, tile + ((int64_t)dim << p.c.page_shift) + (int64_t)cell * (dim >> 4), scales, full);
+        int kc = 0, q_turn[2] = {0, 0};  // pieces and Q tiles so far
+        bool ok = true;
+        Item it{};
+        for (bool first = true; ok; first = false) {
+            if (!first && lane == 0) mbar_arrive(smem_u32(item_want));
+            if (!next_item(it)) break;
+            if (it.nt == 0) continue;
+            const int q_act = tiles_in_use(it);
+            if (p.q_tma) {
+                // 128 / g tokens of g heads: the row order of the item.  (Tokens past the call's are zeros;
+                // those of the next sequence are rows that nobody writes.)
+#pragma unroll
+                for (int qt = 0; qt < QT; qt++) {
+                    if (qt >= q_act || !ok) continue;
+                    if (!(ok = mbar_wait_poll(smem_u32(&q_empty[qt]), (q_turn[qt] & 1) ^ 1, p.err, abort_flag))) continue;
+                    q_turn[qt]++;
+                    if (lane == 0) {
+                        const uint32_t full = smem_u32(&q_full[qt]), dst = smem_u32(smem + L::Q + qt * L::Q_TILE);
+                        mbar_arrive_expect_tx(full, (uint32_t)nh * 128 * 128);
+                        for (int c = 0; c < nh; c++)
+                            tma_load_3d(dst + c * (128 * 128), &qmap, 64 * c, it.h * p.g, it.tok0 + (it.row0 + 128 * qt) / p.g, full);
+                    }
+                    __syncwarp();
                 }
             }
-            __syncwarp();
+#ifdef SYN_TEST_STALL
+            const int n_pieces = 0;  // timeout-test build: no tile is ever loaded, so the waits run out
+#else
+            const int n_pieces = 2 * it.nt;
+#endif
+            const int32_t* table = p.pages + (int64_t)it.s * p.max_pages;
+            for (int i = 0; i < n_pieces && ok; i++, kc++) {
+                const int st = Q8 ? kc % max(NR, 1) : kc % NS;
+                const uint32_t turn = (uint32_t)(Q8 ? kc / max(NR, 1) : kc / NS);
+                const bool is_v = piece_v(i, it.nt);
+                const int j = it.tiles.at(it.t0 + piece_tile(i, it.nt)) * BN + lane * box;
+                int id = -1;  // past the end, or an id outside the pool
+                if (lane < n_box && j < it.len) {
+                    const int x = table[j >> p.c.page_shift];
+                    if ((unsigned)x < (unsigned)p.c.n_pages) id = x;
+                    else record_error(p.err, SYN_DEVERR_BOUNDS);
+                }
+                if (!(ok = mbar_wait_poll(smem_u32(Q8 ? &raw_empty[st] : &kv_empty[st]), (turn & 1) ^ 1, p.err, abort_flag))) break;
+                const int cell = j & ((1 << p.c.page_shift) - 1);
+                if (!Q8) {
+                    // a page that is not there becomes the page after the last: the copy fills it with zeros
+                    const uint32_t full = smem_u32(&kv_full[st]);
+                    if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)nh * BN * 128);
+                    __syncwarp();
+                    if (lane < n_box && SYN_IN_BOUNDS((lane + 1) * box * 128 + (nh - 1) * BN * 128 <= L::STAGE)) {
+                        const uint32_t dst = smem_u32(smem + L::RING + st * L::STAGE) + lane * box * 128;
+                        for (int c = 0; c < nh; c++)
+                            tma_load_4d(dst + c * (BN * 128), is_v ? &vmap : &kmap, 64 * c, cell, it.h, id < 0 ? (int)p.c.n_pages : id, full);
+                    }
+                } else {
+                    // (rows of pages that are not there, or past the end, are zeroed by the expanding warps)
+                    const uint32_t full = smem_u32(&raw_full[st]), there = __ballot_sync(0xffffffffu, id >= 0);
+                    const uint32_t codes = (uint32_t)(box * dim), scales = codes / 16;
+                    if (lane == 0) {
+                        raw_there[st] = there;  // (before the arrival that lets raw_full complete)
+                        mbar_arrive_expect_tx(full, (uint32_t)__popc(there) * (codes + scales));
+                    }
+                    __syncwarp();
+                    if (id >= 0 && SYN_IN_BOUNDS((uint32_t)(lane + 1) * codes <= BN * D && id < p.c.n_pages)) {
+                        const uint32_t dst = smem_u32(smem + L::RAWS + st * L::RAW);
+                        const uint8_t* tile = (is_v ? p.c.v : p.c.k) + (int64_t)id * p.c.page_stride + (int64_t)it.h * p.c.tile;
+                        bulk_g2s(dst + lane * codes, tile + (int64_t)cell * dim, codes, full);
+                        bulk_g2s(dst + BN * D + lane * scales, tile + ((int64_t)dim << p.c.page_shift) + (int64_t)cell * (dim >> 4), scales, full);
+                    }
+                }
+                __syncwarp();
+            }
         }
         // the tiles still in flight (issued, not consumed: only after an abort) land first
         if (p.q_tma)
-            for (int u = 0; u < q_act; u++) mbar_drain(smem_u32(&q_full[u]), 0, p.err);
+#pragma unroll
+            for (int qt = 0; qt < QT; qt++)
+                if (q_turn[qt] > 0) mbar_drain(smem_u32(&q_full[qt]), (q_turn[qt] - 1) & 1, p.err);
         if (Q8) {
-            for (int u = max(0, i - NR); u < i; u++) mbar_drain(smem_u32(&raw_full[u % max(NR, 1)]), (u / max(NR, 1)) & 1, p.err);
+            for (int u = max(0, kc - NR); u < kc; u++) mbar_drain(smem_u32(&raw_full[u % max(NR, 1)]), (u / max(NR, 1)) & 1, p.err);
         } else {
-            for (int u = max(0, i - NS); u < i; u++) mbar_drain(smem_u32(&kv_full[u % NS]), (u / NS) & 1, p.err);
+            for (int u = max(0, kc - NS); u < kc; u++) mbar_drain(smem_u32(&kv_full[u % NS]), (u / NS) & 1, p.err);
         }
+      } else if (warp == L::PLAN_WARP) {
+        // ------------------------------------ scheduler ----------------------------------------
+        // up to 32 sequences: a lane each
+        const int mine = min(lane, p.n_seq - 1);
+        int my_new = 0, my_sum = 0;
+        if (p.n_seq <= 32) {
+            my_new = lane < p.n_seq ? new_tokens(mine) : 0;
+            my_sum = items_of(my_new);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, my_sum, o);
+                if (lane >= o) my_sum += y;
+            }
+        }
+        const int n_tiles_q = p.n_seq <= 32 ? __shfl_sync(0xffffffffu, my_sum, 31) : pre[p.n_seq];
+        const int64_t items = (int64_t)n_tiles_q * p.c.n_kv;
+        // parts of an item: as many as leave every SM one
+        const int max_split = p.split && items > 0 && items < p.sms ? min((int)(p.sms / items), L::MAX_SPLIT) : 1;
+        const int64_t total = items * max_split;
+        int64_t w = blockIdx.x;
+        for (int n = 0;;) {
+            Item it{};
+            it.nt = -1;
+            if (w < total) {
+                const int64_t b = w / max_split;
+                it.index = (int)b;
+                it.sp = (int)(w - b * max_split);
+                // the last tiles of a sequence see the most keys: they go first
+                const int qtile = n_tiles_q - 1 - (int)(b / p.c.n_kv);
+                it.h = (int)(b % p.c.n_kv);
+                int before;
+                if (p.n_seq <= 32) {
+                    it.s = __ffs(__ballot_sync(0xffffffffu, my_sum > qtile)) - 1;
+                    before = it.s > 0 ? __shfl_sync(0xffffffffu, my_sum, max(it.s - 1, 0)) : 0;
+                } else {
+                    int lo = 0, hi = p.n_seq - 1;
+                    while (lo < hi) {
+                        const int mid = (lo + hi) >> 1;
+                        if (pre[mid + 1] > qtile) hi = mid;
+                        else lo = mid + 1;
+                    }
+                    it.s = lo;
+                    before = pre[lo];
+                }
+                it.n_new = new_tokens(it.s);
+                it.tok0 = p.starts[it.s];
+                it.len = min(max(p.lens[it.s], 0), (int)min(p.max_pages << p.c.page_shift, (int64_t)INT_MAX - 1024));
+                it.prefix = p.prefix ? p.prefix[it.s] : 0;
+                it.row0 = (qtile - before) * R;
+                it.rows = (int)min((int64_t)R, (int64_t)it.n_new * p.g - it.row0);
+                // [mf, prefix) then [ml, me): every key that some row sees lies in one of them
+                const int pre_end = min(max(it.prefix, 0), it.len), pos0 = it.len - it.n_new;
+                const int tk0 = it.row0 / p.g, tk1 = (it.row0 + it.rows - 1) / p.g;  // first and last token
+                int mf, ml, me;
+                if (p.first) {
+                    mf = ml = INT_MAX;
+                    me = 0;
+                    for (int t = tk0 + lane; t <= tk1; t += 32) {
+                        const Visible v = visible_of(it.len, pos0 + t, p.first[it.tok0 + t], it.prefix, p.window);
+                        if (v.pre > v.first || v.end > v.low) {
+                            mf = min(mf, v.pre > v.first ? v.first : v.low);
+                            ml = min(ml, v.end > v.low ? v.low : v.pre);
+                            me = max(me, max(v.end, v.pre));
+                        }
+                    }
+                    mf = __reduce_min_sync(0xffffffffu, mf);
+                    ml = __reduce_min_sync(0xffffffffu, ml);
+                    me = __reduce_max_sync(0xffffffffu, me);
+                } else if (pos0 + tk1 >= 0) {  // positions ascend: the first and the last token tell
+                    ml = p.window > 0 ? max(0, max(pos0 + tk0, 0) - p.window + 1) : 0;
+                    mf = pre_end > 0 ? 0 : ml;
+                    me = max(min(pos0 + tk1 + 1, it.len), pre_end);
+                } else {
+                    ml = me = pre_end;
+                    mf = 0;
+                }
+                Tiles& tl = it.tiles;
+                tl.a0 = tl.a1 = tl.b0 = tl.b1 = 0;
+                if (me > 0) {
+                    tl.b0 = ml / BN;
+                    tl.b1 = me > ml ? (me + BN - 1) / BN : tl.b0;
+                    tl.a0 = tl.a1 = mf / BN;
+                    const int ae = min(pre_end, ml);
+                    if (ae > mf) tl.a1 = (ae + BN - 1) / BN;
+                    if (tl.b1 > tl.b0) tl.a1 = max(tl.a0, min(tl.a1, tl.b0));
+                }
+                const int all = tl.count();
+                it.n_split = min(max_split, max(1, all / 2));  // at least two tiles each
+                it.t0 = (int)((int64_t)all * min(it.sp, it.n_split) / it.n_split);
+                it.nt = it.sp < it.n_split ? (int)((int64_t)all * (it.sp + 1) / it.n_split) - it.t0 : -2;
+            }
+            if (it.nt != -2) {  // (-2: the item has fewer parts)
+                const int slot = n & 1;
+                if (!mbar_wait_poll(smem_u32(&item_empty[slot]), ((n >> 1) & 1) ^ 1, p.err, abort_flag)) break;
+                if (lane == 0) {
+                    volatile int* o = item_ints + 24 * slot;
+                    o[0] = it.nt;
+                    o[1] = it.t0;
+                    o[2] = it.n_split;
+                    o[3] = it.sp;
+                    o[4] = it.index;
+                    o[5] = it.s;
+                    o[6] = it.h;
+                    o[7] = it.row0;
+                    o[8] = it.rows;
+                    o[9] = it.n_new;
+                    o[10] = it.tok0;
+                    o[11] = it.len;
+                    o[12] = it.prefix;
+                    o[13] = it.tiles.a0;
+                    o[14] = it.tiles.a1;
+                    o[15] = it.tiles.b0;
+                    o[16] = it.tiles.b1;
+                    mbar_arrive(smem_u32(&item_full[slot]));
+                }
+                __syncwarp();
+                n++;
+                if (it.nt == -1) break;
+            }
+            // The next one: the CTAs' first items are their numbers, the rest are counted out, each when the
+            // loader has the one before on its way (taken earlier, the items of a small call would be
+            // dealt before it shows which CTAs are done first: 6 ragged prompts 101 us, not 79)
+            if (it.nt != -2 && !mbar_wait_poll(smem_u32(item_want), (n - 1) & 1, p.err, abort_flag)) break;
+            int taken = 0;
+            if (lane == 0) taken = atomicAdd(&p.turns[0], 1);
+            w = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, taken, 0);
+        }
+        // the last CTA to get here makes the counters ready for the next call
+        if (lane == 0 && atomicAdd(&p.turns[1], 1) == (int)gridDim.x - 1) p.turns[0] = p.turns[1] = 0;
       }
     } else if (Q8) {
         // ------------------------------------ expand (Q8_0) -------------------------------------
         if (QT == 2) give_registers<L::EXPAND_REGS>();
         const int lt = tid - 32 * EXPAND_WARP;
-        // 16 codes at a time: thread lt takes piece x of rows row0_t, row0_t + per_pass, ...
-        const int per_row = dim >> 4, per_pass = 128 / per_row, row0_t = lt / per_row, x = lt - row0_t * per_row;
-        const int flip = (x >> 2) & 1;  // pieces of the two 64-value chunks store their halves in opposite order (banks)
+        // 16 codes at a time.  A thread takes piece x4 of the 64-value chunks of rows lt/4, lt/4 + 32, ...;
+        // neighbouring rows take the chunks in opposite order, so that the 8 lanes that a shared-memory
+        // access serves at once touch all the banks, reading and storing.
+        constexpr int HALVES = D / 64, UNITS = BN / 32 * HALVES;
+        const int x4 = lt & 3, row_t = lt >> 2;
+        const int n_box = BN >> min(p.c.page_shift, BN == 128 ? 7 : 6), box_shift = min(p.c.page_shift, BN == 128 ? 7 : 6);
+        const uint32_t all_there = n_box == 32 ? 0xffffffffu : (1u << n_box) - 1u;
         const __half2 k1152 = __float2half2_rn(1152.0f);
+        int kc = 0;
+        bool ok = true;
+        Item it{};
+        while (ok && next_item(it)) {
 #ifdef SYN_TEST_STALL
-        const int n_pieces = 0;
+            const int n_pieces = 0;
 #else
-        const int n_pieces = 2 * nt;
+            const int n_pieces = 2 * it.nt;
 #endif
-        const int box_shift = min(p.c.page_shift, BN == 128 ? 7 : 6);
-        for (int i = 0; i < n_pieces; i++) {
-            const int rs = i % max(NR, 1), st = i % NS;
-            if (!mbar_wait_poll(smem_u32(&raw_full[rs]), (i / max(NR, 1)) & 1, p.err, abort_flag)) break;
-            if (!mbar_wait_poll(smem_u32(&kv_empty[st]), ((i / NS) & 1) ^ 1, p.err, abort_flag)) break;
-            const int left = len - tiles.at(t0 + piece_tile(i)) * BN;  // rows of the tile that exist
-            const uint32_t there = raw_there[rs];
-            const uint8_t* raw = smem + L::RAWS + rs * L::RAW;
-            uint8_t* dst = smem + L::RING + st * L::STAGE;
-            if (row0_t < per_pass) {
-#pragma unroll 4
-                for (int row = row0_t; row < BN; row += per_pass) {
-                    // a byte c becomes 1024 + c by a permute with 0x64; value = scale * code, the one rounding
-                    // of the expansion (relative 2^-11, like that of p); rows that are not there are zeros
-                    uint4 code = *reinterpret_cast<const uint4*>(raw + row * dim + 16 * x);
-                    uint16_t bits = *reinterpret_cast<const uint16_t*>(raw + BN * D + 2 * (row * (dim >> 5) + (x >> 1)));
-                    if (!(row < left && ((there >> (row >> box_shift)) & 1))) {
-                        code = make_uint4(0, 0, 0, 0);
-                        bits = 0;
-                    }
-                    const __half2 d = __half2half2(__ushort_as_half(bits));
-                    const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
-                    uint32_t w[8];
+            for (int i = 0; i < n_pieces && ok; i++, kc++) {
+                const int rs = kc % max(NR, 1), st = kc % NS;
+                if (!(ok = mbar_wait_poll(smem_u32(&raw_full[rs]), (kc / max(NR, 1)) & 1, p.err, abort_flag))) break;
+                if (!(ok = mbar_wait_poll(smem_u32(&kv_empty[st]), ((kc / NS) & 1) ^ 1, p.err, abort_flag))) break;
+                const int left = it.len - it.tiles.at(it.t0 + piece_tile(i, it.nt)) * BN;  // rows of the tile that exist
+                const uint32_t there = raw_there[rs];
+                const bool whole = left >= BN && there == all_there;
+                const uint8_t* raw = smem + L::RAWS + rs * L::RAW;
+                uint8_t* dst = smem + L::RING + st * L::STAGE + row_t * 128;
+                const int swap = (((2 * x4) ^ (row_t & 7)) << 4);
+                constexpr int BATCH = UNITS < 4 ? UNITS : 4;
 #pragma unroll
-                    for (int y = 0; y < 4; y++) {
-                        const uint32_t z = cw[y] ^ 0x80808080u;
-                        uint32_t lo = __byte_perm(z, 0x64646464u, 0x4140), hi = __byte_perm(z, 0x64646464u, 0x4342);
-                        const __half2 hl = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&lo), k1152), d);
-                        const __half2 hh = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&hi), k1152), d);
-                        w[2 * y] = *reinterpret_cast<const uint32_t*>(&hl);
-                        w[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&hh);
+                for (int u0 = 0; u0 < UNITS; u0 += BATCH) {
+                    uint4 code[BATCH];
+                    uint32_t bits[BATCH];
+#pragma unroll
+                    for (int u = 0; u < BATCH; u++) {  // (all loads ahead of the stores, which the compiler cannot tell apart)
+                        const int hb = (u0 + u) % HALVES, ru = (u0 + u) / HALVES;
+                        const int half = HALVES > 1 ? hb ^ (row_t & 1) : 0, x = x4 + 4 * half, row = row_t + 32 * ru;
+                        code[u] = make_uint4(0, 0, 0, 0);
+                        bits[u] = 0;
+                        if (16 * x < dim && (whole || (row < left && ((there >> (row >> box_shift)) & 1)))) {
+                            code[u] = *reinterpret_cast<const uint4*>(raw + row * dim + 16 * x);
+                            bits[u] = *reinterpret_cast<const uint16_t*>(raw + BN * D + 2 * (row * (dim >> 5) + (x >> 1)));
+                        }
                     }
-                    uint8_t* to = dst + (x >> 2) * (BN * 128) + row * 128;
-                    const int c = (2 * x) & 7;
-                    const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
-                    *reinterpret_cast<uint4*>(to + (((c + flip) ^ (row & 7)) << 4)) = flip ? b : a;
-                    *reinterpret_cast<uint4*>(to + (((c + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
+#pragma unroll
+                    for (int u = 0; u < BATCH; u++) {
+                        const int hb = (u0 + u) % HALVES, ru = (u0 + u) / HALVES;
+                        const int half = HALVES > 1 ? hb ^ (row_t & 1) : 0;
+                        // a byte c becomes 1024 + c by a permute with 0x64; value = scale * code, the one rounding
+                        // of the expansion (relative 2^-11, like that of p); rows that are not there are zeros
+                        uint32_t db = __byte_perm(bits[u], 0, 0x1010);
+                        const __half2 d = *reinterpret_cast<__half2*>(&db);
+                        const uint32_t cw[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
+                        uint32_t w[8];
+#pragma unroll
+                        for (int y = 0; y < 4; y++) {
+                            const uint32_t z = cw[y] ^ 0x80808080u;
+                            uint32_t lo = __byte_perm(z, 0x64646464u, 0x4140), hi = __byte_perm(z, 0x64646464u, 0x4342);
+                            const __half2 hl = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&lo), k1152), d);
+                            const __half2 hh = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&hi), k1152), d);
+                            w[2 * y] = *reinterpret_cast<const uint32_t*>(&hl);
+                            w[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&hh);
+                        }
+                        if (16 * (x4 + 4 * half) < dim || half < nh) {
+                            uint8_t* to = dst + half * (BN * 128) + ru * (32 * 128);
+                            *reinterpret_cast<uint4*>(to + swap) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4*>(to + (swap ^ 16)) = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
+                    }
                 }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&kv_full[st]));
-                mbar_arrive(smem_u32(&raw_empty[rs]));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&kv_full[st]));
+                    mbar_arrive(smem_u32(&raw_empty[rs]));
+                }
             }
         }
     }
@@ -897,74 +1108,6 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
     if (warp == MMA_WARP) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
-    }
-    if (n_split == 1 || warp >= MMA_WARP) return;  // (the others have given their registers away)
-    // ---- the last of the item's CTAs joins the partials ------------------------------------
-    const int item = (int)b;
-    __threadfence();
-    softmax_sync();
-    if (tid == 0) {
-        const int before = atomicAdd(&p.count[item], 1);
-        info[0] = before == n_split - 1;
-        if (before == n_split - 1) p.count[item] = 0;  // ready for the next call
-    }
-    softmax_sync();
-    if (!info[0] || *abort_flag) return;
-    __threadfence();
-    const float* base = p.part + (int64_t)(blockIdx.x - sp) * R * (D + 2);
-    constexpr int64_t pitch = (int64_t)R * (D + 2);
-    // each row's weights of the parts (the ring is free), then the values: independent loads
-    float* weight = reinterpret_cast<float*>(smem + L::RING);  // [n_split][R]
-    if (row_ok) {
-        float mx = -INFINITY, sum = 0.0f;
-        for (int x0 = 0; x0 < n_split; x0 += 8) {  // (the last batch repeats the last part's loads)
-            float pm[8], pl[8];
-#pragma unroll
-            for (int x = 0; x < 8; x++) {
-                const float* q = base + min(x0 + x, n_split - 1) * pitch + (int64_t)D * R + tid;
-                pm[x] = __ldcg(q);
-                pl[x] = __ldcg(q + R);
-            }
-#pragma unroll
-            for (int x = 0; x < 8; x++) {
-                if (x0 + x >= n_split) continue;
-                const float nm = fmaxf(mx, pm[x]), ms = nm == -INFINITY ? 0.0f : nm;
-                sum = sum * ex2(mx - ms) + pl[x] * ex2(pm[x] - ms);
-                mx = nm;
-                weight[(x0 + x) * R + tid] = pm[x];
-            }
-        }
-        const float ms = mx == -INFINITY ? 0.0f : mx, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        for (int x = 0; x < n_split; x++) weight[x * R + tid] = ex2(weight[x * R + tid] - ms) * inv;
-    }
-    softmax_sync();
-    for (int u0 = tid; u0 < rows * dim; u0 += 4 * R) {
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        int e[4], r[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int u = min(u0 + i * R, rows * dim - 1);
-            e[i] = u / rows;
-            r[i] = u - e[i] * rows;
-        }
-        for (int x0 = 0; x0 < n_split; x0 += 4) {
-            float po[4][4];
-#pragma unroll
-            for (int x = 0; x < 4; x++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) po[x][i] = __ldcg(base + min(x0 + x, n_split - 1) * pitch + (int64_t)e[i] * R + r[i]);
-#pragma unroll
-            for (int x = 0; x < 4; x++)
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (x0 + x < n_split) acc[i] = fmaf(po[x][i], weight[(x0 + x) * R + r[i]], acc[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            if (u0 + i * R >= rows * dim) continue;
-            const int t = (row0 + r[i]) / p.g;
-            store_out(p, (int64_t)(tok0 + t) * p.out_stride + (int64_t)(h * p.g + row0 + r[i] - t * p.g) * dim + e[i], acc[i]);
-        }
     }
 }
 
@@ -1042,7 +1185,8 @@ cudaError_t launch_attn_prefill(const KvCache& c, const AttnDesc& a, int64_t n_s
     p.slopes = a.slopes;
     p.first = a.first;
     p.part = part;
-    p.count = count;
+    p.count = count + 2;
+    p.turns = count;
     p.err = err;
     p.scale = a.scale;
     p.cap = a.cap;
@@ -1065,14 +1209,14 @@ cudaError_t launch_attn_prefill(const KvCache& c, const AttnDesc& a, int64_t n_s
         p.pages = pages + s0 * max_pages;
         p.lens = lens + s0;
         p.prefix = a.prefix ? a.prefix + s0 : nullptr;
-        // every item has a CTA, and the splits of few items at most one per SM
-        const int64_t items = ((n_tok * p.g + R - 1) / R + p.n_seq) * c.n_kv;
-        const int64_t grid = std::max<int64_t>(items, sms);
-        if (grid > INT_MAX) return cudaErrorInvalidValue;
+        // (more items than this many have a row number past 32 bits; the parts of few items are at most
+        // one per SM)
+        if (((n_tok * p.g + R - 1) / R + p.n_seq) * c.n_kv > INT_MAX) return cudaErrorInvalidValue;
+        const int grid = sms;
         cudaError_t e;
 #define SYN_PRE(D)                                                                                              \
-    (c.q8 ? (mod ? run_prefill<D, true, true>(km, vm, qm, p, (int)grid, s) : run_prefill<D, true, false>(km, vm, qm, p, (int)grid, s)) \
-          : (mod ? run_prefill<D, false, true>(km, vm, qm, p, (int)grid, s) : run_prefill<D, false, false>(km, vm, qm, p, (int)grid, s)))
+    (c.q8 ? (mod ? run_prefill<D, true, true>(km, vm, qm, p, grid, s) : run_prefill<D, true, false>(km, vm, qm, p, grid, s)) \
+          : (mod ? run_prefill<D, false, true>(km, vm, qm, p, grid, s) : run_prefill<D, false, false>(km, vm, qm, p, grid, s)))
         e = D == 64 ? SYN_PRE(64) : D == 128 ? SYN_PRE(128) : SYN_PRE(256);
 #undef SYN_PRE
         if (e != cudaSuccess) return e;

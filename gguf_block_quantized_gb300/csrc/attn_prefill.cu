@@ -87,7 +87,7 @@ struct PreShape {
     static constexpr int WARPS = MMA_WARP + 4 + (Q8 ? 4 : 0), THREADS = 32 * WARPS;
     // registers a thread of each kind after the hand-over (two row tiles; their sum over the warps is
     // what the launch gives them: 168 each of 12 warps, 128 each of 16)
-    static constexpr int SOFTMAX_REGS = Q8 ? 184 : 208, MMA_REGS = Q8 ? 64 : 88, EXPAND_REGS = 80;
+    static constexpr int SOFTMAX_REGS = Q8 ? 136 : 208, MMA_REGS = Q8 ? 112 : 88, EXPAND_REGS = 128;
     static_assert(QT == 1 || (Q8 ? 8 * SOFTMAX_REGS + 4 * MMA_REGS + 4 * EXPAND_REGS <= 16 * 128
                                  : 8 * SOFTMAX_REGS + 4 * MMA_REGS <= 12 * 168), "more registers than the launch has");
 };
@@ -413,94 +413,127 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 const int j0 = it.tiles.at(it.t0 + i) * BN;
                 const bool full = !row_ok || (j0 >= vis.low && j0 + BN <= vis.end) || (j0 >= vis.first && j0 + BN <= vis.pre);
                 const bool masked = !__all_sync(0xffffffffu, full);  // (the same for the warp)
-                uint32_t v[BN];  // the row's scores
+                // Scores of columns c0 .. c0 + N - 1, in powers of two where they are capped or biased, masked.
+                auto finish = [&](auto& v, int c0) {
+                    constexpr int N = sizeof(v) / 4;
+                    if (MOD) {
+                        bool small = false;
+                        if (p.cap > 0.0f) {
+                            float big = 0.0f;
 #pragma unroll
-                for (int c = 0; c < BN; c += 32) TMEM_LD32(s_base + c, (v + c));
-#pragma unroll
-                for (int c = 0; c < BN; c += 32) TMEM_LD_WAIT32((v + c));
-                if (MOD) {
-                    float big = 0.0f;
-                    if (p.cap > 0.0f) {
-#pragma unroll
-                        for (int c = 0; c < BN; c += 2)
-                            big = fmaxf(fmaxf(big, fabsf(__uint_as_float(v[c]))), fabsf(__uint_as_float(v[c + 1])));
-                    }
-                    if (p.cap > 0.0f && __all_sync(0xffffffffu, big * to_cap <= 1.0f)) {
-                        // Scores up to the cap in size: tanh(y) = y times a polynomial in y^2, fitted on [0, 1]
-                        // to 5e-7, five paired instructions a score and none of the two special-function ones
-                        // of the general form, which has to share that unit with the powers (1.5 times the
-                        // time a tile's products take; a tile of 128 x 128 3100 -> 1900 cycles).
-                        const uint64_t k2 = pack2(to_cap, to_cap), s2 = pack2(c_log2, c_log2);
-#pragma unroll
-                        for (int c = 0; c < BN; c += 2) {
-                            const uint64_t x = pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-                            const uint64_t y = mul2(x, k2), z = mul2(y, y);
-                            uint64_t t = fma2(z, pack2(-0.00308041f, -0.00308041f), pack2(0.01677678f, 0.01677678f));
-                            t = fma2(z, t, pack2(-0.05163546f, -0.05163546f));
-                            t = fma2(z, t, pack2(0.13282514f, 0.13282514f));
-                            t = fma2(z, t, pack2(-0.3332918f, -0.3332918f));
-                            t = fma2(z, t, pack2(0.99999944f, 0.99999944f));
-                            const float2 r2 = unpack2(mul2(mul2(x, s2), t));
-                            v[c] = __float_as_uint(r2.x);
-                            v[c + 1] = __float_as_uint(r2.y);
+                            for (int c = 0; c < N; c += 2)
+                                big = fmaxf(fmaxf(big, fabsf(__uint_as_float(v[c]))), fabsf(__uint_as_float(v[c + 1])));
+                            small = __all_sync(0xffffffffu, big * to_cap <= 0.5f);
                         }
-                    } else if (p.cap > 0.0f) {
-                        // cap*tanh(x/cap) = cap - 2 cap/(1 + 2^(2 x log2(e)/cap)), all in powers of two
-                        const uint64_t k2 = pack2(to_cap2, to_cap2), one2 = pack2(1.0f, 1.0f);
-                        const uint64_t m2 = pack2(-2.0f * cap_log2, -2.0f * cap_log2), cap2 = pack2(cap_log2, cap_log2);
+                        if (small) {
+                            // Scores up to half the cap in size: tanh(y) = y times a polynomial in y^2, fitted on
+                            // [0, 1/2] to 3e-7, the scale and the cap folded into its coefficients: five paired
+                            // instructions for two scores, and none of the two special-function ones a score of
+                            // the general form, which has to share that unit with the powers.
+                            const float k = to_cap * to_cap;
+                            const float a0 = 0.999999464f * c_log2, a1 = -0.333263761f * c_log2 * k, a2 = 0.131909124f * c_log2 * k * k,
+                                        a3 = -0.0444185817f * c_log2 * k * k * k;
+                            const uint64_t b0 = pack2(a0, a0), b1 = pack2(a1, a1), b2 = pack2(a2, a2), b3 = pack2(a3, a3);
 #pragma unroll
-                        for (int c = 0; c < BN; c += 2) {
-                            const float2 y = unpack2(mul2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2));
-                            const float2 z = unpack2(add2(pack2(ex2(y.x), ex2(y.y)), one2));
-                            const float2 x = unpack2(fma2(pack2(rcp(z.x), rcp(z.y)), m2, cap2));
-                            v[c] = __float_as_uint(x.x);
-                            v[c + 1] = __float_as_uint(x.y);
-                        }
-                    } else {
+                            for (int c = 0; c < N; c += 2) {
+                                const uint64_t x = pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), z = mul2(x, x);
+                                const float2 r2 = unpack2(mul2(x, fma2(z, fma2(z, fma2(z, b3, b2), b1), b0)));
+                                v[c] = __float_as_uint(r2.x);
+                                v[c + 1] = __float_as_uint(r2.y);
+                            }
+                        } else if (p.cap > 0.0f) {
+                            // cap*tanh(x/cap) = cap - 2 cap/(1 + 2^(2 x log2(e)/cap)), all in powers of two
+                            const uint64_t k2 = pack2(to_cap2, to_cap2), one2 = pack2(1.0f, 1.0f);
+                            const uint64_t m2 = pack2(-2.0f * cap_log2, -2.0f * cap_log2), cap2 = pack2(cap_log2, cap_log2);
 #pragma unroll
-                        for (int c = 0; c < BN; c += 2) {
-                            const float2 x = unpack2(mul2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), pack2(c_log2, c_log2)));
-                            v[c] = __float_as_uint(x.x);
-                            v[c + 1] = __float_as_uint(x.y);
+                            for (int c = 0; c < N; c += 2) {
+                                const float2 y = unpack2(mul2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2));
+                                const float2 z = unpack2(add2(pack2(ex2(y.x), ex2(y.y)), one2));
+                                const float2 x = unpack2(fma2(pack2(rcp(z.x), rcp(z.y)), m2, cap2));
+                                v[c] = __float_as_uint(x.x);
+                                v[c + 1] = __float_as_uint(x.y);
+                            }
                         }
-                    }
-                    if (p.slopes) {
-                        const float far = (float)(pos - j0);
-                        if (!p.prefix) {
-                            // no key after the query is seen: the distance is far - c, two scores at a time (c counts
-                            // in whole numbers, exactly)
+                        // (not capped: still to be scaled; c_log2 or 1)
+                        const float left = p.cap > 0.0f ? 1.0f : c_log2;
+                        if (p.slopes && !p.prefix) {
+                            // no key after the query is seen: the distance is far - c, two scores at a time (c counts in
+                            // whole numbers, exactly)
+                            const float far = (float)(pos - j0 - c0);
                             uint64_t c2 = pack2(0.0f, 1.0f);
                             const uint64_t two2 = pack2(2.0f, 2.0f), s2 = pack2(slope, slope), f2 = pack2(-slope * far, -slope * far);
+                            const uint64_t l2 = pack2(left, left);
 #pragma unroll
-                            for (int c = 0; c < BN; c += 2) {
-                                const float2 x = unpack2(add2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), fma2(c2, s2, f2)));
+                            for (int c = 0; c < N; c += 2) {
+                                const float2 x = unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), l2, fma2(c2, s2, f2)));
                                 v[c] = __float_as_uint(x.x);
                                 v[c + 1] = __float_as_uint(x.y);
                                 c2 = add2(c2, two2);
                             }
-                        } else {
+                        } else if (p.slopes) {
+                            const float far = (float)(pos - j0 - c0);
 #pragma unroll
-                            for (int c = 0; c < BN; c++) v[c] = __float_as_uint(fmaf(-slope, fabsf(far - (float)c), __uint_as_float(v[c])));
+                            for (int c = 0; c < N; c++)
+                                v[c] = __float_as_uint(fmaf(-slope, fabsf(far - (float)c), __uint_as_float(v[c]) * left));
+                        } else if (!(p.cap > 0.0f)) {  // (a scale that is not positive)
+#pragma unroll
+                            for (int c = 0; c < N; c++) v[c] = __float_as_uint(__uint_as_float(v[c]) * left);
                         }
                     }
-                }
-                if (masked) {
+                    if (masked) {
 #pragma unroll
-                    for (int w = 0; w < BN / 32; w++) {
-                        const uint32_t bits = row_ok ? span_bits(vis.low - j0, vis.end - j0, w) | span_bits(vis.first - j0, vis.pre - j0, w)
-                                                     : 0xffffffffu;
+                        for (int w = 0; w < N / 32; w++) {
+                            const int j = j0 + c0;
+                            const uint32_t bits = row_ok ? span_bits(vis.low - j, vis.end - j, w) | span_bits(vis.first - j, vis.pre - j, w)
+                                                         : 0xffffffffu;
 #pragma unroll
-                        for (int c = 0; c < 32; c++)
-                            if (!((bits >> c) & 1)) v[32 * w + c] = 0xff800000u;  // -inf
+                            for (int c = 0; c < 32; c++)
+                                if (!((bits >> c) & 1)) v[32 * w + c] = 0xff800000u;  // -inf
+                        }
                     }
+                };
+                auto largest = [&](auto& v, float mx) {
+                    constexpr int N = sizeof(v) / 4;
+                    float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < N; c += 8)
+#pragma unroll
+                        for (int u = 0; u < 4; u++)
+                            m4[u] = fmaxf(fmaxf(m4[u], __uint_as_float(v[c + 2 * u])), __uint_as_float(v[c + 2 * u + 1]));
+                    return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                };
+                // The scores of an F16 cache's row are held, all BN of them.  Beside the expanding warps (Q8_0) a
+                // thread has too few registers for that: they pass twice, 32 at a time: finished, searched for
+                // the maximum and put back, then fetched again for the powers.  (Spilled, the expanding warps'
+                // codes above all, a tile took 6800 cycles: local memory is outside what shared memory
+                // leaves of L1.)
+                constexpr bool HOLD = !Q8;
+                constexpr int N = BN / 32;
+                uint32_t held[HOLD ? BN : 32], other[32];
+                float mx = -INFINITY;
+                if (HOLD) {
+#pragma unroll
+                    for (int c = 0; c < BN; c += 32) TMEM_LD32(s_base + c, (held + (HOLD ? c : 0)));
+#pragma unroll
+                    for (int c = 0; c < BN; c += 32) TMEM_LD_WAIT32((held + (HOLD ? c : 0)));
+                    finish(held, 0);
+                    mx = largest(held, mx);
+                } else {
+                    TMEM_LD32(s_base, held);
+                    TMEM_LD_WAIT32(held);
+#pragma unroll
+                    for (int w = 0; w < N; w++) {
+                        uint32_t(&v)[32] = reinterpret_cast<uint32_t(&)[32]>(*((w & 1) ? other : held));
+                        uint32_t(&next)[32] = reinterpret_cast<uint32_t(&)[32]>(*((w & 1) ? held : other));
+                        if (w + 1 < N) TMEM_LD32(s_base + 32 * (w + 1), next);
+                        finish(v, 32 * w);
+                        mx = largest(v, mx);
+                        if (w + 1 < N) TMEM_LD_WAIT32(next);
+                        if (MOD || masked) TMEM_ST32(s_base + 32 * w, v);
+                    }
+                    if (MOD || masked) tmem_st_wait();
+                    TMEM_LD32(s_base, held);
                 }
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < BN; c += 8)
-#pragma unroll
-                    for (int u = 0; u < 4; u++)
-                        m4[u] = fmaxf(fmaxf(m4[u], __uint_as_float(v[c + 2 * u])), __uint_as_float(v[c + 2 * u + 1]));
-                float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 if (!MOD) mx *= c_log2;
                 // the reference of the powers follows the maximum when that has grown by 2^8
                 const bool grow = mx > m + PRE_GROW_LOG2;  // (or is the first that is not -inf)
@@ -525,20 +558,24 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 const float ms = (m == -INFINITY ? 0.0f : m) - PRE_P_LOG2;
                 const uint64_t c2 = pack2(MOD ? 1.0f : c_log2, MOD ? 1.0f : c_log2), ms2 = pack2(-ms, -ms);
                 uint64_t sum2[2] = {0, 0};
+                if (!HOLD) TMEM_LD_WAIT32(held);
 #pragma unroll
-                for (int w = 0; w < BN / 32; w++) {
+                for (int w = 0; w < N; w++) {
+                    uint32_t(&v)[32] = reinterpret_cast<uint32_t(&)[32]>(*(HOLD ? held + 32 * (HOLD ? w : 0) : (w & 1) ? other : held));
+                    uint32_t(&next)[32] = reinterpret_cast<uint32_t(&)[32]>(*((w & 1) ? held : other));
+                    if (!HOLD && w + 1 < N) TMEM_LD32(s_base + 32 * (w + 1), next);
                     uint32_t pw[16];
 #pragma unroll
                     for (int u = 0; u < 16; u++) {
-                        const int c = 32 * w + 2 * u;
-                        const float2 x = unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), c2, ms2));
+                        const float2 x = unpack2(fma2(pack2(__uint_as_float(v[2 * u]), __uint_as_float(v[2 * u + 1])), c2, ms2));
                         const float a = ex2(x.x), e = ex2(x.y);
                         sum2[u & 1] = add2(sum2[u & 1], pack2(a, e));
                         const __half2 hh = __floats2half2_rn(a, e);
                         pw[u] = *reinterpret_cast<const uint32_t*>(&hh);
                     }
+                    if (!HOLD && w + 1 < N) TMEM_LD_WAIT32(next);  // (before P overwrites scores)
                     TMEM_ST16(s_base + 16 * w, pw);
-                    if (w == BN / 64 - 1) {  // the product with the first half of the tile's keys can begin
+                    if (w == N / 2 - 1) {  // the product with the first half of the tile's keys can begin
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
@@ -1022,7 +1059,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
       }
     } else if (Q8) {
         // ------------------------------------ expand (Q8_0) -------------------------------------
-        if (QT == 2) give_registers<L::EXPAND_REGS>();
+        // (they keep the 128 registers of the launch)
         const int lt = tid - 32 * EXPAND_WARP;
         // 16 codes at a time.  A thread takes piece x4 of the 64-value chunks of rows lt/4, lt/4 + 32, ...;
         // neighbouring rows take the chunks in opposite order, so that the 8 lanes that a shared-memory

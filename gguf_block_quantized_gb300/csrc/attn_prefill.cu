@@ -1066,7 +1066,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         // access serves at once touch all the banks, reading and storing.
         constexpr int HALVES = D / 64, UNITS = BN / 32 * HALVES;
         const int x4 = lt & 3, row_t = lt >> 2;
-        const int n_box = BN >> min(p.c.page_shift, BN == 128 ? 7 : 6), box_shift = min(p.c.page_shift, BN == 128 ? 7 : 6);
+        const int box_shift = min(p.c.page_shift, BN == 128 ? 7 : 6), n_box = BN >> box_shift;
         const uint32_t all_there = n_box == 32 ? 0xffffffffu : (1u << n_box) - 1u;
         const __half2 k1152 = __float2half2_rn(1152.0f);
         int kc = 0;
@@ -1088,46 +1088,57 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 const uint8_t* raw = smem + L::RAWS + rs * L::RAW;
                 uint8_t* dst = smem + L::RING + st * L::STAGE + row_t * 128;
                 const int swap = (((2 * x4) ^ (row_t & 7)) << 4);
-                constexpr int BATCH = UNITS < 4 ? UNITS : 4;
+                // one piece: 16 codes and their scale to 16 halves.  A byte c becomes 1024 + c by a permute with
+                // 0x64; value = scale * code, the one rounding of the expansion (relative 2^-11, like that of p)
+                auto put = [&](uint8_t* to, const uint4& code, uint32_t bits) {
+                    uint32_t db = __byte_perm(bits, 0, 0x1010);
+                    const __half2 d = *reinterpret_cast<__half2*>(&db);
+                    const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
+                    uint32_t w[8];
 #pragma unroll
-                for (int u0 = 0; u0 < UNITS; u0 += BATCH) {
-                    uint4 code[BATCH];
-                    uint32_t bits[BATCH];
+                    for (int y = 0; y < 4; y++) {
+                        const uint32_t z = cw[y] ^ 0x80808080u;
+                        uint32_t lo = __byte_perm(z, 0x64646464u, 0x4140), hi = __byte_perm(z, 0x64646464u, 0x4342);
+                        const __half2 hl = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&lo), k1152), d);
+                        const __half2 hh = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&hi), k1152), d);
+                        w[2 * y] = *reinterpret_cast<const uint32_t*>(&hl);
+                        w[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&hh);
+                    }
+                    *reinterpret_cast<uint4*>(to + swap) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(to + (swap ^ 16)) = make_uint4(w[4], w[5], w[6], w[7]);
+                };
+                if (whole && dim == D) {  // (no test stands between the loads, all ahead of the stores)
+                    constexpr int BATCH = UNITS < 4 ? UNITS : 4;
+                    const uint8_t* codes = raw + row_t * D + 16 * x4;
+                    const uint8_t* scales = raw + BN * D + row_t * (D / 16) + 2 * (x4 >> 1);
+                    const int odd = row_t & 1;
 #pragma unroll
-                    for (int u = 0; u < BATCH; u++) {  // (all loads ahead of the stores, which the compiler cannot tell apart)
-                        const int hb = (u0 + u) % HALVES, ru = (u0 + u) / HALVES;
-                        const int half = HALVES > 1 ? hb ^ (row_t & 1) : 0, x = x4 + 4 * half, row = row_t + 32 * ru;
-                        code[u] = make_uint4(0, 0, 0, 0);
-                        bits[u] = 0;
-                        if (16 * x < dim && (whole || (row < left && ((there >> (row >> box_shift)) & 1)))) {
-                            code[u] = *reinterpret_cast<const uint4*>(raw + row * dim + 16 * x);
-                            bits[u] = *reinterpret_cast<const uint16_t*>(raw + BN * D + 2 * (row * (dim >> 5) + (x >> 1)));
+                    for (int u0 = 0; u0 < UNITS; u0 += BATCH) {
+                        uint4 code[BATCH];
+                        uint32_t bits[BATCH];
+#pragma unroll
+                        for (int u = 0; u < BATCH; u++) {
+                            const int ru = (u0 + u) / HALVES, half = HALVES > 1 ? ((u0 + u) % HALVES) ^ odd : 0;
+                            code[u] = *reinterpret_cast<const uint4*>(codes + ru * (32 * D) + 64 * half);
+                            bits[u] = *reinterpret_cast<const uint16_t*>(scales + ru * (2 * D) + 4 * half);
+                        }
+#pragma unroll
+                        for (int u = 0; u < BATCH; u++) {
+                            const int ru = (u0 + u) / HALVES, half = HALVES > 1 ? ((u0 + u) % HALVES) ^ odd : 0;
+                            put(dst + half * (BN * 128) + ru * (32 * 128), code[u], bits[u]);
                         }
                     }
-#pragma unroll
-                    for (int u = 0; u < BATCH; u++) {
-                        const int hb = (u0 + u) % HALVES, ru = (u0 + u) / HALVES;
-                        const int half = HALVES > 1 ? hb ^ (row_t & 1) : 0;
-                        // a byte c becomes 1024 + c by a permute with 0x64; value = scale * code, the one rounding
-                        // of the expansion (relative 2^-11, like that of p); rows that are not there are zeros
-                        uint32_t db = __byte_perm(bits[u], 0, 0x1010);
-                        const __half2 d = *reinterpret_cast<__half2*>(&db);
-                        const uint32_t cw[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
-                        uint32_t w[8];
-#pragma unroll
-                        for (int y = 0; y < 4; y++) {
-                            const uint32_t z = cw[y] ^ 0x80808080u;
-                            uint32_t lo = __byte_perm(z, 0x64646464u, 0x4140), hi = __byte_perm(z, 0x64646464u, 0x4342);
-                            const __half2 hl = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&lo), k1152), d);
-                            const __half2 hh = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&hi), k1152), d);
-                            w[2 * y] = *reinterpret_cast<const uint32_t*>(&hl);
-                            w[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&hh);
+                } else {  // rows that are not there are zeros
+                    for (int u = 0; u < UNITS; u++) {
+                        const int half = HALVES > 1 ? (u % HALVES) ^ (row_t & 1) : 0, x = x4 + 4 * half, row = row_t + 32 * (u / HALVES);
+                        if (half >= nh) continue;
+                        uint4 code = make_uint4(0, 0, 0, 0);
+                        uint32_t bits = 0;
+                        if (16 * x < dim && row < left && ((there >> (row >> box_shift)) & 1)) {
+                            code = *reinterpret_cast<const uint4*>(raw + row * dim + 16 * x);
+                            bits = *reinterpret_cast<const uint16_t*>(raw + BN * D + 2 * (row * (dim >> 5) + (x >> 1)));
                         }
-                        if (16 * (x4 + 4 * half) < dim || half < nh) {
-                            uint8_t* to = dst + half * (BN * 128) + ru * (32 * 128);
-                            *reinterpret_cast<uint4*>(to + swap) = make_uint4(w[0], w[1], w[2], w[3]);
-                            *reinterpret_cast<uint4*>(to + (swap ^ 16)) = make_uint4(w[4], w[5], w[6], w[7]);
-                        }
+                        put(dst + half * (BN * 128) + (u / HALVES) * (32 * 128), code, bits);
                     }
                 }
                 fence_proxy_async_smem();

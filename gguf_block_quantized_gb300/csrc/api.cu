@@ -13,6 +13,7 @@
 #include <map>
 #include <vector>
 #include <mutex>
+#include <new>
 #include <utility>
 
 #include "common.cuh"
@@ -85,10 +86,14 @@ struct Workspace {
 std::mutex g_mu;
 std::map<int, DeviceState> g_dev;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
-// the attention's workspaces: counters (zero between calls), then partial results
+// the attention's workspaces: counters (zero between calls), then partial results; and the expanded
+// rows of Q8_0 caches.  What they outgrow is kept until syn_release: a graph captured before may use it.
 struct AttnWorkspace {
     void* ptr = nullptr;
     size_t zeroed = 0, rest = 0;
+    void* rows = nullptr;
+    size_t row_bytes = 0;
+    std::vector<void*> outgrown;
 };
 std::map<std::pair<int, cudaStream_t>, AttnWorkspace> g_attn_ws;
 
@@ -198,7 +203,7 @@ int workspace_for(cudaStream_t s, size_t need, void** out) {
 namespace syn {
 void note_launches(int n) { g_launches += n; }
 
-int attn_workspace(cudaStream_t s, size_t zeroed, size_t rest, size_t* zeroed_at, void** out) {
+int attn_workspace(cudaStream_t s, size_t zeroed, size_t rest, size_t* zeroed_at, void** out) try {
     int dev;
     if (current_device(&dev) != SYN_OK) return SYN_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
@@ -206,24 +211,51 @@ int attn_workspace(cudaStream_t s, size_t zeroed, size_t rest, size_t* zeroed_at
     if (w.zeroed < zeroed || w.rest < rest) {
         const size_t z = std::max(w.zeroed, zeroed), r = std::max(w.rest, rest);
         if (cudaDeviceSynchronize() != cudaSuccess) return SYN_ERR_CUDA;  // (refused while capturing)
-        if (w.ptr) cudaFree(w.ptr);
-        w = AttnWorkspace{};
-        if (cudaMalloc(&w.ptr, z + r) != cudaSuccess) {
+        w.outgrown.reserve(w.outgrown.size() + 1);
+        void* p;
+        if (cudaMalloc(&p, z + r) != cudaSuccess) {
             (void)cudaGetLastError();  // not sticky: keep it out of the next launch check
-            w.ptr = nullptr;
             return SYN_ERR_NOMEM;
         }
-        if (cudaMemset(w.ptr, 0, z) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
-            cudaFree(w.ptr);
-            w.ptr = nullptr;
+        if (cudaMemset(p, 0, z) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+            cudaFree(p);
             return SYN_ERR_CUDA;
         }
+        if (w.ptr) w.outgrown.push_back(w.ptr);
+        w.ptr = p;
         w.zeroed = z;
         w.rest = r;
     }
     *zeroed_at = w.zeroed;
     *out = w.ptr;
     return SYN_OK;
+} catch (const std::bad_alloc&) {
+    return SYN_ERR_NOMEM;
+}
+
+int attn_rows_workspace(cudaStream_t s, size_t bytes, void** out) try {
+    int dev;
+    if (current_device(&dev) != SYN_OK) return SYN_ERR_CUDA;
+    std::lock_guard<std::mutex> lk(g_mu);
+    AttnWorkspace& w = g_attn_ws[{dev, s}];
+    if (w.row_bytes < bytes) {
+        size_t n = size_t(1) << 20;  // powers of two: what is outgrown adds up to less than what is used
+        while (n < bytes) n *= 2;
+        if (cudaDeviceSynchronize() != cudaSuccess) return SYN_ERR_CUDA;  // (refused while capturing)
+        w.outgrown.reserve(w.outgrown.size() + 1);
+        void* p;
+        if (cudaMalloc(&p, n) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SYN_ERR_NOMEM;
+        }
+        if (w.rows) w.outgrown.push_back(w.rows);
+        w.rows = p;
+        w.row_bytes = n;
+    }
+    *out = w.rows;
+    return SYN_OK;
+} catch (const std::bad_alloc&) {
+    return SYN_ERR_NOMEM;
 }
 }  // namespace syn
 
@@ -383,6 +415,8 @@ int syn_release(void) {
     for (auto it = g_attn_ws.begin(); it != g_attn_ws.end();) {
         if (it->first.first == dev) {
             cudaFree(it->second.ptr);
+            cudaFree(it->second.rows);
+            for (void* p : it->second.outgrown) cudaFree(p);
             it = g_attn_ws.erase(it);
         } else {
             ++it;

@@ -74,6 +74,21 @@ int check_cuda(cudaError_t e) { return e == cudaSuccess ? SYN_OK : SYN_ERR_CUDA;
 // The attention scratch of a stream: counters first (zero between calls), then the partials.
 constexpr size_t kCountBytes = size_t(1) << 20;
 
+// A Q8_0 prefill expands its cache to fp16 ahead of the kernel, once, where the kernel would expand each
+// row many times: once for every 256 (token, head) rows of a sequence that see it.  It does so from this
+// many such tiles a sequence on average on, and up to kExpandBytes of scratch a pool.  Measured on GB300,
+// 32 / 8 heads, 8 sequences, all rows new, expanded in the kernel / ahead (us):
+//   slopes, heads of 128:  8 tiles 51.2 / 49.2, 16 tiles 88.1 / 88.1, 64 tiles 530 / 432
+//   slopes, heads of 64:   8 tiles 38.7 / 41.0, 16 tiles 70.7 / 70.3, 64 tiles 424 / 352
+//   none, heads of 128:    8 tiles 38.9 / 44.0, 16 tiles 69.7 / 75.8, 64 tiles 380 / 343
+//   none, heads of 256:    8 tiles 52.3 / 57.9, 16 tiles 107 / 111,   64 tiles 764 / 696
+// one sequence with 512 new rows of 16384 (8 tiles), slopes: heads of 128 147 / 138, of 64 103 / 93; none,
+// heads of 128: 117 / 126.  Fewer tiles: 128 new rows of 4096 each (2 tiles), slopes, heads of 128: 57 / 82.
+int64_t expand_tiles(const syn::KvCache& c, const syn::AttnDesc& a) {
+    return (a.slopes || a.cap > 0.0f) && c.dim <= 128 ? 8 : 32;
+}
+constexpr int64_t kExpandBytes = int64_t(1) << 30;
+
 int scratch_for(cudaStream_t s, int64_t count_words, int64_t part_floats, int** count, float** part) {
     // a multiple of a fixed step, so that a growing batch does not reallocate at every call
     const size_t cb = ((size_t)count_words * 4 + kCountBytes - 1) / kCountBytes * kCountBytes;
@@ -224,8 +239,34 @@ int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_
     float* part;
     rc = scratch_for(s, sms + 2, syn::prefill_part_floats(c.dim, sms), &count, &part);
     if (rc) return rc;
+    const syn::KvCache raw = c;
+    const int32_t* raw_pages = pages;
     int launches = 0;
-    rc = check_cuda(syn::launch_attn_prefill(c, a, n_seq, n_tok, q, starts, pages, max_pages, lens, out, part, count,
+    // bytes of a page, as fp16, in one of the two scratch pools
+    const int64_t page = (int64_t(2) * c.dim * c.n_kv) << c.page_shift;
+    if (c.q8 && !syn::deterministic() && n_tok * (a.n_heads / c.n_kv) >= expand_tiles(c, a) * 256 * n_seq &&
+        n_seq * max_pages <= kExpandBytes / page) {
+        const int64_t pool = n_seq * max_pages * page;
+        void* ws;
+        rc = syn::attn_rows_workspace(s, (size_t)(2 * pool + n_seq * max_pages * 4), &ws);
+        if (rc && rc != SYN_ERR_NOMEM) return rc;
+        if (rc == SYN_OK) {  // (no room: expanded in the kernel)
+            uint8_t* k = static_cast<uint8_t*>(ws);
+            int32_t* table = reinterpret_cast<int32_t*>(k + 2 * pool);
+            rc = check_cuda(syn::launch_kv_expand(c, n_seq, starts, pages, max_pages, lens, a.prefix ? 0 : a.window, k, k + pool,
+                                                  table, sms, s));
+            if (rc) return rc;
+            launches = 1;
+            c.q8 = 0;
+            c.k = k;
+            c.v = k + pool;
+            c.page_stride = page;
+            c.tile = page / c.n_kv;
+            c.n_pages = n_seq * max_pages;
+            pages = table;
+        }
+    }
+    rc = check_cuda(syn::launch_attn_prefill(c, raw, a, n_seq, n_tok, q, starts, pages, raw_pages, max_pages, lens, out, part, count,
                                              !syn::deterministic(), words, sms, &launches, s));
     syn::note_launches(launches);
     return rc;

@@ -42,6 +42,8 @@ constexpr float PRE_GROW_LOG2 = 8.0f; // the maximum's lag
 
 struct PrefillParams {
     KvCache c;
+    KvCache raw;               // where row_by_hand reads: the user's cache and table, which are c and pages
+    const int32_t* raw_pages;  // unless c is the expanded copy of a Q8_0 cache
     const __half* q;
     int64_t q_stride, out_stride;
     void* out;
@@ -169,20 +171,20 @@ __device__ __noinline__ void row_by_hand(const PrefillParams& p, const int32_t* 
         const int j0 = tiles.at(t) * PreShape<D, Q8>::BN;
         for (int j = j0; j < min(j0 + PreShape<D, Q8>::BN, len); j++) {
             if (!vis(j)) continue;
-            const int id = table[j >> p.c.page_shift];
-            if (id < 0 || id >= p.c.n_pages) continue;
-            const int cell = j & ((1 << p.c.page_shift) - 1);
-            const int64_t base = (int64_t)id * p.c.page_stride + (int64_t)h * p.c.tile;
+            const int id = table[j >> p.raw.page_shift];
+            if (id < 0 || id >= p.raw.n_pages) continue;
+            const int cell = j & ((1 << p.raw.page_shift) - 1);
+            const int64_t base = (int64_t)id * p.raw.page_stride + (int64_t)h * p.raw.tile;
             auto value = [&](const uint8_t* pool, int e) {
-                if (!Q8) return __half2float(reinterpret_cast<const __half*>(pool + base)[(int64_t)cell * dim + e]);
+                if (!p.raw.q8) return __half2float(reinterpret_cast<const __half*>(pool + base)[(int64_t)cell * dim + e]);
                 const float d = h2f_bits(*reinterpret_cast<const uint16_t*>(
-                    pool + base + ((int64_t)dim << p.c.page_shift) + 2 * ((int64_t)cell * (dim >> 5) + (e >> 5))));
+                    pool + base + ((int64_t)dim << p.raw.page_shift) + 2 * ((int64_t)cell * (dim >> 5) + (e >> 5))));
                 return d * (float)reinterpret_cast<const int8_t*>(pool + base)[(int64_t)cell * dim + e];
             };
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < D / 32; i++)
-                if (lane + 32 * i < dim) s = fmaf(__half2float(qrow[lane + 32 * i]), value(p.c.k, lane + 32 * i), s);
+                if (lane + 32 * i < dim) s = fmaf(__half2float(qrow[lane + 32 * i]), value(p.raw.k, lane + 32 * i), s);
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
             s *= p.scale;
@@ -194,7 +196,7 @@ __device__ __noinline__ void row_by_hand(const PrefillParams& p, const int32_t* 
             l = fmaf(l, f, w);
 #pragma unroll
             for (int i = 0; i < D / 32; i++)
-                if (lane + 32 * i < dim) o[i] = fmaf(o[i], f, w * value(p.c.v, lane + 32 * i));
+                if (lane + 32 * i < dim) o[i] = fmaf(o[i], f, w * value(p.raw.v, lane + 32 * i));
         }
     }
 }
@@ -338,6 +340,11 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
     auto piece_v = [&](int i, int nt) { return QT == 2 ? (i & 1) : i == 2 * nt - 1 || (i > 0 && (i & 1) == 0); };
     auto piece_tile = [&](int i, int nt) { return QT == 2 ? i >> 1 : i == 2 * nt - 1 ? nt - 1 : i == 0 ? 0 : (i & 1) ? (i + 1) >> 1 : (i >> 1) - 1; };
 
+    // An item's tiles go up, or, with a bias by distance, from the last one down: the largest scores come
+    // first, and O is not rescaled tile after tile (a 4096-token prompt with slopes 154 -> 129 us;
+    // without, going down costs 3 %: rows that see nothing of the last tile start late).
+    auto turn_tile = [&](int i, int nt) { return MOD && p.slopes ? nt - 1 - i : i; };
+
     if (warp < MMA_WARP) {
         // ------------------------------------ softmax ------------------------------------------
         if (QT == 2) take_registers<L::SOFTMAX_REGS>();
@@ -410,7 +417,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 if (!mbar_wait_poll(smem_u32(&s_full[slot]), phase, p.err, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t s_base = lane_base + slot * L::SLOT;
-                const int j0 = it.tiles.at(it.t0 + i) * BN;
+                const int j0 = it.tiles.at(it.t0 + turn_tile(i, it.nt)) * BN;
                 const bool full = !row_ok || (j0 >= vis.low && j0 + BN <= vis.end) || (j0 >= vis.first && j0 + BN <= vis.pre);
                 const bool masked = !__all_sync(0xffffffffu, full);  // (the same for the warp)
                 // Scores of columns c0 .. c0 + N - 1, in powers of two where they are capped or biased, masked.
@@ -648,7 +655,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                     const int wpos = __shfl_sync(0xffffffffu, pos, src), wt = __shfl_sync(0xffffffffu, my_tok, src),
                               wh = __shfl_sync(0xffffffffu, my_head, src);
                     float wm, wl, wo[D / 32];
-                    row_by_hand<D, Q8>(p, p.pages + (int64_t)it.s * p.max_pages, it.len, it.h, p.q + (int64_t)wt * p.q_stride + (int64_t)wh * dim, w, wpos,
+                    row_by_hand<D, Q8>(p, p.raw_pages + (int64_t)it.s * p.max_pages, it.len, it.h, p.q + (int64_t)wt * p.q_stride + (int64_t)wh * dim, w, wpos,
                                        p.slopes ? p.slopes[wh] : 0.0f, it.tiles, it.t0, it.t0 + it.nt, wm, wl, wo);
                     const int wr = (r & ~31) + src;
                     __syncwarp();
@@ -776,7 +783,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         auto release = [&](int i) { mma_commit_lead(lead, smem_u32(&kv_empty[i % NS])); };
         // V rows past the sequence's end hold whatever the page holds: zeros
         auto clean = [&](int i, int tile) {
-            const int j0 = it.tiles.at(it.t0 + tile) * BN;
+            const int j0 = it.tiles.at(it.t0 + turn_tile(tile, it.nt)) * BN;
             if (Q8 || j0 + BN <= it.len) return;
             uint8_t* va = smem + L::RING + (i % NS) * L::STAGE;
             const int from = max(it.len - j0, 0);
@@ -879,7 +886,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 const int st = Q8 ? kc % max(NR, 1) : kc % NS;
                 const uint32_t turn = (uint32_t)(Q8 ? kc / max(NR, 1) : kc / NS);
                 const bool is_v = piece_v(i, it.nt);
-                const int j = it.tiles.at(it.t0 + piece_tile(i, it.nt)) * BN + lane * box;
+                const int j = it.tiles.at(it.t0 + turn_tile(piece_tile(i, it.nt), it.nt)) * BN + lane * box;
                 int id = -1;  // past the end, or an id outside the pool
                 if (lane < n_box && j < it.len) {
                     const int x = table[j >> p.c.page_shift];
@@ -1082,7 +1089,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 const int rs = kc % max(NR, 1), st = kc % NS;
                 if (!(ok = mbar_wait_poll(smem_u32(&raw_full[rs]), (kc / max(NR, 1)) & 1, p.err, abort_flag))) break;
                 if (!(ok = mbar_wait_poll(smem_u32(&kv_empty[st]), ((kc / NS) & 1) ^ 1, p.err, abort_flag))) break;
-                const int left = it.len - it.tiles.at(it.t0 + piece_tile(i, it.nt)) * BN;  // rows of the tile that exist
+                const int left = it.len - it.tiles.at(it.t0 + turn_tile(piece_tile(i, it.nt), it.nt)) * BN;  // rows of the tile that exist
                 const uint32_t there = raw_there[rs];
                 const bool whole = left >= BN && there == all_there;
                 const uint8_t* raw = smem + L::RAWS + rs * L::RAW;
@@ -1159,6 +1166,85 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
     }
 }
 
+// ---- a Q8_0 cache expanded ahead of the kernel --------------------------------------------
+//
+// The rows of every sequence as fp16 values (scale * code, rounded once: the values the expanding warps
+// make), in an F16 cache of scratch: page i of sequence s is page s * max_pages + i of it.  Bound: HBM and
+// L2 (17/16 bytes read and 2 written a value).
+struct ExpandParams {
+    KvCache c;      // Q8_0
+    uint8_t* k;     // scratch pools
+    uint8_t* v;
+    int32_t* table; // [n_seq][max_pages]
+    const int32_t* starts;
+    const int32_t* pages;
+    const int32_t* lens;
+    int64_t max_pages;
+    int n_seq, window;
+};
+
+__global__ void __launch_bounds__(256) k_kv_expand(const ExpandParams p) {
+    const int dim = p.c.dim, page = 1 << p.c.page_shift, per_row = dim >> 4, n = page * per_row;  // 16 codes at a time
+    const __half2 k1152 = __float2half2_rn(1152.0f);
+    griddep_release();
+    griddep_wait();
+    const int64_t units = (int64_t)p.n_seq * p.max_pages * 2 * p.c.n_kv;  // (sequence, page, pool, head)
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t sp = u / (2 * p.c.n_kv);
+        const int hp = (int)(u - sp * 2 * p.c.n_kv), h = hp >> 1, is_v = hp & 1;
+        const int s = (int)(sp / p.max_pages);
+        const int64_t i = sp - s * p.max_pages, row0 = i << p.c.page_shift;
+        const int len = p.lens[s];
+        // (rows ahead of every query's window are not read by anyone)
+        // (but all of a tile that a query's window begins in: no number that was never written meets p = 0)
+        const int64_t low = p.window > 0 ? ((int64_t)len - max(p.starts[s + 1] - p.starts[s], 0) - p.window) & ~int64_t(127) : 0;
+        const int id = p.pages[sp];
+        const bool ok = (unsigned)id < (unsigned)p.c.n_pages;
+        // a page outside the pool is one here too: reported if a query's tile takes it
+        if (hp == 0 && threadIdx.x == 0) p.table[sp] = ok ? (int32_t)sp : -1;
+        if (row0 >= len || row0 + page <= low || !ok) continue;
+        const uint8_t* src = (is_v ? p.c.v : p.c.k) + (int64_t)id * p.c.page_stride + (int64_t)h * p.c.tile;
+        uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + (sp * p.c.n_kv + h) * ((int64_t)n * 32));
+#pragma unroll 2
+        for (int x = threadIdx.x; x < n; x += 256) {
+            const uint4 code = *reinterpret_cast<const uint4*>(src + 16 * (int64_t)x);
+            const uint32_t bits = *reinterpret_cast<const uint16_t*>(src + 16 * (int64_t)n + 2 * (x >> 1));  // (2 pieces a block)
+            uint32_t db = __byte_perm(bits, 0, 0x1010);
+            const __half2 d = *reinterpret_cast<__half2*>(&db);
+            const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
+            uint32_t w[8];
+#pragma unroll
+            for (int y = 0; y < 4; y++) {
+                const uint32_t z = cw[y] ^ 0x80808080u;
+                uint32_t lo = __byte_perm(z, 0x64646464u, 0x4140), hi = __byte_perm(z, 0x64646464u, 0x4342);
+                const __half2 hl = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&lo), k1152), d);
+                const __half2 hh = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&hi), k1152), d);
+                w[2 * y] = *reinterpret_cast<const uint32_t*>(&hl);
+                w[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            dst[2 * x] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[2 * x + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
+}
+
+cudaError_t launch_kv_expand(const KvCache& c, int64_t n_seq, const int32_t* starts, const int32_t* pages, int64_t max_pages,
+                             const int32_t* lens, int window, void* k, void* v, int32_t* table, int sms, cudaStream_t s) {
+    ExpandParams p;
+    p.c = c;
+    p.k = static_cast<uint8_t*>(k);
+    p.v = static_cast<uint8_t*>(v);
+    p.table = table;
+    p.starts = starts;
+    p.pages = pages;
+    p.lens = lens;
+    p.max_pages = max_pages;
+    p.n_seq = (int)n_seq;
+    p.window = window;
+    const int64_t units = n_seq * max_pages * 2 * c.n_kv;
+    return launch_overlapped(k_kv_expand, (int)std::min<int64_t>(units, (int64_t)sms * 8), 256, 0, s, p);
+}
+
 // ---- host side ---------------------------------------------------------------------------
 
 template <int D, bool Q8, bool MOD>
@@ -1189,10 +1275,10 @@ int64_t prefill_part_floats(int dim, int sms) {
     return (int64_t)sms * prefill_rows(dim) * ((dim <= 64 ? 64 : dim <= 128 ? 128 : 256) + 2);
 }
 
-cudaError_t launch_attn_prefill(const KvCache& c, const AttnDesc& a, int64_t n_seq, int64_t n_tok, const void* q,
-                                const int32_t* starts, const int32_t* pages, int64_t max_pages, const int32_t* lens,
-                                void* out, float* part, int* count, bool split, int* err, int sms, int* launches,
-                                cudaStream_t s) {
+cudaError_t launch_attn_prefill(const KvCache& c, const KvCache& raw, const AttnDesc& a, int64_t n_seq, int64_t n_tok,
+                                const void* q, const int32_t* starts, const int32_t* pages, const int32_t* raw_pages,
+                                int64_t max_pages, const int32_t* lens, void* out, float* part, int* count, bool split,
+                                int* err, int sms, int* launches, cudaStream_t s) {
     CUtensorMap km, vm, qm;
     const int D = c.dim <= 64 ? 64 : c.dim <= 128 ? 128 : 256, BN = D <= 128 ? 128 : 64;
     PFN_encodeTiled encode = get_encode();
@@ -1225,6 +1311,7 @@ cudaError_t launch_attn_prefill(const KvCache& c, const AttnDesc& a, int64_t n_s
     }
     PrefillParams p;
     p.c = c;
+    p.raw = raw;
     p.q = static_cast<const __half*>(q);
     p.q_stride = a.q_stride;
     p.out_stride = a.out_stride;
@@ -1255,6 +1342,7 @@ cudaError_t launch_attn_prefill(const KvCache& c, const AttnDesc& a, int64_t n_s
         p.n_seq = (int)std::min<int64_t>(PRE_MAX_SEQ, n_seq - s0);
         p.starts = starts + s0;
         p.pages = pages + s0 * max_pages;
+        p.raw_pages = raw_pages + s0 * max_pages;
         p.lens = lens + s0;
         p.prefix = a.prefix ? a.prefix + s0 : nullptr;
         // (more items than this many have a row number past 32 bits; the parts of few items are at most

@@ -101,11 +101,16 @@ int64_t decode_part_floats(int n_heads, int n_kv, int dim, int sms);
 // Several new tokens of each sequence (packed, starts[s] .. starts[s+1]).  part:
 // prefill_part_floats; count: at least `sms` + 2 words, as above.  split: items may be split
 // between CTAs.
-cudaError_t launch_attn_prefill(const KvCache& c, const AttnDesc& a, int64_t n_seq, int64_t n_tok, const void* q,
-                                const int32_t* starts, const int32_t* pages, int64_t max_pages, const int32_t* lens,
-                                void* out, float* part, int* count, bool split, int* err, int sms, int* launches,
-                                cudaStream_t s);
+cudaError_t launch_attn_prefill(const KvCache& c, const KvCache& raw, const AttnDesc& a, int64_t n_seq, int64_t n_tok,
+                                const void* q, const int32_t* starts, const int32_t* pages, const int32_t* raw_pages,
+                                int64_t max_pages, const int32_t* lens, void* out, float* part, int* count, bool split,
+                                int* err, int sms, int* launches, cudaStream_t s);
 int64_t prefill_part_floats(int dim, int sms);
+// The rows of a Q8_0 cache that the sequences hold as the pages of an F16 cache of scratch (k, v: n_seq *
+// max_pages pages of n_kv tiles each; table: its page table, n_seq x max_pages, -1 for a page outside the
+// pool).  window > 0: rows ahead of every query's window are left out.
+cudaError_t launch_kv_expand(const KvCache& c, int64_t n_seq, const int32_t* starts, const int32_t* pages, int64_t max_pages,
+                             const int32_t* lens, int window, void* k, void* v, int32_t* table, int sms, cudaStream_t s);
 
 // What the C entry points of api_attn.cu share with api.cu: the SMs of this call and the
 // status words ([0]) of the current device; the attention's workspace of (device, stream), at
@@ -113,6 +118,8 @@ int64_t prefill_part_floats(int dim, int sms);
 // least `rest` bytes; the deterministic mode.
 int call_state(int* sms, int** words);
 int attn_workspace(cudaStream_t s, size_t zeroed, size_t rest, size_t* zeroed_at, void** out);
+// The workspace of (current device, stream) for the expanded rows of a Q8_0 cache.
+int attn_rows_workspace(cudaStream_t s, size_t bytes, void** out);
 bool deterministic();
 
 // Shared-memory limit and resident CTAs per SM of a kernel, looked up once per device.

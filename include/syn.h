@@ -451,7 +451,8 @@ typedef struct {
  * split, and a sequence's output does not depend on the others of the call).  Pointers 16-byte
  * (q, out, pools) or 4-byte aligned.  The call may allocate its workspace, which belongs to
  * (device, stream) and grows with n_seq * n_heads; make the first call of a size before capturing
- * a graph (growth synchronizes the device).  Asynchronous. */
+ * a graph (growth synchronizes the device; what it replaces lives until syn_release, so graphs
+ * captured earlier stay valid).  Asynchronous. */
 SYN_API int syn_attn_decode(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_seq, const void* q,
                             const int32_t* pages, int64_t max_pages, const int32_t* lens, void* out,
                             syn_stream_t stream);
@@ -466,8 +467,11 @@ SYN_API int syn_attn_decode(const syn_kv_cache* cache, const syn_attn* attn, int
  * about 2^-11 of its row's values, not to fp32's last place (syn_attn_decode is).  A row whose
  * sums are not finite is computed again from the keys it sees alone, far slower.
  * Few tokens over a long cache are split over its length (not in deterministic mode, in which a
- * token's output does not depend on the other sequences of the call).  Workspace, alignment and
- * errors as for syn_attn_decode; SYN_ERR_SHAPE also for n_tok * n_heads >= 2^31 - 1024.
+ * token's output does not depend on the other sequences of the call).  A call of many new tokens
+ * over a Q8_0 cache (not in deterministic mode) first expands the rows of its page table to fp16 in
+ * the workspace, 4 * n_seq * max_pages * page_size * n_kv_heads * head_dim bytes, where that is at
+ * most 2 GiB and there is room.  Workspace, alignment and errors as for syn_attn_decode;
+ * SYN_ERR_SHAPE also for n_tok * n_heads >= 2^31 - 1024.
  * Asynchronous. */
 SYN_API int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_seq, int64_t n_tok,
                              const void* q, const int32_t* starts, const int32_t* pages, int64_t max_pages,

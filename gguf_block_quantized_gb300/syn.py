@@ -299,6 +299,8 @@ def prepare_batch(items, n_tok: int, stream=None, staged=None) -> PreparedBatch:
 
 
 # ---- paged key-value cache and attention ---------------------------------------------------
+# (Outputs the helpers allocate belong to torch's current stream: with another `stream`, give
+# out / q_out and order that stream behind what the buffers were last used for.)
 
 class KVCache:
     """A paged cache over two torch pools (held by reference): ``k`` and ``v`` with the pages in
@@ -311,8 +313,10 @@ class KVCache:
         if tile < 0:
             raise SynError(ERR_TYPE if t not in (F16, Q8_0) else ERR_SHAPE, "KVCache")
         for pool in (k, v):
-            if pool.shape[0] != k.shape[0] or pool.stride(0) * pool.element_size() != k.stride(0) * k.element_size() \
-                    or pool[0].numel() * pool.element_size() != n_kv_heads * tile or not pool[0].is_contiguous():
+            if pool.shape[0] < 1 or pool.shape[0] != k.shape[0] or \
+                    pool[0].numel() * pool.element_size() != n_kv_heads * tile or not pool[0].is_contiguous() or \
+                    (pool.shape[0] > 1 and (pool.stride(0) * pool.element_size() != k.stride(0) * k.element_size() or
+                                            pool.stride(0) < pool[0].numel())):
                 raise ValueError("a pool is (n_pages, ...) with n_kv_heads contiguous tiles of "
                                  f"{tile} bytes per page, both pools alike")
         self.type, self.n_kv_heads, self.head_dim, self.page_size = t, n_kv_heads, head_dim, page_size
@@ -384,9 +388,10 @@ def _typed(x, dtype, what: str):
 
 
 def _rows(x, dtype, head_dim: int, what: str):
-    """(pointer, stride between tokens) of a (tokens, heads, head_dim) tensor whose rows are contiguous."""
+    """(pointer, stride between tokens) of a (tokens, heads, head_dim) tensor whose rows are contiguous.
+    (Tokens that share memory, as expand() makes them, are refused: a stride of 0 means packed.)"""
     if x.dim() != 3 or x.dtype != dtype or x.shape[2] != head_dim or (x.shape[2] > 1 and x.stride(2) != 1) or \
-            (x.shape[1] > 1 and x.stride(1) != head_dim):
+            (x.shape[1] > 1 and x.stride(1) != head_dim) or (x.shape[0] > 1 and x.stride(0) < x.shape[1] * head_dim):
         raise ValueError(f"{what}: a {dtype} tensor (tokens, heads, {head_dim}), each token's rows contiguous")
     return _ptr(x), (x.stride(0) if x.shape[0] > 1 else 0)
 

@@ -8,13 +8,17 @@
 // Bound: HBM; every cached row is read once for all the query heads that share it.
 //   - Warps work alone: each copies chunks of 16 rows of K and V into a ring of its own in shared
 //     memory (cp.async) and multiplies them with mma.sync m16n8k16, the 16 cached rows as the A
-//     operand and up to 8 query heads as the columns: S^T = K Q^T, then O^T += V^T P^T.  The
-//     product is a small share of the time (a chunk costs about 200 issue slots of the 1400 that
-//     its bytes take to arrive), so the tensor path only has to free the other pipes.
+//     operand and up to 8 query heads as the columns: S^T = K Q^T, then O^T += V^T P^T.  A
+//     chunk of 128-wide rows is about 380 instructions (F16) or 670 (Q8_0) of a warp, where its bytes
+//     take 1400 or 750 issue slots of an SM to arrive: Q8_0 is near the issue limit.
 //   - p is split into two fp16 numbers (head and tail, 22 bits) and each chunk's product starts
 //     from zero and is added to the fp32 sums by fma, because the tensor pipe's own additions
-//     truncate.  Scores likewise come from two short chains.  So the result is as exact as fp32
+//     truncate.  Scores likewise come from short chains.  So the result is as exact as fp32
 //     arithmetic allows, which fp32 outputs show.
+//   - Q8_0 codes go into the products as they are, without their scales: exact in fp16.  A key's
+//     scale multiplies its block's 32-value sum, a value's scale goes into p, head and tail.  Key codes
+//     go in with 128 added, as subnormal numbers, and the sums start from what that adds (no
+//     subtraction a code: with the value scales' product in fp16 pairs 740 -> 672 instructions a chunk).
 //   - Work is cut by length, not by sequence: the steps (4 chunks, one per warp) of all
 //     (sequence, kv head) items are dealt to the CTAs in equal contiguous ranges, found on the
 //     device from the lengths (a captured graph keeps working as they grow).  A CTA whose range
@@ -31,6 +35,7 @@ namespace syn {
 constexpr int DEC_WARPS = 4;
 constexpr int DEC_SLOTS = 3;    // of a warp's ring: the keys or the values of a chunk each
 constexpr int DEC_MAX_SEQ = 1024;  // sequences of one launch (their step counts are in shared memory)
+constexpr uint32_t MINUS_128 = 0x80808080u;  // -128 * 2^-24 as fp16, twice
 constexpr float DEC_P_LOG2 = 14.0f;  // p is held as 2^14 p, in fp16: small p stay normal numbers
 
 struct DecodeParams {
@@ -86,6 +91,11 @@ __device__ __forceinline__ void mma16816_zero(float (&c)[4], const uint32_t (&a)
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                  : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
@@ -351,7 +361,8 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
     int item_w = blockIdx.x;
 
     constexpr float LOG2E = 1.4426950408889634f;
-    const float scale_log2 = p.scale * LOG2E;
+    constexpr float CODE = Q8 ? 16777216.0f : 1.0f;  // scores come in units of 2^-24 (q_off)
+    const float scale = p.scale * CODE, scale_log2 = scale * LOG2E;
     uint8_t* ring = smem + warp * L::WARP;
     const uint32_t ring_s = smem_u32(ring);
     const int row_pieces = Q8 ? dim >> 4 : dim >> 3;  // 16-byte pieces of a row
@@ -446,6 +457,22 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     }
                 }
             }
+        }
+        // Q8_0: codes go in as code + 128 in the lowest bits of an fp16, a subnormal number that stands for
+        // 2^-24 (code + 128) exactly; the sums start from -2^-17 times the sum of their q.
+        [[maybe_unused]] float q_off[D / 32][NT][2];
+        if (Q8) {
+#pragma unroll
+            for (int b = 0; b < D / 32; b++)
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    float c[4];
+                    const uint32_t off[4] = {MINUS_128, MINUS_128, MINUS_128, MINUS_128};
+                    mma16816_zero(c, off, qf[2 * b][nt][0], qf[2 * b][nt][1]);
+                    mma16816(c, off, qf[2 * b + 1][nt][0], qf[2 * b + 1][nt][1]);
+                    q_off[b][nt][0] = c[0];
+                    q_off[b][nt][1] = c[1];
+                }
         }
         float slope[NT][2];
 #pragma unroll
@@ -569,7 +596,6 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
             if (Q8) {
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
-                const __half2 k1152 = __float2half2_rn(1152.0f);
                 alignas(16) __half da[D / 32], db[D / 32];
                 row_scales<D, EXACT>(ktp + L::KS, r8, dim, da);
                 row_scales<D, EXACT>(ktp + L::KS, r8 + 8, dim, db);
@@ -582,16 +608,16 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     for (int u = 0; u < 2; u++) {
                         const uint2 w = *reinterpret_cast<const uint2*>(ktp + (r8 + 8 * u) * L::PK + 32 * b + 8 * c4);
                         const uint32_t x = w.x ^ 0x80808080u, y = w.y ^ 0x80808080u;
-                        a0[u] = h2u(__hsub2(u2h(__byte_perm(x, 0x64646464u, 0x4140)), k1152));
-                        a0[2 + u] = h2u(__hsub2(u2h(__byte_perm(x, 0x64646464u, 0x4342)), k1152));
-                        a1[u] = h2u(__hsub2(u2h(__byte_perm(y, 0x64646464u, 0x4140)), k1152));
-                        a1[2 + u] = h2u(__hsub2(u2h(__byte_perm(y, 0x64646464u, 0x4342)), k1152));
+                        a0[u] = __byte_perm(x, 0, 0x4140);
+                        a0[2 + u] = __byte_perm(x, 0, 0x4342);
+                        a1[u] = __byte_perm(y, 0, 0x4140);
+                        a1[2 + u] = __byte_perm(y, 0, 0x4342);
                     }
                     const float fa = __half2float(da[b]), fb = __half2float(db[b]);
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
                         float c[4];
-                        mma16816_zero(c, a0, qf[2 * b][nt][0], qf[2 * b][nt][1]);
+                        mma16816_from(c, a0, qf[2 * b][nt][0], qf[2 * b][nt][1], q_off[b][nt][0], q_off[b][nt][1]);
                         mma16816(c, a1, qf[2 * b + 1][nt][0], qf[2 * b + 1][nt][1]);
                         sc[nt][0] = fmaf(c[0], fa, sc[nt][0]);
                         sc[nt][1] = fmaf(c[1], fa, sc[nt][1]);
@@ -621,14 +647,15 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
             issue_v(sk);
 
             // softmax of the chunk, in powers of two
-            uint32_t ph[NT][2], pl[NT][2];  // F16: P^T as the B operand (heads and tails)
-            float pr[NT][4], alpha[NT][2];
+            uint32_t ph[NT][2], pl[NT][2];  // P^T as the B operand (heads and tails)
+            float alpha[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
+                float pr[4];
                 if (p.cap > 0.0f || p.slopes) {
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        float x = sc[nt][j] * p.scale;
+                        float x = sc[nt][j] * scale;
                         if (p.cap > 0.0f) x = p.cap * tanh_rel(x * p.inv_cap);
                         sc[nt][j] = fmaf(-slope[nt][j & 1], (float)(len - 1 - row0 - r8 - (j >> 1) * 8), x) * LOG2E;
                     }
@@ -649,18 +676,16 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     const float ms = mx == -INFINITY ? 0.0f : mx;  // nothing seen yet
                     alpha[nt][j] = ex2(m[nt][j] - ms);
                     m[nt][j] = mx;
-                    pr[nt][j] = ex2(sc[nt][j] - (ms - DEC_P_LOG2));
-                    pr[nt][j + 2] = ex2(sc[nt][j + 2] - (ms - DEC_P_LOG2));
-                    l[nt][j] = fmaf(l[nt][j], alpha[nt][j], pr[nt][j] + pr[nt][j + 2]);
+                    pr[j] = ex2(sc[nt][j] - (ms - DEC_P_LOG2));
+                    pr[j + 2] = ex2(sc[nt][j + 2] - (ms - DEC_P_LOG2));
+                    l[nt][j] = fmaf(l[nt][j], alpha[nt][j], pr[j] + pr[j + 2]);
                 }
-                if (!Q8) {
 #pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        uint32_t hi, lo;
-                        split_pair(pr[nt][2 * i], pr[nt][2 * i + 1], hi, lo);
-                        ph[nt][i] = transpose8(hi);
-                        pl[nt][i] = transpose8(lo);
-                    }
+                for (int i = 0; i < 2; i++) {
+                    uint32_t hi, lo;
+                    split_pair(pr[2 * i], pr[2 * i + 1], hi, lo);
+                    ph[nt][i] = transpose8(hi);
+                    pl[nt][i] = transpose8(lo);
                 }
             }
             cp_wait<2>();
@@ -668,11 +693,12 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
 
             // O^T = O^T * alpha + V^T P^T
             if (Q8) {
-                // A row's value scales go into p, in fp32 and before the split, relative to 2^e, the
-                // largest power of two among the scales so far: p * scale then fits fp16 whatever
-                // the scales (o is kept in units of 2^e, as it is relative to 2^m).
+                // A row's value scales go into p: with d' the scale relative to 2^e, e the largest exponent
+                // among the scales so far (o is kept in units of 2^e, as it is relative to 2^m), the head
+                // of p * d' is h = fp16(p_hi * d'), and its tail p_lo * d' + (p_hi * d' - h), the bracket
+                // exact in one fma.
                 alignas(16) __half dv[4][D / 32];  // scales of rows 2c, 2c+1, 2c+8, 2c+9
-                uint32_t top = 0;
+                __half2 top2 = __float2half2_rn(0.0f);
 #pragma unroll
                 for (int u = 0; u < 4; u++) {
                     const int r = 2 * c4 + (u & 1) + 8 * (u >> 1);
@@ -682,26 +708,17 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                         for (int b = 0; b < D / 32; b++) dv[u][b] = __ushort_as_half(0);
                     }
 #pragma unroll
-                    for (int b = 0; b < D / 32; b++)
-                        if (b * 32 < dim) top = max(top, (uint32_t)__half_as_ushort(dv[u][b]) & 0x7FFFu);
+                    for (int b = 0; b < D / 32; b += 2) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2*>(&dv[u][b])));
                 }
+                const uint32_t t2 = h2u(top2), top = max(t2 & 0xFFFFu, t2 >> 16);
                 const int e_new = max(e_run, (int)(__reduce_max_sync(0xffffffffu, top) >> 10));
-                const float down = __int_as_float((127 + 15 - e_new) << 23), step = __int_as_float((127 + e_run - e_new) << 23);
+                const float step = __int_as_float((127 + e_run - e_new) << 23);
+                const __half2 down = __float2half2_rn(__int_as_float((127 + 15 - e_new) << 23));
                 e_run = e_new;
-                // p in the B operand's layout (rows 2c, 2c+1, 2c+8, 2c+9 of head lane/4): the upper and
-                // lower halves of the fp32 words transposed apart
-                float pb[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
                     alpha[nt][0] *= step;
                     alpha[nt][1] *= step;
-#pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        const uint32_t x = __float_as_uint(pr[nt][2 * u]), y = __float_as_uint(pr[nt][2 * u + 1]);
-                        const uint32_t hi = transpose8(__byte_perm(x, y, 0x7632)), lo = transpose8(__byte_perm(x, y, 0x5410));
-                        pb[nt][2 * u] = __uint_as_float(__byte_perm(lo, hi, 0x5410)) * down;
-                        pb[nt][2 * u + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632)) * down;
-                    }
                 }
                 const __half2 k1152 = __float2half2_rn(1152.0f);
 #pragma unroll
@@ -719,11 +736,13 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                         a1[2 * u] = h2u(__hsub2(u2h(__byte_perm(x23, 0x64646464u, 0x4140)), k1152));
                         a1[2 * u + 1] = h2u(__hsub2(u2h(__byte_perm(x23, 0x64646464u, 0x4342)), k1152));
                     }
+                    const __half2 d0 = __hmul2(__halves2half2(dv[0][b], dv[1][b]), down), d1 = __hmul2(__halves2half2(dv[2][b], dv[3][b]), down);
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
-                        uint32_t hi0, lo0, hi1, lo1;
-                        split_pair(pb[nt][0] * __half2float(dv[0][b]), pb[nt][1] * __half2float(dv[1][b]), hi0, lo0);
-                        split_pair(pb[nt][2] * __half2float(dv[2][b]), pb[nt][3] * __half2float(dv[3][b]), hi1, lo1);
+                        const __half2 h0 = __hmul2(u2h(ph[nt][0]), d0), h1 = __hmul2(u2h(ph[nt][1]), d1);
+                        const uint32_t lo0 = h2u(__hfma2(u2h(pl[nt][0]), d0, __hfma2(u2h(ph[nt][0]), d0, __hneg2(h0))));
+                        const uint32_t lo1 = h2u(__hfma2(u2h(pl[nt][1]), d1, __hfma2(u2h(ph[nt][1]), d1, __hneg2(h1))));
+                        const uint32_t hi0 = h2u(h0), hi1 = h2u(h1);
 #pragma unroll
                         for (int u = 0; u < 2; u++) {
                             float c[4];
@@ -898,7 +917,8 @@ cudaError_t launch_attn_decode(const KvCache& c, const AttnDesc& a, int64_t n_se
         p.part = part;
         p.count = count;
         p.err = err;
-        p.scale = a.scale;
+        // (Q8_0: the kernel multiplies the scale by 2^24.  Past 2^100 the largest score alone counts.)
+        p.scale = c.q8 ? std::min(std::max(a.scale, -0x1p100f), 0x1p100f) : a.scale;
         p.cap = a.cap;
         p.inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
         p.n_seq = (int)std::min<int64_t>(DEC_MAX_SEQ, n_seq - s0);

@@ -325,19 +325,16 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
     for (int base = 0; base < p.n_seq; base += 32 * DEC_WARPS) {
         const int s = base + tid;
         int n = 0;
-        if (s < p.n_seq) {
-            n = (seq_chunks(seq_visible(p, s, seq_len(p, s))).count() + DEC_WARPS - 1) / DEC_WARPS;
-            if (n == 0) {  // no key to see: zeros, written by the CTAs in turn
-                if (s % gridDim.x == blockIdx.x) {
-                    const int64_t n_out = (int64_t)p.c.n_kv * p.g * dim;
-                    for (int64_t i = 0; i < n_out; i++) {
-                        if (p.out_f16) static_cast<__half*>(p.out)[s * p.out_stride + i] = __float2half_rn(0.0f);
-                        else static_cast<float*>(p.out)[s * p.out_stride + i] = 0.0f;
-                    }
-                }
-            }
-        }
+        if (s < p.n_seq) n = (seq_chunks(seq_visible(p, s, seq_len(p, s))).count() + DEC_WARPS - 1) / DEC_WARPS;
         scan(s, n);
+    }
+    for (int s = blockIdx.x; s < p.n_seq; s += gridDim.x) {  // no key to see: zeros
+        if (pre[s + 1] > pre[s]) continue;
+        const int64_t row = s * p.out_stride;
+        for (int i = tid; i < p.c.n_kv * p.g * dim >> 2; i += 32 * DEC_WARPS) {
+            if (p.out_f16) *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + row + 4 * i) = make_uint2(0, 0);
+            else *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row + 4 * i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
     }
     // Little work is dealt in blocks of 3 steps, one a CTA: a step's loads are in flight together
     // with the next ones', so cutting a short item finer would end it no sooner, and it would have

@@ -20,8 +20,9 @@
 //     go in with 128 added, as subnormal numbers, and the sums start from what that adds (no
 //     subtraction a code: with the value scales' product in fp16 pairs 740 -> 672 instructions a chunk).
 //   - Work is cut by length, not by sequence: the steps (4 chunks, one per warp) of all
-//     (sequence, kv head) items are dealt to the CTAs in equal contiguous ranges, found on the
-//     device from the lengths (a captured graph keeps working as they grow).  A CTA whose range
+//     (sequence, kv head) items, and some for each item's start and end, are dealt to the CTAs in
+//     equal contiguous ranges, found on the device from the lengths (a captured graph keeps working
+//     as they grow).  A CTA whose range
 //     covers an item writes the output; else it leaves a partial in the workspace, and the CTA
 //     that finishes an item last (a counter) joins the partials in order.  No CTA waits.
 #include <algorithm>
@@ -34,6 +35,13 @@ namespace syn {
 
 constexpr int DEC_WARPS = 4;
 constexpr int DEC_SLOTS = 3;    // of a warp's ring: the keys or the values of a chunk each
+// What an item's start and end cost, in steps.  Measured (us, 0 / 2 / 8): 58 sequences of 40 to 14210 rows, 32 / 8
+// heads of 128, Q8_0 117 / 82 / 86, F16 139 / 119 / 117; 58 of 2500 rows each, Q8_0 82 / 82 / 86.
+constexpr int DEC_ITEM = 2;
+// A part's share of the join, per value, against a step (blocks of sqrt(steps * values * this)).
+// Measured (us, 0 / 2e-4 / 8e-4): one sequence of 32768 rows, F16, 24 / 1 heads of 128 74 / 43 / 49; one of
+// 40642, Q8_0, 16 / 2 heads of 64 35 / 27 / 30.
+constexpr float DEC_JOIN = 2e-4f;
 constexpr int DEC_MAX_SEQ = 1024;  // sequences of one launch (their step counts are in shared memory)
 constexpr uint32_t MINUS_128 = 0x80808080u;  // -128 * 2^-24 as fp16, twice
 constexpr float DEC_P_LOG2 = 14.0f;  // p is held as 2^14 p, in fp16: small p stay normal numbers
@@ -292,8 +300,9 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
     extern __shared__ __align__(128) uint8_t smem[];
     float* sm_m = reinterpret_cast<float*>(smem + L::RING);  // [DEC_WARPS][H]
     float* sm_l = sm_m + DEC_WARPS * H;
-    int* flags = reinterpret_cast<int*>(sm_l + DEC_WARPS * H);  // [0] scan carry, [1..4] warp sums, [5] last
-    int* pre = flags + 8;                                        // [n_seq + 1] blocks before each sequence, of one item
+    int* flags = reinterpret_cast<int*>(sm_l + DEC_WARPS * H);  // [0] scan carry, [1..4] warp sums, [5] last, [6] most steps
+    unsigned long long* all_steps = reinterpret_cast<unsigned long long*>(flags + 8);
+    int* pre = flags + 10;                                        // [n_seq + 1] blocks before each sequence, of one item
 
     // (the shuffle tells the compiler that the warp's index is the same for its lanes)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -319,14 +328,33 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
     };
     griddep_release();
     griddep_wait();
-    // steps of every sequence, as a running sum
-    if (tid == 0) flags[0] = 0, pre[0] = 0;
+    // the steps of every sequence: their sum and the most
+    auto chunks_of = [&](int s) { return seq_chunks(seq_visible(p, s, seq_len(p, s))).count(); };
+    if (tid == 0) flags[0] = 0, flags[6] = 0, *all_steps = 0, pre[0] = 0;
     __syncthreads();
+    for (int base = 32 * warp; base < p.n_seq; base += 32 * DEC_WARPS) {
+        const unsigned n = base + lane < p.n_seq ? (unsigned)(chunks_of(base + lane) + DEC_WARPS - 1) / DEC_WARPS : 0u;
+        const unsigned sum = __reduce_add_sync(0xffffffffu, n), most = __reduce_max_sync(0xffffffffu, n);
+        if (lane == 0) {
+            atomicAdd(all_steps, (unsigned long long)sum);
+            atomicMax(&flags[6], (int)most);
+        }
+    }
+    __syncthreads();
+    const int64_t steps = (int64_t)*all_steps;
+    // Little work is dealt in blocks of several steps, one a CTA: 3, as a step's loads are in flight
+    // together with the next ones', and more where the longest item would have so many parts that their
+    // join (heads * dim values a part, by one CTA) took longer than the steps.
+    const int few = max(3, (int)ceilf(sqrtf((float)flags[6] * (float)(min(H, p.g) * dim) * DEC_JOIN)));
+    int block = !p.whole && steps * n_item_h <= (int64_t)few * gridDim.x ? few : 1;
+    if (steps >> 30) block = max(block, (int)(steps >> 30) + 1);  // (the running sum has 32 bits)
+    // Else an item counts DEC_ITEM steps more than it has: what its start and its end cost.
+    const int extra = block == 1 && !p.whole ? DEC_ITEM : 0;
     for (int base = 0; base < p.n_seq; base += 32 * DEC_WARPS) {
         const int s = base + tid;
-        int n = 0;
-        if (s < p.n_seq) n = (seq_chunks(seq_visible(p, s, seq_len(p, s))).count() + DEC_WARPS - 1) / DEC_WARPS;
-        scan(s, n);
+        int x = 0;
+        if (s < p.n_seq) x = (chunks_of(s) + DEC_WARPS * block - 1) / (DEC_WARPS * block);
+        scan(s, x > 0 ? x + extra : 0);
     }
     for (int s = blockIdx.x; s < p.n_seq; s += gridDim.x) {  // no key to see: zeros
         if (pre[s + 1] > pre[s]) continue;
@@ -334,19 +362,6 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
         for (int i = tid; i < p.c.n_kv * p.g * dim >> 2; i += 32 * DEC_WARPS) {
             if (p.out_f16) *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + row + 4 * i) = make_uint2(0, 0);
             else *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row + 4 * i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-    }
-    // Little work is dealt in blocks of 3 steps, one a CTA: a step's loads are in flight together
-    // with the next ones', so cutting a short item finer would end it no sooner, and it would have
-    // to be joined.
-    const int block = !p.whole && (int64_t)pre[p.n_seq] * n_item_h <= 3 * (int64_t)gridDim.x ? 3 : 1;
-    if (block > 1) {
-        if (tid == 0) flags[0] = 0;
-        for (int base = 0; base < p.n_seq; base += 32 * DEC_WARPS) {
-            const int s = base + tid;
-            int x = 0;
-            if (s < p.n_seq) x = (seq_chunks(seq_visible(p, s, seq_len(p, s))).count() + DEC_WARPS * block - 1) / (DEC_WARPS * block);
-            scan(s, x);
         }
     }
     const int64_t total = (int64_t)pre[p.n_seq] * n_item_h;
@@ -415,12 +430,15 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                 else lo = mid + 1;
             }
             s = lo;
-            n_blocks = pre[s + 1] - pre[s];
+            const int n_all = pre[s + 1] - pre[s];
+            n_blocks = n_all - extra;
             const int64_t rel = at - (int64_t)pre[s] * n_item_h;
-            hh = (int)(rel / n_blocks);
-            st0 = (int)(rel - (int64_t)hh * n_blocks);
-            st1 = (int)min((int64_t)n_blocks, st0 + (stop - at));
-            at += st1 - st0;
+            hh = (int)(rel / n_all);
+            const int b0 = (int)(rel - (int64_t)hh * n_all), b1 = (int)min((int64_t)n_all, b0 + (stop - at));
+            at += b1 - b0;
+            st0 = max(b0 - extra, 0);
+            st1 = max(b1 - extra, 0);
+            if (st0 == st1) continue;
         }
         const int h = hh / p.n_hg, hg = hh - h * p.n_hg;
         const int len = seq_len(p, s);
@@ -844,7 +862,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
         }
         if (!direct) {
             // the CTAs that share the item: those whose ranges hold its first and last block
-            const int64_t t0 = (int64_t)pre[s] * n_item_h + (int64_t)hh * n_blocks;
+            const int64_t t0 = (int64_t)pre[s] * n_item_h + (int64_t)hh * (n_blocks + extra) + extra;
             const int i0 = (int)(((t0 + 1) * ctas - 1) / total), i1 = (int)(((t0 + n_blocks) * ctas - 1) / total);
             const int item = s * n_item_h + hh;
             __threadfence();
@@ -869,7 +887,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
 template <int D, int NT, bool Q8, bool EXACT>
 static cudaError_t run_decode_as(const DecodeParams& p, int sms, cudaStream_t s) {
     auto kern = k_attn_decode<D, NT, Q8, EXACT>;
-    constexpr int smem = DecLayout<D, Q8>::RING + 2 * DEC_WARPS * 8 * NT * 4 + 32 + 4 * (DEC_MAX_SEQ + 1);
+    constexpr int smem = DecLayout<D, Q8>::RING + 2 * DEC_WARPS * 8 * NT * 4 + 40 + 4 * (DEC_MAX_SEQ + 1);
     static ResidentCtas resident;  // per device, looked up once
     int per_sm = 0;
     const cudaError_t e = resident.get(reinterpret_cast<const void*>(kern), 32 * DEC_WARPS, smem, &per_sm);

@@ -110,6 +110,42 @@ def test_expanded_cache_nonfinite_and_bad_pages(syn):
     assert (np.abs(got - ref) <= prefill_bound(Q8_0, size, vmax, ref, False))[:260][good[:260]].all()
 
 
+# ---- how decode deals its work --------------------------------------------------------------
+# (ranges over items of unlike lengths, each with some steps for its ends; blocks of steps for few long ones)
+
+@pytest.mark.parametrize("t", [F16, Q8_0])
+@pytest.mark.parametrize("heads,kv,dim,lens,limit", [
+    (8, 2, 64, [3, 40, 0, 64, 65, 2, 700, 1, 1, 1, 128, 30, 5000, 17], 1),
+    (8, 2, 64, [3, 40, 0, 64, 65, 2, 700, 1, 1, 1, 128, 30, 5000, 17] * 3, 7),
+    (4, 4, 128, [40] * 70 + [9000] + [0] * 5 + [33] * 60, 0),
+    (24, 1, 128, [20000], 0),
+    (16, 2, 96, [12000, 1, 300], 0),
+    (8, 1, 256, [5000, 7000], 16),
+])
+def test_decode_ranges(syn, t, heads, kv, dim, lens, limit):
+    import torch
+    rng = np.random.default_rng([t, dim, limit])
+    cache, pages, seqs = make_cache(syn, rng, t, kv, dim, 32, lens)
+    q = rng.standard_normal((len(lens), heads, dim)).astype(np.float16)
+    old = syn.set_sm_limit(limit)
+    try:
+        got = syn.attn_decode(cache, torch.from_numpy(q).cuda(), pages, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    finally:
+        syn.set_sm_limit(old)
+    got = got.double().cpu().numpy()
+    ref, size = reference(q, seqs, [np.array([n - 1]) for n in lens], [np.zeros(1)] * len(lens), [0] * len(lens), 0, dim ** -0.5, 0.0, None)
+    assert (np.abs(got - ref) <= decode_bound(size, ref, False)).all()
+    assert syn.device_status() == syn.OK
+
+
+@pytest.mark.parametrize("t", [F16, Q8_0])
+@pytest.mark.parametrize("heads,kv,dim,lens,new,dtype", [
+    (24, 1, 128, [2000], [9], "float16"), (6, 2, 64, [4096, 1000], [64, 3], "float32"), (5, 1, 256, [3000], [30], "float16"),
+    (3, 1, 96, [5000], [7], "float32")])
+def test_prefill_parts_and_joins(syn, t, heads, kv, dim, lens, new, dtype):
+    run_prefill(syn, t, heads, kv, dim, 16, lens, new, 25, dts=(dtype,))
+
+
 # ---- many sequences, both forms of the cap, empty rows -------------------------------------
 
 @pytest.mark.parametrize("n_seq", [33, 1030])

@@ -13,7 +13,9 @@
 // pieces of up to 16 KB) into a ring in shared memory; eight warps take 4 consecutive values a
 // thread from there, rotate, and store them as 8 bytes (a warp's stores are contiguous).  So about
 // 150 KB of loads are in flight on an SM whatever the threads wait for.  A Q8_0 block is 8
-// neighbouring lanes, its amax three shuffles.
+// neighbouring lanes, its amax three shuffles.  Measured on GB300: 8192 tokens of 32 / 8 heads of 128 into
+// F16 47.9 us, 6.3 TB/s (93 % of a copy's rate; every thread loading for itself 66 us); one token
+// 3.7 us; 4095 tokens into Q8_0 and back (k_kv_read) 42.1 us.
 #include <algorithm>
 
 #include "kernels.h"

@@ -25,6 +25,10 @@
 //     as they grow).  A CTA whose range
 //     covers an item writes the output; else it leaves a partial in the workspace, and the CTA
 //     that finishes an item last (a counter) joins the partials in order.  No CTA waits.
+//
+// Measured on GB300, 32 / 8 heads of 128 (share of a copy's rate): 300 sequences of 2500 rows, F16 96 %,
+// Q8_0 71 %; 48 sequences of 100 to 4000, F16 44.4 us, 71 %; 128 of 500 to 8191, Q8_0, capped 175 us, 65 %;
+// one of 130001, F16 92 us, 85 %; one of 77 (heads of 64) 5.2 us.
 #include <algorithm>
 #include <climits>
 

@@ -27,6 +27,11 @@
 //
 // Few rows over a long cache: an item's tiles are split between CTAs (no CTA waits: the last to
 // finish, by a counter, joins the partials in order).
+//
+// Measured on GB300, 32 / 8 heads of 128, F16: a prompt of 8192 tokens 395 us, 1.39 PFLOP/s (73 % of
+// a library matrix product's rate: a tile of 128 keys takes 2700 cycles, the products of its
+// two row tiles 2048: a row tile's softmax, 1450 cycles, stands between its two products); 6 prompts of up to 1001 tokens, capped in a window of 1024, 68 us; 2 chunks of up
+// to 2000 tokens over 8000 Q8_0 rows, slopes and documents, 105 us; 9 tokens over 709 rows, heads of 64, 12.9 us.
 #include <algorithm>
 #include <climits>
 

@@ -166,12 +166,11 @@ __device__ __forceinline__ Chunks seq_chunks(const Visible& w) {
 
 template <int D, bool Q8>
 struct DecLayout {
-    // row pitches in shared memory.  F16: 16-byte pieces swizzled by the row (ldmatrix reads 8
-    // rows of one piece); Q8_0: pitches that put the rows a half-warp reads on different banks
-    static constexpr int PK = Q8 ? ((D / 32) % 2 ? D : D + 32) : 2 * D;
-    static constexpr int PV = Q8 ? D + 16 : 2 * D;
-    static constexpr int KS = 16 * PK, VS = 16 * PV;  // Q8_0: scales [16][dim/32], behind the rows
-    static constexpr int SLOT = 16 * (PK > PV ? PK : PV) + (Q8 ? D : 0);
+    // row pitch in shared memory: the 8 rows of one 16-byte piece that ldmatrix reads lie on different
+    // banks.  F16: pieces swizzled by the row; Q8_0: an odd number of pieces
+    static constexpr int PITCH = Q8 ? D + 16 : 2 * D;
+    static constexpr int SCALES = 16 * PITCH;  // Q8_0: scales [16][dim/32], behind the rows
+    static constexpr int SLOT = SCALES + (Q8 ? D : 0);
     // (the merge of the warps' parts, up to 16 heads of D fp32 values each, reuses a warp's ring)
     static constexpr int MERGE = (D <= 128 ? 16 : 8) * D * 4;
     static constexpr int WARP = DEC_SLOTS * SLOT > MERGE ? DEC_SLOTS * SLOT : MERGE;
@@ -387,26 +386,32 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
     // as wide as the kernel's: with the swizzle they repeat every 8 rows, without it they are linear.
     constexpr int N_COPY = Q8 ? D / 32 : D / 16;
     constexpr int N_TO = !EXACT ? N_COPY : Q8 ? 1 : D / 32;
-    uint32_t to_k[N_TO], to_v[N_TO];
+    uint32_t to[N_TO];
 #pragma unroll
     for (int i = 0; i < N_TO; i++) {
         const int idx = i * 32 + lane, r = idx / row_pieces, j = idx - r * row_pieces;
-        to_k[i] = r * L::PK + (Q8 ? 16 * j : ((j ^ (r & 7)) << 4));
-        to_v[i] = r * L::PV + (Q8 ? 16 * j : ((j ^ (r & 7)) << 4));
+        to[i] = r * L::PITCH + (Q8 ? 16 * j : ((j ^ (r & 7)) << 4));
     }
-    auto place = [&](const uint32_t (&to)[N_TO], int pitch, int i) -> uint32_t {
+    auto place = [&](int i) -> uint32_t {
         if (!EXACT) return to[i % N_TO];
-        return Q8 ? to[0] + i * (512 / D) * pitch : to[i % N_TO] + (i / N_TO) * 16 * D;
+        return Q8 ? to[0] + i * (512 / D) * L::PITCH : to[i % N_TO] + (i / N_TO) * 16 * D;
     };
-    // F16: where ldmatrix finds 16-byte piece 2i (+ 8 for the next four) of this lane's row
-    uint32_t at_k[4], at_v[4];
+    // Where ldmatrix finds 16-byte piece 2i (+ 8 for the next four) of this lane's row.  Keys: matrices of
+    // rows 0-7 and 8-15 of one piece, then of the next; values, transposed, F16 the same, Q8_0 rows
+    // 0-7 of two pieces, then rows 8-15.
+    uint32_t at_k[Q8 ? 1 : 4], at_v[Q8 ? 1 : 4];
     {
         const int rk = (lane & 7) + ((lane >> 3) & 1) * 8, ck = lane >> 4;
         const int rv = (lane & 7) + (lane >> 4) * 8, cv = (lane >> 3) & 1;
+        if (Q8) {
+            at_k[0] = rk * L::PITCH + 16 * ck;
+            at_v[0] = rv * L::PITCH + 16 * cv;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            at_k[i] = rk * L::PK + (((2 * i + ck) ^ (rk & 7)) << 4);
-            at_v[i] = rv * L::PV + (((2 * i + cv) ^ (rv & 7)) << 4);
+            for (int i = 0; i < (Q8 ? 1 : 4); i++) {
+                at_k[i] = rk * L::PITCH + (((2 * i + ck) ^ (rk & 7)) << 4);
+                at_v[i] = rv * L::PITCH + (((2 * i + cv) ^ (rv & 7)) << 4);
+            }
         }
     }
     [[maybe_unused]] const int64_t pool_end = p.c.tile + (p.c.n_pages - 1) * p.c.page_stride;  // from a head's tile of page 0
@@ -467,7 +472,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                 qf[ks][nt][0] = qf[ks][nt][1] = 0;
                 if (hd < heads && ks * 16 < dim) {
                     if (Q8) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(qr + (ks >> 1) * 32 + 8 * c4 + 4 * (ks & 1));
+                        const uint2 w = *reinterpret_cast<const uint2*>(qr + 16 * ks + 4 * c4);
                         qf[ks][nt][0] = w.x;
                         qf[ks][nt][1] = w.y;
                     } else {
@@ -541,18 +546,18 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
             }
         };
         look_up();
-        auto copy = [&](uint32_t dst, const uint8_t* base, const uint32_t (&to)[N_TO], int pitch, int scales) {
+        auto copy = [&](uint32_t dst, const uint8_t* base) {
             if (v_whole) {
                 const uint8_t* src = base + v_off + 16 * lane;
                 if (!SYN_IN_BOUNDS(v_off >= 0 && v_off + 256 * row_pieces <= pool_end)) return;
 #pragma unroll
                 for (int i = 0; i < N_COPY; i++) {
                     if (2 * i >= row_pieces) break;
-                    cp16_all(dst + place(to, pitch, i), src + 512 * i);
+                    cp16_all(dst + place(i), src + 512 * i);
                 }
                 // Q8_0: the rows' scales, dim/16 pieces (rows of 16 * row_pieces bytes, scales of row_pieces)
                 if (Q8 && lane < row_pieces)
-                    cp16_all(dst + scales + 16 * lane, src + plane - (v_row & page_mask) * (15 * row_pieces));
+                    cp16_all(dst + L::SCALES + 16 * lane, src + plane - (v_row & page_mask) * (15 * row_pieces));
                 return;
             }
             // a chunk at an end of what is seen, or pages of 8 rows: rows that the query does not
@@ -562,8 +567,8 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
 #pragma unroll
             for (int i = 0; i < N_COPY; i++) {
                 if (2 * i >= row_pieces) break;
-                const uint32_t at_dst = place(to, pitch, i);
-                const int r = (int)at_dst / pitch, j = i * 32 + lane - r * row_pieces;
+                const uint32_t at_dst = place(i);
+                const int r = (int)at_dst / L::PITCH, j = i * 32 + lane - r * row_pieces;
                 const bool upper = r >= 8, ok = (upper ? v_hi : v_lo) >= 0 && vis(v_row + r);
                 const int64_t off = ok ? (upper ? page_hi + (int64_t)(cell_hi + r - 8) * (row_pieces * 16)
                                                 : page + (int64_t)(cell + r) * (row_pieces * 16)) + 16 * j
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                 const int64_t off = ok ? plane + (upper ? page_hi + (int64_t)cell_hi * row_pieces + 16 * (lane - row_pieces / 2)
                                                         : page + (int64_t)cell * row_pieces + 16 * lane)
                                        : 0;
-                if (SYN_IN_BOUNDS(off >= 0 && off + 16 <= pool_end)) cp16(dst + scales + 16 * lane, base + off, ok ? 16u : 0u);
+                if (SYN_IN_BOUNDS(off >= 0 && off + 16 <= pool_end)) cp16(dst + L::SCALES + 16 * lane, base + off, ok ? 16u : 0u);
             }
         };
         auto issue_k = [&](int slot) {
@@ -587,14 +592,14 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                 v_hi = id_hi;
                 v_whole = v_lo >= 0 && all_seen(v_row);
                 v_off = (int64_t)((uint64_t)(uint32_t)v_lo * p.stride16 + (uint32_t)((v_row & page_mask) * row_pieces)) << 4;
-                copy(ring_s + slot * L::SLOT, kbase, to_k, L::PK, L::KS);
+                copy(ring_s + slot * L::SLOT, kbase);
                 k_next += DEC_WARPS;
                 look_up();
             }
             cp_commit();
         };
         auto issue_v = [&](int slot) {
-            if (v_row >= 0) copy(ring_s + slot * L::SLOT, vbase, to_v, L::PV, L::VS);
+            if (v_row >= 0) copy(ring_s + slot * L::SLOT, vbase);
             cp_commit();
         };
         issue_k(0);
@@ -616,21 +621,23 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
                 alignas(16) __half da[D / 32], db[D / 32];
-                row_scales<D, EXACT>(ktp + L::KS, r8, dim, da);
-                row_scales<D, EXACT>(ktp + L::KS, r8 + 8, dim, db);
+                row_scales<D, EXACT>(ktp + L::SCALES, r8, dim, da);
+                row_scales<D, EXACT>(ktp + L::SCALES, r8 + 8, dim, db);
 #pragma unroll
                 for (int b = 0; b < D / 32; b++) {
                     if (b * 32 >= dim) break;
                     // codes of a 32-value block: 8 per lane and row, exact in fp16
                     uint32_t a0[4], a1[4];
+                    uint32_t w[4];
+                    ldsm4(kt + at_k[0] + 32 * b, w);
 #pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(ktp + (r8 + 8 * u) * L::PK + 32 * b + 8 * c4);
-                        const uint32_t x = w.x ^ 0x80808080u, y = w.y ^ 0x80808080u;
-                        a0[u] = __byte_perm(x, 0, 0x4140);
-                        a0[2 + u] = __byte_perm(x, 0, 0x4342);
-                        a1[u] = __byte_perm(y, 0, 0x4140);
-                        a1[2 + u] = __byte_perm(y, 0, 0x4342);
+                    for (int u = 0; u < 4; u++) w[u] ^= 0x80808080u;
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {  // values 4c, 4c + 1 and 4c + 2, 4c + 3 of a 16-value half
+                        a0[u] = __byte_perm(w[u], 0, 0x4140);
+                        a0[2 + u] = __byte_perm(w[u], 0, 0x4342);
+                        a1[u] = __byte_perm(w[2 + u], 0, 0x4140);
+                        a1[2 + u] = __byte_perm(w[2 + u], 0, 0x4342);
                     }
                     const float fa = __half2float(da[b]), fb = __half2float(db[b]);
 #pragma unroll
@@ -721,7 +728,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
 #pragma unroll
                 for (int u = 0; u < 4; u++) {
                     const int r = 2 * c4 + (u & 1) + 8 * (u >> 1);
-                    row_scales<D, EXACT>(vtp + L::VS, r, dim, dv[u]);
+                    row_scales<D, EXACT>(vtp + L::SCALES, r, dim, dv[u]);
                     if (!full && !vis(row0 + r)) {
 #pragma unroll
                         for (int b = 0; b < D / 32; b++) dv[u][b] = __ushort_as_half(0);
@@ -744,16 +751,14 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                 for (int b = 0; b < D / 32; b++) {
                     if (b * 32 >= dim) break;
                     uint32_t a0[4], a1[4];
+                    // transposed pairs of codes: rows 2c and 2c + 1 of values 2r, 2r + 1 (r = lane / 4)
+                    uint32_t w[4];
+                    ldsm4t(vt + at_v[0] + 32 * b, w);
 #pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        const uint8_t* vr = vtp + (2 * c4 + 8 * u) * L::PV + 32 * b + 4 * r8;
-                        const uint32_t x = *reinterpret_cast<const uint32_t*>(vr) ^ 0x80808080u;
-                        const uint32_t y = *reinterpret_cast<const uint32_t*>(vr + L::PV) ^ 0x80808080u;
-                        const uint32_t x01 = __byte_perm(x, y, 0x5140), x23 = __byte_perm(x, y, 0x7362);
-                        a0[2 * u] = h2u(__hsub2(u2h(__byte_perm(x01, 0x64646464u, 0x4140)), k1152));
-                        a0[2 * u + 1] = h2u(__hsub2(u2h(__byte_perm(x01, 0x64646464u, 0x4342)), k1152));
-                        a1[2 * u] = h2u(__hsub2(u2h(__byte_perm(x23, 0x64646464u, 0x4140)), k1152));
-                        a1[2 * u + 1] = h2u(__hsub2(u2h(__byte_perm(x23, 0x64646464u, 0x4342)), k1152));
+                    for (int u = 0; u < 4; u++) {
+                        w[u] ^= 0x80808080u;
+                        a0[u] = h2u(__hsub2(u2h(__byte_perm(w[u], 0x64646464u, 0x4240)), k1152));
+                        a1[u] = h2u(__hsub2(u2h(__byte_perm(w[u], 0x64646464u, 0x4341)), k1152));
                     }
                     const __half2 d0 = __hmul2(__halves2half2(dv[0][b], dv[1][b]), down), d1 = __hmul2(__halves2half2(dv[2][b], dv[3][b]), down);
 #pragma unroll
@@ -822,8 +827,8 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     for (int mt = 0; mt < KSTEPS; mt++) {
                         if (mt * 16 >= dim) break;
                         // rows lane/4 and lane/4 + 8 of the tile; Q8_0: the codes' order
-                        const int d0 = Q8 ? (mt >> 1) * 32 + 4 * r8 + 2 * (mt & 1) : mt * 16 + r8;
-                        const int d1 = Q8 ? d0 + 1 : d0 + 8;
+                        const int d0 = Q8 ? (mt >> 1) * 32 + 2 * r8 + (mt & 1) : mt * 16 + r8;
+                        const int d1 = Q8 ? d0 + 16 : d0 + 8;
                         buf[hd * D + d0] = o[mt][nt][j] * f;
                         buf[hd * D + d1] = o[mt][nt][j + 2] * f;
                     }

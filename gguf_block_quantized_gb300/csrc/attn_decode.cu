@@ -9,7 +9,7 @@
 //   - Warps work alone: each copies chunks of 16 rows of K and V into a ring of its own in shared
 //     memory (cp.async) and multiplies them with mma.sync m16n8k16, the 16 cached rows as the A
 //     operand and up to 8 query heads as the columns: S^T = K Q^T, then O^T += V^T P^T.  A
-//     chunk of 128-wide rows is about 380 instructions (F16) or 670 (Q8_0) of a warp, where its bytes
+//     chunk of 128-wide rows is about 390 instructions (F16) or 650 (Q8_0) of a warp, where its bytes
 //     take 1400 or 750 issue slots of an SM to arrive: Q8_0 is near the issue limit.
 //   - p is split into two fp16 numbers (head and tail, 22 bits) and each chunk's product starts
 //     from zero and is added to the fp32 sums by fma, because the tensor pipe's own additions
@@ -18,7 +18,8 @@
 //   - Q8_0 codes go into the products as they are, without their scales: exact in fp16.  A key's
 //     scale multiplies its block's 32-value sum, a value's scale goes into p, head and tail.  Key codes
 //     go in with 128 added, as subnormal numbers, and the sums start from what that adds (no
-//     subtraction a code: with the value scales' product in fp16 pairs 740 -> 672 instructions a chunk).
+//     subtraction a code).  Value codes are subtracted from: as subnormals they need two more products a
+//     block, 175 us against 169 below, and lose a few bits to the tensor pipe's truncation.
 //   - Work is cut by length, not by sequence: the steps (4 chunks, one per warp) of all
 //     (sequence, kv head) items, and some for each item's start and end, are dealt to the CTAs in
 //     equal contiguous ranges, found on the device from the lengths (a captured graph keeps working
@@ -27,7 +28,7 @@
 //     that finishes an item last (a counter) joins the partials in order.  No CTA waits.
 //
 // Measured on GB300, 32 / 8 heads of 128 (share of a copy's rate): 300 sequences of 2500 rows, F16 96 %,
-// Q8_0 71 %; 48 sequences of 100 to 4000, F16 44.4 us, 71 %; 128 of 500 to 8191, Q8_0, capped 175 us, 65 %;
+// Q8_0 71 %; 48 sequences of 100 to 4000, F16 44.4 us, 71 %; 128 of 500 to 8191, Q8_0, capped 169 us, 67 %;
 // one of 130001, F16 92 us, 85 %; one of 77 (heads of 64) 5.2 us.
 #include <algorithm>
 #include <climits>

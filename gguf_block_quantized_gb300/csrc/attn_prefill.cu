@@ -1039,11 +1039,13 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                     if (tl.b1 > tl.b0) tl.a1 = max(tl.a0, min(tl.a1, tl.b0));
                 }
                 const int all = tl.count();
-                // Each part more shortens what a part computes and lengthens the join: sqrt(keys / 64) parts, at
-                // least a tile each.  Measured, one sequence, 32 / 8 heads of 128 (us): 64 tokens over 4096 keys
+                // Each part more shortens what a part computes and lengthens the join: sqrt(keys / 64) parts.
+                // Measured, one sequence, 32 / 8 heads of 128 (us): 64 tokens over 4096 keys
                 // in 16 parts 44, 8 (the rule) 39, 4 39, 2 50; 24 / 1 heads, 8 tokens over 32000 in 125 parts
                 // 145, 22 (the rule) 57; heads of 256, 32 over 4096 in 32 parts 72, 8 45.
-                it.n_split = min(min(max_split, max(all, 1)), max(1, (int)sqrtf((float)all * (BN / 64))));
+                // Up to 512 keys, or 768 where the join has many values, it does not pay: 9 tokens over 400 keys in
+                // 2 parts 17.4, whole 15.2, over 709 in 3 parts 17.0, whole 18.1; 64 over 709 26.6 and 21.7.
+                it.n_split = all * BN <= (it.rows * dim < 16384 ? 512 : 768) ? 1 : min(max_split, (int)sqrtf((float)all * (BN / 64)));
                 it.t0 = (int)((int64_t)all * min(it.sp, it.n_split) / it.n_split);
                 it.nt = it.sp < it.n_split ? (int)((int64_t)all * (it.sp + 1) / it.n_split) - it.t0 : -2;
             }

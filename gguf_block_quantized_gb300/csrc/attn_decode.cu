@@ -349,7 +349,10 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
     // Little work is dealt in blocks of several steps, one a CTA: 3, as a step's loads are in flight
     // together with the next ones', and more where the longest item would have so many parts that their
     // join (heads * dim values a part, by one CTA) took longer than the steps.
-    const int few = max(3, (int)ceilf(sqrtf((float)flags[6] * (float)(min(H, p.g) * dim) * DEC_JOIN)));
+    // Items of 6 steps or fewer (8 where the join has many values) stay whole: 1 sequence of 400 rows in 3
+    // parts / whole (us), F16 32 / 8 heads of 64 9.8 / 8.2, 16 / 1 of 128 15.4 / 11.6; of 709, 10.4 / 12.2 and 15.8 / 17.0.
+    const int values = min(H, p.g) * dim, most = flags[6];
+    const int few = max(most <= (values < 1024 ? 6 : 8) ? most : 3, (int)ceilf(sqrtf((float)most * (float)values * DEC_JOIN)));
     int block = !p.whole && steps * n_item_h <= (int64_t)few * gridDim.x ? few : 1;
     if (steps >> 30) block = max(block, (int)(steps >> 30) + 1);  // (the running sum has 32 bits)
     // Else an item counts DEC_ITEM steps more than it has: what its start and its end cost.

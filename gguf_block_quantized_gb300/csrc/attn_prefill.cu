@@ -31,7 +31,7 @@
 // Measured on GB300, 32 / 8 heads of 128, F16: a prompt of 8192 tokens 395 us, 1.39 PFLOP/s (73 % of
 // a library matrix product's rate: a tile of 128 keys takes 2700 cycles, the products of its
 // two row tiles 2048: a row tile's softmax, 1450 cycles, stands between its two products); 6 prompts of up to 1001 tokens, capped in a window of 1024, 68 us; 2 chunks of up
-// to 2000 tokens over 8000 Q8_0 rows, slopes and documents, 105 us; 9 tokens over 709 rows, heads of 64, 12.9 us.
+// to 2000 tokens over 8000 Q8_0 rows, slopes and documents, 105 us; 9 tokens over 709 rows, heads of 64, 12.6 us.
 #include <algorithm>
 #include <climits>
 
@@ -713,10 +713,12 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 for (int x = 0; x < it.n_split; x++) weight[x * R + tid] = ex2(weight[x * R + tid] - ms) * inv;
             }
             if (!softmax_sync()) break;
-            // a thread joins 4 values of 4 rows at a time, the loads of 4 parts (16 float4) in flight together
-            const int quads = (it.rows + 3) >> 2;
-            for (int u = tid; u < quads * (dim >> 2); u += R) {
-                const int e = u / quads << 2, r4 = (u - (u / quads) * quads) << 2;
+            // A thread joins 4 values of 4 rows at a time, the loads of 4 parts (16 float4) in flight together; a
+            // warp 16 values of 32 rows, so that its loads are whole lines and its stores whole sectors.
+            const int row_blocks = (it.rows + 31) >> 5;
+            for (int u = tid >> 5; u < row_blocks * (dim >> 4); u += R / 32) {
+                const int e = (u / row_blocks << 4) + ((lane >> 3) << 2), r4 = (u - (u / row_blocks) * row_blocks) * 32 + ((lane & 7) << 2);
+                if (r4 >= it.rows) continue;
                 float acc[4][4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;

@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
 #pragma unroll
                             for (int c = 0; c < N; c += 2)
                                 big = fmaxf(fmaxf(big, fabsf(__uint_as_float(v[c]))), fabsf(__uint_as_float(v[c + 1])));
-                            small = __all_sync(0xffffffffu, big * to_cap <= 0.5f);
+                            small = __all_sync(0xffffffffu, big * fabsf(to_cap) <= 0.5f);  // (the scale may be negative)
                         }
                         if (small) {
                             // Scores up to half the cap in size: tanh(y) = y times a polynomial in y^2, fitted on

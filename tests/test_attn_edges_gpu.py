@@ -1,0 +1,49 @@
+"""The paged-cache operators on the GPU at the edges of what they accept: signs, sizes and value ranges
+of the options, tables and lengths that do not agree, and what a query must not notice."""
+import os
+import sys
+
+import numpy as np
+import pytest
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+import attn_ref  # noqa: E402
+from test_attn_gpu import F16, Q8_0, make_cache, options, prefill_bound, decode_bound, reference, syn  # noqa: E402,F401
+from test_attn_paths_gpu import launches  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+# Prefill's ways: an F16 cache, a Q8_0 cache expanded in the kernel (few rows), one expanded ahead of it
+# (8 heads on a kv head, from 256 new tokens with a cap or slopes on).
+WAYS = [(F16, 60), (Q8_0, 60), (Q8_0, 270)]
+
+
+def on(x, dtype=None):
+    import torch
+    y = torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    return y if dtype is None else y.to(dtype)
+
+
+def int32(x):
+    import torch
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ---- a cap and a scale below zero ----------------------------------------------------------
+# (q with the scale -s is -q with the scale s, exactly; the tolerances are those of the positive scale)
+
+@pytest.mark.parametrize("t,new", WAYS)
+@pytest.mark.parametrize("cap,qscale", [(5.0, 1.0), (1.0, 2.0), (50.0, 0.1)])
+def test_cap_with_a_negative_scale(syn, t, new, cap, qscale):
+    rng = np.random.default_rng([t, new, 41])
+    heads, n = 8, new + 50
+    cache, pages, seqs = make_cache(syn, rng, t, 1, 64, 16, [n])
+    q = (qscale * rng.standard_normal((new, heads, 64))).astype(np.float16)
+    ref, size = attn_ref.attention(-q, *seqs[0], np.arange(n - new, n), np.zeros(new), 0, 0, 0.2, cap, None)
+    call = syn.prepare_attn_prefill(cache, on(q), int32([0, new]), pages, int32([n]), scale=-0.2, cap=cap)
+    assert launches(syn, call) == (2 if new > 256 else 1)
+    got = call().double().cpu().numpy()
+    assert (np.abs(got - ref) <= prefill_bound(t, size, np.abs(seqs[0][1]).max(), ref, False)).all()
+    one = syn.attn_decode(cache, on(q[-1:]), pages, int32([n]), scale=-0.2, cap=cap).double().cpu().numpy()
+    assert (np.abs(one - ref[-1:]) <= decode_bound(size[-1:], ref[-1:], False)).all()
+    assert syn.device_status() == syn.OK

@@ -31,7 +31,6 @@
 // Q8_0 71 %; 48 sequences of 100 to 4000, F16 44.4 us, 71 %; 128 of 500 to 8191, Q8_0, capped 169 us, 67 %;
 // one of 130001, F16 92 us, 85 %; one of 77 (heads of 64) 5.2 us.
 #include <algorithm>
-#include <climits>
 
 #include "kernels.h"
 #include "kv_cache.cuh"
@@ -145,9 +144,7 @@ struct Chunks {
 };
 
 __device__ __forceinline__ int seq_len(const DecodeParams& p, int s) {
-    const int64_t most = min(p.max_pages << p.c.page_shift, (int64_t)INT_MAX - 64);
-    const int len = p.lens[s];
-    return len < 0 ? 0 : (int)min((int64_t)len, most);
+    return held_rows(p.lens[s], p.max_pages, p.c.page_shift);
 }
 
 __device__ __forceinline__ Visible seq_visible(const DecodeParams& p, int s, int len) {

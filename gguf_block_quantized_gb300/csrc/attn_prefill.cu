@@ -1000,7 +1000,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 }
                 it.n_new = new_tokens(it.s);
                 it.tok0 = p.starts[it.s];
-                it.len = min(max(p.lens[it.s], 0), (int)min(p.max_pages << p.c.page_shift, (int64_t)INT_MAX - 1024));
+                it.len = held_rows(p.lens[it.s], p.max_pages, p.c.page_shift);
                 it.prefix = p.prefix ? p.prefix[it.s] : 0;
                 it.row0 = (qtile - before) * R;
                 it.rows = (int)min((int64_t)R, (int64_t)it.n_new * p.g - it.row0);
@@ -1220,7 +1220,7 @@ __global__ void __launch_bounds__(256) k_kv_expand(const ExpandParams p) {
         const int hp = (int)(u - sp * 2 * p.c.n_kv), h = hp >> 1, is_v = hp & 1;
         const int s = (int)(sp / p.max_pages);
         const int64_t i = sp - s * p.max_pages, row0 = i << p.c.page_shift;
-        const int len = p.lens[s];
+        const int len = held_rows(p.lens[s], p.max_pages, p.c.page_shift);
         // (rows ahead of every query's window are not read by anyone)
         // (but all of a tile that a query's window begins in: no number that was never written meets p = 0)
         const int64_t low = p.window > 0 ? ((int64_t)len - max(p.starts[s + 1] - p.starts[s], 0) - p.window) & ~int64_t(127) : 0;

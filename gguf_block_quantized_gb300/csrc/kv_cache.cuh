@@ -9,6 +9,8 @@
 // both planes of a tile do: page_size >= 8 and dim % 32 == 0 make page_size*dim and
 // page_size*dim/16 multiples of 16.
 #pragma once
+#include <climits>
+
 #include "common.cuh"
 
 namespace syn {
@@ -21,6 +23,12 @@ struct KvCache {
     int64_t tile;         // bytes of one head's rows of a page
     int n_kv, dim, page_shift, q8;
 };
+
+// The rows of a sequence: a length is cut to what its page table holds (and to what leaves room in 32
+// bits for a row number rounded up to a tile); every kernel that reads lens[] goes by this.
+__device__ __forceinline__ int held_rows(int len, int64_t max_pages, int page_shift) {
+    return (int)min((int64_t)max(len, 0), min(max_pages << page_shift, (int64_t)INT_MAX - 1024));
+}
 
 // The keys a query at position pos of a sequence of len rows sees:
 //   first <= j < len and (j < pre or (low <= j <= pos)),  low = the window's first key.

@@ -47,3 +47,28 @@ def test_cap_with_a_negative_scale(syn, t, new, cap, qscale):
     one = syn.attn_decode(cache, on(q[-1:]), pages, int32([n]), scale=-0.2, cap=cap).double().cpu().numpy()
     assert (np.abs(one - ref[-1:]) <= decode_bound(size[-1:], ref[-1:], False)).all()
     assert syn.device_status() == syn.OK
+
+
+# ---- a length past what the page table holds -----------------------------------------------
+
+@pytest.mark.parametrize("t,new", WAYS)
+@pytest.mark.parametrize("window", [0, 40])
+def test_length_past_the_page_table(syn, t, new, window):
+    """Such a length is cut to the table: the bits of the call with the cut length, whatever the
+    workspace held before."""
+    rng = np.random.default_rng([t, new, 42])
+    heads, held = 8, 512
+    cache, pages, _ = make_cache(syn, rng, t, 1, 64, 16, [held])
+    other, _, _ = make_cache(syn, rng, t, 1, 64, 16, [held])
+    q = on(rng.standard_normal((new, heads, 64)).astype(np.float16))
+    slopes = on(2.0 ** -np.arange(1, heads + 1).astype(np.float32))
+    opt = {"window": window, "slopes": slopes}
+    starts = int32([0, new])
+    syn.attn_prefill(other, q, starts, pages, int32([held]), slopes=slopes)
+    got = syn.attn_prefill(cache, q, starts, pages, int32([1000]), **opt)
+    one = syn.attn_decode(cache, q[:1], pages, int32([1000]), **opt)
+    want = syn.attn_prefill(cache, q, starts, pages, int32([held]), **opt)
+    import torch
+    assert torch.equal(got, want)
+    assert torch.equal(one, syn.attn_decode(cache, q[:1], pages, int32([held]), **opt))
+    assert syn.device_status() == syn.OK

@@ -429,41 +429,45 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 auto finish = [&](auto& v, int c0) {
                     constexpr int N = sizeof(v) / 4;
                     if (MOD) {
-                        bool small = false;
                         if (p.cap > 0.0f) {
+                            // Scores up to half the cap in size: tanh(y) = y times a polynomial in y^2, fitted on
+                            // [0, 1/2] to 3e-7, the scale and the cap folded into its coefficients: five paired
+                            // instructions for two scores, and none of the two special-function ones a score of
+                            // the general form, which has to share that unit with the powers.  Each score goes
+                            // by its own size, so that its bits do not depend on the others'; the vote only spares
+                            // the general form where no score needs it (keys that a row does not see may vote).
+                            const float k = to_cap * to_cap, to_half = fabsf(to_cap);  // (the scale may be negative)
+                            const float a0 = 0.999999464f * c_log2, a1 = -0.333263761f * c_log2 * k, a2 = 0.131909124f * c_log2 * k * k,
+                                        a3 = -0.0444185817f * c_log2 * k * k * k;
+                            const uint64_t b0 = pack2(a0, a0), b1 = pack2(a1, a1), b2 = pack2(a2, a2), b3 = pack2(a3, a3);
+                            auto small2 = [&](uint64_t x) {
+                                const uint64_t z = mul2(x, x);
+                                return unpack2(mul2(x, fma2(z, fma2(z, fma2(z, b3, b2), b1), b0)));
+                            };
                             float big = 0.0f;
 #pragma unroll
                             for (int c = 0; c < N; c += 2)
                                 big = fmaxf(fmaxf(big, fabsf(__uint_as_float(v[c]))), fabsf(__uint_as_float(v[c + 1])));
-                            small = __all_sync(0xffffffffu, big * fabsf(to_cap) <= 0.5f);  // (the scale may be negative)
-                        }
-                        if (small) {
-                            // Scores up to half the cap in size: tanh(y) = y times a polynomial in y^2, fitted on
-                            // [0, 1/2] to 3e-7, the scale and the cap folded into its coefficients: five paired
-                            // instructions for two scores, and none of the two special-function ones a score of
-                            // the general form, which has to share that unit with the powers.
-                            const float k = to_cap * to_cap;
-                            const float a0 = 0.999999464f * c_log2, a1 = -0.333263761f * c_log2 * k, a2 = 0.131909124f * c_log2 * k * k,
-                                        a3 = -0.0444185817f * c_log2 * k * k * k;
-                            const uint64_t b0 = pack2(a0, a0), b1 = pack2(a1, a1), b2 = pack2(a2, a2), b3 = pack2(a3, a3);
+                            if (__all_sync(0xffffffffu, big * to_half <= 0.5f)) {
 #pragma unroll
-                            for (int c = 0; c < N; c += 2) {
-                                const uint64_t x = pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), z = mul2(x, x);
-                                const float2 r2 = unpack2(mul2(x, fma2(z, fma2(z, fma2(z, b3, b2), b1), b0)));
-                                v[c] = __float_as_uint(r2.x);
-                                v[c + 1] = __float_as_uint(r2.y);
-                            }
-                        } else if (p.cap > 0.0f) {
-                            // cap*tanh(x/cap) = cap - 2 cap/(1 + 2^(2 x log2(e)/cap)), all in powers of two
-                            const uint64_t k2 = pack2(to_cap2, to_cap2), one2 = pack2(1.0f, 1.0f);
-                            const uint64_t m2 = pack2(-2.0f * cap_log2, -2.0f * cap_log2), cap2 = pack2(cap_log2, cap_log2);
+                                for (int c = 0; c < N; c += 2) {
+                                    const float2 r2 = small2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
+                                    v[c] = __float_as_uint(r2.x);
+                                    v[c + 1] = __float_as_uint(r2.y);
+                                }
+                            } else {
+                                // cap*tanh(x/cap) = cap - 2 cap/(1 + 2^(2 x log2(e)/cap)), all in powers of two
+                                const uint64_t k2 = pack2(to_cap2, to_cap2), one2 = pack2(1.0f, 1.0f);
+                                const uint64_t m2 = pack2(-2.0f * cap_log2, -2.0f * cap_log2), cap2 = pack2(cap_log2, cap_log2);
 #pragma unroll
-                            for (int c = 0; c < N; c += 2) {
-                                const float2 y = unpack2(mul2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2));
-                                const float2 z = unpack2(add2(pack2(ex2(y.x), ex2(y.y)), one2));
-                                const float2 x = unpack2(fma2(pack2(rcp(z.x), rcp(z.y)), m2, cap2));
-                                v[c] = __float_as_uint(x.x);
-                                v[c + 1] = __float_as_uint(x.y);
+                                for (int c = 0; c < N; c += 2) {
+                                    const float v0 = __uint_as_float(v[c]), v1 = __uint_as_float(v[c + 1]);
+                                    const float2 r2 = small2(pack2(v0, v1)), y = unpack2(mul2(pack2(v0, v1), k2));
+                                    const float2 z = unpack2(add2(pack2(ex2(y.x), ex2(y.y)), one2));
+                                    const float2 x = unpack2(fma2(pack2(rcp(z.x), rcp(z.y)), m2, cap2));
+                                    v[c] = __float_as_uint(fabsf(v0) * to_half <= 0.5f ? r2.x : x.x);
+                                    v[c + 1] = __float_as_uint(fabsf(v1) * to_half <= 0.5f ? r2.y : x.y);
+                                }
                             }
                         }
                         // (not capped: still to be scaled; c_log2 or 1)

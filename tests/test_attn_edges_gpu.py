@@ -72,3 +72,56 @@ def test_length_past_the_page_table(syn, t, new, window):
     assert torch.equal(got, want)
     assert torch.equal(one, syn.attn_decode(cache, q[:1], pages, int32([held]), **opt))
     assert syn.device_status() == syn.OK
+
+
+# ---- what a query does not see, and the bits of a capped score ------------------------------
+
+@pytest.mark.parametrize("t", [F16, Q8_0])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_deterministic_capped_prefill_alone_and_in_a_batch(syn, t, dim):
+    """In deterministic mode a sequence has the same bits alone and with others whose scores are far
+    larger (rows of theirs share its tiles)."""
+    import torch
+    rng = np.random.default_rng([t, dim, 43])
+    heads, lens, new = 4, [50, 300, 40], [10, 70, 33]
+    cache, pages, _ = make_cache(syn, rng, t, 1, dim, 16, lens)
+    st = np.concatenate([[0], np.cumsum(new)])
+    q = rng.standard_normal((st[-1], heads, dim)) * np.repeat([0.3, 30.0, 1.0], new)[:, None, None]
+    q, ld = on(q.astype(np.float16)), int32(lens)
+    old = syn.set_deterministic(True)
+    try:
+        both = syn.attn_prefill(cache, q, int32(st), pages, ld, cap=8.0)
+        for s in range(3):
+            one = syn.attn_prefill(cache, q[st[s]:st[s + 1]].contiguous(), int32([0, new[s]]), pages[s:s + 1].contiguous(),
+                                   ld[s:s + 1].contiguous(), cap=8.0)
+            assert torch.equal(one, both[st[s]:st[s + 1]]), s
+    finally:
+        syn.set_deterministic(old)
+
+
+@pytest.mark.parametrize("t,new", WAYS)
+@pytest.mark.parametrize("opt", [{"cap": 8.0}, {"cap": 8.0, "slopes": True}, {"cap": 8.0, "window": 20}, {}])
+def test_unseen_keys_do_not_change_bits(syn, t, new, opt):
+    """Tokens give the same bits whatever the keys after them (and past the sequence's end) hold."""
+    import torch
+    rng = np.random.default_rng([t, new, 44])
+    heads, dim, page, n = 8, 64, 16, new + 21
+    cache, pages, _ = make_cache(syn, rng, t, 1, dim, page, [n], garbage=0.25)
+    q = on((0.3 * rng.standard_normal((new, heads, dim))).astype(np.float16))
+    kw = dict(opt)
+    if kw.pop("slopes", False):
+        kw["slopes"] = on(2.0 ** -np.arange(1, heads + 1).astype(np.float32))
+    call = syn.prepare_attn_prefill(cache, q, int32([0, new]), pages, int32([n]), **kw)
+    want = call().clone()
+    j = n - 9  # the keys from here on grow a hundredfold, those past the end too
+    for row in range(j, -(-n // page) * page):
+        pg, cell = int(pages[0, row // page]), row % page
+        if t == F16:
+            cache.k[pg, :, cell] *= 100
+        else:
+            at = page * dim + cell * dim // 16
+            s = cache.k[pg, 0, at:at + dim // 16].view(torch.float16)
+            s.copy_(s * 100)
+    got = call()
+    assert torch.equal(got[:new - 9], want[:new - 9])
+    assert not torch.equal(got[new - 9:], want[new - 9:])

@@ -16,7 +16,10 @@
 //     truncate.  Scores likewise come from short chains.  So the result is as exact as fp32
 //     arithmetic allows, which fp32 outputs show.
 //   - Q8_0 codes go into the products as they are, without their scales: exact in fp16.  A key's
-//     scale multiplies its block's 32-value sum, a value's scale goes into p, head and tail.  Key codes
+//     scale multiplies its block's 32-value sum, a value's scale goes into p, head and tail, relative to the
+//     power of two of its row's largest, which goes into the running maximum: what is kept of a row goes by what
+//     it adds to the output (a scale relative to the largest so far: 169 us for 176 below, and a row of large
+//     values with no weight cost the others up to 1 % of their own).  Key codes
 //     go in with 128 added, as subnormal numbers, and the sums start from what that adds (no
 //     subtraction a code).  Value codes are subtracted from: as subnormals they need two more products a
 //     block, 175 us against 169 below, and lose a few bits to the tensor pipe's truncation.
@@ -48,7 +51,9 @@ constexpr int DEC_ITEM = 2;
 constexpr float DEC_JOIN = 2e-4f;
 constexpr int DEC_MAX_SEQ = 1024;  // sequences of one launch (their step counts are in shared memory)
 constexpr uint32_t MINUS_128 = 0x80808080u;  // -128 * 2^-24 as fp16, twice
-constexpr float DEC_P_LOG2 = 14.0f;  // p is held as 2^14 p, in fp16: small p stay normal numbers
+// p is held in fp16 as 2^14 p, so that small p stay normal numbers; Q8_0 as 2^13 p: times a relative scale below 4
+template <bool Q8>
+constexpr float DEC_P_LOG2 = Q8 ? 13.0f : 14.0f;
 
 struct DecodeParams {
     KvCache c;
@@ -509,7 +514,6 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
             }
 
         float m[NT][2], l[NT][2];
-        int e_run = 0;  // Q8_0: o is held relative to 2^(e_run - 15)
         float o[KSTEPS][NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
@@ -673,6 +677,45 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
             __syncwarp();  // every lane has read the keys before their slot is filled again
             issue_v(sk);
 
+            // Q8_0: a row's weight in the product is p times its value scales.  The power of two of the row's
+            // largest scale, 2^e, goes into the score, so that the running maximum m is that of what the rows add
+            // to o, and a row of large values that has next to no weight takes no bits from the others; the scales
+            // go in relative to it, d * 2^(1 - e) in [2, 4) for the largest (an fp16 product that is exact down to
+            // 2^-15 of that).  The sum l takes p * 2^(1 - e): o and l are in the same units.
+            alignas(16) __half dv[Q8 ? 4 : 1][D / 32];  // scales of rows 2c, 2c + 1, 2c + 8, 2c + 9
+            uint32_t down[2];                           // 2^(1 - e) of rows 2c, 2c + 1 and of 2c + 8, 2c + 9
+            float row_e[2] = {0.0f, 0.0f}, row_down[2] = {1.0f, 1.0f};  // of rows lane/4, lane/4 + 8
+            if constexpr (Q8) {
+                cp_wait<2>();  // (the values)
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < 2; u++) {
+                    __half2 top[2];
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        const int r = 2 * c4 + x + 8 * u;
+                        row_scales<D, EXACT>(vtp + L::SCALES, r, dim, dv[2 * u + x]);
+                        if (!full && !vis(row0 + r)) {
+#pragma unroll
+                            for (int b = 0; b < D / 32; b++) dv[2 * u + x][b] = __ushort_as_half(0);
+                        }
+                        top[x] = __habs2(*reinterpret_cast<const __half2*>(&dv[2 * u + x][0]));
+#pragma unroll
+                        for (int b = 2; b < D / 32; b += 2) top[x] = __hmax2(top[x], __habs2(*reinterpret_cast<const __half2*>(&dv[2 * u + x][b])));
+                    }
+                    // the larger half of either row's, its power of two between 2^-14 and 2^15
+                    const __half2 both = __hmax2(u2h(__byte_perm(h2u(top[0]), h2u(top[1]), 0x5410)), u2h(__byte_perm(h2u(top[0]), h2u(top[1]), 0x7632)));
+                    const __half2 power = __hmin2(__hmax2(u2h(h2u(both) & 0x7C007C00u), u2h(0x04000400u)), u2h(0x78007800u));
+                    down[u] = 0x7C007C00u - h2u(power);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; u++) {
+                    const uint32_t w = __shfl_sync(0xffffffffu, down[u], r8 >> 1);  // (lane c holds rows 2c, 2c + 1)
+                    row_down[u] = __half2float(__ushort_as_half((unsigned short)(w >> (16 * (r8 & 1)))));
+                    row_e[u] = 8388736.0f - __uint_as_float((__float_as_uint(row_down[u]) >> 23) | 0x4B000000u);  // (2^23 + 128 less 2^23 + its exponent)
+                }
+            }
+
             // softmax of the chunk, in powers of two
             uint32_t ph[NT][2], pl[NT][2];  // P^T as the B operand (heads and tails)
             float alpha[NT][2];
@@ -684,11 +727,12 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     for (int j = 0; j < 4; j++) {
                         float x = sc[nt][j] * scale;
                         if (p.cap > 0.0f) x = p.cap * tanh_rel(x * p.inv_cap);
-                        sc[nt][j] = fmaf(-slope[nt][j & 1], (float)(len - 1 - row0 - r8 - (j >> 1) * 8), x) * LOG2E;
+                        const float y = fmaf(-slope[nt][j & 1], (float)(len - 1 - row0 - r8 - (j >> 1) * 8), x);
+                        sc[nt][j] = Q8 ? fmaf(y, LOG2E, row_e[j >> 1]) : y * LOG2E;
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 4; j++) sc[nt][j] *= scale_log2;
+                    for (int j = 0; j < 4; j++) sc[nt][j] = Q8 ? fmaf(sc[nt][j], scale_log2, row_e[j >> 1]) : sc[nt][j] * scale_log2;
                 }
                 if (!full) {
                     if (!vis(row0 + r8)) sc[nt][0] = sc[nt][1] = -INFINITY;
@@ -703,9 +747,9 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     const float ms = mx == -INFINITY ? 0.0f : mx;  // nothing seen yet
                     alpha[nt][j] = ex2(m[nt][j] - ms);
                     m[nt][j] = mx;
-                    pr[j] = ex2(sc[nt][j] - (ms - DEC_P_LOG2));
-                    pr[j + 2] = ex2(sc[nt][j + 2] - (ms - DEC_P_LOG2));
-                    l[nt][j] = fmaf(l[nt][j], alpha[nt][j], pr[j] + pr[j + 2]);
+                    pr[j] = ex2(sc[nt][j] - (ms - DEC_P_LOG2<Q8>));
+                    pr[j + 2] = ex2(sc[nt][j + 2] - (ms - DEC_P_LOG2<Q8>));
+                    l[nt][j] = fmaf(l[nt][j], alpha[nt][j], Q8 ? fmaf(pr[j], row_down[0], pr[j + 2] * row_down[1]) : pr[j] + pr[j + 2]);
                 }
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
@@ -715,38 +759,15 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     pl[nt][i] = transpose8(lo);
                 }
             }
-            cp_wait<2>();
-            __syncwarp();
+            if (!Q8) {
+                cp_wait<2>();
+                __syncwarp();
+            }
 
             // O^T = O^T * alpha + V^T P^T
-            if (Q8) {
-                // A row's value scales go into p: with d' the scale relative to 2^e, e the largest exponent
-                // among the scales so far (o is kept in units of 2^e, as it is relative to 2^m), the head
-                // of p * d' is h = fp16(p_hi * d'), and its tail p_lo * d' + (p_hi * d' - h), the bracket
-                // exact in one fma.
-                alignas(16) __half dv[4][D / 32];  // scales of rows 2c, 2c+1, 2c+8, 2c+9
-                __half2 top2 = __float2half2_rn(0.0f);
-#pragma unroll
-                for (int u = 0; u < 4; u++) {
-                    const int r = 2 * c4 + (u & 1) + 8 * (u >> 1);
-                    row_scales<D, EXACT>(vtp + L::SCALES, r, dim, dv[u]);
-                    if (!full && !vis(row0 + r)) {
-#pragma unroll
-                        for (int b = 0; b < D / 32; b++) dv[u][b] = __ushort_as_half(0);
-                    }
-#pragma unroll
-                    for (int b = 0; b < D / 32; b += 2) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2*>(&dv[u][b])));
-                }
-                const uint32_t t2 = h2u(top2), top = max(t2 & 0xFFFFu, t2 >> 16);
-                const int e_new = max(e_run, (int)(__reduce_max_sync(0xffffffffu, top) >> 10));
-                const float step = __int_as_float((127 + e_run - e_new) << 23);
-                const __half2 down = __float2half2_rn(__int_as_float((127 + 15 - e_new) << 23));
-                e_run = e_new;
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++) {
-                    alpha[nt][0] *= step;
-                    alpha[nt][1] *= step;
-                }
+            if constexpr (Q8) {
+                // with d' a relative scale, the head of p * d' is h = fp16(p_hi * d'), and its tail
+                // p_lo * d' + (p_hi * d' - h), the bracket exact in one fma
                 const __half2 k1152 = __float2half2_rn(1152.0f);
 #pragma unroll
                 for (int b = 0; b < D / 32; b++) {
@@ -761,7 +782,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                         a0[u] = h2u(__hsub2(u2h(__byte_perm(w[u], 0x64646464u, 0x4240)), k1152));
                         a1[u] = h2u(__hsub2(u2h(__byte_perm(w[u], 0x64646464u, 0x4341)), k1152));
                     }
-                    const __half2 d0 = __hmul2(__halves2half2(dv[0][b], dv[1][b]), down), d1 = __hmul2(__halves2half2(dv[2][b], dv[3][b]), down);
+                    const __half2 d0 = __hmul2(__halves2half2(dv[0][b], dv[1][b]), u2h(down[0])), d1 = __hmul2(__halves2half2(dv[2][b], dv[3][b]), u2h(down[1]));
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
                         const __half2 h0 = __hmul2(u2h(ph[nt][0]), d0), h1 = __hmul2(u2h(ph[nt][1]), d1);
@@ -820,9 +841,8 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                 const int hd = nt * 8 + 2 * c4 + j;
                 float mx = sm_m[hd];
                 for (int w = 1; w < DEC_WARPS; w++) mx = fmaxf(mx, sm_m[w * H + hd]);
-                float f = ex2(m[nt][j] - (mx == -INFINITY ? 0.0f : mx));
+                const float f = ex2(m[nt][j] - (mx == -INFINITY ? 0.0f : mx));
                 if (r8 == 0) sm_l[warp * H + hd] = l[nt][j] * f;  // (read after the next barrier)
-                if (Q8) f *= __int_as_float((127 - 15 + e_run) << 23);
                 if (hd < heads) {
 #pragma unroll
                     for (int mt = 0; mt < KSTEPS; mt++) {

@@ -125,3 +125,53 @@ def test_unseen_keys_do_not_change_bits(syn, t, new, opt):
     got = call()
     assert torch.equal(got[:new - 9], want[:new - 9])
     assert not torch.equal(got[new - 9:], want[new - 9:])
+
+
+# ---- decode over Q8_0: values and keys of unlike sizes in a row ---------------------------
+
+def q8_pool(codes, scales, page):
+    """(rows, dim) codes and (rows, dim / 32) scales as a pool of one kv head, pages in order."""
+    rows, dim = codes.shape
+    n = -(-rows // page)
+    c = np.zeros((n * page, dim), np.int8)
+    d = np.zeros((n * page, dim // 32), np.float16)
+    c[:rows], d[:rows] = codes, scales
+    raw = np.concatenate([c.reshape(n, 1, -1).view(np.uint8), d.reshape(n, 1, -1).view(np.uint8)], -1)
+    return on(raw)
+
+
+def q8_rows(x):
+    """Rows as codes and scales, and the values that they stand for."""
+    b = x.reshape(len(x), -1, 32)
+    d = (np.abs(b).max(-1) / 127).astype(np.float16)
+    c = np.clip(np.rint(b / np.where(d == 0, 1, d).astype(np.float64)[..., None]), -127, 127).astype(np.int8)
+    return c.reshape(x.shape), d, (c * d.astype(np.float64)[..., None]).reshape(x.shape)
+
+
+# A row of large values that a head gives next to no weight (its score is 60 below the others': weight
+# e^-60) does not limit how exactly that head's output is held: the bound is decode_bound's with the
+# largest |v| and A of the other rows.  2^-30 max|v| e^-30 and less is what the row itself may add.
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("large,small", [(1e4, 0.1), (6e4, 0.1), (6e4, 0.01)])
+@pytest.mark.parametrize("at", [0, 300, 699])
+def test_decode_large_value_row_without_weight(syn, dim, large, small, at):
+    rng = np.random.default_rng([dim, int(large), at])
+    n, heads, page = 700, 4, 16
+    u = rng.choice([-1.0, 1.0], dim)
+    k = 0.3 * rng.standard_normal((n, dim))
+    k[at] = -u * 60 / np.sqrt(dim)
+    v = small * rng.standard_normal((n, dim))
+    v[at] *= large / small
+    kc, kd, kx = q8_rows(k)
+    vc, vd, vx = q8_rows(v)
+    cache = syn.KVCache(Q8_0, 1, dim, page, q8_pool(kc, kd, page), q8_pool(vc, vd, page))
+    q = (u + 0.3 * rng.standard_normal((heads, dim))).astype(np.float16)[None]
+    q[0, 2] = -u  # (one head gives that row all its weight)
+    pages = int32(np.arange(-(-n // page))[None])
+    ref, size = attn_ref.attention(q, kx[:, None], vx[:, None], np.array([n - 1]), np.zeros(1), 0, 0, dim ** -0.5, 0.0, None)
+    others = np.arange(n) != at
+    _, mine = attn_ref.attention(q, kx[others, None], vx[others, None], np.array([n - 2]), np.zeros(1), 0, 0, dim ** -0.5, 0.0, None)
+    mine[:, 2] = size[:, 2]
+    got = syn.attn_decode(cache, on(q), pages, int32([n])).double().cpu().numpy()
+    err = np.abs(got - ref)
+    assert (err <= decode_bound(mine, ref, False)).all(), (err / mine).max((0, 2)) * 2.0 ** 20

@@ -18,11 +18,10 @@
 //   - Q8_0 codes go into the products as they are, without their scales: exact in fp16.  A key's
 //     scale multiplies its block's 32-value sum, a value's scale goes into p, head and tail, relative to the
 //     power of two of its row's largest, which goes into the running maximum: what is kept of a row goes by what
-//     it adds to the output (a scale relative to the largest so far: 169 us for 176 below, and a row of large
-//     values with no weight cost the others up to 1 % of their own).  Key codes
-//     go in with 128 added, as subnormal numbers, and the sums start from what that adds (no
-//     subtraction a code).  Value codes are subtracted from: as subnormals they need two more products a
-//     block, 175 us against 169 below, and lose a few bits to the tensor pipe's truncation.
+//     it adds to the output (a scale relative to the largest so far: 3 % less time, and a row of large
+//     values with no weight cost the others up to 1 % of their own).  A code's 128, added to make its byte an
+//     fp16 number, is subtracted ahead of the product: left in, and taken off the sum, it costs the small
+//     codes beside an outlier channel their last bits in the tensor pipe's truncating sums.
 //   - Work is cut by length, not by sequence: the steps (4 chunks, one per warp) of all
 //     (sequence, kv head) items, and some for each item's start and end, are dealt to the CTAs in
 //     equal contiguous ranges, found on the device from the lengths (a captured graph keeps working
@@ -50,7 +49,6 @@ constexpr int DEC_ITEM = 2;
 // 40642, Q8_0, 16 / 2 heads of 64 35 / 27 / 30.
 constexpr float DEC_JOIN = 2e-4f;
 constexpr int DEC_MAX_SEQ = 1024;  // sequences of one launch (their step counts are in shared memory)
-constexpr uint32_t MINUS_128 = 0x80808080u;  // -128 * 2^-24 as fp16, twice
 // p is held in fp16 as 2^14 p, so that small p stay normal numbers; Q8_0 as 2^13 p: times a relative scale below 4
 template <bool Q8>
 constexpr float DEC_P_LOG2 = Q8 ? 13.0f : 14.0f;
@@ -108,11 +106,6 @@ __device__ __forceinline__ void mma16816_zero(float (&c)[4], const uint32_t (&a)
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                  : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-}
-__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
@@ -382,8 +375,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
     int item_w = blockIdx.x;
 
     constexpr float LOG2E = 1.4426950408889634f;
-    constexpr float CODE = Q8 ? 16777216.0f : 1.0f;  // scores come in units of 2^-24 (q_off)
-    const float scale = p.scale * CODE, scale_log2 = scale * LOG2E;
+    const float scale_log2 = p.scale * LOG2E;
     uint8_t* ring = smem + warp * L::WARP;
     const uint32_t ring_s = smem_u32(ring);
     const int row_pieces = Q8 ? dim >> 4 : dim >> 3;  // 16-byte pieces of a row
@@ -423,6 +415,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
     [[maybe_unused]] const int64_t pool_end = p.c.tile + (p.c.n_pages - 1) * p.c.page_stride;  // from a head's tile of page 0
     const int64_t plane = (int64_t)dim << p.c.page_shift;  // Q8_0: where a tile's scales begin
     const int page_mask = (1 << p.c.page_shift) - 1;
+    [[maybe_unused]] const __half2 k1152 = __float2half2_rn(1152.0f);  // a byte u under 0x64 is the half 1024 + u
 
     while (true) {
         // the next segment: blocks [st0, st1) of item (s, kv head h, head group hg)
@@ -487,22 +480,6 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     }
                 }
             }
-        }
-        // Q8_0: codes go in as code + 128 in the lowest bits of an fp16, a subnormal number that stands for
-        // 2^-24 (code + 128) exactly; the sums start from -2^-17 times the sum of their q.
-        [[maybe_unused]] float q_off[D / 32][NT][2];
-        if (Q8) {
-#pragma unroll
-            for (int b = 0; b < D / 32; b++)
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++) {
-                    float c[4];
-                    const uint32_t off[4] = {MINUS_128, MINUS_128, MINUS_128, MINUS_128};
-                    mma16816_zero(c, off, qf[2 * b][nt][0], qf[2 * b][nt][1]);
-                    mma16816(c, off, qf[2 * b + 1][nt][0], qf[2 * b + 1][nt][1]);
-                    q_off[b][nt][0] = c[0];
-                    q_off[b][nt][1] = c[1];
-                }
         }
         float slope[NT][2];
 #pragma unroll
@@ -639,16 +616,16 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                     for (int u = 0; u < 4; u++) w[u] ^= 0x80808080u;
 #pragma unroll
                     for (int u = 0; u < 2; u++) {  // values 4c, 4c + 1 and 4c + 2, 4c + 3 of a 16-value half
-                        a0[u] = __byte_perm(w[u], 0, 0x4140);
-                        a0[2 + u] = __byte_perm(w[u], 0, 0x4342);
-                        a1[u] = __byte_perm(w[2 + u], 0, 0x4140);
-                        a1[2 + u] = __byte_perm(w[2 + u], 0, 0x4342);
+                        a0[u] = h2u(__hsub2(u2h(__byte_perm(w[u], 0x64646464u, 0x4140)), k1152));
+                        a0[2 + u] = h2u(__hsub2(u2h(__byte_perm(w[u], 0x64646464u, 0x4342)), k1152));
+                        a1[u] = h2u(__hsub2(u2h(__byte_perm(w[2 + u], 0x64646464u, 0x4140)), k1152));
+                        a1[2 + u] = h2u(__hsub2(u2h(__byte_perm(w[2 + u], 0x64646464u, 0x4342)), k1152));
                     }
                     const float fa = __half2float(da[b]), fb = __half2float(db[b]);
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
                         float c[4];
-                        mma16816_from(c, a0, qf[2 * b][nt][0], qf[2 * b][nt][1], q_off[b][nt][0], q_off[b][nt][1]);
+                        mma16816_zero(c, a0, qf[2 * b][nt][0], qf[2 * b][nt][1]);
                         mma16816(c, a1, qf[2 * b + 1][nt][0], qf[2 * b + 1][nt][1]);
                         sc[nt][0] = fmaf(c[0], fa, sc[nt][0]);
                         sc[nt][1] = fmaf(c[1], fa, sc[nt][1]);
@@ -725,7 +702,7 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
                 if (p.cap > 0.0f || p.slopes) {
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        float x = sc[nt][j] * scale;
+                        float x = sc[nt][j] * p.scale;
                         if (p.cap > 0.0f) x = p.cap * tanh_rel(x * p.inv_cap);
                         const float y = fmaf(-slope[nt][j & 1], (float)(len - 1 - row0 - r8 - (j >> 1) * 8), x);
                         sc[nt][j] = Q8 ? fmaf(y, LOG2E, row_e[j >> 1]) : y * LOG2E;
@@ -768,7 +745,6 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
             if constexpr (Q8) {
                 // with d' a relative scale, the head of p * d' is h = fp16(p_hi * d'), and its tail
                 // p_lo * d' + (p_hi * d' - h), the bracket exact in one fma
-                const __half2 k1152 = __float2half2_rn(1152.0f);
 #pragma unroll
                 for (int b = 0; b < D / 32; b++) {
                     if (b * 32 >= dim) break;
@@ -962,8 +938,7 @@ cudaError_t launch_attn_decode(const KvCache& c, const AttnDesc& a, int64_t n_se
         p.part = part;
         p.count = count;
         p.err = err;
-        // (Q8_0: the kernel multiplies the scale by 2^24.  Past 2^100 the largest score alone counts.)
-        p.scale = c.q8 ? std::min(std::max(a.scale, -0x1p100f), 0x1p100f) : a.scale;
+        p.scale = a.scale;
         p.cap = a.cap;
         p.inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
         p.n_seq = (int)std::min<int64_t>(DEC_MAX_SEQ, n_seq - s0);

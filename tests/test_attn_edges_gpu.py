@@ -175,3 +175,28 @@ def test_decode_large_value_row_without_weight(syn, dim, large, small, at):
     got = syn.attn_decode(cache, on(q), pages, int32([n])).double().cpu().numpy()
     err = np.abs(got - ref)
     assert (err <= decode_bound(mine, ref, False)).all(), (err / mine).max((0, 2)) * 2.0 ** 20
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("n", [3, 40])
+def test_decode_key_blocks_with_an_outlier_channel(syn, dim, n):
+    """Keys with one channel a hundred times the others, which the query does not look at: what is left
+    of the score is held as exactly as if that channel were not there."""
+    rng = np.random.default_rng([dim, n, 46])
+    heads, page = 8, 16
+    codes = np.zeros((n, dim), np.int8)
+    for b in range(0, dim, 32):
+        codes[np.arange(n), b + rng.integers(1, 32, n)] = rng.choice([-1, 1], n)
+    codes[:, ::32] = 127
+    kd = np.full((n, dim // 32), 8.0, np.float16)
+    kx = (codes.reshape(n, -1, 32) * kd.astype(np.float64)[..., None]).reshape(n, dim)
+    vc, vd, vx = q8_rows(rng.standard_normal((n, dim)))
+    cache = syn.KVCache(Q8_0, 1, dim, page, q8_pool(codes, kd, page), q8_pool(vc, vd, page))
+    q = np.abs(rng.standard_normal((20, heads, dim))).astype(np.float16)
+    q[:, :, ::32] = 0
+    pages = int32(np.arange(-(-n // page))[None].repeat(20, 0))
+    for scale in (dim ** -0.5, 0.02):
+        ref, size = attn_ref.attention(q, kx[:, None], vx[:, None], np.full(20, n - 1), np.zeros(20), 0, 0, scale, 0.0, None)
+        got = syn.attn_decode(cache, on(q), pages, int32([n] * 20), scale=scale).double().cpu().numpy()
+        err = np.abs(got - ref)
+        assert (err <= decode_bound(size, ref, False)).all(), (scale, (err / size).max() * 2.0 ** 20)

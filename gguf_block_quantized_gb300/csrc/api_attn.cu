@@ -237,7 +237,7 @@ int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int* count;
     float* part;
-    rc = scratch_for(s, sms + 2, syn::prefill_part_floats(c.dim, sms), &count, &part);
+    rc = scratch_for(s, sms + 2, syn::prefill_part_floats(n_seq, n_tok, a.n_heads, c.n_kv, c.dim, sms), &count, &part);
     if (rc) return rc;
     const syn::KvCache raw = c;
     const int32_t* raw_pages = pages;

@@ -23,7 +23,9 @@
 // Rows that a mask empties give zeros.  A masked score is replaced before the maximum; V rows past
 // the sequence's end are zeroed in shared memory.  A V row that only some rows of the item see may
 // still hold infinities or NaN, and 0 * inf is not 0: a row whose sums come out non-finite is
-// computed again, key by key, from the keys it sees.
+// computed again from the keys it sees, in fp32, when its CTA has done its items (no other warp waits for it
+// then).  With an infinite value in the first row of a prompt of 2048 tokens, 32 / 8 heads of 128, every row is:
+// 3.2 ms where it takes 0.050; 8192 tokens 44 ms, not 0.39.
 //
 // Few rows over a long cache: an item's tiles are split between CTAs (no CTA waits: the last to
 // finish, by a counter, joins the partials in order).
@@ -45,6 +47,13 @@ constexpr int PRE_MAX_SEQ = 1024;     // sequences of one launch
 constexpr float PRE_P_LOG2 = 6.0f;    // p is held as 2^6 p
 constexpr float PRE_GROW_LOG2 = 8.0f; // the maximum's lag
 
+// Rows to be computed again, when the CTA has done its items: a warp's rows of an item.
+struct Redo {
+    int s, h, row0;
+    uint32_t bits;
+    int next;  // of the same warp
+};
+
 struct PrefillParams {
     KvCache c;
     KvCache raw;               // where row_by_hand reads: the user's cache and table, which are c and pages
@@ -62,6 +71,8 @@ struct PrefillParams {
     float* part;
     int* count;  // per item, zero between calls
     int* turns;  // [0] items taken past the CTAs' first ones, [1] CTAs done; zero between calls
+    Redo* redo;  // [n_redo] one for each warp's rows of each item
+    int n_redo;
     int* err;
     float scale, cap;
     int n_seq, n_tok, g, window, out_f16, sms, split;
@@ -120,6 +131,27 @@ struct Item {
     Tiles tiles;
 };
 static_assert(sizeof(Item) <= 96, "two items' space in shared memory");
+__device__ __forceinline__ Item item_of(volatile const int* w) {
+    Item it;
+    it.nt = w[0];
+    it.t0 = w[1];
+    it.n_split = w[2];
+    it.sp = w[3];
+    it.index = w[4];
+    it.s = w[5];
+    it.h = w[6];
+    it.row0 = w[7];
+    it.rows = w[8];
+    it.n_new = w[9];
+    it.tok0 = w[10];
+    it.len = w[11];
+    it.prefix = w[12];
+    it.tiles.a0 = w[13];
+    it.tiles.a1 = w[14];
+    it.tiles.b0 = w[15];
+    it.tiles.b1 = w[16];
+    return it;
+}
 
 // bits of the keys 32w .. 32w+31 of a tile that lie in [lo, hi)
 __device__ __forceinline__ uint32_t span_bits(int lo, int hi, int w) {
@@ -161,49 +193,10 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// One row computed key by key by a warp (lane l takes the values l, l + 32, ...): its maximum, sum
-// and weighted values over the keys of tiles [t0, t1) that it sees.
-template <int D, bool Q8>
-__device__ __noinline__ void row_by_hand(const PrefillParams& p, const int32_t* table, int len, int h, const __half* qrow,
-                                         const Visible& vis, int pos, float slope, const Tiles& tiles, int t0, int t1,
-                                         float& m, float& l, float (&o)[D / 32]) {
-    const int lane = threadIdx.x & 31, dim = p.c.dim;
-    m = -INFINITY;
-    l = 0.0f;
-#pragma unroll
-    for (int i = 0; i < D / 32; i++) o[i] = 0.0f;
-    for (int t = t0; t < t1; t++) {
-        const int j0 = tiles.at(t) * PreShape<D, Q8>::BN;
-        for (int j = j0; j < min(j0 + PreShape<D, Q8>::BN, len); j++) {
-            if (!vis(j)) continue;
-            const int id = table[j >> p.raw.page_shift];
-            if (id < 0 || id >= p.raw.n_pages) continue;
-            const int cell = j & ((1 << p.raw.page_shift) - 1);
-            const int64_t base = (int64_t)id * p.raw.page_stride + (int64_t)h * p.raw.tile;
-            auto value = [&](const uint8_t* pool, int e) {
-                if (!p.raw.q8) return __half2float(reinterpret_cast<const __half*>(pool + base)[(int64_t)cell * dim + e]);
-                const float d = h2f_bits(*reinterpret_cast<const uint16_t*>(
-                    pool + base + ((int64_t)dim << p.raw.page_shift) + 2 * ((int64_t)cell * (dim >> 5) + (e >> 5))));
-                return d * (float)reinterpret_cast<const int8_t*>(pool + base)[(int64_t)cell * dim + e];
-            };
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < D / 32; i++)
-                if (lane + 32 * i < dim) s = fmaf(__half2float(qrow[lane + 32 * i]), value(p.raw.k, lane + 32 * i), s);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-            s *= p.scale;
-            if (p.cap > 0.0f) s = p.cap * tanhf(s / p.cap);
-            s = fmaf(-slope, fabsf((float)(pos - j)), s) * 1.4426950408889634f;
-            const float nm = fmaxf(m, s), ms = nm == -INFINITY ? 0.0f : nm;
-            const float f = ex2(m - ms), w = ex2(s - ms + PRE_P_LOG2);
-            m = nm;
-            l = fmaf(l, f, w);
-#pragma unroll
-            for (int i = 0; i < D / 32; i++)
-                if (lane + 32 * i < dim) o[i] = fmaf(o[i], f, w * value(p.raw.v, lane + 32 * i));
-        }
-    }
+// (starts that run backwards or past the call's tokens count as none)
+__device__ __forceinline__ int new_tokens(const PrefillParams& p, int s) {
+    const int a = p.starts[s], b = p.starts[s + 1];
+    return a < 0 || b > p.n_tok ? 0 : max(b - a, 0);
 }
 
 __device__ __forceinline__ void store_out(const PrefillParams& p, int64_t at, float y) {
@@ -211,10 +204,130 @@ __device__ __forceinline__ void store_out(const PrefillParams& p, int64_t at, fl
     else static_cast<float*>(p.out)[at] = y;
 }
 
+// 8 values of the user's cache from value `at` of a tile on.
+template <bool Q8>
+__device__ __forceinline__ void cached8(const uint8_t* tile, int64_t scales, int64_t at, float (&x)[8]) {
+    if (!Q8) {
+        const uint4 w = *reinterpret_cast<const uint4*>(tile + 2 * at);
+        const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+            x[2 * i] = y.x;
+            x[2 * i + 1] = y.y;
+        }
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(tile + at);
+        const float d = h2f_bits(*reinterpret_cast<const uint16_t*>(tile + scales + 2 * (at >> 5)));
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            x[i] = d * (float)(int8_t)(w.x >> (8 * i));
+            x[4 + i] = d * (float)(int8_t)(w.y >> (8 * i));
+        }
+    }
+}
+
+// The rows row0, row0 + 1, ... of sequence s (a row: a token and a query head of kv head h) that `bits` names,
+// a lane each, computed again in fp32 from the keys that they see in tiles [t0, t1) of `tiles` (t1 = 0: from all that
+// they see), 8 keys' scores at a time, then their values, which all lanes read together.  Writes the outputs,
+// or, part: the rows' place in a partial of R rows and D values.  It ends where every sum is NaN, which
+// nothing mends.  (Q8: the user's cache is Q8_0.)
+template <bool Q8>
+__device__ __noinline__ void rows_by_hand(const PrefillParams& p, int s, int h, int row0, uint32_t bits, Tiles tiles, int t0, int t1,
+                                          int BN, float* part, int R, int D) {
+    const int lane = threadIdx.x & 31, dim = p.c.dim, shift = p.raw.page_shift, mask = (1 << shift) - 1;
+    const int64_t scales = (int64_t)dim << shift;  // Q8_0: where a tile's scales begin
+    const bool mine = (bits >> lane) & 1;
+    const int t = mine ? (row0 + lane) / p.g : 0, tok = p.starts[s] + t;
+    const int head = h * p.g + (mine ? row0 + lane - t * p.g : 0);
+    const int len = held_rows(p.lens[s], p.max_pages, p.c.page_shift), pos = len - new_tokens(p, s) + t;
+    const Visible vis = visible_of(len, pos, p.first ? p.first[tok] : 0, p.prefix ? p.prefix[s] : 0, p.window);
+    const int32_t* table = p.raw_pages + (int64_t)s * p.max_pages;
+    const __half* qrow = p.q + (int64_t)tok * p.q_stride + (int64_t)head * dim;
+    const float slope = p.slopes ? p.slopes[head] : 0.0f;
+    if (t1 == 0) {
+        const bool early = mine && vis.pre > vis.first, late = mine && vis.end > vis.low;
+        const int lo = early ? vis.first : late ? vis.low : INT_MAX, hi = max(early ? vis.pre : 0, late ? vis.end : 0);
+        tiles.a0 = tiles.a1 = 0;
+        tiles.b1 = (__reduce_max_sync(0xffffffffu, hi) + BN - 1) / BN;
+        tiles.b0 = min(__reduce_min_sync(0xffffffffu, lo) / BN, tiles.b1);
+        t0 = 0;
+        t1 = tiles.count();
+    }
+    float o[256];  // (in local memory: read and written once for 8 keys)
+    float m = -INFINITY, l = 0.0f;
+    for (int e = 0; e < dim; e++) o[e] = 0.0f;
+    bool left = true;
+    for (int64_t n = (int64_t)t0 * BN; n < (int64_t)t1 * BN && left; n += 8) {
+        const int jb = tiles.at((int)(n / BN)) * BN + (int)(n % BN);
+        uint32_t seen = mine ? (span_bits(vis.low - jb, vis.end - jb, 0) | span_bits(vis.first - jb, vis.pre - jb, 0)) & 0xffu : 0u;
+        if (!__any_sync(0xffffffffu, seen != 0)) continue;
+        const int id = table[jb >> shift];  // (8 keys lie in one page)
+        if ((unsigned)id >= (unsigned)p.raw.n_pages) continue;
+        const int64_t tile = (int64_t)id * p.raw.page_stride + (int64_t)h * p.raw.tile, row = (int64_t)(jb & mask) * dim;
+        float sc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+        for (int e = 0; e < dim; e += 8) {
+            float q[8];
+            cached8<false>(reinterpret_cast<const uint8_t*>(qrow), 0, e, q);
+#pragma unroll
+            for (int c = 0; c < 8; c++) {
+                float k[8];
+                cached8<Q8>(p.raw.k + tile, scales, row + c * dim + e, k);
+#pragma unroll
+                for (int i = 0; i < 8; i++) sc[c] = fmaf(q[i], k[i], sc[c]);
+            }
+        }
+        float nm = m;
+#pragma unroll
+        for (int c = 0; c < 8; c++) {
+            float x = sc[c] * p.scale;
+            if (p.cap > 0.0f) x = p.cap * tanhf(x / p.cap);
+            x = fmaf(-slope, fabsf((float)(pos - jb - c)), x) * 1.4426950408889634f;
+            sc[c] = (seen >> c) & 1 ? x : -INFINITY;
+            nm = fmaxf(nm, sc[c]);
+        }
+        const float ms = nm == -INFINITY ? 0.0f : nm, f = ex2(m - ms);
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 8; c++) {
+            sc[c] = (seen >> c) & 1 ? ex2(sc[c] - ms + PRE_P_LOG2) : 0.0f;
+            sum += sc[c];
+        }
+        m = nm;
+        l = fmaf(l, f, sum);
+        left = __any_sync(0xffffffffu, mine && l == l);
+#pragma unroll 2
+        for (int e = 0; e < dim; e += 8) {
+            float acc[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) acc[i] = o[e + i] * f;
+#pragma unroll
+            for (int c = 0; c < 8; c++) {
+                float v[8];
+                cached8<Q8>(p.raw.v + tile, scales, row + c * dim + e, v);
+#pragma unroll
+                for (int i = 0; i < 8; i++) acc[i] = (seen >> c) & 1 ? fmaf(sc[c], v[i], acc[i]) : acc[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++) o[e + i] = acc[i];
+        }
+    }
+    if (!mine) return;
+    if (part) {
+        for (int e = 0; e < dim; e++) __stcg(part + (int64_t)e * R, o[e]);
+        __stcg(part + (int64_t)D * R, m);
+        __stcg(part + (int64_t)(D + 1) * R, l);
+    } else {
+        const int64_t out0 = (int64_t)tok * p.out_stride + (int64_t)head * dim;
+        for (int e = 0; e < dim; e++) store_out(p, out0 + e, l == 0.0f ? 0.0f : o[e] / l);
+    }
+}
+
 template <int D, bool Q8, bool MOD>
 __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
     k_attn_prefill(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                   const __grid_constant__ CUtensorMap qmap, const PrefillParams p) {
+                   const __grid_constant__ CUtensorMap qmap, const __grid_constant__ PrefillParams p) {
     using L = PreShape<D, Q8>;
     constexpr int QT = L::QT, BN = L::BN, NS = L::NS, NR = L::NR, R = L::R, THREADS = L::THREADS;
     constexpr int MMA_WARP = L::MMA_WARP, LOAD_WARP = L::LOAD_WARP, EXPAND_WARP = L::EXPAND_WARP;
@@ -279,16 +392,12 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
     griddep_release();
     griddep_wait();
 
-    auto new_tokens = [&](int s) {  // (starts that run backwards or past the call's tokens count as none)
-        const int a = p.starts[s], b = p.starts[s + 1];
-        return a < 0 || b > p.n_tok ? 0 : max(b - a, 0);
-    };
     auto items_of = [&](int n_new) { return (int)(((int64_t)n_new * p.g + R - 1) / R); };
     if (p.n_seq > 32) {  // (up to 32 sequences are the scheduler's lanes)
         __syncthreads();
         for (int base = 0; base < p.n_seq; base += THREADS) {
             const int sq = base + tid;
-            int x = sq < p.n_seq ? items_of(new_tokens(sq)) : 0;
+            int x = sq < p.n_seq ? items_of(new_tokens(p, sq)) : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -314,25 +423,8 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
     int n_items = 0;
     auto next_item = [&](Item& it) {
         const int slot = n_items & 1;
-        if (!mbar_wait_poll(smem_u32(&item_full[slot]), (n_items >> 1) & 1, p.err, abort_flag)) return false;
-        volatile int* w = item_ints + 24 * slot;
-        it.nt = w[0];
-        it.t0 = w[1];
-        it.n_split = w[2];
-        it.sp = w[3];
-        it.index = w[4];
-        it.s = w[5];
-        it.h = w[6];
-        it.row0 = w[7];
-        it.rows = w[8];
-        it.n_new = w[9];
-        it.tok0 = w[10];
-        it.len = w[11];
-        it.prefix = w[12];
-        it.tiles.a0 = w[13];
-        it.tiles.a1 = w[14];
-        it.tiles.b0 = w[15];
-        it.tiles.b1 = w[16];
+        if (!mbar_wait(smem_u32(&item_full[slot]), (n_items >> 1) & 1, p.err, abort_flag)) return false;
+        it = item_of(item_ints + 24 * slot);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&item_empty[slot]));
         n_items++;
@@ -364,14 +456,10 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         auto softmax_sync = [&]() {  // (bounded, as every wait: a warp may have given up)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(join_bar));
-            return mbar_wait_poll(smem_u32(join_bar), joins++ & 1, p.err, abort_flag);
+            return mbar_wait(smem_u32(join_bar), joins++ & 1, p.err, abort_flag);
         };
-        int owed = -1;  // the split item whose counter this CTA has not added to yet
-        auto count_part = [&](const Item& it, int index) {  // true: this was its last part
-            const int before = atomicAdd(&p.count[index], 1);
-            if (before == it.n_split - 1) p.count[index] = 0;  // ready for the next call
-            return before == it.n_split - 1;
-        };
+        int redo_list = -1, split_slot = -1;  // this warp's rows to be computed again; where the split item is, if this is one's part
+        uint32_t split_redo = 0;              // this warp's rows of that part
         Item it{};
         while (next_item(it)) {
             const bool row_ok = tid < it.rows;
@@ -391,13 +479,12 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                     for (int e = 0; e < dim; e++) store_out(p, out0 + e, 0.0f);
                 continue;
             }
-            if (qt >= tiles_in_use(it) && it.n_split == 1) continue;
             float* part = p.part + (int64_t)blockIdx.x * R * (D + 2);  // [D][R] values, [R] maxima, [R] sums
-            if (it.n_split > 1) owed = it.index;
-            if (qt < tiles_in_use(it)) {
+            if (it.n_split > 1) split_slot = (n_items - 1) & 1;  // (the CTA's only item)
+            if (qt >= tiles_in_use(it)) continue;
             if (!p.q_tma) {
                 // this thread's Q row into shared memory, 16-byte piece j of chunk c at j ^ (row % 8)
-                if (!mbar_wait_poll(smem_u32(&q_empty[qt]), (q_turn & 1) ^ 1, p.err, abort_flag)) break;
+                if (!mbar_wait(smem_u32(&q_empty[qt]), (q_turn & 1) ^ 1, p.err, abort_flag)) break;
                 uint8_t* qs = smem + L::Q + qt * L::Q_TILE + (tid & 127) * 128;
                 const uint4* qrow = reinterpret_cast<const uint4*>(p.q + (int64_t)my_tok * p.q_stride + (int64_t)my_head * dim);
 #pragma unroll
@@ -419,7 +506,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             for (int i = 0; i < it.nt; i++, done++) {
                 const int slot = QT == 2 ? qt : done & 1;
                 const uint32_t phase = QT == 2 ? done & 1 : (done >> 1) & 1;
-                if (!mbar_wait_poll(smem_u32(&s_full[slot]), phase, p.err, abort_flag)) { ok = false; break; }
+                if (!mbar_wait(smem_u32(&s_full[slot]), phase, p.err, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t s_base = lane_base + slot * L::SLOT;
                 const int j0 = it.tiles.at(it.t0 + turn_tile(i, it.nt)) * BN;
@@ -560,7 +647,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 }
                 if (i > 0 && __any_sync(0xffffffffu, grow)) {
                     // O holds the tiles before: wait for the last product into it, then scale
-                    if (!mbar_wait_poll(smem_u32(&o_done[qt]), (done - 1) & 1, p.err, abort_flag)) { ok = false; break; }
+                    if (!mbar_wait(smem_u32(&o_done[qt]), (done - 1) & 1, p.err, abort_flag)) { ok = false; break; }
                     tc_fence_after();
                     for (int c = 0; c < dim; c += 16) {
                         uint32_t o[16];
@@ -607,8 +694,8 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             }
             // (one row tile: S of a tile is issued before the product of the one before, so the last
             // two products may both be outstanding, and a parity tells only neighbours apart)
-            if (QT == 1 && it.nt > 1) ok = ok && mbar_wait_poll(smem_u32(&o_done[qt]), (done - 2) & 1, p.err, abort_flag);
-            if (!ok || !mbar_wait_poll(smem_u32(&o_done[qt]), (done - 1) & 1, p.err, abort_flag)) break;
+            if (QT == 1 && it.nt > 1) ok = ok && mbar_wait(smem_u32(&o_done[qt]), (done - 2) & 1, p.err, abort_flag);
+            if (!ok || !mbar_wait(smem_u32(&o_done[qt]), (done - 1) & 1, p.err, abort_flag)) break;
             tc_fence_after();
             {
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -649,46 +736,49 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                     __stcg(part + (int64_t)D * R + r, m);
                     __stcg(part + (int64_t)(D + 1) * R + r, l);
                 }
-                // rows with a non-finite sum, one after the other, by the whole warp
-                __syncwarp();
-                const float2 odd = unpack2(fma2(pack2(l, l), 0, odd2));
-                uint32_t redo = __ballot_sync(0xffffffffu, row_ok && !(odd.x + odd.y == 0.0f));
-                while (redo) {
-                    const int src = __ffs(redo) - 1;
-                    redo &= redo - 1;
-                    Visible w;
-                    w.first = __shfl_sync(0xffffffffu, vis.first, src);
-                    w.pre = __shfl_sync(0xffffffffu, vis.pre, src);
-                    w.low = __shfl_sync(0xffffffffu, vis.low, src);
-                    w.end = __shfl_sync(0xffffffffu, vis.end, src);
-                    const int wpos = __shfl_sync(0xffffffffu, pos, src), wt = __shfl_sync(0xffffffffu, my_tok, src),
-                              wh = __shfl_sync(0xffffffffu, my_head, src);
-                    float wm, wl, wo[D / 32];
-                    row_by_hand<D, Q8>(p, p.raw_pages + (int64_t)it.s * p.max_pages, it.len, it.h, p.q + (int64_t)wt * p.q_stride + (int64_t)wh * dim, w, wpos,
-                                       p.slopes ? p.slopes[wh] : 0.0f, it.tiles, it.t0, it.t0 + it.nt, wm, wl, wo);
-                    const int wr = (r & ~31) + src;
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < D / 32; e++) {
-                        if (lane + 32 * e >= dim) continue;
-                        if (it.n_split > 1) __stcg(part + (int64_t)(lane + 32 * e) * R + wr, wo[e]);
-                        else store_out(p, (int64_t)wt * p.out_stride + (int64_t)wh * dim + lane + 32 * e, wl == 0.0f ? 0.0f : wo[e] / wl);
-                    }
-                    if (it.n_split > 1 && lane == 0) {
-                        __stcg(part + (int64_t)D * R + wr, wm);
-                        __stcg(part + (int64_t)(D + 1) * R + wr, wl);
+                // Rows whose weighted values are not finite are computed again: a value that the row does
+                // not see may have come in as 0 * inf.  Where the sum of the weights is not finite itself a score
+                // that the row sees is not, and its outputs are NaN as they are; but over Q8_0 the key may only
+                // have been past what fp16 holds.  That is slow, so it waits until no other warp waits for this one.
+                const float2 odd = unpack2(odd2);
+                const bool odd_l = !(l * 0.0f == 0.0f), odd_o = !(odd.x + odd.y == 0.0f);
+                const uint32_t redo = __ballot_sync(0xffffffffu, row_ok && (odd_l ? p.raw.q8 : odd_o));
+                if (it.n_split > 1) {
+                    split_redo = redo;
+                } else if (redo) {
+                    const int64_t at = (int64_t)it.index * (R / 32) + warp;
+                    if (at < p.n_redo) {  // (more items than that only where starts[] does not ascend)
+                        if (lane == 0) p.redo[at] = Redo{it.s, it.h, it.row0 + 32 * warp, redo, redo_list};
+                        redo_list = (int)at;
                     }
                 }
             }
-            }
-            if (it.n_split == 1) continue;
-            // ---- the last of the item's CTAs joins the partials ------------------------------------
+        }
+        __syncwarp();
+        auto by_hand = [&](int s, int h, int row0, uint32_t bits, const Tiles& tiles, int t0, int t1, float* part) {
+            if (Q8 || p.raw.q8) rows_by_hand<true>(p, s, h, row0, bits, tiles, t0, t1, BN, part, R, D);
+            else rows_by_hand<false>(p, s, h, row0, bits, tiles, t0, t1, BN, part, R, D);
+        };
+        while (redo_list >= 0) {
+            const Redo x = p.redo[redo_list];
+            by_hand(x.s, x.h, x.row0, x.bits, Tiles{}, 0, 0, nullptr);
+            redo_list = x.next;
+        }
+        // ---- the last of a split item's CTAs joins the partials ------------------------------------
+        if (split_slot >= 0) do {
+            it = item_of(item_ints + 24 * split_slot);
+            if (split_redo)
+                by_hand(it.s, it.h, it.row0 + 32 * warp, split_redo, it.tiles, it.t0, it.t0 + it.nt,
+                        p.part + (int64_t)blockIdx.x * R * (D + 2) + r);
             __threadfence();
-            if (!softmax_sync()) break;
-            if (tid == 0) info[1] = count_part(it, it.index);
-            owed = -1;
-            if (!softmax_sync()) break;
-            if (!info[1]) continue;
+            const bool together = softmax_sync();
+            if (tid == 0) {  // (also where a wait gave up: the counters of the calls to come start from zero)
+                const int before = atomicAdd(&p.count[it.index], 1);
+                info[1] = before == it.n_split - 1;
+                if (before == it.n_split - 1) p.count[it.index] = 0;
+            }
+            if (!together || !softmax_sync() || !info[1]) break;
+            const bool row_ok = tid < it.rows;
             __threadfence();
             const float* base = p.part + (int64_t)(blockIdx.x - it.sp) * R * (D + 2);
             constexpr int64_t pitch = (int64_t)R * (D + 2);
@@ -760,9 +850,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                     }
                 }
             }
-        }
-        // (after a wait that gave up: the counters of the calls to come start from zero all the same)
-        if (tid == 0 && owed >= 0) count_part(it, owed);
+        } while (false);
     } else if (warp < EXPAND_WARP) {
       if (QT == 2) give_registers<L::MMA_REGS>();
       if (warp == MMA_WARP) {
@@ -772,7 +860,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         bool ok = true;
         Item it{};
         auto take = [&](int i) {  // wait for piece i of the ring
-            if (!mbar_wait_poll(smem_u32(&kv_full[i % NS]), (i / NS) & 1, p.err, abort_flag)) return false;
+            if (!mbar_wait(smem_u32(&kv_full[i % NS]), (i / NS) & 1, p.err, abort_flag)) return false;
             tc_fence_after();
             return true;
         };
@@ -792,7 +880,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             const uint64_t vd = n_major + ((ring_s + (i % NS) * L::STAGE) >> 4);
 #pragma unroll
             for (int half = 0; half < 2; half++) {
-                if (!mbar_wait_poll(smem_u32(half ? &p_full[slot] : &p_half[slot]), phase, p.err, abort_flag)) return false;
+                if (!mbar_wait(smem_u32(half ? &p_full[slot] : &p_half[slot]), phase, p.err, abort_flag)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < BN / 32; k++) {
@@ -823,7 +911,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             if (nt == 0) continue;
 #pragma unroll
             for (int qt = 0; qt < QT; qt++)
-                if (qt < q_act) ok = ok && mbar_wait_poll(smem_u32(&q_full[qt]), q_turn[qt]++ & 1, p.err, abort_flag);
+                if (qt < q_act) ok = ok && mbar_wait(smem_u32(&q_full[qt]), q_turn[qt]++ & 1, p.err, abort_flag);
             if (!ok || !(ok = take(rc))) break;
             // (S of the first tile goes where P of the last item's last tile was: in order behind its product)
 #pragma unroll
@@ -889,7 +977,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
 #pragma unroll
                 for (int qt = 0; qt < QT; qt++) {
                     if (qt >= q_act || !ok) continue;
-                    if (!(ok = mbar_wait_poll(smem_u32(&q_empty[qt]), (q_turn[qt] & 1) ^ 1, p.err, abort_flag))) continue;
+                    if (!(ok = mbar_wait(smem_u32(&q_empty[qt]), (q_turn[qt] & 1) ^ 1, p.err, abort_flag))) continue;
                     q_turn[qt]++;
                     if (lane == 0) {
                         const uint32_t full = smem_u32(&q_full[qt]), dst = smem_u32(smem + L::Q + qt * L::Q_TILE);
@@ -917,7 +1005,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                     if ((unsigned)x < (unsigned)p.c.n_pages) id = x;
                     else record_error(p.err, SYN_DEVERR_BOUNDS);
                 }
-                if (!(ok = mbar_wait_poll(smem_u32(Q8 ? &raw_empty[st] : &kv_empty[st]), (turn & 1) ^ 1, p.err, abort_flag))) break;
+                if (!(ok = mbar_wait(smem_u32(Q8 ? &raw_empty[st] : &kv_empty[st]), (turn & 1) ^ 1, p.err, abort_flag))) break;
                 const int cell = j & ((1 << p.c.page_shift) - 1);
                 if (!Q8) {
                     // a page that is not there becomes the page after the last: the copy fills it with zeros
@@ -964,7 +1052,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         const int mine = min(lane, p.n_seq - 1);
         int my_new = 0, my_sum = 0;
         if (p.n_seq <= 32) {
-            my_new = lane < p.n_seq ? new_tokens(mine) : 0;
+            my_new = lane < p.n_seq ? new_tokens(p, mine) : 0;
             my_sum = items_of(my_new);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -1002,7 +1090,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                     it.s = lo;
                     before = pre[lo];
                 }
-                it.n_new = new_tokens(it.s);
+                it.n_new = new_tokens(p, it.s);
                 it.tok0 = p.starts[it.s];
                 it.len = held_rows(p.lens[it.s], p.max_pages, p.c.page_shift);
                 it.prefix = p.prefix ? p.prefix[it.s] : 0;
@@ -1057,7 +1145,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             }
             if (it.nt != -2) {  // (-2: the item has fewer parts)
                 const int slot = n & 1;
-                if (!mbar_wait_poll(smem_u32(&item_empty[slot]), ((n >> 1) & 1) ^ 1, p.err, abort_flag)) break;
+                if (!mbar_wait(smem_u32(&item_empty[slot]), ((n >> 1) & 1) ^ 1, p.err, abort_flag)) break;
                 if (lane == 0) {
                     volatile int* o = item_ints + 24 * slot;
                     o[0] = it.nt;
@@ -1086,7 +1174,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             // The next one: the CTAs' first items are their numbers, the rest are counted out, each when the
             // loader has the one before on its way (taken earlier, the items of a small call would be
             // dealt before it shows which CTAs are done first: 6 ragged prompts 101 us, not 79)
-            if (it.nt != -2 && !mbar_wait_poll(smem_u32(item_want), (n - 1) & 1, p.err, abort_flag)) break;
+            if (it.nt != -2 && !mbar_wait(smem_u32(item_want), (n - 1) & 1, p.err, abort_flag)) break;
             int taken = 0;
             if (lane == 0) taken = atomicAdd(&p.turns[0], 1);
             w = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, taken, 0);
@@ -1117,8 +1205,8 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
 #endif
             for (int i = 0; i < n_pieces && ok; i++, kc++) {
                 const int rs = kc % max(NR, 1), st = kc % NS;
-                if (!(ok = mbar_wait_poll(smem_u32(&raw_full[rs]), (kc / max(NR, 1)) & 1, p.err, abort_flag))) break;
-                if (!(ok = mbar_wait_poll(smem_u32(&kv_empty[st]), ((kc / NS) & 1) ^ 1, p.err, abort_flag))) break;
+                if (!(ok = mbar_wait(smem_u32(&raw_full[rs]), (kc / max(NR, 1)) & 1, p.err, abort_flag))) break;
+                if (!(ok = mbar_wait(smem_u32(&kv_empty[st]), ((kc / NS) & 1) ^ 1, p.err, abort_flag))) break;
                 const int left = it.len - it.tiles.at(it.t0 + turn_tile(piece_tile(i, it.nt), it.nt)) * BN;  // rows of the tile that exist
                 const uint32_t there = raw_there[rs];
                 const bool whole = left >= BN && there == all_there;
@@ -1301,8 +1389,19 @@ static cudaError_t run_prefill(const CUtensorMap& km, const CUtensorMap& vm, con
 static int prefill_rows(int dim) { return dim <= 128 ? 256 : 128; }
 
 // at most one split item per SM has a counter, one CTA per SM a partial
-int64_t prefill_part_floats(int dim, int sms) {
+static int64_t part_floats(int dim, int sms) {
     return (int64_t)sms * prefill_rows(dim) * ((dim <= 64 ? 64 : dim <= 128 ? 128 : 256) + 2);
+}
+// an entry of `redo` for each 32 rows of an item (a power of two: a growing prompt seldom needs more than the last)
+static int64_t redo_entries(int64_t n_seq, int64_t n_tok, int n_heads, int n_kv, int dim) {
+    const int R = prefill_rows(dim);
+    const int64_t need = (n_tok * (n_heads / n_kv) / R + std::min<int64_t>({n_seq, n_tok, PRE_MAX_SEQ})) * n_kv * (R / 32);
+    int64_t n = 4096;
+    while (n < need) n *= 2;
+    return n;
+}
+int64_t prefill_part_floats(int64_t n_seq, int64_t n_tok, int n_heads, int n_kv, int dim, int sms) {
+    return part_floats(dim, sms) + redo_entries(n_seq, n_tok, n_heads, n_kv, dim) * (int64_t)(sizeof(Redo) / 4);
 }
 
 cudaError_t launch_attn_prefill(const KvCache& c, const KvCache& raw, const AttnDesc& a, int64_t n_seq, int64_t n_tok,
@@ -1350,6 +1449,8 @@ cudaError_t launch_attn_prefill(const KvCache& c, const KvCache& raw, const Attn
     p.slopes = a.slopes;
     p.first = a.first;
     p.part = part;
+    p.redo = reinterpret_cast<Redo*>(part + part_floats(c.dim, sms));
+    p.n_redo = (int)redo_entries(n_seq, n_tok, a.n_heads, c.n_kv, c.dim);
     p.count = count + 2;
     p.turns = count;
     p.err = err;

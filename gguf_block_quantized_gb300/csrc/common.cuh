@@ -200,24 +200,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* er
     }
 }
 
-// The same for waits that end within a few hundred cycles as a rule: looks at the clock and the abort
-// flag only every 64 polls (no difference in the prefill's time to mbar_wait; fewer instructions beside it).
-__device__ __forceinline__ bool mbar_wait_poll(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 64; i++)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-        if (clock64() - t0 > SYN_WAIT_CYCLES) {
-            record_error(err, SYN_DEVERR_TIMEOUT);
-            *abort = 1;
-            return false;
-        }
-    }
-}
-
 // Wait for a phase whose copies (or tensor-core commits) were issued by this CTA, ignoring
 // the abort flag: after a kernel gave up, every asynchronous write into its shared memory
 // must have landed before the CTA leaves, or it would land in the next CTA's.  Bounded by

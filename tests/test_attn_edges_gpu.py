@@ -200,3 +200,67 @@ def test_decode_key_blocks_with_an_outlier_channel(syn, dim, n):
         got = syn.attn_decode(cache, on(q), pages, int32([n] * 20), scale=scale).double().cpu().numpy()
         err = np.abs(got - ref)
         assert (err <= decode_bound(size, ref, False)).all(), (scale, (err / size).max() * 2.0 ** 20)
+
+
+# ---- rows computed again -------------------------------------------------------------------
+
+@pytest.mark.parametrize("t", [F16, Q8_0])
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("opt", [{}, {"cap": 6.0, "slopes": True}, {"window": 300, "prefix": 40}])
+def test_rows_beside_infinite_values(syn, t, dim, opt):
+    """Infinite values (F16) or scales (Q8_0) that the last tokens see: the tokens before them are right,
+    and where they are seen the columns that do not hold them."""
+    import torch
+    rng = np.random.default_rng([t, dim, 52])
+    heads, page, n, new = 4, 16, 1100, 90
+    cache, pages, seqs = make_cache(syn, rng, t, 1, dim, page, [n])
+    k, v = seqs[0]
+    bad = n - 33
+    pg, cell = int(pages[0, bad // page]), bad % page
+    if t == F16:
+        cache.v[pg, 0, cell, 3] = float("inf")
+    else:
+        at = page * dim + cell * dim // 16
+        cache.v[pg, 0, at:at + 2] = torch.tensor([0, 0x7C], dtype=torch.uint8, device="cuda")
+    q = rng.standard_normal((new, heads, dim)).astype(np.float16)
+    sl = (2.0 ** -np.arange(1.0, heads + 1)).astype(np.float32) if opt.get("slopes") else None
+    prefix, window, cap = opt.get("prefix", 0), opt.get("window", 0), opt.get("cap", 0.0)
+    pos = np.arange(n - new, n)
+    ref, size = attn_ref.attention(q, k, v, pos, np.zeros(new), prefix, window, dim ** -0.5, cap, sl)
+    got = syn.attn_prefill(cache, on(q), int32([0, new]), pages, int32([n]), cap=cap, window=window,
+                           slopes=None if sl is None else on(sl), prefix=int32([prefix]) if prefix else None).double().cpu().numpy()
+    ok = np.abs(got - ref) <= prefill_bound(t, size, np.abs(v).max(), ref, False)
+    seen, cols = pos >= bad, slice(3, 4) if t == F16 else slice(0, 32)
+    assert ok[~seen].all()
+    assert not np.isfinite(got[seen][:, :, cols]).any()
+    ok[:, :, cols] = True
+    assert ok[seen].all()
+    assert syn.device_status() == syn.OK
+
+
+def test_long_rows_computed_again_in_time(syn):
+    """A CTA whose rows are all computed again over a long cache is waited for by its other warps: no
+    wait runs out, and its rows are right.  (Deterministic mode: one CTA has all the keys.)"""
+    import torch
+    heads, dim, page, n = 32, 64, 64, 200000
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    cache = syn.KVCache.empty(F16, 1, dim, page, n // page)
+    cache.k.normal_(generator=gen)
+    cache.v.normal_(generator=gen)
+    q = torch.randn((5, heads, dim), device="cuda", generator=gen).half()
+    bad = n - 1  # seen by the last token alone
+    cache.v[bad // page, 0, bad % page, 11] = float("inf")
+    pages = torch.arange(n // page, dtype=torch.int32, device="cuda").view(1, -1)
+    old = syn.set_deterministic(True)
+    try:
+        got = syn.attn_prefill(cache, q, int32([0, 5]), pages, int32([n]))
+    finally:
+        syn.set_deterministic(old)
+    assert syn.device_status(clear=True) == syn.OK
+    k, v = (x.view(n, dim).double() for x in (cache.k, cache.v))
+    for i in (0, 3):
+        p = torch.softmax((q[i].double() @ k[:n - 4 + i].T) / 8, -1)
+        want = p @ v[:n - 4 + i]
+        # sums of 2e5 terms in fp32, some 2^-24 of the sum of their sizes each, beside prefill's own bound
+        assert (got[i].double() - want).abs().max() <= v[:-1].abs().max() * (2.0 ** -11 + 2.0 ** -24 * 16 * 30)
+    assert torch.isinf(got[4, :, 11]).all() and torch.isfinite(got[4, :, :11]).all()

@@ -160,6 +160,14 @@ __device__ __forceinline__ uint32_t span_bits(int lo, int hi, int w) {
     return below_b & ~below_a;
 }
 
+// A Q8_0 block's scale, twice, for its expansion to fp16.  From 512 on a block may hold values that fp16 does not:
+// it is expanded to NaN, so that the rows that see it are computed again from the cache itself.  (An infinite
+// key alone would not show: a score of -inf has no weight.)
+__device__ __forceinline__ __half2 expand_scale(uint32_t bits) {
+    uint32_t db = __byte_perm((bits & 0x7FFFu) < 0x6000u ? bits : 0x7FFFu, 0, 0x1010);
+    return *reinterpret_cast<__half2*>(&db);
+}
+
 // two fp32 operations in one instruction
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
     uint64_t r;
@@ -1216,8 +1224,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 // one piece: 16 codes and their scale to 16 halves.  A byte c becomes 1024 + c by a permute with
                 // 0x64; value = scale * code, the one rounding of the expansion (relative 2^-11, like that of p)
                 auto put = [&](uint8_t* to, const uint4& code, uint32_t bits) {
-                    uint32_t db = __byte_perm(bits, 0, 0x1010);
-                    const __half2 d = *reinterpret_cast<__half2*>(&db);
+                    const __half2 d = expand_scale(bits);
                     const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
                     uint32_t w[8];
 #pragma unroll
@@ -1327,8 +1334,7 @@ __global__ void __launch_bounds__(256) k_kv_expand(const ExpandParams p) {
         for (int x = threadIdx.x; x < n; x += 256) {
             const uint4 code = *reinterpret_cast<const uint4*>(src + 16 * (int64_t)x);
             const uint32_t bits = *reinterpret_cast<const uint16_t*>(src + 16 * (int64_t)n + 2 * (x >> 1));  // (2 pieces a block)
-            uint32_t db = __byte_perm(bits, 0, 0x1010);
-            const __half2 d = *reinterpret_cast<__half2*>(&db);
+            const __half2 d = expand_scale(bits);
             const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
             uint32_t w[8];
 #pragma unroll

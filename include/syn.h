@@ -465,8 +465,9 @@ SYN_API int syn_attn_decode(const syn_kv_cache* cache, const syn_attn* attn, int
  * The products run on the tensor cores with fp16 operands: p and (Q8_0) the expanded key and value
  * are rounded to fp16 once, scores, sums and maxima are fp32, so an output of either type is exact to
  * about 2^-11 of its row's values, not to fp32's last place (syn_attn_decode is).  A row
- * whose sums are not finite is computed again from the keys it sees alone, in fp32: where that comes to
- * every row of a call, the call takes some hundred times as long.
+ * whose sums are not finite, or that sees a Q8_0 block with a scale of 512 or more (whose values may be past
+ * fp16), is computed again from the keys it sees alone, in fp32: where that comes to every row of a call, the
+ * call takes some hundred times as long.
  * Few tokens over a long cache are split over its length (not in deterministic mode, in which a
  * token's output does not depend on the other sequences of the call).  A call of many new tokens
  * over a Q8_0 cache (not in deterministic mode) first expands the rows of its page table to fp16 in

@@ -264,3 +264,26 @@ def test_long_rows_computed_again_in_time(syn):
         # sums of 2e5 terms in fp32, some 2^-24 of the sum of their sizes each, beside prefill's own bound
         assert (got[i].double() - want).abs().max() <= v[:-1].abs().max() * (2.0 ** -11 + 2.0 ** -24 * 16 * 30)
     assert torch.isinf(got[4, :, 11]).all() and torch.isfinite(got[4, :, :11]).all()
+
+
+@pytest.mark.parametrize("new", [60, 270])
+def test_cached_keys_past_fp16(syn, new):
+    """Keys of a Q8_0 cache that fp16 does not hold (a scale above 516) are finite all the same: rows
+    that see one are right, in one or the other way of expanding."""
+    rng = np.random.default_rng([new, 53])
+    heads, dim, page, n = 8, 64, 16, new + 60
+    kc, kd, kx = q8_rows(rng.standard_normal((n, dim)))
+    vc, vd, vx = q8_rows(rng.standard_normal((n, dim)))
+    j = n - 20
+    kc[j, :32] = 0
+    kc[j, 7] = 127
+    kd[j, 0] = 1500.0
+    kx[j, :32] = kc[j, :32] * 1500.0
+    cache = syn.KVCache(Q8_0, 1, dim, page, q8_pool(kc, kd, page), q8_pool(vc, vd, page))
+    q = rng.standard_normal((new, heads, dim)).astype(np.float16)
+    q[:, ::2, 7] = -(2.0 ** -14)  # (the score of that key: near -1.5 for half of the heads, of all sizes for the others)
+    pos = np.arange(n - new, n)
+    ref, size = attn_ref.attention(q, kx[:, None], vx[:, None], pos, np.zeros(new), 0, 0, dim ** -0.5, 30.0, None)
+    got = syn.attn_prefill(cache, on(q), int32([0, new]), int32(np.arange(-(-n // page))[None]), int32([n]), cap=30.0).double().cpu().numpy()
+    assert (np.abs(got - ref) <= prefill_bound(Q8_0, size, np.abs(vx).max(), ref, False)).all()
+    assert syn.device_status() == syn.OK

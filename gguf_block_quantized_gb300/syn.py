@@ -312,13 +312,14 @@ class KVCache:
         tile = int(syn_kv_tile_bytes(t, head_dim, page_size))
         if tile < 0:
             raise SynError(ERR_TYPE if t not in (F16, Q8_0) else ERR_SHAPE, "KVCache")
+        torch = _torch()
+        dtype, page = (torch.float16, (n_kv_heads, page_size, head_dim)) if t == F16 else (torch.uint8, (n_kv_heads, tile))
         for pool in (k, v):
-            if pool.shape[0] < 1 or pool.shape[0] != k.shape[0] or \
-                    pool[0].numel() * pool.element_size() != n_kv_heads * tile or not pool[0].is_contiguous() or \
-                    (pool.shape[0] > 1 and (pool.stride(0) * pool.element_size() != k.stride(0) * k.element_size() or
-                                            pool.stride(0) < pool[0].numel())):
-                raise ValueError("a pool is (n_pages, ...) with n_kv_heads contiguous tiles of "
-                                 f"{tile} bytes per page, both pools alike")
+            if pool.dtype != dtype or pool.dim() != 1 + len(page) or pool.shape[1:] != page or pool.shape[0] < 1 or \
+                    pool.shape[0] != k.shape[0] or pool.device != k.device or not pool[0].is_contiguous() or \
+                    (pool.shape[0] > 1 and (pool.stride(0) != k.stride(0) or pool.stride(0) < pool[0].numel())):
+                raise ValueError(f"a pool is a {dtype} tensor (n_pages, {', '.join(map(str, page))}) of contiguous pages, "
+                                 "both pools alike")
         self.type, self.n_kv_heads, self.head_dim, self.page_size = t, n_kv_heads, head_dim, page_size
         self.n_pages, self.k, self.v = k.shape[0], k, v
         stride = k.stride(0) * k.element_size() if k.shape[0] > 1 else 0

@@ -43,7 +43,7 @@ int cache_of(const syn_kv_cache* c, syn::KvCache* out) {
     return SYN_OK;
 }
 
-// Checks the attention's options and q / out against the cache.
+// Checks the attention's options and, where there are rows, q / out against the cache.
 int attn_of(const syn_attn* a, const syn::KvCache& c, int64_t rows, const void* q, const void* out, syn::AttnDesc* d) {
     if (!a) return SYN_ERR_NULL;
     if (a->out_type != SYN_OUT_F32 && a->out_type != SYN_OUT_F16) return SYN_ERR_TYPE;
@@ -52,8 +52,9 @@ int attn_of(const syn_attn* a, const syn::KvCache& c, int64_t rows, const void* 
         return SYN_ERR_SHAPE;
     const int64_t row = (int64_t)a->n_heads * c.dim;
     const int64_t qs = a->q_stride ? a->q_stride : row, os = a->out_stride ? a->out_stride : row;
-    if (qs < row || os < row || qs % 8 || os % 8 || qs > kMaxElems / rows || os > kMaxElems / rows) return SYN_ERR_SHAPE;
-    if (!q || !out) return SYN_ERR_NULL;
+    const int64_t most = kMaxElems / (rows ? rows : 1);
+    if (qs < row || os < row || qs % 8 || os % 8 || qs > most || os > most) return SYN_ERR_SHAPE;
+    if (rows && (!q || !out)) return SYN_ERR_NULL;
     if (!aligned(q, 16) || !aligned(out, 16)) return SYN_ERR_ALIGN;
     if (!aligned(a->slopes, 4) || !aligned(a->prefix, 4) || !aligned(a->first, 4)) return SYN_ERR_ALIGN;
     d->slopes = a->slopes;
@@ -194,9 +195,9 @@ int syn_attn_decode(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_s
     syn::KvCache c;
     int rc = cache_of(cache, &c);
     if (rc) return rc;
-    if (n_seq < 0 || n_seq > INT32_MAX || max_pages < 1 || max_pages > INT32_MAX) return SYN_ERR_SHAPE;
+    if (n_seq < 0 || n_seq > INT32_MAX || max_pages < (n_seq > 0) || max_pages > INT32_MAX) return SYN_ERR_SHAPE;
     syn::AttnDesc a;
-    rc = attn_of(attn, c, n_seq ? n_seq : 1, q, out, &a);
+    rc = attn_of(attn, c, n_seq, q, out, &a);
     if (rc) return rc;
     if (n_seq == 0) return SYN_OK;
     if (!pages || !lens) return SYN_ERR_NULL;
@@ -223,9 +224,10 @@ int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_
     syn::KvCache c;
     int rc = cache_of(cache, &c);
     if (rc) return rc;
-    if (n_seq < 0 || n_seq > INT32_MAX || n_tok < 0 || max_pages < 1 || max_pages > INT32_MAX) return SYN_ERR_SHAPE;
+    if (n_seq < 0 || n_seq > INT32_MAX || n_tok < 0 || max_pages < (n_seq > 0 && n_tok > 0) || max_pages > INT32_MAX)
+        return SYN_ERR_SHAPE;
     syn::AttnDesc a;
-    rc = attn_of(attn, c, n_tok ? n_tok : 1, q, out, &a);
+    rc = attn_of(attn, c, n_seq ? n_tok : 0, q, out, &a);
     if (rc) return rc;
     if (n_tok > (INT32_MAX - 1024) / a.n_heads) return SYN_ERR_SHAPE;  // 32-bit row numbers
     if (n_seq == 0 || n_tok == 0) return SYN_OK;

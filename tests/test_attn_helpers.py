@@ -32,3 +32,25 @@ def test_pools_hold_what_the_cache_says(syn):
     for v in (half.to(torch.bfloat16), half.to("meta"), byte):
         with pytest.raises(ValueError):
             syn.KVCache(F16, 2, 64, 16, half, v)
+
+
+def test_calls_of_no_tokens(syn):
+    """Empty tensors, whose pointers are 0: such calls do nothing, as kv_append and kv_read of nothing."""
+    import torch
+    c = syn.KVCache.empty(F16, 2, 64, 16, 4, device="cpu")
+    q, i32 = torch.zeros((0, 4, 64), dtype=torch.float16), lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    assert q.data_ptr() == 0
+    none = {"stream": 0}
+    for width in (3, 0):
+        assert syn.attn_decode(c, q, i32(0, width), i32(0), **none).shape == q.shape
+        assert syn.attn_prefill(c, q, i32(1), i32(0, width), i32(0), **none).shape == q.shape
+        assert syn.attn_prefill(c, q, i32(3), i32(2, width), i32(2), **none).shape == q.shape
+    half = torch.zeros((0, 4, 64), dtype=torch.float16)
+    opt = {"slopes": torch.zeros(4), "prefix": i32(0), "first": i32(0), "window": 7, "cap": 3.0}
+    assert syn.attn_decode(c, q, i32(0, 3), i32(0), half, **opt, **none) is half
+    k = torch.zeros((0, 2, 64))
+    assert syn.kv_append(c, syn.Rope(0, device="cpu"), k, k, None, torch.zeros(0, dtype=torch.int64), **none) is None
+    assert syn.kv_read(c, torch.zeros(0, dtype=torch.int64), **none)[0].shape == (0, 2, 64)
+    for bad in ({"window": -1}, {"cap": -1.0}):  # (the options are checked all the same)
+        with pytest.raises(syn.SynError):
+            syn.attn_decode(c, q, i32(0, 3), i32(0), **bad, **none)

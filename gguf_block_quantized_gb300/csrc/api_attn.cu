@@ -77,7 +77,7 @@ constexpr size_t kCountBytes = size_t(1) << 20;
 
 // A Q8_0 prefill expands its cache to fp16 ahead of the kernel, once, where the kernel would expand each
 // row many times: once for every 256 (token, head) rows of a sequence that see it.  It does so from this
-// many such tiles a sequence on average on, and up to kExpandBytes of scratch a pool.  Measured on GB300,
+// many such tiles a sequence on average on, and up to kExpandBytes of scratch in all.  Measured on GB300,
 // 32 / 8 heads, 8 sequences, all rows new, expanded in the kernel / ahead (us):
 //   slopes, heads of 128:  8 tiles 51.2 / 49.2, 16 tiles 88.1 / 88.1, 64 tiles 530 / 432
 //   slopes, heads of 64:   8 tiles 38.7 / 41.0, 16 tiles 70.7 / 70.3, 64 tiles 424 / 352
@@ -88,7 +88,7 @@ constexpr size_t kCountBytes = size_t(1) << 20;
 int64_t expand_tiles(const syn::KvCache& c, const syn::AttnDesc& a) {
     return (a.slopes || a.cap > 0.0f) && c.dim <= 128 ? 8 : 32;
 }
-constexpr int64_t kExpandBytes = int64_t(1) << 30;
+constexpr int64_t kExpandBytes = int64_t(1) << 31;  // (a power of two: so is what the workspace is rounded up to)
 
 int scratch_for(cudaStream_t s, int64_t count_words, int64_t part_floats, int** count, float** part) {
     // a multiple of a fixed step, so that a growing batch does not reallocate at every call
@@ -247,7 +247,7 @@ int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_
     // bytes of a page, as fp16, in one of the two scratch pools
     const int64_t page = (int64_t(2) * c.dim * c.n_kv) << c.page_shift;
     if (c.q8 && !syn::deterministic() && n_tok * (a.n_heads / c.n_kv) >= expand_tiles(c, a) * 256 * n_seq &&
-        n_seq * max_pages <= kExpandBytes / page) {
+        n_seq * max_pages <= kExpandBytes / (2 * page + 4)) {
         const int64_t pool = n_seq * max_pages * page;
         void* ws;
         rc = syn::attn_rows_workspace(s, (size_t)(2 * pool + n_seq * max_pages * 4), &ws);

@@ -287,3 +287,26 @@ def test_cached_keys_past_fp16(syn, new):
     got = syn.attn_prefill(cache, on(q), int32([0, new]), int32(np.arange(-(-n // page))[None]), int32([n]), cap=30.0).double().cpu().numpy()
     assert (np.abs(got - ref) <= prefill_bound(Q8_0, size, np.abs(vx).max(), ref, False)).all()
     assert syn.device_status() == syn.OK
+
+
+# ---- page tables far wider than the lengths ------------------------------------------------
+
+@pytest.mark.parametrize("width,want", [(8191, 2), (8192, 1)])
+def test_expansion_keeps_to_its_room(syn, width, want):
+    """The workspace of the expansion is 2 GiB at the most, the page table in it counted."""
+    import torch
+    kv, dim, page = 8, 128, 64
+    cache = syn.KVCache.empty(Q8_0, kv, dim, page, 8)
+    pages = torch.zeros((1, width), dtype=torch.int32, device="cuda")
+    pages[0, :8] = torch.arange(8)
+    side = torch.cuda.Stream()
+    q = torch.zeros((300, 8 * kv, dim), dtype=torch.float16, device="cuda")
+    call = syn.prepare_attn_prefill(cache, q, int32([0, 300]), pages, int32([400]), cap=5.0, stream=side)
+    small = syn.prepare_attn_prefill(cache, q[:3], int32([0, 3]), pages, int32([400]), cap=5.0, stream=side)
+    small()  # (the workspace for partial results)
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    assert launches(syn, call) == want
+    torch.cuda.synchronize()
+    assert before - torch.cuda.mem_get_info()[0] <= 2 ** 31 + 2 ** 22
+    syn.check(syn.syn_release(), "syn_release")

@@ -255,7 +255,7 @@ int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_
         if (rc == SYN_OK) {  // (no room: expanded in the kernel)
             uint8_t* k = static_cast<uint8_t*>(ws);
             int32_t* table = reinterpret_cast<int32_t*>(k + 2 * pool);
-            rc = check_cuda(syn::launch_kv_expand(c, n_seq, starts, pages, max_pages, lens, a.prefix ? 0 : a.window, k, k + pool,
+            rc = check_cuda(syn::launch_kv_expand(c, n_seq, n_tok, starts, pages, max_pages, lens, a.prefix ? 0 : a.window, k, k + pool,
                                                   table, sms, s));
             if (rc) return rc;
             launches = 1;

@@ -202,9 +202,9 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 // (starts that run backwards or past the call's tokens count as none)
-__device__ __forceinline__ int new_tokens(const PrefillParams& p, int s) {
-    const int a = p.starts[s], b = p.starts[s + 1];
-    return a < 0 || b > p.n_tok ? 0 : max(b - a, 0);
+__device__ __forceinline__ int new_tokens(const int32_t* starts, int s, int n_tok) {
+    const int a = starts[s], b = starts[s + 1];
+    return a < 0 || b > n_tok ? 0 : max(b - a, 0);
 }
 
 __device__ __forceinline__ void store_out(const PrefillParams& p, int64_t at, float y) {
@@ -248,7 +248,7 @@ __device__ __noinline__ void rows_by_hand(const PrefillParams& p, int s, int h, 
     const bool mine = (bits >> lane) & 1;
     const int t = mine ? (row0 + lane) / p.g : 0, tok = p.starts[s] + t;
     const int head = h * p.g + (mine ? row0 + lane - t * p.g : 0);
-    const int len = held_rows(p.lens[s], p.max_pages, p.c.page_shift), pos = len - new_tokens(p, s) + t;
+    const int len = held_rows(p.lens[s], p.max_pages, p.c.page_shift), pos = len - new_tokens(p.starts, s, p.n_tok) + t;
     const Visible vis = visible_of(len, pos, p.first ? p.first[tok] : 0, p.prefix ? p.prefix[s] : 0, p.window);
     const int32_t* table = p.raw_pages + (int64_t)s * p.max_pages;
     const __half* qrow = p.q + (int64_t)tok * p.q_stride + (int64_t)head * dim;
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         __syncthreads();
         for (int base = 0; base < p.n_seq; base += THREADS) {
             const int sq = base + tid;
-            int x = sq < p.n_seq ? items_of(new_tokens(p, sq)) : 0;
+            int x = sq < p.n_seq ? items_of(new_tokens(p.starts, sq, p.n_tok)) : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -1060,7 +1060,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         const int mine = min(lane, p.n_seq - 1);
         int my_new = 0, my_sum = 0;
         if (p.n_seq <= 32) {
-            my_new = lane < p.n_seq ? new_tokens(p, mine) : 0;
+            my_new = lane < p.n_seq ? new_tokens(p.starts, mine, p.n_tok) : 0;
             my_sum = items_of(my_new);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -1098,7 +1098,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                     it.s = lo;
                     before = pre[lo];
                 }
-                it.n_new = new_tokens(p, it.s);
+                it.n_new = new_tokens(p.starts, it.s, p.n_tok);
                 it.tok0 = p.starts[it.s];
                 it.len = held_rows(p.lens[it.s], p.max_pages, p.c.page_shift);
                 it.prefix = p.prefix ? p.prefix[it.s] : 0;
@@ -1295,7 +1295,9 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
 //
 // The rows of every sequence as fp16 values (scale * code, rounded once: the values the expanding warps
 // make), in an F16 cache of scratch: page i of sequence s is page s * max_pages + i of it.  Bound: HBM and
-// L2 (17/16 bytes read and 2 written a value).
+// L2 (17/16 bytes read and 2 written a value).  The work is counted by what the sequences hold, 256 of them at a
+// time, not by the page table's width: 8 prompts of 512 tokens, pages of 64, 75 us with the prefill itself for
+// tables of 8 to 1000 pages (by the width: 74 to 183 us).
 struct ExpandParams {
     KvCache c;      // Q8_0
     uint8_t* k;     // scratch pools
@@ -1305,29 +1307,13 @@ struct ExpandParams {
     const int32_t* pages;
     const int32_t* lens;
     int64_t max_pages;
-    int n_seq, window;
+    int n_seq, n_tok, window;
 };
 
 __global__ void __launch_bounds__(256) k_kv_expand(const ExpandParams p) {
     const int dim = p.c.dim, page = 1 << p.c.page_shift, per_row = dim >> 4, n = page * per_row;  // 16 codes at a time
     const __half2 k1152 = __float2half2_rn(1152.0f);
-    griddep_release();
-    griddep_wait();
-    const int64_t units = (int64_t)p.n_seq * p.max_pages * 2 * p.c.n_kv;  // (sequence, page, pool, head)
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t sp = u / (2 * p.c.n_kv);
-        const int hp = (int)(u - sp * 2 * p.c.n_kv), h = hp >> 1, is_v = hp & 1;
-        const int s = (int)(sp / p.max_pages);
-        const int64_t i = sp - s * p.max_pages, row0 = i << p.c.page_shift;
-        const int len = held_rows(p.lens[s], p.max_pages, p.c.page_shift);
-        // (rows ahead of every query's window are not read by anyone)
-        // (but all of a tile that a query's window begins in: no number that was never written meets p = 0)
-        const int64_t low = p.window > 0 ? ((int64_t)len - max(p.starts[s + 1] - p.starts[s], 0) - p.window) & ~int64_t(127) : 0;
-        const int id = p.pages[sp];
-        const bool ok = (unsigned)id < (unsigned)p.c.n_pages;
-        // a page outside the pool is one here too: reported if a query's tile takes it
-        if (hp == 0 && threadIdx.x == 0) p.table[sp] = ok ? (int32_t)sp : -1;
-        if (row0 >= len || row0 + page <= low || !ok) continue;
+    auto expand = [&](int64_t sp, int id, int h, int is_v) {
         const uint8_t* src = (is_v ? p.c.v : p.c.k) + (int64_t)id * p.c.page_stride + (int64_t)h * p.c.tile;
         uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + (sp * p.c.n_kv + h) * ((int64_t)n * 32));
 #pragma unroll 2
@@ -1349,10 +1335,62 @@ __global__ void __launch_bounds__(256) k_kv_expand(const ExpandParams p) {
             dst[2 * x] = make_uint4(w[0], w[1], w[2], w[3]);
             dst[2 * x + 1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
+    };
+    griddep_release();
+    griddep_wait();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, per_page = 2 * p.c.n_kv;
+    // The pages of sequence s that some query reads: [first, end).  Rows ahead of every query's window are not
+    // read, but all of a tile (of up to 128 rows) that a query's window begins in is: no number that was never
+    // written meets p = 0.  (Far fewer than 2^31 in all: the scratch has room for them.)
+    auto pages_of = [&](int s, int& first, int& end) {
+        const int len = held_rows(p.lens[s], p.max_pages, p.c.page_shift), n_new = new_tokens(p.starts, s, p.n_tok);
+        const int64_t low = p.window > 0 ? ((int64_t)len - n_new - p.window) & ~int64_t(127) : 0;
+        end = n_new > 0 ? (len + page - 1) >> p.c.page_shift : 0;
+        first = (int)min((int64_t)end, max(low, (int64_t)0) >> p.c.page_shift);
+    };
+    __shared__ int before[257], sums[8];  // units (page, pool, head) ahead of each sequence
+    int u = blockIdx.x;
+    for (int s0 = 0; s0 < p.n_seq; s0 += 256) {
+        int x = 0;
+        if (s0 + tid < p.n_seq) {
+            int first, end;
+            pages_of(s0 + tid, first, end);
+            x = (end - first) * per_page;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) sums[warp] = x;
+        __syncthreads();
+        for (int w = 0; w < warp; w++) x += sums[w];
+        before[tid + 1] = x;
+        if (tid == 0) before[0] = 0;
+        __syncthreads();
+        for (; u < before[256]; u += gridDim.x) {
+            int lo = 0, hi = 255;  // the sequence whose units hold u
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (before[mid + 1] > u) hi = mid;
+                else lo = mid + 1;
+            }
+            int first, end;
+            pages_of(s0 + lo, first, end);
+            const int i = (u - before[lo]) / per_page, hp = u - before[lo] - i * per_page, h = hp >> 1, is_v = hp & 1;
+            const int64_t sp = (s0 + lo) * p.max_pages + first + i;
+            const int id = p.pages[sp];
+            const bool ok = (unsigned)id < (unsigned)p.c.n_pages;
+            // a page outside the pool is one here too: reported if a query's tile takes it
+            if (hp == 0 && tid == 0) p.table[sp] = ok ? (int32_t)sp : -1;
+            if (ok) expand(sp, id, h, is_v);
+        }
+        u -= before[256];
+        __syncthreads();
     }
 }
 
-cudaError_t launch_kv_expand(const KvCache& c, int64_t n_seq, const int32_t* starts, const int32_t* pages, int64_t max_pages,
+cudaError_t launch_kv_expand(const KvCache& c, int64_t n_seq, int64_t n_tok, const int32_t* starts, const int32_t* pages, int64_t max_pages,
                              const int32_t* lens, int window, void* k, void* v, int32_t* table, int sms, cudaStream_t s) {
     ExpandParams p;
     p.c = c;
@@ -1364,6 +1402,7 @@ cudaError_t launch_kv_expand(const KvCache& c, int64_t n_seq, const int32_t* sta
     p.lens = lens;
     p.max_pages = max_pages;
     p.n_seq = (int)n_seq;
+    p.n_tok = (int)n_tok;
     p.window = window;
     const int64_t units = n_seq * max_pages * 2 * c.n_kv;
     return launch_overlapped(k_kv_expand, (int)std::min<int64_t>(units, (int64_t)sms * 8), 256, 0, s, p);

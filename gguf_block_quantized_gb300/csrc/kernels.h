@@ -109,7 +109,7 @@ int64_t prefill_part_floats(int64_t n_seq, int64_t n_tok, int n_heads, int n_kv,
 // The rows of a Q8_0 cache that the sequences hold as the pages of an F16 cache of scratch (k, v: n_seq *
 // max_pages pages of n_kv tiles each; table: its page table, n_seq x max_pages, -1 for a page outside the
 // pool).  window > 0: rows ahead of every query's window are left out.
-cudaError_t launch_kv_expand(const KvCache& c, int64_t n_seq, const int32_t* starts, const int32_t* pages, int64_t max_pages,
+cudaError_t launch_kv_expand(const KvCache& c, int64_t n_seq, int64_t n_tok, const int32_t* starts, const int32_t* pages, int64_t max_pages,
                              const int32_t* lens, int window, void* k, void* v, int32_t* table, int sms, cudaStream_t s);
 
 // What the C entry points of api_attn.cu share with api.cu: the SMs of this call and the

@@ -310,3 +310,26 @@ def test_expansion_keeps_to_its_room(syn, width, want):
     torch.cuda.synchronize()
     assert before - torch.cuda.mem_get_info()[0] <= 2 ** 31 + 2 ** 22
     syn.check(syn.syn_release(), "syn_release")
+
+
+@pytest.mark.parametrize("n_seq,width", [(2, 4096), (300, 64)])
+@pytest.mark.parametrize("window", [0, 40])
+def test_expansion_of_few_pages_of_a_wide_table(syn, n_seq, width, window):
+    """A Q8_0 cache expanded ahead of the prefill gives the same bits whatever room its page table has
+    behind the lengths, and whatever ids stand there."""
+    import torch
+    rng = np.random.default_rng([n_seq, width, 51])
+    heads, dim, page = 16, 64, 16
+    new = [int(x) for x in rng.integers(100, 400, n_seq)]
+    lens = [m + int(rng.integers(0, 200)) if i % 7 else m // 2 for i, m in enumerate(new)]
+    cache, pages, _ = make_cache(syn, rng, Q8_0, 1, dim, page, lens)
+    q = on(rng.standard_normal((sum(new), heads, dim)).astype(np.float16))
+    opt = {"slopes": on(2.0 ** -np.arange(1, heads + 1).astype(np.float32)), "window": window}
+    starts = int32(np.concatenate([[0], np.cumsum(new)]))
+    narrow = syn.prepare_attn_prefill(cache, q, starts, pages, int32(lens), **opt)
+    assert launches(syn, narrow) == 2
+    wide = torch.randint(-9, 10 ** 6, (n_seq, width), dtype=torch.int32, device="cuda")
+    for s, n in enumerate(lens):
+        wide[s, :-(-n // page)] = pages[s, :-(-n // page)]
+    assert torch.equal(syn.attn_prefill(cache, q, starts, wide, int32(lens), **opt), narrow())
+    assert syn.device_status() == syn.OK

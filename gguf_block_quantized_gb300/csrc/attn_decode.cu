@@ -523,8 +523,13 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, NT == 1 ? DEC_RESIDENT<D, Q8> 
         auto look_up = [&]() {
             if (k_next < chunk_end) {
                 const int row = ch.at(k_next) << 4;
-                id_lo = page_of(row);
-                id_hi = p.c.page_shift >= 4 ? id_lo : page_of(row + 8);
+                // (a chunk holds a key that is seen; half of one, a page of its own, may not)
+                if (p.c.page_shift >= 4) {
+                    id_lo = id_hi = page_of(row);
+                } else {
+                    id_lo = vis.any(row, row + 8) ? page_of(row) : -1;
+                    id_hi = vis.any(row + 8, row + 16) ? page_of(row + 8) : -1;
+                }
             }
         };
         look_up();

@@ -129,6 +129,7 @@ struct Item {
     int n_split, sp, index;  // parts of the item, this one, the item's number
     int s, h, row0, rows, n_new, tok0, len, prefix;
     Tiles tiles;
+    Visible seen;  // what some row sees lies in here
 };
 static_assert(sizeof(Item) <= 96, "two items' space in shared memory");
 __device__ __forceinline__ Item item_of(volatile const int* w) {
@@ -150,6 +151,10 @@ __device__ __forceinline__ Item item_of(volatile const int* w) {
     it.tiles.a1 = w[14];
     it.tiles.b0 = w[15];
     it.tiles.b1 = w[16];
+    it.seen.first = w[17];
+    it.seen.pre = w[18];
+    it.seen.low = w[19];
+    it.seen.end = w[20];
     return it;
 }
 
@@ -1011,7 +1016,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 if (lane < n_box && j < it.len) {
                     const int x = table[j >> p.c.page_shift];
                     if ((unsigned)x < (unsigned)p.c.n_pages) id = x;
-                    else record_error(p.err, SYN_DEVERR_BOUNDS);
+                    else if (it.seen.any(j, j + box)) record_error(p.err, SYN_DEVERR_BOUNDS);  // (else it may be gone)
                 }
                 if (!(ok = mbar_wait(smem_u32(Q8 ? &raw_empty[st] : &kv_empty[st]), (turn & 1) ^ 1, p.err, abort_flag))) break;
                 const int cell = j & ((1 << p.c.page_shift) - 1);
@@ -1140,6 +1145,10 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                     if (ae > mf) tl.a1 = (ae + BN - 1) / BN;
                     if (tl.b1 > tl.b0) tl.a1 = max(tl.a0, min(tl.a1, tl.b0));
                 }
+                it.seen.first = mf;
+                it.seen.pre = pre_end;
+                it.seen.low = ml;
+                it.seen.end = me;
                 const int all = tl.count();
                 // Each part more shortens what a part computes and lengthens the join: sqrt(keys / 64) parts.
                 // Measured, one sequence, 32 / 8 heads of 128 (us): 64 tokens over 4096 keys
@@ -1173,6 +1182,10 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                     o[14] = it.tiles.a1;
                     o[15] = it.tiles.b0;
                     o[16] = it.tiles.b1;
+                    o[17] = it.seen.first;
+                    o[18] = it.seen.pre;
+                    o[19] = it.seen.low;
+                    o[20] = it.seen.end;
                     mbar_arrive(smem_u32(&item_full[slot]));
                 }
                 __syncwarp();

@@ -38,6 +38,9 @@ struct Visible {
     __device__ __forceinline__ bool operator()(int j) const {
         return j >= first && (j < pre || (j >= low && j < end));
     }
+    __device__ __forceinline__ bool any(int a, int b) const {  // of the keys a .. b - 1
+        return max(a, first) < min(b, pre) || max(a, low) < min(b, end);
+    }
 };
 
 __device__ __forceinline__ Visible visible_of(int len, int pos, int first, int prefix, int window) {

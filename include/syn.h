@@ -354,7 +354,8 @@ SYN_API int syn_mul_mat_prefill_static(int type, const void* W, int64_t n_out, i
  * Lengths, tables, slots and positions are read on the device, so a captured graph can be
  * replayed as they change.  A page or slot index outside the pool is not followed: that row is
  * skipped (or reads as zeros) and syn_device_status returns SYN_ERR_BOUNDS; the outputs that
- * depend on it are invalid.  A length that its page table cannot hold is cut to it.  A call of no
+ * depend on it are invalid.  The ids of pages none of whose rows a query sees (ahead of the window, past
+ * the length) may be anything.  A length that its page table cannot hold is cut to it.  A call of no
  * tokens or no sequences does nothing: its tensors may be NULL, and its tables have no columns.
  * ====================================================================================== */
 typedef struct {

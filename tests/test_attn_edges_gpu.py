@@ -333,3 +333,44 @@ def test_expansion_of_few_pages_of_a_wide_table(syn, n_seq, width, window):
         wide[s, :-(-n // page)] = pages[s, :-(-n // page)]
     assert torch.equal(syn.attn_prefill(cache, q, starts, wide, int32(lens), **opt), narrow())
     assert syn.device_status() == syn.OK
+
+
+# ---- pages that no query sees --------------------------------------------------------------
+
+@pytest.mark.parametrize("t,new", WAYS)
+@pytest.mark.parametrize("page", [8, 16, 64])
+def test_pages_that_no_query_sees_may_be_gone(syn, t, new, page):
+    """A server gives back the pages that have left the window: their ids in the table are no error, and
+    an id outside the pool in a page that a query sees still is one."""
+    import torch
+    rng = np.random.default_rng([t, new, page, 47])
+    heads, window = 8, 37
+    n = 700 + page // 2 + 3
+    cache, pages, _ = make_cache(syn, rng, t, 1, 64, page, [n])
+    q = on(rng.standard_normal((new, heads, 64)).astype(np.float16))
+    slopes = on(2.0 ** -np.arange(1, heads + 1).astype(np.float32))
+    opt = {"window": window, "slopes": slopes}
+    calls = {"prefill": (new, lambda p: syn.attn_prefill(cache, q, int32([0, new]), p, int32([n]), **opt)),
+             "decode": (1, lambda p: syn.attn_decode(cache, q[:1], p, int32([n]), **opt))}
+    for name, (m, call) in calls.items():
+        want = call(pages)
+        low = n - m - window + 1  # the first row that some query sees
+        gone = pages.clone()
+        gone[0, :low // page] = -1
+        assert torch.equal(call(gone), want), name
+        assert syn.device_status(clear=True) == syn.OK, name
+        gone[0, low // page] = -1
+        call(gone)
+        assert syn.device_status(clear=True) == syn.ERR_BOUNDS, name
+    # a prefix is seen past the window: its pages stay, the ones between may go
+    prefix = int32([page + 3])
+    want = syn.attn_decode(cache, q[:1], pages, int32([n]), prefix=prefix, **opt)
+    gone = pages.clone()
+    gone[0, 2:(n - window) // page] = -1
+    assert torch.equal(syn.attn_decode(cache, q[:1], gone, int32([n]), prefix=prefix, **opt), want)
+    assert syn.device_status(clear=True) == syn.OK
+    want = syn.attn_prefill(cache, q, int32([0, new]), pages, int32([n]), prefix=prefix, **opt)
+    gone[0, 2:] = pages[0, 2:]
+    gone[0, 2:(n - new - window + 1) // page] = -1
+    assert torch.equal(syn.attn_prefill(cache, q, int32([0, new]), gone, int32([n]), prefix=prefix, **opt), want)
+    assert syn.device_status(clear=True) == syn.OK

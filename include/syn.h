@@ -430,7 +430,9 @@ enum {
  *   out = sum_j softmax(s)_j v_j over the visible keys; zeros where no key is visible
  * so first[] (one per query) separates packed documents, and a prefix is seen by every query of
  * its sequence, before and after it and past the window.  What a key or value that a query does
- * not see holds (infinities and NaN included) does not reach that query's output. */
+ * not see holds (infinities and NaN included) does not reach that query's output.  An infinite or NaN
+ * value that it does see makes its column of the output infinite or NaN, no other; which of the two is not
+ * defined (weights are held in parts, and a part of 0 times infinity is NaN). */
 typedef struct {
     int n_heads;            /* query heads, a multiple of n_kv_heads: head i reads kv head
                                i / (n_heads / n_kv_heads) */

@@ -374,3 +374,32 @@ def test_pages_that_no_query_sees_may_be_gone(syn, t, new, page):
     gone[0, 2:(n - new - window + 1) // page] = -1
     assert torch.equal(syn.attn_prefill(cache, q, int32([0, new]), gone, int32([n]), prefix=prefix, **opt), want)
     assert syn.device_status(clear=True) == syn.OK
+
+
+# ---- infinite values that a query sees ------------------------------------------------------
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_decode_infinite_values(syn, dim):
+    """An infinity or NaN among the values that a query sees reaches its column of the output alone (as an
+    infinity or NaN); the other columns, heads and sequences are as they are."""
+    rng = np.random.default_rng([dim, 48])
+    heads, kv, page, lens = 8, 2, 16, [400, 90, 3000]
+    cache, pages, seqs = make_cache(syn, rng, F16, kv, dim, page, lens)
+
+    def put(s, row, h, e, x):
+        cache.v[int(pages[s, row // page]), h, row % page, e] = x
+
+    put(0, 17, 0, 5, float("inf")), put(0, 333, 0, 5, float("inf"))
+    put(0, 200, 0, 9, float("-inf"))
+    put(0, 40, 1, 1, float("inf")), put(0, 41, 1, 1, float("-inf"))
+    put(0, 60, 1, 2, float("nan"))
+    put(2, 2222, 0, 31, float("inf"))
+    q = rng.standard_normal((3, heads, dim)).astype(np.float16)
+    ref, size = reference(q, seqs, [np.array([n - 1]) for n in lens], [np.zeros(1)] * 3, [0] * 3, 0, dim ** -0.5, 0.0, None)
+    got = syn.attn_decode(cache, on(q), pages, int32(lens)).double().cpu().numpy()
+    g = heads // kv
+    for s, heads_of, e in ((0, slice(0, g), 5), (0, slice(0, g), 9), (0, slice(g, None), 1), (0, slice(g, None), 2), (2, slice(0, g), 31)):
+        assert not np.isfinite(got[s, heads_of, e]).any()
+        got[s, heads_of, e] = ref[s, heads_of, e]
+    assert (np.abs(got - ref) <= decode_bound(size, ref, False)).all()
+    assert syn.device_status() == syn.OK

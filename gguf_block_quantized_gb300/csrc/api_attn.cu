@@ -3,6 +3,7 @@
 // attn_prefill.cu.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -65,7 +66,8 @@ int attn_of(const syn_attn* a, const syn::KvCache& c, int64_t rows, const void* 
     d->n_heads = a->n_heads;
     d->window = a->window;
     d->out_f16 = a->out_type == SYN_OUT_F16;
-    d->scale = a->scale;
+    // (past 2^100 the largest score alone counts, as fp16 products are multiples of 2^-48; times log2(e) it stays finite)
+    d->scale = std::min(std::max(a->scale, -0x1p100f), 0x1p100f);
     d->cap = a->cap;
     return SYN_OK;
 }

@@ -945,7 +945,7 @@ cudaError_t launch_attn_decode(const KvCache& c, const AttnDesc& a, int64_t n_se
         p.err = err;
         p.scale = a.scale;
         p.cap = a.cap;
-        p.inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
+        p.inv_cap = a.cap > 0.0f ? std::min(1.0f / a.cap, 0x1p127f) : 0.0f;  // (finite: a score of 0 stays 0)
         p.n_seq = (int)std::min<int64_t>(DEC_MAX_SEQ, n_seq - s0);
         p.g = a.n_heads / c.n_kv;
         const int nt = decode_nt(p.g, c.dim);

@@ -464,7 +464,8 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
         const uint32_t o_base = lane_base + L::O_COL + qt * D;
         const float c_log2 = p.scale * 1.4426950408889634f;
         const float cap_log2 = p.cap * 1.4426950408889634f;
-        const float to_cap = p.cap > 0.0f ? p.scale / p.cap : 0.0f, to_cap2 = 2.0f * 1.4426950408889634f * to_cap;
+        // (finite however small the cap is: a score of 0 stays 0)
+        const float to_cap = p.cap > 0.0f ? fminf(fmaxf(p.scale / p.cap, -1e38f), 1e38f) : 0.0f, to_cap2 = 2.0f * 1.4426950408889634f * to_cap;
         int done = 0, q_turn = 0, joins = 0;  // tiles and Q tiles of this row tile, syncs of the softmax warps so far
         auto softmax_sync = [&]() {  // (bounded, as every wait: a warp may have given up)
             __syncwarp();
@@ -536,10 +537,12 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                             // the general form, which has to share that unit with the powers.  Each score goes
                             // by its own size, so that its bits do not depend on the others'; the vote only spares
                             // the general form where no score needs it (keys that a row does not see may vote).
-                            const float k = to_cap * to_cap, to_half = fabsf(to_cap);  // (the scale may be negative)
+                            const float k = to_cap * to_cap;
                             const float a0 = 0.999999464f * c_log2, a1 = -0.333263761f * c_log2 * k, a2 = 0.131909124f * c_log2 * k * k,
                                         a3 = -0.0444185817f * c_log2 * k * k * k;
                             const uint64_t b0 = pack2(a0, a0), b1 = pack2(a1, a1), b2 = pack2(a2, a2), b3 = pack2(a3, a3);
+                            // (the scale may be negative; with a cap so small that a coefficient overflows no score is small)
+                            const float to_half = fabsf(a3) < INFINITY ? fabsf(to_cap) : INFINITY;
                             auto small2 = [&](uint64_t x) {
                                 const uint64_t z = mul2(x, x);
                                 return unpack2(mul2(x, fma2(z, fma2(z, fma2(z, b3, b2), b1), b0)));
@@ -755,7 +758,10 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 // have been past what fp16 holds.  That is slow, so it waits until no other warp waits for this one.
                 const float2 odd = unpack2(odd2);
                 const bool odd_l = !(l * 0.0f == 0.0f), odd_o = !(odd.x + odd.y == 0.0f);
-                const uint32_t redo = __ballot_sync(0xffffffffu, row_ok && (odd_l ? p.raw.q8 : odd_o));
+                // (And where scores are in the millions: the powers take scores times the scale, unrounded, less a rounded
+                // maximum, and what lies between the two has to stay well below 1.)
+                const bool far = !MOD && fabsf(m) > 0x1p22f && fabsf(m) < INFINITY;
+                const uint32_t redo = __ballot_sync(0xffffffffu, row_ok && (far || (odd_l ? p.raw.q8 : odd_o)));
                 if (it.n_split > 1) {
                     split_redo = redo;
                 } else if (redo) {

@@ -403,3 +403,53 @@ def test_decode_infinite_values(syn, dim):
         got[s, heads_of, e] = ref[s, heads_of, e]
     assert (np.abs(got - ref) <= decode_bound(size, ref, False)).all()
     assert syn.device_status() == syn.OK
+
+
+# ---- options at the ends of the float range --------------------------------------------------
+
+@pytest.mark.parametrize("t,new", WAYS)
+@pytest.mark.parametrize("cap", [1e-7, 1e-12, 1e-39, 1e38])
+def test_caps_at_the_ends_of_the_range(syn, t, new, cap):
+    """Scores of zero stay zero however small the cap is; a cap far above every score changes nothing."""
+    rng = np.random.default_rng([t, new, 49])
+    heads, n = 8, new + 30
+    cache, pages, seqs = make_cache(syn, rng, t, 1, 64, 16, [n])
+    q = rng.standard_normal((new, heads, 64)).astype(np.float16)
+    q[::3] = 0
+    cap = float(np.float32(cap))
+    ref, size = attn_ref.attention(q, *seqs[0], np.arange(n - new, n), np.zeros(new), 0, 0, 0.125, 0.0 if cap > 1 else cap, None)
+    got = syn.attn_prefill(cache, on(q), int32([0, new]), pages, int32([n]), cap=cap).double().cpu().numpy()
+    assert (np.abs(got - ref) <= prefill_bound(t, size, np.abs(seqs[0][1]).max(), ref, False)).all()
+    one = syn.attn_decode(cache, on(q[-4:]), pages.expand(4, -1).contiguous(), int32([n] * 4), cap=cap).double().cpu().numpy()
+    last, size = attn_ref.attention(q[-4:], *seqs[0], np.array([n - 1] * 4), np.zeros(4), 0, 0, 0.125, 0.0 if cap > 1 else cap, None)
+    assert (np.abs(one - last) <= decode_bound(size, last, False)).all()
+
+
+@pytest.mark.parametrize("t,new", WAYS[:2])
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.0 ** 34])
+def test_scales_at_the_ends_of_the_range(syn, t, new, scale):
+    """The key of the largest score takes all the weight; queries of zeros see every key alike."""
+    rng = np.random.default_rng([t, new, 50])
+    heads, n, dim = 8, new + 30, 64
+    k = np.zeros((n, 1, dim), np.float16)
+    k[:, 0, 0] = rng.permutation(n) - n // 2  # (products: whole numbers apart)
+    codes = k[:, 0].astype(np.int8)
+    v = rng.integers(-100, 100, (n, dim)).astype(np.int8)
+    rows = -(-n // 16) * 16
+    if t == F16:
+        pad = lambda x: on(np.pad(x, ((0, rows - n), (0, 0))).astype(np.float16).reshape(-1, 1, 16, dim))  # noqa: E731
+        cache = syn.KVCache(F16, 1, dim, 16, pad(codes), pad(v))
+    else:
+        one = np.ones((n, dim // 32), np.float16)
+        cache = syn.KVCache(Q8_0, 1, dim, 16, q8_pool(codes, one, 16), q8_pool(v, one, 16))
+    q = np.zeros((new, heads, dim), np.float16)
+    q[:, 1::2, 0] = 2.0 ** -8
+    pages = int32(np.arange(rows // 16)[None])
+    got = syn.attn_prefill(cache, on(q), int32([0, new]), pages, int32([n]), scale=scale).double().cpu().numpy()
+    one = syn.attn_decode(cache, on(q[-1:]), pages, int32([n]), scale=scale).double().cpu().numpy()
+    for i in range(new):
+        seen = codes[:n - new + i + 1, 0].astype(int) * (1 if scale > 0 else -1)
+        top = v[seen.argmax()].astype(np.float64)
+        mean = v[:len(seen)].astype(np.float64).mean(0)
+        assert (got[i, 1::2] == top).all() and (np.abs(got[i, ::2] - mean) <= 100 * 2.0 ** -11).all()
+    assert (one[0, 1::2] == top).all() and (np.abs(one[0, ::2] - mean) <= 100 * 2.0 ** -20).all()

@@ -85,7 +85,19 @@ struct Workspace {
 
 std::mutex g_mu;
 std::map<int, DeviceState> g_dev;
-std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
+// A workspace belongs to a device and a stream.  The handle of the per-thread default stream names another
+// stream in every thread: its key is the id of the calling thread's.
+using StreamKey = std::pair<int, unsigned long long>;
+bool stream_key(int dev, cudaStream_t s, StreamKey* out) {
+    unsigned long long id = s == cudaStreamLegacy ? 0 : reinterpret_cast<uintptr_t>(s);
+    if (s == cudaStreamPerThread) {
+        if (cudaStreamGetId(s, &id) != cudaSuccess) return false;
+        id |= 1ull << 63;  // (no handle's bit)
+    }
+    *out = {dev, id};
+    return true;
+}
+std::map<StreamKey, Workspace> g_ws;
 // the attention's workspaces: counters (zero between calls), then partial results; and the expanded
 // rows of Q8_0 caches.  What they outgrow is kept until syn_release: a graph captured before may use it.
 struct AttnWorkspace {
@@ -95,7 +107,7 @@ struct AttnWorkspace {
     size_t row_bytes = 0;
     std::vector<void*> outgrown;
 };
-std::map<std::pair<int, cudaStream_t>, AttnWorkspace> g_attn_ws;
+std::map<StreamKey, AttnWorkspace> g_attn_ws;
 
 int current_device(int* dev) {
     return cudaGetDevice(dev) == cudaSuccess ? SYN_OK : SYN_ERR_CUDA;
@@ -177,9 +189,10 @@ size_t prefill_ws_bytes(int64_t n_in, int64_t n_tok) { return (size_t)(n_in * n_
 
 int workspace_for(cudaStream_t s, size_t need, void** out) {
     int dev;
-    if (current_device(&dev) != SYN_OK) return SYN_ERR_CUDA;
+    StreamKey key;
+    if (current_device(&dev) != SYN_OK || !stream_key(dev, s, &key)) return SYN_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
-    Workspace& w = g_ws[{dev, s}];
+    Workspace& w = g_ws[key];
     if (w.bytes < need) {
         if (w.ptr) {
             if (cudaDeviceSynchronize() != cudaSuccess) return SYN_ERR_CUDA;
@@ -205,9 +218,10 @@ void note_launches(int n) { g_launches += n; }
 
 int attn_workspace(cudaStream_t s, size_t zeroed, size_t rest, size_t* zeroed_at, void** out) try {
     int dev;
-    if (current_device(&dev) != SYN_OK) return SYN_ERR_CUDA;
+    StreamKey key;
+    if (current_device(&dev) != SYN_OK || !stream_key(dev, s, &key)) return SYN_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
-    AttnWorkspace& w = g_attn_ws[{dev, s}];
+    AttnWorkspace& w = g_attn_ws[key];
     if (w.zeroed < zeroed || w.rest < rest) {
         const size_t z = std::max(w.zeroed, zeroed), r = std::max(w.rest, rest);
         if (cudaDeviceSynchronize() != cudaSuccess) return SYN_ERR_CUDA;  // (refused while capturing)
@@ -235,9 +249,10 @@ int attn_workspace(cudaStream_t s, size_t zeroed, size_t rest, size_t* zeroed_at
 
 int attn_rows_workspace(cudaStream_t s, size_t bytes, void** out) try {
     int dev;
-    if (current_device(&dev) != SYN_OK) return SYN_ERR_CUDA;
+    StreamKey key;
+    if (current_device(&dev) != SYN_OK || !stream_key(dev, s, &key)) return SYN_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
-    AttnWorkspace& w = g_attn_ws[{dev, s}];
+    AttnWorkspace& w = g_attn_ws[key];
     if (w.row_bytes < bytes) {
         size_t n = size_t(1) << 20;  // powers of two: what is outgrown adds up to less than what is used
         while (n < bytes) n *= 2;

@@ -300,7 +300,9 @@ def prepare_batch(items, n_tok: int, stream=None, staged=None) -> PreparedBatch:
 
 # ---- paged key-value cache and attention ---------------------------------------------------
 # (Outputs the helpers allocate belong to torch's current stream: with another `stream`, give
-# out / q_out and order that stream behind what the buffers were last used for.)
+# out / q_out and order that stream behind what the buffers were last used for.  A graph keeps the
+# workspace of the stream it was captured on: capture graphs that are to run at the same time on streams of
+# their own, not on torch's one default capture stream.)
 
 class KVCache:
     """A paged cache over two torch pools (held by reference): ``k`` and ``v`` with the pages in

@@ -171,7 +171,10 @@ SYN_API int syn_quantize_activations(int wtype, const float* X, int64_t n_tok, i
  * n_tok == 0 is a no-op.  Asynchronous.  The prefill path may grow the workspace (see
  * syn_reserve); growth allocates device memory and synchronizes the device, so reserve
  * before capturing a CUDA graph.  The workspace belongs to (device, stream): calls on one
- * stream are ordered; calls on different streams use different workspaces. */
+ * stream are ordered; calls on different streams use different workspaces (every thread's
+ * cudaStreamPerThread is a stream of its own).  A captured graph keeps the workspace of the
+ * stream that it was captured on: graphs captured on one stream, and calls on that stream, must
+ * not run at the same time. */
 SYN_API int syn_mul_mat(int type, const void* W, int64_t n_out, int64_t n_in,
                 const float* X, int64_t n_tok, float* Y, syn_stream_t stream);
 

@@ -453,3 +453,43 @@ def test_scales_at_the_ends_of_the_range(syn, t, new, scale):
         mean = v[:len(seen)].astype(np.float64).mean(0)
         assert (got[i, 1::2] == top).all() and (np.abs(got[i, ::2] - mean) <= 100 * 2.0 ** -11).all()
     assert (one[0, 1::2] == top).all() and (np.abs(one[0, ::2] - mean) <= 100 * 2.0 ** -20).all()
+
+
+# ---- the calling thread's own stream --------------------------------------------------------
+
+def test_threads_on_their_own_default_streams(syn):
+    """The handle of the per-thread default stream names another stream in every thread: split calls of
+    two threads at once, each with a workspace of its own, give what they give one after the other."""
+    import threading
+
+    import torch
+    rng = np.random.default_rng(54)
+    heads, kv, dim, page, n = 8, 2, 128, 64, 30000
+    cache, pages, _ = make_cache(syn, rng, F16, kv, dim, page, [n])
+    qs = [on(rng.standard_normal((1, heads, dim)).astype(np.float16)) for _ in range(2)]
+    ld = int32([n])
+    want = [syn.attn_decode(cache, q, pages, ld) for q in qs]
+    outs = [[torch.zeros_like(want[0]) for _ in range(100)] for _ in qs]
+    torch.cuda.synchronize()
+    gate, wrong = threading.Barrier(2), []
+
+    def work(i):
+        calls = [syn.prepare_attn_decode(cache, qs[i], pages, ld, out, stream=2) for out in outs[i]]  # cudaStreamPerThread
+        try:
+            gate.wait(20)
+            for call in calls:
+                call()
+        except Exception as e:  # (told below)
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong
+    for i in range(2):
+        for out in outs[i]:
+            assert torch.equal(out, want[i])
+    assert syn.device_status() == syn.OK

@@ -80,13 +80,17 @@ constexpr size_t kCountBytes = size_t(1) << 20;
 // A Q8_0 prefill expands its cache to fp16 ahead of the kernel, once, where the kernel would expand each
 // row many times: once for every 256 (token, head) rows of a sequence that see it.  It does so from this
 // many such tiles a sequence on average on, and up to kExpandBytes of scratch in all.  Measured on GB300,
-// 32 / 8 heads, 8 sequences, all rows new, expanded in the kernel / ahead (us):
-//   slopes, heads of 128:  8 tiles 51.2 / 49.2, 16 tiles 88.1 / 88.1, 64 tiles 530 / 432
-//   slopes, heads of 64:   8 tiles 38.7 / 41.0, 16 tiles 70.7 / 70.3, 64 tiles 424 / 352
-//   none, heads of 128:    8 tiles 38.9 / 44.0, 16 tiles 69.7 / 75.8, 64 tiles 380 / 343
-//   none, heads of 256:    8 tiles 52.3 / 57.9, 16 tiles 107 / 111,   64 tiles 764 / 696
-// one sequence with 512 new rows of 16384 (8 tiles), slopes: heads of 128 147 / 138, of 64 103 / 93; none,
-// heads of 128: 117 / 126.  Fewer tiles: 128 new rows of 4096 each (2 tiles), slopes, heads of 128: 57 / 82.
+// 32 / 8 heads, one call at a time over a cold L2, expanded in the kernel / ahead (us).  8 sequences of 256, 512,
+// 1024 and 2048 tokens, all new (4, 8, 16 and 32 tiles each):
+//   slopes, heads of 64:   31 / 33,  56 / 54,  128 / 109,  378 / 279
+//   slopes, heads of 128:  40 / 41,  68 / 66,  156 / 128,  453 / 316
+//   slopes, heads of 256:  44 / 50,  93 / 95,  253 / 220,  828 / 657
+//   none, heads of 64:     24 / 28,  42 / 47,   89 / 88,   236 / 219
+//   none, heads of 128:    29 / 36,  50 / 58,  113 / 111,  322 / 279
+//   none, heads of 256:    42 / 45,  87 / 82,  234 / 203,  760 / 607
+// One sequence of 16384 rows, the last 512, 1024 and 2048 new (8, 16 and 32 tiles): slopes, heads of 128
+// 240 / 164, 416 / 259, 746 / 456; none, heads of 128 162 / 144, 283 / 227, 515 / 394.
+// (So 32 is late where there are no slopes and many cached rows, and for heads of 256.)
 int64_t expand_tiles(const syn::KvCache& c, const syn::AttnDesc& a) {
     return (a.slopes || a.cap > 0.0f) && c.dim <= 128 ? 8 : 32;
 }

@@ -9,8 +9,9 @@
 //   - Warps work alone: each copies chunks of 16 rows of K and V into a ring of its own in shared
 //     memory (cp.async) and multiplies them with mma.sync m16n8k16, the 16 cached rows as the A
 //     operand and up to 8 query heads as the columns: S^T = K Q^T, then O^T += V^T P^T.  A
-//     chunk of 128-wide rows is about 390 instructions (F16) or 650 (Q8_0) of a warp, where its bytes
-//     take 1400 or 750 issue slots of an SM to arrive: Q8_0 is near the issue limit.
+//     chunk of 128-wide rows is about 430 instructions (F16) or 710 (Q8_0) of a warp, where its bytes
+//     take 1400 or 750 issue slots of an SM to arrive.  Q8_0 fills 60 % of the slots, its busiest pipe (integer
+//     and conversion) 40 %: four warps a scheduler do not hide what their instructions wait for each other.
 //   - p is split into two fp16 numbers (head and tail, 22 bits) and each chunk's product starts
 //     from zero and is added to the fp32 sums by fma, because the tensor pipe's own additions
 //     truncate.  Scores likewise come from short chains.  So the result is as exact as fp32
@@ -29,9 +30,9 @@
 //     covers an item writes the output; else it leaves a partial in the workspace, and the CTA
 //     that finishes an item last (a counter) joins the partials in order.  No CTA waits.
 //
-// Measured on GB300, 32 / 8 heads of 128 (share of a copy's rate): 300 sequences of 2500 rows, F16 96 %,
-// Q8_0 71 %; 48 sequences of 100 to 4000, F16 44.4 us, 71 %; 128 of 500 to 8191, Q8_0, capped 169 us, 67 %;
-// one of 130001, F16 92 us, 85 %; one of 77 (heads of 64) 5.2 us.
+// Measured on GB300, 32 / 8 heads of 128 (share of a copy's rate): 300 sequences of 2500 rows, F16 98 %,
+// Q8_0 77 %; 48 sequences of 100 to 4000, F16 44.5 us, 71 %; 128 of 500 to 8191, Q8_0, capped 175 us, 65 %;
+// one of 130001, F16 92 us, 85 %; one of 77 (heads of 64) 5.3 us.
 #include <algorithm>
 
 #include "kernels.h"
@@ -42,11 +43,11 @@ namespace syn {
 constexpr int DEC_WARPS = 4;
 constexpr int DEC_SLOTS = 3;    // of a warp's ring: the keys or the values of a chunk each
 // What an item's start and end cost, in steps.  Measured (us, 0 / 2 / 8): 58 sequences of 40 to 14210 rows, 32 / 8
-// heads of 128, Q8_0 117 / 82 / 86, F16 139 / 119 / 117; 58 of 2500 rows each, Q8_0 82 / 82 / 86.
+// heads of 128, Q8_0 117 / 72 / 80, F16 140 / 101 / 100; 58 of 2500 rows each, Q8_0 75 / 73 / 78.
 constexpr int DEC_ITEM = 2;
 // A part's share of the join, per value, against a step (blocks of sqrt(steps * values * this)).
-// Measured (us, 0 / 2e-4 / 8e-4): one sequence of 32768 rows, F16, 24 / 1 heads of 128 74 / 43 / 49; one of
-// 40642, Q8_0, 16 / 2 heads of 64 35 / 27 / 30.
+// Measured (us, 0 / 2e-4 / 8e-4): one sequence of 32768 rows, F16, 24 / 1 heads of 128 72 / 40 / 49; one of
+// 40642, Q8_0, 16 / 2 heads of 64 30 / 27 / 31.
 constexpr float DEC_JOIN = 2e-4f;
 constexpr int DEC_MAX_SEQ = 1024;  // sequences of one launch (their step counts are in shared memory)
 // p is held in fp16 as 2^14 p, so that small p stay normal numbers; Q8_0 as 2^13 p: times a relative scale below 4

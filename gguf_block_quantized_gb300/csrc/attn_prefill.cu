@@ -6,7 +6,8 @@
 //
 // An item is 128 or 256 rows of (new token, query head of one kv head), the heads of a token next to
 // each other, so that all the heads of a kv head share the cached rows; its keys come in tiles of
-// BN.  One persistent CTA per SM takes items until none is left, the longest first.  Warp roles:
+// BN.  One persistent CTA per SM takes items until none is left, from the packed batch's end: of a sequence
+// the last tokens, which see the most keys, come first.  Warp roles:
 //   schedule one warp: takes the next item (a counter), works out what it needs, an item ahead of the
 //            others, so that loads and products of an item begin while the one before is written;
 //   softmax  4 warps per 128 rows, a thread per row: S from tensor memory, the row's maximum, p in
@@ -30,10 +31,10 @@
 // Few rows over a long cache: an item's tiles are split between CTAs (no CTA waits: the last to
 // finish, by a counter, joins the partials in order).
 //
-// Measured on GB300, 32 / 8 heads of 128, F16: a prompt of 8192 tokens 395 us, 1.39 PFLOP/s (73 % of
+// Measured on GB300, 32 / 8 heads of 128, F16: a prompt of 8192 tokens 395 us, 1.40 PFLOP/s (71 % of
 // a library matrix product's rate: a tile of 128 keys takes 2700 cycles, the products of its
-// two row tiles 2048: a row tile's softmax, 1450 cycles, stands between its two products); 6 prompts of up to 1001 tokens, capped in a window of 1024, 68 us; 2 chunks of up
-// to 2000 tokens over 8000 Q8_0 rows, slopes and documents, 105 us; 9 tokens over 709 rows, heads of 64, 12.6 us.
+// two row tiles 2048: a row tile's softmax, 1450 cycles, stands between its two products); 6 prompts of up to 1001 tokens, capped in a window of 1024, 69 us; 2 chunks of up
+// to 2000 tokens over 8000 Q8_0 rows, slopes and documents, 98 us; 9 tokens over 709 rows, heads of 64, 12.2 us.
 #include <algorithm>
 #include <climits>
 
@@ -1092,7 +1093,7 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
                 const int64_t b = w / max_split;
                 it.index = (int)b;
                 it.sp = (int)(w - b * max_split);
-                // the last tiles of a sequence see the most keys: they go first
+                // the last tiles of a sequence see the most keys: they go first (of the sequences, the last)
                 const int qtile = n_tiles_q - 1 - (int)(b / p.c.n_kv);
                 it.h = (int)(b % p.c.n_kv);
                 int before;

@@ -15,7 +15,9 @@
 // 150 KB of loads are in flight on an SM whatever the threads wait for.  A Q8_0 block is 8
 // neighbouring lanes, its amax three shuffles.  Measured on GB300: 8192 tokens of 32 / 8 heads of 128 into
 // F16 47.9 us, 6.3 TB/s (93 % of a copy's rate; every thread loading for itself 66 us); one token
-// 3.7 us; 4095 tokens into Q8_0 and back (k_kv_read) 42.1 us.
+// 3.8 us; 4095 tokens into F16 26.5 us (84 %), into Q8_0 31.3 (68 %), there instructions bound it: 68 % of the
+// issue slots, the integer and conversion pipe at 50 %.  Read back (k_kv_read) 10.7 us either way: its loads wait
+// for the slot they go by, and start and end are most of it.
 #include <algorithm>
 
 #include "kernels.h"

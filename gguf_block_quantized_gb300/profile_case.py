@@ -19,7 +19,9 @@ Cases (synthetic weights ~N(0, 0.02), activations ~N(0, 1)):
   attn_decode_f16, attn_decode_q8  one token of each of 48 sequences of 2000 cached tokens, 32 / 8
                      heads of 128, pages of 64 (F16: 393 MB of rows)
   attn_decode_long_f16, attn_decode_long_q8  one token of one sequence of 96000 rows
-  attn_prefill_f16, attn_prefill_q8  a prompt of 4096 tokens, 32 / 8 heads of 128
+  attn_prefill_f16, attn_prefill_q8  a prompt of 4096 tokens, 32 / 8 heads of 128 (Q8_0: expanded ahead)
+  attn_prefill_batch_f16, attn_prefill_batch_q8  8 prompts of 512 tokens (Q8_0: expanded in the kernel)
+  kv_read_f16, kv_read_q8  the rows of 4096 tokens back as fp16
 """
 from __future__ import annotations
 
@@ -36,7 +38,8 @@ CASES = {
 
 
 ATTN = ["kv_append_f16", "kv_append_q8", "attn_decode_f16", "attn_decode_q8", "attn_decode_long_f16",
-        "attn_decode_long_q8", "attn_prefill_f16", "attn_prefill_q8"]
+        "attn_decode_long_q8", "attn_prefill_f16", "attn_prefill_q8", "attn_prefill_batch_f16", "attn_prefill_batch_q8",
+        "kv_read_f16", "kv_read_q8"]
 
 
 def attn_case(case: str, reps: int):
@@ -47,7 +50,7 @@ def attn_case(case: str, reps: int):
 
     heads, kv, dim, page = 32, 8, 128, 64
     t = syn.Q8_0 if case.endswith("q8") else syn.F16
-    seqs, rows = (1, 96000) if "long" in case else (48, 2000) if "decode" in case else (1, 4096)
+    seqs, rows = (1, 96000) if "long" in case else (48, 2000) if "decode" in case else (8, 512) if "batch" in case else (1, 4096)
     per = -(-rows // page)
     cache = syn.KVCache.empty(t, kv, dim, page, seqs * per)
     pages = torch.randperm(seqs * per, device="cuda").to(torch.int32).view(seqs, per)
@@ -65,10 +68,13 @@ def attn_case(case: str, reps: int):
     lens = torch.full((seqs,), rows, dtype=torch.int32, device="cuda")
     if case.startswith("kv_append"):
         step = append
+    elif case.startswith("kv_read"):
+        step = syn.prepare_kv_read(cache, slots)
     elif "decode" in case:
         step = syn.prepare_attn_decode(cache, q[:seqs].contiguous(), pages, lens)
     else:
-        step = syn.prepare_attn_prefill(cache, q, torch.tensor([0, rows], dtype=torch.int32, device="cuda"), pages, lens)
+        step = syn.prepare_attn_prefill(cache, torch.cat([q] * seqs), torch.arange(0, seqs * rows + 1, rows, dtype=torch.int32, device="cuda"),
+                                        pages, lens)
     for _ in range(reps):
         step()
     torch.cuda.synchronize()

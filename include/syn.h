@@ -468,7 +468,7 @@ SYN_API int syn_attn_decode(const syn_kv_cache* cache, const syn_attn* attn, int
  * starts[s+1] - 1 (starts: n_seq + 1, ascending from 0, starts[n_seq] = n_tok), the last of its
  * lens[s] rows (all of them in the cache: append first), so token i of its n stands at position
  * lens[s] - n + i.  q: n_tok x n_heads x head_dim fp16; out likewise, fp32 or fp16.  A sequence may
- * have no new token; a token before position 0 (lens[s] < n) sees nothing.
+ * have no new token; a token before position 0 (lens[s] < n) sees the prefix alone, if there is one.
  * The products run on the tensor cores with fp16 operands: p and (Q8_0) the expanded key and value
  * are rounded to fp16 once, scores, sums and maxima are fp32, so an output of either type is exact to
  * about 2^-11 of its row's values, not to fp32's last place (syn_attn_decode is).  A row

@@ -493,3 +493,28 @@ def test_threads_on_their_own_default_streams(syn):
         for out in outs[i]:
             assert torch.equal(out, want[i])
     assert syn.device_status() == syn.OK
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_decode_scales_of_every_size(syn, dim):
+    """Value scales from zero and subnormal numbers to fp16's largest, in any order, and the code -128."""
+    rng = np.random.default_rng([dim, 55])
+    n, heads, page = 333, 8, 16
+    kc, kd, kx = q8_rows(0.5 * rng.standard_normal((n, dim)))
+    vc = rng.integers(-128, 128, (n, dim)).astype(np.int8)
+    vd = (2.0 ** rng.uniform(-24, 9, (n, dim // 32))).astype(np.float16)
+    vd[rng.random(vd.shape) < 0.3] = 0
+    vd[:40] = 0
+    vd[120:] = (2.0 ** rng.uniform(-24, -9, (n - 120, dim // 32))).astype(np.float16)
+    vx = (vc.reshape(n, -1, 32) * vd.astype(np.float64)[..., None]).reshape(n, dim)
+    cache = syn.KVCache(Q8_0, 1, dim, page, q8_pool(kc, kd, page), q8_pool(vc, vd, page))
+    q = rng.standard_normal((4, heads, dim)).astype(np.float16)
+    lens = [n, 37, 70, n]
+    first = np.array([0, 0, 41, 130], np.int32)  # (the second sees zeros alone, the last small scales alone)
+    pages = int32(np.arange(-(-n // page))[None].repeat(4, 0))
+    got = syn.attn_decode(cache, on(q), pages, int32(lens), first=on(first)).double().cpu().numpy()
+    for i in range(4):
+        ref, size = attn_ref.attention(q[i:i + 1], kx[first[i]:lens[i], None], vx[first[i]:lens[i], None], np.array([lens[i] - first[i] - 1]),
+                                       np.zeros(1), 0, 0, dim ** -0.5, 0.0, None)
+        assert (np.abs(got[i:i + 1] - ref) <= decode_bound(size, ref, False)).all(), i
+    assert (got[1] == 0).all() and np.abs(got[3]).max() > 0

@@ -480,7 +480,8 @@ SYN_API int syn_attn_decode(const syn_kv_cache* cache, const syn_attn* attn, int
  * over a Q8_0 cache (not in deterministic mode) first expands the rows of its page table to fp16 in
  * the workspace, n_seq * max_pages * (4 * page_size * n_kv_heads * head_dim + 4) bytes, where that is at
  * most 2 GiB and there is room (rounded up to a power of two; what it outgrew, less than as much again, is
- * kept until syn_release).  Workspace, alignment and errors as for syn_attn_decode;
+ * kept until syn_release).  Workspace (which here grows with n_tok * n_heads), alignment and errors as for
+ * syn_attn_decode;
  * SYN_ERR_SHAPE also for n_tok * n_heads >= 2^31 - 1024.
  * Asynchronous. */
 SYN_API int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_seq, int64_t n_tok,

@@ -26,7 +26,7 @@
 // still hold infinities or NaN, and 0 * inf is not 0: a row whose sums come out non-finite is
 // computed again from the keys it sees, in fp32, when its CTA has done its items (no other warp waits for it
 // then).  With an infinite value in the first row of a prompt of 2048 tokens, 32 / 8 heads of 128, every row is:
-// 3.2 ms where it takes 0.050; 8192 tokens 44 ms, not 0.39.
+// 3.7 ms where it takes 0.050; 8192 tokens 50 ms, not 0.39.
 //
 // Few rows over a long cache: an item's tiles are split between CTAs (no CTA waits: the last to
 // finish, by a counter, joins the partials in order).
@@ -57,7 +57,7 @@ struct Redo {
 
 struct PrefillParams {
     KvCache c;
-    KvCache raw;               // where row_by_hand reads: the user's cache and table, which are c and pages
+    KvCache raw;               // where rows_by_hand reads: the user's cache and table, which are c and pages
     const int32_t* raw_pages;  // unless c is the expanded copy of a Q8_0 cache
     const __half* q;
     int64_t q_stride, out_stride;
@@ -243,12 +243,13 @@ __device__ __forceinline__ void cached8(const uint8_t* tile, int64_t scales, int
 
 // The rows row0, row0 + 1, ... of sequence s (a row: a token and a query head of kv head h) that `bits` names,
 // a lane each, computed again in fp32 from the keys that they see in tiles [t0, t1) of `tiles` (t1 = 0: from all that
-// they see), 8 keys' scores at a time, then their values, which all lanes read together.  Writes the outputs,
-// or, part: the rows' place in a partial of R rows and D values.  It ends where every sum is NaN, which
-// nothing mends.  (Q8: the user's cache is Q8_0.)
+// they see), 8 keys' scores at a time, then their values, which all lanes read together.  The sums are held in this
+// lane's row of the CTA's partial (o: R rows, D values each, then maxima and sums), which is where a part's go
+// in the end; else the outputs are written.  It ends where every sum is NaN, which nothing mends.  (Q8: the
+// user's cache is Q8_0.)
 template <bool Q8>
 __device__ __noinline__ void rows_by_hand(const PrefillParams& p, int s, int h, int row0, uint32_t bits, Tiles tiles, int t0, int t1,
-                                          int BN, float* part, int R, int D) {
+                                          int BN, bool part, float* o, int R, int D) {
     const int lane = threadIdx.x & 31, dim = p.c.dim, shift = p.raw.page_shift, mask = (1 << shift) - 1;
     const int64_t scales = (int64_t)dim << shift;  // Q8_0: where a tile's scales begin
     const bool mine = (bits >> lane) & 1;
@@ -268,9 +269,8 @@ __device__ __noinline__ void rows_by_hand(const PrefillParams& p, int s, int h, 
         t0 = 0;
         t1 = tiles.count();
     }
-    float o[256];  // (in local memory: read and written once for 8 keys)
     float m = -INFINITY, l = 0.0f;
-    for (int e = 0; e < dim; e++) o[e] = 0.0f;
+    for (int e = 0; e < dim && mine; e++) o[(int64_t)e * R] = 0.0f;
     bool left = true;
     for (int64_t n = (int64_t)t0 * BN; n < (int64_t)t1 * BN && left; n += 8) {
         const int jb = tiles.at((int)(n / BN)) * BN + (int)(n % BN);
@@ -315,7 +315,7 @@ __device__ __noinline__ void rows_by_hand(const PrefillParams& p, int s, int h, 
         for (int e = 0; e < dim; e += 8) {
             float acc[8];
 #pragma unroll
-            for (int i = 0; i < 8; i++) acc[i] = o[e + i] * f;
+            for (int i = 0; i < 8; i++) acc[i] = o[(int64_t)(e + i) * R] * f;
 #pragma unroll
             for (int c = 0; c < 8; c++) {
                 float v[8];
@@ -324,17 +324,17 @@ __device__ __noinline__ void rows_by_hand(const PrefillParams& p, int s, int h, 
                 for (int i = 0; i < 8; i++) acc[i] = (seen >> c) & 1 ? fmaf(sc[c], v[i], acc[i]) : acc[i];
             }
 #pragma unroll
-            for (int i = 0; i < 8; i++) o[e + i] = acc[i];
+            for (int i = 0; i < 8; i++)
+                if (mine) o[(int64_t)(e + i) * R] = acc[i];
         }
     }
     if (!mine) return;
     if (part) {
-        for (int e = 0; e < dim; e++) __stcg(part + (int64_t)e * R, o[e]);
-        __stcg(part + (int64_t)D * R, m);
-        __stcg(part + (int64_t)(D + 1) * R, l);
+        o[(int64_t)D * R] = m;
+        o[(int64_t)(D + 1) * R] = l;
     } else {
         const int64_t out0 = (int64_t)tok * p.out_stride + (int64_t)head * dim;
-        for (int e = 0; e < dim; e++) store_out(p, out0 + e, l == 0.0f ? 0.0f : o[e] / l);
+        for (int e = 0; e < dim; e++) store_out(p, out0 + e, l == 0.0f ? 0.0f : o[(int64_t)e * R] / l);
     }
 }
 
@@ -778,21 +778,21 @@ __global__ void __launch_bounds__(PreShape<D, Q8>::THREADS, 1)
             }
         }
         __syncwarp();
-        auto by_hand = [&](int s, int h, int row0, uint32_t bits, const Tiles& tiles, int t0, int t1, float* part) {
-            if (Q8 || p.raw.q8) rows_by_hand<true>(p, s, h, row0, bits, tiles, t0, t1, BN, part, R, D);
-            else rows_by_hand<false>(p, s, h, row0, bits, tiles, t0, t1, BN, part, R, D);
+        auto by_hand = [&](int s, int h, int row0, uint32_t bits, const Tiles& tiles, int t0, int t1, bool part) {
+            float* o = p.part + (int64_t)blockIdx.x * R * (D + 2) + r;
+            if (Q8 || p.raw.q8) rows_by_hand<true>(p, s, h, row0, bits, tiles, t0, t1, BN, part, o, R, D);
+            else rows_by_hand<false>(p, s, h, row0, bits, tiles, t0, t1, BN, part, o, R, D);
         };
         while (redo_list >= 0) {
             const Redo x = p.redo[redo_list];
-            by_hand(x.s, x.h, x.row0, x.bits, Tiles{}, 0, 0, nullptr);
+            by_hand(x.s, x.h, x.row0, x.bits, Tiles{}, 0, 0, false);
             redo_list = x.next;
         }
         // ---- the last of a split item's CTAs joins the partials ------------------------------------
         if (split_slot >= 0) do {
             it = item_of(item_ints + 24 * split_slot);
             if (split_redo)
-                by_hand(it.s, it.h, it.row0 + 32 * warp, split_redo, it.tiles, it.t0, it.t0 + it.nt,
-                        p.part + (int64_t)blockIdx.x * R * (D + 2) + r);
+                by_hand(it.s, it.h, it.row0 + 32 * warp, split_redo, it.tiles, it.t0, it.t0 + it.nt, true);
             __threadfence();
             const bool together = softmax_sync();
             if (tid == 0) {  // (also where a wait gave up: the counters of the calls to come start from zero)

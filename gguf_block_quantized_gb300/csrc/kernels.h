@@ -99,7 +99,7 @@ int64_t decode_count_words(int64_t n_seq, int n_heads, int n_kv, int dim);
 int64_t decode_part_floats(int n_heads, int n_kv, int dim, int sms);
 
 // Several new tokens of each sequence (packed, starts[s] .. starts[s+1]).  part:
-// prefill_part_floats; count: at least `sms` + 2 words, as above.  split: items may be split
+// prefill_part_floats (partials, then the list of rows to be computed again); count: at least `sms` + 2 words, as above.  split: items may be split
 // between CTAs.
 cudaError_t launch_attn_prefill(const KvCache& c, const KvCache& raw, const AttnDesc& a, int64_t n_seq, int64_t n_tok,
                                 const void* q, const int32_t* starts, const int32_t* pages, const int32_t* raw_pages,

@@ -86,16 +86,13 @@ struct Workspace {
 std::mutex g_mu;
 std::map<int, DeviceState> g_dev;
 // A workspace belongs to a device and a stream.  The handle of the per-thread default stream names another
-// stream in every thread: its key is the id of the calling thread's.
+// stream in every thread: its key is a number of the calling thread's own (the stream's id, which would be
+// one too, cannot be asked for while it is captured).
 using StreamKey = std::pair<int, unsigned long long>;
-bool stream_key(int dev, cudaStream_t s, StreamKey* out) {
-    unsigned long long id = s == cudaStreamLegacy ? 0 : reinterpret_cast<uintptr_t>(s);
-    if (s == cudaStreamPerThread) {
-        if (cudaStreamGetId(s, &id) != cudaSuccess) return false;
-        id |= 1ull << 63;  // (no handle's bit)
-    }
-    *out = {dev, id};
-    return true;
+StreamKey stream_key(int dev, cudaStream_t s) {
+    static std::atomic<unsigned long long> threads{0};
+    static thread_local const unsigned long long mine = (1ull << 63) | threads++;  // (no handle has that bit)
+    return {dev, s == cudaStreamPerThread ? mine : s == cudaStreamLegacy ? 0ull : reinterpret_cast<uintptr_t>(s)};
 }
 std::map<StreamKey, Workspace> g_ws;
 // the attention's workspaces: counters (zero between calls), then partial results; and the expanded
@@ -189,10 +186,9 @@ size_t prefill_ws_bytes(int64_t n_in, int64_t n_tok) { return (size_t)(n_in * n_
 
 int workspace_for(cudaStream_t s, size_t need, void** out) {
     int dev;
-    StreamKey key;
-    if (current_device(&dev) != SYN_OK || !stream_key(dev, s, &key)) return SYN_ERR_CUDA;
+    if (current_device(&dev) != SYN_OK) return SYN_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
-    Workspace& w = g_ws[key];
+    Workspace& w = g_ws[stream_key(dev, s)];
     if (w.bytes < need) {
         if (w.ptr) {
             if (cudaDeviceSynchronize() != cudaSuccess) return SYN_ERR_CUDA;
@@ -218,10 +214,9 @@ void note_launches(int n) { g_launches += n; }
 
 int attn_workspace(cudaStream_t s, size_t zeroed, size_t rest, size_t* zeroed_at, void** out) try {
     int dev;
-    StreamKey key;
-    if (current_device(&dev) != SYN_OK || !stream_key(dev, s, &key)) return SYN_ERR_CUDA;
+    if (current_device(&dev) != SYN_OK) return SYN_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
-    AttnWorkspace& w = g_attn_ws[key];
+    AttnWorkspace& w = g_attn_ws[stream_key(dev, s)];
     if (w.zeroed < zeroed || w.rest < rest) {
         const size_t z = std::max(w.zeroed, zeroed), r = std::max(w.rest, rest);
         if (cudaDeviceSynchronize() != cudaSuccess) return SYN_ERR_CUDA;  // (refused while capturing)
@@ -249,10 +244,9 @@ int attn_workspace(cudaStream_t s, size_t zeroed, size_t rest, size_t* zeroed_at
 
 int attn_rows_workspace(cudaStream_t s, size_t bytes, void** out) try {
     int dev;
-    StreamKey key;
-    if (current_device(&dev) != SYN_OK || !stream_key(dev, s, &key)) return SYN_ERR_CUDA;
+    if (current_device(&dev) != SYN_OK) return SYN_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
-    AttnWorkspace& w = g_attn_ws[key];
+    AttnWorkspace& w = g_attn_ws[stream_key(dev, s)];
     if (w.row_bytes < bytes) {
         size_t n = size_t(1) << 20;  // powers of two: what is outgrown adds up to less than what is used
         while (n < bytes) n *= 2;

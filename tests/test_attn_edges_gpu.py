@@ -518,3 +518,23 @@ def test_decode_scales_of_every_size(syn, dim):
                                        np.zeros(1), 0, 0, dim ** -0.5, 0.0, None)
         assert (np.abs(got[i:i + 1] - ref) <= decode_bound(size, ref, False)).all(), i
     assert (got[1] == 0).all() and np.abs(got[3]).max() > 0
+
+
+def test_a_graph_captured_on_the_threads_own_stream(syn):
+    import torch
+    rng = np.random.default_rng(56)
+    cache, pages, _ = make_cache(syn, rng, F16, 2, 64, 16, [3000])
+    q, ld = on(rng.standard_normal((1, 8, 64)).astype(np.float16)), int32([3000])
+    want = syn.attn_decode(cache, q, pages, ld)
+    out = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    step = syn.prepare_attn_decode(cache, q, pages, ld, out, stream=2)  # cudaStreamPerThread
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.ExternalStream(2)):
+        step()
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)

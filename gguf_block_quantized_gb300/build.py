@@ -26,7 +26,7 @@ LIB = os.path.join(HERE, "libsyn.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["api.cu", "quant.cu", "gemv.cu", "gemv_f16.cu", "gemm.cu", "noalloc.cu", "kv_append.cu", "attn_decode.cu",
-           "attn_prefill.cu", "api_attn.cu", "gguf.cpp"]
+           "attn_prefill.cu", "kv_pages.cu", "logprobs.cu", "api_attn.cu", "gguf.cpp"]
 HEADERS = ["common.cuh", "quant_dev.cuh", "kv_cache.cuh", "tcgen05.cuh", "kernels.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -1,6 +1,6 @@
-// api_attn.cu — the C entry points of the paged key-value cache and its attention (declared in
-// include/syn.h): argument checks, workspaces, dispatch to kv_append.cu, attn_decode.cu and
-// attn_prefill.cu.
+// api_attn.cu — the C entry points of the paged key-value cache, its pages and its attention, and of the
+// log probabilities (declared in include/syn.h): argument checks, workspaces, dispatch to kv_append.cu,
+// kv_pages.cu, attn_decode.cu, attn_prefill.cu and logprobs.cu.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -278,6 +278,152 @@ int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_
                                              !syn::deterministic(), words, sms, &launches, s));
     syn::note_launches(launches);
     return rc;
+}
+
+int syn_kv_fork(const syn_kv_cache* cache, int32_t* refs, int64_t n_seq, const int32_t* pages, int64_t max_pages,
+                const int32_t* lens, int64_t n_new, const int32_t* from, int32_t* new_pages, int32_t* new_lens,
+                syn_stream_t stream) {
+    syn::KvCache c;
+    int rc = cache_of(cache, &c);
+    if (rc) return rc;
+    if (n_seq < 0 || n_seq > INT32_MAX || n_new < 0 || n_new > INT32_MAX || max_pages < (n_new > 0) || max_pages > INT32_MAX)
+        return SYN_ERR_SHAPE;
+    if (n_new == 0) return SYN_OK;
+    if (!refs || !from || !new_pages || !new_lens || (n_seq && (!pages || !lens))) return SYN_ERR_NULL;
+    if (!aligned(refs, 4) || !aligned(from, 4) || !aligned(new_pages, 4) || !aligned(new_lens, 4) || !aligned(pages, 4) ||
+        !aligned(lens, 4))
+        return SYN_ERR_ALIGN;
+    int sms, *words;
+    rc = syn::call_state(&sms, &words);
+    if (rc) return rc;
+    rc = check_cuda(syn::launch_kv_fork(c, refs, n_seq, pages, max_pages, lens, n_new, from, new_pages, new_lens, words, sms,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+    if (rc == SYN_OK) syn::note_launches(1);
+    return rc;
+}
+
+int syn_kv_extend(const syn_kv_cache* cache, int32_t* refs, int64_t n_seq, int64_t n_tok, int32_t* pages, int64_t max_pages,
+                  const int32_t* lens, const int32_t* starts, int32_t* new_lens, int64_t* slots, syn_stream_t stream) {
+    syn::KvCache c;
+    int rc = cache_of(cache, &c);
+    if (rc) return rc;
+    if (n_seq < 0 || n_seq > syn::KV_EXTEND_SEQS || n_tok < 0 || n_tok > INT32_MAX - 1024 || (!starts && n_tok != n_seq) ||
+        max_pages < (n_seq > 0) || max_pages > INT32_MAX)
+        return SYN_ERR_SHAPE;
+    if (n_seq == 0) return SYN_OK;
+    if (!refs || !pages || !lens || !new_lens) return SYN_ERR_NULL;
+    if (!aligned(refs, 4) || !aligned(pages, 4) || !aligned(lens, 4) || !aligned(starts, 4) || !aligned(new_lens, 4) ||
+        !aligned(slots, 8))
+        return SYN_ERR_ALIGN;
+    int sms, *words;
+    rc = syn::call_state(&sms, &words);
+    if (rc) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int* count;
+    float* scratch;
+    rc = scratch_for(s, 1, 4 * n_seq + 2 * syn::extend_items(c, n_seq, n_tok), &count, &scratch);
+    if (rc) return rc;
+    int launches = 0;
+    rc = check_cuda(syn::launch_kv_extend(c, refs, n_seq, n_tok, pages, max_pages, lens, starts, new_lens, slots, scratch, words,
+                                          sms, &launches, s));
+    syn::note_launches(launches);
+    return rc;
+}
+
+int syn_kv_compact(const syn_kv_cache* cache, const int32_t* refs, int64_t n_seq, int64_t n_rows, const int32_t* pages,
+                   int64_t max_pages, const int32_t* base, const int32_t* starts, const int32_t* rows, int32_t* new_lens,
+                   syn_stream_t stream) {
+    syn::KvCache c;
+    int rc = cache_of(cache, &c);
+    if (rc) return rc;
+    // (a CTA for each column of a tile: at most 17 of them)
+    if (n_seq < 0 || n_seq > INT32_MAX / (34 * (int64_t)c.n_kv) || n_rows < 0 || n_rows > INT32_MAX - 1024 ||
+        max_pages < (n_seq > 0) || max_pages > INT32_MAX)
+        return SYN_ERR_SHAPE;
+    if (n_seq == 0) return SYN_OK;
+    if (!pages || !base || !starts || !new_lens || (n_rows && !rows)) return SYN_ERR_NULL;
+    if (!aligned(refs, 4) || !aligned(pages, 4) || !aligned(base, 4) || !aligned(starts, 4) || !aligned(rows, 4) ||
+        !aligned(new_lens, 4))
+        return SYN_ERR_ALIGN;
+    int sms, *words;
+    rc = syn::call_state(&sms, &words);
+    if (rc) return rc;
+    rc = check_cuda(syn::launch_kv_compact(c, refs, n_seq, n_rows, pages, max_pages, base, starts, rows, new_lens, words, sms,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+    if (rc == SYN_OK) syn::note_launches(1);
+    return rc;
+}
+
+int syn_kv_trim(const syn_kv_cache* cache, int32_t* refs, int64_t n_seq, int32_t* pages, int64_t max_pages,
+                const int32_t* lens, syn_stream_t stream) {
+    syn::KvCache c;
+    int rc = cache_of(cache, &c);
+    if (rc) return rc;
+    if (n_seq < 0 || n_seq > INT32_MAX || max_pages < (n_seq > 0) || max_pages > INT32_MAX) return SYN_ERR_SHAPE;
+    if (n_seq == 0) return SYN_OK;
+    if (!refs || !pages || !lens) return SYN_ERR_NULL;
+    if (!aligned(refs, 4) || !aligned(pages, 4) || !aligned(lens, 4)) return SYN_ERR_ALIGN;
+    int sms, *words;
+    rc = syn::call_state(&sms, &words);
+    if (rc) return rc;
+    rc = check_cuda(syn::launch_kv_trim(c, refs, n_seq, pages, max_pages, lens, words, sms,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+    if (rc == SYN_OK) syn::note_launches(1);
+    return rc;
+}
+
+int syn_kv_copy(const syn_kv_cache* from, const syn_kv_cache* to, int64_t n, const int32_t* src, const int32_t* dst,
+                syn_stream_t stream) {
+    syn::KvCache a, b;
+    int rc = cache_of(from, &a);
+    if (rc == SYN_OK) rc = cache_of(to, &b);
+    if (rc) return rc;
+    if (a.q8 != b.q8) return SYN_ERR_TYPE;
+    if (a.dim != b.dim || a.n_kv != b.n_kv || a.page_shift != b.page_shift || n < 0 || n > INT32_MAX) return SYN_ERR_SHAPE;
+    if (n == 0) return SYN_OK;
+    if (!src || !dst) return SYN_ERR_NULL;
+    if (!aligned(src, 4) || !aligned(dst, 4)) return SYN_ERR_ALIGN;
+    int sms, *words;
+    rc = syn::call_state(&sms, &words);
+    if (rc) return rc;
+    rc = check_cuda(syn::launch_kv_copy(a, b, n, src, dst, words, sms, reinterpret_cast<cudaStream_t>(stream)));
+    if (rc == SYN_OK) syn::note_launches(1);
+    return rc;
+}
+
+int syn_logprobs(const syn_logits* opt, int64_t n_rows, int64_t n_vocab, const void* logits, int64_t n_ids, const int32_t* ids,
+                 float* logprob, float* entropy, int64_t n_top, int32_t* top, float* top_logprob, syn_stream_t stream) {
+    if (!opt) return SYN_ERR_NULL;
+    if (opt->type != SYN_OUT_F32 && opt->type != SYN_OUT_F16) return SYN_ERR_TYPE;
+    const int64_t words_of = (n_vocab + 31) / 32;
+    const int64_t stride = opt->stride ? opt->stride : n_vocab, mask_stride = opt->mask_stride ? opt->mask_stride : words_of;
+    if (n_rows < 0 || n_rows > INT32_MAX / 8 || n_vocab < 1 || n_vocab > (1 << 30) || stride < n_vocab || mask_stride < words_of ||
+        n_ids < 0 || n_ids > 65536 || n_top < 0 || n_top > syn::LOGPROBS_TOP || !std::isfinite(opt->scale) ||
+        !(opt->scale > 0.0f) || !std::isfinite(opt->cap) || opt->cap < 0.0f)
+        return SYN_ERR_SHAPE;
+    if (n_rows == 0) return SYN_OK;
+    if (stride > kMaxElems / n_rows || mask_stride > kMaxElems / n_rows) return SYN_ERR_SHAPE;
+    if (!logits || (n_ids && (!ids || !logprob)) || (n_top && (!top || !top_logprob))) return SYN_ERR_NULL;
+    const bool f16 = opt->type == SYN_OUT_F16;
+    if (!aligned(logits, f16 ? 2 : 4) || !aligned(opt->scales, 4) || !aligned(opt->mask, 4) || !aligned(ids, 4) ||
+        !aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(top, 4) || !aligned(top_logprob, 4))
+        return SYN_ERR_ALIGN;
+    int sms, *words;
+    const int rc = syn::call_state(&sms, &words);
+    if (rc) return rc;
+    syn::LogitsDesc d;
+    d.stride = stride;
+    d.scales = opt->scales;
+    d.mask = opt->mask;
+    d.mask_stride = mask_stride;
+    d.f16 = f16;
+    d.scale = opt->scale;
+    d.cap = opt->cap;
+    const int e = check_cuda(syn::launch_logprobs(d, n_rows, (int)n_vocab, logits, ids, (int)n_ids, logprob, entropy, (int)n_top,
+                                                  top, top_logprob, syn::deterministic(), words, sms,
+                                                  reinterpret_cast<cudaStream_t>(stream)));
+    if (e == SYN_OK) syn::note_launches(1);
+    return e;
 }
 
 }  // extern "C"

@@ -112,6 +112,43 @@ int64_t prefill_part_floats(int64_t n_seq, int64_t n_tok, int n_heads, int n_kv,
 cudaError_t launch_kv_expand(const KvCache& c, int64_t n_seq, int64_t n_tok, const int32_t* starts, const int32_t* pages, int64_t max_pages,
                              const int32_t* lens, int window, void* k, void* v, int32_t* table, int sms, cudaStream_t s);
 
+// ---- the pages of a cache as sequences hold them (kv_pages.cu) -----------------------------
+
+constexpr int KV_EXTEND_SEQS = 4096;  // sequences of an extend call (their items are counted in shared memory)
+
+cudaError_t launch_kv_fork(const KvCache& c, int32_t* refs, int64_t n_seq, const int32_t* pages, int64_t max_pages,
+                           const int32_t* lens, int64_t n_new, const int32_t* from, int32_t* new_pages, int32_t* new_lens,
+                           int* err, int sms, cudaStream_t s);
+cudaError_t launch_kv_trim(const KvCache& c, int32_t* refs, int64_t n_seq, int32_t* pages, int64_t max_pages,
+                           const int32_t* lens, int* err, int sms, cudaStream_t s);
+// scratch: 16 bytes a sequence, then 8 an item (extend_items), 16-byte aligned.
+cudaError_t launch_kv_extend(const KvCache& c, int32_t* refs, int64_t n_seq, int64_t n_tok, int32_t* pages, int64_t max_pages,
+                             const int32_t* lens, const int32_t* starts, int32_t* new_lens, int64_t* slots, void* scratch,
+                             int* err, int sms, int* launches, cudaStream_t s);
+int64_t extend_items(const KvCache& c, int64_t n_seq, int64_t n_tok);
+cudaError_t launch_kv_compact(const KvCache& c, const int32_t* refs, int64_t n_seq, int64_t n_rows, const int32_t* pages,
+                              int64_t max_pages, const int32_t* base, const int32_t* starts, const int32_t* rows,
+                              int32_t* new_lens, int* err, int sms, cudaStream_t s);
+cudaError_t launch_kv_copy(const KvCache& from, const KvCache& to, int64_t n, const int32_t* src, const int32_t* dst, int* err,
+                           int sms, cudaStream_t s);
+
+// ---- log probabilities (logprobs.cu) -------------------------------------------------------
+
+constexpr int LOGPROBS_TOP = 64;  // most alternatives
+
+struct LogitsDesc {
+    int64_t stride;        // values between rows
+    const float* scales;   // per row, or NULL
+    const uint32_t* mask;  // a bit a token, or NULL
+    int64_t mask_stride;   // words between rows
+    int f16;
+    float scale, cap;
+};
+// whole: a row's results do not depend on how many rows the call has.
+cudaError_t launch_logprobs(const LogitsDesc& d, int64_t n_rows, int n_vocab, const void* x, const int32_t* ids, int n_ids,
+                            float* logprob, float* entropy, int n_top, int32_t* top, float* top_logprob, bool whole,
+                            int* err, int sms, cudaStream_t s);
+
 // What the C entry points of api_attn.cu share with api.cu: the SMs of this call and the
 // status words ([0]) of the current device; the attention's workspace of (device, stream), at
 // least `zeroed` bytes that were zero when it was allocated, then (from byte *zeroed_at on) at
@@ -185,6 +222,7 @@ int debug_bounds_gemm(int clear);
 int debug_bounds_kv_append(int clear);
 int debug_bounds_attn_decode(int clear);
 int debug_bounds_attn_prefill(int clear);
+int debug_bounds_kv_pages(int clear);
 cudaError_t launch_bounds_selftest(cudaStream_t s);
 #endif
 

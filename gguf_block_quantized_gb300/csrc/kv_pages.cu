@@ -1,0 +1,566 @@
+// kv_pages.cu — the pages of a paged cache as sequences hold them: forked, extended, packed, given back
+// and copied.
+//
+// refs[page] counts the page-table entries that hold the page; 0: free.  Pages are taken lowest first,
+// in the order of sequences and columns, so that what a call does depends on its arguments alone,
+// whatever the order of the atomics.
+//
+// Bound: the tables are a few KB, so fork, extend and trim are their launches' latency; rows and pages
+// move at HBM's rate, read and written once.
+#include <algorithm>
+#include <climits>
+
+#include "kernels.h"
+#include "kv_cache.cuh"
+
+namespace syn {
+
+constexpr int PG_THREADS = 256;
+
+// ---- fork and trim: a thread per table entry --------------------------------------------
+
+struct ForkParams {
+    int32_t* refs;
+    const int32_t* from;
+    const int32_t* pages;
+    const int32_t* lens;
+    int32_t* new_pages;
+    int32_t* new_lens;
+    int* err;
+    int64_t n_seq, n_new, max_pages, n_pages;
+    int page_shift;
+};
+
+__global__ void __launch_bounds__(PG_THREADS) k_kv_fork(const ForkParams p) {
+    griddep_release();
+    griddep_wait();
+    const int64_t total = p.n_new * p.max_pages, step = (int64_t)gridDim.x * PG_THREADS;
+    for (int64_t u = (int64_t)blockIdx.x * PG_THREADS + threadIdx.x; u < total; u += step) {
+        const int64_t i = u / p.max_pages, j = u - i * p.max_pages;
+        const int s = p.from[i];
+        if (s >= p.n_seq && j == 0) record_error(p.err, SYN_DEVERR_BOUNDS);
+        const int len = s >= 0 && s < p.n_seq ? held_rows(p.lens[s], p.max_pages, p.page_shift) : 0;
+        int id = -1;
+        if (j < ((int64_t)len + (1 << p.page_shift) - 1) >> p.page_shift) {
+            id = p.pages[s * p.max_pages + j];
+            if ((unsigned)id < (unsigned)p.n_pages) {
+                atomicAdd(p.refs + id, 1);
+            } else {
+                record_error(p.err, SYN_DEVERR_BOUNDS);
+                id = -1;
+            }
+        }
+        p.new_pages[u] = id;
+        if (j == 0) p.new_lens[i] = len;
+    }
+}
+
+struct TrimParams {
+    int32_t* refs;
+    int32_t* pages;
+    const int32_t* lens;
+    int* err;
+    int64_t n_seq, max_pages, n_pages;
+    int page_shift;
+};
+
+__global__ void __launch_bounds__(PG_THREADS) k_kv_trim(const TrimParams p) {
+    griddep_release();
+    griddep_wait();
+    const int64_t total = p.n_seq * p.max_pages, step = (int64_t)gridDim.x * PG_THREADS;
+    for (int64_t u = (int64_t)blockIdx.x * PG_THREADS + threadIdx.x; u < total; u += step) {
+        const int64_t s = u / p.max_pages, j = u - s * p.max_pages;
+        if (j < ((int64_t)max(p.lens[s], 0) + (1 << p.page_shift) - 1) >> p.page_shift) continue;
+        const int id = p.pages[u];
+        if (id < 0) continue;
+        p.pages[u] = -1;
+        if (id >= p.n_pages) {
+            record_error(p.err, SYN_DEVERR_BOUNDS);
+        } else if (atomicSub(p.refs + id, 1) <= 0) {  // (given back before)
+            atomicAdd(p.refs + id, 1);
+            record_error(p.err, SYN_DEVERR_BOUNDS);
+        }
+    }
+}
+
+static int table_grid(int64_t entries, int sms) {
+    return (int)std::min<int64_t>((entries + PG_THREADS - 1) / PG_THREADS, (int64_t)sms * 8);
+}
+
+cudaError_t launch_kv_fork(const KvCache& c, int32_t* refs, int64_t n_seq, const int32_t* pages, int64_t max_pages,
+                           const int32_t* lens, int64_t n_new, const int32_t* from, int32_t* new_pages, int32_t* new_lens,
+                           int* err, int sms, cudaStream_t s) {
+    const ForkParams p{refs, from, pages, lens, new_pages, new_lens, err, n_seq, n_new, max_pages, c.n_pages, c.page_shift};
+    return launch_overlapped(k_kv_fork, table_grid(n_new * max_pages, sms), PG_THREADS, 0, s, p);
+}
+
+cudaError_t launch_kv_trim(const KvCache& c, int32_t* refs, int64_t n_seq, int32_t* pages, int64_t max_pages,
+                           const int32_t* lens, int* err, int sms, cudaStream_t s) {
+    const TrimParams p{refs, pages, lens, err, n_seq, max_pages, c.n_pages, c.page_shift};
+    return launch_overlapped(k_kv_trim, table_grid(n_seq * max_pages, sms), PG_THREADS, 0, s, p);
+}
+
+// ---- extend ------------------------------------------------------------------------------
+//
+// The columns a sequence's new rows fall into are items, counted through over the sequences.  An item
+// whose entry is empty (missing), or whose page others hold too (shared), needs a page.  One CTA plans:
+//   1. each shared item takes its entry off its page's count; where a count comes to 0 every holder
+//      writes, and the last of them (by a minimum over negative numbers) keeps the page;
+//   2. the free pages are listed, lowest first, as many as are needed;
+//   3. where they suffice the items take them in order; where they do not, nobody keeps a shared page, and
+//      the sequences whose needs, summed up to them, fit, take theirs.
+// The second kernel gives out the slots and copies the rows of first pages that were shared.
+
+constexpr int EXT_THREADS = 1024;
+
+struct ExtendParams {
+    KvCache c;
+    int32_t* refs;
+    int32_t* pages;
+    const int32_t* lens;
+    int32_t* new_lens;
+    const int32_t* starts;  // NULL: one row each
+    int64_t* slots;
+    int4* plan;      // per sequence: page copied from (-1: none), copied to, length, whether it was extended
+    int32_t* need;   // [items] 0: a page of its own, 1: missing, 2: shared; then, where pages are short, sums
+    int32_t* free_list;  // [items]
+    int* err;
+    int64_t max_pages, n_tok, max_items;
+    int n_seq;
+};
+
+// (rows that run backwards or past the call's tokens count as none)
+__device__ __forceinline__ int new_rows(const ExtendParams& p, int s) {
+    if (!p.starts) return 1;
+    const int a = p.starts[s], b = p.starts[s + 1];
+    return a < 0 || b > p.n_tok ? 0 : max(b - a, 0);
+}
+
+// The inclusive sum over the CTA's threads, and their total.
+__device__ __forceinline__ int block_sum(int x, int* sums, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // (the sums before this one have been read)
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    int w = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+    }
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    return x + (warp > 0 ? before : 0);
+}
+
+__global__ void __launch_bounds__(EXT_THREADS) k_kv_extend_plan(const ExtendParams p) {
+    __shared__ int off[KV_EXTEND_SEQS + 1];  // items before each sequence
+    __shared__ int sums[32];
+    const int tid = threadIdx.x, shift = p.c.page_shift, page = 1 << shift;
+    griddep_release();
+    griddep_wait();
+    // ---- the items ---------------------------------------------------------------------------
+    int items = 0;
+    if (tid == 0) off[0] = 0;
+    for (int s0 = 0; s0 < p.n_seq; s0 += EXT_THREADS) {
+        const int s = s0 + tid;
+        int columns = 0;
+        if (s < p.n_seq) {
+            const int len = held_rows(p.lens[s], p.max_pages, shift), n = new_rows(p, s);
+            const int64_t end = ((int64_t)len + n + page - 1) >> shift;
+            const bool fits = end <= p.max_pages && (int64_t)len + n <= INT_MAX - 1024;
+            if (fits && n > 0) columns = (int)(end - (len >> shift));
+            p.plan[s] = make_int4(-1, -1, len, fits);
+        }
+        int total;
+        const int sum = block_sum(columns, sums, total);
+        if (s < p.n_seq) off[s + 1] = items + sum;
+        items += total;
+    }
+    __syncthreads();
+    // (starts that overlap could name more rows than the call has)
+    if (items > p.max_items) {
+        if (tid == 0) record_error(p.err, SYN_DEVERR_BOUNDS);
+        for (int s = tid; s < p.n_seq; s += EXT_THREADS) {
+            p.new_lens[s] = p.plan[s].z;
+            p.plan[s].w = 0;
+        }
+        return;
+    }
+    auto sequence_of = [&](int u) {
+        int lo = 0, hi = p.n_seq - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (off[mid + 1] > u) hi = mid;
+            else lo = mid + 1;
+        }
+        return lo;
+    };
+    auto entry_of = [&](int u, int s) { return (int64_t)s * p.max_pages + (p.plan[s].z >> shift) + (u - off[s]); };
+    volatile int32_t* refs = p.refs;
+    // ---- missing and shared ------------------------------------------------------------------
+    int any_shared = 0;
+    for (int u = tid; u < items; u += EXT_THREADS) {
+        const int id = p.pages[entry_of(u, sequence_of(u))];
+        int what = 1;
+        if ((unsigned)id < (unsigned)p.c.n_pages) {
+            what = refs[id] > 1 ? 2 : 0;
+        } else if (id >= 0) {
+            record_error(p.err, SYN_DEVERR_BOUNDS);
+        }
+        any_shared |= what == 2;
+        p.need[u] = what;
+    }
+    any_shared = __syncthreads_or(any_shared);
+    if (any_shared) {
+        for (int u = tid; u < items; u += EXT_THREADS)
+            if (p.need[u] == 2) atomicSub(p.refs + p.pages[entry_of(u, sequence_of(u))], 1);
+        __syncthreads();
+        for (int u = tid; u < items; u += EXT_THREADS)
+            if (p.need[u] == 2) {
+                const int id = p.pages[entry_of(u, sequence_of(u))];
+                if (refs[id] <= 0) atomicMin(p.refs + id, -1 - u);
+            }
+        __syncthreads();
+    }
+    auto keeps = [&](int u, int id) { return refs[id] == -1 - u; };
+    // ---- the free pages ----------------------------------------------------------------------
+    int wanted = 0;
+    for (int u0 = 0; u0 < items; u0 += EXT_THREADS) {
+        const int u = u0 + tid, what = u < items ? p.need[u] : 0;
+        const bool want = what == 1 || (what == 2 && !keeps(u, p.pages[entry_of(u, sequence_of(u))]));
+        wanted += __syncthreads_count(want);
+    }
+    int n_free = 0;
+    constexpr int EACH = 8;  // counts a thread looks at, in a row
+    for (int64_t b = 0; b < p.c.n_pages && n_free < wanted; b += EXT_THREADS * EACH) {
+        const int64_t at = b + (int64_t)tid * EACH;
+        int bits = 0;
+#pragma unroll
+        for (int i = 0; i < EACH; i++)
+            if (at + i < p.c.n_pages && refs[at + i] == 0) bits |= 1 << i;
+        int total;
+        int rank = n_free + block_sum(__popc(bits), sums, total) - __popc(bits);
+        n_free += total;
+        for (; bits; bits &= bits - 1, rank++)
+            if (rank < p.max_items) p.free_list[rank] = (int)at + __ffs(bits) - 1;
+    }
+    __syncthreads();
+    const bool enough = n_free >= wanted;
+    if (!enough) {
+        // ---- pages are short: who is served, and the counts as they were for the others -------------
+        int base = 0;
+        for (int u0 = 0; u0 < items; u0 += EXT_THREADS) {
+            const int u = u0 + tid;
+            int total;
+            const int what = u < items ? p.need[u] : 0, sum = base + block_sum(what != 0, sums, total);
+            if (what == 2) {
+                const int id = p.pages[entry_of(u, sequence_of(u))];
+                if (keeps(u, id)) refs[id] = 0;
+            }
+            if (u < items) p.need[u] = sum << 2 | what;
+            base += total;
+        }
+        __syncthreads();
+        for (int s = tid; s < p.n_seq; s += EXT_THREADS) {
+            const int before = off[s] ? p.need[off[s] - 1] >> 2 : 0, upto = off[s + 1] ? p.need[off[s + 1] - 1] >> 2 : 0;
+            if (p.plan[s].w) p.plan[s].w = upto == before || upto <= n_free;
+        }
+        __syncthreads();
+        for (int u = tid; u < items; u += EXT_THREADS) {
+            const int s = sequence_of(u);
+            if ((p.need[u] & 3) == 2 && !p.plan[s].w) atomicAdd(p.refs + p.pages[entry_of(u, s)], 1);
+        }
+        __syncthreads();
+    }
+    // ---- the pages dealt out -----------------------------------------------------------------
+    int given = 0;
+    for (int u0 = 0; u0 < items; u0 += EXT_THREADS) {
+        const int u = u0 + tid, s = u < items ? sequence_of(u) : 0;
+        const int what = u < items && p.plan[s].w ? p.need[u] & 3 : 0;
+        const int64_t entry = u < items ? entry_of(u, s) : 0;
+        const int id = what ? p.pages[entry] : -1;
+        const bool kept = enough && what == 2 && keeps(u, id), take = what && !kept;
+        int total;
+        const int rank = given + block_sum(take, sums, total) - 1;
+        given += total;
+        if (kept) refs[id] = 1;
+        if (take) {
+            const int got = p.free_list[rank];
+            refs[got] = 1;
+            p.pages[entry] = got;
+            if (what == 2 && u == off[s]) {
+                p.plan[s].x = id;
+                p.plan[s].y = got;
+            }
+        }
+    }
+    __syncthreads();
+    for (int s = tid; s < p.n_seq; s += EXT_THREADS) {
+        const int4 a = p.plan[s];
+        p.new_lens[s] = a.z + (a.w ? new_rows(p, s) : 0);
+    }
+}
+
+__global__ void __launch_bounds__(PG_THREADS) k_kv_extend_rows(const ExtendParams p) {
+    const int shift = p.c.page_shift, page = 1 << shift, tid = threadIdx.x;
+    griddep_release();
+    griddep_wait();
+    if (p.slots)
+        for (int64_t t = (int64_t)blockIdx.x * PG_THREADS + tid; t < p.n_tok; t += (int64_t)gridDim.x * PG_THREADS) {
+            int lo = 0, hi = p.n_seq;  // the last sequence that starts at t or before it
+            if (p.starts) {
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (p.starts[mid] <= t) lo = mid;
+                    else hi = mid;
+                }
+            } else {
+                lo = (int)t;
+            }
+            const int64_t at = p.starts ? t - p.starts[lo] : 0;
+            const int4 a = p.plan[lo];
+            int64_t slot = -1;
+            if (a.w && at >= 0 && at < new_rows(p, lo)) {
+                const int row = a.z + (int)at;
+                slot = ((int64_t)p.pages[lo * p.max_pages + (row >> shift)] << shift) + (row & (page - 1));
+            }
+            p.slots[t] = slot;
+        }
+    // the rows of a tile (one kv head, keys or values) that move with their sequence
+    const int tiles = 2 * p.c.n_kv, n16 = p.c.dim >> (p.c.q8 ? 4 : 3);  // 16-byte pieces of a row
+    for (int64_t x = blockIdx.x; x < (int64_t)p.n_seq * tiles; x += gridDim.x) {
+        const int s = (int)(x / tiles), h = (int)(x - (int64_t)s * tiles) >> 1;
+        const int4 a = p.plan[s];
+        if (a.x < 0) continue;
+        uint8_t* pool = x & 1 ? p.c.v : p.c.k;
+        const uint8_t* src = pool + a.x * p.c.page_stride + h * p.c.tile;
+        uint8_t* dst = pool + a.y * p.c.page_stride + h * p.c.tile;
+        const int rows = a.z & (page - 1);
+        for (int i = tid; i < rows * n16; i += PG_THREADS)
+            reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i];
+        if (p.c.q8) {
+            const int64_t scales = (int64_t)p.c.dim << shift;
+            for (int i = tid; i < rows * (p.c.dim >> 5); i += PG_THREADS)
+                reinterpret_cast<uint16_t*>(dst + scales)[i] = reinterpret_cast<const uint16_t*>(src + scales)[i];
+        }
+    }
+}
+
+int64_t extend_items(const KvCache& c, int64_t n_seq, int64_t n_tok) { return (n_tok >> c.page_shift) + 2 * n_seq; }
+
+cudaError_t launch_kv_extend(const KvCache& c, int32_t* refs, int64_t n_seq, int64_t n_tok, int32_t* pages, int64_t max_pages,
+                             const int32_t* lens, const int32_t* starts, int32_t* new_lens, int64_t* slots, void* scratch,
+                             int* err, int sms, int* launches, cudaStream_t s) {
+    ExtendParams p;
+    p.c = c;
+    p.refs = refs;
+    p.pages = pages;
+    p.lens = lens;
+    p.new_lens = new_lens;
+    p.starts = starts;
+    p.slots = slots;
+    p.max_items = extend_items(c, n_seq, n_tok);
+    p.plan = static_cast<int4*>(scratch);
+    p.need = reinterpret_cast<int32_t*>(p.plan + n_seq);
+    p.free_list = p.need + p.max_items;
+    p.err = err;
+    p.max_pages = max_pages;
+    p.n_tok = n_tok;
+    p.n_seq = (int)n_seq;
+    cudaError_t e = launch_overlapped(k_kv_extend_plan, 1, EXT_THREADS, 0, s, p);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    const int64_t work = std::max<int64_t>((slots ? n_tok + PG_THREADS - 1 : 0) / PG_THREADS, n_seq * 2 * c.n_kv);
+    e = launch_overlapped(k_kv_extend_rows, (int)std::min<int64_t>(work, (int64_t)sms * 8), PG_THREADS, 0, s, p);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
+// ---- compact -----------------------------------------------------------------------------
+//
+// Rows move down in place: row base + i comes from base + rows[i] >= base + i.  A CTA has a sequence's tile
+// column (a kv head, keys or values, some 16-byte pieces of each row) to itself and goes through
+// the rows in order, a batch loaded whole before any of it is stored: what a batch overwrites are rows
+// that it or a batch before has loaded, so no CTA waits for another.
+
+constexpr int CMP_THREADS = 256;
+constexpr int CMP_ROWS = 512;   // rows of a batch
+constexpr int CMP_UNITS = 8;    // pieces a thread holds
+
+struct CompactParams {
+    KvCache c;
+    const int32_t* refs;
+    const int32_t* pages;
+    const int32_t* base;
+    const int32_t* starts;
+    const int32_t* rows;
+    int32_t* new_lens;
+    int* err;
+    int64_t max_pages, n_rows;
+    int n_seq, cut, width;  // columns a tile is cut into (Q8_0: and one of scales), 16-byte pieces of one
+};
+
+template <typename U>
+__device__ __forceinline__ void move_rows(const CompactParams& p, uint8_t* tiles, int64_t plane, int pitch, int first, int width,
+                                          const int64_t* src, const int64_t* dst, int n) {
+    const int units = n * width;
+    U held[CMP_UNITS];
+    for (int u0 = 0; u0 < units; u0 += CMP_THREADS * CMP_UNITS) {
+#pragma unroll
+        for (int i = 0; i < CMP_UNITS; i++) {
+            const int u = u0 + i * CMP_THREADS + threadIdx.x, r = u / width, x = first + u - r * width;
+            if (u < units && src[r] >= 0) {
+                const int64_t cell = src[r] & ((int64_t(1) << p.c.page_shift) - 1);
+                held[i] = reinterpret_cast<const U*>(tiles + (src[r] >> p.c.page_shift) * p.c.page_stride + plane + cell * pitch)[x];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < CMP_UNITS; i++) {
+            const int u = u0 + i * CMP_THREADS + threadIdx.x, r = u / width, x = first + u - r * width;
+            if (u < units && src[r] >= 0) {
+                const int64_t cell = dst[r] & ((int64_t(1) << p.c.page_shift) - 1);
+                reinterpret_cast<U*>(tiles + (dst[r] >> p.c.page_shift) * p.c.page_stride + plane + cell * pitch)[x] = held[i];
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(CMP_THREADS) k_kv_compact(const CompactParams p) {
+    __shared__ int64_t src[CMP_ROWS], dst[CMP_ROWS];  // slots; -1: the row stays
+    const int tid = threadIdx.x, shift = p.c.page_shift, per = p.cut + p.c.q8;
+    griddep_release();
+    griddep_wait();
+    for (int unit = blockIdx.x; unit < p.n_seq * per * 2 * p.c.n_kv; unit += gridDim.x) {
+        const int column = unit % per, tile = unit / per % (2 * p.c.n_kv), s = unit / (per * 2 * p.c.n_kv);
+        const int a = p.starts[s], b = p.starts[s + 1], n = a < 0 || b > p.n_rows ? 0 : max(b - a, 0);
+        const int base = max(p.base[s], 0);
+        const bool tells = column == 0 && tile == 0;
+        if (tells && tid == 0) p.new_lens[s] = (int)min((int64_t)base + n, (int64_t)INT_MAX);
+        uint8_t* tiles = (tile & 1 ? p.c.v : p.c.k) + (tile >> 1) * p.c.tile;
+        const int32_t* table = p.pages + (int64_t)s * p.max_pages;
+        const int64_t held = min(p.max_pages << shift, (int64_t)INT_MAX);
+        auto slot_of = [&](int64_t row) -> int64_t {
+            if (row >= held) return -1;
+            const int id = table[row >> shift];
+            return (unsigned)id < (unsigned)p.c.n_pages ? ((int64_t)id << shift) + (row & ((1 << shift) - 1)) : -1;
+        };
+        for (int i0 = 0; i0 < n; i0 += CMP_ROWS) {
+            const int m = min(n - i0, CMP_ROWS);
+            __syncthreads();  // (the batch before is stored)
+            for (int i = tid; i < m; i += CMP_THREADS) {
+                const int row = p.rows[a + i0 + i];
+                int64_t from = -1, to = -1;
+                if (row != i0 + i) {
+                    // (a row that would come from before its place, or not after the one before, may be gone already)
+                    const bool ok = row > i0 + i && (i0 + i == 0 || p.rows[a + i0 + i - 1] < row);
+                    if (ok) {
+                        from = slot_of((int64_t)base + row);
+                        to = slot_of((int64_t)base + i0 + i);
+                    }
+                    // (a page that others hold too is not written to)
+                    if (to >= 0 && p.refs && p.refs[to >> shift] > 1) to = -1;
+                    if (from < 0 || to < 0) {
+                        from = -1;
+                        if (tells) record_error(p.err, SYN_DEVERR_BOUNDS);
+                    }
+                }
+                src[i] = from;
+                dst[i] = to;
+            }
+            __syncthreads();
+            if (column < p.cut) {
+                const int pieces = p.c.dim >> (p.c.q8 ? 4 : 3), first = column * p.width;
+                move_rows<uint4>(p, tiles, 0, pieces * 16, first, min(p.width, pieces - first), src, dst, m);
+            } else {
+                move_rows<uint16_t>(p, tiles, (int64_t)p.c.dim << shift, p.c.dim >> 4, 0, p.c.dim >> 5, src, dst, m);
+            }
+        }
+    }
+}
+
+cudaError_t launch_kv_compact(const KvCache& c, const int32_t* refs, int64_t n_seq, int64_t n_rows, const int32_t* pages,
+                              int64_t max_pages, const int32_t* base, const int32_t* starts, const int32_t* rows,
+                              int32_t* new_lens, int* err, int sms, cudaStream_t s) {
+    CompactParams p;
+    p.c = c;
+    p.refs = refs;
+    p.pages = pages;
+    p.base = base;
+    p.starts = starts;
+    p.rows = rows;
+    p.new_lens = new_lens;
+    p.err = err;
+    p.max_pages = max_pages;
+    p.n_rows = n_rows;
+    p.n_seq = (int)n_seq;
+    // columns of at least 32 bytes of a row (a sector), as many as it takes to fill the SMs
+    const int pieces = c.dim >> (c.q8 ? 4 : 3);
+    int width = pieces;
+    while (width > 2 && n_seq * 2 * c.n_kv * ((pieces + width - 1) / width) < 4 * (int64_t)sms) width = (width + 1) / 2;
+    p.width = width;
+    p.cut = (pieces + width - 1) / width;
+    return launch_overlapped(k_kv_compact, (int)std::min<int64_t>(n_seq * 2 * c.n_kv * (p.cut + c.q8), (int64_t)sms * 8),
+                             CMP_THREADS, 0, s, p);
+}
+
+// ---- copy --------------------------------------------------------------------------------
+//
+// Whole pages, 16 KB a turn of a CTA, eight 16-byte loads of a thread on their way together.
+
+struct CopyParams {
+    KvCache from, to;
+    const int32_t* src;
+    const int32_t* dst;
+    int* err;
+    int64_t n, bytes;  // bytes of a page in one pool
+};
+
+constexpr int COPY_UNITS = 8;
+
+__global__ void __launch_bounds__(PG_THREADS) k_kv_copy(const CopyParams p) {
+    griddep_release();
+    griddep_wait();
+    constexpr int64_t CHUNK = (int64_t)PG_THREADS * COPY_UNITS * 16;
+    const int64_t chunks = (p.bytes + CHUNK - 1) / CHUNK, total = 2 * p.n * chunks;
+    for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
+        const int64_t i = u / (2 * chunks), at = u - i * 2 * chunks, is_v = at >= chunks, off = (at - is_v * chunks) * CHUNK;
+        const int from = p.src[i], to = p.dst[i];
+        if ((unsigned)from >= (unsigned)p.from.n_pages || (unsigned)to >= (unsigned)p.to.n_pages) {
+            if (at == 0 && threadIdx.x == 0) record_error(p.err, SYN_DEVERR_BOUNDS);
+            continue;
+        }
+        const uint8_t* a = (is_v ? p.from.v : p.from.k) + from * p.from.page_stride;
+        uint8_t* b = (is_v ? p.to.v : p.to.k) + to * p.to.page_stride;
+        uint4 held[COPY_UNITS];
+#pragma unroll
+        for (int x = 0; x < COPY_UNITS; x++) {
+            const int64_t o = off + (x * PG_THREADS + threadIdx.x) * 16;
+            if (o < p.bytes) held[x] = *reinterpret_cast<const uint4*>(a + o);
+        }
+#pragma unroll
+        for (int x = 0; x < COPY_UNITS; x++) {
+            const int64_t o = off + (x * PG_THREADS + threadIdx.x) * 16;
+            if (o < p.bytes) *reinterpret_cast<uint4*>(b + o) = held[x];
+        }
+    }
+}
+
+cudaError_t launch_kv_copy(const KvCache& from, const KvCache& to, int64_t n, const int32_t* src, const int32_t* dst, int* err,
+                           int sms, cudaStream_t s) {
+    const CopyParams p{from, to, src, dst, err, n, from.tile * from.n_kv};
+    const int64_t chunk = (int64_t)PG_THREADS * COPY_UNITS * 16, total = 2 * n * ((p.bytes + chunk - 1) / chunk);
+    return launch_overlapped(k_kv_copy, (int)std::min<int64_t>(total, (int64_t)sms * 16), PG_THREADS, 0, s, p);
+}
+
+#ifdef SYN_DEBUG
+SYN_BOUNDS_READER(debug_bounds_kv_pages)
+#endif
+
+}  // namespace syn

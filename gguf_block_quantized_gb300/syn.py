@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import typing
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsyn.so")
@@ -119,6 +120,12 @@ class RopeDesc(ctypes.Structure):
                 ("axis", _vp)]
 
 
+class LogitsDesc(ctypes.Structure):
+    """syn_logits."""
+    _fields_ = [("type", _i32), ("scale", ctypes.c_float), ("cap", ctypes.c_float), ("scales", _vp), ("mask", _vp),
+                ("stride", _i64), ("mask_stride", _i64)]
+
+
 class AttnDesc(ctypes.Structure):
     """syn_attn."""
     _fields_ = [("n_heads", _i32), ("window", _i32), ("scale", ctypes.c_float), ("cap", ctypes.c_float),
@@ -134,6 +141,12 @@ EXPORTS += [
     ("syn_kv_read", _i32, [_P(KVCacheDesc), _i64, _vp, _vp, _vp, _vp]),
     ("syn_attn_decode", _i32, [_P(KVCacheDesc), _P(AttnDesc), _i64, _vp, _vp, _i64, _vp, _vp, _vp]),
     ("syn_attn_prefill", _i32, [_P(KVCacheDesc), _P(AttnDesc), _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
+    ("syn_kv_fork", _i32, [_P(KVCacheDesc), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]),
+    ("syn_kv_extend", _i32, [_P(KVCacheDesc), _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
+    ("syn_kv_compact", _i32, [_P(KVCacheDesc), _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
+    ("syn_kv_trim", _i32, [_P(KVCacheDesc), _vp, _i64, _vp, _i64, _vp, _vp]),
+    ("syn_kv_copy", _i32, [_P(KVCacheDesc), _P(KVCacheDesc), _i64, _vp, _vp, _vp]),
+    ("syn_logprobs", _i32, [_P(LogitsDesc), _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
 ]
 
 for _name, _res, _args in EXPORTS:
@@ -494,6 +507,160 @@ def prepare_attn_prefill(cache: KVCache, q, starts, pages, lens, out=None, scale
 
 def attn_prefill(cache: KVCache, q, starts, pages, lens, out=None, **options):
     return prepare_attn_prefill(cache, q, starts, pages, lens, out, **options)()
+
+
+# ---- the pages of a cache, as sequences hold them ------------------------------------------
+
+def _int32(x, what: str, *shape):
+    """Pointer of a contiguous int32 tensor of the given shape (None: any size there)."""
+    p = _typed(x, _torch().int32, what)
+    if x.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, x.shape)):
+        raise ValueError(f"{what}: an int32 tensor of shape ({', '.join('any' if n is None else str(n) for n in shape)})")
+    return p
+
+
+def _one_device(cache: KVCache, *tensors) -> None:
+    for x in tensors:
+        if x is not None and x.device != tensors[0].device:
+            raise ValueError("all tensors of a call lie on one device")
+    if cache.k.device != tensors[0].device:
+        raise ValueError("tables, counts and lengths lie on the cache's device")
+
+
+def prepare_kv_fork(cache: KVCache, refs, source, pages, lens, new_pages=None, new_lens=None, stream=None) -> Prepared:
+    """syn_kv_fork: sequence i of the new tables starts as source[i] of pages (n_seq, max_pages) and lens.
+    The call returns (new_pages, new_lens); tables that are given are overwritten, not given back."""
+    torch = _torch()
+    n_new, n_seq = source.numel(), lens.numel()
+    new_pages = torch.empty((n_new, pages.shape[1]), dtype=torch.int32, device=pages.device) if new_pages is None else new_pages
+    new_lens = torch.empty(n_new, dtype=torch.int32, device=pages.device) if new_lens is None else new_lens
+    _one_device(cache, refs, source, pages, lens, new_pages, new_lens)
+    args = (ctypes.byref(cache.desc), _int32(refs, "refs", cache.n_pages), n_seq, _int32(pages, "pages", n_seq, None), pages.shape[1],
+            _int32(lens, "lens", n_seq), n_new, _int32(source, "source", n_new), _int32(new_pages, "new_pages", n_new, pages.shape[1]),
+            _int32(new_lens, "new_lens", n_new), _stream(stream))
+    return Prepared("syn_kv_fork", args, (new_pages, new_lens), (cache, refs, source, pages, lens))
+
+
+def kv_fork(cache: KVCache, refs, source, pages, lens, new_pages=None, new_lens=None, stream=None):
+    return prepare_kv_fork(cache, refs, source, pages, lens, new_pages, new_lens, stream)()
+
+
+def prepare_kv_extend(cache: KVCache, refs, pages, lens, new_lens=None, slots=None, starts=None, n_tok=None, stream=None) -> Prepared:
+    """syn_kv_extend: room for starts[s+1] - starts[s] new rows of each sequence (starts None: one each; n_tok:
+    how many in all, which slots tell where they are given).  new_lens None: lens is updated.
+    The call returns (new_lens, slots)."""
+    torch = _torch()
+    n_seq = lens.numel()
+    if starts is None:
+        n_tok = n_seq
+    elif n_tok is None:
+        if slots is None:
+            raise ValueError("n_tok or slots tell how many new rows there are")
+        n_tok = slots.numel()
+    new_lens = lens if new_lens is None else new_lens
+    slots = torch.empty(n_tok, dtype=torch.int64, device=pages.device) if slots is None else slots
+    if slots.numel() != n_tok:
+        raise ValueError("slots: one for each new row")
+    _one_device(cache, refs, pages, lens, new_lens, slots, starts)
+    args = (ctypes.byref(cache.desc), _int32(refs, "refs", cache.n_pages), n_seq, n_tok, _int32(pages, "pages", n_seq, None),
+            pages.shape[1], _int32(lens, "lens", n_seq), None if starts is None else _int32(starts, "starts", n_seq + 1),
+            _int32(new_lens, "new_lens", n_seq), _typed(slots, torch.int64, "slots"), _stream(stream))
+    return Prepared("syn_kv_extend", args, (new_lens, slots), (cache, refs, pages, lens, starts))
+
+
+def kv_extend(cache: KVCache, refs, pages, lens, new_lens=None, slots=None, starts=None, n_tok=None, stream=None):
+    return prepare_kv_extend(cache, refs, pages, lens, new_lens, slots, starts, n_tok, stream)()
+
+
+def prepare_kv_compact(cache: KVCache, refs, pages, base, starts, rows, new_lens=None, stream=None) -> Prepared:
+    """syn_kv_compact: row base[s] + i becomes what row base[s] + rows[starts[s] + i] was.  refs may be None.
+    The call returns new_lens."""
+    torch = _torch()
+    n_seq = base.numel()
+    new_lens = torch.empty(n_seq, dtype=torch.int32, device=pages.device) if new_lens is None else new_lens
+    _one_device(cache, pages, refs, base, starts, rows, new_lens)
+    args = (ctypes.byref(cache.desc), None if refs is None else _int32(refs, "refs", cache.n_pages), n_seq, rows.numel(),
+            _int32(pages, "pages", n_seq, None), pages.shape[1], _int32(base, "base", n_seq), _int32(starts, "starts", n_seq + 1),
+            _int32(rows, "rows", None), _int32(new_lens, "new_lens", n_seq), _stream(stream))
+    return Prepared("syn_kv_compact", args, new_lens, (cache, refs, pages, base, starts, rows))
+
+
+def kv_compact(cache: KVCache, refs, pages, base, starts, rows, new_lens=None, stream=None):
+    return prepare_kv_compact(cache, refs, pages, base, starts, rows, new_lens, stream)()
+
+
+def prepare_kv_trim(cache: KVCache, refs, pages, lens, stream=None) -> Prepared:
+    """syn_kv_trim: the pages behind the first lens[s] rows of each sequence are given back.  Returns pages."""
+    n_seq = lens.numel()
+    _one_device(cache, refs, pages, lens)
+    args = (ctypes.byref(cache.desc), _int32(refs, "refs", cache.n_pages), n_seq, _int32(pages, "pages", n_seq, None), pages.shape[1],
+            _int32(lens, "lens", n_seq), _stream(stream))
+    return Prepared("syn_kv_trim", args, pages, (cache, refs, pages, lens))
+
+
+def kv_trim(cache: KVCache, refs, pages, lens, stream=None):
+    return prepare_kv_trim(cache, refs, pages, lens, stream)()
+
+
+def prepare_kv_copy(source: KVCache, target: KVCache, src, dst, stream=None) -> Prepared:
+    """syn_kv_copy: page src[i] of one cache to page dst[i] of another, or of the same."""
+    n = src.numel()
+    _one_device(source, src, dst)
+    _one_device(target, src)
+    args = (ctypes.byref(source.desc), ctypes.byref(target.desc), n, _int32(src, "src", n), _int32(dst, "dst", n), _stream(stream))
+    return Prepared("syn_kv_copy", args, None, (source, target, src, dst))
+
+
+def kv_copy(source: KVCache, target: KVCache, src, dst, stream=None):
+    return prepare_kv_copy(source, target, src, dst, stream)()
+
+
+# ---- log probabilities ---------------------------------------------------------------------
+
+class LogProbs(typing.NamedTuple):
+    """What syn_logprobs gives for each row; logprob is None without ids, top and top_logprob without n_top."""
+    logprob: object
+    entropy: object
+    top: object
+    top_logprob: object
+
+
+def prepare_logprobs(logits, ids=None, n_top: int = 0, scale: float = 1.0, cap: float = 0.0, scales=None, mask=None,
+                     stream=None) -> Prepared:
+    """syn_logprobs: logits float32 or float16 (n_rows, n_vocab), each row contiguous; ids int32 (n_rows, any) or
+    (n_rows,); scales float32 (n_rows); mask int32 (n_rows, at least n_vocab / 32), bit v % 32 of word v / 32 for
+    token v, each row contiguous.  The call returns LogProbs in buffers of its own."""
+    torch = _torch()
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.float16) or \
+            (logits.shape[1] > 1 and logits.stride(1) != 1) or (logits.shape[0] > 1 and logits.stride(0) < logits.shape[1]):
+        raise ValueError("logits: a float32 or float16 tensor (rows, vocabulary), each row contiguous")
+    n, vocab = logits.shape
+    n_ids = 0 if ids is None or n == 0 else ids.numel() // n
+    if ids is not None and (ids.numel() != n * n_ids or ids.shape[0] != n or ids.dim() > 2):
+        raise ValueError("ids: an int32 tensor (rows, tokens) or (rows,)")
+    if scales is not None and scales.shape != (n,):
+        raise ValueError("scales: one for each row")
+    if mask is not None and (mask.dim() != 2 or mask.dtype != torch.int32 or mask.shape[0] != n or 32 * mask.shape[1] < vocab or
+                             (mask.shape[1] > 1 and mask.stride(1) != 1) or (n > 1 and mask.stride(0) < mask.shape[1])):
+        raise ValueError("mask: an int32 tensor (rows, words), a bit for each token, each row contiguous")
+    for x in (ids, scales, mask):
+        if x is not None and x.device != logits.device:
+            raise ValueError("all tensors of a call lie on one device")
+    f32 = {"dtype": torch.float32, "device": logits.device}
+    out = LogProbs(None if ids is None else torch.empty(ids.shape, **f32), torch.empty(n, **f32),
+                   torch.empty((n, n_top), dtype=torch.int32, device=logits.device) if n_top > 0 else None,
+                   torch.empty((n, n_top), **f32) if n_top > 0 else None)
+    desc = LogitsDesc(OUT_F16 if logits.dtype == torch.float16 else OUT_F32, scale, cap, _typed(scales, torch.float32, "scales"),
+                      None if mask is None else _ptr(mask), logits.stride(0) if n > 1 else 0, mask.stride(0) if mask is not None and n > 1
+                      else 0)
+    args = (ctypes.byref(desc), n, vocab, _ptr(logits), n_ids, _typed(ids, torch.int32, "ids"),
+            None if ids is None else _ptr(out.logprob), _ptr(out.entropy), n_top, None if n_top <= 0 else _ptr(out.top),
+            None if n_top <= 0 else _ptr(out.top_logprob), _stream(stream))
+    return Prepared("syn_logprobs", args, out, (desc, logits, ids, scales, mask))
+
+
+def logprobs(logits, ids=None, n_top: int = 0, **options):
+    return prepare_logprobs(logits, ids, n_top, **options)()
 
 
 def block_sums(t: int, W, n_out: int, n_in: int, Xq, n_tok: int, stream=None):

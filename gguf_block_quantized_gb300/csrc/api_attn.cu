@@ -1,6 +1,6 @@
 // api_attn.cu — the C entry points of the paged key-value cache, its pages and its attention, and of the
 // log probabilities (declared in include/syn.h): argument checks, workspaces, dispatch to kv_append.cu,
-// kv_pages.cu, attn_decode.cu, attn_prefill.cu and logprobs.cu.
+// kv_pages.cu, attn_decode.cu, attn_prefill.cu, attn_tree.cu and logprobs.cu.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -276,6 +276,36 @@ int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_
     }
     rc = check_cuda(syn::launch_attn_prefill(c, raw, a, n_seq, n_tok, q, starts, pages, raw_pages, max_pages, lens, out, part, count,
                                              !syn::deterministic(), words, sms, &launches, s));
+    syn::note_launches(launches);
+    return rc;
+}
+
+int syn_attn_tree(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_seq, int64_t n_tok, const void* q,
+                  const int32_t* starts, const int32_t* parents, const int32_t* pages, int64_t max_pages, const int32_t* lens,
+                  void* out, syn_stream_t stream) {
+    syn::KvCache c;
+    int rc = cache_of(cache, &c);
+    if (rc) return rc;
+    if (n_seq < 0 || n_seq > INT32_MAX || n_tok < 0 || max_pages < (n_seq > 0 && n_tok > 0) || max_pages > INT32_MAX)
+        return SYN_ERR_SHAPE;
+    syn::AttnDesc a;
+    rc = attn_of(attn, c, n_seq ? n_tok : 0, q, out, &a);
+    if (rc) return rc;
+    if (n_tok > (INT32_MAX - 1024) / a.n_heads) return SYN_ERR_SHAPE;  // 32-bit row numbers
+    if (n_seq == 0 || n_tok == 0) return SYN_OK;
+    if (!starts || !parents || !pages || !lens) return SYN_ERR_NULL;
+    if (!aligned(starts, 4) || !aligned(parents, 4) || !aligned(pages, 4) || !aligned(lens, 4)) return SYN_ERR_ALIGN;
+    int sms, *words;
+    rc = syn::call_state(&sms, &words);
+    if (rc) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int* count;
+    float* part;
+    rc = scratch_for(s, sms + 2, syn::prefill_part_floats(n_seq, n_tok, a.n_heads, c.n_kv, c.dim, sms), &count, &part);
+    if (rc) return rc;
+    int launches = 0;
+    rc = check_cuda(syn::launch_attn_tree(c, a, n_seq, n_tok, q, starts, parents, pages, max_pages, lens, out, part, count,
+                                          !syn::deterministic(), words, sms, &launches, s));
     syn::note_launches(launches);
     return rc;
 }

@@ -141,6 +141,7 @@ EXPORTS += [
     ("syn_kv_read", _i32, [_P(KVCacheDesc), _i64, _vp, _vp, _vp, _vp]),
     ("syn_attn_decode", _i32, [_P(KVCacheDesc), _P(AttnDesc), _i64, _vp, _vp, _i64, _vp, _vp, _vp]),
     ("syn_attn_prefill", _i32, [_P(KVCacheDesc), _P(AttnDesc), _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
+    ("syn_attn_tree", _i32, [_P(KVCacheDesc), _P(AttnDesc), _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
     ("syn_kv_fork", _i32, [_P(KVCacheDesc), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]),
     ("syn_kv_extend", _i32, [_P(KVCacheDesc), _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
     ("syn_kv_compact", _i32, [_P(KVCacheDesc), _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
@@ -509,6 +510,26 @@ def attn_prefill(cache: KVCache, q, starts, pages, lens, out=None, **options):
     return prepare_attn_prefill(cache, q, starts, pages, lens, out, **options)()
 
 
+def prepare_attn_tree(cache: KVCache, q, starts, parents, pages, lens, out=None, scale=None, cap: float = 0.0,
+                      window: int = 0, slopes=None, prefix=None, first=None, stream=None) -> Prepared:
+    """syn_attn_tree: as prepare_attn_prefill, with parents int32 (n_tok): each new token's parent among its
+    sequence's new tokens, -1 for none.  The call returns out."""
+    torch = _torch()
+    n_seq = lens.numel()
+    if starts.numel() != n_seq + 1 or parents.numel() != q.shape[0]:
+        raise ValueError("starts: one more than the sequences; parents: one for each token")
+    desc, qp, out, op = _attn_desc(cache, q, out, n_seq, pages, lens, scale, cap, window, slopes, prefix, first)
+    _one_device(cache, q, starts, parents, pages, lens, out, slopes, prefix, first)
+    args = (ctypes.byref(cache.desc), ctypes.byref(desc), n_seq, q.shape[0], qp, _typed(starts, torch.int32, "starts"),
+            _typed(parents, torch.int32, "parents"), _typed(pages, torch.int32, "pages"), pages.shape[1],
+            _typed(lens, torch.int32, "lens"), op, _stream(stream))
+    return Prepared("syn_attn_tree", args, out, (cache, desc, q, starts, parents, pages, lens, out, slopes, prefix, first))
+
+
+def attn_tree(cache: KVCache, q, starts, parents, pages, lens, out=None, **options):
+    return prepare_attn_tree(cache, q, starts, parents, pages, lens, out, **options)()
+
+
 # ---- the pages of a cache, as sequences hold them ------------------------------------------
 
 def _int32(x, what: str, *shape):
@@ -524,7 +545,7 @@ def _one_device(cache: KVCache, *tensors) -> None:
         if x is not None and x.device != tensors[0].device:
             raise ValueError("all tensors of a call lie on one device")
     if cache.k.device != tensors[0].device:
-        raise ValueError("tables, counts and lengths lie on the cache's device")
+        raise ValueError("a call's tensors lie on its cache's device")
 
 
 def prepare_kv_fork(cache: KVCache, refs, source, pages, lens, new_pages=None, new_lens=None, stream=None) -> Prepared:

@@ -488,6 +488,23 @@ SYN_API int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, in
                              const void* q, const int32_t* starts, const int32_t* pages, int64_t max_pages,
                              const int32_t* lens, void* out, syn_stream_t stream);
 
+/* Attention of drafted tokens, the nodes of a tree for each sequence (several continuations verified in
+ * one call): as syn_attn_prefill, but of a sequence's n new tokens (starts, lens as there: the last n
+ * of its rows) token i has the parent parents[starts[s] + i], a token before it of the same sequence
+ * (0 .. i - 1), or -1: none.  With c = lens[s] - n rows of context and d(i) its number of ancestors, a
+ * node stands at position c + d(i) (which is what syn_kv_append is given for it), and sees
+ *   of the context   keys j < c with first <= j and (j < prefix or window == 0 or c + d(i) - j < window)
+ *   of the drafts    itself and its ancestors a with first <= c + a and (window == 0 or d(i) - d(a) < window)
+ * with a bias of slopes[head] times the distance of the positions.  (A prefix ends with the context.)
+ * A parent that is not before its token counts as none, and syn_device_status returns SYN_ERR_BOUNDS.
+ * Chains, whose parents are i - 1, give what syn_attn_prefill gives.  The drafts' rows are in the
+ * cache in the order of the tokens; syn_kv_compact packs an accepted path.  Accuracy, splitting,
+ * deterministic mode, workspace, alignment and errors as for syn_attn_prefill (a Q8_0 cache is not
+ * expanded ahead).  Asynchronous. */
+SYN_API int syn_attn_tree(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_seq, int64_t n_tok, const void* q,
+                          const int32_t* starts, const int32_t* parents, const int32_t* pages, int64_t max_pages,
+                          const int32_t* lens, void* out, syn_stream_t stream);
+
 /* ======================================================================================
  * The pages of a cache, as sequences hold them.  The caller keeps, on the device, a page table
  * (n_seq x max_pages; -1, or any other negative number: no page) and the lengths of its sequences, and refs, one count for each of

@@ -158,3 +158,36 @@ def test_helpers_refuse(syn):
     for more in ({"n_top": 65}, {"n_top": -1}, {"scale": 0.0}, {"cap": -1.0}):
         with pytest.raises(syn.SynError):
             syn.logprobs(x, **more, **kw)
+
+
+def tree(syn, c=None, **kw):
+    d = dict(n_heads=4, window=0, scale=0.125, cap=0.0, slopes=None, prefix=None, first=None, q_stride=0, out_stride=0, out_type=0)
+    a = dict(n_seq=2, n_tok=9, q=P, starts=P, parents=P, pages=P, max_pages=2, lens=P, out=P)
+    for k, v in kw.items():
+        assert k in d or k in a
+        (d if k in d else a)[k] = v
+    return syn.syn_attn_tree(c or cache(syn), syn.AttnDesc(*d.values()), *a.values(), None)
+
+
+@pytest.mark.parametrize("kw,err", [
+    ({"n_heads": 3}, "SHAPE"), ({"n_heads": 0}, "SHAPE"), ({"window": -1}, "SHAPE"), ({"scale": math.nan}, "SHAPE"), ({"cap": -1.0}, "SHAPE"),
+    ({"q_stride": 100}, "SHAPE"), ({"out_stride": LAST}, "SHAPE"), ({"out_type": 2}, "TYPE"), ({"n_seq": -1}, "SHAPE"),
+    ({"n_tok": -1}, "SHAPE"), ({"n_tok": 1 << 30}, "SHAPE"), ({"max_pages": 0}, "SHAPE"), ({"max_pages": LAST}, "SHAPE"), ({"q": None}, "NULL"),
+    ({"starts": None}, "NULL"), ({"parents": None}, "NULL"), ({"pages": None}, "NULL"), ({"lens": None}, "NULL"), ({"out": None}, "NULL"),
+    ({"q": P + 8}, "ALIGN"), ({"starts": P + 2}, "ALIGN"), ({"parents": P + 2}, "ALIGN"), ({"pages": P + 1}, "ALIGN"), ({"lens": P + 2}, "ALIGN"),
+    ({"out": P + 4}, "ALIGN"), ({"first": P + 2}, "ALIGN"), ({"prefix": P + 2}, "ALIGN"), ({"slopes": P + 2}, "ALIGN")])
+def test_tree_refusals(syn, kw, err):
+    assert tree(syn, **kw) == getattr(syn, "ERR_" + err)
+
+
+def test_tree_checks_its_structures(syn):
+    import torch
+    assert tree(syn, cache(syn, type=3)) == syn.ERR_TYPE and tree(syn, cache(syn, k=None)) == syn.ERR_NULL
+    assert syn.syn_attn_tree(cache(syn), None, 1, 1, P, P, P, P, 1, P, P, None) == syn.ERR_NULL
+    assert tree(syn, n_tok=0) == syn.OK and tree(syn, n_seq=0, n_tok=0) == syn.OK
+    c = syn.KVCache.empty(F16, 2, 64, 16, 4, device="cpu")
+    q, i = torch.zeros((3, 4, 64), dtype=torch.float16), lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    for a in ((q, i(2), i(3), i(2, 3), i(2)), (q, i(3), i(4), i(2, 3), i(2)), (q, i(3), i(3).long(), i(2, 3), i(2)), (q, i(3), i(3), i(1, 3), i(2)),
+              (q.float(), i(3), i(3), i(2, 3), i(2)), (q, i(3), i(3).to("meta"), i(2, 3), i(2))):
+        with pytest.raises(ValueError):
+            syn.attn_tree(c, *a, stream=0)

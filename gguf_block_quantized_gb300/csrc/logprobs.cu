@@ -1,19 +1,19 @@
 // logprobs.cu — log probabilities of given tokens, the entropy and the most likely tokens of rows of
 // logits, in one pass over the logits.
 //
-//   z = scale * (cap > 0 ? cap*tanh(x/cap) : x) over the allowed tokens, d = z - z(largest x)
-//   S = sum e^d, T = sum d e^d;  logp(v) = d_v - ln S,  entropy = ln S - T/S
-// Both sums follow a running maximum: when it moves by r, S' = S e^r and T' = (T + r S) e^r.
+//   z = cap > 0 ? cap*tanh(x/cap) : x,  y = scale log2(e) (z - the largest z)
+//   S = sum 2^y, T = sum y 2^y;  logp(v) = ln2 (y_v - log2 S),  entropy = ln2 (log2 S - T/S)
+// Both sums follow a running maximum: when it grows by g (as y counts), S' = S 2^-g and T' = (T - g S) 2^-g.
 //
 // Bound: HBM (or L2, where the product that made the logits has just written them): every logit is read
-// once, into the registers of the thread that keeps them, 32 at a time.
+// once; a thread holds four 16-byte pieces while the next four are on their way.  fp16 logits come close to
+// the issue slots (5 instructions a logit).
 //   - A row is cut between the CTAs of a cluster (1 to 8, as many as the rows leave room for), which
 //     send what they found to the first through its shared memory.  No CTA waits for another row's.
-//   - The n_top largest: the 512 threads' own maxima are counted against a threshold, which is halved
-//     in until between n_top and 2 n_top of them reach it; every logit below it is beaten by n_top others, so only the few
-//     threads above it look through their 32 logits.  What they find is ordered by counting, for
-//     each, the larger ones (ties: the lower token first).  Later pieces of a row start from the
-//     n_top-th largest found so far.
+//   - The n_top largest: a thread notes the largest of each eighth of its logits (a unit).  At the row's end the
+//     threads' own maxima are counted against a threshold, which is halved in until between n_top and 2 n_top of
+//     them reach it; every logit below it is beaten by n_top others, so only the units that reach it are read
+//     again (from L2).  What they hold is ordered by counting, for each, the larger ones (ties: the lower token first).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -26,11 +26,11 @@ namespace cg = cooperative_groups;
 
 namespace syn {
 
-constexpr int LP_THREADS = 512;
-constexpr int LP_HOLD = 32;      // logits in a thread's registers
 constexpr int LP_TOP = LOGPROBS_TOP;
 constexpr int LP_CLUSTER = 8;
-constexpr uint32_t LP_NONE = 0x007FFFFFu;  // order_of(-inf)
+constexpr int LP_UNITS = 8;      // of a thread
+constexpr int LP_PIECES = 4;     // 16-byte pieces a thread holds
+constexpr float LP_LN2 = 0.693147180559945309f, LP_LOG2E = 1.44269504088896341f;
 
 struct LogprobParams {
     const void* x;
@@ -54,12 +54,15 @@ __device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t b = __float_as_uint(x);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float of_order(uint32_t u) {
-    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
-}
+__device__ __forceinline__ float of_order(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u); }
 __device__ __forceinline__ float max_nan(float a, float b) {
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 __device__ __forceinline__ uint4 load_once(const void* p) {
@@ -74,19 +77,103 @@ struct Sums {
     float x, s, t;
 };
 
+// A row's logits: 16-byte pieces from the boundary at or below its first, so that the first piece may begin before the
+// row and the last end behind it (those are read logit by logit).
 template <bool F16>
-__device__ __forceinline__ float logit_at(const void* row, int64_t i) {
-    return F16 ? __half2float(static_cast<const __half*>(row)[i]) : static_cast<const float*>(row)[i];
-}
+struct Row {
+    static constexpr int E = F16 ? 8 : 4;  // logits of a piece
+    const uint8_t* at;
+    const uint32_t* mask;
+    int n, head, pieces;
+
+    __device__ __forceinline__ float one(int64_t i) const {
+        return F16 ? __half2float(reinterpret_cast<const __half*>(at)[i]) : reinterpret_cast<const float*>(at)[i];
+    }
+    __device__ __forceinline__ int token(int piece, int j) const { return piece * E - head + j; }
+    // A piece's bits; in those of logits that are not the row's, -inf.
+    __device__ __forceinline__ uint4 load(int piece, int end) const {
+        const int e0 = token(piece, 0);
+        if (piece < end && e0 >= 0 && e0 + E <= n) return load_once(at + (int64_t)e0 * (F16 ? 2 : 4));
+        uint32_t w[4] = {F16 ? 0xFC00FC00u : 0xFF800000u, F16 ? 0xFC00FC00u : 0xFF800000u, F16 ? 0xFC00FC00u : 0xFF800000u,
+                         F16 ? 0xFC00FC00u : 0xFF800000u};
+        if (piece < end) {
+#pragma unroll
+            for (int j = 0; j < E; j++)
+                if (e0 + j >= 0 && e0 + j < n) {
+                    if (F16) {
+                        const uint32_t h = reinterpret_cast<const uint16_t*>(at)[e0 + j];
+                        w[j / 2] = j & 1 ? (w[j / 2] & 0xFFFFu) | h << 16 : (w[j / 2] & 0xFFFF0000u) | h;
+                    } else {
+                        w[j % 4] = reinterpret_cast<const uint32_t*>(at)[e0 + j];
+                    }
+                }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // The piece with -inf where the mask does not allow the token.
+    __device__ __forceinline__ uint4 allowed(const uint4& piece, int index) const {
+        const int e0 = token(index, 0), w = max(e0, 0) >> 5;
+        const bool any = e0 < n;
+        const uint32_t lo = any ? __ldg(mask + w) : 0u;
+        const uint32_t hi = any && (e0 & 31) + E > 32 && e0 >= 0 && w < (n - 1) >> 5 ? __ldg(mask + w + 1) : 0u;
+        const uint32_t bits = e0 < 0 ? lo << -e0 : __funnelshift_r(lo, hi, e0 & 31);
+        uint32_t u[4] = {piece.x, piece.y, piece.z, piece.w};
+#pragma unroll
+        for (int j = 0; j < E; j++)
+            if (!((bits >> j) & 1)) {
+                if (F16) u[j / 2] = j & 1 ? (u[j / 2] & 0xFFFFu) | 0xFC000000u : (u[j / 2] & 0xFFFF0000u) | 0xFC00u;
+                else u[j % 4] = 0xFF800000u;
+            }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
 
 template <bool F16>
-__global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(const LogprobParams p) {
-    constexpr int E = F16 ? 8 : 4, V = LP_HOLD / E;  // logits of a 16-byte piece, pieces a thread holds
-    constexpr int WARPS = LP_THREADS / 32;
-    __shared__ uint64_t found[LP_TOP + 2 * LP_TOP * LP_HOLD], best[LP_TOP];
+__device__ __forceinline__ void values_of(const uint4& piece, float (&v)[F16 ? 8 : 4]) {
+    const uint32_t u[4] = {piece.x, piece.y, piece.z, piece.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        if (F16) {
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+            v[F16 ? 2 * j : j] = y.x;
+            v[F16 ? 2 * j + 1 : j] = y.y;
+        } else {
+            v[j] = __uint_as_float(u[j]);
+        }
+    }
+}
+// The largest value of a thread's pieces (NaN where there is one).
+template <bool F16>
+__device__ __forceinline__ float largest_of(const uint4 (&piece)[LP_PIECES]) {
+    if (F16) {
+        __half2 m = __float2half2_rn(-INFINITY);
+#pragma unroll
+        for (int i = 0; i < LP_PIECES; i++) {
+            const uint32_t u[4] = {piece[i].x, piece[i].y, piece[i].z, piece[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) m = __hmax2_nan(m, *reinterpret_cast<const __half2*>(&u[j]));
+        }
+        return max_nan(__low2float(m), __high2float(m));
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < LP_PIECES; i++) {
+        m = max_nan(m, __uint_as_float(piece[i].x), __uint_as_float(piece[i].y));
+        m = max_nan(m, __uint_as_float(piece[i].z), __uint_as_float(piece[i].w));
+    }
+    return m;
+}
+
+template <bool F16, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const LogprobParams p) {
+    constexpr int E = Row<F16>::E, WARPS = THREADS / 32, MOST = LP_TOP + THREADS * E;
+    static_assert(MOST * 8 >= LP_UNITS * THREADS * 4, "the units' maxima lie where the found keys will");
+    __shared__ uint64_t found[MOST], best[LP_TOP];
+    float* unit_max = reinterpret_cast<float*>(found);
     __shared__ uint64_t sent[LP_CLUSTER * LP_TOP];  // (the first CTA's) the others' largest
+    __shared__ int units[LP_UNITS * 2 * LP_TOP];
     __shared__ Sums sent_sums[LP_CLUSTER], warp_sums[WARPS];
-    __shared__ int sent_n[LP_CLUSTER], n_found;
+    __shared__ int sent_n[LP_CLUSTER], n_found, n_units;
     __shared__ uint32_t warp_lo[WARPS], warp_hi[WARPS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int part = p.cut > 1 ? (int)cg::this_cluster().block_rank() : 0;
@@ -96,203 +183,208 @@ __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(const LogprobParams 
 
     const int64_t rows_at_once = gridDim.x / p.cut;
     for (int64_t r = blockIdx.x / p.cut; r < p.n_rows; r += rows_at_once) {
-        const uint8_t* row = static_cast<const uint8_t*>(p.x) + r * p.stride * (F16 ? 2 : 4);
-        const uint32_t* mask = p.mask ? p.mask + r * p.mask_stride : nullptr;
+        Row<F16> row;
+        row.at = static_cast<const uint8_t*>(p.x) + r * p.stride * (F16 ? 2 : 4);
+        row.mask = p.mask ? p.mask + r * p.mask_stride : nullptr;
+        row.n = p.n_vocab;
+        row.head = (int)(reinterpret_cast<uintptr_t>(row.at) & 15) / (F16 ? 2 : 4);
+        row.pieces = (row.head + p.n_vocab + E - 1) / E;
+        const int per = (row.pieces + p.cut - 1) / p.cut, begin = per * part, end = min(row.pieces, begin + per);
+        // a turn: the CTA's next LP_PIECES * THREADS pieces; group: turns of a unit
+        const int turns = max(0, (end - begin + LP_PIECES * THREADS - 1) / (LP_PIECES * THREADS)), group = (turns + LP_UNITS - 1) / LP_UNITS;
+        auto piece_of = [&](int turn, int i) { return begin + (turn * LP_PIECES + i) * THREADS + tid; };
+        uint4 next[LP_PIECES];
+#pragma unroll
+        for (int i = 0; i < LP_PIECES; i++) next[i] = row.load(piece_of(0, i), end);
+
         const float scale = p.scales ? p.scale * p.scales[r] : p.scale;
         const bool scale_ok = scale > 0.0f && scale < INFINITY;
-        // pieces start on 16-byte boundaries: the first may begin before the row, the last end behind it
-        const int head = (int)(reinterpret_cast<uintptr_t>(row) & 15) / (F16 ? 2 : 4);
-        const int pieces = (head + p.n_vocab + E - 1) / E;
-        const int per = (pieces + p.cut - 1) / p.cut, end = min(pieces, per * (part + 1));
-        // (the larger logit's d is 0 exactly; a logit of -inf counts as a token that is not allowed)
-        auto from = [&](float x, float x0) {
-            return p.cap > 0.0f ? scale * (p.cap * tanhf(x / p.cap) - p.cap * tanhf(x0 / p.cap)) : scale * (x - x0);
-        };
-        auto join = [&](Sums a, const Sums& b) {
-            const float x = max_nan(a.x, b.x), x0 = x == -INFINITY ? 0.0f : x;
-            const float ra = a.x == -INFINITY ? 0.0f : from(a.x, x0), rb = b.x == -INFINITY ? 0.0f : from(b.x, x0);
-            // (e^-200 is 0; 0 times infinity stays out)
-            const float fa = expf(fmaxf(ra, -200.0f)), fb = expf(fmaxf(rb, -200.0f));
+        const float c = scale * LP_LOG2E;
+        auto capped = [&](float x) { return p.cap > 0.0f ? p.cap * tanhf(x / p.cap) : x; };
+        auto join = [&](const Sums& a, const Sums& b) {
             Sums y;
-            y.x = x;
+            y.x = max_nan(a.x, b.x);
+            const float z = capped(y.x);
+            // (2^-300 is 0, which keeps infinities out)
+            const float ga = a.s > 0.0f ? fminf(c * (z - capped(a.x)), 300.0f) : 0.0f, gb = b.s > 0.0f ? fminf(c * (z - capped(b.x)), 300.0f) : 0.0f;
+            const float fa = ex2(-ga), fb = ex2(-gb);
             y.s = a.s * fa + b.s * fb;
-            y.t = (a.t + fmaxf(ra, -200.0f) * a.s) * fa + (b.t + fmaxf(rb, -200.0f) * b.s) * fb;
+            y.t = (a.t - ga * a.s) * fa + (b.t - gb * b.s) * fb;
             return y;
-        };
-        auto key_of = [&](float x, int token) { return ((uint64_t)order_of(x) << 32) | (uint32_t)~token; };
-        // the n_top largest of the n keys in `found`, in order, into `best`; both stay as they are till the next barrier
-        auto rank_found = [&](int n) {
-            for (int i = tid; i < n; i += LP_THREADS) {
-                const uint64_t mine = found[i];
-                int rank = 0;
-                for (int j = 0; j < n; j++) rank += found[j] > mine;
-                if (rank < p.n_top) best[rank] = mine;
-            }
         };
 
         Sums mine{-INFINITY, 0.0f, 0.0f};
-        int n_best = 0;
-        uint32_t floor_at = LP_NONE;  // logits up to here are out
-        for (int base = per * part; base < end; base += LP_THREADS * V) {
-            float v[LP_HOLD];
+        float z0 = 0.0f, unit = -INFINITY;  // z0: that of mine.x
+        for (int turn = 0, left = group, u = 0; turn < turns; turn++) {
+            uint4 now[LP_PIECES];
 #pragma unroll
-            for (int i = 0; i < V; i++) {
-                const int at = base + i * LP_THREADS + tid, e0 = at * E - head;
-                if (at < end && e0 >= 0 && e0 + E <= p.n_vocab) {
-                    const uint4 w = load_once(row + (int64_t)e0 * (F16 ? 2 : 4));
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            for (int i = 0; i < LP_PIECES; i++) now[i] = next[i];
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        if (F16) {
-                            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-                            v[i * E + 2 * j % E] = y.x;
-                            v[i * E + (2 * j + 1) % E] = y.y;
-                        } else {
-                            v[i * E + j] = __uint_as_float(u[j]);
-                        }
-                    }
-                } else {
+            for (int i = 0; i < LP_PIECES; i++) next[i] = row.load(piece_of(turn + 1, i), turn + 1 < turns ? end : 0);
+            if (row.mask)
 #pragma unroll
-                    for (int j = 0; j < E; j++)
-                        v[i * E + j] = at < end && e0 + j >= 0 && e0 + j < p.n_vocab ? logit_at<F16>(row, e0 + j) : -INFINITY;
-                }
+                for (int i = 0; i < LP_PIECES; i++) now[i] = row.allowed(now[i], piece_of(turn, i));
+            const float x = largest_of<F16>(now);
+            unit = max_nan(unit, x);
+            if (--left == 0 || turn + 1 == turns) {
+                if (p.n_top > 0) unit_max[u++ * THREADS + tid] = unit;
+                left = group;
+                unit = -INFINITY;
             }
-            if (mask) {
-                const int words = (p.n_vocab + 31) >> 5;
-#pragma unroll
-                for (int i = 0; i < V; i++) {
-                    const int at = base + i * LP_THREADS + tid, e0 = at * E - head, w = max(e0, 0) >> 5;
-                    const uint32_t lo = at < end ? __ldg(mask + w) : 0u;
-                    const uint32_t hi = at < end && (e0 & 31) + E > 32 && e0 >= 0 && w + 1 < words ? __ldg(mask + w + 1) : 0u;
-                    const uint32_t bits = e0 < 0 ? lo << -e0 : __funnelshift_r(lo, hi, e0 & 31);
-#pragma unroll
-                    for (int j = 0; j < E; j++)
-                        if (!((bits >> j) & 1)) v[i * E + j] = -INFINITY;
+            if (x == -INFINITY) continue;
+            if (!(x <= mine.x)) {
+                mine.x = max_nan(mine.x, x);
+                const float z = capped(mine.x), g = fminf(c * (z - z0), 300.0f), f = ex2(-g);
+                if (mine.s > 0.0f) {
+                    mine.t = (mine.t - g * mine.s) * f;
+                    mine.s *= f;
                 }
+                z0 = z;
             }
-            float x = -INFINITY;
+            uint64_t s2 = 0, t2 = 0;
+            const uint64_t c2 = pack2(c, c), z2 = pack2(-z0, -z0);
 #pragma unroll
-            for (int j = 0; j < LP_HOLD; j++) x = max_nan(x, v[j]);
-            // ---- the sums -----------------------------------------------------------------------
-            if (x != -INFINITY) {
-                if (!(x <= mine.x)) {
-                    if (mine.x != -INFINITY) mine = join(mine, Sums{x, 0.0f, 0.0f});
-                    mine.x = max_nan(mine.x, x);
-                }
-                float s[2] = {0.0f, 0.0f}, t[2] = {0.0f, 0.0f};
+            for (int i = 0; i < LP_PIECES; i++) {
+                float v[E];
+                values_of<F16>(now[i], v);
                 if (p.cap > 0.0f) {
-                    const float z0 = p.cap * tanhf(mine.x / p.cap);
 #pragma unroll
-                    for (int j = 0; j < LP_HOLD; j++) {
-                        float d = scale * (p.cap * tanhf(v[j] / p.cap) - z0);
-                        d = v[j] == -INFINITY ? -200.0f : fmaxf(d, -200.0f);
-                        const float e = ex2(d * 1.4426950408889634f);
-                        s[j & 1] += e;
-                        t[j & 1] = fmaf(e, d, t[j & 1]);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < LP_HOLD; j++) {
-                        const float d = fmaxf(scale * (v[j] - mine.x), -200.0f);  // (2^-288 is 0)
-                        const float e = ex2(d * 1.4426950408889634f);
-                        s[j & 1] += e;
-                        t[j & 1] = fmaf(e, d, t[j & 1]);
-                    }
+                    for (int j = 0; j < E; j++) v[j] = v[j] == -INFINITY ? -INFINITY : capped(v[j]);
                 }
-                mine.s += s[0] + s[1];
-                mine.t += t[0] + t[1];
+#pragma unroll
+                for (int j = 0; j < E; j += 2) {
+                    float2 y = unpack2(mul2(add2(pack2(v[j], v[j + 1]), z2), c2));
+                    y.x = fmaxf(y.x, -300.0f);
+                    y.y = fmaxf(y.y, -300.0f);
+                    const uint64_t e2 = pack2(ex2(y.x), ex2(y.y));
+                    s2 = add2(s2, e2);
+                    t2 = fma2(e2, pack2(y.x, y.y), t2);
+                }
             }
-            // ---- the largest --------------------------------------------------------------------
-            if (p.n_top > 0) {
-                const int k = p.n_top;
-                const uint32_t u = x == x ? order_of(x + 0.0f) : 0u;  // (-0 is 0)
-                int n = __syncthreads_count(u > floor_at);
-                if (n == 0) continue;
-                uint32_t at_least = floor_at + 1;
-                int tie = 0x7fffffff;  // of the logits at the threshold, those up to this token
-                if (n > 2 * k) {
-                    const uint32_t wl = __reduce_min_sync(0xffffffffu, u > floor_at ? u : 0xffffffffu), wh = __reduce_max_sync(0xffffffffu, u);
-                    if (lane == 0) {
-                        warp_lo[warp] = wl;
-                        warp_hi[warp] = wh;
-                    }
-                    __syncthreads();
-                    uint32_t lo = warp_lo[lane % WARPS], hi = warp_hi[lane % WARPS];
-                    lo = __reduce_min_sync(0xffffffffu, lo);
-                    hi = __reduce_max_sync(0xffffffffu, hi);
-                    while (lo < hi && n > 2 * k) {  // (n: how many reach lo; fewer than k reach hi + 1)
-                        const uint32_t mid = lo + (hi - lo) / 2 + 1;
-                        const int c = __syncthreads_count(u >= mid);
-                        if (c >= k) {
-                            lo = mid;
-                            n = c;
-                        } else {
-                            hi = mid - 1;
-                        }
-                    }
-                    at_least = lo;
-                    if (n > 2 * k) {  // many maxima are the same: the same again over the first tokens that have it
-                        const float same = of_order(lo);
-                        int first = 0x7fffffff;
-#pragma unroll
-                        for (int j = LP_HOLD - 1; j >= 0; j--)
-                            if (v[j] == same) first = (base + j / E * LP_THREADS + tid) * E - head + j % E;
-                        if (u > lo) first = -1;
-                        int a = -1, b = p.n_vocab - 1;  // (fewer than k are at most a; more than 2k at most b)
-                        while (n > 2 * k) {
-                            const int mid = a + (b - a) / 2;
-                            const int c = __syncthreads_count(first <= mid);
-                            if (c >= k) {
-                                b = mid;
-                                n = c;
-                            } else {
-                                a = mid;
-                            }
-                        }
-                        tie = b;
-                    }
-                }
-                if (tid == 0) n_found = n_best;
-                if (tid < n_best) found[tid] = best[tid];
-                __syncthreads();
-                if (u >= at_least) {
-                    const float least = of_order(at_least);
-#pragma unroll
-                    for (int j = 0; j < LP_HOLD; j++) {
-                        const int token = (base + j / E * LP_THREADS + tid) * E - head + j % E;
-                        if (v[j] > least || (v[j] == least && token <= tie)) {
-                            const int at = atomicAdd(&n_found, 1);
-                            found[min(at, LP_TOP + 2 * LP_TOP * LP_HOLD - 1)] = key_of(v[j] + 0.0f, token);
-                        }
-                    }
-                }
-                __syncthreads();
-                const int m = n_found;
-                rank_found(m);
-                __syncthreads();
-                n_best = min(m, k);
-                if (n_best == k) floor_at = (uint32_t)(best[k - 1] >> 32);
-            }
+            const float2 s = unpack2(s2), t = unpack2(t2);
+            mine.s += s.x + s.y;
+            mine.t += t.x + t.y;
         }
 
-        // ---- the CTA's, then the row's -----------------------------------------------------------
+        // ---- the sums of the CTA ---------------------------------------------------------------
+        Sums sums = mine;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const Sums other{__shfl_xor_sync(0xffffffffu, mine.x, o), __shfl_xor_sync(0xffffffffu, mine.s, o),
-                             __shfl_xor_sync(0xffffffffu, mine.t, o)};
-            mine = lane & o ? join(other, mine) : join(mine, other);  // (the same order in both)
+            const Sums other{__shfl_xor_sync(0xffffffffu, sums.x, o), __shfl_xor_sync(0xffffffffu, sums.s, o),
+                             __shfl_xor_sync(0xffffffffu, sums.t, o)};
+            sums = lane & o ? join(other, sums) : join(sums, other);  // (the same order in both)
         }
-        if (lane == 0) warp_sums[warp] = mine;
+        if (lane == 0) warp_sums[warp] = sums;
+        // ---- the CTA's largest -----------------------------------------------------------------
+        // the n_top largest of the n keys in `found`, in order, into `best`
+        auto rank_found = [&](int n) {
+            for (int i = tid; i < n; i += THREADS) {
+                const uint64_t key = found[i];
+                int rank = 0;
+                for (int j = 0; j < n; j++) rank += found[j] > key;
+                if (rank < p.n_top) best[rank] = key;
+            }
+        };
+        int n_best = 0;
+        if (p.n_top > 0) {
+            const int k = p.n_top;
+            const uint32_t none = order_of(-INFINITY), u = mine.x == mine.x ? order_of(mine.x + 0.0f) : none;  // (-0 is 0)
+            const uint32_t wl = __reduce_min_sync(0xffffffffu, u > none ? u : 0xffffffffu), wh = __reduce_max_sync(0xffffffffu, u);
+            if (lane == 0) {
+                warp_lo[warp] = wl;
+                warp_hi[warp] = wh;
+            }
+            if (tid == 0) n_found = n_units = 0;
+            int n = __syncthreads_count(u > none);
+            uint32_t lo = __reduce_min_sync(0xffffffffu, warp_lo[lane % WARPS]), hi = __reduce_max_sync(0xffffffffu, warp_hi[lane % WARPS]);
+            while (lo < hi && n > 2 * k) {  // (n: how many reach lo; fewer than k reach hi + 1)
+                const uint32_t mid = lo + (hi - lo) / 2 + 1;
+                const int reach = __syncthreads_count(u >= mid);
+                if (reach >= k) {
+                    lo = mid;
+                    n = reach;
+                } else {
+                    hi = mid - 1;
+                }
+            }
+            if (n < k) lo = none + 1;  // (fewer threads have a logit than are wanted: all their logits count)
+            const float least = of_order(lo);
+            int tie = 0x7fffffff, first = -1;  // of the logits at the threshold those up to token `tie` count; this thread's first
+            if (n > 2 * k) {  // many maxima are the same: the same search over the tokens that have it
+                first = u > lo ? -1 : 0x7fffffff;
+                for (int turn = 0; turn < turns && u == lo && first > p.n_vocab; turn++)
+#pragma unroll
+                    for (int i = LP_PIECES - 1; i >= 0; i--) {
+                        float v[E];
+                        const uint4 piece = row.load(piece_of(turn, i), end);
+                        values_of<F16>(row.mask ? row.allowed(piece, piece_of(turn, i)) : piece, v);
+#pragma unroll
+                        for (int j = E - 1; j >= 0; j--)
+                            if (v[j] == least) first = row.token(piece_of(turn, i), j);
+                    }
+                int a = -1, b = p.n_vocab - 1;  // (fewer than k are at most a; more than 2k at most b)
+                while (n > 2 * k) {
+                    const int mid = a + (b - a) / 2;
+                    const int reach = __syncthreads_count(first <= mid);
+                    if (reach >= k) {
+                        b = mid;
+                        n = reach;
+                    } else {
+                        a = mid;
+                    }
+                }
+                tie = b;
+            }
+            if (n > 0 && u >= lo && first <= tie)  // (at most 2k threads)
+                for (int i = 0; i < LP_UNITS && i * group < turns; i++)
+                    if (unit_max[i * THREADS + tid] >= least) units[atomicAdd(&n_units, 1)] = i * THREADS + tid;
+            __syncthreads();
+            const int per_unit = group * LP_PIECES, loads = n_units * per_unit;
+            uint64_t above = 0;  // what is not above this key is out
+            for (int l0 = 0; l0 < loads; l0 += THREADS) {
+                if (l0 > 0) {
+                    __syncthreads();
+                    if (n_found + THREADS * E > MOST) {  // (rows whose large logits crowd in few threads)
+                        const int m = n_found;
+                        rank_found(m);
+                        __syncthreads();
+                        if (tid < min(m, k)) found[tid] = best[tid];
+                        if (m >= k) above = best[k - 1];
+                        if (tid == 0) n_found = min(m, k);
+                        __syncthreads();
+                    }
+                }
+                const int l = l0 + tid;
+                if (l < loads) {
+                    const int which = units[l / per_unit], x = l % per_unit, of = which % THREADS;
+                    const int turn = which / THREADS * group + x / LP_PIECES;
+                    const int piece = begin + (turn * LP_PIECES + x % LP_PIECES) * THREADS + of;
+                    float v[E];
+                    const uint4 raw = row.load(piece, turn < turns ? end : 0);
+                    values_of<F16>(row.mask ? row.allowed(raw, piece) : raw, v);
+#pragma unroll
+                    for (int j = 0; j < E; j++) {
+                        const int token = row.token(piece, j);
+                        const uint64_t key = ((uint64_t)order_of(v[j] + 0.0f) << 32) | (uint32_t)~token;
+                        if ((v[j] > least || (v[j] == least && token <= tie)) && key > above) found[atomicAdd(&n_found, 1)] = key;
+                    }
+                }
+            }
+            __syncthreads();
+            n_best = min(n_found, k);
+            rank_found(n_found);
+        }
         __syncthreads();
         if (warp == 0) {
-            mine = warp_sums[lane % WARPS];
+            sums = warp_sums[lane % WARPS];
 #pragma unroll
             for (int o = WARPS / 2; o > 0; o >>= 1) {
-                const Sums other{__shfl_xor_sync(0xffffffffu, mine.x, o), __shfl_xor_sync(0xffffffffu, mine.s, o),
-                                 __shfl_xor_sync(0xffffffffu, mine.t, o)};
-                mine = lane & o ? join(other, mine) : join(mine, other);
+                const Sums other{__shfl_xor_sync(0xffffffffu, sums.x, o), __shfl_xor_sync(0xffffffffu, sums.s, o),
+                                 __shfl_xor_sync(0xffffffffu, sums.t, o)};
+                sums = lane & o ? join(other, sums) : join(sums, other);
             }
         }
+        // ---- the row's -------------------------------------------------------------------------
         if (p.cut > 1) {
             auto cluster = cg::this_cluster();
             cluster.barrier_wait();
@@ -300,19 +392,19 @@ __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(const LogprobParams 
             int* to_n = cluster.map_shared_rank(sent_n, 0);
             uint64_t* to = cluster.map_shared_rank(sent, 0);
             if (tid == 0) {
-                to_sums[part] = mine;
+                to_sums[part] = sums;
                 to_n[part] = n_best;
             }
             if (tid < n_best) to[part * LP_TOP + tid] = best[tid];
             cluster.sync();
             if (part == 0) {
                 int at = 0;
-                for (int c = 0; c < p.cut; c++) {
-                    if (tid < sent_n[c]) found[at + tid] = sent[c * LP_TOP + tid];
-                    at += sent_n[c];
+                for (int i = 0; i < p.cut; i++) {
+                    if (tid < sent_n[i]) found[at + tid] = sent[i * LP_TOP + tid];
+                    at += sent_n[i];
                 }
-                mine = sent_sums[0];
-                for (int c = 1; c < p.cut; c++) mine = join(mine, sent_sums[c]);
+                sums = sent_sums[0];
+                for (int i = 1; i < p.cut; i++) sums = join(sums, sent_sums[i]);
                 if (r + rows_at_once < p.n_rows) cluster.barrier_arrive();  // (what was sent has been read)
                 __syncthreads();
                 rank_found(at);
@@ -322,31 +414,49 @@ __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(const LogprobParams 
                 continue;
             }
         }
-        if (tid == 0) warp_sums[0] = mine;
+        if (tid == 0) warp_sums[0] = sums;
         __syncthreads();
-        mine = warp_sums[0];
-        const bool bad = !(mine.x < INFINITY) || !scale_ok;  // NaN or infinite logits, a scale that is none
-        const float nan = __int_as_float(0x7fffffff);
-        const float log_s = mine.s > 0.0f ? logf(mine.s) : 0.0f;
-        if (tid == 0 && p.entropy) p.entropy[r] = bad ? nan : mine.s > 0.0f ? log_s - mine.t / mine.s : 0.0f;
-        for (int i = tid; i < p.n_ids; i += LP_THREADS) {
+        sums = warp_sums[0];
+        const bool bad = !(sums.x < INFINITY) || !scale_ok;  // NaN or infinite logits, a scale that is none
+        const float nan = __int_as_float(0x7fffffff), row_z = capped(sums.x), log_s = sums.s > 0.0f ? log2f(sums.s) : 0.0f;
+        auto logp = [&](float x) { return LP_LN2 * (c * (capped(x) - row_z) - log_s); };
+        if (tid == 0 && p.entropy) p.entropy[r] = bad ? nan : sums.s > 0.0f ? LP_LN2 * (log_s - sums.t / sums.s) : 0.0f;
+        for (int i = tid; i < p.n_ids; i += THREADS) {
             const int token = p.ids[r * p.n_ids + i];
             float y = 0.0f;
             if (token >= p.n_vocab) record_error(p.err, SYN_DEVERR_BOUNDS);
             else if (token >= 0) {
-                const float x = logit_at<F16>(row, token);
-                const bool on = (!mask || ((mask[token >> 5] >> (token & 31)) & 1)) && x > -INFINITY;
-                y = bad ? nan : on ? from(x, mine.x) - log_s : -INFINITY;
+                const float x = row.one(token);
+                const bool on = (!row.mask || ((row.mask[token >> 5] >> (token & 31)) & 1)) && x > -INFINITY;
+                y = bad ? nan : on ? logp(x) : -INFINITY;
             }
             p.logprob[r * p.n_ids + i] = y;
         }
-        for (int i = tid; i < p.n_top; i += LP_THREADS) {
+        for (int i = tid; i < p.n_top; i += THREADS) {
             const bool there = i < n_best && !bad;
             p.top[r * p.n_top + i] = there ? (int32_t)~(uint32_t)best[i] : -1;
-            p.top_logprob[r * p.n_top + i] = bad ? nan : there ? from(of_order((uint32_t)(best[i] >> 32)), mine.x) - log_s : -INFINITY;
+            p.top_logprob[r * p.n_top + i] = bad ? nan : there ? logp(of_order((uint32_t)(best[i] >> 32))) : -INFINITY;
         }
         __syncthreads();  // (the next row uses the same shared memory)
     }
+}
+
+template <bool F16, int THREADS>
+static cudaError_t run_logprobs(const LogprobParams& p, int sms, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    // (no more CTAs than run at once: a row's end costs a CTA what its start costs the next)
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(p.n_rows * p.cut, std::max(1024 / THREADS * sms / p.cut, 1) * p.cut));
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.cut;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cut > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_logprobs<F16, THREADS>, p);
 }
 
 cudaError_t launch_logprobs(const LogitsDesc& d, int64_t n_rows, int n_vocab, const void* x, const int32_t* ids, int n_ids,
@@ -370,25 +480,16 @@ cudaError_t launch_logprobs(const LogitsDesc& d, int64_t n_rows, int n_vocab, co
     p.n_top = n_top;
     p.scale = d.scale;
     p.cap = d.cap;
-    // As many CTAs a row as the rows leave room for (two CTAs an SM), and each still has a thread's worth
-    // for all of its threads; whole: what a row's sums are does not depend on how many rows there are.
+    // CTAs of 128 threads for short rows, whose starts and ends they overlap, else of 512; as many a row as the rows
+    // leave room for, while each still has a turn for all of its threads.  (whole: what a row's sums are does not
+    // depend on how many rows there are.)
+    const int e = d.f16 ? 8 : 4, threads = n_vocab <= 128 * LP_PIECES * e * 4 ? 128 : 512;
+    const int64_t turn = (int64_t)threads * LP_PIECES * e;
     int cut = 1;
-    const int64_t hold = (int64_t)LP_THREADS * LP_HOLD;
-    while (cut < LP_CLUSTER && n_vocab > hold * cut && (whole || 2 * cut * n_rows <= 2 * (int64_t)sms)) cut *= 2;
+    while (cut < LP_CLUSTER && n_vocab > turn * cut && (whole || 2 * cut * n_rows <= 1024 / threads * (int64_t)sms)) cut *= 2;
     p.cut = cut;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(n_rows * cut, std::max(2 * sms / cut, 1) * cut));
-    cfg.blockDim = dim3(LP_THREADS);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cut;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cut > 1 ? 2 : 1;
-    return d.f16 ? cudaLaunchKernelEx(&cfg, k_logprobs<true>, p) : cudaLaunchKernelEx(&cfg, k_logprobs<false>, p);
+    if (threads == 128) return d.f16 ? run_logprobs<true, 128>(p, sms, s) : run_logprobs<false, 128>(p, sms, s);
+    return d.f16 ? run_logprobs<true, 512>(p, sms, s) : run_logprobs<false, 512>(p, sms, s);
 }
 
 }  // namespace syn

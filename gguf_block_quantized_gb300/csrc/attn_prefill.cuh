@@ -177,12 +177,6 @@ __device__ __forceinline__ __half2 expand_scale(uint32_t bits) {
     return *reinterpret_cast<__half2*>(&db);
 }
 
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // (starts that run backwards or past the call's tokens count as none)
 __device__ __forceinline__ int new_tokens(const int32_t* starts, int s, int n_tok) {
     const int a = starts[s], b = starts[s + 1];

@@ -46,7 +46,7 @@ struct LogprobParams {
     int* err;
     int64_t n_rows;
     int n_vocab, n_ids, n_top, cut;  // cut: CTAs of a row
-    float scale, cap;
+    float scale, cap, inv_cap;
 };
 
 // A number that grows with the value (no NaN), and back.
@@ -86,6 +86,9 @@ struct Row {
     const uint32_t* mask;
     int n, head, pieces;
 
+    __device__ __forceinline__ Row(const LogprobParams& p, int64_t r)
+        : at(static_cast<const uint8_t*>(p.x) + r * p.stride * (F16 ? 2 : 4)), mask(p.mask ? p.mask + r * p.mask_stride : nullptr),
+          n(p.n_vocab), head((int)(reinterpret_cast<uintptr_t>(at) & 15) / (F16 ? 2 : 4)), pieces((head + n + E - 1) / E) {}
     __device__ __forceinline__ float one(int64_t i) const {
         return F16 ? __half2float(reinterpret_cast<const __half*>(at)[i]) : reinterpret_cast<const float*>(at)[i];
     }
@@ -183,12 +186,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
 
     const int64_t rows_at_once = gridDim.x / p.cut;
     for (int64_t r = blockIdx.x / p.cut; r < p.n_rows; r += rows_at_once) {
-        Row<F16> row;
-        row.at = static_cast<const uint8_t*>(p.x) + r * p.stride * (F16 ? 2 : 4);
-        row.mask = p.mask ? p.mask + r * p.mask_stride : nullptr;
-        row.n = p.n_vocab;
-        row.head = (int)(reinterpret_cast<uintptr_t>(row.at) & 15) / (F16 ? 2 : 4);
-        row.pieces = (row.head + p.n_vocab + E - 1) / E;
+        const Row<F16> row(p, r);
         const int per = (row.pieces + p.cut - 1) / p.cut, begin = per * part, end = min(row.pieces, begin + per);
         // a turn: the CTA's next LP_PIECES * THREADS pieces; group: turns of a unit
         const int turns = max(0, (end - begin + LP_PIECES * THREADS - 1) / (LP_PIECES * THREADS)), group = (turns + LP_UNITS - 1) / LP_UNITS;
@@ -196,22 +194,29 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
         uint4 next[LP_PIECES];
 #pragma unroll
         for (int i = 0; i < LP_PIECES; i++) next[i] = row.load(piece_of(0, i), end);
-
         const float scale = p.scales ? p.scale * p.scales[r] : p.scale;
         const bool scale_ok = scale > 0.0f && scale < INFINITY;
         const float c = scale * LP_LOG2E;
-        auto capped = [&](float x) { return p.cap > 0.0f ? p.cap * tanhf(x / p.cap) : x; };
-        auto join = [&](const Sums& a, const Sums& b) {
-            Sums y;
-            y.x = max_nan(a.x, b.x);
-            const float z = capped(y.x);
-            // (2^-300 is 0, which keeps infinities out)
-            const float ga = a.s > 0.0f ? fminf(c * (z - capped(a.x)), 300.0f) : 0.0f, gb = b.s > 0.0f ? fminf(c * (z - capped(b.x)), 300.0f) : 0.0f;
-            const float fa = ex2(-ga), fb = ex2(-gb);
-            y.s = a.s * fa + b.s * fb;
-            y.t = (a.t - ga * a.s) * fa + (b.t - gb * b.s) * fb;
-            return y;
+        // cap*tanh(x/cap): up to half the cap x times a polynomial in (x/cap)^2, fitted on [0, 1/2] to 3e-7, past it
+        // cap - 2 cap/(1 + 2^(2 x log2(e)/cap)), which is as exact as that there (CUDA's tanhf: 17.0 us, not 14.7, for 61
+        // masked rows of 50257)
+        auto capped = [&](float x) {
+            if (!(p.cap > 0.0f)) return x;
+            const float y = x * p.inv_cap, q = y * y;
+            const float small = x * fmaf(q, fmaf(q, fmaf(q, -0.0444185817f, 0.131909124f), -0.333263761f), 0.999999464f);
+            const float large = fmaf(-2.0f * p.cap, rcp(1.0f + ex2(y * (2.0f * LP_LOG2E))), p.cap);
+            return fabsf(y) <= 0.5f ? small : large;
         };
+        // sums over a maximum of x0, as they are over one of x, which is not smaller (z: its capped value)
+        auto move_to = [&](float x0, float z, float& s, float& t) {
+            const float g = s > 0.0f ? fminf(c * (z - capped(x0)), 300.0f) : 0.0f, f = ex2(-g);  // (2^-300 is 0, which keeps infinities out)
+            t = (t - g * s) * f;
+            s *= f;
+        };
+        // a logit that is asked for, on its way while the row streams
+        const int asked = part == 0 && tid < p.n_ids ? p.ids[r * p.n_ids + tid] : -1;
+        const bool asked_on = asked >= 0 && asked < p.n_vocab && (!row.mask || ((row.mask[asked >> 5] >> (asked & 31)) & 1));
+        const float asked_x = asked_on ? row.one(asked) : -INFINITY;
 
         Sums mine{-INFINITY, 0.0f, 0.0f};
         float z0 = 0.0f, unit = -INFINITY;  // z0: that of mine.x
@@ -234,11 +239,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
             if (x == -INFINITY) continue;
             if (!(x <= mine.x)) {
                 mine.x = max_nan(mine.x, x);
-                const float z = capped(mine.x), g = fminf(c * (z - z0), 300.0f), f = ex2(-g);
-                if (mine.s > 0.0f) {
-                    mine.t = (mine.t - g * mine.s) * f;
-                    mine.s *= f;
-                }
+                const float z = capped(mine.x), g = mine.s > 0.0f ? fminf(c * (z - z0), 300.0f) : 0.0f, f = ex2(-g);
+                mine.t = (mine.t - g * mine.s) * f;
+                mine.s *= f;
                 z0 = z;
             }
             uint64_t s2 = 0, t2 = 0;
@@ -267,12 +270,24 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
         }
 
         // ---- the sums of the CTA ---------------------------------------------------------------
-        Sums sums = mine;
+        const uint32_t none = order_of(-INFINITY), nan_order = 0xffffffffu;
+        const uint32_t u = mine.x == mine.x ? order_of(mine.x + 0.0f) : nan_order;  // (-0 is 0)
+        {
+            const uint32_t wl = __reduce_min_sync(0xffffffffu, u > none ? u : nan_order), wh = __reduce_max_sync(0xffffffffu, u);
+            if (lane == 0) {
+                warp_lo[warp] = wl;
+                warp_hi[warp] = wh;
+            }
+            if (tid == 0) n_found = n_units = 0;
+        }
+        int n = __syncthreads_count(u > none);
+        uint32_t lo = __reduce_min_sync(0xffffffffu, warp_lo[lane % WARPS]), hi = __reduce_max_sync(0xffffffffu, warp_hi[lane % WARPS]);
+        Sums sums{hi == nan_order ? __int_as_float(0x7fffffff) : of_order(hi), mine.s, mine.t};
+        move_to(mine.x, capped(sums.x), sums.s, sums.t);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const Sums other{__shfl_xor_sync(0xffffffffu, sums.x, o), __shfl_xor_sync(0xffffffffu, sums.s, o),
-                             __shfl_xor_sync(0xffffffffu, sums.t, o)};
-            sums = lane & o ? join(other, sums) : join(sums, other);  // (the same order in both)
+            sums.s += __shfl_xor_sync(0xffffffffu, sums.s, o);
+            sums.t += __shfl_xor_sync(0xffffffffu, sums.t, o);
         }
         if (lane == 0) warp_sums[warp] = sums;
         // ---- the CTA's largest -----------------------------------------------------------------
@@ -281,22 +296,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
             for (int i = tid; i < n; i += THREADS) {
                 const uint64_t key = found[i];
                 int rank = 0;
+#pragma unroll 8
                 for (int j = 0; j < n; j++) rank += found[j] > key;
                 if (rank < p.n_top) best[rank] = key;
             }
         };
         int n_best = 0;
-        if (p.n_top > 0) {
+        if (p.n_top > 0 && hi != nan_order) {
             const int k = p.n_top;
-            const uint32_t none = order_of(-INFINITY), u = mine.x == mine.x ? order_of(mine.x + 0.0f) : none;  // (-0 is 0)
-            const uint32_t wl = __reduce_min_sync(0xffffffffu, u > none ? u : 0xffffffffu), wh = __reduce_max_sync(0xffffffffu, u);
-            if (lane == 0) {
-                warp_lo[warp] = wl;
-                warp_hi[warp] = wh;
-            }
-            if (tid == 0) n_found = n_units = 0;
-            int n = __syncthreads_count(u > none);
-            uint32_t lo = __reduce_min_sync(0xffffffffu, warp_lo[lane % WARPS]), hi = __reduce_max_sync(0xffffffffu, warp_hi[lane % WARPS]);
             while (lo < hi && n > 2 * k) {  // (n: how many reach lo; fewer than k reach hi + 1)
                 const uint32_t mid = lo + (hi - lo) / 2 + 1;
                 const int reach = __syncthreads_count(u >= mid);
@@ -323,7 +330,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
                             if (v[j] == least) first = row.token(piece_of(turn, i), j);
                     }
                 int a = -1, b = p.n_vocab - 1;  // (fewer than k are at most a; more than 2k at most b)
-                while (n > 2 * k) {
+                while (n > 2 * k && a + 1 < b) {
                     const int mid = a + (b - a) / 2;
                     const int reach = __syncthreads_count(first <= mid);
                     if (reach >= k) {
@@ -375,62 +382,63 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
             rank_found(n_found);
         }
         __syncthreads();
-        if (warp == 0) {
-            sums = warp_sums[lane % WARPS];
+        // (each warp for itself, in the same order)
+        sums = warp_sums[lane % WARPS];
 #pragma unroll
-            for (int o = WARPS / 2; o > 0; o >>= 1) {
-                const Sums other{__shfl_xor_sync(0xffffffffu, sums.x, o), __shfl_xor_sync(0xffffffffu, sums.s, o),
-                                 __shfl_xor_sync(0xffffffffu, sums.t, o)};
-                sums = lane & o ? join(other, sums) : join(sums, other);
-            }
+        for (int o = WARPS / 2; o > 0; o >>= 1) {
+            sums.s += __shfl_xor_sync(0xffffffffu, sums.s, o);
+            sums.t += __shfl_xor_sync(0xffffffffu, sums.t, o);
         }
         // ---- the row's -------------------------------------------------------------------------
         if (p.cut > 1) {
             auto cluster = cg::this_cluster();
             cluster.barrier_wait();
-            Sums* to_sums = cluster.map_shared_rank(sent_sums, 0);
-            int* to_n = cluster.map_shared_rank(sent_n, 0);
-            uint64_t* to = cluster.map_shared_rank(sent, 0);
             if (tid == 0) {
-                to_sums[part] = sums;
-                to_n[part] = n_best;
+                cluster.map_shared_rank(sent_sums, 0)[part] = sums;
+                cluster.map_shared_rank(sent_n, 0)[part] = n_best;
             }
-            if (tid < n_best) to[part * LP_TOP + tid] = best[tid];
+            if (tid < n_best) cluster.map_shared_rank(sent, 0)[part * LP_TOP + tid] = best[tid];
             cluster.sync();
-            if (part == 0) {
-                int at = 0;
-                for (int i = 0; i < p.cut; i++) {
-                    if (tid < sent_n[i]) found[at + tid] = sent[i * LP_TOP + tid];
-                    at += sent_n[i];
-                }
-                sums = sent_sums[0];
-                for (int i = 1; i < p.cut; i++) sums = join(sums, sent_sums[i]);
-                if (r + rows_at_once < p.n_rows) cluster.barrier_arrive();  // (what was sent has been read)
-                __syncthreads();
-                rank_found(at);
-                n_best = min(at, p.n_top);
-            } else {
+            if (part > 0) {
                 if (r + rows_at_once < p.n_rows) cluster.barrier_arrive();
                 continue;
             }
+            sums = sent_sums[lane % p.cut];
+            float x = sums.x;
+            for (int o = p.cut / 2; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
+            move_to(sums.x, capped(x), sums.s, sums.t);
+            sums.x = x;
+            for (int o = p.cut / 2; o > 0; o >>= 1) {
+                sums.s += __shfl_xor_sync(0xffffffffu, sums.s, o);
+                sums.t += __shfl_xor_sync(0xffffffffu, sums.t, o);
+            }
+            if (p.n_top > 0) {
+                int at = 0;
+                for (int i = 0; i < p.cut; i++) {
+                    const int m = sent_n[i];
+                    if (tid < m) found[at + tid] = sent[i * LP_TOP + tid];
+                    at += m;
+                }
+                __syncthreads();
+                rank_found(at);
+                n_best = min(at, p.n_top);
+                __syncthreads();
+            }
+            if (r + rows_at_once < p.n_rows) cluster.barrier_arrive();  // (what was sent has been read)
         }
-        if (tid == 0) warp_sums[0] = sums;
-        __syncthreads();
-        sums = warp_sums[0];
         const bool bad = !(sums.x < INFINITY) || !scale_ok;  // NaN or infinite logits, a scale that is none
         const float nan = __int_as_float(0x7fffffff), row_z = capped(sums.x), log_s = sums.s > 0.0f ? log2f(sums.s) : 0.0f;
         auto logp = [&](float x) { return LP_LN2 * (c * (capped(x) - row_z) - log_s); };
         if (tid == 0 && p.entropy) p.entropy[r] = bad ? nan : sums.s > 0.0f ? LP_LN2 * (log_s - sums.t / sums.s) : 0.0f;
-        for (int i = tid; i < p.n_ids; i += THREADS) {
-            const int token = p.ids[r * p.n_ids + i];
-            float y = 0.0f;
+        auto tell = [&](int i, int token, float x) {
             if (token >= p.n_vocab) record_error(p.err, SYN_DEVERR_BOUNDS);
-            else if (token >= 0) {
-                const float x = row.one(token);
-                const bool on = (!row.mask || ((row.mask[token >> 5] >> (token & 31)) & 1)) && x > -INFINITY;
-                y = bad ? nan : on ? logp(x) : -INFINITY;
-            }
-            p.logprob[r * p.n_ids + i] = y;
+            p.logprob[r * p.n_ids + i] = token < 0 || token >= p.n_vocab ? 0.0f : bad ? nan : x == -INFINITY ? -INFINITY : logp(x);
+        };
+        if (tid < p.n_ids) tell(tid, asked, asked_x);
+        for (int i = tid + THREADS; i < p.n_ids; i += THREADS) {
+            const int token = p.ids[r * p.n_ids + i];
+            const bool on = token >= 0 && token < p.n_vocab && (!row.mask || ((row.mask[token >> 5] >> (token & 31)) & 1));
+            tell(i, token, on ? row.one(token) : -INFINITY);
         }
         for (int i = tid; i < p.n_top; i += THREADS) {
             const bool there = i < n_best && !bad;
@@ -480,14 +488,18 @@ cudaError_t launch_logprobs(const LogitsDesc& d, int64_t n_rows, int n_vocab, co
     p.n_top = n_top;
     p.scale = d.scale;
     p.cap = d.cap;
-    // CTAs of 128 threads for short rows, whose starts and ends they overlap, else of 512; as many a row as the rows
-    // leave room for, while each still has a turn for all of its threads.  (whole: what a row's sums are does not
+    p.inv_cap = d.cap > 0.0f ? std::min(1.0f / d.cap, 1e38f) : 0.0f;  // (finite: a logit of 0 stays 0)
+    // An SM holds 1024 threads: four CTAs of 256, so that others stream while one is at a row's end (600 rows of
+    // 128256 fp32 logits 52.4 us, with two of 512 56.0, with eight of 128 54.7; 4095 fp16 rows 202, 240 and 204), eight of 128
+    // for short rows, one of 512 where a few rows leave SMs idle (one row 8.8 us, with 256 9.4, with 128 13.2).  As many CTAs a
+    // row as the rows leave room for, while each still has a turn for all of its threads.  (whole: what a row's sums are does not
     // depend on how many rows there are.)
-    const int e = d.f16 ? 8 : 4, threads = n_vocab <= 128 * LP_PIECES * e * 4 ? 128 : 512;
+    const int e = d.f16 ? 8 : 4, threads = n_vocab <= 128 * LP_PIECES * e * 4 ? 128 : !whole && LP_CLUSTER * n_rows <= sms ? 512 : 256;
     const int64_t turn = (int64_t)threads * LP_PIECES * e;
     int cut = 1;
     while (cut < LP_CLUSTER && n_vocab > turn * cut && (whole || 2 * cut * n_rows <= 1024 / threads * (int64_t)sms)) cut *= 2;
     p.cut = cut;
+    if (threads == 256) return d.f16 ? run_logprobs<true, 256>(p, sms, s) : run_logprobs<false, 256>(p, sms, s);
     if (threads == 128) return d.f16 ? run_logprobs<true, 128>(p, sms, s) : run_logprobs<false, 128>(p, sms, s);
     return d.f16 ? run_logprobs<true, 512>(p, sms, s) : run_logprobs<false, 512>(p, sms, s);
 }

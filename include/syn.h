@@ -594,7 +594,7 @@ typedef struct {
  * shape; a negative id asks for nothing and gets 0, one past the vocabulary 0 and SYN_ERR_BOUNDS); entropy (n_rows, or NULL), in nats; the n_top
  * (0 to 64) allowed tokens of the largest logits, in order, ties to the lower token: top and top_logprob (n_rows x
  * n_top); where fewer are allowed, -1 and -inf.  Sums are fp32 over a running maximum; every result is
- * exact to about 1e-6 of the larger of 1 and its own size, capped logits to 1e-7 * cap * scale.  Logits may start
+ * exact to about 1e-6 of the larger of 1 and its own size, capped logits to 5e-7 * cap * scale.  Logits may start
  * anywhere their type may; 16-byte aligned rows load fastest.  Asynchronous.  (In deterministic mode a row's results do not
  * depend on the number of rows.)  SYN_ERR_TYPE, SYN_ERR_SHAPE (n_vocab up to 2^30, n_ids up to 65536), SYN_ERR_NULL,
  * SYN_ERR_ALIGN. */

@@ -5,8 +5,8 @@ powers at a time, then pieces, threads and CTAs join: fewer than 64 additions in
 positive numbers, and each power is off by 2^-22 and by what its exponent's rounding gives (|d| e^d <= 1/e): ln S is off by less
 than 2^-17, S's own rounding included, at the largest vocabularies here.  So a log probability is off by at
 most 2^-17 + 2^-22 |logp|, the entropy by as much for ln S and 2^-17 of T/S (whose terms add up in the same
-way).  A cap's tanhf is off by 2^-22 of itself at most, and its product by 2^-24: 2^-21 cap scale for a z, twice that for a
-difference of two, which moves ln S by as much.
+way).  A capped logit is off by 2^-21 of the cap at most (tanh to 3e-7, its rounding), a difference of two by twice that,
+which moves ln S by as much.
 """
 import numpy as np
 import pytest

@@ -485,9 +485,172 @@ __global__ void __launch_bounds__(CMP_THREADS) k_kv_compact(const CompactParams 
     }
 }
 
+// Long lists: a chunk of rows (all of its heads' tiles, or a group of them) is a CTA's.  Chunks are taken in
+// order, by a counter; each loads its rows, says so, and stores them once every chunk of its sequence before it has
+// loaded its own: those hold whatever it overwrites.  A chunk thus waits for chunks that were taken
+// before it and that wait for nothing before they say so.  It looks back over the flags, 256 at a time, to one
+// that says that all up to there have loaded.
+
+struct LongParams {
+    CompactParams m;
+    int* next;   // the next chunk to be taken; zero before the call
+    int* flags;  // [groups][chunks] 0; 1: loaded; 2: all up to it have; zero before the call
+    int chunks, chunk_rows, groups, group_tiles;
+};
+
+template <typename S>
+__global__ void __launch_bounds__(CMP_THREADS, 4) k_kv_compact_long(const LongParams q) {
+    const CompactParams& p = q.m;
+    __shared__ int64_t src[CMP_ROWS], dst[CMP_ROWS];  // slots; -1: the row stays
+    __shared__ int taken, first_seq, gave_up;
+    const int tid = threadIdx.x, shift = p.c.page_shift;
+    griddep_release();
+    griddep_wait();
+    const int64_t held = min(p.max_pages << shift, (int64_t)INT_MAX), cell_mask = (int64_t(1) << shift) - 1;
+    const int n16 = p.c.dim >> (p.c.q8 ? 4 : 3), ns = p.c.q8 ? (p.c.dim >> 4) / (int)sizeof(S) : 0;  // units of a row of a tile
+    if (tid == 0) gave_up = 0;
+    // the lengths
+    for (int s = blockIdx.x * CMP_THREADS + tid; s < p.n_seq; s += gridDim.x * CMP_THREADS) {
+        const int a = p.starts[s], b = p.starts[s + 1], n = a < 0 || b > p.n_rows ? 0 : max(b - a, 0);
+        p.new_lens[s] = (int)min((int64_t)max(p.base[s], 0) + n, (int64_t)INT_MAX);
+    }
+    while (true) {
+        __syncthreads();
+        if (tid == 0) taken = atomicAdd(q.next, 1);
+        __syncthreads();
+        if (taken >= q.chunks * q.groups || gave_up) return;
+        const int chunk = taken / q.groups, group = taken % q.groups, r0 = chunk * q.chunk_rows;
+        const int m = min(q.chunk_rows, (int)p.n_rows - r0);
+        bool moves = false;
+        for (int i = tid; i < m; i += CMP_THREADS) {
+            const int r = r0 + i;
+            int lo = 0, hi = p.n_seq;  // the last sequence that starts at r or before it
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (p.starts[mid] <= r) lo = mid;
+                else hi = mid;
+            }
+            if (i == 0) first_seq = lo;
+            const int a = p.starts[lo], b = p.starts[lo + 1], at = r - a;
+            int64_t from = -1, to = -1;
+            if (a >= 0 && at >= 0 && b <= p.n_rows && r < b) {
+                const int row = p.rows[r], base = max(p.base[lo], 0);
+                if (row != at) {
+                    auto slot_of = [&](int64_t x) -> int64_t {
+                        if (x >= held) return -1;
+                        const int id = p.pages[(int64_t)lo * p.max_pages + (x >> shift)];
+                        return (unsigned)id < (unsigned)p.c.n_pages ? ((int64_t)id << shift) + (x & cell_mask) : -1;
+                    };
+                    if (row > at && (at == 0 || p.rows[r - 1] < row)) {
+                        from = slot_of((int64_t)base + row);
+                        to = slot_of((int64_t)base + at);
+                    }
+                    if (to >= 0 && p.refs && p.refs[to >> shift] > 1) to = -1;
+                    if (from < 0 || to < 0) {
+                        from = -1;
+                        record_error(p.err, SYN_DEVERR_BOUNDS);
+                    }
+                }
+            }
+            moves |= from >= 0;
+            src[i] = from;
+            dst[i] = to;
+        }
+        moves = __syncthreads_or(moves);
+        // unit u of the chunk's: a row, a tile, a piece of it
+        const int tile0 = group * q.group_tiles, tiles = min(q.group_tiles, 2 * p.c.n_kv - tile0);
+        auto place = [&](const int64_t* slots, int u, int per_tile, int64_t plane, int pitch, int size) -> uint8_t* {
+            const int row = u / (tiles * per_tile), x = u - row * tiles * per_tile, t = x / per_tile, tile = tile0 + t;
+            const int64_t slot = slots[row];
+            if (src[row] < 0) return nullptr;
+            return (tile & 1 ? p.c.v : p.c.k) + (slot >> shift) * p.c.page_stride + (tile >> 1) * p.c.tile + plane + (slot & cell_mask) * pitch +
+                   (x - t * per_tile) * size;
+        };
+        const int units = moves ? m * tiles * n16 : 0, s_units = moves ? m * tiles * ns : 0;
+        const int64_t scales = (int64_t)p.c.dim << shift;
+        uint4 w[CMP_UNITS];
+        S ws[2];
+#pragma unroll
+        for (int i = 0; i < CMP_UNITS; i++) {
+            const int u = i * CMP_THREADS + tid;
+            const uint8_t* a = u < units ? place(src, u, n16, 0, n16 * 16, 16) : nullptr;
+            if (a) w[i] = *reinterpret_cast<const uint4*>(a);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const int u = i * CMP_THREADS + tid;
+            const uint8_t* a = u < s_units ? place(src, u, ns, scales, p.c.dim >> 4, sizeof(S)) : nullptr;
+            if (a) ws[i] = *reinterpret_cast<const S*>(a);
+        }
+        __threadfence();
+        __syncthreads();
+        int* flags = q.flags + (int64_t)group * q.chunks;
+        const int stop = max(p.starts[first_seq], 0) / q.chunk_rows;  // the sequence's first chunk
+        const bool alone = stop >= chunk;
+        if (tid == 0) atomicExch(flags + chunk, alone ? 2 : 1);
+        if (!alone && moves) {
+            for (int end = chunk;;) {  // flags [end - 256, end) next
+                const int j = end - 1 - tid;
+                int state = 2;
+                if (j >= stop) {
+                    const long long t0 = clock64();
+                    while ((state = *reinterpret_cast<volatile int*>(flags + j)) == 0)
+                        if (clock64() - t0 > SYN_WAIT_CYCLES) {
+                            record_error(p.err, SYN_DEVERR_TIMEOUT);
+                            gave_up = 1;
+                            break;
+                        }
+                }
+                end -= CMP_THREADS;
+                if (__syncthreads_or(state == 2)) break;
+            }
+            __threadfence();
+            if (gave_up) return;
+            if (tid == 0) atomicExch(flags + chunk, 2);
+        }
+#pragma unroll
+        for (int i = 0; i < CMP_UNITS; i++) {
+            const int u = i * CMP_THREADS + tid;
+            uint8_t* b = u < units ? place(dst, u, n16, 0, n16 * 16, 16) : nullptr;
+            if (b) *reinterpret_cast<uint4*>(b) = w[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const int u = i * CMP_THREADS + tid;
+            uint8_t* b = u < s_units ? place(dst, u, ns, scales, p.c.dim >> 4, sizeof(S)) : nullptr;
+            if (b) *reinterpret_cast<S*>(b) = ws[i];
+        }
+    }
+}
+
+// Rows from which a list counts as long.
+constexpr int64_t CMP_LONG = 4096;
+
+// How a long list is cut: 16-byte units (and 2-byte to 8-byte ones of scales) that a CTA holds at once.
+static int64_t cut_long(const KvCache& c, int64_t n_rows, LongParams* q) {
+    const int n16 = c.dim >> (c.q8 ? 4 : 3), ns = c.q8 ? (c.dim >> 4) / (c.dim % 128 == 0 ? 8 : c.dim % 64 == 0 ? 4 : 2) : 0;
+    const int most = CMP_THREADS * CMP_UNITS, most_s = CMP_THREADS * 2;
+    int tiles = std::min(2 * c.n_kv, most / n16);
+    if (ns) tiles = std::min(tiles, most_s / ns);
+    int rows = most / (tiles * n16);
+    if (ns) rows = std::min(rows, most_s / (tiles * ns));
+    q->group_tiles = tiles;
+    q->groups = (2 * c.n_kv + tiles - 1) / tiles;
+    q->chunk_rows = std::min(rows, CMP_ROWS);
+    q->chunks = (int)((n_rows + q->chunk_rows - 1) / q->chunk_rows);
+    return (int64_t)q->chunks * q->groups;
+}
+
+int64_t compact_scratch_words(const KvCache& c, int64_t n_rows) {
+    if (n_rows < CMP_LONG) return 0;
+    LongParams q;
+    const int64_t n = cut_long(c, n_rows, &q);
+    return n < INT_MAX ? n + 1 : -1;
+}
+
 cudaError_t launch_kv_compact(const KvCache& c, const int32_t* refs, int64_t n_seq, int64_t n_rows, const int32_t* pages,
                               int64_t max_pages, const int32_t* base, const int32_t* starts, const int32_t* rows,
-                              int32_t* new_lens, int* err, int sms, cudaStream_t s) {
+                              int32_t* new_lens, int* scratch, int* err, int sms, int* launches, cudaStream_t s) {
     CompactParams p;
     p.c = c;
     p.refs = refs;
@@ -500,14 +663,31 @@ cudaError_t launch_kv_compact(const KvCache& c, const int32_t* refs, int64_t n_s
     p.max_pages = max_pages;
     p.n_rows = n_rows;
     p.n_seq = (int)n_seq;
-    // columns of at least 32 bytes of a row (a sector), as many as it takes to fill the SMs
-    const int pieces = c.dim >> (c.q8 ? 4 : 3);
-    int width = pieces;
-    while (width > 2 && n_seq * 2 * c.n_kv * ((pieces + width - 1) / width) < 4 * (int64_t)sms) width = (width + 1) / 2;
-    p.width = width;
-    p.cut = (pieces + width - 1) / width;
-    return launch_overlapped(k_kv_compact, (int)std::min<int64_t>(n_seq * 2 * c.n_kv * (p.cut + c.q8), (int64_t)sms * 8),
-                             CMP_THREADS, 0, s, p);
+    cudaError_t e;
+    if (n_rows >= CMP_LONG) {
+        LongParams q;
+        q.m = p;
+        const int64_t n = cut_long(c, n_rows, &q);
+        q.next = scratch;
+        q.flags = scratch + 1;
+        e = cudaMemsetAsync(scratch, 0, (size_t)(n + 1) * 4, s);
+        if (e != cudaSuccess) return e;
+        auto kern = c.dim % 128 == 0 ? k_kv_compact_long<uint2> : c.dim % 64 == 0 ? k_kv_compact_long<uint32_t> : k_kv_compact_long<uint16_t>;
+        const int grid = (int)std::min<int64_t>(n, (int64_t)sms * 4);
+        kern<<<grid, CMP_THREADS, 0, s>>>(q);
+        e = cudaGetLastError();
+    } else {
+        // columns of at least 32 bytes of a row (a sector), as many as it takes to fill the SMs
+        const int pieces = c.dim >> (c.q8 ? 4 : 3);
+        int width = pieces;
+        while (width > 2 && n_seq * 2 * c.n_kv * ((pieces + width - 1) / width) < 4 * (int64_t)sms) width = (width + 1) / 2;
+        p.width = width;
+        p.cut = (pieces + width - 1) / width;
+        e = launch_overlapped(k_kv_compact, (int)std::min<int64_t>(n_seq * 2 * c.n_kv * (p.cut + c.q8), (int64_t)sms * 8),
+                              CMP_THREADS, 0, s, p);
+    }
+    if (e == cudaSuccess) ++*launches;
+    return e;
 }
 
 // ---- copy --------------------------------------------------------------------------------

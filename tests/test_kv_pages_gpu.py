@@ -310,3 +310,61 @@ def test_captured(syn):
             same(d_pages, pages, i)
             same(d_refs, refs, i)
             same(d_lens, lens, i)
+
+
+@pytest.mark.parametrize("t,kv,dim,page", [(F16, 1, 64, 8), (F16, 2, 160, 64), (Q8_0, 3, 96, 16), (Q8_0, 2, 128, 32), (Q8_0, 1, 64, 8),
+                                           (F16, 9, 256, 16)])
+def test_compact_of_long_lists(syn, t, kv, dim, page):
+    """Lists that many CTAs share: nearly all rows kept, few, runs that stay, sequences of one row between long ones."""
+    rng = np.random.default_rng([t, kv, dim])
+    lens = [1, 9000, 3, 0, 4100, 1, 300, 5000]
+    need = [-(-n // page) for n in lens]
+    n_pages, width = sum(need), max(need)
+    cache = make_cache(syn, t, kv, dim, page, n_pages, 11)
+    table = np.full((len(lens), width), -1, np.int32)
+    order, at = rng.permutation(n_pages), 0
+    for s, m in enumerate(need):
+        table[s, :m] = order[at:at + m]
+        at += m
+    refs = counts(n_pages, table)
+    for kind in ("most", "half", "gap", "late"):
+        rows = []
+        for n in lens:
+            if kind == "most":
+                keep = rng.random(n) < 0.999
+            elif kind == "half":
+                keep = rng.random(n) < 0.5
+            elif kind == "gap":  # all but the first: every row moves down by one
+                keep = np.arange(n) != 0
+            else:  # the first stay where they are
+                keep = (np.arange(n) < n // 2) | (rng.random(n) < 0.3)
+            rows.append(np.nonzero(keep)[0])
+        starts = np.concatenate([[0], np.cumsum([len(r) for r in rows])])
+        assert starts[-1] > 4096
+        want = planes(cache, dim, page)
+        for x in want:
+            for s, r in enumerate(rows):
+                to = np.arange(len(r))
+                x[table[s, to // page], :, to % page] = x[table[s, r // page], :, r % page]
+        got = syn.kv_compact(cache, dev(refs), dev(table), dev(np.zeros(len(lens))), dev(starts), dev(np.concatenate(rows)))
+        same(got, np.diff(starts), kind)
+        for x, y in zip(planes(cache, dim, page), want):
+            assert np.array_equal(x, y), kind
+    # again with few SMs, and bad rows in the middle
+    old = syn.set_sm_limit(1)
+    try:
+        want = planes(cache, dim, page)
+        rows = np.arange(1, 5000)
+        rows[3000] = 1
+        bad = rows.copy()
+        ok = np.ones(len(rows), bool)
+        ok[3000] = False
+        for x in want:
+            to = np.arange(len(rows))[ok]
+            x[table[1, to // page], :, to % page] = x[table[1, rows[ok] // page], :, rows[ok] % page]
+        syn.kv_compact(cache, dev(refs), dev(table[1:2]), dev([0]), dev([0, len(rows)]), dev(bad))
+        assert syn.device_status() == syn.ERR_BOUNDS
+        for x, y in zip(planes(cache, dim, page), want):
+            assert np.array_equal(x, y)
+    finally:
+        syn.set_sm_limit(old)

@@ -390,8 +390,11 @@ cudaError_t launch_kv_extend(const KvCache& c, int32_t* refs, int64_t n_seq, int
 // that it or a batch before has loaded, so no CTA waits for another.
 
 constexpr int CMP_THREADS = 256;
-constexpr int CMP_ROWS = 512;   // rows of a batch
+constexpr int CMP_ROWS = 256;   // rows of a batch
+constexpr int CMP_CHUNK = 64;   // most rows of a chunk of a long list
 constexpr int CMP_UNITS = 8;    // pieces a thread holds
+constexpr int CMP_SCALES = 4;   // and pieces of scales
+constexpr int CMP_CTAS = 4;     // of an SM, for long lists
 
 struct CompactParams {
     KvCache c;
@@ -486,41 +489,42 @@ __global__ void __launch_bounds__(CMP_THREADS) k_kv_compact(const CompactParams 
 }
 
 // Long lists: a chunk of rows (all of its heads' tiles, or a group of them) is a CTA's.  Chunks are taken in
-// order, by a counter; each loads its rows, says so, and stores them once every chunk of its sequence before it has
-// loaded its own: those hold whatever it overwrites.  A chunk thus waits for chunks that were taken
-// before it and that wait for nothing before they say so.  It looks back over the flags, 256 at a time, to one
-// that says that all up to there have loaded.
+// order, by a counter; each loads its rows, says so, and stores them once the chunks whose rows lie where it
+// stores (one or two, found by a search in the ascending list while the loads are on their way) have loaded
+// theirs.  Those chunks are not after it, and wait for nothing before they say so: every wait ends.
 
 struct LongParams {
     CompactParams m;
     int* next;   // the next chunk to be taken; zero before the call
-    int* flags;  // [groups][chunks] 0; 1: loaded; 2: all up to it have; zero before the call
+    int* flags;  // [groups][chunks] 1: loaded; zero before the call
     int chunks, chunk_rows, groups, group_tiles;
 };
 
 template <typename S>
-__global__ void __launch_bounds__(CMP_THREADS, 4) k_kv_compact_long(const LongParams q) {
+__global__ void __launch_bounds__(CMP_THREADS, CMP_CTAS) k_kv_compact_long(const LongParams q) {
     const CompactParams& p = q.m;
-    __shared__ int64_t src[CMP_ROWS], dst[CMP_ROWS];  // slots; -1: the row stays
-    __shared__ int taken, first_seq, gave_up;
-    const int tid = threadIdx.x, shift = p.c.page_shift;
+    __shared__ int64_t src[2][CMP_CHUNK], dst[2][CMP_CHUNK];      // where a row's values are in a pool's tile 0; -1: the row stays
+    __shared__ int64_t src_s[2][CMP_CHUNK], dst_s[2][CMP_CHUNK];  // (Q8_0) its scales
+    __shared__ int taken[2], first_seq[2], gave_up;
+    extern __shared__ uint4 pieces[];  // [CMP_UNITS][CMP_THREADS] on their way, each thread's its own
+    uint4* held16 = pieces + threadIdx.x;
+    const int tid = threadIdx.x, shift = p.c.page_shift, total = q.chunks * q.groups;
     griddep_release();
     griddep_wait();
     const int64_t held = min(p.max_pages << shift, (int64_t)INT_MAX), cell_mask = (int64_t(1) << shift) - 1;
     const int n16 = p.c.dim >> (p.c.q8 ? 4 : 3), ns = p.c.q8 ? (p.c.dim >> 4) / (int)sizeof(S) : 0;  // units of a row of a tile
-    if (tid == 0) gave_up = 0;
+    if (tid == 0) {
+        gave_up = 0;
+        taken[0] = atomicAdd(q.next, 1);
+    }
     // the lengths
     for (int s = blockIdx.x * CMP_THREADS + tid; s < p.n_seq; s += gridDim.x * CMP_THREADS) {
         const int a = p.starts[s], b = p.starts[s + 1], n = a < 0 || b > p.n_rows ? 0 : max(b - a, 0);
         p.new_lens[s] = (int)min((int64_t)max(p.base[s], 0) + n, (int64_t)INT_MAX);
     }
-    while (true) {
-        __syncthreads();
-        if (tid == 0) taken = atomicAdd(q.next, 1);
-        __syncthreads();
-        if (taken >= q.chunks * q.groups || gave_up) return;
-        const int chunk = taken / q.groups, group = taken % q.groups, r0 = chunk * q.chunk_rows;
-        const int m = min(q.chunk_rows, (int)p.n_rows - r0);
+    // the slots of the chunk taken[x], into src[x] and dst[x]; whether a row of it moves
+    auto find_slots = [&](int x) {
+        const int r0 = taken[x] / q.groups * q.chunk_rows, m = min(q.chunk_rows, (int)p.n_rows - r0);
         bool moves = false;
         for (int i = tid; i < m; i += CMP_THREADS) {
             const int r = r0 + i;
@@ -530,18 +534,18 @@ __global__ void __launch_bounds__(CMP_THREADS, 4) k_kv_compact_long(const LongPa
                 if (p.starts[mid] <= r) lo = mid;
                 else hi = mid;
             }
-            if (i == 0) first_seq = lo;
+            if (i == 0) first_seq[x] = lo;
             const int a = p.starts[lo], b = p.starts[lo + 1], at = r - a;
             int64_t from = -1, to = -1;
             if (a >= 0 && at >= 0 && b <= p.n_rows && r < b) {
-                const int row = p.rows[r], base = max(p.base[lo], 0);
+                const int row = p.rows[r], before = at ? p.rows[r - 1] : -1, base = max(p.base[lo], 0);
                 if (row != at) {
-                    auto slot_of = [&](int64_t x) -> int64_t {
-                        if (x >= held) return -1;
-                        const int id = p.pages[(int64_t)lo * p.max_pages + (x >> shift)];
-                        return (unsigned)id < (unsigned)p.c.n_pages ? ((int64_t)id << shift) + (x & cell_mask) : -1;
+                    auto slot_of = [&](int64_t y) -> int64_t {
+                        if (y >= held) return -1;
+                        const int id = p.pages[(int64_t)lo * p.max_pages + (y >> shift)];
+                        return (unsigned)id < (unsigned)p.c.n_pages ? ((int64_t)id << shift) + (y & cell_mask) : -1;
                     };
-                    if (row > at && (at == 0 || p.rows[r - 1] < row)) {
+                    if (row > at && before < row) {
                         from = slot_of((int64_t)base + row);
                         to = slot_of((int64_t)base + at);
                     }
@@ -553,90 +557,107 @@ __global__ void __launch_bounds__(CMP_THREADS, 4) k_kv_compact_long(const LongPa
                 }
             }
             moves |= from >= 0;
-            src[i] = from;
-            dst[i] = to;
+            const int64_t pitch = p.c.dim * (p.c.q8 ? 1 : 2), scales = (int64_t)p.c.dim << shift;
+            const int64_t from0 = (from >> shift) * p.c.page_stride, to0 = (to >> shift) * p.c.page_stride;
+            src[x][i] = from < 0 ? -1 : from0 + (from & cell_mask) * pitch;
+            dst[x][i] = to0 + (to & cell_mask) * pitch;
+            src_s[x][i] = from0 + scales + (from & cell_mask) * (p.c.dim >> 4);
+            dst_s[x][i] = to0 + scales + (to & cell_mask) * (p.c.dim >> 4);
         }
-        moves = __syncthreads_or(moves);
-        // unit u of the chunk's: a row, a tile, a piece of it
+        return __syncthreads_or(moves) != 0;
+    };
+    __syncthreads();
+    if (taken[0] >= total) return;
+    bool moves = find_slots(0);
+    for (int x = 0;; x ^= 1) {
+        const int chunk = taken[x] / q.groups, group = taken[x] % q.groups, r0 = chunk * q.chunk_rows;
+        const int m = min(q.chunk_rows, (int)p.n_rows - r0);
+        // this thread's piece of a row (one 16 bytes of a tile), and the rows it takes: tid / u16, then every per16-th
         const int tile0 = group * q.group_tiles, tiles = min(q.group_tiles, 2 * p.c.n_kv - tile0);
-        auto place = [&](const int64_t* slots, int u, int per_tile, int64_t plane, int pitch, int size) -> uint8_t* {
-            const int row = u / (tiles * per_tile), x = u - row * tiles * per_tile, t = x / per_tile, tile = tile0 + t;
-            const int64_t slot = slots[row];
-            if (src[row] < 0) return nullptr;
-            return (tile & 1 ? p.c.v : p.c.k) + (slot >> shift) * p.c.page_stride + (tile >> 1) * p.c.tile + plane + (slot & cell_mask) * pitch +
-                   (x - t * per_tile) * size;
-        };
-        const int units = moves ? m * tiles * n16 : 0, s_units = moves ? m * tiles * ns : 0;
-        const int64_t scales = (int64_t)p.c.dim << shift;
-        uint4 w[CMP_UNITS];
-        S ws[2];
+        const int u16 = tiles * n16, us = tiles * ns, per16 = CMP_THREADS / u16, per_s = us ? CMP_THREADS / us : 1;
+        const int row16 = tid / u16, t16 = (tid - row16 * u16) / n16, row_s = us ? tid / us : 0, t_s = us ? (tid - row_s * us) / ns : 0;
+        uint8_t* at16 = ((tile0 + t16) & 1 ? p.c.v : p.c.k) + ((tile0 + t16) >> 1) * p.c.tile + (tid - row16 * u16 - t16 * n16) * 16;
+        uint8_t* at_s = ((tile0 + t_s) & 1 ? p.c.v : p.c.k) + ((tile0 + t_s) >> 1) * p.c.tile + (tid - row_s * us - t_s * ns) * (int)sizeof(S);
+        const int end16 = moves && row16 < per16 ? m : 0, end_s = moves && us && row_s < per_s ? m : 0;
+        S ws[CMP_SCALES];
 #pragma unroll
         for (int i = 0; i < CMP_UNITS; i++) {
-            const int u = i * CMP_THREADS + tid;
-            const uint8_t* a = u < units ? place(src, u, n16, 0, n16 * 16, 16) : nullptr;
-            if (a) w[i] = *reinterpret_cast<const uint4*>(a);
+            const int r = row16 + i * per16;
+            if (r < end16 && src[x][r] >= 0) cp16_all(smem_u32(held16 + i * CMP_THREADS), at16 + src[x][r]);
         }
+        cp_commit();
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const int u = i * CMP_THREADS + tid;
-            const uint8_t* a = u < s_units ? place(src, u, ns, scales, p.c.dim >> 4, sizeof(S)) : nullptr;
-            if (a) ws[i] = *reinterpret_cast<const S*>(a);
+        for (int i = 0; i < CMP_SCALES; i++) {
+            const int r = row_s + i * per_s;
+            if (r < end_s && src[x][r] >= 0) ws[i] = *reinterpret_cast<const S*>(at_s + src_s[x][r]);
+        }
+        if (tid == 0) taken[x ^ 1] = atomicAdd(q.next, 1);
+        // the chunks [c0, c1) that hold what lies at the places of this one's rows of its first sequence (those
+        // of sequences that begin in it are its own)
+        const int a = max(p.starts[first_seq[x]], 0), b = min(max(p.starts[first_seq[x] + 1], a), (int)p.n_rows);
+        int c0 = 0, c1 = 0;
+        if (moves && a < r0) {
+            const int place = r0 - a;
+            int lo = a, n = min(r0 + m, b) - a;  // (a row is not before its place: none after this chunk)
+            while (n > 0) {  // the list's first row that is not below the first place
+                const int step = (n + CMP_THREADS - 1) / CMP_THREADS, at = lo + tid * step;
+                const int below = __syncthreads_count(tid * step < n && p.rows[at] < place);
+                // rows lo + step * (below - 1) and before are below; row lo + step * below is not
+                if (below == 0) break;
+                lo += (below - 1) * step + 1;
+                n = min(step - 1, max(n - ((below - 1) * step + 1), 0));
+            }
+            c0 = lo / q.chunk_rows;
+            c1 = min((lo + m + q.chunk_rows - 1) / q.chunk_rows, chunk);  // (at most m rows lie at m places)
+        }
+        cp_wait<0>();
+        __threadfence();  // (what was loaded is loaded)
+        __syncthreads();
+        int* flags = q.flags + (int64_t)group * q.chunks;
+        if (tid == 0) atomicExch(flags + chunk, 1);
+        const bool more = taken[x ^ 1] < total;
+        const bool moves_next = more && find_slots(x ^ 1);
+        for (int j = c0 + tid; j < c1; j += CMP_THREADS) {
+            const long long t0 = clock64();
+            while (*reinterpret_cast<volatile int*>(flags + j) == 0)
+                if (clock64() - t0 > SYN_WAIT_CYCLES) {
+                    record_error(p.err, SYN_DEVERR_TIMEOUT);
+                    gave_up = 1;
+                    break;
+                }
         }
         __threadfence();
         __syncthreads();
-        int* flags = q.flags + (int64_t)group * q.chunks;
-        const int stop = max(p.starts[first_seq], 0) / q.chunk_rows;  // the sequence's first chunk
-        const bool alone = stop >= chunk;
-        if (tid == 0) atomicExch(flags + chunk, alone ? 2 : 1);
-        if (!alone && moves) {
-            for (int end = chunk;;) {  // flags [end - 256, end) next
-                const int j = end - 1 - tid;
-                int state = 2;
-                if (j >= stop) {
-                    const long long t0 = clock64();
-                    while ((state = *reinterpret_cast<volatile int*>(flags + j)) == 0)
-                        if (clock64() - t0 > SYN_WAIT_CYCLES) {
-                            record_error(p.err, SYN_DEVERR_TIMEOUT);
-                            gave_up = 1;
-                            break;
-                        }
-                }
-                end -= CMP_THREADS;
-                if (__syncthreads_or(state == 2)) break;
-            }
-            __threadfence();
-            if (gave_up) return;
-            if (tid == 0) atomicExch(flags + chunk, 2);
-        }
+        if (gave_up) return;
 #pragma unroll
         for (int i = 0; i < CMP_UNITS; i++) {
-            const int u = i * CMP_THREADS + tid;
-            uint8_t* b = u < units ? place(dst, u, n16, 0, n16 * 16, 16) : nullptr;
-            if (b) *reinterpret_cast<uint4*>(b) = w[i];
+            const int r = row16 + i * per16;
+            if (r < end16 && src[x][r] >= 0) *reinterpret_cast<uint4*>(at16 + dst[x][r]) = held16[i * CMP_THREADS];
         }
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const int u = i * CMP_THREADS + tid;
-            uint8_t* b = u < s_units ? place(dst, u, ns, scales, p.c.dim >> 4, sizeof(S)) : nullptr;
-            if (b) *reinterpret_cast<S*>(b) = ws[i];
+        for (int i = 0; i < CMP_SCALES; i++) {
+            const int r = row_s + i * per_s;
+            if (r < end_s && src[x][r] >= 0) *reinterpret_cast<S*>(at_s + dst_s[x][r]) = ws[i];
         }
+        if (!more) return;
+        moves = moves_next;
+        __syncthreads();  // (the slots have been used)
     }
 }
 
 // Rows from which a list counts as long.
 constexpr int64_t CMP_LONG = 4096;
 
-// How a long list is cut: 16-byte units (and 2-byte to 8-byte ones of scales) that a CTA holds at once.
+// How a long list is cut: a thread for each 16 bytes of a row of a group's tiles, some rows a pass (and for each 2 to 8 bytes
+// of scales).
 static int64_t cut_long(const KvCache& c, int64_t n_rows, LongParams* q) {
     const int n16 = c.dim >> (c.q8 ? 4 : 3), ns = c.q8 ? (c.dim >> 4) / (c.dim % 128 == 0 ? 8 : c.dim % 64 == 0 ? 4 : 2) : 0;
-    const int most = CMP_THREADS * CMP_UNITS, most_s = CMP_THREADS * 2;
-    int tiles = std::min(2 * c.n_kv, most / n16);
-    if (ns) tiles = std::min(tiles, most_s / ns);
-    int rows = most / (tiles * n16);
-    if (ns) rows = std::min(rows, most_s / (tiles * ns));
+    const int tiles = std::min(2 * c.n_kv, CMP_THREADS / n16);
+    int rows = CMP_THREADS / (tiles * n16) * CMP_UNITS;
+    if (ns) rows = std::min(rows, CMP_THREADS / (tiles * ns) * CMP_SCALES);
     q->group_tiles = tiles;
     q->groups = (2 * c.n_kv + tiles - 1) / tiles;
-    q->chunk_rows = std::min(rows, CMP_ROWS);
+    q->chunk_rows = std::min(rows, CMP_CHUNK);
     q->chunks = (int)((n_rows + q->chunk_rows - 1) / q->chunk_rows);
     return (int64_t)q->chunks * q->groups;
 }
@@ -673,8 +694,8 @@ cudaError_t launch_kv_compact(const KvCache& c, const int32_t* refs, int64_t n_s
         e = cudaMemsetAsync(scratch, 0, (size_t)(n + 1) * 4, s);
         if (e != cudaSuccess) return e;
         auto kern = c.dim % 128 == 0 ? k_kv_compact_long<uint2> : c.dim % 64 == 0 ? k_kv_compact_long<uint32_t> : k_kv_compact_long<uint16_t>;
-        const int grid = (int)std::min<int64_t>(n, (int64_t)sms * 4);
-        kern<<<grid, CMP_THREADS, 0, s>>>(q);
+        const int grid = (int)std::min<int64_t>(n, (int64_t)sms * CMP_CTAS);
+        kern<<<grid, CMP_THREADS, CMP_UNITS * CMP_THREADS * 16, s>>>(q);
         e = cudaGetLastError();
     } else {
         // columns of at least 32 bytes of a row (a sector), as many as it takes to fill the SMs

@@ -27,7 +27,7 @@ INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["api.cu", "quant.cu", "gemv.cu", "gemv_f16.cu", "gemm.cu", "noalloc.cu", "kv_append.cu", "attn_decode.cu",
            "attn_prefill.cu", "attn_tree.cu", "kv_pages.cu", "logprobs.cu", "api_attn.cu", "gguf.cpp"]
-HEADERS = ["common.cuh", "quant_dev.cuh", "kv_cache.cuh", "tcgen05.cuh", "attn_prefill.cuh", "kernels.h"]
+HEADERS = ["common.cuh", "quant_dev.cuh", "kv_cache.cuh", "tcgen05.cuh", "attn_tokens.cuh", "kernels.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

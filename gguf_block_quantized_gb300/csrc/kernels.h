@@ -105,11 +105,13 @@ cudaError_t launch_attn_prefill(const KvCache& c, const KvCache& raw, const Attn
                                 const void* q, const int32_t* starts, const int32_t* pages, const int32_t* raw_pages,
                                 int64_t max_pages, const int32_t* lens, void* out, float* part, int* count, bool split,
                                 int* err, int sms, int* launches, cudaStream_t s);
-// The same for new tokens that are the nodes of trees (parents: per token, among its sequence's; scratch alike).
+// The same for new tokens that are the nodes of trees (parents: per token, among its sequence's).  part: tree_part_floats;
+// count: 2 words, as above.
 cudaError_t launch_attn_tree(const KvCache& c, const AttnDesc& a, int64_t n_seq, int64_t n_tok, const void* q,
                              const int32_t* starts, const int32_t* parents, const int32_t* pages, int64_t max_pages,
                              const int32_t* lens, void* out, float* part, int* count, bool split, int* err, int sms,
                              int* launches, cudaStream_t s);
+int64_t tree_part_floats(int64_t n_seq, int64_t n_tok, int n_heads, int n_kv, int dim, int sms);
 int64_t prefill_part_floats(int64_t n_seq, int64_t n_tok, int n_heads, int n_kv, int dim, int sms);
 // The rows of a Q8_0 cache that the sequences hold as the pages of an F16 cache of scratch (k, v: n_seq *
 // max_pages pages of n_kv tiles each; table: its page table, n_seq x max_pages, -1 for a page outside the

@@ -301,7 +301,7 @@ int syn_attn_tree(const syn_kv_cache* cache, const syn_attn* attn, int64_t n_seq
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int* count;
     float* part;
-    rc = scratch_for(s, 2, syn::tree_part_floats(n_seq, n_tok, a.n_heads, c.n_kv, c.dim, sms), &count, &part);
+    rc = scratch_for(s, 4, syn::tree_part_floats(n_seq, n_tok, a.n_heads, c.n_kv, c.dim, sms), &count, &part);
     if (rc) return rc;
     int launches = 0;
     rc = check_cuda(syn::launch_attn_tree(c, a, n_seq, n_tok, q, starts, parents, pages, max_pages, lens, out, part, count,

@@ -107,11 +107,6 @@ struct PreShape {
                                  : 8 * SOFTMAX_REGS + 4 * MMA_REGS <= 12 * 168), "more registers than the launch has");
 };
 
-template <int N>
-__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 // What the scheduler tells the other warps of an item.
 struct Item {
     int nt;      // tiles of this part (0: no row sees a key; -1: no item is left)

@@ -11,6 +11,11 @@ namespace syn {
 constexpr float PRE_P_LOG2 = 6.0f;    // p is held as 2^6 p
 constexpr float PRE_GROW_LOG2 = 8.0f; // the maximum's lag
 
+template <int N>
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // the tiles that hold a key some row of the item sees: [a0, a1) of the prefix, [b0, b1)
 struct Tiles {
     int a0, a1, b0, b1;

@@ -24,7 +24,7 @@
 //   MMA      one warp: S = Q K^T (from shared memory), O += P V (P from tensor memory, V as it lies);
 //   loader   one warp: F16: tensor-map copies of page pieces into a ring of tiles (128-byte swizzle); Q8_0:
 //            bulk copies of codes and scales into a ring of raw tiles, which
-//   expand   (Q8_0) four warps turn into fp16 tiles of the same layout.
+//   expand   (Q8_0) eight warps turn into fp16 tiles of the same layout.
 // All hand-offs are mbarriers with bounded waits.
 //
 // A masked score is replaced before the maximum; V rows past the sequence's end are zeroed in shared memory.  A V
@@ -38,7 +38,7 @@
 
 namespace syn {
 
-constexpr int TREE_MAX_SEQ = 1024;  // sequences of one launch
+constexpr int TREE_MAX_SEQ = 256;   // sequences of one launch
 constexpr int TREE_ITEM = 1;        // what an item's start and end cost, in tiles
 constexpr int TREE_JOIN = 4;        // and a part's share of the join: what is no longer than the ranges by more is not split
 
@@ -49,9 +49,17 @@ struct TreeRedo {  // rows to be computed again, when the CTA has done its items
     int t0, t1, slot;  // a part's tiles and partial (-1: the item is whole)
     int next;          // of the same warp
 };
+struct TreeSeq {  // a sequence of the launch
+    int cost_before, items_before;  // tiles (and what items cost besides) and items of those ahead of it
+    int first;                      // the first key that some node sees
+    int tok0, n_new, len, prefix;
+};
 struct TreeSplit {  // an item that several CTAs share
     int tok0, h, row0, rows, first, parts;  // first: the CTA of its first part
+    int before, pad;                        // the join's tasks for the items listed before it
 };
+
+constexpr int JOIN_VALUES = 8;  // of 32 rows: a task of the join
 
 struct TreeParams {
     KvCache c;
@@ -68,7 +76,7 @@ struct TreeParams {
     const int32_t* first;
     float* part;        // three partials a CTA: of an item it goes on with, of one it begins, of rows computed again
     TreeSplit* splits;
-    int* n_splits;      // [0] how many, [1] CTAs of the join done; zero between calls
+    int* n_splits;      // [0] the join's tasks and [1] how many (one 64-bit number), [2] CTAs of the join done; zero between calls
     TreeRedo* redo;     // [n_redo] one for each warp's rows of each item, then [CTAs][2][warps] of parts
     int64_t n_redo;
     int* err;
@@ -83,7 +91,7 @@ struct TreeShape {
     static constexpr int QT = D <= 128 ? 2 : 1;     // softmax groups, and 128-row tiles of an item
     static constexpr int BN = D <= 128 ? 128 : 64;  // keys of a tile
     static constexpr int NS = D <= 64 ? 6 : Q8 ? 3 : 4;  // tiles (K or V) in the ring
-    static constexpr int NR = Q8 ? 2 : 0;           // raw tiles (codes, then scales) ahead of it
+    static constexpr int NR = Q8 ? 3 : 0;           // raw tiles (codes, then scales) ahead of it
     static constexpr int R = 128 * QT;
     static constexpr int STAGE = BN * D * 2;
     static constexpr int RAW = BN * D + BN * D / 16;
@@ -93,15 +101,24 @@ struct TreeShape {
     static constexpr int RAWS = RING + NS * STAGE;
     static constexpr int BARS = RAWS + NR * RAW;
     static constexpr int INFO = BARS + (8 * (2 * NS + 2 * NR + 20) + 8 + 15) / 16 * 16;
-    // [64 bytes] flags, [2][24] items, [2][128] maxima and sums, [4] rows, then per sequence: cost and items before it, first key
+    // [64 bytes] flags, [2][24] items, [2][128] maxima and sums, [4] rows, then the sequences
     static constexpr int SUMS = INFO + 64 + 2 * 96, SEQS = SUMS + 2 * 128 * 8 + 16;
-    static constexpr int BYTES = SEQS + 16 * (TREE_MAX_SEQ + 1);
+    static constexpr int BYTES = SEQS + (int)sizeof(TreeSeq) * (TREE_MAX_SEQ + 1);
     static constexpr int O_COL = QT == 2 ? 256 : 128;  // S slots below it
     static constexpr int SLOT = QT == 2 ? 128 : 64;    // columns of an S slot
-    // warps: softmax, then MMA, loader, scheduler and one that idles, then (Q8_0) four that expand
+    // warps: softmax, then MMA, loader, scheduler and one that idles, then (Q8_0) eight that expand
     static constexpr int MMA_WARP = 4 * QT, LOAD_WARP = MMA_WARP + 1, PLAN_WARP = MMA_WARP + 2, EXPAND_WARP = MMA_WARP + 4;
-    static constexpr int READERS = MMA_WARP + 2 + (Q8 ? 4 : 0);  // warps that follow the scheduler
-    static constexpr int WARPS = MMA_WARP + 4 + (Q8 ? 4 : 0), THREADS = 32 * WARPS;
+    static constexpr int EXPANDERS = Q8 ? 8 : 0;
+    static constexpr int READERS = MMA_WARP + 2 + EXPANDERS;  // warps that follow the scheduler
+    static constexpr int WARPS = MMA_WARP + 4 + EXPANDERS, THREADS = 32 * WARPS;
+    // Registers a thread of each kind after the hand-over (their sum over the warps is what the launch gives them):
+    // a softmax thread holds its row's 64 scores beside what masks, caps and biases them, and what it spills lies outside
+    // what shared memory leaves of L1.
+    static constexpr int LAUNCH_REGS = THREADS == 640 ? 96 : THREADS == 512 ? 128 : 168;
+    static constexpr int SOFTMAX_REGS = !Q8 ? 208 : QT == 2 ? 136 : 232, MMA_REGS = !Q8 ? 88 : QT == 2 ? 80 : 88, EXPAND_REGS = QT == 2 ? 64 : 96;
+    static constexpr bool HAND_OVER = QT == 2 || Q8;  // (else 8 warps, which have 255 each)
+    static_assert(!HAND_OVER || MMA_WARP * SOFTMAX_REGS + 4 * MMA_REGS + EXPANDERS * EXPAND_REGS <= WARPS * LAUNCH_REGS,
+                  "more registers than the launch has");
     static constexpr int64_t PART = (int64_t)R * (D + 2);  // of a partial: [D][R] values, [R] maxima, [R] sums
 };
 
@@ -310,15 +327,12 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
     uint64_t* mma_idle = meet_bar + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* info = reinterpret_cast<int*>(smem + L::INFO);  // the scan's carry: [0] cost (64 bits), [2] items, [3] the longest item
+    int* info = reinterpret_cast<int*>(smem + L::INFO);  // the scan's carry: [0] cost, [1] items, [2] the longest item
     volatile uint32_t* raw_there = reinterpret_cast<volatile uint32_t*>(info + 12);  // [NR] pieces that arrived
     volatile int* item_ints = info + 16;                                             // [2][24] items
     float2* sums = reinterpret_cast<float2*>(smem + L::SUMS);                        // [2][128] a group's maxima and sums
     volatile uint32_t* odd_rows = reinterpret_cast<volatile uint32_t*>(sums + 256);  // [4]
-    // of each sequence: the cost of those before it, the items before it, the first key some node sees
-    int64_t* cost_before = reinterpret_cast<int64_t*>(smem + L::SEQS);
-    int* items_before = reinterpret_cast<int*>(cost_before + TREE_MAX_SEQ + 1);
-    int* first_of = items_before + TREE_MAX_SEQ + 1;
+    TreeSeq* seqs = reinterpret_cast<TreeSeq*>(smem + L::SEQS);  // [n_seq], and the totals
 
     // (the shuffle tells the compiler that the warp's index is the same for its lanes)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -327,7 +341,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
     // ---- set-up that touches no global memory, ahead of the kernel before this one -----------
     if (tid == 0) {
         for (int i = 0; i < NS; i++) {
-            mbar_init(smem_u32(&kv_full[i]), Q8 ? 4 : 1);
+            mbar_init(smem_u32(&kv_full[i]), Q8 ? L::EXPANDERS : 1);
             mbar_init(smem_u32(&kv_empty[i]), 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -343,12 +357,12 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
         }
         for (int i = 0; i < NR; i++) {
             mbar_init(smem_u32(&raw_full[i]), 1);
-            mbar_init(smem_u32(&raw_empty[i]), 4);
+            mbar_init(smem_u32(&raw_empty[i]), L::EXPANDERS);
         }
         mbar_init(smem_u32(mma_idle), 1);
         mbar_init(smem_u32(meet_bar), MMA_WARP);
         *abort_flag = 0;
-        info[0] = info[1] = info[2] = info[3] = 0;
+        info[0] = info[1] = info[2] = 0;
         fence_mbar_init();
     }
     if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_slot), 512);
@@ -356,69 +370,69 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
     griddep_wait();
 
     auto rows_tiles = [&](int n_new) { return (int)(((int64_t)n_new * p.g + R - 1) / R); };
-    // sequence s: its items, what they cost, its tiles and first key
+    // Sequence s into its place: its items, what they cost (past 2^30: so much), the tiles of one.
     struct Work {
-        int64_t cost;
-        int items, nt, first;
+        int items, nt, cost;
     };
     auto work_of = [&](int s) {
-        Work w{0, 0, 0, 0};
+        Work w{0, 0, 0};
         if (s >= p.n_seq) return w;
-        const int n_new = new_tokens(p.starts, s, p.n_tok), len = held_rows(p.lens[s], p.max_pages, p.c.page_shift);
+        const int tok0 = p.starts[s], n_new = new_tokens(p.starts, s, p.n_tok), len = held_rows(p.lens[s], p.max_pages, p.c.page_shift);
+        const int prefix = p.prefix ? p.prefix[s] : 0;
+        int first = 0;
         if (p.first && n_new > 0) {
-            w.first = INT_MAX;
-            for (int t = p.starts[s]; t < p.starts[s] + n_new; t++) w.first = min(w.first, p.first[t]);
+            first = INT_MAX;
+            for (int t = tok0; t < tok0 + n_new; t++) first = min(first, p.first[t]);
         }
-        w.nt = tiles_of(p, len, len - n_new, w.first, p.prefix ? p.prefix[s] : 0, BN).count();
+        seqs[s].first = first;
+        seqs[s].tok0 = tok0;
+        seqs[s].n_new = n_new;
+        seqs[s].len = len;
+        seqs[s].prefix = prefix;
         w.items = rows_tiles(n_new) * p.c.n_kv;
-        w.cost = (int64_t)w.items * (max(w.nt, 1) + TREE_ITEM);
-        if (w.items == 0) w.nt = 0;
+        w.nt = w.items ? tiles_of(p, len, len - n_new, first, prefix, BN).count() : 0;
+        w.cost = (int)min((int64_t)w.items * (max(w.nt, 1) + TREE_ITEM), int64_t(1) << 30);
         return w;
     };
-    if (p.n_seq > 32) {  // (up to 32 sequences are the scheduler's lanes)
+    // (sums past 2^31: no call comes to that many tiles but by sequences that share their pages; nothing is split then)
+    auto add = [](int a, int b) { return (int)min((unsigned)a + (unsigned)b, 1u << 30); };
+    auto scan = [&](Work& w) {  // over the warp's lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int c = __shfl_up_sync(0xffffffffu, w.cost, o), x = __shfl_up_sync(0xffffffffu, w.items, o);
+            if (lane >= o) {
+                w.cost = add(w.cost, c);
+                w.items += x;
+            }
+        }
+    };
+    if (p.n_seq > 64) {  // (up to 64 sequences: the scheduler alone)
         __syncthreads();
-        int64_t* warp_cost = reinterpret_cast<int64_t*>(smem);  // (nothing else uses it yet)
-        int* warp_items = reinterpret_cast<int*>(warp_cost + 32);
+        Work* of_warps = reinterpret_cast<Work*>(smem);  // (nothing else uses it yet)
         for (int base = 0; base < p.n_seq; base += THREADS) {
             const int s = base + tid;
-            const Work w = work_of(s);
-            int64_t cost = w.cost;
-            int items = w.items;
+            Work w = work_of(s);
             const int nt = __reduce_max_sync(0xffffffffu, w.nt);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t c = __shfl_up_sync(0xffffffffu, cost, o);
-                const int x = __shfl_up_sync(0xffffffffu, items, o);
-                if (lane >= o) {
-                    cost += c;
-                    items += x;
-                }
-            }
-            if (lane == 31) {
-                warp_cost[warp] = cost;
-                warp_items[warp] = items;
-            }
-            if (lane == 0) atomicMax(&info[3], nt);
+            scan(w);
+            if (lane == 31) of_warps[warp] = w;
+            if (lane == 0) atomicMax(&info[2], nt);
             __syncthreads();
-            int64_t before = *reinterpret_cast<int64_t*>(info);
-            int items_ahead = info[2];
+            int cost = info[0], items = info[1];
             for (int i = 0; i < warp; i++) {
-                before += warp_cost[i];
-                items_ahead += warp_items[i];
+                cost = add(cost, of_warps[i].cost);
+                items += of_warps[i].items;
             }
+            cost = add(cost, w.cost);
+            items += w.items;
             if (s < p.n_seq) {
-                cost_before[s + 1] = before + cost;
-                items_before[s + 1] = items_ahead + items;
-                first_of[s] = w.first;
+                seqs[s + 1].cost_before = cost;
+                seqs[s + 1].items_before = items;
             }
-            if (s == 0) {
-                cost_before[0] = 0;
-                items_before[0] = 0;
-            }
+            if (s == 0) seqs[0].cost_before = seqs[0].items_before = 0;
             __syncthreads();
             if (tid == THREADS - 1) {
-                *reinterpret_cast<int64_t*>(info) = before + cost;
-                info[2] = items_ahead + items;
+                info[0] = cost;
+                info[1] = items;
             }
             __syncthreads();
         }
@@ -449,6 +463,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
 
     if (warp < MMA_WARP) {
         // ------------------------------------ softmax ------------------------------------------
+        if (L::HAND_OVER) take_registers<L::SOFTMAX_REGS>();
         const int st = warp >> 2;  // group
         const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t o_base = lane_base + L::O_COL + st * D;
@@ -794,7 +809,9 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
             tree_rows_by_hand<Q8>(p, x, BN, o, R, D);
             redo_list = x.next;
         }
-    } else if (warp == MMA_WARP) {
+    } else if (warp < EXPAND_WARP) {
+      if (L::HAND_OVER) give_registers<L::MMA_REGS>();
+      if (warp == MMA_WARP) {
         // ------------------------------------ MMA ----------------------------------------------
         int rc = 0;                        // ring pieces taken so far
         uint32_t uses = 0;                 // bit x: the phase of S slot x
@@ -905,7 +922,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
         // have seen the last one finish, except after an abort)
         mma_commit_lead(lead, smem_u32(mma_idle));
         mbar_drain(smem_u32(mma_idle), 0, p.err);
-    } else if (warp == LOAD_WARP) {
+      } else if (warp == LOAD_WARP) {
         // ------------------------------------ loader -------------------------------------------
         const int box = min(BN, 1 << p.c.page_shift), n_box = BN / box;  // rows of a copy; lane l does the l-th
         int kc = 0, q_turn[2] = {0, 0};  // pieces and Q tiles so far
@@ -995,85 +1012,74 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
         } else {
             for (int u = max(0, kc - NS); u < kc; u++) mbar_drain(smem_u32(&kv_full[u % NS]), (u / NS) & 1, p.err);
         }
-    } else if (warp == L::PLAN_WARP) {
+      } else if (warp == L::PLAN_WARP) {
         // ------------------------------------ scheduler ----------------------------------------
-        int64_t total;
-        int items, longest;
-        if (p.n_seq <= 32) {
-            const Work w = work_of(lane);
-            int64_t cost = w.cost;
-            items = w.items;
-            longest = __reduce_max_sync(0xffffffffu, w.nt);
+        int longest = info[2];
+        if (p.n_seq <= 64) {
+            int cost = 0, items = 0;
+            Work w[2];
+            w[0] = work_of(lane);
+            w[1] = p.n_seq > 32 ? work_of(32 + lane) : Work{0, 0, 0};
+            longest = __reduce_max_sync(0xffffffffu, max(w[0].nt, w[1].nt));
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t c = __shfl_up_sync(0xffffffffu, cost, o);
-                const int x = __shfl_up_sync(0xffffffffu, items, o);
-                if (lane >= o) {
-                    cost += c;
-                    items += x;
+            for (int x = 0; x < 2; x++) {
+                const int s = 32 * x + lane;
+                scan(w[x]);
+                if (s < p.n_seq) {
+                    seqs[s + 1].cost_before = add(cost, w[x].cost);
+                    seqs[s + 1].items_before = items + w[x].items;
                 }
+                cost = add(cost, __shfl_sync(0xffffffffu, w[x].cost, 31));
+                items += __shfl_sync(0xffffffffu, w[x].items, 31);
             }
-            cost_before[lane + 1] = cost;
-            items_before[lane + 1] = items;
-            first_of[lane] = w.first;
-            if (lane == 0) {
-                cost_before[0] = 0;
-                items_before[0] = 0;
-            }
+            if (lane == 0) seqs[0].cost_before = seqs[0].items_before = 0;
             __syncwarp();
-        } else {
-            longest = info[3];
         }
-        total = cost_before[p.n_seq];
-        items = items_before[p.n_seq];
+        const int total = seqs[p.n_seq].cost_before, items = seqs[p.n_seq].items_before, ctas = (int)gridDim.x;
         // Ranges of `range` tiles, or whole items in turn: where nothing may be split, or splitting would not pay.
-        const int64_t ctas = gridDim.x, range = max((total + ctas - 1) / ctas, (int64_t)1);
-        const bool whole = !p.split || (items <= ctas && longest + TREE_ITEM <= range + TREE_JOIN);
-        int64_t at = whole ? blockIdx.x : blockIdx.x * range;  // an item's number, or a place in the work
-        const int64_t to = whole ? items : min(at + range, total);
+        const int range = max((total + ctas - 1) / ctas, 1);
+        const bool whole = !p.split || total >= 1 << 30 || (items <= ctas && longest + TREE_ITEM <= range + TREE_JOIN);
+        int64_t at = whole ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * range;  // an item's number, or a place in the work
+        const int64_t to = whole ? (int64_t)items : min(at + range, (int64_t)total);
         for (int n = 0;;) {
             TreeItem it{};
             it.nt = -1;
             it.slot = -1;
+            int split0 = 0, split1 = 0;  // the CTAs of an item's first and last part
             if (at < to) {
                 int lo = 0, hi = p.n_seq - 1;  // the sequence
                 while (lo < hi) {
                     const int mid = (lo + hi) >> 1;
-                    if ((whole ? (int64_t)items_before[mid + 1] : cost_before[mid + 1]) > at) hi = mid;
+                    if ((whole ? seqs[mid + 1].items_before : seqs[mid + 1].cost_before) > (int)at) hi = mid;
                     else lo = mid + 1;
                 }
+                const TreeSeq q = seqs[lo];
                 it.s = lo;
-                it.n_new = new_tokens(p.starts, lo, p.n_tok);
-                it.tok0 = p.starts[lo];
-                it.len = held_rows(p.lens[lo], p.max_pages, p.c.page_shift);
-                it.prefix = p.prefix ? p.prefix[lo] : 0;
+                it.n_new = q.n_new;
+                it.tok0 = q.tok0;
+                it.len = q.len;
+                it.prefix = q.prefix;
                 const int pos0 = it.len - it.n_new;
-                it.tiles = tiles_of(p, it.len, pos0, first_of[lo], it.prefix, BN);
+                it.tiles = tiles_of(p, it.len, pos0, q.first, it.prefix, BN);
                 const int nt = it.tiles.count(), tiles_q = rows_tiles(it.n_new);
-                const int64_t each = max(nt, 1) + TREE_ITEM, within = whole ? at - items_before[lo] : (at - cost_before[lo]) / each;
-                it.index = items_before[lo] + (int)within;
-                it.h = (int)(within / tiles_q);
-                it.row0 = (int)(within - (int64_t)it.h * tiles_q) * R;
+                const int each = max(nt, 1) + TREE_ITEM, within = whole ? (int)at - q.items_before : ((int)at - q.cost_before) / each;
+                it.index = q.items_before + within;
+                it.h = within / tiles_q;
+                it.row0 = (within - it.h * tiles_q) * R;
                 it.rows = (int)min((int64_t)R, (int64_t)it.n_new * p.g - it.row0);
                 bool mine = true;  // (else: only the cost of the item's end lies in this range)
                 if (whole) {
                     it.nt = nt;
                     at += ctas;
                 } else {
-                    const int64_t begin = cost_before[lo] + within * each, from = at - begin;
-                    it.t0 = (int)min(from, (int64_t)nt);
-                    it.nt = (int)min(from + (to - at), (int64_t)nt) - it.t0;
+                    const int begin = q.cost_before + within * each, from = (int)at - begin;
+                    it.t0 = min(from, nt);
+                    it.nt = min(from + (int)(to - at), nt) - it.t0;
                     mine = nt > 0 ? it.nt > 0 : from == 0;
-                    const int64_t c0 = begin / range, c1 = (begin + max(nt, 1) - 1) / range;
-                    if (mine && c1 > c0) {
-                        it.slot = it.t0 > 0 ? 0 : 1;
-                        if (it.t0 == 0 && lane == 0) {
-                            const int x = atomicAdd(p.n_splits, 1);
-                            if (x < (int)gridDim.x)  // (each end of a range splits one at most)
-                                p.splits[x] = TreeSplit{it.tok0, it.h, it.row0, it.rows, (int)c0, (int)(c1 - c0) + 1};
-                        }
-                    }
-                    at = min(begin + each, to);
+                    split0 = begin / range;
+                    split1 = (begin + max(nt, 1) - 1) / range;
+                    if (split1 > split0) it.slot = it.t0 > 0 ? 0 : 1;
+                    at = min((int64_t)begin + each, to);
                 }
                 if (!mine) continue;
                 // [mf, pre) and [ml, me): every key that some row sees lies in one of them
@@ -1117,17 +1123,26 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                 for (int i = 0; i < 20; i++) item_ints[24 * slot + i] = o[i];
                 mbar_arrive(smem_u32(&item_full[slot]));
             }
+            if (it.slot == 1 && lane == 0) {  // (its first part)
+                const unsigned long long tasks = (unsigned long long)((it.rows + 31) / 32 * (dim / JOIN_VALUES));
+                const unsigned long long before = atomicAdd(reinterpret_cast<unsigned long long*>(p.n_splits), (1ull << 32) + tasks);
+                const int x = (int)(before >> 32);
+                if (x < ctas)  // (each end of a range splits one at most)
+                    p.splits[x] = TreeSplit{it.tok0, it.h, it.row0, it.rows, split0, split1 - split0 + 1, (int)before, 0};
+            }
             __syncwarp();
             n++;
             if (it.nt == -1) break;
         }
-    } else if (Q8 && warp >= EXPAND_WARP) {
+      }
+    } else if (Q8) {
         // ------------------------------------ expand (Q8_0) -------------------------------------
+        if (L::EXPAND_REGS < L::LAUNCH_REGS) give_registers<L::EXPAND_REGS>();
         const int lt = tid - 32 * EXPAND_WARP;
-        // 16 codes at a time.  A thread takes piece x4 of the 64-value chunks of rows lt/4, lt/4 + 32, ...;
+        // 16 codes at a time.  A thread takes piece x4 of the 64-value chunks of rows lt/4, lt/4 + ROWS, ...;
         // neighbouring rows take the chunks in opposite order, so that the 8 lanes that a shared-memory
         // access serves at once touch all the banks, reading and storing.
-        constexpr int HALVES = D / 64, UNITS = BN / 32 * HALVES;
+        constexpr int ROWS = 8 * L::EXPANDERS, HALVES = D / 64, UNITS = BN / (Q8 ? ROWS : BN) * HALVES;  // (ROWS: a pass)
         const int x4 = lt & 3, row_t = lt >> 2;
         const int box_shift = min(p.c.page_shift, BN == 128 ? 7 : 6), n_box = BN >> box_shift;
         const uint32_t all_there = n_box == 32 ? 0xffffffffu : (1u << n_box) - 1u;
@@ -1182,18 +1197,18 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
 #pragma unroll
                         for (int u = 0; u < BATCH; u++) {
                             const int ru = (u0 + u) / HALVES, half = HALVES > 1 ? ((u0 + u) % HALVES) ^ odd : 0;
-                            code[u] = *reinterpret_cast<const uint4*>(codes + ru * (32 * D) + 64 * half);
-                            bits[u] = *reinterpret_cast<const uint16_t*>(scales + ru * (2 * D) + 4 * half);
+                            code[u] = *reinterpret_cast<const uint4*>(codes + ru * (ROWS * D) + 64 * half);
+                            bits[u] = *reinterpret_cast<const uint16_t*>(scales + ru * (ROWS * D / 16) + 4 * half);
                         }
 #pragma unroll
                         for (int u = 0; u < BATCH; u++) {
                             const int ru = (u0 + u) / HALVES, half = HALVES > 1 ? ((u0 + u) % HALVES) ^ odd : 0;
-                            put(dst + half * (BN * 128) + ru * (32 * 128), code[u], bits[u]);
+                            put(dst + half * (BN * 128) + ru * (ROWS * 128), code[u], bits[u]);
                         }
                     }
                 } else {  // rows that are not there are zeros
                     for (int u = 0; u < UNITS; u++) {
-                        const int half = HALVES > 1 ? (u % HALVES) ^ (row_t & 1) : 0, x = x4 + 4 * half, row = row_t + 32 * (u / HALVES);
+                        const int half = HALVES > 1 ? (u % HALVES) ^ (row_t & 1) : 0, x = x4 + 4 * half, row = row_t + ROWS * (u / HALVES);
                         if (half >= nh) continue;
                         uint4 code = make_uint4(0, 0, 0, 0);
                         uint32_t bits = 0;
@@ -1201,7 +1216,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                             code = *reinterpret_cast<const uint4*>(raw + row * dim + 16 * x);
                             bits = *reinterpret_cast<const uint16_t*>(raw + BN * D + 2 * (row * (dim >> 5) + (x >> 1)));
                         }
-                        put(dst + half * (BN * 128) + (u / HALVES) * (32 * 128), code, bits);
+                        put(dst + half * (BN * 128) + (u / HALVES) * (ROWS * 128), code, bits);
                     }
                 }
                 fence_proxy_async_smem();
@@ -1224,9 +1239,9 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
 
 // ---- the join of split items ---------------------------------------------------------------
 //
-// A warp joins 8 values of 32 rows of an item: the parts' weights from their maxima and sums, then their values, four
+// A warp joins 8 values of 32 rows of an item: the parts' weights from their maxima and sums, with their values, four
 // parts' loads on their way together.
-constexpr int JOIN_VALUES = 8, JOIN_THREADS = 256;
+constexpr int JOIN_THREADS = 256, JOIN_MOST = 1024;
 
 struct JoinParams {
     const float* part;
@@ -1234,18 +1249,26 @@ struct JoinParams {
     int* n_splits;
     void* out;
     int64_t out_stride, part_floats;  // of a partial
-    int R, D, dim, g, out_f16, most;
+    int R, D, dim, g, out_f16;
 };
 
 __global__ void __launch_bounds__(JOIN_THREADS) k_attn_tree_join(const JoinParams p) {
+    __shared__ int before[JOIN_MOST];
     griddep_release();
     griddep_wait();
-    const int lane = threadIdx.x & 31, n = min(*const_cast<volatile int*>(p.n_splits), p.most);
-    const int blocks = p.R / 32, chunks = p.dim / JOIN_VALUES, each = blocks * chunks, warps = gridDim.x * (JOIN_THREADS / 32);
-    for (int u = blockIdx.x * (JOIN_THREADS / 32) + (threadIdx.x >> 5); u < n * each; u += warps) {
-        const TreeSplit x = p.splits[u / each];
-        const int v = u % each, row = v / chunks * 32 + lane, e0 = v % chunks * JOIN_VALUES;
-        if (row - lane >= x.rows) continue;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = p.dim / JOIN_VALUES;
+    const int tasks = const_cast<volatile int*>(p.n_splits)[0], n = min(const_cast<volatile int*>(p.n_splits)[1], JOIN_MOST);
+    for (int i = threadIdx.x; i < n; i += JOIN_THREADS) before[i] = p.splits[i].before;
+    __syncthreads();
+    for (int u = blockIdx.x * (JOIN_THREADS / 32) + warp; u < tasks; u += gridDim.x * (JOIN_THREADS / 32)) {
+        int lo = 0, hi = n;  // the last item whose tasks begin at u or before it
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (before[mid] <= u) lo = mid;
+            else hi = mid;
+        }
+        const TreeSplit x = p.splits[lo];
+        const int row = (u - x.before) / chunks * 32 + lane, e0 = (u - x.before) % chunks * JOIN_VALUES;
         // part i: what the CTA first + i went on with; of the first what it began
         auto part = [&](int i) { return p.part + ((int64_t)(x.first + i) * 3 + (i == 0)) * p.part_floats + row; };
         float mx = -INFINITY, sum = 0.0f, acc[JOIN_VALUES];
@@ -1301,7 +1324,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_tree_join(const JoinParam
     }
     // the last CTA to get here makes the count ready for the next call
     __syncthreads();
-    if (threadIdx.x == 0 && atomicAdd(p.n_splits + 1, 1) == (int)gridDim.x - 1) p.n_splits[0] = p.n_splits[1] = 0;
+    if (threadIdx.x == 0 && atomicAdd(p.n_splits + 2, 1) == (int)gridDim.x - 1) p.n_splits[0] = p.n_splits[1] = p.n_splits[2] = 0;
 }
 
 // ---- host side ---------------------------------------------------------------------------
@@ -1315,6 +1338,14 @@ static cudaError_t run_tree(const CUtensorMap& km, const CUtensorMap& vm, const 
     int n;
     cudaError_t e = resident.get(reinterpret_cast<const void*>(kern), TreeShape<D, Q8>::THREADS, smem, &n);
     if (e != cudaSuccess) return e;
+    if (TreeShape<D, Q8>::HAND_OVER) {
+        // the hand-over of registers deals out what the launch has: a build with fewer must not start
+        static const int regs = [&] {
+            cudaFuncAttributes a;
+            return cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kern)) == cudaSuccess ? a.numRegs : 0;
+        }();
+        if (regs < TreeShape<D, Q8>::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+    }
     return launch_overlapped(kern, grid, TreeShape<D, Q8>::THREADS, smem, s, km, vm, qm, p);
 }
 
@@ -1338,6 +1369,7 @@ cudaError_t launch_attn_tree(const KvCache& c, const AttnDesc& a, int64_t n_seq,
                              const int32_t* starts, const int32_t* parents, const int32_t* pages, int64_t max_pages,
                              const int32_t* lens, void* out, float* part, int* count, bool split, int* err, int sms,
                              int* launches, cudaStream_t s) {
+    if (sms > JOIN_MOST) return cudaErrorInvalidConfiguration;
     CUtensorMap km, vm, qm;
     const int D = tree_width(c.dim), BN = D <= 128 ? 128 : 64, R = tree_rows(c.dim);
     PFN_encodeTiled encode = get_encode();
@@ -1398,7 +1430,7 @@ cudaError_t launch_attn_tree(const KvCache& c, const AttnDesc& a, int64_t n_seq,
     p.idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(c.dim >> 3) << 17) | (8u << 24);
     // (a scale that is not positive takes the general path: the fast one scales the maximum)
     const bool mod = a.cap > 0.0f || a.slopes || !(a.scale > 0.0f);
-    const JoinParams j{part, p.splits, p.n_splits, out, a.out_stride, tree_partial(c.dim), R, D, c.dim, g, a.out_f16, sms};
+    const JoinParams j{part, p.splits, p.n_splits, out, a.out_stride, tree_partial(c.dim), R, D, c.dim, g, a.out_f16};
     for (int64_t s0 = 0; s0 < n_seq; s0 += TREE_MAX_SEQ) {
         p.n_seq = (int)std::min<int64_t>(TREE_MAX_SEQ, n_seq - s0);
         p.starts = starts + s0;

@@ -106,7 +106,7 @@ cudaError_t launch_attn_prefill(const KvCache& c, const KvCache& raw, const Attn
                                 int64_t max_pages, const int32_t* lens, void* out, float* part, int* count, bool split,
                                 int* err, int sms, int* launches, cudaStream_t s);
 // The same for new tokens that are the nodes of trees (parents: per token, among its sequence's).  part: tree_part_floats;
-// count: 2 words, as above.
+// count: 4 words, 8-byte aligned, as above.
 cudaError_t launch_attn_tree(const KvCache& c, const AttnDesc& a, int64_t n_seq, int64_t n_tok, const void* q,
                              const int32_t* starts, const int32_t* parents, const int32_t* pages, int64_t max_pages,
                              const int32_t* lens, void* out, float* part, int* count, bool split, int* err, int sms,

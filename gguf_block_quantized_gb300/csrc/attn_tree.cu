@@ -38,7 +38,6 @@
 
 namespace syn {
 
-constexpr int TREE_MAX_SEQ = 256;   // sequences of one launch
 constexpr int TREE_ITEM = 1;        // what an item's start and end cost, in tiles
 constexpr int TREE_JOIN = 4;        // and a part's share of the join: what is no longer than the ranges by more is not split
 
@@ -86,6 +85,9 @@ struct TreeParams {
     uint32_t idesc_s, idesc_o;
 };
 
+// Sequences of one launch: as shared memory has room.
+constexpr int tree_max_seq(int D, bool q8) { return q8 && D >= 128 ? 256 : 512; }
+
 template <int D, bool Q8>
 struct TreeShape {
     static constexpr int QT = D <= 128 ? 2 : 1;     // softmax groups, and 128-row tiles of an item
@@ -101,9 +103,9 @@ struct TreeShape {
     static constexpr int RAWS = RING + NS * STAGE;
     static constexpr int BARS = RAWS + NR * RAW;
     static constexpr int INFO = BARS + (8 * (2 * NS + 2 * NR + 20) + 8 + 15) / 16 * 16;
-    // [64 bytes] flags, [2][24] items, [2][128] maxima and sums, [4] rows, then the sequences
+    // [64 bytes] flags, [2][24] items, [2][128] maxima and sums, [4] rows, the sequences
     static constexpr int SUMS = INFO + 64 + 2 * 96, SEQS = SUMS + 2 * 128 * 8 + 16;
-    static constexpr int BYTES = SEQS + (int)sizeof(TreeSeq) * (TREE_MAX_SEQ + 1);
+    static constexpr int BYTES = SEQS + (int)sizeof(TreeSeq) * (tree_max_seq(D, Q8) + 1);
     static constexpr int O_COL = QT == 2 ? 256 : 128;  // S slots below it
     static constexpr int SLOT = QT == 2 ? 128 : 64;    // columns of an S slot
     // warps: softmax, then MMA, loader, scheduler and one that idles, then (Q8_0) eight that expand
@@ -455,6 +457,9 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
     };
     // two row tiles, a softmax group each; else one, and a half of each tile's keys each (D > 128: one group)
     auto two_tiles = [&](const TreeItem& it) { return QT == 2 && it.rows > 128; };
+    // An item's tiles go up, or, with a bias by distance, from the last one down: the largest scores come
+    // first, and O is not rescaled tile after tile.
+    auto turn_tile = [&](int i, int nt) { return MOD && p.slopes ? nt - 1 - i : i; };
 
     // The ring's order: K of the first tile, then (two row tiles) V and the next K, or (one) the
     // next K and V.  Piece i of an item's 2*nt: is it V, and of which tile.
@@ -531,7 +536,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                 tc_fence_after();
                 for (int half = halves ? st : 0; half < (two ? 2 : halves ? st + 1 : 1); half++) {
                     const uint32_t s_base = lane_base + slot * L::SLOT + 64 * half;
-                    const int j0 = it.tiles.at(it.t0 + i) * BN + 64 * half;
+                    const int j0 = it.tiles.at(it.t0 + turn_tile(i, it.nt)) * BN + 64 * half;
                     // the products into O so far: of the tile before, or of this one's first half
                     auto wait_o = [&]() {
                         if (two && half) return mbar_wait(smem_u32(&o_done[2 * st]), done & 1, p.err, abort_flag);
@@ -584,11 +589,26 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                             for (int c = 0; c < 64; c += 2)
                                 big = fmaxf(fmaxf(big, fabsf(__uint_as_float(v[c]))), fabsf(__uint_as_float(v[c + 1])));
                             if (__all_sync(0xffffffffu, big * to_half <= 0.5f)) {
+                                // (eight pairs a step at a time: one after the other each waits for its own five)
 #pragma unroll
-                                for (int c = 0; c < 64; c += 2) {
-                                    const float2 r2 = small2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
-                                    v[c] = __float_as_uint(r2.x);
-                                    v[c + 1] = __float_as_uint(r2.y);
+                                for (int c = 0; c < 64; c += 16) {
+                                    uint64_t x[8], z[8], y[8];
+#pragma unroll
+                                    for (int u = 0; u < 8; u++) x[u] = pack2(__uint_as_float(v[c + 2 * u]), __uint_as_float(v[c + 2 * u + 1]));
+#pragma unroll
+                                    for (int u = 0; u < 8; u++) z[u] = mul2(x[u], x[u]);
+#pragma unroll
+                                    for (int u = 0; u < 8; u++) y[u] = fma2(z[u], b3, b2);
+#pragma unroll
+                                    for (int u = 0; u < 8; u++) y[u] = fma2(z[u], y[u], b1);
+#pragma unroll
+                                    for (int u = 0; u < 8; u++) y[u] = fma2(z[u], y[u], b0);
+#pragma unroll
+                                    for (int u = 0; u < 8; u++) {
+                                        const float2 r2 = unpack2(mul2(x[u], y[u]));
+                                        v[c + 2 * u] = __float_as_uint(r2.x);
+                                        v[c + 2 * u + 1] = __float_as_uint(r2.y);
+                                    }
                                 }
                             } else {
                                 // cap*tanh(x/cap) = cap - 2 cap/(1 + 2^(2 x log2(e)/cap)), all in powers of two
@@ -850,7 +870,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
         auto release = [&](int i) { mma_commit_lead(lead, smem_u32(&kv_empty[i % NS])); };
         // V rows past the sequence's end hold whatever the page holds: zeros
         auto clean = [&](int i, int tile) {
-            const int j0 = it.tiles.at(it.t0 + tile) * BN;
+            const int j0 = it.tiles.at(it.t0 + turn_tile(tile, it.nt)) * BN;
             if (Q8 || j0 + BN <= it.len) return;
             uint8_t* va = smem + L::RING + (i % NS) * L::STAGE;
             const int from = max(it.len - j0, 0);
@@ -954,7 +974,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
             const int n_pieces = 2 * it.nt;
 #endif
             const int32_t* table = p.pages + (int64_t)it.s * p.max_pages;
-            auto first_key = [&](int i) { return it.tiles.at(it.t0 + piece_tile(i, it.nt, two)) * BN + lane * box; };  // of this lane's box
+            auto first_key = [&](int i) { return it.tiles.at(it.t0 + turn_tile(piece_tile(i, it.nt, two), it.nt)) * BN + lane * box; };  // of this lane's box
             auto look_up = [&](int i) {  // the page (asked for a piece ahead)
                 const int j = i < n_pieces ? first_key(i) : INT_MAX;
                 return lane < n_box && j < it.len ? __ldg(table + (j >> p.c.page_shift)) : -1;
@@ -1014,25 +1034,24 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
         }
       } else if (warp == L::PLAN_WARP) {
         // ------------------------------------ scheduler ----------------------------------------
+        // (Much of what a small call takes passes here, ahead of the first load, and most of that in fetching code
+        // that runs once: what the first item needs comes first, without a division that a sum can spare.)
         int longest = info[2];
         if (p.n_seq <= 64) {
             int cost = 0, items = 0;
-            Work w[2];
-            w[0] = work_of(lane);
-            w[1] = p.n_seq > 32 ? work_of(32 + lane) : Work{0, 0, 0};
-            longest = __reduce_max_sync(0xffffffffu, max(w[0].nt, w[1].nt));
-#pragma unroll
-            for (int x = 0; x < 2; x++) {
-                const int s = 32 * x + lane;
-                scan(w[x]);
-                if (s < p.n_seq) {
-                    seqs[s + 1].cost_before = add(cost, w[x].cost);
-                    seqs[s + 1].items_before = items + w[x].items;
-                }
-                cost = add(cost, __shfl_sync(0xffffffffu, w[x].cost, 31));
-                items += __shfl_sync(0xffffffffu, w[x].items, 31);
-            }
             if (lane == 0) seqs[0].cost_before = seqs[0].items_before = 0;
+#pragma unroll 1
+            for (int base = 0; base < p.n_seq; base += 32) {
+                Work w = work_of(base + lane);
+                longest = max(longest, __reduce_max_sync(0xffffffffu, w.nt));
+                scan(w);
+                if (base + lane < p.n_seq) {
+                    seqs[base + lane + 1].cost_before = add(cost, w.cost);
+                    seqs[base + lane + 1].items_before = items + w.items;
+                }
+                cost = add(cost, __shfl_sync(0xffffffffu, w.cost, 31));
+                items += __shfl_sync(0xffffffffu, w.items, 31);
+            }
             __syncwarp();
         }
         const int total = seqs[p.n_seq].cost_before, items = seqs[p.n_seq].items_before, ctas = (int)gridDim.x;
@@ -1045,7 +1064,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
             TreeItem it{};
             it.nt = -1;
             it.slot = -1;
-            int split0 = 0, split1 = 0;  // the CTAs of an item's first and last part
+            int rest = 0;  // tiles of an item that others go on with
             if (at < to) {
                 int lo = 0, hi = p.n_seq - 1;  // the sequence
                 while (lo < hi) {
@@ -1064,7 +1083,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                 const int nt = it.tiles.count(), tiles_q = rows_tiles(it.n_new);
                 const int each = max(nt, 1) + TREE_ITEM, within = whole ? (int)at - q.items_before : ((int)at - q.cost_before) / each;
                 it.index = q.items_before + within;
-                it.h = within / tiles_q;
+                it.h = tiles_q == 1 ? within : within / tiles_q;
                 it.row0 = (within - it.h * tiles_q) * R;
                 it.rows = (int)min((int64_t)R, (int64_t)it.n_new * p.g - it.row0);
                 bool mine = true;  // (else: only the cost of the item's end lies in this range)
@@ -1076,17 +1095,16 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                     it.t0 = min(from, nt);
                     it.nt = min(from + (int)(to - at), nt) - it.t0;
                     mine = nt > 0 ? it.nt > 0 : from == 0;
-                    split0 = begin / range;
-                    split1 = (begin + max(nt, 1) - 1) / range;
-                    if (split1 > split0) it.slot = it.t0 > 0 ? 0 : 1;
+                    rest = nt - it.t0 - it.nt;
+                    if (mine && (it.t0 > 0 || rest > 0)) it.slot = it.t0 > 0 ? 0 : 1;
                     at = min((int64_t)begin + each, to);
                 }
                 if (!mine) continue;
                 // [mf, pre) and [ml, me): every key that some row sees lies in one of them
                 const int pre_end = min(max(it.prefix, 0), max(pos0, 0));
-                const int tk0 = it.row0 / p.g, tk1 = (it.row0 + it.rows - 1) / p.g;  // first and last token
                 int mf = INT_MAX, ml = INT_MAX, me = 0;
                 if (p.first || p.window) {
+                    const int tk0 = it.row0 / p.g, tk1 = (it.row0 + it.rows - 1) / p.g;  // first and last token
                     for (int t = tk0 + lane; t <= tk1; t += 32) {
                         const Visible v = visible_context(pos0, p.window ? pos0 + depth_of(p, it.tok0, t) : pos0,
                                                           p.first ? p.first[it.tok0 + t] : 0, it.prefix, p.window);
@@ -1106,7 +1124,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                     me = __reduce_max_sync(0xffffffffu, me);
                 } else {
                     ml = 0;
-                    me = max(pos0 + tk1 + 1, 0);
+                    me = it.len;
                     mf = pre_end > 0 ? 0 : INT_MAX;
                 }
                 it.seen.first = min(mf, ml);
@@ -1128,7 +1146,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                 const unsigned long long before = atomicAdd(reinterpret_cast<unsigned long long*>(p.n_splits), (1ull << 32) + tasks);
                 const int x = (int)(before >> 32);
                 if (x < ctas)  // (each end of a range splits one at most)
-                    p.splits[x] = TreeSplit{it.tok0, it.h, it.row0, it.rows, split0, split1 - split0 + 1, (int)before, 0};
+                    p.splits[x] = TreeSplit{it.tok0, it.h, it.row0, it.rows, (int)blockIdx.x, 1 + (rest + range - 1) / range, (int)before, 0};
             }
             __syncwarp();
             n++;
@@ -1161,7 +1179,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                 const int rs = kc % max(NR, 1), st = kc % NS;
                 if (!(ok = mbar_wait(smem_u32(&raw_full[rs]), (kc / max(NR, 1)) & 1, p.err, abort_flag))) break;
                 if (!(ok = mbar_wait(smem_u32(&kv_empty[st]), ((kc / NS) & 1) ^ 1, p.err, abort_flag))) break;
-                const int left = it.len - it.tiles.at(it.t0 + piece_tile(i, it.nt, two)) * BN;  // rows of the tile that exist
+                const int left = it.len - it.tiles.at(it.t0 + turn_tile(piece_tile(i, it.nt, two), it.nt)) * BN;  // rows of the tile that exist
                 const uint32_t there = raw_there[rs];
                 const bool whole = left >= BN && there == all_there;
                 const uint8_t* raw = smem + L::RAWS + rs * L::RAW;
@@ -1355,7 +1373,7 @@ static int64_t tree_partial(int dim) { return (int64_t)tree_rows(dim) * (tree_wi
 // an entry for each 32 rows of an item (a power of two: a growing batch seldom needs more than the last)
 static int64_t tree_redo(int64_t n_seq, int64_t n_tok, int n_heads, int n_kv, int dim) {
     const int R = tree_rows(dim);
-    const int64_t need = (n_tok * (n_heads / n_kv) / R + std::min<int64_t>({n_seq, n_tok, TREE_MAX_SEQ})) * n_kv * (R / 32);
+    const int64_t need = (n_tok * (n_heads / n_kv) / R + std::min<int64_t>({n_seq, n_tok, 512})) * n_kv * (R / 32);
     int64_t n = 4096;
     while (n < need) n *= 2;
     return n;
@@ -1376,6 +1394,7 @@ cudaError_t launch_attn_tree(const KvCache& c, const AttnDesc& a, int64_t n_seq,
     if (!encode) return cudaErrorNotSupported;
     const int g = a.n_heads / c.n_kv;
     const bool q_tma = g <= 128 && 128 % g == 0;
+    qm = CUtensorMap{};  // (unused else)
     if (q_tma) {
         cuuint64_t dims[3] = {(cuuint64_t)c.dim, (cuuint64_t)a.n_heads, (cuuint64_t)n_tok};
         cuuint64_t strides[2] = {(cuuint64_t)c.dim * 2, (cuuint64_t)a.q_stride * 2};
@@ -1384,8 +1403,6 @@ cudaError_t launch_attn_tree(const KvCache& c, const AttnDesc& a, int64_t n_seq,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
-    } else {
-        qm = CUtensorMap{};  // unused
     }
     if (!c.q8) {
         const int64_t page = int64_t(1) << c.page_shift;
@@ -1431,8 +1448,9 @@ cudaError_t launch_attn_tree(const KvCache& c, const AttnDesc& a, int64_t n_seq,
     // (a scale that is not positive takes the general path: the fast one scales the maximum)
     const bool mod = a.cap > 0.0f || a.slopes || !(a.scale > 0.0f);
     const JoinParams j{part, p.splits, p.n_splits, out, a.out_stride, tree_partial(c.dim), R, D, c.dim, g, a.out_f16};
-    for (int64_t s0 = 0; s0 < n_seq; s0 += TREE_MAX_SEQ) {
-        p.n_seq = (int)std::min<int64_t>(TREE_MAX_SEQ, n_seq - s0);
+    const int most = tree_max_seq(D, c.q8);
+    for (int64_t s0 = 0; s0 < n_seq; s0 += most) {
+        p.n_seq = (int)std::min<int64_t>(most, n_seq - s0);
         p.starts = starts + s0;
         p.pages = pages + s0 * max_pages;
         p.lens = lens + s0;

@@ -38,7 +38,7 @@
 
 namespace syn {
 
-constexpr int TREE_ITEM = 1;        // what an item's start and end cost, in tiles
+constexpr int TREE_ITEM = 2;        // what an item's start and end cost, in tiles
 constexpr int TREE_JOIN = 4;        // and a part's share of the join: what is no longer than the ranges by more is not split
 
 struct TreeRedo {  // rows to be computed again, when the CTA has done its items: a warp's rows of an item
@@ -58,7 +58,7 @@ struct TreeSplit {  // an item that several CTAs share
     int before, pad;                        // the join's tasks for the items listed before it
 };
 
-constexpr int JOIN_VALUES = 8;  // of 32 rows: a task of the join
+constexpr int JOIN_VALUES = 4;  // of 32 rows: a task of the join
 
 struct TreeParams {
     KvCache c;
@@ -108,18 +108,19 @@ struct TreeShape {
     static constexpr int BYTES = SEQS + (int)sizeof(TreeSeq) * (tree_max_seq(D, Q8) + 1);
     static constexpr int O_COL = QT == 2 ? 256 : 128;  // S slots below it
     static constexpr int SLOT = QT == 2 ? 128 : 64;    // columns of an S slot
-    // warps: softmax, then MMA, loader, scheduler and one that idles, then (Q8_0) eight that expand
-    static constexpr int MMA_WARP = 4 * QT, LOAD_WARP = MMA_WARP + 1, PLAN_WARP = MMA_WARP + 2, EXPAND_WARP = MMA_WARP + 4;
+    // warps: softmax, then one that idles, scheduler, loader and MMA (beside the softmax warps of the last rows, which few
+    // items have), then (Q8_0) eight that expand
+    static constexpr int SOFTMAX = 4 * QT, PLAN_WARP = SOFTMAX + 1, LOAD_WARP = SOFTMAX + 2, MMA_WARP = SOFTMAX + 3, EXPAND_WARP = SOFTMAX + 4;
     static constexpr int EXPANDERS = Q8 ? 8 : 0;
-    static constexpr int READERS = MMA_WARP + 2 + EXPANDERS;  // warps that follow the scheduler
-    static constexpr int WARPS = MMA_WARP + 4 + EXPANDERS, THREADS = 32 * WARPS;
+    static constexpr int READERS = SOFTMAX + 2 + EXPANDERS;  // warps that follow the scheduler
+    static constexpr int WARPS = SOFTMAX + 4 + EXPANDERS, THREADS = 32 * WARPS;
     // Registers a thread of each kind after the hand-over (their sum over the warps is what the launch gives them):
     // a softmax thread holds its row's 64 scores beside what masks, caps and biases them, and what it spills lies outside
     // what shared memory leaves of L1.
     static constexpr int LAUNCH_REGS = THREADS == 640 ? 96 : THREADS == 512 ? 128 : 168;
     static constexpr int SOFTMAX_REGS = !Q8 ? 208 : QT == 2 ? 136 : 232, MMA_REGS = !Q8 ? 88 : QT == 2 ? 80 : 88, EXPAND_REGS = QT == 2 ? 64 : 96;
     static constexpr bool HAND_OVER = QT == 2 || Q8;  // (else 8 warps, which have 255 each)
-    static_assert(!HAND_OVER || MMA_WARP * SOFTMAX_REGS + 4 * MMA_REGS + EXPANDERS * EXPAND_REGS <= WARPS * LAUNCH_REGS,
+    static_assert(!HAND_OVER || SOFTMAX * SOFTMAX_REGS + 4 * MMA_REGS + EXPANDERS * EXPAND_REGS <= WARPS * LAUNCH_REGS,
                   "more registers than the launch has");
     static constexpr int64_t PART = (int64_t)R * (D + 2);  // of a partial: [D][R] values, [R] maxima, [R] sums
 };
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
             mbar_init(smem_u32(&raw_empty[i]), L::EXPANDERS);
         }
         mbar_init(smem_u32(mma_idle), 1);
-        mbar_init(smem_u32(meet_bar), MMA_WARP);
+        mbar_init(smem_u32(meet_bar), L::SOFTMAX);
         *abort_flag = 0;
         info[0] = info[1] = info[2] = 0;
         fence_mbar_init();
@@ -379,8 +380,10 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
     auto work_of = [&](int s) {
         Work w{0, 0, 0};
         if (s >= p.n_seq) return w;
-        const int tok0 = p.starts[s], n_new = new_tokens(p.starts, s, p.n_tok), len = held_rows(p.lens[s], p.max_pages, p.c.page_shift);
-        const int prefix = p.prefix ? p.prefix[s] : 0;
+        // (all on their way together)
+        const int tok0 = __ldcg(p.starts + s), tok1 = __ldcg(p.starts + s + 1), rows = __ldcg(p.lens + s);
+        const int prefix = p.prefix ? __ldcg(p.prefix + s) : 0;
+        const int n_new = tok0 < 0 || tok1 > p.n_tok ? 0 : max(tok1 - tok0, 0), len = held_rows(rows, p.max_pages, p.c.page_shift);
         int first = 0;
         if (p.first && n_new > 0) {
             first = INT_MAX;
@@ -455,6 +458,19 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
         n_items++;
         return it.nt >= 0;
     };
+    // (what names the item's place in the call is fetched again at its end, which spares registers: the place is given
+    // back then)
+    auto hold_item = [&](TreeItem& it) {
+        const int slot = n_items & 1;
+        if (!mbar_wait(smem_u32(&item_full[slot]), (n_items >> 1) & 1, p.err, abort_flag)) return false;
+        it = tree_item(item_ints + 24 * slot);
+        return it.nt >= 0;
+    };
+    auto drop_item = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&item_empty[n_items & 1]));
+        n_items++;
+    };
     // two row tiles, a softmax group each; else one, and a half of each tile's keys each (D > 128: one group)
     auto two_tiles = [&](const TreeItem& it) { return QT == 2 && it.rows > 128; };
     // An item's tiles go up, or, with a bias by distance, from the last one down: the largest scores come
@@ -466,7 +482,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
     auto piece_v = [&](int i, int nt, bool two) { return two ? (i & 1) : i == 2 * nt - 1 || (i > 0 && (i & 1) == 0); };
     auto piece_tile = [&](int i, int nt, bool two) { return two ? i >> 1 : i == 2 * nt - 1 ? nt - 1 : i == 0 ? 0 : (i & 1) ? (i + 1) >> 1 : (i >> 1) - 1; };
 
-    if (warp < MMA_WARP) {
+    if (warp < L::SOFTMAX) {
         // ------------------------------------ softmax ------------------------------------------
         if (L::HAND_OVER) take_registers<L::SOFTMAX_REGS>();
         const int st = warp >> 2;  // group
@@ -486,24 +502,30 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
         };
         int redo_list = -1;
         TreeItem it{};
-        while (next_item(it)) {
+        while (hold_item(it)) {
             const bool two = two_tiles(it), halves = QT == 2 && !two;  // (halves: of a tile's keys)
             const int r = two ? tid : tid & 127;                       // row of the item
             const bool row_ok = r < it.rows, idle = (r & ~31) >= it.rows;  // (idle: the whole warp has none)
             const int context = it.len - it.n_new;
             Visible vis;
             vis.first = vis.pre = vis.low = vis.end = 0;
-            int pos = 0, node = 0, my_head = 0;
+            int pos = 0, node = 0;
+            float slope = 0.0f;
             if (row_ok) {
                 node = (it.row0 + r) / p.g;
-                my_head = it.h * p.g + (it.row0 + r - node * p.g);
+                if (MOD && p.slopes) slope = p.slopes[it.h * p.g + (it.row0 + r - node * p.g)] * 1.4426950408889634f;
                 pos = context + (p.window || (MOD && p.slopes) ? depth_of(p, it.tok0, node) : 0);
                 vis = visible_context(context, pos, p.first ? p.first[it.tok0 + node] : 0, it.prefix, p.window);
             }
-            const int64_t out0 = (int64_t)(it.tok0 + node) * p.out_stride + (int64_t)my_head * dim;
+            auto place_of = [&](const TreeItem& it) {  // of this thread's row
+                const int node = (it.row0 + r) / p.g;
+                return make_int2(it.tok0 + node, it.h * p.g + (it.row0 + r - node * p.g));
+            };
             if (it.nt == 0) {  // no row of the item sees a key
+                const int2 at = place_of(it);
                 if (row_ok && (two || st == 0))
-                    for (int e = 0; e < dim; e++) store_out(p, out0 + e, 0.0f);
+                    for (int e = 0; e < dim; e++) store_out(p, (int64_t)at.x * p.out_stride + (int64_t)at.y * dim + e, 0.0f);
+                drop_item();
                 continue;
             }
             if (!p.q_tma && (two || st == 0)) {
@@ -511,7 +533,8 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                 const int qt = two ? st : 0;
                 if (!mbar_wait(smem_u32(&q_empty[qt]), (q_turn & 1) ^ 1, p.err, abort_flag)) break;
                 uint8_t* qs = smem + L::Q + qt * L::Q_TILE + (tid & 127) * 128;
-                const uint4* qrow = reinterpret_cast<const uint4*>(p.q + (int64_t)(it.tok0 + node) * p.q_stride + (int64_t)my_head * dim);
+                const int2 place = place_of(it);
+                const uint4* qrow = reinterpret_cast<const uint4*>(p.q + (int64_t)place.x * p.q_stride + (int64_t)place.y * dim);
 #pragma unroll
                 for (int j0 = 0; j0 < D / 8; j0 += 8) {  // (8 loads on their way at a time)
                     uint4 w[8];
@@ -525,7 +548,6 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                 if (lane == 0) mbar_arrive(smem_u32(&q_full[qt]));
                 q_turn++;
             }
-            const float slope = MOD && p.slopes && row_ok ? p.slopes[my_head] * 1.4426950408889634f : 0.0f;
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
             for (int i = 0; i < it.nt && ok; i++) {
@@ -718,6 +740,10 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
             if (!ok || !mbar_wait(smem_u32(two ? &o_done[2 * st + 1] : &o_done[2 * st]), (two ? done2 - 1 : done - 1) & 1, p.err, abort_flag)) break;
             tc_fence_after();
             // ---- the item's end: a row's values, from one accumulator or (halves) two ------------------
+            it = tree_item(item_ints + 24 * (n_items & 1));
+            drop_item();
+            const int2 place = place_of(it);
+            const int64_t out0 = (int64_t)place.x * p.out_stride + (int64_t)place.y * dim;
             float f0 = 1.0f, f1 = 0.0f, all_l = l, all_m = m;
             if (halves) {
                 sums[st * 128 + r] = make_float2(m, l);
@@ -951,6 +977,18 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
         while (ok && next_item(it)) {
             if (it.nt == 0) continue;
             const bool two = two_tiles(it);
+#ifdef SYN_TEST_STALL
+            const int n_pieces = 0;  // timeout-test build: no tile is ever loaded, so the waits run out
+#else
+            const int n_pieces = 2 * it.nt;
+#endif
+            const int32_t* table = p.pages + (int64_t)it.s * p.max_pages;
+            auto first_key = [&](int i) { return it.tiles.at(it.t0 + turn_tile(piece_tile(i, it.nt, two), it.nt)) * BN + lane * box; };  // of this lane's box
+            auto look_up = [&](int i) {  // the page (asked for a piece ahead)
+                const int j = i < n_pieces ? first_key(i) : INT_MAX;
+                return lane < n_box && j < it.len ? __ldg(table + (j >> p.c.page_shift)) : -1;
+            };
+            int entry = look_up(0);
             if (p.q_tma) {
                 // 128 / g tokens of g heads: the row order of the item.  (Tokens past the call's are zeros;
                 // those of the next sequence are rows that nobody writes.)
@@ -968,18 +1006,6 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                     __syncwarp();
                 }
             }
-#ifdef SYN_TEST_STALL
-            const int n_pieces = 0;  // timeout-test build: no tile is ever loaded, so the waits run out
-#else
-            const int n_pieces = 2 * it.nt;
-#endif
-            const int32_t* table = p.pages + (int64_t)it.s * p.max_pages;
-            auto first_key = [&](int i) { return it.tiles.at(it.t0 + turn_tile(piece_tile(i, it.nt, two), it.nt)) * BN + lane * box; };  // of this lane's box
-            auto look_up = [&](int i) {  // the page (asked for a piece ahead)
-                const int j = i < n_pieces ? first_key(i) : INT_MAX;
-                return lane < n_box && j < it.len ? __ldg(table + (j >> p.c.page_shift)) : -1;
-            };
-            int entry = look_up(0);
             for (int i = 0; i < n_pieces && ok; i++, kc++) {
                 const int st = Q8 ? kc % max(NR, 1) : kc % NS;
                 const uint32_t turn = (uint32_t)(Q8 ? kc / max(NR, 1) : kc / NS);
@@ -1066,11 +1092,10 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
             it.slot = -1;
             int rest = 0;  // tiles of an item that others go on with
             if (at < to) {
-                int lo = 0, hi = p.n_seq - 1;  // the sequence
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if ((whole ? seqs[mid + 1].items_before : seqs[mid + 1].cost_before) > (int)at) hi = mid;
-                    else lo = mid + 1;
+                int lo = 0;  // the sequence: 32 at a time
+                for (uint32_t past = 0; !past; lo += past ? __ffs(past) - 1 : 32) {
+                    const TreeSeq* q = &seqs[min(lo + lane, p.n_seq - 1) + 1];
+                    past = __ballot_sync(0xffffffffu, (whole ? q->items_before : q->cost_before) > (int)at);
                 }
                 const TreeSeq q = seqs[lo];
                 it.s = lo;
@@ -1100,6 +1125,11 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                     at = min((int64_t)begin + each, to);
                 }
                 if (!mine) continue;
+                if (n == 0) {  // the loader's first look at the page table, ahead of it
+                    const int j = it.tiles.at(it.t0) * BN + lane * min(BN, 1 << p.c.page_shift);
+                    if (it.nt > 0 && lane * min(BN, 1 << p.c.page_shift) < BN && j < it.len)
+                        asm volatile("{\n\t.reg .b32 x;\n\tld.global.ca.b32 x, [%0];\n\t}" ::"l"(p.pages + (int64_t)it.s * p.max_pages + (j >> p.c.page_shift)));
+                }
                 // [mf, pre) and [ml, me): every key that some row sees lies in one of them
                 const int pre_end = min(max(it.prefix, 0), max(pos0, 0));
                 int mf = INT_MAX, ml = INT_MAX, me = 0;
@@ -1257,9 +1287,9 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
 
 // ---- the join of split items ---------------------------------------------------------------
 //
-// A warp joins 8 values of 32 rows of an item: the parts' weights from their maxima and sums, with their values, four
+// A warp joins 4 values of 32 rows of an item: the parts' weights from their maxima and sums, with their values, four
 // parts' loads on their way together.
-constexpr int JOIN_THREADS = 256, JOIN_MOST = 1024;
+constexpr int JOIN_THREADS = 256, JOIN_MOST = 1024, JOIN_PARTS = 4, JOIN_CTAS = 4;
 
 struct JoinParams {
     const float* part;
@@ -1270,7 +1300,7 @@ struct JoinParams {
     int R, D, dim, g, out_f16;
 };
 
-__global__ void __launch_bounds__(JOIN_THREADS) k_attn_tree_join(const JoinParams p) {
+__global__ void __launch_bounds__(JOIN_THREADS, JOIN_CTAS) k_attn_tree_join(const JoinParams p) {
     __shared__ int before[JOIN_MOST];
     griddep_release();
     griddep_wait();
@@ -1292,10 +1322,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_tree_join(const JoinParam
         float mx = -INFINITY, sum = 0.0f, acc[JOIN_VALUES];
 #pragma unroll
         for (int e = 0; e < JOIN_VALUES; e++) acc[e] = 0.0f;
-        for (int i0 = 0; i0 < x.parts; i0 += 4) {  // (the last batch repeats the last part's loads)
-            float m[4], l[4], o[4][JOIN_VALUES];
+        for (int i0 = 0; i0 < x.parts; i0 += JOIN_PARTS) {  // (the last batch repeats the last part's loads)
+            float m[JOIN_PARTS], l[JOIN_PARTS], o[JOIN_PARTS][JOIN_VALUES];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < JOIN_PARTS; i++) {
                 const float* q = part(min(i0 + i, x.parts - 1));
                 m[i] = __ldcg(q + (int64_t)p.D * p.R);
                 l[i] = __ldcg(q + (int64_t)(p.D + 1) * p.R);
@@ -1304,7 +1334,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_tree_join(const JoinParam
             }
             float nm = mx;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < JOIN_PARTS; i++) {
                 if (i0 + i >= x.parts) m[i] = -INFINITY;
                 nm = fmaxf(nm, m[i]);
             }
@@ -1314,7 +1344,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_tree_join(const JoinParam
 #pragma unroll
             for (int e = 0; e < JOIN_VALUES; e++) acc[e] *= f;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < JOIN_PARTS; i++) {
                 if (i0 + i >= x.parts) continue;
                 const float w = ex2(m[i] - ms);
                 sum = fmaf(l[i], w, sum);
@@ -1327,17 +1357,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_tree_join(const JoinParam
         const int t = (x.row0 + row) / p.g;
         const int64_t at = (int64_t)(x.tok0 + t) * p.out_stride + (int64_t)(x.h * p.g + x.row0 + row - t * p.g) * p.dim + e0;
         if (p.out_f16) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const __half2 hh = __floats2half2_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-                w[e] = *reinterpret_cast<const uint32_t*>(&hh);
-            }
-            *reinterpret_cast<uint4*>(static_cast<__half*>(p.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            const __half2 a = __floats2half2_rn(acc[0] * inv, acc[1] * inv), b = __floats2half2_rn(acc[2] * inv, acc[3] * inv);
+            *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
         } else {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-            dst[0] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-            dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
         }
     }
     // the last CTA to get here makes the count ready for the next call
@@ -1466,7 +1490,7 @@ cudaError_t launch_attn_tree(const KvCache& c, const AttnDesc& a, int64_t n_seq,
         if (e != cudaSuccess) return e;
         ++*launches;
         if (!p.split) continue;
-        e = launch_overlapped(k_attn_tree_join, 2 * sms, JOIN_THREADS, 0, s, j);
+        e = launch_overlapped(k_attn_tree_join, JOIN_CTAS * sms, JOIN_THREADS, 0, s, j);
         if (e != cudaSuccess) return e;
         ++*launches;
     }

@@ -369,6 +369,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
         fence_mbar_init();
     }
     if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_slot), 512);
+    if (warp == LOAD_WARP && lane < 3) prefetch_map(lane == 0 ? &kmap : lane == 1 ? &vmap : &qmap);
     griddep_release();
     griddep_wait();
 

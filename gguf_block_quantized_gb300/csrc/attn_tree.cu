@@ -305,7 +305,12 @@ __device__ __noinline__ void tree_rows_by_hand(const TreeParams& p, const TreeRe
     }
 }
 
-template <int D, bool Q8, bool MOD>
+// What happens to scores besides their scale: nothing, a cap, or all there is (biases, scales that are not positive).  A
+// kernel with all of it is slower without it: the code that it jumps over (48 sequences over Q8_0, capped: 160 us,
+// not 147).
+enum { PLAIN = 0, CAPPED = 1, GENERAL = 2 };
+
+template <int D, bool Q8, int MOD>
 __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
     k_attn_tree(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const __grid_constant__ CUtensorMap qmap, const __grid_constant__ TreeParams p) {
@@ -476,7 +481,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
     auto two_tiles = [&](const TreeItem& it) { return QT == 2 && it.rows > 128; };
     // An item's tiles go up, or, with a bias by distance, from the last one down: the largest scores come
     // first, and O is not rescaled tile after tile.
-    auto turn_tile = [&](int i, int nt) { return MOD && p.slopes ? nt - 1 - i : i; };
+    auto turn_tile = [&](int i, int nt) { return MOD == GENERAL && p.slopes ? nt - 1 - i : i; };
 
     // The ring's order: K of the first tile, then (two row tiles) V and the next K, or (one) the
     // next K and V.  Piece i of an item's 2*nt: is it V, and of which tile.
@@ -514,8 +519,8 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
             float slope = 0.0f;
             if (row_ok) {
                 node = (it.row0 + r) / p.g;
-                if (MOD && p.slopes) slope = p.slopes[it.h * p.g + (it.row0 + r - node * p.g)] * 1.4426950408889634f;
-                pos = context + (p.window || (MOD && p.slopes) ? depth_of(p, it.tok0, node) : 0);
+                if (MOD == GENERAL && p.slopes) slope = p.slopes[it.h * p.g + (it.row0 + r - node * p.g)] * 1.4426950408889634f;
+                pos = context + (p.window || (MOD == GENERAL && p.slopes) ? depth_of(p, it.tok0, node) : 0);
                 vis = visible_context(context, pos, p.first ? p.first[it.tok0 + node] : 0, it.prefix, p.window);
             }
             auto place_of = [&](const TreeItem& it) {  // of this thread's row
@@ -592,7 +597,7 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                     TMEM_LD_WAIT32(v);
                     TMEM_LD_WAIT32((v + 32));
                     if (MOD) {
-                        if (p.cap > 0.0f) {
+                        if (MOD == CAPPED || p.cap > 0.0f) {
                             // Scores up to half the cap in size: tanh(y) = y times a polynomial in y^2, fitted on
                             // [0, 1/2] to 3e-7, the scale and the cap folded into its coefficients; past it the
                             // general form.  Each score goes by its own size, so that its bits do not depend on
@@ -648,31 +653,33 @@ __global__ void __launch_bounds__(TreeShape<D, Q8>::THREADS, 1)
                                 }
                             }
                         }
-                        // (not capped: still to be scaled; c_log2 or 1)
-                        const float to_scale = p.cap > 0.0f ? 1.0f : c_log2;
-                        if (p.slopes && drafts) {  // (the context's keys by position, the chain's by how many of it are nearer)
+                        if (MOD == GENERAL) {
+                            // (not capped: still to be scaled; c_log2 or 1)
+                            const float to_scale = p.cap > 0.0f ? 1.0f : c_log2;
+                            if (p.slopes && drafts) {  // (the context's keys by position, the chain's by how many of it are nearer)
 #pragma unroll
-                            for (int c = 0; c < 64; c++) {
-                                const int b = c & 31, of_chain = nearer + (c < 32 ? __popc(chain[1]) : 0) + (b < 31 ? __popc(chain[c >> 5] >> (b + 1)) : 0);
-                                const float by = (float)(j0 + c < context ? pos - j0 - c : of_chain);
-                                v[c] = __float_as_uint(fmaf(-slope, by, __uint_as_float(v[c]) * to_scale));
+                                for (int c = 0; c < 64; c++) {
+                                    const int b = c & 31, of_chain = nearer + (c < 32 ? __popc(chain[1]) : 0) + (b < 31 ? __popc(chain[c >> 5] >> (b + 1)) : 0);
+                                    const float by = (float)(j0 + c < context ? pos - j0 - c : of_chain);
+                                    v[c] = __float_as_uint(fmaf(-slope, by, __uint_as_float(v[c]) * to_scale));
+                                }
+                            } else if (p.slopes) {
+                                // the distance is far - c, two scores at a time (c counts in whole numbers, exactly)
+                                const float far = (float)(pos - j0);
+                                uint64_t c2 = pack2(0.0f, 1.0f);
+                                const uint64_t two2 = pack2(2.0f, 2.0f), s2 = pack2(slope, slope), f2 = pack2(-slope * far, -slope * far);
+                                const uint64_t l2 = pack2(to_scale, to_scale);
+#pragma unroll
+                                for (int c = 0; c < 64; c += 2) {
+                                    const float2 x = unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), l2, fma2(c2, s2, f2)));
+                                    v[c] = __float_as_uint(x.x);
+                                    v[c + 1] = __float_as_uint(x.y);
+                                    c2 = add2(c2, two2);
+                                }
+                            } else if (!(p.cap > 0.0f)) {  // (a scale that is not positive)
+#pragma unroll
+                                for (int c = 0; c < 64; c++) v[c] = __float_as_uint(__uint_as_float(v[c]) * to_scale);
                             }
-                        } else if (p.slopes) {
-                            // the distance is far - c, two scores at a time (c counts in whole numbers, exactly)
-                            const float far = (float)(pos - j0);
-                            uint64_t c2 = pack2(0.0f, 1.0f);
-                            const uint64_t two2 = pack2(2.0f, 2.0f), s2 = pack2(slope, slope), f2 = pack2(-slope * far, -slope * far);
-                            const uint64_t l2 = pack2(to_scale, to_scale);
-#pragma unroll
-                            for (int c = 0; c < 64; c += 2) {
-                                const float2 x = unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), l2, fma2(c2, s2, f2)));
-                                v[c] = __float_as_uint(x.x);
-                                v[c + 1] = __float_as_uint(x.y);
-                                c2 = add2(c2, two2);
-                            }
-                        } else if (!(p.cap > 0.0f)) {  // (a scale that is not positive)
-#pragma unroll
-                            for (int c = 0; c < 64; c++) v[c] = __float_as_uint(__uint_as_float(v[c]) * to_scale);
                         }
                     }
                     if (masked) {
@@ -1372,7 +1379,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, JOIN_CTAS) k_attn_tree_join(cons
 
 // ---- host side ---------------------------------------------------------------------------
 
-template <int D, bool Q8, bool MOD>
+template <int D, bool Q8, int MOD>
 static cudaError_t run_tree(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm, const TreeParams& p, int grid, cudaStream_t s) {
     auto kern = k_attn_tree<D, Q8, MOD>;
     constexpr int smem = 1024 + TreeShape<D, Q8>::BYTES;
@@ -1471,7 +1478,7 @@ cudaError_t launch_attn_tree(const KvCache& c, const AttnDesc& a, int64_t n_seq,
     p.idesc_s = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | (8u << 24);
     p.idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(c.dim >> 3) << 17) | (8u << 24);
     // (a scale that is not positive takes the general path: the fast one scales the maximum)
-    const bool mod = a.cap > 0.0f || a.slopes || !(a.scale > 0.0f);
+    const int mod = a.slopes || !(a.scale > 0.0f) ? GENERAL : a.cap > 0.0f ? CAPPED : PLAIN;
     const JoinParams j{part, p.splits, p.n_splits, out, a.out_stride, tree_partial(c.dim), R, D, c.dim, g, a.out_f16};
     const int most = tree_max_seq(D, c.q8);
     for (int64_t s0 = 0; s0 < n_seq; s0 += most) {
@@ -1483,11 +1490,14 @@ cudaError_t launch_attn_tree(const KvCache& c, const AttnDesc& a, int64_t n_seq,
         // (more items than this many have a row number past 32 bits)
         if (((n_tok * p.g + R - 1) / R + p.n_seq) * c.n_kv > INT_MAX) return cudaErrorInvalidValue;
         cudaError_t e;
-#define SYN_TREE(D)                                                                                     \
-    (c.q8 ? (mod ? run_tree<D, true, true>(km, vm, qm, p, sms, s) : run_tree<D, true, false>(km, vm, qm, p, sms, s)) \
-          : (mod ? run_tree<D, false, true>(km, vm, qm, p, sms, s) : run_tree<D, false, false>(km, vm, qm, p, sms, s)))
+#define SYN_TREE_MOD(D, Q8)                                                    \
+    (mod == PLAIN    ? run_tree<D, Q8, PLAIN>(km, vm, qm, p, sms, s)           \
+     : mod == CAPPED ? run_tree<D, Q8, CAPPED>(km, vm, qm, p, sms, s)          \
+                     : run_tree<D, Q8, GENERAL>(km, vm, qm, p, sms, s))
+#define SYN_TREE(D) (c.q8 ? SYN_TREE_MOD(D, true) : SYN_TREE_MOD(D, false))
         e = D == 64 ? SYN_TREE(64) : D == 128 ? SYN_TREE(128) : SYN_TREE(256);
 #undef SYN_TREE
+#undef SYN_TREE_MOD
         if (e != cudaSuccess) return e;
         ++*launches;
         if (!p.split) continue;

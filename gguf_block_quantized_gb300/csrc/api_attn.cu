@@ -375,21 +375,21 @@ int syn_kv_compact(const syn_kv_cache* cache, const int32_t* refs, int64_t n_seq
     if (!aligned(refs, 4) || !aligned(pages, 4) || !aligned(base, 4) || !aligned(starts, 4) || !aligned(rows, 4) ||
         !aligned(new_lens, 4))
         return SYN_ERR_ALIGN;
-    const int64_t scratch_words = syn::compact_scratch_words(c, n_rows);
-    if (scratch_words < 0) return SYN_ERR_SHAPE;
+    const int64_t count_words = syn::compact_count_words(c, n_seq, n_rows);
+    if (count_words < 0) return SYN_ERR_SHAPE;
     int sms, *words;
     rc = syn::call_state(&sms, &words);
     if (rc) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int* count;
-    float* scratch = nullptr;
-    if (scratch_words) {
-        rc = scratch_for(s, 1, scratch_words, &count, &scratch);
+    int* count = nullptr;
+    float* part;
+    if (count_words) {
+        rc = scratch_for(s, count_words, 1, &count, &part);
         if (rc) return rc;
     }
     int launches = 0;
     rc = check_cuda(syn::launch_kv_compact(c, refs, n_seq, n_rows, pages, max_pages, base, starts, rows, new_lens,
-                                           reinterpret_cast<int*>(scratch), words, sms, &launches, s));
+                                           count, words, sms, &launches, s));
     syn::note_launches(launches);
     return rc;
 }

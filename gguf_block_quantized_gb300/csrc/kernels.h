@@ -135,8 +135,9 @@ cudaError_t launch_kv_extend(const KvCache& c, int32_t* refs, int64_t n_seq, int
 int64_t extend_items(const KvCache& c, int64_t n_seq, int64_t n_tok);
 cudaError_t launch_kv_compact(const KvCache& c, const int32_t* refs, int64_t n_seq, int64_t n_rows, const int32_t* pages,
                               int64_t max_pages, const int32_t* base, const int32_t* starts, const int32_t* rows,
-                              int32_t* new_lens, int* scratch, int* err, int sms, int* launches, cudaStream_t s);
-int64_t compact_scratch_words(const KvCache& c, int64_t n_rows);  // (0: none is needed; -1: too long a list)
+                              int32_t* new_lens, int* count, int* err, int sms, int* launches, cudaStream_t s);
+// count's words, zero before the first call and left zero by every call (0: none is needed; -1: too long a list).
+int64_t compact_count_words(const KvCache& c, int64_t n_seq, int64_t n_rows);
 cudaError_t launch_kv_copy(const KvCache& from, const KvCache& to, int64_t n, const int32_t* src, const int32_t* dst, int* err,
                            int sms, cudaStream_t s);
 

@@ -5,8 +5,10 @@
 // in the order of sequences and columns, so that what a call does depends on its arguments alone,
 // whatever the order of the atomics.
 //
-// Bound: the tables are a few KB, so fork, extend and trim are their launches' latency; rows and pages
-// move at HBM's rate, read and written once.
+// Bound: the tables are a few KB, so fork, extend and trim are their launches' latency and a chain of dependent loads (from
+// a graph on GB300: trim, fork and extend of 4 beams 10.8 us; extend, compact and trim of the drafts of 64
+// sequences 13.1 us).  Rows and pages are read and written once: 733 MB of pages copied in 108 us (6.8 TB/s);
+// 254 MB of single rows of 128 bytes packed in 55 us (4.6 TB/s).
 #include <algorithm>
 #include <climits>
 
@@ -109,9 +111,11 @@ cudaError_t launch_kv_trim(const KvCache& c, int32_t* refs, int64_t n_seq, int32
 //   2. the free pages are listed, lowest first, as many as are needed;
 //   3. where they suffice the items take them in order; where they do not, nobody keeps a shared page, and
 //      the sequences whose needs, summed up to them, fit, take theirs.
-// The second kernel gives out the slots and copies the rows of first pages that were shared.
+// A second kernel gives out the slots and copies the rows of first pages that were shared.  (One kernel, in which
+// the other CTAs wait for the plan behind a flag, took longer: trim, fork and extend of 4 beams, from a graph, 14.1 us and
+// not 10.8; the accepted drafts of 64 sequences 22.4 and not 18.9.)
 
-constexpr int EXT_THREADS = 1024;
+constexpr int EXT_THREADS = 512;  // of the plan
 
 struct ExtendParams {
     KvCache c;
@@ -138,6 +142,7 @@ __device__ __forceinline__ int new_rows(const ExtendParams& p, int s) {
 
 // The inclusive sum over the CTA's threads, and their total.
 __device__ __forceinline__ int block_sum(int x, int* sums, int& total) {
+    constexpr int WARPS = EXT_THREADS / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -147,23 +152,36 @@ __device__ __forceinline__ int block_sum(int x, int* sums, int& total) {
     __syncthreads();  // (the sums before this one have been read)
     if (lane == 31) sums[warp] = x;
     __syncthreads();
-    int w = sums[lane];
+    int w = lane < WARPS ? sums[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < WARPS; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += y;
     }
-    total = __shfl_sync(0xffffffffu, w, 31);
+    total = __shfl_sync(0xffffffffu, w, WARPS - 1);
     const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
     return x + (warp > 0 ? before : 0);
 }
 
-__global__ void __launch_bounds__(EXT_THREADS) k_kv_extend_plan(const ExtendParams p) {
-    __shared__ int off[KV_EXTEND_SEQS + 1];  // items before each sequence
-    __shared__ int sums[32];
+// Which of counts[at .. at + 8) are 0.
+__device__ __forceinline__ int free_of(const int32_t* counts, int64_t at, int64_t n) {
+    int bits = 0;
+    if (at + 8 <= n && (reinterpret_cast<uintptr_t>(counts + at) & 15) == 0) {
+        const int4 a = __ldcg(reinterpret_cast<const int4*>(counts + at)), b = __ldcg(reinterpret_cast<const int4*>(counts + at) + 1);
+        const int x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; i++) bits |= x[i] == 0 ? 1 << i : 0;
+    } else {
+        for (int i = 0; i < 8; i++)
+            if (at + i < n && __ldcg(counts + at + i) == 0) bits |= 1 << i;
+    }
+    return bits;
+}
+
+__device__ void plan_pages(const ExtendParams& p, int* off, int* sums) {
     const int tid = threadIdx.x, shift = p.c.page_shift, page = 1 << shift;
-    griddep_release();
-    griddep_wait();
+    // (the first counts, on their way; a page that this call takes off its holders is not free for it)
+    const int bits0 = free_of(p.refs, (int64_t)tid * 8, p.c.n_pages);
     // ---- the items ---------------------------------------------------------------------------
     int items = 0;
     if (tid == 0) off[0] = 0;
@@ -192,21 +210,32 @@ __global__ void __launch_bounds__(EXT_THREADS) k_kv_extend_plan(const ExtendPara
         }
         return;
     }
-    auto sequence_of = [&](int u) {
+    volatile int32_t* refs = p.refs;
+    struct Item {
+        int s, id;
+        int64_t entry;
+    };
+    auto fetch = [&](int u) {
+        Item x{0, -1, 0};
+        if (u >= items) return x;
         int lo = 0, hi = p.n_seq - 1;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (off[mid + 1] > u) hi = mid;
             else lo = mid + 1;
         }
-        return lo;
+        x.s = lo;
+        x.entry = (int64_t)lo * p.max_pages + (p.plan[lo].z >> shift) + (u - off[lo]);
+        x.id = p.pages[x.entry];
+        return x;
     };
-    auto entry_of = [&](int u, int s) { return (int64_t)s * p.max_pages + (p.plan[s].z >> shift) + (u - off[s]); };
-    volatile int32_t* refs = p.refs;
+    // (a thread's first item, mostly its only one, stays in registers)
+    const Item mine = fetch(tid);
+    auto item = [&](int u) { return u == tid ? mine : fetch(u); };
     // ---- missing and shared ------------------------------------------------------------------
     int any_shared = 0;
     for (int u = tid; u < items; u += EXT_THREADS) {
-        const int id = p.pages[entry_of(u, sequence_of(u))];
+        const int id = item(u).id;
         int what = 1;
         if ((unsigned)id < (unsigned)p.c.n_pages) {
             what = refs[id] > 1 ? 2 : 0;
@@ -219,11 +248,11 @@ __global__ void __launch_bounds__(EXT_THREADS) k_kv_extend_plan(const ExtendPara
     any_shared = __syncthreads_or(any_shared);
     if (any_shared) {
         for (int u = tid; u < items; u += EXT_THREADS)
-            if (p.need[u] == 2) atomicSub(p.refs + p.pages[entry_of(u, sequence_of(u))], 1);
+            if (p.need[u] == 2) atomicSub(p.refs + item(u).id, 1);
         __syncthreads();
         for (int u = tid; u < items; u += EXT_THREADS)
             if (p.need[u] == 2) {
-                const int id = p.pages[entry_of(u, sequence_of(u))];
+                const int id = item(u).id;
                 if (refs[id] <= 0) atomicMin(p.refs + id, -1 - u);
             }
         __syncthreads();
@@ -233,17 +262,12 @@ __global__ void __launch_bounds__(EXT_THREADS) k_kv_extend_plan(const ExtendPara
     int wanted = 0;
     for (int u0 = 0; u0 < items; u0 += EXT_THREADS) {
         const int u = u0 + tid, what = u < items ? p.need[u] : 0;
-        const bool want = what == 1 || (what == 2 && !keeps(u, p.pages[entry_of(u, sequence_of(u))]));
-        wanted += __syncthreads_count(want);
+        wanted += __syncthreads_count(what == 1 || (what == 2 && !keeps(u, item(u).id)));
     }
     int n_free = 0;
-    constexpr int EACH = 8;  // counts a thread looks at, in a row
-    for (int64_t b = 0; b < p.c.n_pages && n_free < wanted; b += EXT_THREADS * EACH) {
-        const int64_t at = b + (int64_t)tid * EACH;
-        int bits = 0;
-#pragma unroll
-        for (int i = 0; i < EACH; i++)
-            if (at + i < p.c.n_pages && refs[at + i] == 0) bits |= 1 << i;
+    for (int64_t b = 0; b < p.c.n_pages && n_free < wanted; b += EXT_THREADS * 8) {
+        const int64_t at = b + (int64_t)tid * 8;
+        int bits = b == 0 ? bits0 : free_of(p.refs, at, p.c.n_pages);
         int total;
         int rank = n_free + block_sum(__popc(bits), sums, total) - __popc(bits);
         n_free += total;
@@ -260,7 +284,7 @@ __global__ void __launch_bounds__(EXT_THREADS) k_kv_extend_plan(const ExtendPara
             int total;
             const int what = u < items ? p.need[u] : 0, sum = base + block_sum(what != 0, sums, total);
             if (what == 2) {
-                const int id = p.pages[entry_of(u, sequence_of(u))];
+                const int id = item(u).id;
                 if (keeps(u, id)) refs[id] = 0;
             }
             if (u < items) p.need[u] = sum << 2 | what;
@@ -273,30 +297,29 @@ __global__ void __launch_bounds__(EXT_THREADS) k_kv_extend_plan(const ExtendPara
         }
         __syncthreads();
         for (int u = tid; u < items; u += EXT_THREADS) {
-            const int s = sequence_of(u);
-            if ((p.need[u] & 3) == 2 && !p.plan[s].w) atomicAdd(p.refs + p.pages[entry_of(u, s)], 1);
+            const Item x = item(u);
+            if ((p.need[u] & 3) == 2 && !p.plan[x.s].w) atomicAdd(p.refs + x.id, 1);
         }
         __syncthreads();
     }
     // ---- the pages dealt out -----------------------------------------------------------------
     int given = 0;
     for (int u0 = 0; u0 < items; u0 += EXT_THREADS) {
-        const int u = u0 + tid, s = u < items ? sequence_of(u) : 0;
-        const int what = u < items && p.plan[s].w ? p.need[u] & 3 : 0;
-        const int64_t entry = u < items ? entry_of(u, s) : 0;
-        const int id = what ? p.pages[entry] : -1;
-        const bool kept = enough && what == 2 && keeps(u, id), take = what && !kept;
+        const int u = u0 + tid;
+        const Item x = item(u);
+        const int what = u < items && (enough || p.plan[x.s].w) ? p.need[u] & 3 : 0;
+        const bool kept = enough && what == 2 && keeps(u, x.id), take = what && !kept;
         int total;
         const int rank = given + block_sum(take, sums, total) - 1;
         given += total;
-        if (kept) refs[id] = 1;
+        if (kept) refs[x.id] = 1;
         if (take) {
             const int got = p.free_list[rank];
             refs[got] = 1;
-            p.pages[entry] = got;
-            if (what == 2 && u == off[s]) {
-                p.plan[s].x = id;
-                p.plan[s].y = got;
+            p.pages[x.entry] = got;
+            if (what == 2 && u == off[x.s]) {
+                p.plan[x.s].x = x.id;
+                p.plan[x.s].y = got;
             }
         }
     }
@@ -307,6 +330,13 @@ __global__ void __launch_bounds__(EXT_THREADS) k_kv_extend_plan(const ExtendPara
     }
 }
 
+__global__ void __launch_bounds__(EXT_THREADS) k_kv_extend_plan(const ExtendParams p) {
+    __shared__ int off[KV_EXTEND_SEQS + 1];
+    __shared__ int sums[32];
+    griddep_release();
+    griddep_wait();
+    plan_pages(p, off, sums);
+}
 __global__ void __launch_bounds__(PG_THREADS) k_kv_extend_rows(const ExtendParams p) {
     const int shift = p.c.page_shift, page = 1 << shift, tid = threadIdx.x;
     griddep_release();
@@ -324,8 +354,8 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_extend_rows(const ExtendParam
                 lo = (int)t;
             }
             const int64_t at = p.starts ? t - p.starts[lo] : 0;
-            const int4 a = p.plan[lo];
             int64_t slot = -1;
+            const int4 a = p.plan[lo];
             if (a.w && at >= 0 && at < new_rows(p, lo)) {
                 const int row = a.z + (int)at;
                 slot = ((int64_t)p.pages[lo * p.max_pages + (row >> shift)] << shift) + (row & (page - 1));
@@ -377,24 +407,29 @@ cudaError_t launch_kv_extend(const KvCache& c, int32_t* refs, int64_t n_seq, int
     if (e != cudaSuccess) return e;
     ++*launches;
     const int64_t work = std::max<int64_t>((slots ? n_tok + PG_THREADS - 1 : 0) / PG_THREADS, n_seq * 2 * c.n_kv);
-    e = launch_overlapped(k_kv_extend_rows, (int)std::min<int64_t>(work, (int64_t)sms * 8), PG_THREADS, 0, s, p);
+    e = launch_overlapped(k_kv_extend_rows, (int)std::min<int64_t>(work, 2 * sms), PG_THREADS, 0, s, p);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
 
 // ---- compact -----------------------------------------------------------------------------
 //
-// Rows move down in place: row base + i comes from base + rows[i] >= base + i.  A CTA has a sequence's tile
-// column (a kv head, keys or values, some 16-byte pieces of each row) to itself and goes through
+// Rows move down in place: row base + i comes from base + rows[i] >= base + i.  A CTA has columns of a sequence's
+// tiles (a tile: a kv head, keys or values; a column: some 16-byte pieces of each row) to itself and goes through
 // the rows in order, a batch loaded whole before any of it is stored: what a batch overwrites are rows
-// that it or a batch before has loaded, so no CTA waits for another.
+// that it or a batch before has loaded, so no CTA waits for another.  Short lists are a chain of dependent loads
+// (starts, rows, page ids, counts, rows): what makes a call longer is the CTAs it takes to start.
 
 constexpr int CMP_THREADS = 256;
 constexpr int CMP_ROWS = 256;   // rows of a batch
-constexpr int CMP_CHUNK = 64;   // most rows of a chunk of a long list
+// Most rows of a chunk of a long list (3 sequences of 21001 to 60001 Q8_0 rows, half kept: 16, 32, 64, 128 rows: 57.0, 55.7,
+// 58.0, 68.5 us).
+constexpr int CMP_CHUNK = 32;
 constexpr int CMP_UNITS = 8;    // pieces a thread holds
+constexpr int CMP_SHORT = 4;    // and of a short one (8: 114 registers, which leave two CTAs an SM)
 constexpr int CMP_SCALES = 4;   // and pieces of scales
-constexpr int CMP_CTAS = 4;     // of an SM, for long lists
+constexpr int CMP_CTAS = 4;     // of an SM, for long lists (2, 3, 4: 68.1, 59.4, 57.0 us)
+constexpr int CMP_TARGET = 3;   // and for short ones (64 sequences, 2048 and 4096 F16 rows: 2: 5.8, 8.8 us, 3: 4.8, 7.1 us)
 
 struct CompactParams {
     KvCache c;
@@ -406,47 +441,53 @@ struct CompactParams {
     int32_t* new_lens;
     int* err;
     int64_t max_pages, n_rows;
-    int n_seq, cut, width;  // columns a tile is cut into (Q8_0: and one of scales), 16-byte pieces of one
+    int n_seq, cut, width, group;  // columns a tile is cut into, 16-byte pieces of one; tiles of a CTA
+    int apart;                     // (Q8_0) the scales are a column more, not the last one's
 };
 
 template <typename U>
-__device__ __forceinline__ void move_rows(const CompactParams& p, uint8_t* tiles, int64_t plane, int pitch, int first, int width,
-                                          const int64_t* src, const int64_t* dst, int n) {
-    const int units = n * width;
-    U held[CMP_UNITS];
-    for (int u0 = 0; u0 < units; u0 += CMP_THREADS * CMP_UNITS) {
+__device__ __forceinline__ void move_rows(const CompactParams& p, int tile0, int n_tiles, int first, int width, const int64_t* src,
+                                          const int64_t* dst, int n) {
+    const int each = n * width, units = n_tiles * each;
+    // unit u is piece x of row r of tile t; the next of a thread is CMP_THREADS on
+    const int dt = CMP_THREADS / each, dr = (CMP_THREADS - dt * each) / width, dx = CMP_THREADS - dt * each - dr * width;
+    int t = threadIdx.x / each, r = (threadIdx.x - t * each) / width, x = threadIdx.x - t * each - r * width;
+    auto on = [&]() {
+        x += dx, r += dr, t += dt;
+        if (x >= width) x -= width, r++;
+        if (r >= n) r -= n, t++;
+    };
+    auto at = [&](int64_t row) {
+        const int tile = tile0 + t;
+        return reinterpret_cast<U*>((tile & 1 ? p.c.v : p.c.k) + row + (tile >> 1) * p.c.tile) + first + x;
+    };
+    U held[CMP_SHORT];
+    for (int u0 = 0; u0 < units; u0 += CMP_THREADS * CMP_SHORT) {
+        const int t0 = t, r0 = r, x0 = x;
 #pragma unroll
-        for (int i = 0; i < CMP_UNITS; i++) {
-            const int u = u0 + i * CMP_THREADS + threadIdx.x, r = u / width, x = first + u - r * width;
-            if (u < units && src[r] >= 0) {
-                const int64_t cell = src[r] & ((int64_t(1) << p.c.page_shift) - 1);
-                held[i] = reinterpret_cast<const U*>(tiles + (src[r] >> p.c.page_shift) * p.c.page_stride + plane + cell * pitch)[x];
-            }
-        }
+        for (int i = 0; i < CMP_SHORT; i++, on())
+            if (t < n_tiles && src[r] >= 0) held[i] = *at(src[r]);
         __syncthreads();
+        t = t0, r = r0, x = x0;
 #pragma unroll
-        for (int i = 0; i < CMP_UNITS; i++) {
-            const int u = u0 + i * CMP_THREADS + threadIdx.x, r = u / width, x = first + u - r * width;
-            if (u < units && src[r] >= 0) {
-                const int64_t cell = dst[r] & ((int64_t(1) << p.c.page_shift) - 1);
-                reinterpret_cast<U*>(tiles + (dst[r] >> p.c.page_shift) * p.c.page_stride + plane + cell * pitch)[x] = held[i];
-            }
-        }
+        for (int i = 0; i < CMP_SHORT; i++, on())
+            if (t < n_tiles && src[r] >= 0) *at(dst[r]) = held[i];
     }
 }
 
-__global__ void __launch_bounds__(CMP_THREADS) k_kv_compact(const CompactParams p) {
-    __shared__ int64_t src[CMP_ROWS], dst[CMP_ROWS];  // slots; -1: the row stays
-    const int tid = threadIdx.x, shift = p.c.page_shift, per = p.cut + p.c.q8;
+__global__ void __launch_bounds__(CMP_THREADS, 4) k_kv_compact(const CompactParams p) {
+    // where a row's values are in a pool's tile 0, and (Q8_0) its scales; -1: the row stays
+    __shared__ int64_t src[CMP_ROWS], dst[CMP_ROWS], src_s[CMP_ROWS], dst_s[CMP_ROWS];
+    const int tid = threadIdx.x, shift = p.c.page_shift, tiles = 2 * p.c.n_kv, groups = (tiles + p.group - 1) / p.group,
+              per = p.cut + p.apart;
     griddep_release();
     griddep_wait();
-    for (int unit = blockIdx.x; unit < p.n_seq * per * 2 * p.c.n_kv; unit += gridDim.x) {
-        const int column = unit % per, tile = unit / per % (2 * p.c.n_kv), s = unit / (per * 2 * p.c.n_kv);
+    for (int unit = blockIdx.x; unit < p.n_seq * per * groups; unit += gridDim.x) {
+        const int column = unit % per, tile0 = unit / per % groups * p.group, s = unit / (per * groups);
         const int a = p.starts[s], b = p.starts[s + 1], n = a < 0 || b > p.n_rows ? 0 : max(b - a, 0);
-        const int base = max(p.base[s], 0);
-        const bool tells = column == 0 && tile == 0;
+        const int base = max(p.base[s], 0), n_tiles = min(p.group, tiles - tile0);
+        const bool tells = column == 0 && tile0 == 0;
         if (tells && tid == 0) p.new_lens[s] = (int)min((int64_t)base + n, (int64_t)INT_MAX);
-        uint8_t* tiles = (tile & 1 ? p.c.v : p.c.k) + (tile >> 1) * p.c.tile;
         const int32_t* table = p.pages + (int64_t)s * p.max_pages;
         const int64_t held = min(p.max_pages << shift, (int64_t)INT_MAX);
         auto slot_of = [&](int64_t row) -> int64_t {
@@ -474,185 +515,241 @@ __global__ void __launch_bounds__(CMP_THREADS) k_kv_compact(const CompactParams 
                         if (tells) record_error(p.err, SYN_DEVERR_BOUNDS);
                     }
                 }
-                src[i] = from;
-                dst[i] = to;
+                const int64_t cells = (int64_t(1) << shift) - 1, pitch = p.c.q8 ? p.c.dim : 2 * p.c.dim;
+                const int64_t f = (from >> shift) * p.c.page_stride, o = (to >> shift) * p.c.page_stride;
+                src[i] = from < 0 ? -1 : f + (from & cells) * pitch;
+                dst[i] = o + (to & cells) * pitch;
+                if (p.c.q8) {
+                    src_s[i] = from < 0 ? -1 : f + ((int64_t)p.c.dim << shift) + (from & cells) * (p.c.dim >> 4);
+                    dst_s[i] = o + ((int64_t)p.c.dim << shift) + (to & cells) * (p.c.dim >> 4);
+                }
             }
             __syncthreads();
-            if (column < p.cut) {
-                const int pieces = p.c.dim >> (p.c.q8 ? 4 : 3), first = column * p.width;
-                move_rows<uint4>(p, tiles, 0, pieces * 16, first, min(p.width, pieces - first), src, dst, m);
-            } else {
-                move_rows<uint16_t>(p, tiles, (int64_t)p.c.dim << shift, p.c.dim >> 4, 0, p.c.dim >> 5, src, dst, m);
-            }
+            const int pieces = p.c.dim >> (p.c.q8 ? 4 : 3), first = column * p.width;
+            if (column < p.cut) move_rows<uint4>(p, tile0, n_tiles, first, min(p.width, pieces - first), src, dst, m);
+            if (p.c.q8 && column == per - 1)
+                move_rows<uint16_t>(p, tile0, n_tiles, 0, p.c.dim >> 5, src_s, dst_s, m);
         }
     }
 }
 
-// Long lists: a chunk of rows (all of its heads' tiles, or a group of them) is a CTA's.  Chunks are taken in
-// order, by a counter; each loads its rows, says so, and stores them once the chunks whose rows lie where it
-// stores (one or two, found by a search in the ascending list while the loads are on their way) have loaded
-// theirs.  Those chunks are not after it, and wait for nothing before they say so: every wait ends.
+// Long lists: a chunk of rows (of a group of its heads' tiles) is a CTA's.  Chunks are taken in order, by a
+// counter; each loads its rows, says so, and stores them once the chunks whose rows lie where it stores (one or two,
+// found by a search in the ascending list) have loaded theirs.  Those chunks are not after it, and wait for
+// nothing before they say so but their CTA's chunk before: every wait ends.  What a chunk needs to know is a chain of
+// dependent loads (sequence, rows, page ids, counts; the search), so a warp of its own finds it out a chunk
+// ahead.  (Not two: a chunk that is taken and not loaded keeps others waiting, 87 to 109 us instead of 57.)
 
 struct LongParams {
     CompactParams m;
-    int* next;   // the next chunk to be taken; zero before the call
-    int* flags;  // [groups][chunks] 1: loaded; zero before the call
+    int* turn;   // [0] the next chunk to be taken, [1] CTAs done; zero between calls
+    int* flags;  // [groups][chunks] 1: loaded; zero between calls
     int chunks, chunk_rows, groups, group_tiles;
 };
+struct LongChunk {
+    int64_t src[CMP_CHUNK], dst[CMP_CHUNK];      // where a row's values are in a pool's tile 0; -1: the row stays
+    int64_t src_s[CMP_CHUNK], dst_s[CMP_CHUNK];  // (Q8_0) its scales
+    int chunk, group, rows, c0, c1;              // rows: 0: none moves, -1: no chunk is left; [c0, c1): chunks waited for
+};
 
-template <typename S>
-__global__ void __launch_bounds__(CMP_THREADS, CMP_CTAS) k_kv_compact_long(const LongParams q) {
+// A warp's: what the CTAs need to know of the chunk taken.
+__device__ __forceinline__ void plan_chunk(const LongParams& q, int taken, LongChunk* out) {
     const CompactParams& p = q.m;
-    __shared__ int64_t src[2][CMP_CHUNK], dst[2][CMP_CHUNK];      // where a row's values are in a pool's tile 0; -1: the row stays
-    __shared__ int64_t src_s[2][CMP_CHUNK], dst_s[2][CMP_CHUNK];  // (Q8_0) its scales
-    __shared__ int taken[2], first_seq[2], gave_up;
-    extern __shared__ uint4 pieces[];  // [CMP_UNITS][CMP_THREADS] on their way, each thread's its own
-    uint4* held16 = pieces + threadIdx.x;
-    const int tid = threadIdx.x, shift = p.c.page_shift, total = q.chunks * q.groups;
-    griddep_release();
-    griddep_wait();
+    const int lane = threadIdx.x & 31, shift = p.c.page_shift;
+    if (taken >= q.chunks * q.groups) {
+        if (lane == 0) out->rows = -1;
+        return;
+    }
     const int64_t held = min(p.max_pages << shift, (int64_t)INT_MAX), cell_mask = (int64_t(1) << shift) - 1;
-    const int n16 = p.c.dim >> (p.c.q8 ? 4 : 3), ns = p.c.q8 ? (p.c.dim >> 4) / (int)sizeof(S) : 0;  // units of a row of a tile
-    if (tid == 0) {
-        gave_up = 0;
-        taken[0] = atomicAdd(q.next, 1);
-    }
-    // the lengths
-    for (int s = blockIdx.x * CMP_THREADS + tid; s < p.n_seq; s += gridDim.x * CMP_THREADS) {
-        const int a = p.starts[s], b = p.starts[s + 1], n = a < 0 || b > p.n_rows ? 0 : max(b - a, 0);
-        p.new_lens[s] = (int)min((int64_t)max(p.base[s], 0) + n, (int64_t)INT_MAX);
-    }
-    // the slots of the chunk taken[x], into src[x] and dst[x]; whether a row of it moves
-    auto find_slots = [&](int x) {
-        const int r0 = taken[x] / q.groups * q.chunk_rows, m = min(q.chunk_rows, (int)p.n_rows - r0);
-        bool moves = false;
-        for (int i = tid; i < m; i += CMP_THREADS) {
-            const int r = r0 + i;
-            int lo = 0, hi = p.n_seq;  // the last sequence that starts at r or before it
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (p.starts[mid] <= r) lo = mid;
-                else hi = mid;
-            }
-            if (i == 0) first_seq[x] = lo;
-            const int a = p.starts[lo], b = p.starts[lo + 1], at = r - a;
-            int64_t from = -1, to = -1;
-            if (a >= 0 && at >= 0 && b <= p.n_rows && r < b) {
-                const int row = p.rows[r], before = at ? p.rows[r - 1] : -1, base = max(p.base[lo], 0);
-                if (row != at) {
-                    auto slot_of = [&](int64_t y) -> int64_t {
-                        if (y >= held) return -1;
-                        const int id = p.pages[(int64_t)lo * p.max_pages + (y >> shift)];
-                        return (unsigned)id < (unsigned)p.c.n_pages ? ((int64_t)id << shift) + (y & cell_mask) : -1;
-                    };
-                    if (row > at && before < row) {
-                        from = slot_of((int64_t)base + row);
-                        to = slot_of((int64_t)base + at);
-                    }
-                    if (to >= 0 && p.refs && p.refs[to >> shift] > 1) to = -1;
-                    if (from < 0 || to < 0) {
-                        from = -1;
-                        record_error(p.err, SYN_DEVERR_BOUNDS);
-                    }
+    const int chunk = taken / q.groups, group = taken - chunk * q.groups, r0 = chunk * q.chunk_rows;
+    const int m = min(q.chunk_rows, (int)p.n_rows - r0);
+    auto sequence_of = [&](int r) {  // the last sequence that starts at r or before it
+        int lo = 0, hi = p.n_seq;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.starts[mid] <= r) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    };
+    bool moves = false;
+    int first_seq = 0;
+#pragma unroll
+    for (int k = 0; k < CMP_CHUNK / 32; k++) {
+        const int i = lane + 32 * k, r = r0 + i;
+        if (i >= m) continue;
+        const int lo = sequence_of(r);
+        if (k == 0) first_seq = lo;
+        const int a = p.starts[lo], b = p.starts[lo + 1], at = r - a;
+        int64_t from = -1, to = -1;
+        if (a >= 0 && at >= 0 && b <= p.n_rows && r < b) {
+            const int row = p.rows[r], before = at ? p.rows[r - 1] : -1, base = max(p.base[lo], 0);
+            if (row != at) {
+                auto slot_of = [&](int64_t y) -> int64_t {
+                    if (y >= held) return -1;
+                    const int id = p.pages[(int64_t)lo * p.max_pages + (y >> shift)];
+                    return (unsigned)id < (unsigned)p.c.n_pages ? ((int64_t)id << shift) + (y & cell_mask) : -1;
+                };
+                if (row > at && before < row) {
+                    from = slot_of((int64_t)base + row);
+                    to = slot_of((int64_t)base + at);
+                }
+                if (to >= 0 && p.refs && p.refs[to >> shift] > 1) to = -1;
+                if (from < 0 || to < 0) {
+                    from = -1;
+                    record_error(p.err, SYN_DEVERR_BOUNDS);
                 }
             }
-            moves |= from >= 0;
-            const int64_t pitch = p.c.dim * (p.c.q8 ? 1 : 2), scales = (int64_t)p.c.dim << shift;
-            const int64_t from0 = (from >> shift) * p.c.page_stride, to0 = (to >> shift) * p.c.page_stride;
-            src[x][i] = from < 0 ? -1 : from0 + (from & cell_mask) * pitch;
-            dst[x][i] = to0 + (to & cell_mask) * pitch;
-            src_s[x][i] = from0 + scales + (from & cell_mask) * (p.c.dim >> 4);
-            dst_s[x][i] = to0 + scales + (to & cell_mask) * (p.c.dim >> 4);
         }
-        return __syncthreads_or(moves) != 0;
+        moves |= from >= 0;
+        const int64_t pitch = p.c.dim * (p.c.q8 ? 1 : 2), scales = (int64_t)p.c.dim << shift;
+        const int64_t from0 = (from >> shift) * p.c.page_stride, to0 = (to >> shift) * p.c.page_stride;
+        out->src[i] = from < 0 ? -1 : from0 + (from & cell_mask) * pitch;
+        out->dst[i] = to0 + (to & cell_mask) * pitch;
+        out->src_s[i] = from0 + scales + (from & cell_mask) * (p.c.dim >> 4);
+        out->dst_s[i] = to0 + scales + (to & cell_mask) * (p.c.dim >> 4);
+    }
+    moves = __any_sync(0xffffffffu, moves);
+    first_seq = __shfl_sync(0xffffffffu, first_seq, 0);
+    // the chunks [c0, c1) that hold what lies at the places of this one's rows of its first sequence (those
+    // of sequences that begin in it are its own)
+    const int a = max(p.starts[first_seq], 0), b = min(max(p.starts[first_seq + 1], a), (int)p.n_rows);
+    int c0 = 0, c1 = 0;
+    if (moves && a < r0) {
+        const int place = r0 - a;
+        int lo = a, n = min(r0 + m, b) - a;  // (a row is not before its place: none after this chunk)
+        while (n > 0) {  // the list's first row that is not below the first place
+            const int step = (n + 31) / 32, at = lo + lane * step;
+            const int below = __popc(__ballot_sync(0xffffffffu, lane * step < n && p.rows[at] < place));
+            // rows lo + step * (below - 1) and before are below; row lo + step * below is not
+            if (below == 0) break;
+            lo += (below - 1) * step + 1;
+            n = min(step - 1, max(n - ((below - 1) * step + 1), 0));
+        }
+        c0 = lo / q.chunk_rows;
+        c1 = min((lo + m + q.chunk_rows - 1) / q.chunk_rows, chunk);  // (at most m rows lie at m places)
+    }
+    if (lane == 0) {
+        out->chunk = chunk;
+        out->group = group;
+        out->rows = moves ? m : 0;
+        out->c0 = c0;
+        out->c1 = c1;
+    }
+}
+
+constexpr int CMP_LONG_THREADS = CMP_THREADS + 32;  // the last warp plans
+__device__ __forceinline__ void copiers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CMP_THREADS) : "memory"); }
+
+template <typename S>
+__global__ void __launch_bounds__(CMP_LONG_THREADS, CMP_CTAS) k_kv_compact_long(const LongParams q) {
+    const CompactParams& p = q.m;
+    __shared__ LongChunk plans[2];
+    __shared__ int gave_up, last;
+    extern __shared__ uint4 pieces[];  // [CMP_UNITS][CMP_THREADS] on their way, each thread's its own
+    const int tid = threadIdx.x;
+    const bool plans_ahead = tid >= CMP_THREADS;
+    griddep_release();
+    griddep_wait();
+    auto take = [&]() {
+        int t = 0;
+        if (tid == CMP_THREADS) t = atomicAdd(q.turn, 1);
+        return __shfl_sync(0xffffffffu, t, 0);
     };
-    __syncthreads();
-    if (taken[0] >= total) return;
-    bool moves = find_slots(0);
+    if (plans_ahead) {
+        plan_chunk(q, take(), &plans[0]);
+    } else {
+        if (tid == 0) gave_up = 0;
+        // the lengths
+        for (int s = blockIdx.x * CMP_THREADS + tid; s < p.n_seq; s += gridDim.x * CMP_THREADS) {
+            const int a = p.starts[s], b = p.starts[s + 1], n = a < 0 || b > p.n_rows ? 0 : max(b - a, 0);
+            p.new_lens[s] = (int)min((int64_t)max(p.base[s], 0) + n, (int64_t)INT_MAX);
+        }
+    }
+    const int n16 = p.c.dim >> (p.c.q8 ? 4 : 3), ns = p.c.q8 ? (p.c.dim >> 4) / (int)sizeof(S) : 0;  // units of a row of a tile
+    uint4* held16 = pieces + tid;
     for (int x = 0;; x ^= 1) {
-        const int chunk = taken[x] / q.groups, group = taken[x] % q.groups, r0 = chunk * q.chunk_rows;
-        const int m = min(q.chunk_rows, (int)p.n_rows - r0);
+        __syncthreads();  // (plans[x] is made, plans[x ^ 1] and the pieces have been used)
+        const LongChunk& w = plans[x];
+        if (w.rows < 0) break;
+        if (plans_ahead) {
+            plan_chunk(q, take(), &plans[x ^ 1]);
+            continue;
+        }
         // this thread's piece of a row (one 16 bytes of a tile), and the rows it takes: tid / u16, then every per16-th
-        const int tile0 = group * q.group_tiles, tiles = min(q.group_tiles, 2 * p.c.n_kv - tile0);
+        const int tile0 = w.group * q.group_tiles, tiles = min(q.group_tiles, 2 * p.c.n_kv - tile0);
         const int u16 = tiles * n16, us = tiles * ns, per16 = CMP_THREADS / u16, per_s = us ? CMP_THREADS / us : 1;
         const int row16 = tid / u16, t16 = (tid - row16 * u16) / n16, row_s = us ? tid / us : 0, t_s = us ? (tid - row_s * us) / ns : 0;
         uint8_t* at16 = ((tile0 + t16) & 1 ? p.c.v : p.c.k) + ((tile0 + t16) >> 1) * p.c.tile + (tid - row16 * u16 - t16 * n16) * 16;
         uint8_t* at_s = ((tile0 + t_s) & 1 ? p.c.v : p.c.k) + ((tile0 + t_s) >> 1) * p.c.tile + (tid - row_s * us - t_s * ns) * (int)sizeof(S);
-        const int end16 = moves && row16 < per16 ? m : 0, end_s = moves && us && row_s < per_s ? m : 0;
+        const int end16 = row16 < per16 ? w.rows : 0, end_s = us && row_s < per_s ? w.rows : 0;
         S ws[CMP_SCALES];
 #pragma unroll
         for (int i = 0; i < CMP_UNITS; i++) {
             const int r = row16 + i * per16;
-            if (r < end16 && src[x][r] >= 0) cp16_all(smem_u32(held16 + i * CMP_THREADS), at16 + src[x][r]);
+            if (r < end16 && w.src[r] >= 0) cp16_all(smem_u32(held16 + i * CMP_THREADS), at16 + w.src[r]);
         }
         cp_commit();
 #pragma unroll
         for (int i = 0; i < CMP_SCALES; i++) {
             const int r = row_s + i * per_s;
-            if (r < end_s && src[x][r] >= 0) ws[i] = *reinterpret_cast<const S*>(at_s + src_s[x][r]);
-        }
-        if (tid == 0) taken[x ^ 1] = atomicAdd(q.next, 1);
-        // the chunks [c0, c1) that hold what lies at the places of this one's rows of its first sequence (those
-        // of sequences that begin in it are its own)
-        const int a = max(p.starts[first_seq[x]], 0), b = min(max(p.starts[first_seq[x] + 1], a), (int)p.n_rows);
-        int c0 = 0, c1 = 0;
-        if (moves && a < r0) {
-            const int place = r0 - a;
-            int lo = a, n = min(r0 + m, b) - a;  // (a row is not before its place: none after this chunk)
-            while (n > 0) {  // the list's first row that is not below the first place
-                const int step = (n + CMP_THREADS - 1) / CMP_THREADS, at = lo + tid * step;
-                const int below = __syncthreads_count(tid * step < n && p.rows[at] < place);
-                // rows lo + step * (below - 1) and before are below; row lo + step * below is not
-                if (below == 0) break;
-                lo += (below - 1) * step + 1;
-                n = min(step - 1, max(n - ((below - 1) * step + 1), 0));
-            }
-            c0 = lo / q.chunk_rows;
-            c1 = min((lo + m + q.chunk_rows - 1) / q.chunk_rows, chunk);  // (at most m rows lie at m places)
+            if (r < end_s && w.src[r] >= 0) ws[i] = *reinterpret_cast<const S*>(at_s + w.src_s[r]);
         }
         cp_wait<0>();
-        __threadfence();  // (what was loaded is loaded)
-        __syncthreads();
-        int* flags = q.flags + (int64_t)group * q.chunks;
-        if (tid == 0) atomicExch(flags + chunk, 1);
-        const bool more = taken[x ^ 1] < total;
-        const bool moves_next = more && find_slots(x ^ 1);
-        for (int j = c0 + tid; j < c1; j += CMP_THREADS) {
-            const long long t0 = clock64();
-            while (*reinterpret_cast<volatile int*>(flags + j) == 0)
-                if (clock64() - t0 > SYN_WAIT_CYCLES) {
-                    record_error(p.err, SYN_DEVERR_TIMEOUT);
-                    gave_up = 1;
-                    break;
-                }
+        copiers_sync();  // (what was loaded is loaded)
+        int* flags = q.flags + (int64_t)w.group * q.chunks;
+        if (tid == 0) {
+            __threadfence();
+            atomicExch(flags + w.chunk, 1);
         }
-        __threadfence();
-        __syncthreads();
-        if (gave_up) return;
+        if (w.c0 + tid < w.c1 && !gave_up) {
+            const long long t0 = clock64();
+            for (int j = w.c0 + tid; j < w.c1; j += CMP_THREADS)
+                while (*reinterpret_cast<volatile int*>(flags + j) == 0)
+                    if (clock64() - t0 > SYN_WAIT_CYCLES) {
+                        record_error(p.err, SYN_DEVERR_TIMEOUT);
+                        gave_up = 1;
+                        break;
+                    }
+            __threadfence();
+        }
+        copiers_sync();
+        if (gave_up) continue;
 #pragma unroll
         for (int i = 0; i < CMP_UNITS; i++) {
             const int r = row16 + i * per16;
-            if (r < end16 && src[x][r] >= 0) *reinterpret_cast<uint4*>(at16 + dst[x][r]) = held16[i * CMP_THREADS];
+            if (r < end16 && w.src[r] >= 0) *reinterpret_cast<uint4*>(at16 + w.dst[r]) = held16[i * CMP_THREADS];
         }
 #pragma unroll
         for (int i = 0; i < CMP_SCALES; i++) {
             const int r = row_s + i * per_s;
-            if (r < end_s && src[x][r] >= 0) *reinterpret_cast<S*>(at_s + dst_s[x][r]) = ws[i];
+            if (r < end_s && w.src[r] >= 0) *reinterpret_cast<S*>(at_s + w.dst_s[r]) = ws[i];
         }
-        if (!more) return;
-        moves = moves_next;
-        __syncthreads();  // (the slots have been used)
     }
+    // the last CTA to get here leaves the counters and flags as they were
+    if (tid == 0) last = atomicAdd(q.turn + 1, 1) == (int)gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    if (tid < 2) q.turn[tid] = 0;
+    for (int i = tid; i < q.chunks * q.groups; i += CMP_LONG_THREADS) q.flags[i] = 0;
 }
 
-// Rows from which a list counts as long.
-constexpr int64_t CMP_LONG = 4096;
+// Which lists count as long.  The kernel of short ones goes through a sequence's rows one batch after the other, but starts
+// faster, and many sequences have tiles enough for all SMs (where one of them may have most of the rows, so not
+// past 8192).  us from a graph, every second row kept, 8 heads of 128, F16 / Q8_0, long : short:
+//    1 sequence,   1024 rows   7.3 : 10.0 /  7.1 :  9.6     2048   8.8 : 18.7 /  7.9 : 17.9
+//    4             2048        8.9 :  8.0 /  7.9 :  8.7     4096   9.7 : 14.8 /  9.7 : 15.6
+//    8             4096        9.7 :  9.2 /  9.7 : 11.3     8192  18.7 : 18.2 / 10.8 : 22.3
+//   16             4096        9.6 :  7.6 /  9.6 :  7.7     8192  18.9 : 16.2 / 10.8 : 14.1
+//   64             4096        9.7 :  7.2 /  9.4 :  6.6     8192  18.4 : 14.6 / 10.8 :  9.4
+static bool long_lists(int64_t n_seq, int64_t n_rows) { return n_rows >= std::min<int64_t>(512 * (n_seq + 1), 8192); }
 
 // How a long list is cut: a thread for each 16 bytes of a row of a group's tiles, some rows a pass (and for each 2 to 8 bytes
 // of scales).
 static int64_t cut_long(const KvCache& c, int64_t n_rows, LongParams* q) {
     const int n16 = c.dim >> (c.q8 ? 4 : 3), ns = c.q8 ? (c.dim >> 4) / (c.dim % 128 == 0 ? 8 : c.dim % 64 == 0 ? 4 : 2) : 0;
-    const int tiles = std::min(2 * c.n_kv, CMP_THREADS / n16);
+    // (as few tiles as make chunks of CMP_CHUNK rows: what lies together is moved together)
+    const int tiles = std::min(2 * c.n_kv, std::max(1, std::min(CMP_THREADS, CMP_THREADS * CMP_UNITS / CMP_CHUNK) / n16));
     int rows = CMP_THREADS / (tiles * n16) * CMP_UNITS;
     if (ns) rows = std::min(rows, CMP_THREADS / (tiles * ns) * CMP_SCALES);
     q->group_tiles = tiles;
@@ -662,16 +759,16 @@ static int64_t cut_long(const KvCache& c, int64_t n_rows, LongParams* q) {
     return (int64_t)q->chunks * q->groups;
 }
 
-int64_t compact_scratch_words(const KvCache& c, int64_t n_rows) {
-    if (n_rows < CMP_LONG) return 0;
+int64_t compact_count_words(const KvCache& c, int64_t n_seq, int64_t n_rows) {
+    if (!long_lists(n_seq, n_rows)) return 0;
     LongParams q;
     const int64_t n = cut_long(c, n_rows, &q);
-    return n < INT_MAX ? n + 1 : -1;
+    return n < INT_MAX - 2 ? n + 2 : -1;
 }
 
 cudaError_t launch_kv_compact(const KvCache& c, const int32_t* refs, int64_t n_seq, int64_t n_rows, const int32_t* pages,
                               int64_t max_pages, const int32_t* base, const int32_t* starts, const int32_t* rows,
-                              int32_t* new_lens, int* scratch, int* err, int sms, int* launches, cudaStream_t s) {
+                              int32_t* new_lens, int* count, int* err, int sms, int* launches, cudaStream_t s) {
     CompactParams p;
     p.c = c;
     p.refs = refs;
@@ -685,27 +782,27 @@ cudaError_t launch_kv_compact(const KvCache& c, const int32_t* refs, int64_t n_s
     p.n_rows = n_rows;
     p.n_seq = (int)n_seq;
     cudaError_t e;
-    if (n_rows >= CMP_LONG) {
+    if (long_lists(n_seq, n_rows)) {
         LongParams q;
         q.m = p;
         const int64_t n = cut_long(c, n_rows, &q);
-        q.next = scratch;
-        q.flags = scratch + 1;
-        e = cudaMemsetAsync(scratch, 0, (size_t)(n + 1) * 4, s);
-        if (e != cudaSuccess) return e;
+        q.turn = count;
+        q.flags = count + 2;
         auto kern = c.dim % 128 == 0 ? k_kv_compact_long<uint2> : c.dim % 64 == 0 ? k_kv_compact_long<uint32_t> : k_kv_compact_long<uint16_t>;
         const int grid = (int)std::min<int64_t>(n, (int64_t)sms * CMP_CTAS);
-        kern<<<grid, CMP_THREADS, CMP_UNITS * CMP_THREADS * 16, s>>>(q);
-        e = cudaGetLastError();
+        e = launch_overlapped(kern, grid, CMP_LONG_THREADS, CMP_UNITS * CMP_THREADS * 16, s, q);
     } else {
-        // columns of at least 32 bytes of a row (a sector), as many as it takes to fill the SMs
-        const int pieces = c.dim >> (c.q8 ? 4 : 3);
-        int width = pieces;
-        while (width > 2 && n_seq * 2 * c.n_kv * ((pieces + width - 1) / width) < 4 * (int64_t)sms) width = (width + 1) / 2;
-        p.width = width;
-        p.cut = (pieces + width - 1) / width;
-        e = launch_overlapped(k_kv_compact, (int)std::min<int64_t>(n_seq * 2 * c.n_kv * (p.cut + c.q8), (int64_t)sms * 8),
-                              CMP_THREADS, 0, s, p);
+        // About CMP_TARGET CTAs an SM: several tiles to one where there are many sequences, columns of at least 32 bytes of a row
+        // (a sector) where there are few.
+        const int pieces = c.dim >> (c.q8 ? 4 : 3), tiles = 2 * c.n_kv;
+        const int64_t want = (int64_t)CMP_TARGET * sms;
+        p.group = (int)std::min<int64_t>(std::max<int64_t>(n_seq * tiles / want, 1), tiles);
+        const int64_t units = n_seq * ((tiles + p.group - 1) / p.group);
+        p.width = pieces;
+        while (p.width > 2 && units * ((pieces + p.width - 1) / p.width) < want) p.width = (p.width + 1) / 2;
+        p.cut = (pieces + p.width - 1) / p.width;
+        p.apart = c.q8 && p.cut > 1;
+        e = launch_overlapped(k_kv_compact, (int)std::min<int64_t>(units * (p.cut + p.apart), (int64_t)sms * 8), CMP_THREADS, 0, s, p);
     }
     if (e == cudaSuccess) ++*launches;
     return e;

@@ -507,24 +507,25 @@ SYN_API int syn_attn_tree(const syn_kv_cache* cache, const syn_attn* attn, int64
 
 /* ======================================================================================
  * The pages of a cache, as sequences hold them.  The caller keeps, on the device, a page table
- * (n_seq x max_pages; -1, or any other negative number: no page) and the lengths of its sequences, and refs, one count for each of
- * the cache's n_pages pages: the table entries that hold it.  0 is a free page; a new cache's are
- * all 0.  These calls keep the counts; sequences that share pages (a prompt's, or beams of one
- * history) hold them together until one of them writes.
+ * (n_seq x max_pages; -1, or any other negative number: no page) and the lengths of its sequences,
+ * and refs, one count for each of the cache's n_pages pages: the table entries that hold it.  0 is a
+ * free page; a new cache's are all 0.  These calls keep the counts; sequences that share pages (a
+ * prompt's, or beams of one history) hold them together until one of them writes.
  *
  * Pages are taken lowest first, in the order of sequences and columns: what a call does depends on
  * its arguments alone.  The counts belong to all the sequences of a cache: calls that use the same
- * refs are ordered by the caller (one stream, or events).  A page id outside the pool counts as no page and
- * syn_device_status then returns SYN_ERR_BOUNDS.  Of each cache argument fork and trim use n_pages
- * and page_size alone.  Tables, counts and lengths are 4-byte aligned, slots 8-byte.  All are asynchronous and
- * read their tables on the device, so captured graphs follow them.
+ * refs are ordered by the caller (one stream, or events).  A page id outside the pool counts as no
+ * page and syn_device_status then returns SYN_ERR_BOUNDS.  Of each cache argument fork and trim use
+ * n_pages and page_size alone.  Tables, counts and lengths are 4-byte aligned, slots 8-byte.  All
+ * are asynchronous and read their tables on the device, so captured graphs follow them.
  * ====================================================================================== */
 
 /* New tables of n_new sequences: sequence i starts as from[i] (of the n_seq sequences of pages and
- * lens) is now: the pages that hold its rows, counted once more each, the rest of the row -1; new_lens[i] =
- * lens[from[i]] (cut to what the table holds).  A negative from[i] gives an empty sequence, one past n_seq too (and
- * SYN_ERR_BOUNDS).  new_pages (n_new x max_pages) and new_lens must not overlap pages and lens;
- * what new_pages held is overwritten, not given back (syn_kv_trim first). */
+ * lens) is now: the pages that hold its rows, counted once more each, the rest of the row -1;
+ * new_lens[i] = lens[from[i]] (cut to what the table holds).  A negative from[i] gives an empty
+ * sequence, one past n_seq too (and SYN_ERR_BOUNDS).  new_pages (n_new x max_pages) and new_lens
+ * must not overlap pages and lens; what new_pages held is overwritten, not given back (syn_kv_trim
+ * first). */
 SYN_API int syn_kv_fork(const syn_kv_cache* cache, int32_t* refs, int64_t n_seq, const int32_t* pages, int64_t max_pages,
                         const int32_t* lens, int64_t n_new, const int32_t* from, int32_t* new_pages, int32_t* new_lens,
                         syn_stream_t stream);
@@ -535,11 +536,12 @@ SYN_API int syn_kv_fork(const syn_kv_cache* cache, int32_t* refs, int64_t n_seq,
  * too is replaced by a free one, to which the rows that the sequence has in it are copied.  (If every
  * entry that holds a page is written to by this call, the last of them keeps it.)  new_lens[s] gets the
  * new length (it may be lens), slots (n_tok, or NULL) each new row's slot for syn_kv_append.
- * Where free pages do not suffice nobody keeps a shared page, and pages go to the first sequences, as long
- * as the sum of their needs fits; sequences that need none are extended too.  The others, and those whose table has too
- * few columns, stay as they are: their length, and -1 as slots (which syn_kv_append does not store).
- * n_seq up to 4096 (SYN_ERR_SHAPE).  Uses the stream's attention workspace, 16 bytes a sequence and 8 a page
- * that new rows fall into: make the first call of a size before capturing a graph. */
+ * Where free pages do not suffice nobody keeps a shared page, and pages go to the first sequences,
+ * as long as the sum of their needs fits; sequences that need none are extended too.  The others, and
+ * those whose table has too few columns, stay as they are: their length, and -1 as slots (which
+ * syn_kv_append does not store).  n_seq up to 4096 (SYN_ERR_SHAPE).  Uses the attention workspace of
+ * (device, stream), 16 bytes a sequence and 8 a page that new rows fall into: make the first call of a
+ * size before capturing a graph (and graphs as for syn_mul_mat). */
 SYN_API int syn_kv_extend(const syn_kv_cache* cache, int32_t* refs, int64_t n_seq, int64_t n_tok, int32_t* pages,
                           int64_t max_pages, const int32_t* lens, const int32_t* starts, int32_t* new_lens, int64_t* slots,
                           syn_stream_t stream);
@@ -547,11 +549,14 @@ SYN_API int syn_kv_extend(const syn_kv_cache* cache, int32_t* refs, int64_t n_se
 /* Packs the rows that a sequence keeps (the accepted path of its drafts, or what an eviction leaves), in
  * place: with n = starts[s+1] - starts[s] rows listed for it (starts: n_seq + 1, from 0 ascending to
  * n_rows), row base[s] + i becomes what row base[s] + rows[starts[s] + i] was, for i < n, and
- * new_lens[s] = base[s] + n.  A sequence's list ascends (so rows only move down).  Rows behind the last
- * keep what they hold.  refs (or NULL): a row whose new place is in a page that other entries hold too is
- * not moved.  Such a row, one out of order and one outside the table are skipped and
- * syn_device_status returns SYN_ERR_BOUNDS; without refs the caller sees to it that no page that
- * it writes to is shared.  new_lens must not overlap base. */
+ * new_lens[s] = base[s] + n.  A sequence's list ascends (so rows only move down).  Rows behind the
+ * last keep what they hold.  refs (or NULL): a row whose new place is in a page that other entries
+ * hold too is not moved; without refs the caller sees to it that no page that it writes to is shared.
+ * Such a row, one out of order (not after the one before it: what a list that does not ascend leaves
+ * in its sequence's packed rows is not defined) and one outside the table are skipped, and
+ * syn_device_status returns SYN_ERR_BOUNDS.  new_lens must not overlap base.  Calls of 1024 rows and
+ * more may use the attention workspace of (device, stream): make the first one of a size before
+ * capturing a graph (and graphs as for syn_mul_mat). */
 SYN_API int syn_kv_compact(const syn_kv_cache* cache, const int32_t* refs, int64_t n_seq, int64_t n_rows,
                            const int32_t* pages, int64_t max_pages, const int32_t* base, const int32_t* starts,
                            const int32_t* rows, int32_t* new_lens, syn_stream_t stream);
@@ -574,10 +579,10 @@ SYN_API int syn_kv_copy(const syn_kv_cache* from, const syn_kv_cache* to, int64_
  *   z_v = scale * scales[r] * (cap > 0 ? cap * tanh(x_v / cap) : x_v),  logp(v) = z_v - log(sum_w exp(z_w)),
  *   entropy = -sum_v exp(logp(v)) logp(v)    over the allowed tokens
  *
- * A token that the mask does not allow, or whose logit is -inf, has log probability -inf and adds nothing,
- * whatever its logit holds.  A row without a token has entropy 0 and log probabilities of -inf.  A
- * row with a NaN or +inf among its allowed logits, or whose scale is not positive and finite, has NaN for its results
- * (and no alternatives: -1).
+ * A token that the mask does not allow, or whose logit is -inf, has log probability -inf and adds
+ * nothing, whatever its logit holds.  A row without a token has entropy 0 and log probabilities of
+ * -inf.  A row with a NaN or +inf among its allowed logits, or whose scale is not positive and finite,
+ * has NaN for its results (and no alternatives: -1).
  * ====================================================================================== */
 typedef struct {
     int type;             /* SYN_OUT_F32 or SYN_OUT_F16: the logits' */
@@ -591,13 +596,14 @@ typedef struct {
 } syn_logits;
 
 /* For each of n_rows rows of n_vocab logits: logprob (n_rows x n_ids) of the tokens ids (the same
- * shape; a negative id asks for nothing and gets 0, one past the vocabulary 0 and SYN_ERR_BOUNDS); entropy (n_rows, or NULL), in nats; the n_top
- * (0 to 64) allowed tokens of the largest logits, in order, ties to the lower token: top and top_logprob (n_rows x
- * n_top); where fewer are allowed, -1 and -inf.  Sums are fp32 over a running maximum; every result is
- * exact to about 1e-6 of the larger of 1 and its own size, capped logits to 5e-7 * cap * scale.  Logits may start
- * anywhere their type may; 16-byte aligned rows load fastest.  Asynchronous.  (In deterministic mode a row's results do not
- * depend on the number of rows.)  SYN_ERR_TYPE, SYN_ERR_SHAPE (n_vocab up to 2^30, n_ids up to 65536), SYN_ERR_NULL,
- * SYN_ERR_ALIGN. */
+ * shape; a negative id asks for nothing and gets 0, one past the vocabulary 0 and SYN_ERR_BOUNDS);
+ * entropy (n_rows, or NULL), in nats; the n_top (0 to 64) allowed tokens of the largest logits, in
+ * order, ties to the lower token: top and top_logprob (n_rows x n_top); where fewer are allowed, -1 and
+ * -inf.  Sums are fp32 over a running maximum; every result is exact to about 1e-6 of the larger of 1
+ * and its own size, capped logits to 5e-7 * cap * scale.  Logits may start anywhere their type may;
+ * 16-byte aligned rows load fastest.  Asynchronous.  (In deterministic mode a row's results do not
+ * depend on the number of rows.)  SYN_ERR_TYPE, SYN_ERR_SHAPE (n_vocab up to 2^30, n_ids up to
+ * 65536), SYN_ERR_NULL, SYN_ERR_ALIGN. */
 SYN_API int syn_logprobs(const syn_logits* opt, int64_t n_rows, int64_t n_vocab, const void* logits, int64_t n_ids,
                          const int32_t* ids, float* logprob, float* entropy, int64_t n_top, int32_t* top, float* top_logprob,
                          syn_stream_t stream);

@@ -368,3 +368,33 @@ def test_compact_of_long_lists(syn, t, kv, dim, page):
             assert np.array_equal(x, y)
     finally:
         syn.set_sm_limit(old)
+
+
+@pytest.mark.parametrize("t,kv,dim,page", [(F16, 8, 128, 16), (Q8_0, 8, 128, 16), (F16, 5, 96, 8), (Q8_0, 3, 160, 64), (Q8_0, 1, 64, 8)])
+@pytest.mark.parametrize("n_seq", [9, 61, 190])
+def test_compact_of_many_sequences(syn, t, kv, dim, page, n_seq):
+    """Several tiles to a CTA, batches that end inside a tile; no rows, one row and some hundred of a sequence."""
+    rng = np.random.default_rng([t, kv, dim, n_seq])
+    lens = rng.integers(0, 40, n_seq)
+    lens[rng.integers(0, n_seq, 3)] = [0, 1, 700]
+    base = rng.integers(0, 30, n_seq)
+    need = -(-(base + lens) // page)
+    n_pages, width = int(need.sum()), int(need.max())
+    cache = make_cache(syn, t, kv, dim, page, n_pages, 12)
+    table = np.full((n_seq, width), -1, np.int32)
+    order, at = rng.permutation(n_pages), 0
+    for s, m in enumerate(need):
+        table[s, :m] = order[at:at + m]
+        at += m
+    rows = [np.nonzero(rng.random(n) < 0.5)[0] for n in lens]
+    starts = np.concatenate([[0], np.cumsum([len(r) for r in rows])])
+    want = planes(cache, dim, page)
+    for x in want:
+        for s, r in enumerate(rows):
+            to, r = base[s] + np.arange(len(r)), base[s] + r
+            x[table[s, to // page], :, to % page] = x[table[s, r // page], :, r % page]
+    got = syn.kv_compact(cache, dev(counts(n_pages, table)), dev(table), dev(base), dev(starts), dev(np.concatenate(rows)))
+    same(got, base + np.diff(starts), "lengths")
+    for x, y in zip(planes(cache, dim, page), want):
+        assert np.array_equal(x, y)
+    assert syn.device_status() == syn.OK

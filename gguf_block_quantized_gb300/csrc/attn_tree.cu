@@ -27,6 +27,11 @@
 //   expand   (Q8_0) eight warps turn into fp16 tiles of the same layout.
 // All hand-offs are mbarriers with bounded waits.
 //
+// Measured on GB300 (cold L2; 32 / 8 heads of 128, pages of 64): 24 F16 sequences of 190 to 4000 rows with up to 26
+// drafts 43 us (133 MB, 3.1 TB/s: 5 us to the first product, 7 us of join); 48 Q8_0 sequences of 500 to 6001 with up
+// to 13 drafts, capped, 136 us (240 MB, 1.8 TB/s: the expanding and softmax warps' instructions; 105 us without the
+// cap); 64 drafts over 120001 F16 rows 120 us (493 MB, 4.1 TB/s, and 1.05 PFLOP/s: softmax).
+//
 // A masked score is replaced before the maximum; V rows past the sequence's end are zeroed in shared memory.  A V
 // row that only some rows of the item see may still hold infinities or NaN, and 0 * inf is not 0: a row whose
 // sums come out non-finite is computed again from the keys it sees, in fp32, when its CTA has done its items.
@@ -38,8 +43,24 @@
 
 namespace syn {
 
-constexpr int TREE_ITEM = 2;        // what an item's start and end cost, in tiles
-constexpr int TREE_JOIN = 4;        // and a part's share of the join: what is no longer than the ranges by more is not split
+// What an item's start and end cost, in tiles (1, 2, 3, 4: 24 sequences of 190 to 4000 rows 45.1, 42.8, 43.3, 44.1 us).
+constexpr int TREE_ITEM = 2;
+// And a part's share of the join: items no longer than the ranges by more are not split (4 sequences of 300 to 500 rows: 0: 17.9
+// us, 4 and more: 12.6).
+constexpr int TREE_JOIN = 4;
+// Tables of at most this many tiles: whole items and no join, which costs some 5 us even where it finds nothing to do (it waits
+// for the first kernel's end).  us, whole : split, up to 26 drafts, heads of 128 (F16 / Q8_0):
+//    1 sequence of 700 rows 15.1 : 18.7 / 18.0 : 19.8,   1000: 17.4 : 18.2 / 21.0 : 19.9,   1300: 22.5 : 20.1 / 25.6 : 20.8
+//    6 of 1000: 18.1 : 21.2 / 21.4 : 23.9,   1600: 24.9 : 22.0 / 29.6 : 24.2
+//   19 of 1000: 21.9 : 27.3 / 23.5 : 28.7,   2000: 32.8 : 38.1 / 36.7 : 42.1
+//   96 of 500 to 1000: 73.3 : 85.9 / 94.3 : 113.3
+// Heads of 256 (tiles of 64 keys), pages of 16, 1 sequence: 300 rows 16.6 : 18.0,  600: 26.6 : 19.3;  pages of 64, 48 of 350 to
+// 700: 56.2 : 66.4.  Heads of 64, pages of 16 (a tile is eight copies), 1 sequence: 600 rows 13.7 : 16.8,  900: 18.5 : 16.8;
+// 24 of 450 to 900: 29.3 : 29.5,  950 to 1900: 48.8 : 38.3.
+// (One long sequence among short ones would wait for itself: so not past 16 tiles.)
+constexpr int tree_whole(int D, bool large_pages, bool many) {
+    return large_pages ? (D <= 128 ? 8 : 6) * (many ? 2 : 1) : many ? 8 : 6;
+}
 
 struct TreeRedo {  // rows to be computed again, when the CTA has done its items: a warp's rows of an item
     int s, h, row0;
@@ -1472,8 +1493,8 @@ cudaError_t launch_attn_tree(const KvCache& c, const AttnDesc& a, int64_t n_seq,
     p.q_tma = q_tma;
     p.window = a.window;
     p.out_f16 = a.out_f16;
-    // (tables that hold few tiles: whole items, and no second launch)
-    p.split = split && (max_pages << c.page_shift) > (int64_t)TREE_JOIN * BN;
+    // (many: items for more than half the SMs, at least)
+    p.split = split && (max_pages << c.page_shift) > (int64_t)tree_whole(D, c.page_shift >= 6, 2 * n_seq * c.n_kv > sms) * BN;
     // kind::f16: D fp32, A and B fp16, M = 128; S: B K-major, N = BN; O: B MN-major, N = dim
     p.idesc_s = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | (8u << 24);
     p.idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(c.dim >> 3) << 17) | (8u << 24);

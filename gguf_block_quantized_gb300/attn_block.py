@@ -191,7 +191,7 @@ def run_drafts(cache_type: int, prompt: int, tokens: int, seqs: int, nodes: int,
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
     refs = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
 
-    def judge(out, ids=None, n_top=0):
+    def score(out, ids=None, n_top=0):
         return syn.logprobs(syn.mul_mat(syn.Q6_K, head, vocab, width, out), ids, n_top)
 
     def forked(pages, lens, n):
@@ -203,7 +203,7 @@ def run_drafts(cache_type: int, prompt: int, tokens: int, seqs: int, nodes: int,
     x = table[torch.randint(0, vocab, (prompt,), device="cuda", generator=gen)]
     out = torch.empty((prompt, width), device="cuda")
     block.prepare_prompt(x, out, torch.arange(prompt, dtype=torch.int32, device="cuda"), slots, i32([0, prompt]), pages, lens)()
-    first = judge(out[-1:].contiguous(), n_top=seqs).top[0].tolist()
+    first = score(out[-1:].contiguous(), n_top=seqs).top[0].tolist()
 
     def plain():  # one token at a time: tokens and log probabilities
         mine, ln = forked(pages, lens, seqs)
@@ -212,7 +212,7 @@ def run_drafts(cache_type: int, prompt: int, tokens: int, seqs: int, nodes: int,
             _, slots = syn.kv_extend(block.cache, refs, mine, ln)
             out = torch.empty((seqs, width), device="cuda")
             block.prepare_token(table[i32(now)], out, ln - 1, slots, mine, ln)()
-            got = judge(out, n_top=1)
+            got = score(out, n_top=1)
             now = got.top[:, 0].tolist()
             for s, (t, p) in enumerate(zip(now, got.top_logprob[:, 0].tolist())):
                 said[s].append(t)
@@ -236,7 +236,7 @@ def run_drafts(cache_type: int, prompt: int, tokens: int, seqs: int, nodes: int,
         out = torch.empty((sum(n), width), device="cuda")
         block.prepare_draft(table[i32([t for x in trees for t in x[0]])], out, ln[of] + depth, slots, starts,
                             i32([a for t in trees for a in t[1]]), mine, long)()
-        got = judge(out, n_top=1)
+        got = score(out, n_top=1)
         top, logp, at, paths = got.top[:, 0].tolist(), got.top_logprob[:, 0].tolist(), 0, []
         for s, (tok, parents, _) in enumerate(trees):
             path = [0] if tok else []

@@ -16,7 +16,7 @@
 //     again (from L2).  What they hold is ordered by counting, for each, the larger ones (ties: the lower token first).
 //
 // Measured on GB300 (cold L2): one fp32 row of 128256 logits, top 20, 8.8 us; 61 masked, capped rows of 50257 15.5 us; 600 rows of
-// 128256, top 8, 52 us (5.9 TB/s); 4095 fp16 rows of 128256 202 us (5.2 TB/s).
+// 128256, top 8, 52 us (5.9 TB/s); 4095 fp16 rows of 128256 202 to 205 us (5.1 TB/s).
 #include <cooperative_groups.h>
 
 #include <algorithm>

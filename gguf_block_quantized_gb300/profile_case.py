@@ -22,6 +22,10 @@ Cases (synthetic weights ~N(0, 0.02), activations ~N(0, 1)):
   attn_prefill_f16, attn_prefill_q8  a prompt of 4096 tokens, 32 / 8 heads of 128 (Q8_0: expanded ahead)
   attn_prefill_batch_f16, attn_prefill_batch_q8  8 prompts of 512 tokens (Q8_0: expanded in the kernel)
   kv_read_f16, kv_read_q8  the rows of 4096 tokens back as fp16
+  attn_tree_f16, attn_tree_q8  trees of 24 drafts over each of 48 sequences of 2000 rows (F16: 393 MB)
+  attn_tree_long_f16, attn_tree_long_q8  a tree of 64 drafts over one sequence of 96000 rows
+  kv_compact_f16, kv_compact_q8  one sequence of 40000 rows packed to every second one
+  logprobs_f32, logprobs_f16  512 and 1024 rows of 128256 logits (263 MB), one token and the 8 most likely of each
 """
 from __future__ import annotations
 
@@ -40,6 +44,8 @@ CASES = {
 ATTN = ["kv_append_f16", "kv_append_q8", "attn_decode_f16", "attn_decode_q8", "attn_decode_long_f16",
         "attn_decode_long_q8", "attn_prefill_f16", "attn_prefill_q8", "attn_prefill_batch_f16", "attn_prefill_batch_q8",
         "kv_read_f16", "kv_read_q8"]
+DRAFTS = ["attn_tree_f16", "attn_tree_q8", "attn_tree_long_f16", "attn_tree_long_q8", "kv_compact_f16", "kv_compact_q8",
+          "logprobs_f32", "logprobs_f16"]
 
 
 def attn_case(case: str, reps: int):
@@ -82,10 +88,41 @@ def attn_case(case: str, reps: int):
     print(f"{case}: {reps} calls done")
 
 
+def draft_case(case: str, reps: int):
+    """The operators of drafted tokens: 32 / 8 heads of 128, pages of 64, zeroed caches."""
+    import torch
+
+    from gguf_block_quantized_gb300 import syn
+
+    def ints(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    if case.startswith("logprobs"):
+        rows, dtype = (512, torch.float32) if case.endswith("f32") else (1024, torch.float16)
+        logits = (4.0 * torch.randn((rows, 128256), device="cuda")).to(dtype)
+        step = syn.prepare_logprobs(logits, ids=torch.randint(128256, (rows, 1), device="cuda").to(torch.int32), n_top=8)
+    else:
+        seqs, rows, n = (1, 40000, 20000) if "compact" in case else (1, 96000, 64) if "long" in case else (48, 2000, 24)
+        per = -(-rows // 64)
+        cache = syn.KVCache.empty(syn.Q8_0 if case.endswith("q8") else syn.F16, 8, 128, 64, seqs * per)
+        pages = torch.randperm(seqs * per, device="cuda").to(torch.int32).view(seqs, per)
+        if "compact" in case:
+            step = syn.prepare_kv_compact(cache, None, pages, ints([0]), ints([0, n]), ints(range(1, rows, 2)))
+        else:
+            q = torch.randn((seqs * n, 32, 128), device="cuda").half()
+            parents = ints([(i + 1) // 2 - 1 for i in range(n)] * seqs)
+            step = syn.prepare_attn_tree(cache, q, ints(range(0, seqs * n + 1, n)), parents, pages, ints([rows] * seqs))
+    for _ in range(reps):
+        step()
+    torch.cuda.synchronize()
+    assert syn.device_status() == syn.OK
+    print(f"{case}: {reps} calls done")
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--case", required=True, choices=sorted(CASES) + ["gemv_llama1b_layer", "gemv_llama8b_layers",
-                                                                     "prefill_llama8b_layer"] + ATTN)
+                                                                     "prefill_llama8b_layer"] + ATTN + DRAFTS)
     ap.add_argument("--reps", type=int, default=3)
     args = ap.parse_args()
     import torch
@@ -94,6 +131,9 @@ def main():
 
     if args.case in ATTN:
         attn_case(args.case, args.reps)
+        return
+    if args.case in DRAFTS:
+        draft_case(args.case, args.reps)
         return
     if args.case == "gemv_llama1b_layer":
         from gguf_block_quantized_gb300 import workloads

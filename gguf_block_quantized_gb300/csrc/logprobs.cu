@@ -354,8 +354,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
             for (int l0 = 0; l0 < loads; l0 += THREADS) {
                 if (l0 > 0) {
                     __syncthreads();
-                    if (n_found + THREADS * E > MOST) {  // (rows whose large logits crowd in few threads)
-                        const int m = n_found;
+                    const int m = n_found;
+                    __syncthreads();  // (every thread goes by the same count: none has added to it since)
+                    if (m + THREADS * E > MOST) {  // (rows whose large logits crowd in few threads)
                         rank_found(m);
                         __syncthreads();
                         if (tid < min(m, k)) found[tid] = best[tid];

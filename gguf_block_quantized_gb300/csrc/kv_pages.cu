@@ -726,8 +726,13 @@ __global__ void __launch_bounds__(CMP_LONG_THREADS, CMP_CTAS) k_kv_compact_long(
             if (r < end_s && w.src[r] >= 0) *reinterpret_cast<S*>(at_s + w.dst_s[r]) = ws[i];
         }
     }
-    // the last CTA to get here leaves the counters and flags as they were
-    if (tid == 0) last = atomicAdd(q.turn + 1, 1) == (int)gridDim.x - 1;
+    // the last CTA to get here leaves the counters and flags as they were (behind every CTA's own: the fences
+    // order each flag that was set before its CTA's count, and the last count before the zeros)
+    if (tid == 0) {
+        __threadfence();
+        last = atomicAdd(q.turn + 1, 1) == (int)gridDim.x - 1;
+        __threadfence();
+    }
     __syncthreads();
     if (!last) return;
     if (tid < 2) q.turn[tid] = 0;

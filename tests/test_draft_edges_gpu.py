@@ -49,3 +49,46 @@ def test_candidates_over_several_turns(syn, rows, n_top, half):
             z = x.gather(1, want.long()).double() - torch.logsumexp(x.double(), 1, keepdim=True)
             # 2^-17 for ln S, 2^-22 of the log probability
             assert ((got.top_logprob - z).abs() <= 2.0 ** -17 + 2.0 ** -22 * z.abs()).all()
+
+
+def packed_case(syn, rng, t, kv, dim, page, n):
+    """A cache of random bits that one sequence of n rows fills, its table, and the pools' planes [pages, kv, page, bytes]."""
+    import torch
+    n_pages = -(-n // page)
+    shape = (kv, page, dim * 2) if t == F16 else (kv, page * dim // 16 * 17)
+    pools = [torch.randint(0, 256, (n_pages, *shape), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache = syn.KVCache(t, kv, dim, page, *(p.view(torch.float16) if t == F16 else p for p in pools))
+    planes = pools if t == F16 else [x for p in pools for x in (p[..., :page * dim].unflatten(-1, (page, dim)),
+                                                                p[..., page * dim:].unflatten(-1, (page, dim // 16)))]
+    return cache, torch.from_numpy(rng.permutation(n_pages)).cuda(), planes
+
+
+def pack(planes, table, rows, page):
+    """The planes as the rows (numpy, ascending) leave them."""
+    import torch
+    to, come = torch.arange(len(rows), device="cuda"), torch.from_numpy(rows).cuda()
+    out = []
+    for x in planes:
+        y = x.clone()
+        y[table[to // page], :, to % page] = x[table[come // page], :, come % page]
+        out.append(y)
+    return out
+
+
+@pytest.mark.parametrize("t,kv,dim", [(F16, 2, 64), (Q8_0, 4, 128), (Q8_0, 1, 32)])
+def test_long_lists_one_after_the_other(syn, t, kv, dim):
+    """Calls that follow each other on a stream use the same counters and flags: each leaves them at zero."""
+    import torch
+    rng, page, n = np.random.default_rng(dim), 16, 9000
+    cases = [packed_case(syn, rng, t, kv, dim, page, n) for _ in range(6)]
+    for turn in range(10):
+        keep = [np.nonzero(rng.random(n) < share)[0] for share in (0.5, 0.999, 0.3, 0.97, 0.6, 0.9)]
+        want = [pack(planes, table, r, page) for (_, table, planes), r in zip(cases, keep)]
+        steps = [syn.prepare_kv_compact(cache, None, table[None].int(), torch.zeros(1, dtype=torch.int32, device="cuda"),
+                                        torch.tensor([0, len(r)], dtype=torch.int32, device="cuda"),
+                                        torch.from_numpy(r.astype(np.int32)).cuda()) for (cache, table, _), r in zip(cases, keep)]
+        torch.cuda.synchronize()
+        lens = [step() for step in steps]
+        assert [x.item() for x in lens] == [len(r) for r in keep]
+        for (_, _, planes), w in zip(cases, want):
+            assert all(torch.equal(x, y) for x, y in zip(planes, w)), turn

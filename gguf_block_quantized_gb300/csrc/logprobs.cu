@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
         for (int i = 0; i < LP_PIECES; i++) next[i] = row.load(piece_of(0, i), end);
         const float scale = p.scales ? p.scale * p.scales[r] : p.scale;
         const bool scale_ok = scale > 0.0f && scale < INFINITY;
-        const float c = scale * LP_LOG2E;
+        const float c = fminf(scale * LP_LOG2E, 0x1.fffffep127f);  // (finite: the largest logit's y is 0)
         // cap*tanh(x/cap): up to half the cap x times a polynomial in (x/cap)^2, fitted on [0, 1/2] to 1e-7, past it
         // cap - 2 cap/(1 + 2^(2 x log2(e)/cap)), which is off by 2e-7 cap at most (CUDA's tanhf: 17.0 us, not 14.7, for 61
         // masked rows of 50257)
@@ -432,7 +432,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
         }
         const bool bad = !(sums.x < INFINITY) || !scale_ok;  // NaN or infinite logits, a scale that is none
         const float nan = __int_as_float(0x7fffffff), row_z = capped(sums.x), log_s = sums.s > 0.0f ? log2f(sums.s) : 0.0f;
-        auto logp = [&](float x) { return LP_LN2 * (c * (capped(x) - row_z) - log_s); };
+        // (by the scale itself: 2^y of a logit of the type's lowest value is 0, its log probability need not be -inf)
+        auto logp = [&](float x) {
+            const float z = capped(x), d = z - row_z;
+            return fmaf(-LP_LN2, log_s, d > -INFINITY ? scale * d : scale * z - scale * row_z);
+        };
         if (tid == 0 && p.entropy) p.entropy[r] = bad ? nan : sums.s > 0.0f ? LP_LN2 * (log_s - sums.t / sums.s) : 0.0f;
         auto tell = [&](int i, int token, float x) {
             if (token >= p.n_vocab) record_error(p.err, SYN_DEVERR_BOUNDS);

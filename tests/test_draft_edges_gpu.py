@@ -92,3 +92,57 @@ def test_long_lists_one_after_the_other(syn, t, kv, dim):
         assert [x.item() for x in lens] == [len(r) for r in keep]
         for (_, _, planes), w in zip(cases, want):
             assert all(torch.equal(x, y) for x, y in zip(planes, w)), turn
+
+
+def reference(x, scale=1.0, cap=0.0):
+    """Log probabilities and entropy of rows without NaN, in 64 bits."""
+    import torch
+    x = x.double()
+    z = cap * torch.tanh(x / cap) if cap else x
+    z = torch.where(x == -torch.inf, x, z) * scale
+    z = z - z.amax(1, keepdim=True)
+    logp = z - torch.log(torch.exp(z).sum(1, keepdim=True))
+    p = torch.exp(logp)
+    return logp, -torch.where(p > 0, p * logp, torch.zeros_like(p)).sum(1)
+
+
+@pytest.mark.parametrize("v", [40, 20001, 128256])
+def test_logits_of_the_types_lowest_value(syn, v):
+    """A mask of finfo.min instead of -inf: such a token's log probability is a number as long as fp32 holds it."""
+    import torch
+    for t in (torch.float32, torch.float16):
+        low = torch.finfo(t).min
+        x = torch.randn((6, v), device="cuda").to(t)
+        x[0, 1:] = low
+        x[1, ::2] = low
+        x[2, v // 2:] = low
+        x[3] = low  # (all alike)
+        x[4] = low
+        x[4, 3] = -low
+        ids = torch.tensor([[v - 1, 0], [0, 1], [v - 1, 0], [0, v - 1], [3, 0], [0, v - 1]], dtype=torch.int32, device="cuda")
+        for scale in (1.0, 0.25, 3.0, 1e-30):
+            want, entropy = reference(x, scale)
+            got = syn.logprobs(x, ids, 3, scale=scale)
+            for value, want in ((got.logprob, want.gather(1, ids.long())), (got.top_logprob, want.gather(1, most_likely(x, 3).long())),
+                                (got.entropy, entropy)):
+                limit = torch.finfo(torch.float32).max
+                over = want < -limit * (1 + 2.0 ** -24)  # (what fp32 does not hold is -inf)
+                assert (value[over] == -torch.inf).all()
+                off = (value.double() - want)[~over].abs()
+                assert (off <= 2.0 ** -17 + 2.0 ** -22 * want[~over].abs()).all(), (t, scale)
+            assert torch.equal(got.top, most_likely(x, 3))
+
+
+def test_scales_at_the_ends_of_the_float_range(syn):
+    """The largest logits alone count under the largest scales, all alike under the smallest."""
+    import torch
+    x = torch.randn((3, 5000), device="cuda")
+    x[1, 7:9] = 20.0
+    x[2, 9] = 30.0
+    for scale in (3e38, 1e30):
+        got = syn.logprobs(x, x.argmax(1, keepdim=True).int(), 2, scale=scale)
+        want = torch.tensor([0.0, float(np.log(2.0)), 0.0], dtype=torch.float32, device="cuda")
+        assert torch.allclose(got.entropy, want, rtol=0, atol=1e-6) and torch.allclose(got.logprob[:, 0], -want, rtol=0, atol=1e-6)
+        assert got.top_logprob[0, 1] < -1e25 and got.top_logprob[2, 1] < -1e25
+    got = syn.logprobs(x, n_top=1, scale=1e-38)
+    assert torch.allclose(got.entropy, torch.full((3,), float(np.log(5000.0)), device="cuda"), rtol=1e-6, atol=0)

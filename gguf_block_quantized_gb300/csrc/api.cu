@@ -702,7 +702,7 @@ int syn_device_status(int clear) {
     for (int v : {syn::debug_bounds_quant(clear), syn::debug_bounds_gemv(clear), syn::debug_bounds_gemv_f16(clear),
                   syn::debug_bounds_gemm(clear), syn::debug_bounds_kv_append(clear), syn::debug_bounds_attn_decode(clear),
                   syn::debug_bounds_attn_prefill(clear), syn::debug_bounds_attn_tree(clear),
-                  syn::debug_bounds_kv_pages(clear)}) {
+                  syn::debug_bounds_kv_pages(clear), syn::debug_bounds_logprobs(clear)}) {
         if (v < 0) return SYN_ERR_CUDA;
         wb |= v;
     }

@@ -1326,7 +1326,7 @@ struct JoinParams {
     int* n_splits;
     void* out;
     int64_t out_stride, part_floats;  // of a partial
-    int R, D, dim, g, out_f16;
+    int R, D, dim, g, out_f16, ctas;  // ctas: of the first kernel
 };
 
 __global__ void __launch_bounds__(JOIN_THREADS, JOIN_CTAS) k_attn_tree_join(const JoinParams p) {
@@ -1346,6 +1346,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, JOIN_CTAS) k_attn_tree_join(cons
         }
         const TreeSplit x = p.splits[lo];
         const int row = (u - x.before) / chunks * 32 + lane, e0 = (u - x.before) % chunks * JOIN_VALUES;
+        if (!SYN_IN_BOUNDS(u >= x.before && x.parts >= 1 && x.first >= 0 && x.first + x.parts <= p.ctas && row < p.R)) continue;
         // part i: what the CTA first + i went on with; of the first what it began
         auto part = [&](int i) { return p.part + ((int64_t)(x.first + i) * 3 + (i == 0)) * p.part_floats + row; };
         float mx = -INFINITY, sum = 0.0f, acc[JOIN_VALUES];
@@ -1500,7 +1501,7 @@ cudaError_t launch_attn_tree(const KvCache& c, const AttnDesc& a, int64_t n_seq,
     p.idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(c.dim >> 3) << 17) | (8u << 24);
     // (a scale that is not positive takes the general path: the fast one scales the maximum)
     const int mod = a.slopes || !(a.scale > 0.0f) ? GENERAL : a.cap > 0.0f ? CAPPED : PLAIN;
-    const JoinParams j{part, p.splits, p.n_splits, out, a.out_stride, tree_partial(c.dim), R, D, c.dim, g, a.out_f16};
+    const JoinParams j{part, p.splits, p.n_splits, out, a.out_stride, tree_partial(c.dim), R, D, c.dim, g, a.out_f16, sms};
     const int most = tree_max_seq(D, c.q8);
     for (int64_t s0 = 0; s0 < n_seq; s0 += most) {
         p.n_seq = (int)std::min<int64_t>(most, n_seq - s0);

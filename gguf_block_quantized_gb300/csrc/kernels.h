@@ -233,6 +233,7 @@ int debug_bounds_attn_decode(int clear);
 int debug_bounds_attn_prefill(int clear);
 int debug_bounds_attn_tree(int clear);
 int debug_bounds_kv_pages(int clear);
+int debug_bounds_logprobs(int clear);
 cudaError_t launch_bounds_selftest(cudaStream_t s);
 #endif
 

@@ -19,6 +19,11 @@ namespace syn {
 
 constexpr int PG_THREADS = 256;
 
+// (for the index checks: `bytes` from byte `at` of a pool on lie in it)
+__device__ __forceinline__ bool in_pool(const KvCache& c, int64_t at, int bytes) {
+    return at >= 0 && at + bytes <= (c.n_pages - 1) * c.page_stride + c.n_kv * c.tile;
+}
+
 // ---- fork and trim: a thread per table entry --------------------------------------------
 
 struct ForkParams {
@@ -42,6 +47,7 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_fork(const ForkParams p) {
         const int s = p.from[i];
         if (s >= p.n_seq && j == 0) record_error(p.err, SYN_DEVERR_BOUNDS);
         const int len = s >= 0 && s < p.n_seq ? held_rows(p.lens[s], p.max_pages, p.page_shift) : 0;
+        if (!SYN_IN_BOUNDS(i < p.n_new && j < p.max_pages)) continue;
         int id = -1;
         if (j < ((int64_t)len + (1 << p.page_shift) - 1) >> p.page_shift) {
             id = p.pages[s * p.max_pages + j];
@@ -73,6 +79,7 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_trim(const TrimParams p) {
     for (int64_t u = (int64_t)blockIdx.x * PG_THREADS + threadIdx.x; u < total; u += step) {
         const int64_t s = u / p.max_pages, j = u - s * p.max_pages;
         if (j < ((int64_t)max(p.lens[s], 0) + (1 << p.page_shift) - 1) >> p.page_shift) continue;
+        if (!SYN_IN_BOUNDS(s < p.n_seq)) continue;
         const int id = p.pages[u];
         if (id < 0) continue;
         p.pages[u] = -1;
@@ -226,6 +233,7 @@ __device__ void plan_pages(const ExtendParams& p, int* off, int* sums) {
         }
         x.s = lo;
         x.entry = (int64_t)lo * p.max_pages + (p.plan[lo].z >> shift) + (u - off[lo]);
+        if (!SYN_IN_BOUNDS(u >= off[lo] && x.entry < (int64_t)(lo + 1) * p.max_pages)) return x;
         x.id = p.pages[x.entry];
         return x;
     };
@@ -243,7 +251,7 @@ __device__ void plan_pages(const ExtendParams& p, int* off, int* sums) {
             record_error(p.err, SYN_DEVERR_BOUNDS);
         }
         any_shared |= what == 2;
-        p.need[u] = what;
+        if (SYN_IN_BOUNDS(u < p.max_items)) p.need[u] = what;
     }
     any_shared = __syncthreads_or(any_shared);
     if (any_shared) {
@@ -272,7 +280,7 @@ __device__ void plan_pages(const ExtendParams& p, int* off, int* sums) {
         int rank = n_free + block_sum(__popc(bits), sums, total) - __popc(bits);
         n_free += total;
         for (; bits; bits &= bits - 1, rank++)
-            if (rank < p.max_items) p.free_list[rank] = (int)at + __ffs(bits) - 1;
+            if (rank < p.max_items && SYN_IN_BOUNDS(rank >= 0 && at + __ffs(bits) <= p.c.n_pages)) p.free_list[rank] = (int)at + __ffs(bits) - 1;
     }
     __syncthreads();
     const bool enough = n_free >= wanted;
@@ -313,7 +321,7 @@ __device__ void plan_pages(const ExtendParams& p, int* off, int* sums) {
         const int rank = given + block_sum(take, sums, total) - 1;
         given += total;
         if (kept) refs[x.id] = 1;
-        if (take) {
+        if (take && SYN_IN_BOUNDS(rank >= 0 && rank < n_free && rank < p.max_items)) {
             const int got = p.free_list[rank];
             refs[got] = 1;
             p.pages[x.entry] = got;
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_extend_rows(const ExtendParam
             const int4 a = p.plan[lo];
             if (a.w && at >= 0 && at < new_rows(p, lo)) {
                 const int row = a.z + (int)at;
-                slot = ((int64_t)p.pages[lo * p.max_pages + (row >> shift)] << shift) + (row & (page - 1));
+                if (SYN_IN_BOUNDS((row >> shift) < p.max_pages)) slot = ((int64_t)p.pages[lo * p.max_pages + (row >> shift)] << shift) + (row & (page - 1));
             }
             p.slots[t] = slot;
         }
@@ -372,6 +380,7 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_extend_rows(const ExtendParam
         const uint8_t* src = pool + a.x * p.c.page_stride + h * p.c.tile;
         uint8_t* dst = pool + a.y * p.c.page_stride + h * p.c.tile;
         const int rows = a.z & (page - 1);
+        if (!SYN_IN_BOUNDS(in_pool(p.c, src - pool, (int)p.c.tile) && in_pool(p.c, dst - pool, (int)p.c.tile))) continue;
         for (int i = tid; i < rows * n16; i += PG_THREADS)
             reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i];
         if (p.c.q8) {
@@ -461,17 +470,21 @@ __device__ __forceinline__ void move_rows(const CompactParams& p, int tile0, int
         const int tile = tile0 + t;
         return reinterpret_cast<U*>((tile & 1 ? p.c.v : p.c.k) + row + (tile >> 1) * p.c.tile) + first + x;
     };
+    auto inside = [&](int64_t row) {  // (for the index checks)
+        const int tile = tile0 + t;
+        return r < CMP_ROWS && tile < 2 * p.c.n_kv && in_pool(p.c, row + (tile >> 1) * p.c.tile + (first + x) * (int)sizeof(U), sizeof(U));
+    };
     U held[CMP_SHORT];
     for (int u0 = 0; u0 < units; u0 += CMP_THREADS * CMP_SHORT) {
         const int t0 = t, r0 = r, x0 = x;
 #pragma unroll
         for (int i = 0; i < CMP_SHORT; i++, on())
-            if (t < n_tiles && src[r] >= 0) held[i] = *at(src[r]);
+            if (t < n_tiles && src[r] >= 0 && SYN_IN_BOUNDS(inside(src[r]))) held[i] = *at(src[r]);
         __syncthreads();
         t = t0, r = r0, x = x0;
 #pragma unroll
         for (int i = 0; i < CMP_SHORT; i++, on())
-            if (t < n_tiles && src[r] >= 0) *at(dst[r]) = held[i];
+            if (t < n_tiles && src[r] >= 0 && SYN_IN_BOUNDS(inside(src[r]) && inside(dst[r]))) *at(dst[r]) = held[i];
     }
 }
 
@@ -577,7 +590,7 @@ __device__ __forceinline__ void plan_chunk(const LongParams& q, int taken, LongC
 #pragma unroll
     for (int k = 0; k < CMP_CHUNK / 32; k++) {
         const int i = lane + 32 * k, r = r0 + i;
-        if (i >= m) continue;
+        if (i >= m || !SYN_IN_BOUNDS(i < CMP_CHUNK && r < p.n_rows)) continue;
         const int lo = sequence_of(r);
         if (k == 0) first_seq = lo;
         const int a = p.starts[lo], b = p.starts[lo + 1], at = r - a;
@@ -683,22 +696,25 @@ __global__ void __launch_bounds__(CMP_LONG_THREADS, CMP_CTAS) k_kv_compact_long(
         uint8_t* at16 = ((tile0 + t16) & 1 ? p.c.v : p.c.k) + ((tile0 + t16) >> 1) * p.c.tile + (tid - row16 * u16 - t16 * n16) * 16;
         uint8_t* at_s = ((tile0 + t_s) & 1 ? p.c.v : p.c.k) + ((tile0 + t_s) >> 1) * p.c.tile + (tid - row_s * us - t_s * ns) * (int)sizeof(S);
         const int end16 = row16 < per16 ? w.rows : 0, end_s = us && row_s < per_s ? w.rows : 0;
+        // (for the index checks: this thread's piece of 16 bytes, or of scales, of the row at `row` of tile 0)
+        auto in16 = [&](int64_t row) { return in_pool(p.c, at16 - ((tile0 + t16) & 1 ? p.c.v : p.c.k) + row, 16); };
+        auto in_s = [&](int64_t row) { return in_pool(p.c, at_s - ((tile0 + t_s) & 1 ? p.c.v : p.c.k) + row, sizeof(S)); };
         S ws[CMP_SCALES];
 #pragma unroll
         for (int i = 0; i < CMP_UNITS; i++) {
             const int r = row16 + i * per16;
-            if (r < end16 && w.src[r] >= 0) cp16_all(smem_u32(held16 + i * CMP_THREADS), at16 + w.src[r]);
+            if (r < end16 && w.src[r] >= 0 && SYN_IN_BOUNDS(r < CMP_CHUNK && in16(w.src[r]))) cp16_all(smem_u32(held16 + i * CMP_THREADS), at16 + w.src[r]);
         }
         cp_commit();
 #pragma unroll
         for (int i = 0; i < CMP_SCALES; i++) {
             const int r = row_s + i * per_s;
-            if (r < end_s && w.src[r] >= 0) ws[i] = *reinterpret_cast<const S*>(at_s + w.src_s[r]);
+            if (r < end_s && w.src[r] >= 0 && SYN_IN_BOUNDS(r < CMP_CHUNK && in_s(w.src_s[r]))) ws[i] = *reinterpret_cast<const S*>(at_s + w.src_s[r]);
         }
         cp_wait<0>();
         copiers_sync();  // (what was loaded is loaded)
         int* flags = q.flags + (int64_t)w.group * q.chunks;
-        if (tid == 0) {
+        if (tid == 0 && SYN_IN_BOUNDS(w.chunk >= 0 && w.chunk < q.chunks && w.group < q.groups && w.c1 <= q.chunks)) {
             __threadfence();
             atomicExch(flags + w.chunk, 1);
         }
@@ -718,12 +734,12 @@ __global__ void __launch_bounds__(CMP_LONG_THREADS, CMP_CTAS) k_kv_compact_long(
 #pragma unroll
         for (int i = 0; i < CMP_UNITS; i++) {
             const int r = row16 + i * per16;
-            if (r < end16 && w.src[r] >= 0) *reinterpret_cast<uint4*>(at16 + w.dst[r]) = held16[i * CMP_THREADS];
+            if (r < end16 && w.src[r] >= 0 && SYN_IN_BOUNDS(in16(w.dst[r]))) *reinterpret_cast<uint4*>(at16 + w.dst[r]) = held16[i * CMP_THREADS];
         }
 #pragma unroll
         for (int i = 0; i < CMP_SCALES; i++) {
             const int r = row_s + i * per_s;
-            if (r < end_s && w.src[r] >= 0) *reinterpret_cast<S*>(at_s + w.dst_s[r]) = ws[i];
+            if (r < end_s && w.src[r] >= 0 && SYN_IN_BOUNDS(in_s(w.dst_s[r]))) *reinterpret_cast<S*>(at_s + w.dst_s[r]) = ws[i];
         }
     }
     // the last CTA to get here leaves the counters and flags as they were (behind every CTA's own: the fences
@@ -845,12 +861,12 @@ __global__ void __launch_bounds__(PG_THREADS) k_kv_copy(const CopyParams p) {
 #pragma unroll
         for (int x = 0; x < COPY_UNITS; x++) {
             const int64_t o = off + (x * PG_THREADS + threadIdx.x) * 16;
-            if (o < p.bytes) held[x] = *reinterpret_cast<const uint4*>(a + o);
+            if (o < p.bytes && SYN_IN_BOUNDS(in_pool(p.from, a + o - (is_v ? p.from.v : p.from.k), 16))) held[x] = *reinterpret_cast<const uint4*>(a + o);
         }
 #pragma unroll
         for (int x = 0; x < COPY_UNITS; x++) {
             const int64_t o = off + (x * PG_THREADS + threadIdx.x) * 16;
-            if (o < p.bytes) *reinterpret_cast<uint4*>(b + o) = held[x];
+            if (o < p.bytes && SYN_IN_BOUNDS(in_pool(p.to, b + o - (is_v ? p.to.v : p.to.k), 16))) *reinterpret_cast<uint4*>(b + o) = held[x];
         }
     }
 }

@@ -99,7 +99,8 @@ struct Row {
     // A piece's bits; in those of logits that are not the row's, -inf.
     __device__ __forceinline__ uint4 load(int piece, int end) const {
         const int e0 = token(piece, 0);
-        if (piece < end && e0 >= 0 && e0 + E <= n) return load_once(at + (int64_t)e0 * (F16 ? 2 : 4));
+        if (piece < end && e0 >= 0 && e0 + E <= n && SYN_IN_BOUNDS(piece >= 0 && piece < pieces && (reinterpret_cast<uintptr_t>(at + (int64_t)e0 * (F16 ? 2 : 4)) & 15) == 0))
+            return load_once(at + (int64_t)e0 * (F16 ? 2 : 4));
         uint32_t w[4] = {F16 ? 0xFC00FC00u : 0xFF800000u, F16 ? 0xFC00FC00u : 0xFF800000u, F16 ? 0xFC00FC00u : 0xFF800000u,
                          F16 ? 0xFC00FC00u : 0xFF800000u};
         if (piece < end) {
@@ -120,7 +121,7 @@ struct Row {
     __device__ __forceinline__ uint4 allowed(const uint4& piece, int index) const {
         const int e0 = token(index, 0), w = max(e0, 0) >> 5;
         const bool any = e0 < n;
-        const uint32_t lo = any ? __ldg(mask + w) : 0u;
+        const uint32_t lo = any && SYN_IN_BOUNDS(w <= (n - 1) >> 5) ? __ldg(mask + w) : 0u;
         const uint32_t hi = any && (e0 & 31) + E > 32 && e0 >= 0 && w < (n - 1) >> 5 ? __ldg(mask + w + 1) : 0u;
         const uint32_t bits = e0 < 0 ? lo << -e0 : __funnelshift_r(lo, hi, e0 & 31);
         uint32_t u[4] = {piece.x, piece.y, piece.z, piece.w};
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
             const float x = largest_of<F16>(now);
             unit = max_nan(unit, x);
             if (--left == 0 || turn + 1 == turns) {
-                if (p.n_top > 0) unit_max[u++ * THREADS + tid] = unit;
+                if (p.n_top > 0 && SYN_IN_BOUNDS(u < LP_UNITS)) unit_max[u++ * THREADS + tid] = unit;
                 left = group;
                 unit = -INFINITY;
             }
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
                 int rank = 0;
 #pragma unroll 8
                 for (int j = 0; j < n; j++) rank += found[j] > key;
-                if (rank < p.n_top) best[rank] = key;
+                if (rank < p.n_top && SYN_IN_BOUNDS(rank < LP_TOP && n <= MOST)) best[rank] = key;
             }
         };
         int n_best = 0;
@@ -347,7 +348,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
             }
             if (n > 0 && u >= lo && first <= tie)  // (at most 2k threads)
                 for (int i = 0; i < LP_UNITS && i * group < turns; i++)
-                    if (unit_max[i * THREADS + tid] >= least) units[atomicAdd(&n_units, 1)] = i * THREADS + tid;
+                    if (unit_max[i * THREADS + tid] >= least) {
+                        const int slot = atomicAdd(&n_units, 1);
+                        if (SYN_IN_BOUNDS(slot < LP_UNITS * 2 * LP_TOP)) units[slot] = i * THREADS + tid;
+                    }
             __syncthreads();
             const int per_unit = group * LP_PIECES, loads = n_units * per_unit;
             uint64_t above = 0;  // what is not above this key is out
@@ -377,7 +381,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
                     for (int j = 0; j < E; j++) {
                         const int token = row.token(piece, j);
                         const uint64_t key = ((uint64_t)order_of(v[j] + 0.0f) << 32) | (uint32_t)~token;
-                        if ((v[j] > least || (v[j] == least && token <= tie)) && key > above) found[atomicAdd(&n_found, 1)] = key;
+                        if ((v[j] > least || (v[j] == least && token <= tie)) && key > above) {
+                            const int slot = atomicAdd(&n_found, 1);
+                            if (SYN_IN_BOUNDS(slot < MOST)) found[slot] = key;
+                        }
                     }
                 }
             }
@@ -401,7 +408,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
                 cluster.map_shared_rank(sent_sums, 0)[part] = sums;
                 cluster.map_shared_rank(sent_n, 0)[part] = n_best;
             }
-            if (tid < n_best) cluster.map_shared_rank(sent, 0)[part * LP_TOP + tid] = best[tid];
+            if (tid < n_best && SYN_IN_BOUNDS(part < LP_CLUSTER && n_best <= LP_TOP)) cluster.map_shared_rank(sent, 0)[part * LP_TOP + tid] = best[tid];
             cluster.sync();
             if (part > 0) {
                 if (r + rows_at_once < p.n_rows) cluster.barrier_arrive();
@@ -420,7 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
                 int at = 0;
                 for (int i = 0; i < p.cut; i++) {
                     const int m = sent_n[i];
-                    if (tid < m) found[at + tid] = sent[i * LP_TOP + tid];
+                    if (tid < m && SYN_IN_BOUNDS(m <= LP_TOP && at + m <= MOST)) found[at + tid] = sent[i * LP_TOP + tid];
                     at += m;
                 }
                 __syncthreads();
@@ -511,5 +518,9 @@ cudaError_t launch_logprobs(const LogitsDesc& d, int64_t n_rows, int n_vocab, co
     if (threads == 128) return d.f16 ? run_logprobs<true, 128>(p, sms, s) : run_logprobs<false, 128>(p, sms, s);
     return d.f16 ? run_logprobs<true, 512>(p, sms, s) : run_logprobs<false, 512>(p, sms, s);
 }
+
+#ifdef SYN_DEBUG
+SYN_BOUNDS_READER(debug_bounds_logprobs)
+#endif
 
 }  // namespace syn

@@ -1,4 +1,6 @@
-"""Pages and log probabilities in the debug build: every index check passes and results are those of the product build."""
+"""Pages and log probabilities in the checking builds: in the debug build every index check passes and results are those of
+the product build; in the stall build, where no chunk of a long list says that it is loaded, the waits run out and are reported,
+and the next call finds its counters as they should be."""
 import ctypes
 import os
 import sys
@@ -96,3 +98,25 @@ def test_logprobs_in_the_debug_build(libs, n, v, half):
             out.append((p, e, best, q))
         for a, b in zip(*out):
             assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+
+
+def test_waits_of_a_long_list_run_out():
+    from gguf_block_quantized_gb300 import build, syn
+    stall = syn.bind(build.build(variant="stall"))
+    stall.syn_device_status(1)
+    page, n = 16, 6000
+    rows, starts, base = i32(np.arange(1, n)), i32([0, n - 1]), i32([0])
+    table, out = torch.randperm(n // page, device="cuda")[None].to(torch.int32), torch.empty(1, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        cache, pools = random_cache(syn, F16, 2, 64, page, n // page, 1)
+        assert stall.syn_kv_compact(ctypes.byref(cache.desc), None, 1, n - 1, table.data_ptr(), n // page, base.data_ptr(), starts.data_ptr(),
+                                    rows.data_ptr(), out.data_ptr(), stream()) == syn.OK
+        assert stall.syn_device_status(1) == syn.ERR_TIMEOUT and stall.syn_device_status(1) == syn.OK
+        assert out.item() == n - 1
+        # the product library, on the same device
+        cache, pools = random_cache(syn, F16, 2, 64, page, n // page, 2)
+        before = [p[table[0].long()].transpose(1, 2).flatten(0, 1).clone() for p in pools]  # rows in order
+        syn.kv_compact(cache, None, table, base, starts, rows)
+        for p, x in zip(pools, before):
+            assert torch.equal(p[table[0].long()].transpose(1, 2).flatten(0, 1)[:n - 1], x[1:])
+        assert syn.device_status() == syn.OK

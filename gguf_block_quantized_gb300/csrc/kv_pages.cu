@@ -786,7 +786,8 @@ int64_t compact_count_words(const KvCache& c, int64_t n_seq, int64_t n_rows) {
     if (!long_lists(n_seq, n_rows)) return 0;
     LongParams q;
     const int64_t n = cut_long(c, n_rows, &q);
-    return n < INT_MAX - 2 ? n + 2 : -1;
+    // (the counter of chunks goes past the last by one for each CTA: it stays within 32 bits)
+    return n <= INT_MAX - (1 << 20) ? n + 2 : -1;
 }
 
 cudaError_t launch_kv_compact(const KvCache& c, const int32_t* refs, int64_t n_seq, int64_t n_rows, const int32_t* pages,

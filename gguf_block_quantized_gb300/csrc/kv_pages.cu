@@ -147,14 +147,18 @@ __device__ __forceinline__ int new_rows(const ExtendParams& p, int s) {
     return a < 0 || b > p.n_tok ? 0 : max(b - a, 0);
 }
 
-// The inclusive sum over the CTA's threads, and their total.
+// Two numbers up to 2^30 added, up to 2^30.
+__device__ __forceinline__ int add_up_to(int a, int b) { return (int)min((unsigned)a + (unsigned)b, 1u << 30); }
+
+// The inclusive sum over the CTA's threads, and their total, up to 2^30 (which only starts that overlap come to: a call has
+// at most 2^28 pages of new rows, and some for its sequences).
 __device__ __forceinline__ int block_sum(int x, int* sums, int& total) {
     constexpr int WARPS = EXT_THREADS / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        if (lane >= o) x = add_up_to(x, y);
     }
     __syncthreads();  // (the sums before this one have been read)
     if (lane == 31) sums[warp] = x;
@@ -163,11 +167,11 @@ __device__ __forceinline__ int block_sum(int x, int* sums, int& total) {
 #pragma unroll
     for (int o = 1; o < WARPS; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
+        if (lane >= o) w = add_up_to(w, y);
     }
     total = __shfl_sync(0xffffffffu, w, WARPS - 1);
     const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
-    return x + (warp > 0 ? before : 0);
+    return add_up_to(x, warp > 0 ? before : 0);
 }
 
 // Which of counts[at .. at + 8) are 0.
@@ -204,8 +208,8 @@ __device__ void plan_pages(const ExtendParams& p, int* off, int* sums) {
         }
         int total;
         const int sum = block_sum(columns, sums, total);
-        if (s < p.n_seq) off[s + 1] = items + sum;
-        items += total;
+        if (s < p.n_seq) off[s + 1] = add_up_to(items, sum);
+        items = add_up_to(items, total);
     }
     __syncthreads();
     // (starts that overlap could name more rows than the call has)

@@ -146,3 +146,15 @@ def test_scales_at_the_ends_of_the_float_range(syn):
         assert got.top_logprob[0, 1] < -1e25 and got.top_logprob[2, 1] < -1e25
     got = syn.logprobs(x, n_top=1, scale=1e-38)
     assert torch.allclose(got.entropy, torch.full((3,), float(np.log(5000.0)), device="cuda"), rtol=1e-6, atol=0)
+
+
+def test_starts_that_overlap_are_refused(syn):
+    """More new rows in all than the call has: nothing changes, and it is reported.  (Sums of columns stop at 2^30, so that
+    none comes out small.)"""
+    import torch
+    cache = syn.KVCache.empty(F16, 1, 32, 8, 200)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    refs, pages, lens = i32([0] * 200), torch.full((9, 8), -1, dtype=torch.int32, device="cuda"), i32([3] * 9)
+    _, slots = syn.kv_extend(cache, refs, pages, lens, starts=i32([0, 40] * 5), n_tok=40)
+    assert syn.device_status() == syn.ERR_BOUNDS
+    assert lens.tolist() == [3] * 9 and (refs == 0).all() and (pages == -1).all() and (slots == -1).all()

@@ -66,8 +66,9 @@ int attn_of(const syn_attn* a, const syn::KvCache& c, int64_t rows, const void* 
     d->n_heads = a->n_heads;
     d->window = a->window;
     d->out_f16 = a->out_type == SYN_OUT_F16;
-    // (past 2^100 the largest score alone counts, as fp16 products are multiples of 2^-48; times log2(e) it stays finite)
-    d->scale = std::min(std::max(a->scale, -0x1p100f), 0x1p100f);
+    // (past 2^80 the largest score alone counts, as products are multiples of 2^-48; they are below 2^47, with Q8_0
+    // keys of the largest scale, so that a score times log2(e) stays finite)
+    d->scale = std::min(std::max(a->scale, -0x1p80f), 0x1p80f);
     d->cap = a->cap;
     return SYN_OK;
 }

@@ -158,3 +158,32 @@ def test_starts_that_overlap_are_refused(syn):
     _, slots = syn.kv_extend(cache, refs, pages, lens, starts=i32([0, 40] * 5), n_tok=40)
     assert syn.device_status() == syn.ERR_BOUNDS
     assert lens.tolist() == [3] * 9 and (refs == 0).all() and (pages == -1).all() and (slots == -1).all()
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.0 ** 90])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_large_products_under_large_scales(syn, scale, slopes):
+    """The key of the largest product takes all the weight, in every form of the attention, where products are past 2^28 and
+    the scale is the float range's end; queries of zeros see every key alike (without slopes)."""
+    import torch
+    rng = np.random.default_rng(51)
+    n, new, heads, dim = 120, 20, 4, 64
+    k = np.zeros((128, 1, dim), np.float16)
+    k[:n, 0, 0] = 512.0 * (rng.permutation(n) - n // 2)  # (7 bits: exact; 2^15 at most)
+    v = rng.integers(-100, 100, (128, dim)).astype(np.float16)
+    q = np.zeros((new, heads, dim), np.float16)
+    q[:, 1::2, 0] = 2.0 ** 15  # products up to 2^30
+    pool = lambda x: torch.from_numpy(x.reshape(8, 1, 16, dim)).cuda()  # noqa: E731
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache, pages, on = syn.KVCache(F16, 1, dim, 16, pool(k), pool(v)), i32([list(range(8))]), torch.from_numpy(q).cuda()
+    opt = {"scale": scale, "slopes": torch.full((heads,), 0.125, device="cuda") if slopes else None}
+    tree = syn.attn_tree(cache, on, i32([0, new]), i32(range(-1, new - 1)), pages, i32([n]), **opt).double().cpu().numpy()
+    prefill = syn.attn_prefill(cache, on, i32([0, new]), pages, i32([n]), **opt).double().cpu().numpy()
+    one = syn.attn_decode(cache, on[-1:], pages, i32([n]), **opt).double().cpu().numpy()
+    for i in range(new):
+        seen = k[:n - new + i + 1, 0, 0].astype(np.float64) * np.sign(scale)
+        top, mean = v[seen.argmax()].astype(np.float64), v[:len(seen)].astype(np.float64).mean(0)
+        for got in (tree[i], prefill[i]) + ((one[0],) if i == new - 1 else ()):
+            assert (got[1::2] == top).all(), i
+            assert slopes or (np.abs(got[::2] - mean) <= 100 * 2.0 ** -11).all()
+    assert syn.device_status() == syn.OK

@@ -203,7 +203,8 @@ def run_drafts(cache_type: int, prompt: int, tokens: int, seqs: int, nodes: int,
     x = table[torch.randint(0, vocab, (prompt,), device="cuda", generator=gen)]
     out = torch.empty((prompt, width), device="cuda")
     block.prepare_prompt(x, out, torch.arange(prompt, dtype=torch.int32, device="cuda"), slots, i32([0, prompt]), pages, lens)()
-    first = score(out[-1:].contiguous(), n_top=seqs).top[0].tolist()
+    best = score(out[-1:].contiguous(), n_top=min(seqs, 64, vocab)).top[0].tolist()  # (64: the most that logprobs gives)
+    first = [best[s % len(best)] for s in range(seqs)]
 
     def plain():  # one token at a time: tokens and log probabilities
         mine, ln = forked(pages, lens, seqs)
@@ -270,6 +271,8 @@ def main() -> None:
     ap.add_argument("--seqs", type=int, default=4)
     ap.add_argument("--draft", type=int, default=0, metavar="NODES")
     a = ap.parse_args()
+    if min(a.prompt, a.steps, a.seqs) < 1 or a.draft < 0:
+        ap.error("--prompt, --steps and --seqs: at least 1; --draft: 0 or more")
     if a.draft:
         r = run_drafts(Q8_0 if a.type == "q8_0" else F16, a.prompt, a.steps, a.seqs, a.draft)
         print(f"{a.seqs} sequences, {a.type} cache, trees of {a.draft} drafts: {r['per_step']:.2f} tokens a step and sequence, "

@@ -187,3 +187,12 @@ def test_large_products_under_large_scales(syn, scale, slopes):
             assert (got[1::2] == top).all(), i
             assert slopes or (np.abs(got[::2] - mean) <= 100 * 2.0 ** -11).all()
     assert syn.device_status() == syn.OK
+
+
+def test_drafts_of_more_sequences_than_alternatives(syn):
+    """logprobs gives at most 64 first tokens: more sequences share them."""
+    from gguf_block_quantized_gb300 import attn_block
+    r = attn_block.run_drafts(F16, 20, 3, 70, 4, vocab=1000, page=16)
+    # (as tests/test_draft_block_gpu.py derives.  The tokens need not be the same: the best two lie closer together than the forms
+    # differ in some of 280 draws of 1000 logits, by 0.0009 to 0.0053 where the forms differ by up to 0.013.)
+    assert r["held"] == 0 and r["difference"] <= 16 * 8 * 2.0 ** -11 and r["per_step"] >= 1.0

@@ -600,10 +600,11 @@ typedef struct {
  * entropy (n_rows, or NULL), in nats; the n_top (0 to 64) allowed tokens of the largest logits, in
  * order, ties to the lower token: top and top_logprob (n_rows x n_top); where fewer are allowed, -1 and
  * -inf.  Sums are fp32 over a running maximum; every result is exact to about 1e-6 of the larger of 1
- * and its own size, capped logits to 5e-7 * cap * scale.  Logits may start anywhere their type may;
- * 16-byte aligned rows load fastest.  Asynchronous.  (In deterministic mode a row's results do not
- * depend on the number of rows.)  SYN_ERR_TYPE, SYN_ERR_SHAPE (n_vocab up to 2^30, n_ids up to
- * 65536), SYN_ERR_NULL, SYN_ERR_ALIGN. */
+ * and its own size, with a cap to 5e-7 * cap * scale more (the entropy to that times the larger of 1 and
+ * itself).  A log probability past fp32's range is -inf; a logit further below the largest than that range adds
+ * nothing to the sums.  Logits may start anywhere their type may; 16-byte aligned rows load fastest.
+ * Asynchronous.  (In deterministic mode a row's results do not depend on the number of rows.)  SYN_ERR_TYPE,
+ * SYN_ERR_SHAPE (n_vocab up to 2^30, n_ids up to 65536), SYN_ERR_NULL, SYN_ERR_ALIGN. */
 SYN_API int syn_logprobs(const syn_logits* opt, int64_t n_rows, int64_t n_vocab, const void* logits, int64_t n_ids,
                          const int32_t* ids, float* logprob, float* entropy, int64_t n_top, int32_t* top, float* top_logprob,
                          syn_stream_t stream);

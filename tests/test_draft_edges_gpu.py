@@ -196,3 +196,31 @@ def test_drafts_of_more_sequences_than_alternatives(syn):
     # (as tests/test_draft_block_gpu.py derives.  The tokens need not be the same: the best two lie closer together than the forms
     # differ in some of 280 draws of 1000 logits, by 0.0009 to 0.0053 where the forms differ by up to 0.013.)
     assert r["held"] == 0 and r["difference"] <= 16 * 8 * 2.0 ** -11 and r["per_step"] >= 1.0
+
+
+def held_to(got, want, more=0.0):
+    """The public bound (include/syn.h): 1e-6 of the larger of 1 and the result's size, and what a cap adds.  (Of a
+    result: d and its product 2^-23 of themselves; ln S 2^-22 by its powers, their exponents' roundings 2^-22 of T/S,
+    which is below the entropy, its additions some 2^-24 each way; together below 2^-20 of the larger of 1 and the result.)"""
+    off = (got.double() - want).abs()
+    bound = 1e-6 * want.abs().clamp(min=1) + more
+    assert (off <= bound).all(), float((off / bound).max())
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("n,v", [(3, 1), (40, 33), (64, 5003), (2, 50257), (300, 50257), (1, 128256), (320, 128256), (700, 20011)])
+@pytest.mark.parametrize("spread", [0.0, 0.3, 2.5, 12.0])
+def test_log_probabilities_are_as_exact_as_stated(syn, n, v, half, spread):
+    """Rows nearly alike, ordinary and peaked, up to a vocabulary that one CTA sums alone."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(v + n)
+    x = (torch.randn((n, v), device="cuda", generator=gen) * spread).to(torch.float16 if half else torch.float32)
+    ids = torch.randint(0, v, (n, 8), dtype=torch.int32, device="cuda", generator=gen)
+    k = min(v, 20)
+    for scale, cap in ((1.0, 0.0), (0.7, 0.0), (1.0, 30.0), (1.25, 5.0)):
+        want, entropy = reference(x, float(np.float32(scale)), cap)
+        got = syn.logprobs(x, ids, k, scale=scale, cap=cap)
+        lax = 5e-7 * cap * scale
+        held_to(got.logprob, want.gather(1, ids.long()), lax)
+        held_to(got.top_logprob, want.gather(1, most_likely(x, k).long()), lax)
+        held_to(got.entropy, entropy, lax * entropy.clamp(min=1))

@@ -429,8 +429,11 @@ cudaError_t launch_kv_extend(const KvCache& c, int32_t* refs, int64_t n_seq, int
 //
 // Rows move down in place: row base + i comes from base + rows[i] >= base + i.  A CTA has columns of a sequence's
 // tiles (a tile: a kv head, keys or values; a column: some 16-byte pieces of each row) to itself and goes through
-// the rows in order, a batch loaded whole before any of it is stored: what a batch overwrites are rows
-// that it or a batch before has loaded, so no CTA waits for another.  Short lists are a chain of dependent loads
+// them in passes of CMP_SHORT units a thread (a unit: a piece of a row), in the order of the rows within each tile: a pass
+// is loaded whole before any of it is stored.  A unit of list row i overwrites the piece of a list row k with
+// rows[k] = i, if there is one; as rows ascend k <= i, so that piece was loaded in this pass or one before, and what later
+// passes load lies past every place stored so far.  (So a tile's units stay in the order of its rows.)  No CTA
+// waits for another.  Short lists are a chain of dependent loads
 // (starts, rows, page ids, counts, rows): what makes a call longer is the CTAs it takes to start.
 
 constexpr int CMP_THREADS = 256;

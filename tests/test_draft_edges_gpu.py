@@ -224,3 +224,53 @@ def test_log_probabilities_are_as_exact_as_stated(syn, n, v, half, spread):
         held_to(got.logprob, want.gather(1, ids.long()), lax)
         held_to(got.top_logprob, want.gather(1, most_likely(x, k).long()), lax)
         held_to(got.entropy, entropy, lax * entropy.clamp(min=1))
+
+
+@pytest.mark.parametrize("limit", [1, 3, 20])
+@pytest.mark.parametrize("t,kv,dim", [(F16, 1, 64), (Q8_0, 2, 128), (F16, 3, 256), (Q8_0, 1, 96)])
+def test_long_lists_on_few_sms(syn, t, kv, dim, limit):
+    """A CTA takes many chunks one after the other, and waits for those of the few others."""
+    import torch
+    rng, page, n = np.random.default_rng([dim, limit]), 16, 12000
+    old = syn.set_sm_limit(limit)
+    try:
+        for share in (0.5, 0.9995, 0.05):
+            cache, table, planes = packed_case(syn, rng, t, kv, dim, page, n)
+            rows = np.nonzero(rng.random(n) < share)[0]
+            rows = rows if len(rows) >= 1024 else np.sort(rng.permutation(n)[:1024])
+            want = pack(planes, table, rows, page)
+            got = syn.kv_compact(cache, None, table[None].int(), torch.zeros(1, dtype=torch.int32, device="cuda"),
+                                 torch.tensor([0, len(rows)], dtype=torch.int32, device="cuda"), torch.from_numpy(rows.astype(np.int32)).cuda())
+            assert got.item() == len(rows)
+            assert all(torch.equal(x, y) for x, y in zip(planes, want)), share
+    finally:
+        syn.set_sm_limit(old)
+
+
+def test_a_list_that_does_not_ascend_leaves_the_others_alone(syn):
+    """What its own sequence's packed rows hold is not defined; the other sequences, the rows behind, the lengths and the report are."""
+    import torch
+    rng, page, n = np.random.default_rng(77), 16, 4000
+    for small in (False, True):
+        m = 60 if small else n
+        cache, table, planes = packed_case(syn, rng, F16, 2, 64, page, 3 * m)
+        pages = table[:3 * m // page].view(3, -1) if 3 * m % (3 * page) == 0 else table[:3 * (m // page)].view(3, -1)
+        held = pages.shape[1] * page
+        good = np.nonzero(rng.random(held) < 0.6)[0]
+        bad = np.arange(1, held // 2)
+        bad[len(bad) // 3] = 0
+        rows = [good, bad, good]
+        want = [x.clone() for x in planes]
+        for s in (0, 2):
+            for i, y in enumerate(pack(planes, pages[s], good, page)):
+                own = pages[s]
+                want[i][own] = y[own]
+        starts = np.concatenate([[0], np.cumsum([len(r) for r in rows])]).astype(np.int32)
+        got = syn.kv_compact(cache, None, pages.int().contiguous(), torch.zeros(3, dtype=torch.int32, device="cuda"), torch.from_numpy(starts).cuda(),
+                             torch.from_numpy(np.concatenate(rows).astype(np.int32)).cuda())
+        assert syn.device_status() == syn.ERR_BOUNDS
+        assert got.tolist() == [len(r) for r in rows]
+        row = torch.arange(len(bad), device="cuda")
+        for x, w in zip(planes, want):  # (the second sequence's packed rows aside)
+            w[pages[1][row // page], :, row % page] = x[pages[1][row // page], :, row % page]
+            assert torch.equal(x, w)

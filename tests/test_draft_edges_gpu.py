@@ -274,3 +274,70 @@ def test_a_list_that_does_not_ascend_leaves_the_others_alone(syn):
         for x, w in zip(planes, want):  # (the second sequence's packed rows aside)
             w[pages[1][row // page], :, row % page] = x[pages[1][row // page], :, row % page]
             assert torch.equal(x, w)
+
+
+@pytest.mark.parametrize("t", [F16, Q8_0])
+@pytest.mark.parametrize("heads,kv,dim", [(256, 1, 32), (1024, 1, 32), (600, 2, 64), (300, 1, 256), (1024, 1024, 32)])
+def test_trees_of_many_heads(syn, t, heads, kv, dim):
+    """A token's heads over one item or several, in numbers that divide 128 or do not."""
+    from test_attn_tree_gpu import run
+    run(syn, t, heads, kv, dim, 16, [60, 33], [4, 3], [heads, dim], dts=("float32",))
+    run(syn, t, heads, kv, dim, 16, [60, 33], [4, 3], [heads, dim], dts=("float32",), window=3, slopes=True)
+
+
+def test_as_many_sequences_as_extend_takes(syn):
+    import pages_ref
+    import torch
+    rng, n, width, page, n_pages = np.random.default_rng(8), 4096, 5, 8, 15000
+    cache = syn.KVCache.empty(F16, 1, 32, page, n_pages)
+    refs, pages, lens = np.zeros(n_pages, np.int32), np.full((n, width), -1, np.int32), np.zeros(n, np.int32)
+    on = [torch.from_numpy(x.copy()).cuda() for x in (refs, pages, lens)]
+    for new in (rng.integers(0, 12, n), rng.integers(0, 20, n), np.ones(n, np.int64), rng.integers(0, 30, n)):  # (the last: pages are short)
+        refs, pages, lens, slots, _ = pages_ref.extend(refs, pages, lens, new, page)
+        starts = torch.from_numpy(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)).cuda()
+        _, got = syn.kv_extend(cache, *on, starts=starts, n_tok=int(new.sum()))
+        for x, y in zip((*on, got), (refs, pages, lens, slots)):
+            assert np.array_equal(x.cpu().numpy(), y)
+
+
+@pytest.mark.parametrize("t", [F16, Q8_0])
+def test_pools_past_32_bit_offsets(syn, t):
+    """Rows and pages at the end of pools of 5 GB: extended, copied, packed and read by trees as in a small pool."""
+    import torch
+    dim, kv, page = 128, 8, 64
+    tile = page * dim * 2 if t == F16 else page * dim // 16 * 17
+    n_pages, few = 5 * 10 ** 9 // (tile * kv), 80
+    shape = (kv, page, dim) if t == F16 else (kv, page * dim // 16 * 17)
+    kind = torch.float16 if t == F16 else torch.uint8
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rows = [torch.randn((few, *shape), device="cuda", generator=gen).half() if t == F16 else
+            torch.randint(0, 40, (few, *shape), dtype=torch.uint8, device="cuda", generator=gen) for _ in range(2)]
+    results = []
+    for n in (n_pages, few):
+        pools = [torch.empty((n, *shape), dtype=kind, device="cuda") for _ in range(2)]
+        for p, r in zip(pools, rows):
+            p[-few:] = r
+        cache, at = syn.KVCache(t, kv, dim, page, *pools), n - few
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        refs = torch.ones(n, dtype=torch.int32, device="cuda")
+        refs[at + 40:] = 0  # (two sequences of 20 pages share the first 20 once, then pages are free)
+        pages = torch.full((2, 24), -1, dtype=torch.int32, device="cuda")
+        pages[0, :20] = torch.arange(at, at + 20, device="cuda")
+        pages[1, :20] = torch.arange(at, at + 20, device="cuda")
+        refs[at:at + 20] = 2
+        lens, starts = i32([19 * 64 + 5] * 2), i32([0, 70, 140])
+        long, slots = syn.kv_extend(cache, refs, pages, lens, torch.empty_like(lens), starts=starts, n_tok=140)
+        syn.kv_copy(cache, cache, i32([at + 21, at + 22]), i32([at + 70, at + 71]))
+        q = torch.randn((140, 32, dim), device="cuda", generator=torch.Generator(device="cuda").manual_seed(4)).half()
+        parents = i32([(i - 1) // 2 if i else -1 for i in range(70)] * 2)
+        out = syn.attn_tree(cache, q, starts, parents, pages, long)
+        own = pages.clone()
+        own[:, :19] = torch.arange(at + 41, at + 79, device="cuda").view(2, 19)  # (pages of their own, to be written to)
+        keep = torch.arange(0, 19 * 64, 2, dtype=torch.int32, device="cuda")
+        for much in (keep, keep[:100]):
+            got = syn.kv_compact(cache, None, own, i32([0, 0]), i32([0, much.numel(), 2 * much.numel()]), much.repeat(2))
+        results.append([pages - at * (pages >= 0), slots - at * page, refs[at:], long, out, got, *(p[-few:].clone() for p in pools)])
+        del pools, cache
+    assert syn.device_status() == syn.OK
+    for a, b in zip(*results):
+        assert torch.equal(a, b)

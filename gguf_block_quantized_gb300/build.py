@@ -9,9 +9,9 @@ the product path; the tests load them beside libsyn.so):
          against the buffers before each access, records SYN_DEVERR_BOUNDS and skips the
          access (syn_device_status then returns SYN_ERR_BOUNDS).
   stall  libsyn_stall.so  -DSYN_TEST_STALL and a 20,000,000-cycle wait bound: the decode and
-         prefill kernels never receive their activations, and no chunk of a long list of rows says that it is
-         loaded, so their bounded waits run out
-         (syn_device_status then returns SYN_ERR_TIMEOUT); the timeout tests use it.
+         prefill kernels never receive their activations, and no chunk of a long list of rows
+         says that it is loaded, so their bounded waits run out (syn_device_status then returns
+         SYN_ERR_TIMEOUT); the timeout tests use it.
 """
 from __future__ import annotations
 

@@ -29,8 +29,12 @@
 //
 // Measured on GB300 (cold L2; 32 / 8 heads of 128, pages of 64): 24 F16 sequences of 190 to 4000 rows with up to 26
 // drafts 43 us (133 MB, 3.1 TB/s: 5 us to the first product, 7 us of join); 48 Q8_0 sequences of 500 to 6001 with up
-// to 13 drafts, capped, 136 us (240 MB, 1.8 TB/s: the expanding and softmax warps' instructions; 105 us without the
-// cap); 64 drafts over 120001 F16 rows 120 us (493 MB, 4.1 TB/s, and 1.05 PFLOP/s: softmax).
+// to 13 drafts, capped, 136 us (240 MB, 1.8 TB/s; 105 us without the cap: nothing is full, no scheduler's issue slots past 53 %,
+// the tensor pipe 28 %, DRAM 34 %, so a tile's chain of expansion, S, softmax and P V bounds it, one and a half tiles ahead);
+// 64 drafts over 120001 F16 rows 118 to 124 us (493 MB, 4.1 TB/s, and 1.0 PFLOP/s): softmax of 256 rows, 1.83 us a tile, is 90 of
+// them, what does not grow with the length the rest.
+//
+// What is alike in attn_prefill.cu (cap, expansion, loader, rows computed again) is mended in both.
 //
 // A masked score is replaced before the maximum; V rows past the sequence's end are zeroed in shared memory.  A V
 // row that only some rows of the item see may still hold infinities or NaN, and 0 * inf is not 0: a row whose

@@ -497,7 +497,10 @@ SYN_API int syn_attn_prefill(const syn_kv_cache* cache, const syn_attn* attn, in
  *   of the drafts    itself and its ancestors a with first <= c + a and (window == 0 or d(i) - d(a) < window)
  * with a bias of slopes[head] times the distance of the positions.  (A prefix ends with the context.)
  * A parent that is not before its token counts as none, and syn_device_status returns SYN_ERR_BOUNDS.
- * Chains, whose parents are i - 1, give what syn_attn_prefill gives.  The drafts' rows are in the
+ * Chains, whose parents are i - 1, give what syn_attn_prefill gives, but are walked node by node for every
+ * tile of keys among the drafts: past some hundred nodes the time grows with the cube of their number (chains over 4096
+ * rows, 32 heads of 128, on GB300: 64 nodes 43 us where syn_attn_prefill takes 40, 256 128 for 42, 1024 1.3 ms for
+ * 0.07, 8192 0.45 s for 0.0007), so long chains are syn_attn_prefill's.  The drafts' rows are in the
  * cache in the order of the tokens; syn_kv_compact packs an accepted path.  Accuracy, splitting,
  * deterministic mode, workspace, alignment and errors as for syn_attn_prefill (a Q8_0 cache is not
  * expanded ahead).  Asynchronous. */
@@ -538,8 +541,10 @@ SYN_API int syn_kv_fork(const syn_kv_cache* cache, int32_t* refs, int64_t n_seq,
  * new length (it may be lens), slots (n_tok, or NULL) each new row's slot for syn_kv_append.
  * Where free pages do not suffice nobody keeps a shared page, and pages go to the first sequences,
  * as long as the sum of their needs fits; sequences that need none are extended too.  The others, and
- * those whose table has too few columns, stay as they are: their length, and -1 as slots (which
- * syn_kv_append does not store).  n_seq up to 4096 (SYN_ERR_SHAPE).  Uses the attention workspace of
+ * those whose table has too few columns, stay as they are: their length (cut to what the table holds), and -1 as slots
+ * (which syn_kv_append does not store).  starts that overlap, so that they name more rows than the call has, change
+ * nothing (SYN_ERR_BOUNDS).  The counts are read from page 0 on until there are enough free ones (11 us on GB300 where the first
+ * pages are free, 62 behind 200000 held ones).  n_seq up to 4096 (SYN_ERR_SHAPE).  Uses the attention workspace of
  * (device, stream), 16 bytes a sequence and 8 a page that new rows fall into: make the first call of a
  * size before capturing a graph (and graphs as for syn_mul_mat). */
 SYN_API int syn_kv_extend(const syn_kv_cache* cache, int32_t* refs, int64_t n_seq, int64_t n_tok, int32_t* pages,
